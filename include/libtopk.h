@@ -53,7 +53,8 @@ typedef enum {
   TOPK_ERR_CUDA = 5,                /* a CUDA runtime call failed (launch, query, copy) */
   TOPK_ERR_BARRIER_TIMEOUT = 6,     /* reported by topk_get_status: a wait on the device gave up */
   TOPK_ERR_LENGTH_CLAMPED = 7,      /* reported by topk_get_status: some length was outside [0, row_stride] */
-  TOPK_ERR_PLAN = 8                 /* no launch configuration fits the device (e.g. kernel not resident) */
+  TOPK_ERR_PLAN = 8,                /* no launch configuration fits the device (e.g. kernel not resident) */
+  TOPK_ERR_UNSUPPORTED = 9          /* a type, head layout or dimension outside what the paged calls take */
 } topk_status;
 
 /* Sticky bits of the device status word (first 4 bytes of the workspace). */
@@ -65,6 +66,12 @@ typedef enum {
  * so this launch wrote rows of -1 instead of merging through them. Every such
  * launch does the same until topk_workspace_init clears the workspace. */
 #define TOPK_DEV_WORKSPACE_DIRTY 0x8u
+/* The paged calls (topk_kv_map, topk_index_logits, topk_paged_attention). */
+#define TOPK_DEV_BLOCKS_EXHAUSTED 0x10u /* topk_kv_map: free_blocks ran out; the tokens concerned got slot -1 */
+#define TOPK_DEV_TABLE_FULL 0x20u       /* topk_kv_map: a request outgrew its row of the table; slot -1 */
+#define TOPK_DEV_TOKENS_DROPPED 0x40u   /* topk_kv_map: more new tokens than max_tokens; the rest got no block and are not listed */
+#define TOPK_DEV_BAD_BLOCK 0x80u        /* a valid token's block, or a row's request, lies outside the cache or the table */
+#define TOPK_DEV_PIPELINE_TIMEOUT 0x100u /* a wait between the warps of a CTA gave up: the launch's results are void */
 
 /* Tuning and test knobs for topk_ragged_ex. Zero-initialise, then set fields.
  * A field left at 0 takes the value of its environment variable, read once per
@@ -317,6 +324,149 @@ int topk_query_device(int device, topk_device_props* props);
  */
 int topk_make_plan(const topk_device_props* props, int64_t num_rows, int64_t row_stride,
                    int next_n, int topk, const topk_options* options, topk_plan* plan);
+
+/* ------------------------------------------------------------------------
+ * The calls around the selection: a paged cache's map, the logits that
+ * topk_ragged selects from, and attention over what it selected. The pages
+ * name the model step that does this (vLLM PR #54110 page, "Feature and
+ * motivation": DSA models in long-context inference) and describe none of it.
+ *
+ * A paged cache holds tokens in num_blocks blocks of block_size tokens; token
+ * i of request b lies in block block_table[b][i / block_size], at place
+ * i % block_size. Conventions of this header hold: device pointers owned by the
+ * caller, host-side errors returned before anything is enqueued, no allocation
+ * or synchronisation, capture in CUDA graphs (make the first call on a device
+ * before a capture). `workspace` starts with a status word as topk_ragged's does:
+ * zero it once with topk_workspace_init, read it with topk_get_status. Calls
+ * that may overlap on the GPU must not share one, and none shares topk_ragged's.
+ * The kernels use programmatic dependent launch as the short-row kernel does
+ * (LIBTOPK_DEPENDENT_LAUNCH=2 turns it off).
+ * ------------------------------------------------------------------------ */
+
+/* Element types of queries and caches. */
+typedef enum { TOPK_DTYPE_F16 = 1, TOPK_DTYPE_BF16 = 2, TOPK_DTYPE_F8E4M3 = 3 } topk_dtype;
+
+/* Workspace bytes of topk_kv_map and topk_index_logits. */
+#define TOPK_PAGED_WORKSPACE_BYTES 256
+
+/*
+ * Block tables and slot maps for one step (topk_kv_map): request r has
+ * context_lens[r] cached tokens and brings new_lens[r] more (negative reads as
+ * 0). Blocks for them are taken from free_blocks[*taken ...], requests in order,
+ * each request's blocks in order, and entered in its row of the table; columns
+ * of blocks that it already has stay as they are. For the new tokens, packed
+ * request after request, the call lists where each goes and what it sees.
+ */
+typedef struct {
+  const int32_t* context_lens; /* [num_requests] */
+  const int32_t* new_lens;     /* [num_requests] */
+  int64_t num_requests;        /* 0..2^31-1 */
+  int block_size;              /* >= 1 */
+  int32_t* block_table;        /* [num_requests, max_blocks], updated in place */
+  int64_t table_stride;        /* elements between the table's rows, >= max_blocks */
+  int64_t max_blocks;          /* columns of the table, >= 1 */
+  const int32_t* free_blocks;  /* [num_free] block ids that may be handed out */
+  int64_t num_free;
+  const int32_t* taken;        /* [1] entries of free_blocks handed out before this call */
+  int32_t* taken_out;          /* [1] the same after it, at most num_free; may be `taken` itself */
+  int64_t* slots;              /* [max_tokens] block * block_size + place, or -1 where there is no block */
+  int32_t* row_lens;           /* [max_tokens] position + 1: the lengths of topk_ragged and of the calls below */
+  int32_t* row_request;        /* [max_tokens] the token's request */
+  int32_t* token_start;        /* [num_requests + 1] first new token of each request, then the number listed */
+  int64_t max_tokens;          /* 0..2^31-1; entries past the last token are filled with -1, 0 and -1 */
+  void* workspace;             /* TOPK_PAGED_WORKSPACE_BYTES, 16-byte aligned */
+} topk_kv_map_args;
+
+int topk_kv_map(const topk_kv_map_args* args, void* stream);
+
+/* The rows of a call and where their requests' tokens lie. */
+typedef struct {
+  int64_t num_rows;           /* 0..2^31-1; 0 is a no-op */
+  int next_n;                 /* rows per request where row_request is NULL; must divide num_rows */
+  int block_size;             /* >= 1 */
+  int64_t num_requests;       /* rows of the table */
+  int64_t num_blocks;         /* blocks of the cache */
+  const int32_t* lengths;     /* [num_rows] tokens that the row sees; clamped into [0, max_blocks * block_size] */
+  const int32_t* row_request; /* [num_rows] each row's request (negative: the row sees nothing), or NULL: row / next_n */
+  const int32_t* block_table; /* [num_requests, max_blocks] */
+  int64_t table_stride;
+  int64_t max_blocks;
+} topk_paged_rows;
+
+/*
+ * logits[r, t] = key_scales[t] * sum over h of weights[r, h] * max(0, q[r, h, :] . keys[t, :])
+ * for every token t < len_r of row r's request: the scores that a sparse-attention
+ * indexer gives the cached tokens. Entries from len_r on are not written.
+ * Products and sums are in fp32; a NaN product counts as NaN. A token whose block
+ * lies outside the cache scores -inf (TOPK_DEV_BAD_BLOCK).
+ * heads 1..128, dim 8..128 (multiples of 8; of 16 for 8-bit types). q and keys are
+ * read in pieces of 16 bytes: their addresses and strides are multiples of that.
+ */
+typedef struct {
+  topk_paged_rows rows;
+  int dtype; /* topk_dtype of q and keys */
+  int heads;
+  int dim;
+  const void* q; /* [num_rows, heads, dim], strides in elements, the last one 1 */
+  int64_t q_row_stride, q_head_stride;
+  const float* weights; /* [num_rows, heads] */
+  int64_t weight_row_stride;
+  const void* keys; /* [num_blocks, block_size, dim] */
+  int64_t key_block_stride, key_token_stride;
+  const float* key_scales; /* [num_blocks, block_size], or NULL: 1 */
+  int64_t scale_block_stride, scale_token_stride;
+  float* logits; /* [num_rows, max_len] */
+  int64_t logits_row_stride;
+  int64_t max_len; /* columns; lengths above it are clamped to it (TOPK_DEV_LENGTH_CLAMPED) */
+  void* workspace; /* TOPK_PAGED_WORKSPACE_BYTES, 16-byte aligned */
+} topk_index_logits_args;
+
+int topk_index_logits(const topk_index_logits_args* args, void* stream);
+
+/*
+ * Attention of each row's heads over the tokens t < len_r of its request, or over
+ * those that its index list names:
+ *   out[r, h, :] = sum_t p_t * v_t,  p = softmax over t of scale * q[r, h, :] . k_t,
+ *   lse[r, h] = log of the sum of exp(scale * q . k_t).
+ * Query head h reads key-value head h / (heads / kv_heads). With v NULL the value of
+ * a token is the first dv elements of its key: absorbed latent attention, in which
+ * key and value are one vector (kv_heads is then 1 in such models; any number is taken).
+ * Indices may stand in any order; one outside [0, len_r) is skipped (the -1 padding of
+ * topk_ragged), a repeated one counts as often as it stands there. A row that sees
+ * nothing, or whose scores are all -inf, gets out = 0 and lse = -inf. Masked places
+ * of the cache are never used, whatever they hold. A token whose block lies outside the
+ * cache is skipped (TOPK_DEV_BAD_BLOCK). Sums and softmax statistics are in fp32;
+ * probabilities are rounded to the input type for the product with v.
+ * dk 8..576 and dv 8..512 in multiples of 8, dv <= dk where v is NULL; types f16 and bf16.
+ * q, k, v and out are accessed in pieces of up to 16 bytes: addresses and strides are
+ * multiples of that.
+ */
+typedef struct {
+  topk_paged_rows rows;
+  int dtype; /* TOPK_DTYPE_F16 or TOPK_DTYPE_BF16: of q, k, v and out */
+  int heads, kv_heads, dk, dv;
+  float scale;   /* finite, > 0 */
+  const void* q; /* [num_rows, heads, dk], strides in elements, the last one 1 */
+  int64_t q_row_stride, q_head_stride;
+  const void* k; /* [num_blocks, block_size, kv_heads, dk] */
+  int64_t k_block_stride, k_token_stride, k_head_stride;
+  const void* v; /* [num_blocks, block_size, kv_heads, dv], or NULL */
+  int64_t v_block_stride, v_token_stride, v_head_stride;
+  const int32_t* indices; /* [num_rows, num_indices], or NULL: every token */
+  int64_t index_row_stride;
+  int num_indices; /* 1..2^20 */
+  void* out;       /* [num_rows, heads, dv] */
+  int64_t out_row_stride, out_head_stride;
+  float* lse; /* [num_rows, heads], contiguous, or NULL */
+  void* workspace;
+  size_t workspace_bytes; /* at least topk_attention_workspace_size; 16-byte aligned */
+} topk_attention_args;
+
+/* Workspace bytes that topk_paged_attention needs on `device`, whatever its arguments; 0 if the device
+ * cannot be queried. Only the first TOPK_PAGED_WORKSPACE_BYTES have to be zeroed (topk_workspace_init). */
+size_t topk_attention_workspace_size(int device);
+
+int topk_paged_attention(const topk_attention_args* args, void* stream);
 
 #ifdef __cplusplus
 }

@@ -20,7 +20,9 @@ __all__ = [
     "topk_workspace_size", "topk_workspace_init", "topk_ragged", "topk_ragged_ex", "topk_ragged_static",
     "topk_ragged_strided", "topk_gather_sort",
     "topk_get_status", "topk_status_string", "topk_query_device", "topk_make_plan",
-    "library_path", "Selector",
+    "topk_kv_map", "topk_index_logits", "topk_paged_attention", "topk_attention_workspace_size",
+    "TopkPagedRows", "TopkKvMapArgs", "TopkIndexLogitsArgs", "TopkAttentionArgs",
+    "library_path", "Selector", "PagedDecoder", "KvMap",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -37,6 +39,7 @@ TOPK_ERR_CUDA = 5
 TOPK_ERR_BARRIER_TIMEOUT = 6
 TOPK_ERR_LENGTH_CLAMPED = 7
 TOPK_ERR_PLAN = 8
+TOPK_ERR_UNSUPPORTED = 9
 
 TOPK_MERGE_AUTO = 0
 TOPK_MERGE_WORKSPACE = 1
@@ -52,10 +55,22 @@ TOPK_DEV_LENGTH_CLAMPED = 0x1
 TOPK_DEV_BARRIER_TIMEOUT = 0x2
 TOPK_DEV_STAGE_TIMEOUT = 0x4
 TOPK_DEV_WORKSPACE_DIRTY = 0x8
+TOPK_DEV_BLOCKS_EXHAUSTED = 0x10
+TOPK_DEV_TABLE_FULL = 0x20
+TOPK_DEV_TOKENS_DROPPED = 0x40
+TOPK_DEV_BAD_BLOCK = 0x80
+TOPK_DEV_PIPELINE_TIMEOUT = 0x100
+
+TOPK_DTYPE_F16 = 1
+TOPK_DTYPE_BF16 = 2
+TOPK_DTYPE_F8E4M3 = 3
+
+TOPK_PAGED_WORKSPACE_BYTES = 256
 
 EXPORTED = ("topk_workspace_size", "topk_workspace_init", "topk_ragged", "topk_ragged_ex", "topk_ragged_static",
             "topk_ragged_strided", "topk_gather_sort", "topk_get_status", "topk_status_string",
-            "topk_query_device", "topk_make_plan")
+            "topk_query_device", "topk_make_plan", "topk_kv_map", "topk_index_logits", "topk_paged_attention",
+            "topk_attention_workspace_size")
 
 
 class TopkError(RuntimeError):
@@ -105,6 +120,44 @@ class TopkPlan(ctypes.Structure):
                 ("shape", ctypes.c_int)]
 
 
+class TopkPagedRows(ctypes.Structure):
+    _fields_ = [("num_rows", ctypes.c_int64), ("next_n", ctypes.c_int), ("block_size", ctypes.c_int),
+                ("num_requests", ctypes.c_int64), ("num_blocks", ctypes.c_int64), ("lengths", ctypes.c_void_p),
+                ("row_request", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("max_blocks", ctypes.c_int64)]
+
+
+class TopkKvMapArgs(ctypes.Structure):
+    _fields_ = [("context_lens", ctypes.c_void_p), ("new_lens", ctypes.c_void_p), ("num_requests", ctypes.c_int64),
+                ("block_size", ctypes.c_int), ("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("max_blocks", ctypes.c_int64), ("free_blocks", ctypes.c_void_p), ("num_free", ctypes.c_int64),
+                ("taken", ctypes.c_void_p), ("taken_out", ctypes.c_void_p), ("slots", ctypes.c_void_p),
+                ("row_lens", ctypes.c_void_p), ("row_request", ctypes.c_void_p), ("token_start", ctypes.c_void_p),
+                ("max_tokens", ctypes.c_int64), ("workspace", ctypes.c_void_p)]
+
+
+class TopkIndexLogitsArgs(ctypes.Structure):
+    _fields_ = [("rows", TopkPagedRows), ("dtype", ctypes.c_int), ("heads", ctypes.c_int), ("dim", ctypes.c_int),
+                ("q", ctypes.c_void_p), ("q_row_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("weights", ctypes.c_void_p), ("weight_row_stride", ctypes.c_int64), ("keys", ctypes.c_void_p),
+                ("key_block_stride", ctypes.c_int64), ("key_token_stride", ctypes.c_int64),
+                ("key_scales", ctypes.c_void_p), ("scale_block_stride", ctypes.c_int64),
+                ("scale_token_stride", ctypes.c_int64), ("logits", ctypes.c_void_p),
+                ("logits_row_stride", ctypes.c_int64), ("max_len", ctypes.c_int64), ("workspace", ctypes.c_void_p)]
+
+
+class TopkAttentionArgs(ctypes.Structure):
+    _fields_ = [("rows", TopkPagedRows), ("dtype", ctypes.c_int), ("heads", ctypes.c_int), ("kv_heads", ctypes.c_int),
+                ("dk", ctypes.c_int), ("dv", ctypes.c_int), ("scale", ctypes.c_float), ("q", ctypes.c_void_p),
+                ("q_row_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64), ("k", ctypes.c_void_p),
+                ("k_block_stride", ctypes.c_int64), ("k_token_stride", ctypes.c_int64),
+                ("k_head_stride", ctypes.c_int64), ("v", ctypes.c_void_p), ("v_block_stride", ctypes.c_int64),
+                ("v_token_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64), ("indices", ctypes.c_void_p),
+                ("index_row_stride", ctypes.c_int64), ("num_indices", ctypes.c_int), ("out", ctypes.c_void_p),
+                ("out_row_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64), ("lse", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
 def library_path() -> str:
     return _LIB_PATH
 
@@ -145,6 +198,11 @@ def _load():
         lib.topk_make_plan.restype = i32
         lib.topk_make_plan.argtypes = [ctypes.POINTER(TopkDeviceProps), i64, i64, i32, i32,
                                        ctypes.POINTER(TopkOptions), ctypes.POINTER(TopkPlan)]
+        for name in ("topk_kv_map", "topk_index_logits", "topk_paged_attention"):
+            getattr(lib, name).restype = i32
+            getattr(lib, name).argtypes = [vp, vp]
+        lib.topk_attention_workspace_size.restype = ctypes.c_size_t
+        lib.topk_attention_workspace_size.argtypes = [i32]
         _lib = lib
         return lib
 
@@ -249,6 +307,22 @@ def topk_make_plan(props: TopkDeviceProps, num_rows: int, row_stride: int, next_
     return int(rc), plan
 
 
+def topk_kv_map(args: TopkKvMapArgs, stream=None) -> int:
+    return int(_load().topk_kv_map(ctypes.byref(args), _stream(stream)))
+
+
+def topk_index_logits(args: TopkIndexLogitsArgs, stream=None) -> int:
+    return int(_load().topk_index_logits(ctypes.byref(args), _stream(stream)))
+
+
+def topk_paged_attention(args: TopkAttentionArgs, stream=None) -> int:
+    return int(_load().topk_paged_attention(ctypes.byref(args), _stream(stream)))
+
+
+def topk_attention_workspace_size(device: int) -> int:
+    return int(_load().topk_attention_workspace_size(device))
+
+
 class Selector:
     """Owns one workspace on one device and runs calls on a stream.
 
@@ -314,3 +388,6 @@ class Selector:
         rc = topk_workspace_init(self.workspace, self.nbytes, stream)
         if rc != TOPK_OK:
             raise TopkError(rc, "topk_workspace_init")
+
+
+from .paged import KvMap, PagedDecoder  # noqa: E402

@@ -227,6 +227,7 @@ const char* topk_status_string(int code) {
     case TOPK_ERR_BARRIER_TIMEOUT: return "a device-side wait timed out";
     case TOPK_ERR_LENGTH_CLAMPED: return "a row length was outside [0, row_stride]";
     case TOPK_ERR_PLAN: return "no launch configuration fits the device";
+    case TOPK_ERR_UNSUPPORTED: return "unsupported type, head layout or dimension";
     default: return "unknown status";
   }
 }
