@@ -1,71 +1,714 @@
-// Attention of each row's heads over a paged cache. One CTA a (row, head):
-// every warp takes every fourth token with an online softmax in fp32; the
-// warps' sums are joined at the end.
+// Attention of each row's heads over a paged cache (topk_paged_attention), on
+// the tensor cores.
+//
+//   s_t = scale * q . k_t,   out = sum_t exp(s_t - m) v_t / sum_t exp(s_t - m)
+//
+// Shape of the work. A unit is a group of rows that read the same tokens (one
+// row, or a request's next_n rows where no index list tells them apart) and one
+// key-value head; its queries are columns (row j, head h) and come in blocks of
+// up to 64. Tokens come in tiles of 128. Both products are taken with the tokens
+// and values as the long side, M = 128, and the queries as N = 16, 32 or 64:
+//   S^T [128 tokens x N]     = K [128 x dk] . Q^T [dk x N]
+//   O^T [128 values x N] (+)= V^T [128 x 128 tokens] . P^T [128 tokens x N]
+// so that few heads waste no rows of the tensor core, a tile of the cache is
+// read in the layout that it has in memory by both products (K-major for the
+// first, MN-major for the second), and latent attention's O^T, 512 values of 64
+// heads, takes 256 of the 512 columns of tensor memory.
+//
+// Split. The units' tiles, in order, are dealt in equal runs to the CTAs, one
+// on each SM; a unit that falls into several runs leaves its sums and statistics in
+// the workspace, and a second kernel joins them in the order of the tokens. The
+// lengths are read on the device: every CTA sums up the rows' tiles to find its
+// run. With more than 64 columns, neighbouring CTAs take the column blocks of one
+// run and meet its tokens in L2.
+//
+// Roles in a CTA (13 warps): 4 copy tokens into a ring of 32 KB pieces (128
+// tokens x 128 dims) with 16-byte asynchronous copies, which take any page size,
+// stride and index list and write zeros for what is masked (whatever the cache
+// holds there); 1 thread issues the products; 8 warps do the softmax, a thread
+// per token and half of the columns. A column's maximum runs over the tokens,
+// that is over threads: a butterfly of shuffles in each warp, then four
+// numbers per column through shared memory. The maximum in use is moved only
+// when a tile's exceeds it by 2^8, which leaves the sums exact in fp32 and
+// spares nearly every rescaling of O^T in tensor memory.
 #include "paged.cuh"
+#include "umma.cuh"
 
 namespace ltk {
 namespace paged {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kMaxQk = 576, kMaxV = 512;
+using namespace ltk::umma;
 
-struct AttentionParams {
-  topk_attention_args a;
-  Rows R;
+constexpr int kTile = 128;             // tokens
+constexpr int kChunk = 128 * 128;      // bytes of 128 tokens x 64 dims
+constexpr int kPiece = 2 * kChunk;     // a ring slot
+constexpr int kSoftmaxWarps = 8, kCopyWarps = 4;
+constexpr int kCopyThreads = kCopyWarps * 32;
+constexpr int kMmaWarp = kSoftmaxWarps + kCopyWarps;
+constexpr int kThreads = (kMmaWarp + 1) * 32;
+constexpr int kTokenSlots = 8;  // more than the tiles that the copies can be ahead of the softmax: ring slots + 1
+constexpr int kMaxSlots = 6;
+constexpr int kMaxQk = 576, kMaxV = 512;
+constexpr int kMaxBlockCols = 64;
+constexpr int kJoinThreads = 128, kJoinCols = 8;
+constexpr float kMoveAbove = 8.f;  // in powers of two
+
+struct Join {  // what the join kernel has to know of the unit that ends in a slice and began before it
+  int64_t rowgroup;
+  int32_t kv_head;
+  int32_t first, last;  // slices
+  int32_t first_slot;   // which of its two places the first slice used
+  int64_t tiles;        // of all units
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) paged_attention_kernel(const AttentionParams p) {
-  __shared__ float sum_l[4], sum_m[4];
-  __shared__ float acc[4][kMaxV];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+struct Params {
+  topk_attention_args a;
+  Rows R;
+  int32_t pack;          // rows of a unit
+  int32_t group;         // heads a key-value head
+  int32_t cols;          // pack * group
+  int32_t blocks;        // column blocks of a unit
+  int32_t block_cols;    // columns of a block (the last one may have fewer)
+  int32_t k_chunks;      // of 64 dims
+  int32_t k_pieces, v_pieces;
+  int32_t latent;        // values are the first dims of the keys
+  int32_t rest;          // 1: the last half piece of the keys has a buffer of its own
+  int32_t rest_is_p;     // 1: and P takes its place after it has been used
+  int32_t slots;         // of the ring
+  int32_t ahead;         // 1: the next tile's scores are taken before this tile's values
+  int32_t slices;
+  int32_t row_tiles;     // tiles of every unit where index lists are given, else 0
+  int64_t row_groups;
+  uint32_t tmem_cols;
+  uint32_t q_bytes;
+  float scale2;          // scale * log2(e)
+  float* part;           // [slices][2][blocks][N][v_pieces * 128]
+  float2* stat;          // [slices][2][blocks][N]: maximum (in powers of two) and sum
+  Join* join;            // [slices]
+};
+
+template <int N>
+struct Smem {  // behind the tiles
+  static constexpr int kHalf = N / 2;
+  int32_t token[kTokenSlots][kTile];  // position of each token of a tile, INT_MAX where nothing is to be seen
+  float column_max[2][2][4][kHalf];   // [parity][half][warp]
+  float moved[kSoftmaxWarps][2][kHalf];  // maximum in use, factor of the old sums
+  float column_sum[2][4][kHalf];
+  int32_t limit[2][2][kHalf];  // [parity of the segment][half]: tokens that a column sees
+  int32_t least[2][2];
+  uint64_t full[kMaxSlots], empty[kMaxSlots];
+  uint64_t q_full, q_empty, rest_full, rest_empty, s_full[2], p_full, o_done, token_full[kTokenSlots], all_done;
+  int64_t scan[kThreads / 32];
+  int64_t start_group, tiles;
+  int64_t start_at;
+  uint32_t tmem;
+  uint32_t gave_up;
+};
+
+__device__ __forceinline__ int group_length(const Params& p, int64_t g, bool report) {
+  int most = 0;
+  for (int j = 0; j < p.pack; ++j) most = max(most, row_length(p.R, g * p.pack + j, report));
+  return most;
+}
+
+// Tiles of a unit; one at least, so that every unit is met and its rows written.
+__device__ __forceinline__ int group_tiles(const Params& p, int64_t g, bool report) {
+  if (p.row_tiles) return p.row_tiles;
+  const int n = group_length(p, g, report);
+  return n == 0 ? 1 : (n + kTile - 1) / kTile;
+}
+
+__device__ __forceinline__ int64_t slice_begin(int64_t tiles, int slices, int s) { return tiles * s / slices; }
+__device__ __forceinline__ int slice_of(int64_t tiles, int slices, int64_t x) {
+  return static_cast<int>(((x + 1) * slices - 1) / tiles);
+}
+
+// A slice's run of tiles, walked segment by segment (a segment: the tiles of one unit in the run).
+struct Walk {
+  int64_t group;
+  int64_t left;  // tiles of the run from here on
+  int kv_head, at, tiles;  // the unit, the segment's first tile, the unit's tiles
+  int count;               // tiles of the segment
+  __device__ void size() { count = static_cast<int>(min(static_cast<int64_t>(tiles - at), left)); }
+  __device__ void next(const Params& p) {
+    left -= count;
+    at = 0;
+    if (++kv_head == p.a.kv_heads) {
+      kv_head = 0;
+      ++group;
+      if (left > 0) tiles = group_tiles(p, group, false);
+    }
+    size();
+  }
+};
+
+// Reduces v[c] over the warp's lanes; lane i gets column i % N.
+template <int N, bool kMax>
+__device__ __forceinline__ float reduce_columns(const float (&v)[N], int lane) {
+  float t[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) t[i] = v[i];
+#pragma unroll
+  for (int w = N / 2; w > 0; w >>= 1) {
+    const bool up = lane & w;
+#pragma unroll
+    for (int j = 0; j < w; ++j) {
+      const float keep = up ? t[j + w] : t[j], send = up ? t[j] : t[j + w];
+      const float other = __shfl_xor_sync(~0u, send, w);
+      t[j] = kMax ? fmaxf(keep, other) : keep + other;
+    }
+  }
+#pragma unroll
+  for (int d = N; d < 32; d <<= 1) {
+    const float other = __shfl_xor_sync(~0u, t[0], d);
+    t[0] = kMax ? fmaxf(t[0], other) : t[0] + other;
+  }
+  return t[0];
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (kBf16) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
+    return reinterpret_cast<const uint32_t&>(x);
+  } else {
+    const __half2 x = __floats2half2_rn(lo, hi);
+    return reinterpret_cast<const uint32_t&>(x);
+  }
+}
+
+template <int N, bool kBf16>
+__global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ Params p) {
+  extern __shared__ __align__(1024) uint8_t raw[];
+  const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
+  const uint32_t q_at = base, ring = q_at + p.q_bytes, rest = ring + p.slots * kPiece;
+  const uint32_t p_at = rest + (p.rest && !p.rest_is_p ? kChunk : 0);
+  Smem<N>& sm = *reinterpret_cast<Smem<N>*>(raw + (p_at + kChunk - smem_addr(raw)));
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int block = blockIdx.x % p.blocks, slice = blockIdx.x / p.blocks;
+  const Guard guard{&sm.gave_up, p.R.status};
+
+  if (tid == 0) {
+    for (int i = 0; i < kMaxSlots; ++i) {
+      mbar_init(smem_addr(&sm.full[i]), kCopyThreads);
+      mbar_init(smem_addr(&sm.empty[i]), 1);
+    }
+    mbar_init(smem_addr(&sm.q_full), kCopyThreads);
+    mbar_init(smem_addr(&sm.q_empty), 1);
+    mbar_init(smem_addr(&sm.rest_full), kCopyThreads);
+    mbar_init(smem_addr(&sm.rest_empty), 1);
+    mbar_init(smem_addr(&sm.s_full[0]), 1);
+    mbar_init(smem_addr(&sm.s_full[1]), 1);
+    mbar_init(smem_addr(&sm.p_full), kSoftmaxWarps);
+    mbar_init(smem_addr(&sm.o_done), 1);
+    mbar_init(smem_addr(&sm.all_done), 1);
+    for (int i = 0; i < kTokenSlots; ++i) mbar_init(smem_addr(&sm.token_full[i]), kCopyThreads);
+    sm.gave_up = 0;
+    fence_async();
+  }
+  if (warp == kMmaWarp) tmem_alloc(smem_addr(&sm.tmem), p.tmem_cols);
   dependent_wait();
   dependent_launch();
-  const topk_attention_args& a = p.a;
-  for (int64_t u = blockIdx.x; u < p.R.num_rows * a.heads; u += gridDim.x) {
-    const int64_t row = u / a.heads;
-    const int head = static_cast<int>(u % a.heads), kvh = head / (a.heads / a.kv_heads);
-    const int len = row_length(p.R, row, threadIdx.x == 0);
-    const T* q = static_cast<const T*>(a.q) + row * a.q_row_stride + head * a.q_head_stride;
-    float o[kMaxV / 32] = {}, m = -INFINITY, l = 0;
-    const int n = len == 0 ? 0 : (a.indices ? a.num_indices : len);
-    for (int i = warp; i < n; i += 4) {
-      const int t = a.indices ? a.indices[row * a.index_row_stride + i] : i;
-      if (t < 0 || t >= len) continue;
-      int64_t block;
-      int place;
-      if (!locate(p.R, row_request(p.R, row), t, &block, &place)) continue;
-      const T* k = static_cast<const T*>(a.k) + block * a.k_block_stride + place * a.k_token_stride + kvh * a.k_head_stride;
-      const T* v = a.v ? static_cast<const T*>(a.v) + block * a.v_block_stride + place * a.v_token_stride + kvh * a.v_head_stride : k;
-      float s = 0;
-      for (int d = lane; d < a.dk; d += 32) s += static_cast<float>(q[d]) * static_cast<float>(k[d]);
-      for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
-      s *= a.scale;
-      const float m2 = s > m ? s : m, base = m2 == -INFINITY ? 0.f : m2;
-      const float w = expf(m - base), e = expf(s - base);
-      l = l * w + e;
-      for (int j = 0; j < kMaxV / 32; ++j)
-        if (j * 32 + lane < a.dv) o[j] = o[j] * w + e * static_cast<float>(v[j * 32 + lane]);
+
+  // where this slice's run begins
+  if (p.row_tiles) {
+    if (tid == 0) {
+      sm.tiles = p.row_groups * p.a.kv_heads * p.row_tiles;
+      const int64_t begin = slice_begin(sm.tiles, p.slices, slice), unit = begin / p.row_tiles;
+      sm.start_group = unit / p.a.kv_heads;
+      sm.start_at = begin - sm.start_group * p.a.kv_heads * p.row_tiles;
+    }
+  } else {
+    const int64_t per = (p.row_groups + kThreads - 1) / kThreads;
+    const int64_t g0 = min(per * tid, p.row_groups), g1 = min(g0 + per, p.row_groups);
+    int64_t mine = 0;
+    for (int64_t g = g0; g < g1; ++g) mine += group_tiles(p, g, blockIdx.x == 0);
+    int64_t pre = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t x = __shfl_up_sync(~0u, pre, d);
+      if (lane >= d) pre += x;
+    }
+    if (lane == 31) sm.scan[warp] = pre;
+    __syncthreads();
+    int64_t total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) pre += sm.scan[w];
+      total += sm.scan[w];
+    }
+    total *= p.a.kv_heads;
+    const int64_t begin = slice_begin(total, p.slices, slice);
+    int64_t at = (pre - mine) * p.a.kv_heads;
+    if (begin >= at && begin < pre * p.a.kv_heads) {
+      for (int64_t g = g0; g < g1; ++g) {
+        const int64_t n = static_cast<int64_t>(group_tiles(p, g, false)) * p.a.kv_heads;
+        if (begin < at + n) {
+          sm.start_group = g;
+          sm.start_at = begin - at;
+          break;
+        }
+        at += n;
+      }
+    }
+    if (tid == 0) sm.tiles = total;
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = sm.tmem;
+  const int64_t all_tiles = sm.tiles, run_begin = slice_begin(all_tiles, p.slices, slice);
+  Walk walk;
+  walk.left = slice_begin(all_tiles, p.slices, slice + 1) - run_begin;
+  walk.group = sm.start_group;
+  walk.count = 0;
+  if (walk.left > 0) {
+    walk.tiles = group_tiles(p, walk.group, false);
+    walk.kv_head = static_cast<int>(sm.start_at / walk.tiles);
+    walk.at = static_cast<int>(sm.start_at % walk.tiles);
+    walk.size();
+  }
+  const int k_ring = p.k_pieces - p.rest;                       // pieces of the keys in the ring
+  const int tile_pieces = k_ring + (p.latent ? 0 : p.v_pieces);  // ring pieces of a tile
+  const uint32_t s_cols = static_cast<uint32_t>(p.v_pieces) * N;  // columns before the scores'
+  const int block_cols = min(p.block_cols, p.cols - block * p.block_cols);
+
+  if (warp >= kSoftmaxWarps && warp < kMmaWarp) {
+    // ---- copies -----------------------------------------------------------
+    const int me = tid - kSoftmaxWarps * 32;  // this thread's token of a tile
+    const int sub = lane >> 3, col = lane & 7;
+    uint32_t piece = 0;  // ring pieces begun
+    uint32_t tile = 0, segment = 0;
+    for (; walk.left > 0; walk.next(p), ++segment) {
+      const int64_t row0 = walk.group * p.pack;
+      // the segment's queries, zeros past the block's columns and past dk
+      mbar_wait(smem_addr(&sm.q_empty), (segment & 1) ^ 1, guard);
+      for (int n = me >> 3; n < N; n += kCopyThreads / 8) {
+        const int c = block * p.block_cols + n, j = c / p.group;
+        const uint16_t* q = static_cast<const uint16_t*>(p.a.q);
+        const bool real = n < block_cols;
+        if (real) q += (row0 + j) * p.a.q_row_stride + static_cast<int64_t>(walk.kv_head * p.group + c - j * p.group) * p.a.q_head_stride;
+        const uint32_t dst = q_at + n * 128 + ((col ^ (n & 7)) << 4);
+        for (int ch = 0; ch < p.k_chunks; ++ch) {
+          const int dim = ch * 64 + col * 8;
+          const bool in = real && dim < p.a.dk;
+          copy16(dst + ch * (N * 128), in ? q + dim : static_cast<const uint16_t*>(p.a.q), in ? 16 : 0);
+        }
+      }
+      copies_arrive(smem_addr(&sm.q_full));
+      const int length = group_length(p, walk.group, false);
+      const int64_t request = length > 0 ? row_request(p.R, row0) : 0;
+      const int32_t* list = p.a.indices ? p.a.indices + row0 * p.a.index_row_stride : nullptr;
+      // A tile's tokens are found in two steps, each a tile earlier than its result is used: the position (from
+      // the list), then the block (from the table).
+      const auto listed = [&](int t) {
+        const int i = (walk.at + t) * kTile + me;
+        if (t >= walk.count) return -1;
+        return !list ? i : (i < p.a.num_indices ? list[i] : -1);
+      };
+      const auto column = [&](int x) { return p.R.block_shift >= 0 ? x >> p.R.block_shift : x / p.R.block_size; };
+      const auto table_entry = [&](int x) {
+        return x >= 0 && x < length ? __ldg(p.R.block_table + request * p.R.table_stride + column(x)) : 0;
+      };
+      int at_token = listed(0), at_block = table_entry(at_token), next_token = listed(1);
+      for (int t = 0; t < walk.count; ++t, ++tile) {
+        int pos = INT_MAX, place = 0;
+        if (at_token >= 0 && at_token < length) {
+          place = at_token - column(at_token) * p.R.block_size;
+          if (at_block >= 0 && at_block < p.R.num_blocks)
+            pos = at_token;
+          else
+            atomicOr(p.R.status, TOPK_DEV_BAD_BLOCK);
+        }
+        sm.token[tile % kTokenSlots][me] = pos;
+        mbar_arrive(smem_addr(&sm.token_full[tile % kTokenSlots]));
+        const bool seen = pos != INT_MAX;
+        const uint16_t* kp = static_cast<const uint16_t*>(p.a.k);
+        const uint16_t* vp = static_cast<const uint16_t*>(p.a.v);
+        if (seen) {
+          kp += static_cast<int64_t>(at_block) * p.a.k_block_stride + place * p.a.k_token_stride + walk.kv_head * p.a.k_head_stride;
+          if (!p.latent) vp += static_cast<int64_t>(at_block) * p.a.v_block_stride + place * p.a.v_token_stride + walk.kv_head * p.a.v_head_stride;
+        }
+        const int next_block = table_entry(next_token), later_token = listed(t + 2);
+        const unsigned seen_mask = __ballot_sync(~0u, seen);
+        const auto copy_piece = [&](const uint16_t* ptr, uint32_t dst, int chunk0, int chunks, int dims) {
+          const uint64_t mine = reinterpret_cast<uint64_t>(ptr);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int from = i * 4 + sub, token = (warp - kSoftmaxWarps) * 32 + from;
+            const char* src = reinterpret_cast<const char*>(__shfl_sync(~0u, mine, from));
+            const bool on = (seen_mask >> from) & 1;
+            const uint32_t to = dst + token * 128 + ((col ^ (token & 7)) << 4);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              if (c < chunks) {
+                const int dim = (chunk0 + c) * 64 + col * 8;
+                const bool in = on && dim < dims;
+                copy16(to + c * kChunk, in ? src + dim * 2 : static_cast<const char*>(p.a.k), in ? 16 : 0);
+              }
+            }
+          }
+        };
+        for (int u = 0; u < tile_pieces; ++u, ++piece) {
+          const int slot = piece % p.slots;
+          mbar_wait(smem_addr(&sm.empty[slot]), ((piece / p.slots) & 1) ^ 1, guard);
+          if (u < k_ring)
+            copy_piece(kp, ring + slot * kPiece, u * 2, min(2, p.k_chunks - u * 2), p.a.dk);
+          else
+            copy_piece(vp, ring + slot * kPiece, (u - k_ring) * 2, 2, p.a.dv);
+          copies_arrive(smem_addr(&sm.full[slot]));
+        }
+        if (p.rest) {
+          mbar_wait(smem_addr(&sm.rest_empty), (tile & 1) ^ 1, guard);
+          copy_piece(kp, rest, k_ring * 2, 1, p.a.dk);
+          copies_arrive(smem_addr(&sm.rest_full));
+        }
+        at_token = next_token;
+        at_block = next_block;
+        next_token = later_token;
+      }
+    }
+    copies_wait_all();
+  } else if (warp == kMmaWarp) {
+    // ---- products ---------------------------------------------------------
+    if (lane == 0) {
+      constexpr uint32_t kInstS = instruction(kBf16 ? kBF16 : kF16, N, false);
+      constexpr uint32_t kInstO = instruction(kBf16 ? kBF16 : kF16, N, true);
+      uint32_t tile = 0, segment = 0;
+      // S^T of one tile, into one of its two places
+      const auto scores = [&](uint32_t tl) {
+        const uint32_t d = tmem + s_cols + (tl & 1) * N;
+        bool add = false;
+        for (int u = 0; u < p.k_pieces; ++u) {
+          uint32_t at, piece = 0;
+          if (u < k_ring) {
+            piece = tl * tile_pieces + u;
+            at = ring + (piece % p.slots) * kPiece;
+            mbar_wait(smem_addr(&sm.full[piece % p.slots]), (piece / p.slots) & 1, guard);
+          } else {
+            at = rest;
+            mbar_wait(smem_addr(&sm.rest_full), tl & 1, guard);
+          }
+          fence_async();
+          const int dims = min(p.a.dk - u * 128, 128);
+          for (int k = 0; k * 16 < dims; ++k) {
+            const uint32_t off = (k & 3) * 32, half = k >> 2;
+            mma16(d, operand(at + half * kChunk + off, 16), operand(q_at + (u * 2 + half) * (N * 128) + off, 16), kInstS, add);
+            add = true;
+          }
+          // keys that are no values are done with
+          if (u < k_ring && !(p.latent && u < p.v_pieces)) commit(smem_addr(&sm.empty[piece % p.slots]));
+          if (u >= k_ring && !p.rest_is_p) commit(smem_addr(&sm.rest_empty));
+        }
+        commit(smem_addr(&sm.s_full[tl & 1]));
+      };
+      for (; walk.left > 0; walk.next(p), ++segment) {
+        mbar_wait(smem_addr(&sm.q_full), segment & 1, guard);
+        fence_async();
+        if (p.ahead) scores(tile);
+        for (int t = 0; t < walk.count; ++t, ++tile) {
+          const bool last = t + 1 == walk.count;
+          if (!p.ahead) scores(tile);
+          if (p.ahead && !last) scores(tile + 1);
+          if (p.ahead ? t + 2 == walk.count || walk.count == 1 : last) commit(smem_addr(&sm.q_empty));
+          mbar_wait(smem_addr(&sm.p_full), tile & 1, guard);
+          fence_after();
+          for (int u = 0; u < p.v_pieces; ++u) {
+            const uint32_t piece = tile * tile_pieces + (p.latent ? u : k_ring + u), slot = piece % p.slots;
+            const uint32_t at = ring + slot * kPiece;
+            if (!p.latent) {
+              mbar_wait(smem_addr(&sm.full[slot]), (piece / p.slots) & 1, guard);
+              fence_async();
+            }
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+              mma16(tmem + u * N, operand(at + k * 2048, kChunk), operand(p_at + k * 2048, 1024), kInstO, t > 0 || k > 0);
+            commit(smem_addr(&sm.empty[slot]));
+          }
+          if (p.rest && p.rest_is_p) commit(smem_addr(&sm.rest_empty));
+          commit(smem_addr(&sm.o_done));
+        }
+      }
+      commit(smem_addr(&sm.all_done));
+      mbar_wait(smem_addr(&sm.all_done), 0, guard);
+    }
+    __syncwarp();
+  } else {
+    // ---- softmax and output ------------------------------------------------
+    constexpr int H = N / 2;
+    constexpr float kShift = kBf16 ? 0.f : 7.f;  // fp16: probabilities use the upper half of its range, at most 2^15
+    const int half = warp >> 2, quarter = warp & 3, token = quarter * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    const int my_col = half * H + (lane & (H - 1));  // the column whose statistics this lane keeps
+    uint32_t tile = 0, segment = 0;
+    bool first_segment = true;
+    for (; walk.left > 0; walk.next(p), ++segment) {
+      const int64_t row0 = walk.group * p.pack;
+      if (quarter == 0) {  // what each column sees
+        const int c = block * p.block_cols + my_col;
+        int n = INT_MAX;
+        if (my_col < block_cols) n = row_length(p.R, row0 + c / p.group, p.row_tiles != 0 && block == 0);
+        int least = n;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) least = min(least, __shfl_xor_sync(~0u, least, d));
+        if (lane < H) sm.limit[segment & 1][half][lane] = n == INT_MAX ? 0 : n;
+        if (lane == 0) sm.least[segment & 1][half] = least;
+      }
+      named_sync(1 + half, 128);
+      const int least = sm.least[segment & 1][half];
+      float m = -INFINITY, in_use = 0.f;  // of my_col, in powers of two
+      float l[H];
+#pragma unroll
+      for (int i = 0; i < H; ++i) l[i] = 0.f;
+      for (int t = 0; t < walk.count; ++t, ++tile) {
+        mbar_wait(smem_addr(&sm.token_full[tile % kTokenSlots]), (tile / kTokenSlots) & 1, guard);
+        const int pos = sm.token[tile % kTokenSlots][token];
+        mbar_wait(smem_addr(&sm.s_full[tile & 1]), (tile >> 1) & 1, guard);
+        fence_after();
+        float s[H];
+        tmem_load(tmem + lanes + s_cols + (tile & 1) * N + half * H, s);
+        load_wait(s);
+        if (pos >= least) {
+#pragma unroll
+          for (int i = 0; i < H; ++i)
+            if (pos >= sm.limit[segment & 1][half][i]) s[i] = -INFINITY;
+        }
+        const float warp_max = reduce_columns<H, true>(s, lane);
+        if (lane < H) sm.column_max[tile & 1][half][quarter][lane] = warp_max;
+        named_sync(1 + half, 128);
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) top = fmaxf(top, sm.column_max[tile & 1][half][w][lane & (H - 1)]);
+        top *= p.scale2;
+        const bool move = top > m + kMoveAbove || (m == -INFINITY && top > m);
+        const bool rescale = __any_sync(~0u, move && m > -INFINITY);
+        const float factor = move && m > -INFINITY ? exp2_fast(m - top) : 1.f;
+        if (move) {
+          m = top;
+          in_use = m - kShift;
+        }
+        if (lane < H) {
+          sm.moved[warp][0][lane] = in_use;
+          sm.moved[warp][1][lane] = factor;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < H; i += 4) {
+          const float4 u = *reinterpret_cast<const float4*>(&sm.moved[warp][0][i]);
+          s[i] = exp2_fast(fmaf(s[i], p.scale2, -u.x));
+          s[i + 1] = exp2_fast(fmaf(s[i + 1], p.scale2, -u.y));
+          s[i + 2] = exp2_fast(fmaf(s[i + 2], p.scale2, -u.z));
+          s[i + 3] = exp2_fast(fmaf(s[i + 3], p.scale2, -u.w));
+        }
+        // the last tile's product has read P and written O
+        if (tile > 0) mbar_wait(smem_addr(&sm.o_done), (tile - 1) & 1, guard);
+        fence_after();
+        if (rescale) {  // the same for all warps of this half: they hold the same maxima
+#pragma unroll
+          for (int i = 0; i < H; ++i) l[i] *= sm.moved[warp][1][i];
+          for (int u = 0; u < p.v_pieces; ++u) {
+#pragma unroll
+            for (int i = 0; i < H; i += 8) {
+              float o[8];
+              const uint32_t at = tmem + lanes + u * N + half * H + i;
+              tmem_load(at, o);
+              load_wait(o);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) o[j] *= sm.moved[warp][1][i + j];
+              tmem_store8(at, o);
+            }
+          }
+          store_wait();
+        }
+#pragma unroll
+        for (int i = 0; i < H; ++i) l[i] += s[i];
+        const uint32_t row = p_at + token * 128;
+#pragma unroll
+        for (int i = 0; i < H; i += 8) {
+          const uint32_t at = row + ((((half * H + i) >> 3) ^ (token & 7)) << 4);
+          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(pack2<kBf16>(s[i], s[i + 1])),
+                       "r"(pack2<kBf16>(s[i + 2], s[i + 3])), "r"(pack2<kBf16>(s[i + 4], s[i + 5])),
+                       "r"(pack2<kBf16>(s[i + 6], s[i + 7]))
+                       : "memory");
+        }
+        fence_async();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sm.p_full));
+      }
+      // the segment's sums
+      const float part_l = reduce_columns<H, false>(l, lane);
+      if (lane < H) sm.column_sum[half][quarter][lane] = part_l;
+      named_sync(1 + half, 128);
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) sum += sm.column_sum[half][w][lane & (H - 1)];
+      const bool whole = walk.count == walk.tiles;
+      const int64_t slot = ((static_cast<int64_t>(slice) * 2 + (first_segment ? 0 : 1)) * p.blocks + block) * N;
+      if (lane < H) sm.moved[warp][0][lane] = sum == 0.f ? 0.f : (whole ? 1.f / sum : 1.f);
+      if (quarter == 0 && lane < H) {
+        if (!whole) {
+          p.stat[slot + my_col] = make_float2(m == -INFINITY ? -INFINITY : in_use, sum);
+        } else if (p.a.lse && my_col < block_cols) {
+          const int c = block * p.block_cols + my_col, j = c / p.group;
+          p.a.lse[(row0 + j) * p.a.heads + walk.kv_head * p.group + c - j * p.group] =
+              sum == 0.f ? -INFINITY : (in_use + log2f(sum)) * 0.69314718055994531f;
+        }
+      }
+      __syncwarp();
+      mbar_wait(smem_addr(&sm.o_done), (tile - 1) & 1, guard);
+      fence_after();
+      for (int u = 0; u < p.v_pieces; ++u) {
+        float o[H];
+        tmem_load(tmem + lanes + u * N + half * H, o);
+        load_wait(o);
+        const int dim = u * 128 + token;
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+          const float f = sm.moved[warp][0][i];
+          o[i] = f == 0.f ? 0.f : o[i] * f;
+        }
+        if (!whole) {
+          float* to = p.part + (slot + half * H) * (p.v_pieces * 128) + dim;
+#pragma unroll
+          for (int i = 0; i < H; ++i)
+            if (half * H + i < block_cols) to[static_cast<int64_t>(i) * (p.v_pieces * 128)] = o[i];
+        } else {
+          // two columns at a time: neighbouring lanes exchange values and store pairs of dims
+#pragma unroll
+          for (int i = 0; i < H; i += 2) {
+            const bool odd = lane & 1;
+            const float other = __shfl_xor_sync(~0u, odd ? o[i] : o[i + 1], 1);
+            const int n = half * H + i + odd;
+            const int c = block * p.block_cols + n, j = c / p.group;
+            const int d = dim - odd;
+            if (n < block_cols && d < p.a.dv) {
+              uint16_t* to = static_cast<uint16_t*>(p.a.out) + (row0 + j) * p.a.out_row_stride +
+                             static_cast<int64_t>(walk.kv_head * p.group + c - j * p.group) * p.a.out_head_stride + d;
+              *reinterpret_cast<uint32_t*>(to) = odd ? pack2<kBf16>(other, o[i + 1]) : pack2<kBf16>(o[i], other);
+            }
+          }
+        }
+      }
+      fence_before();
+      if (tid == 0 && block == 0 && first_segment) {  // a unit that began before this slice and ends in it
+        Join j{};
+        j.last = -1;
+        if (walk.at > 0 && walk.at + walk.count == walk.tiles) {
+          const int64_t unit_begin = run_begin - walk.at;
+          j.rowgroup = walk.group;
+          j.kv_head = walk.kv_head;
+          j.first = slice_of(all_tiles, p.slices, unit_begin);
+          j.last = slice;
+          j.first_slot = slice_begin(all_tiles, p.slices, j.first) == unit_begin ? 0 : 1;
+          j.tiles = all_tiles;
+        }
+        p.join[slice] = j;
+      }
+      first_segment = false;
+    }
+    if (first_segment && tid == 0 && block == 0) {  // an empty run
+      Join j{};
+      j.last = -1;
+      p.join[slice] = j;
+    }
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == kMmaWarp) tmem_free(tmem, p.tmem_cols);
+}
+
+// Joins the parts of the units that fell into several slices: eight columns of a unit a CTA.
+template <int N, bool kBf16>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Params p) {
+  dependent_wait();
+  dependent_launch();
+  const int per = N / kJoinCols;
+  const int slice = blockIdx.x / (p.blocks * per), block = blockIdx.x / per % p.blocks, col0 = blockIdx.x % per * kJoinCols;
+  const Join jn = p.join[slice];
+  if (jn.last < 0) return;
+  const int width = p.v_pieces * 128;
+  const int block_cols = min(p.block_cols, p.cols - block * p.block_cols);
+  const int64_t row0 = jn.rowgroup * p.pack;
+  for (int n = col0; n < min(col0 + kJoinCols, block_cols); ++n) {
+    float m = -INFINITY, sum = 0.f;
+    for (int s = jn.first; s <= jn.last; ++s) {
+      if (slice_begin(jn.tiles, p.slices, s) == slice_begin(jn.tiles, p.slices, s + 1)) continue;
+      const int64_t slot = ((static_cast<int64_t>(s) * 2 + (s == jn.first ? jn.first_slot : 0)) * p.blocks + block) * N;
+      const float2 st = p.stat[slot + n];
+      const float m2 = fmaxf(m, st.x), b = m2 == -INFINITY ? 0.f : m2;
+      sum = sum * exp2f(m - b) + st.y * exp2f(st.x - b);
       m = m2;
     }
-    for (int j = 0; j < kMaxV / 32; ++j) acc[warp][j * 32 + lane] = o[j];
-    sum_m[warp] = m;
-    sum_l[warp] = l;
-    __syncthreads();
-    float mm = -INFINITY, ll = 0;
-    for (int w = 0; w < 4; ++w) mm = fmaxf(mm, sum_m[w]);
-    const float base = mm == -INFINITY ? 0.f : mm;
-    for (int w = 0; w < 4; ++w) ll += sum_l[w] * expf(sum_m[w] - base);
-    T* out = static_cast<T*>(a.out) + row * a.out_row_stride + head * a.out_head_stride;
-    for (int d = threadIdx.x; d < a.dv; d += kThreads) {
-      float x = 0;
-      for (int w = 0; w < 4; ++w) x += acc[w][d] * expf(sum_m[w] - base);
-      out[d] = static_cast<T>(ll == 0.f ? 0.f : x / ll);
+    const float b = m == -INFINITY ? 0.f : m, inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int c = block * p.block_cols + n, j = c / p.group;
+    const int64_t head = jn.kv_head * p.group + c - j * p.group;
+    if (p.a.lse && threadIdx.x == 0) p.a.lse[(row0 + j) * p.a.heads + head] = sum == 0.f ? -INFINITY : (b + log2f(sum)) * 0.69314718055994531f;
+    for (int d = threadIdx.x * 4; d < p.a.dv; d += kJoinThreads * 4) {
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int s = jn.first; s <= jn.last; ++s) {
+        if (slice_begin(jn.tiles, p.slices, s) == slice_begin(jn.tiles, p.slices, s + 1)) continue;
+        const int64_t slot = ((static_cast<int64_t>(s) * 2 + (s == jn.first ? jn.first_slot : 0)) * p.blocks + block) * N;
+        const float f = exp2f(p.stat[slot + n].x - b);
+        const float4 y = *reinterpret_cast<const float4*>(p.part + (slot + n) * width + d);
+        x.x += f * y.x;
+        x.y += f * y.y;
+        x.z += f * y.z;
+        x.w += f * y.w;
+      }
+      uint2 packed;
+      if (sum == 0.f) x = make_float4(0.f, 0.f, 0.f, 0.f);
+      packed.x = pack2<kBf16>(x.x * inv, x.y * inv);
+      packed.y = pack2<kBf16>(x.z * inv, x.w * inv);
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.a.out) + (row0 + j) * p.a.out_row_stride + head * p.a.out_head_stride + d) = packed;
     }
-    if (a.lse && threadIdx.x == 0) a.lse[row * a.heads + head] = ll == 0.f ? -INFINITY : base + logf(ll);
-    __syncthreads();
   }
+}
+
+constexpr size_t kJoinBytes = sizeof(Join);
+
+// CTAs of a launch: one on each SM, or one for each column block where there are more of those.
+int most_ctas(int sms) { return sms > 16 ? sms : 16; }
+
+size_t workspace_for(int sms) {
+  const size_t slots = static_cast<size_t>(most_ctas(sms)) * 2;
+  return TOPK_PAGED_WORKSPACE_BYTES + (most_ctas(sms) * kJoinBytes + 255) / 256 * 256 + slots * kMaxBlockCols * (kMaxV * sizeof(float) + sizeof(float2));
+}
+
+static_assert(sizeof(Smem<64>) + 1024 + 9 * 64 * 128 + 4 * kPiece + kChunk <= 232448, "latent attention of 64 columns: four pieces of the ring");
+
+template <int N, bool kBf16>
+int run(Params& p, int smem_limit, bool joins, cudaStream_t stream) {
+  const int extra = static_cast<int>(sizeof(Smem<N>)) + 1024;
+  p.q_bytes = p.k_chunks * N * 128;
+  p.rest_is_p = 0;
+  int room = smem_limit - extra - static_cast<int>(p.q_bytes) - kChunk;  // for the ring and, where it is not P, the rest
+  if (p.rest) {
+    // a buffer of its own for the rest lets the next tile's last keys come early, if the ring loses nothing by it
+    p.rest_is_p = (room - kChunk) / kPiece < room / kPiece;
+    if (!p.rest_is_p) room -= kChunk;
+  }
+  p.slots = room / kPiece < kMaxSlots ? room / kPiece : kMaxSlots;
+  const int k_ring = p.k_pieces - p.rest, tile_pieces = k_ring + (p.latent ? 0 : p.v_pieces);
+  if (p.slots < (p.latent ? tile_pieces : 1)) return TOPK_ERR_PLAN;
+  p.ahead = !p.rest_is_p && p.slots >= tile_pieces + k_ring;
+  p.tmem_cols = 32;
+  while (p.tmem_cols < static_cast<uint32_t>((p.v_pieces + 2) * N)) p.tmem_cols *= 2;
+  const size_t smem = p.q_bytes + static_cast<size_t>(p.slots) * kPiece + (p.rest && !p.rest_is_p ? kChunk : 0) + kChunk + extra;
+  if (cudaFuncSetAttribute(attention_kernel<N, kBf16>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) {
+    cudaGetLastError();
+    return TOPK_ERR_CUDA;
+  }
+  int rc = launch(attention_kernel<N, kBf16>, static_cast<const Params&>(p), static_cast<int64_t>(p.slices) * p.blocks, kThreads, smem, stream);
+  if (rc != TOPK_OK || !joins) return rc;
+  return launch(join_kernel<N, kBf16>, static_cast<const Params&>(p), static_cast<int64_t>(p.slices) * p.blocks * (N / kJoinCols), kJoinThreads, 0, stream);
 }
 
 }  // namespace
@@ -75,7 +718,7 @@ __global__ void __launch_bounds__(kThreads) paged_attention_kernel(const Attenti
 extern "C" size_t topk_attention_workspace_size(int device) {
   topk_device_props p{};
   if (topk_query_device(device, &p) != TOPK_OK) return 0;
-  return TOPK_PAGED_WORKSPACE_BYTES;
+  return ltk::paged::workspace_for(p.num_sms);
 }
 
 extern "C" int topk_paged_attention(const topk_attention_args* args, void* stream) {
@@ -84,8 +727,10 @@ extern "C" int topk_paged_attention(const topk_attention_args* args, void* strea
   const topk_attention_args& a = *args;
   int rc = check_rows(a.rows);
   if (rc != TOPK_OK) return rc;
-  if (!(a.scale > 0.f) || a.scale > 3.4e38f || a.heads < 1 || a.kv_heads < 1 || a.heads % a.kv_heads != 0) return TOPK_ERR_INVALID_ARG;
-  if (a.indices != nullptr && (a.num_indices < 1 || a.num_indices > (1 << 20) || a.index_row_stride < 0)) return TOPK_ERR_INVALID_ARG;
+  if (!(a.scale > 0.f) || a.scale > 3.4e38f || a.heads < 1 || a.kv_heads < 1 || a.heads % a.kv_heads != 0)
+    return TOPK_ERR_INVALID_ARG;
+  if (a.indices != nullptr && (a.num_indices < 1 || a.num_indices > (1 << 20) || a.index_row_stride < 0))
+    return TOPK_ERR_INVALID_ARG;
   if ((a.dtype != TOPK_DTYPE_F16 && a.dtype != TOPK_DTYPE_BF16) || a.heads > 1024 || a.dk < 8 || a.dk > kMaxQk || a.dk % 8 ||
       a.dv < 8 || a.dv > kMaxV || a.dv % 8 || (a.v == nullptr && a.dv > a.dk))
     return TOPK_ERR_UNSUPPORTED;
@@ -98,14 +743,51 @@ extern "C" int topk_paged_attention(const topk_attention_args* args, void* strea
       misaligned(a.indices, 4) || misaligned(a.lse, 4) || misaligned(a.workspace, 16) ||
       (a.v && (misaligned(a.v, 16) || a.v_block_stride % 8 || a.v_token_stride % 8 || a.v_head_stride % 8)))
     return TOPK_ERR_MISALIGNED;
-  const int sms = num_sms();
-  if (sms < 1) return TOPK_ERR_CUDA;
-  if (a.workspace_bytes < TOPK_PAGED_WORKSPACE_BYTES) return TOPK_ERR_WORKSPACE_TOO_SMALL;
-  AttentionParams p{};
+  int dev = 0;
+  topk_device_props props{};
+  if (cudaGetDevice(&dev) != cudaSuccess || topk_query_device(dev, &props) != TOPK_OK) {
+    cudaGetLastError();
+    return TOPK_ERR_CUDA;
+  }
+  const int sms = props.num_sms;
+  if (a.workspace_bytes < workspace_for(sms)) return TOPK_ERR_WORKSPACE_TOO_SMALL;
+
+  Params p{};
   p.a = a;
   p.R = make_rows(a.rows, INT32_MAX, a.workspace);
-  const int64_t units = a.rows.num_rows * a.heads, grid = units < sms * 8 ? units : sms * 8;
+  p.group = a.heads / a.kv_heads;
+  // the rows of a request share its tokens, unless index lists tell them apart
+  p.pack = a.indices == nullptr && a.rows.row_request == nullptr && a.rows.next_n * static_cast<int64_t>(p.group) <= 1024 ? a.rows.next_n : 1;
+  p.cols = p.pack * p.group;
+  p.blocks = (p.cols + kMaxBlockCols - 1) / kMaxBlockCols;
+  p.block_cols = (p.cols + p.blocks - 1) / p.blocks;
+  p.k_chunks = (a.dk + 63) / 64;
+  p.k_pieces = (p.k_chunks + 1) / 2;
+  p.v_pieces = (a.dv + 127) / 128;
+  p.latent = a.v == nullptr;
+  p.rest = p.latent && p.k_chunks % 2 == 1 && p.k_pieces > p.v_pieces;
+  p.row_groups = a.rows.num_rows / p.pack;
+  p.row_tiles = a.indices ? (a.num_indices + kTile - 1) / kTile : 0;
+  p.scale2 = a.scale * 1.4426950408889634f;
+  const int64_t units = p.row_groups * a.kv_heads;
+  const int64_t most = units * (a.indices ? p.row_tiles : (p.R.max_len + kTile - 1) / kTile);
+  int64_t slices = sms / p.blocks < 1 ? 1 : sms / p.blocks;
+  if (slices > most) slices = most;
+  p.slices = static_cast<int32_t>(slices);
+  bool joins = true;
+  if (p.row_tiles) {  // every unit has as many tiles: the host can see whether a slice begins inside one
+    joins = false;
+    for (int s = 1; s < p.slices; ++s) joins = joins || (units * p.row_tiles * s / p.slices) % p.row_tiles != 0;
+  }
+  char* w = static_cast<char*>(a.workspace) + TOPK_PAGED_WORKSPACE_BYTES;
+  p.join = reinterpret_cast<Join*>(w);
+  w += (most_ctas(sms) * kJoinBytes + 255) / 256 * 256;
+  p.stat = reinterpret_cast<float2*>(w);
+  w += static_cast<size_t>(most_ctas(sms)) * 2 * kMaxBlockCols * sizeof(float2);
+  p.part = reinterpret_cast<float*>(w);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (a.dtype == TOPK_DTYPE_F16) return launch(paged_attention_kernel<__half>, p, grid, kThreads, 0, s);
-  return launch(paged_attention_kernel<__nv_bfloat16>, p, grid, kThreads, 0, s);
+  const bool bf = a.dtype == TOPK_DTYPE_BF16;
+  if (p.block_cols <= 16) return bf ? run<16, true>(p, props.max_smem_optin, joins, s) : run<16, false>(p, props.max_smem_optin, joins, s);
+  if (p.block_cols <= 32) return bf ? run<32, true>(p, props.max_smem_optin, joins, s) : run<32, false>(p, props.max_smem_optin, joins, s);
+  return bf ? run<64, true>(p, props.max_smem_optin, joins, s) : run<64, false>(p, props.max_smem_optin, joins, s);
 }

@@ -1,0 +1,197 @@
+// The instructions that the tensor-core kernels of the paged calls use:
+// mbarriers, asynchronous copies into shared memory, tcgen05 products with
+// their operands in shared memory and their sums in tensor memory.
+//
+// Operand tiles are stored as the 128-byte swizzle wants them: rows of 128
+// bytes, in groups of eight rows (1024 bytes, aligned to that), the 16-byte
+// piece c of row r at place c ^ (r & 7). Such a tile serves as a K-major operand
+// (its rows run along M or N, its bytes along K) and as an MN-major one (its rows
+// run along K): the same keys are the A operand of K Q^T and, read the other
+// way, of V^T P^T.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "libtopk.h"
+
+namespace ltk {
+namespace umma {
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
+// A CTA's waits. One that runs out sets the flag, after which every wait of the CTA returns at once: the
+// loops run to their end without waiting, over memory that stays in bounds, and the launch's status says
+// that its results are void.
+struct Guard {
+  volatile uint32_t* gave_up;  // shared memory
+  uint32_t* status;
+};
+
+constexpr uint64_t kWaitLimitNs = 1000ull * 1000ull * 1000ull;
+
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+  return t;
+}
+
+__device__ __noinline__ void mbar_wait_slow(uint32_t bar, uint32_t parity, volatile uint32_t* gave_up, uint32_t* status) {
+  const uint64_t t0 = now_ns();
+  while (!mbar_try(bar, parity)) {
+    if (*gave_up) return;
+    if (now_ns() - t0 > kWaitLimitNs) {
+      *gave_up = 1;
+      atomicOr(status, TOPK_DEV_PIPELINE_TIMEOUT);
+      return;
+    }
+  }
+}
+
+__device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, const Guard& g) {
+  if (!mbar_try(bar, parity)) mbar_wait_slow(bar, parity, g.gave_up, g.status);
+}
+
+// 16 bytes into shared memory; `bytes` 0 writes zeros and reads nothing.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// One arrival on `bar` when every copy that this thread has begun has landed.
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void copies_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Orders this thread's (and, after a barrier, others') writes to shared memory before the tensor cores' reads.
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// ---- tensor memory --------------------------------------------------------
+
+__device__ __forceinline__ void tmem_alloc(uint32_t where, uint32_t columns) {  // a whole warp
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(where), "r"(columns) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_free(uint32_t base, uint32_t columns) {  // the same warp
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(columns) : "memory");
+}
+
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Waits for this thread's loads from tensor memory; `v` may be used afterwards, not before.
+template <int N>
+__device__ __forceinline__ void load_wait(float (&v)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
+}
+__device__ __forceinline__ void store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Columns [addr, addr + 8) of this warp's 32 lanes; a thread gets its lane's. load_wait() before they are used.
+__device__ __forceinline__ void tmem_load8(uint32_t addr, float* v) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+               : "r"(addr));
+}
+
+__device__ __forceinline__ void tmem_load16(uint32_t addr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(addr));
+}
+
+__device__ __forceinline__ void tmem_load32(uint32_t addr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(addr));
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[N]) {
+  static_assert(N == 8 || N == 16 || N == 32);
+  if constexpr (N == 8) tmem_load8(addr, v);
+  if constexpr (N == 16) tmem_load16(addr, v);
+  if constexpr (N == 32) tmem_load32(addr, v);
+}
+
+__device__ __forceinline__ void tmem_store8(uint32_t addr, const float* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "f"(v[0]), "f"(v[1]),
+               "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
+// ---- products -------------------------------------------------------------
+
+// Descriptor of an operand tile at shared-memory address `addr` (16-byte aligned), 128-byte swizzle, groups of
+// eight rows 1024 bytes apart. `leading` matters to MN-major operands of more than 64 elements only: bytes
+// from one 128-byte column of the tile to the next.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t leading) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | (static_cast<uint64_t>((leading >> 4) & 0x3FFF) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+enum Format : uint32_t { kF16 = 0, kBF16 = 1, kE4M3 = 0 };
+
+// Instruction descriptor: fp32 sums, M = 128, N columns, both operands of one format; `mn_major`: both are MN-major.
+__host__ __device__ constexpr uint32_t instruction(uint32_t format, uint32_t n, bool mn_major) {
+  return (1u << 4) | (format << 7) | (format << 10) | (mn_major ? (1u << 15) | (1u << 16) : 0u) | ((n >> 3) << 17) |
+         ((128u >> 4) << 24);
+}
+
+// One thread: D (tensor memory) = A B, or D += A B. K = 16 elements of two bytes.
+__device__ __forceinline__ void mma16(uint32_t d, uint64_t a, uint64_t b, uint32_t inst, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(inst), "r"(static_cast<uint32_t>(add))
+      : "memory");
+}
+
+// The same for 8-bit elements: K = 32.
+__device__ __forceinline__ void mma8(uint32_t d, uint64_t a, uint64_t b, uint32_t inst, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(inst), "r"(static_cast<uint32_t>(add))
+      : "memory");
+}
+
+// One arrival on `bar` when every product that this thread has issued is done.
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+}  // namespace umma
+}  // namespace ltk
