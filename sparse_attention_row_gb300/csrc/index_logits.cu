@@ -1,53 +1,436 @@
-// Logits of the sparse-attention indexer over a paged key cache:
+// Logits of the sparse-attention indexer over a paged key cache
+// (topk_index_logits), on the tensor cores:
 //   logits[r, t] = s_t * sum_h w[r, h] * max(0, q[r, h, :] . k[t, :]).
-// One thread a (row, token): plain fp32.
-#include <cuda_fp8.h>
-
+//
+// A unit is a few consecutive rows; where they belong to one request (drafted
+// tokens, a prompt's piece) they share a pass over its keys, otherwise each has a
+// pass of its own. A pass takes tiles of 128 tokens: one product
+//   S^T [128 tokens x N] = K [128 x dim] . Q^T [dim x N],  N = rows x heads <= 256,
+// puts a token's scores for all rows and heads in one lane of tensor memory, so
+// that the weighted sum over the heads is one thread's own: no exchange at all.
+// Two places of 256 columns let one tile's sums run while the next is multiplied.
+//
+// The units' tiles are dealt in equal runs to the CTAs, one on each SM; every CTA
+// sums up the rows' tiles to find its run. Rows are independent over the tokens,
+// so nothing has to be joined.
+//
+// Roles in a CTA (13 warps): 4 copy keys into a ring of 128-token tiles with
+// 16-byte asynchronous copies (any page size and stride; zeros where there is no
+// token), 1 thread issues the products, two groups of 4 warps take the tiles in
+// turn, a thread per token.
 #include "paged.cuh"
+#include "umma.cuh"
 
 namespace ltk {
 namespace paged {
 namespace {
 
-constexpr int kThreads = 128;
+using namespace ltk::umma;
 
-struct LogitsParams {
+constexpr int kTile = 128;
+constexpr int kChunk = 128 * 128;  // bytes of 128 tokens x 128 bytes
+constexpr int kSumWarps = 8, kCopyWarps = 4;
+constexpr int kCopyThreads = kCopyWarps * 32;
+constexpr int kMmaWarp = kSumWarps + kCopyWarps;
+constexpr int kThreads = (kMmaWarp + 1) * 32;
+constexpr int kMaxSlots = 8;
+constexpr int kTokenSlots = 16;  // more than the tiles that the copies can be ahead of the sums: ring slots + 3
+constexpr int kSegmentSlots = 4;  // a segment's weights are written when at most two segments are still being summed
+constexpr int kMaxCols = 256, kMaxRows = 16;
+
+struct Params {
   topk_index_logits_args a;
   Rows R;
+  int32_t pack;      // rows of a unit
+  int32_t head_cols; // columns of a row: heads rounded up to 16
+  int32_t row_bytes; // of a key
+  int32_t chunks;    // of 128 bytes
+  int32_t slots;
+  int32_t slices;
+  int64_t units;
+  uint32_t q_bytes;
+  uint32_t inst;     // instruction descriptor without N
 };
 
-template <typename T>
-__device__ __forceinline__ float as_float(T x) { return static_cast<float>(x); }
+struct Smem {
+  float scale[kTokenSlots][kTile];
+  uint8_t found[kTokenSlots][kTile];
+  float weight[kSegmentSlots][kMaxCols];
+  int32_t length[kSegmentSlots][kMaxRows];
+  uint64_t full[kMaxSlots], empty[kMaxSlots];
+  uint64_t q_full, q_empty, s_full[2], s_empty[2], token_full[kTokenSlots], segment_full[kSegmentSlots], all_done;
+  int64_t scan[kThreads / 32];
+  int64_t start_unit, start_at, tiles;
+  uint32_t tmem, gave_up;
+};
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) index_logits_kernel(const LogitsParams p) {
-  __shared__ float q[128 * 128];
-  dependent_wait();
-  dependent_launch();
-  const topk_index_logits_args& a = p.a;
-  for (int64_t row = blockIdx.x; row < p.R.num_rows; row += gridDim.x) {
-    const int len = row_length(p.R, row, threadIdx.x == 0);
-    const T* qr = static_cast<const T*>(a.q) + row * a.q_row_stride;
-    __syncthreads();
-    for (int i = threadIdx.x; i < a.heads * a.dim; i += kThreads) q[i] = as_float(qr[(i / a.dim) * a.q_head_stride + i % a.dim]);
-    __syncthreads();
-    for (int t = threadIdx.x; t < len; t += kThreads) {
-      int64_t block;
-      int place;
-      float sum = -INFINITY;
-      if (locate(p.R, row_request(p.R, row), t, &block, &place)) {
-        const T* k = static_cast<const T*>(a.keys) + block * a.key_block_stride + place * a.key_token_stride;
-        sum = 0;
-        for (int h = 0; h < a.heads; ++h) {
-          float dot = 0;
-          for (int d = 0; d < a.dim; ++d) dot += q[h * a.dim + d] * as_float(k[d]);
-          sum += a.weights[row * a.weight_row_stride + h] * (dot < 0 ? 0 : dot);
-        }
-        if (a.key_scales) sum *= a.key_scales[block * a.scale_block_stride + place * a.scale_token_stride];
+__device__ __forceinline__ int tiles_of(int length) { return (length + kTile - 1) / kTile; }
+
+// The rows of a unit: whether those that see anything have one request, and the unit's tiles.
+struct Unit {
+  int64_t row0;
+  int rows;
+  bool shared;
+  int64_t tiles;
+  __device__ Unit(const Params& p, int64_t u, bool report) {
+    row0 = u * p.pack;
+    rows = static_cast<int>(min(static_cast<int64_t>(p.pack), p.R.num_rows - row0));
+    shared = true;
+    int most = 0;
+    int64_t sum = 0, request = -1;
+    for (int j = 0; j < rows; ++j) {
+      const int n = row_length(p.R, row0 + j, report);
+      if (n == 0) continue;
+      most = max(most, n);
+      sum += tiles_of(n);
+      const int64_t b = row_request(p.R, row0 + j);
+      if (request >= 0 && b != request) shared = false;
+      request = b;
+    }
+    tiles = shared ? tiles_of(most) : sum;
+  }
+};
+
+// A slice's run of tiles, segment by segment (a segment: the tiles of one pass in the run).
+struct Walk {
+  int64_t unit, left;
+  int64_t row0;      // of the pass
+  int64_t request;
+  int first, rows;   // the pass's rows within the unit
+  int unit_rows;
+  bool shared;
+  int at, count, longest;
+  __device__ void pass(const Params& p, int from) {  // the pass that begins with the unit's row `from` or a later one
+    longest = 0;
+    first = from;
+    rows = 0;
+    if (shared) {
+      if (from > 0) return;
+      rows = unit_rows;
+      for (int j = 0; j < rows; ++j) {
+        const int n = row_length(p.R, row0 + j, false);
+        if (n > 0) request = row_request(p.R, row0 + j);
+        longest = max(longest, n);
       }
-      a.logits[row * a.logits_row_stride + t] = sum;
+    } else {
+      for (; first < unit_rows; ++first) {
+        longest = row_length(p.R, row0 + first, false);
+        if (longest > 0) {
+          rows = 1;
+          request = row_request(p.R, row0 + first);
+          return;
+        }
+      }
     }
   }
+  __device__ void enter(const Params& p, int64_t u) {
+    const Unit x(p, u, false);
+    unit = u;
+    row0 = x.row0;
+    unit_rows = x.rows;
+    shared = x.shared;
+    pass(p, 0);
+  }
+  __device__ void size() { count = static_cast<int>(min(static_cast<int64_t>(tiles_of(longest) - at), left)); }
+  __device__ void start(const Params& p, int64_t u, int64_t offset) {
+    enter(p, u);
+    while (offset >= tiles_of(longest)) {
+      offset -= tiles_of(longest);
+      pass(p, first + 1);
+    }
+    at = static_cast<int>(offset);
+    size();
+  }
+  __device__ void next(const Params& p) {
+    left -= count;
+    at = 0;
+    if (left <= 0) return;
+    pass(p, shared ? 1 : first + 1);
+    while (longest == 0) enter(p, unit + 1);  // there are tiles left, so some later unit has them
+    size();
+  }
+};
+
+__device__ __forceinline__ float relu(float x) {
+  float y;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The weighted sums of one tile for this thread's token, `C` columns at a time.
+template <int C>
+__device__ __forceinline__ void sum_tile(const Params& p, uint32_t at, const float* weight, const int32_t* length, int rows,
+                                         int pos, float scale, bool found, int64_t row0) {
+  float v[2][C];
+  const int cols = rows * p.head_cols;
+  tmem_load(at, v[0]);
+  int row = 0, in_row = 0;
+  float sum = 0.f;
+  const auto take = [&](float (&x)[C], int c) {
+    // columns past the heads hold zeros times a key: not numbers where the key is none
+    const int real = min(C, p.a.heads - in_row);
+    float s0 = 0.f, s1 = 0.f;
+    if (real == C) {
+#pragma unroll
+      for (int i = 0; i < C; i += 4) {
+        const float4 w = *reinterpret_cast<const float4*>(weight + c + i);
+        s0 = fmaf(w.x, relu(x[i]), s0);
+        s1 = fmaf(w.y, relu(x[i + 1]), s1);
+        s0 = fmaf(w.z, relu(x[i + 2]), s0);
+        s1 = fmaf(w.w, relu(x[i + 3]), s1);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+        if (i < real) s0 = fmaf(weight[c + i], relu(x[i]), s0);
+    }
+    sum += s0 + s1;
+    in_row += C;
+    if (in_row == p.head_cols) {
+      if (pos < length[row]) p.a.logits[(row0 + row) * p.a.logits_row_stride + pos] = found ? sum * scale : -INFINITY;
+      ++row;
+      in_row = 0;
+      sum = 0.f;
+    }
+  };
+  for (int c = 0; c < cols; c += 2 * C) {
+    load_wait(v[0]);
+    if (c + C < cols) tmem_load(at + c + C, v[1]);
+    take(v[0], c);
+    if (c + C < cols) {
+      load_wait(v[1]);
+      if (c + 2 * C < cols) tmem_load(at + c + 2 * C, v[0]);
+      take(v[1], c + C);
+    }
+  }
+}
+
+template <bool k8Bit>
+__global__ void __launch_bounds__(kThreads, 1) index_logits_kernel(const __grid_constant__ Params p) {
+  extern __shared__ __align__(1024) uint8_t raw[];
+  const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
+  const uint32_t q_at = base, ring = q_at + p.q_bytes, slot_bytes = p.chunks * kChunk;
+  Smem& sm = *reinterpret_cast<Smem*>(raw + (ring + p.slots * slot_bytes - smem_addr(raw)));
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, slice = blockIdx.x;
+  const Guard guard{&sm.gave_up, p.R.status};
+  if (tid == 0) {
+    for (int i = 0; i < kMaxSlots; ++i) {
+      mbar_init(smem_addr(&sm.full[i]), kCopyThreads);
+      mbar_init(smem_addr(&sm.empty[i]), 1);
+    }
+    mbar_init(smem_addr(&sm.q_full), kCopyThreads);
+    mbar_init(smem_addr(&sm.q_empty), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&sm.s_full[i]), 1);
+      mbar_init(smem_addr(&sm.s_empty[i]), kSumWarps / 2);
+    }
+    for (int i = 0; i < kTokenSlots; ++i) mbar_init(smem_addr(&sm.token_full[i]), kCopyThreads);
+    for (int i = 0; i < kSegmentSlots; ++i) mbar_init(smem_addr(&sm.segment_full[i]), kCopyThreads);
+    mbar_init(smem_addr(&sm.all_done), 1);
+    sm.gave_up = 0;
+    fence_async();
+  }
+  if (warp == kMmaWarp) tmem_alloc(smem_addr(&sm.tmem), 2 * kMaxCols);
+  dependent_wait();
+  dependent_launch();
+  {  // where this slice's run begins
+    const int64_t per = (p.units + kThreads - 1) / kThreads;
+    const int64_t u0 = min(per * tid, p.units), u1 = min(u0 + per, p.units);
+    int64_t mine = 0;
+    for (int64_t u = u0; u < u1; ++u) mine += Unit(p, u, slice == 0).tiles;
+    int64_t pre = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t x = __shfl_up_sync(~0u, pre, d);
+      if (lane >= d) pre += x;
+    }
+    if (lane == 31) sm.scan[warp] = pre;
+    __syncthreads();
+    int64_t total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) pre += sm.scan[w];
+      total += sm.scan[w];
+    }
+    const int64_t begin = total * slice / p.slices;
+    int64_t at = pre - mine;
+    if (begin >= at && begin < pre) {
+      for (int64_t u = u0; u < u1; ++u) {
+        const int64_t n = Unit(p, u, false).tiles;
+        if (begin < at + n) {
+          sm.start_unit = u;
+          sm.start_at = begin - at;
+          break;
+        }
+        at += n;
+      }
+    }
+    if (tid == 0) sm.tiles = total;
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = sm.tmem;
+  Walk walk;
+  walk.left = sm.tiles * (slice + 1) / p.slices - sm.tiles * slice / p.slices;
+  if (walk.left > 0) walk.start(p, sm.start_unit, sm.start_at);
+  const int elem = k8Bit ? 1 : 2;
+
+  if (warp >= kSumWarps && warp < kMmaWarp) {
+    // ---- copies -----------------------------------------------------------
+    const int me = tid - kSumWarps * 32, sub = lane >> 3, col = lane & 7;
+    const char* q = static_cast<const char*>(p.a.q);
+    const char* keys = static_cast<const char*>(p.a.keys);
+    uint32_t tile = 0, segment = 0;
+    for (; walk.left > 0; walk.next(p), ++segment) {
+      mbar_wait(smem_addr(&sm.q_empty), (segment & 1) ^ 1, guard);
+      const int cols = walk.rows * p.head_cols;
+      const int64_t row0 = walk.row0 + walk.first;
+      for (int n = me >> 3; n < cols; n += kCopyThreads / 8) {
+        const int j = n / p.head_cols, h = n - j * p.head_cols;
+        const char* from = q + ((row0 + j) * p.a.q_row_stride + h * p.a.q_head_stride) * elem;
+        for (int ch = 0; ch < p.chunks; ++ch) {
+          const int byte = ch * 128 + col * 16;
+          const bool in = h < p.a.heads && byte < p.row_bytes;
+          copy16(q_at + ch * (p.pack * p.head_cols * 128) + n * 128 + ((col ^ (n & 7)) << 4), in ? from + byte : q, in ? 16 : 0);
+        }
+      }
+      copies_arrive(smem_addr(&sm.q_full));
+      const int ss = segment % kSegmentSlots;
+      for (int n = me; n < cols; n += kCopyThreads) {
+        const int j = n / p.head_cols, h = n - j * p.head_cols;
+        sm.weight[ss][n] = h < p.a.heads ? p.a.weights[(row0 + j) * p.a.weight_row_stride + h] : 0.f;
+      }
+      for (int j = me; j < walk.rows; j += kCopyThreads) sm.length[ss][j] = row_length(p.R, row0 + j, false);
+      mbar_arrive(smem_addr(&sm.segment_full[ss]));
+      // A tile's tokens are found in steps, each a tile earlier than its result is used: the block, then the scale.
+      const auto position = [&](int t) { return t < walk.count ? (walk.at + t) * kTile + me : INT_MAX; };
+      const auto column = [&](int x) { return p.R.block_shift >= 0 ? x >> p.R.block_shift : x / p.R.block_size; };
+      const auto table_entry = [&](int x) {
+        return x < walk.longest ? __ldg(p.R.block_table + walk.request * p.R.table_stride + column(x)) : 0;
+      };
+      const auto in_cache = [&](int x, int b) { return x < walk.longest && b >= 0 && b < p.R.num_blocks; };
+      const auto token_scale = [&](int x, int b) {
+        return p.a.key_scales && in_cache(x, b)
+                   ? __ldg(p.a.key_scales + b * p.a.scale_block_stride + (x - column(x) * p.R.block_size) * p.a.scale_token_stride)
+                   : 1.f;
+      };
+      int at_block = table_entry(position(0)), next_block = table_entry(position(1));
+      float scale = token_scale(position(0), at_block);
+      for (int t = 0; t < walk.count; ++t, ++tile) {
+        const int x = position(t), later_block = table_entry(position(t + 2));
+        const float next_scale = token_scale(position(t + 1), next_block);
+        const bool here = in_cache(x, at_block);
+        if (x < walk.longest && !here) atomicOr(p.R.status, TOPK_DEV_BAD_BLOCK);
+        const char* from = keys;
+        if (here) from += (at_block * p.a.key_block_stride + (x - column(x) * p.R.block_size) * p.a.key_token_stride) * elem;
+        const unsigned here_mask = __ballot_sync(~0u, here);
+        const int slot = tile % p.slots;
+        mbar_wait(smem_addr(&sm.empty[slot]), ((tile / p.slots) & 1) ^ 1, guard);
+        const uint32_t dst = ring + slot * slot_bytes;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int lane_from = i * 4 + sub, token = (warp - kSumWarps) * 32 + lane_from;
+          const char* src = reinterpret_cast<const char*>(__shfl_sync(~0u, reinterpret_cast<uint64_t>(from), lane_from));
+          const bool on = (here_mask >> lane_from) & 1;
+          const uint32_t to = dst + token * 128 + ((col ^ (token & 7)) << 4);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            if (c < p.chunks) {
+              const int byte = c * 128 + col * 16;
+              const bool in = on && byte < p.row_bytes;
+              copy16(to + c * kChunk, in ? src + byte : keys, in ? 16 : 0);
+            }
+          }
+        }
+        copies_arrive(smem_addr(&sm.full[slot]));
+        sm.scale[tile % kTokenSlots][me] = scale;
+        sm.found[tile % kTokenSlots][me] = here;
+        mbar_arrive(smem_addr(&sm.token_full[tile % kTokenSlots]));
+        at_block = next_block;
+        next_block = later_block;
+        scale = next_scale;
+      }
+    }
+    copies_wait_all();
+  } else if (warp == kMmaWarp) {
+    // ---- products ---------------------------------------------------------
+    if (lane == 0) {
+      uint32_t tile = 0, segment = 0;
+      const int steps = (p.row_bytes + 31) / 32;
+      for (; walk.left > 0; walk.next(p), ++segment) {
+        const uint32_t inst = p.inst | (static_cast<uint32_t>(walk.rows * p.head_cols >> 3) << 17);
+        mbar_wait(smem_addr(&sm.q_full), segment & 1, guard);
+        fence_async();
+        for (int t = 0; t < walk.count; ++t, ++tile) {
+          const int slot = tile % p.slots;
+          mbar_wait(smem_addr(&sm.full[slot]), (tile / p.slots) & 1, guard);
+          fence_async();
+          mbar_wait(smem_addr(&sm.s_empty[tile & 1]), ((tile >> 1) & 1) ^ 1, guard);
+          fence_after();
+          for (int k = 0; k < steps; ++k) {
+            const uint32_t off = (k & 3) * 32, ch = k >> 2;
+            const uint64_t a = operand(ring + slot * slot_bytes + ch * kChunk + off, 16);
+            const uint64_t b = operand(q_at + ch * (p.pack * p.head_cols * 128) + off, 16);
+            if (k8Bit)
+              mma8(tmem + (tile & 1) * kMaxCols, a, b, inst, k > 0);
+            else
+              mma16(tmem + (tile & 1) * kMaxCols, a, b, inst, k > 0);
+          }
+          commit(smem_addr(&sm.empty[slot]));
+          if (t + 1 == walk.count) commit(smem_addr(&sm.q_empty));
+          commit(smem_addr(&sm.s_full[tile & 1]));
+        }
+      }
+      commit(smem_addr(&sm.all_done));
+      mbar_wait(smem_addr(&sm.all_done), 0, guard);
+    }
+    __syncwarp();
+  } else {
+    // ---- sums -------------------------------------------------------------
+    const uint32_t turn = warp >> 2;
+    const int quarter = warp & 3, token = quarter * 32 + lane;
+    const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + turn * kMaxCols;
+    const bool wide = p.head_cols % 32 == 0;
+    uint32_t tile = 0, segment = 0;
+    for (; walk.left > 0; walk.next(p), ++segment) {
+      const int ss = segment % kSegmentSlots;
+      mbar_wait(smem_addr(&sm.segment_full[ss]), (segment / kSegmentSlots) & 1, guard);
+      for (int t = 0; t < walk.count; ++t, ++tile) {
+        if ((tile & 1) != turn) continue;
+        mbar_wait(smem_addr(&sm.token_full[tile % kTokenSlots]), (tile / kTokenSlots) & 1, guard);
+        const float scale = sm.scale[tile % kTokenSlots][token];
+        const bool found = sm.found[tile % kTokenSlots][token];
+        mbar_wait(smem_addr(&sm.s_full[turn]), (tile >> 1) & 1, guard);
+        fence_after();
+        const int pos = (walk.at + t) * kTile + token;
+        if (wide)
+          sum_tile<32>(p, at, sm.weight[ss], sm.length[ss], walk.rows, pos, scale, found, walk.row0 + walk.first);
+        else
+          sum_tile<16>(p, at, sm.weight[ss], sm.length[ss], walk.rows, pos, scale, found, walk.row0 + walk.first);
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sm.s_empty[turn]));
+      }
+    }
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == kMmaWarp) tmem_free(tmem, 2 * kMaxCols);
+}
+
+template <bool k8Bit>
+int run(Params& p, int smem_limit, cudaStream_t stream) {
+  const int extra = static_cast<int>(sizeof(Smem)) + 1024;
+  const int slot = p.chunks * kChunk, room = smem_limit - extra - static_cast<int>(p.q_bytes);
+  p.slots = room / slot < kMaxSlots ? room / slot : kMaxSlots;
+  if (p.slots < 1) return TOPK_ERR_PLAN;
+  const size_t smem = p.q_bytes + static_cast<size_t>(p.slots) * slot + extra;
+  if (cudaFuncSetAttribute(index_logits_kernel<k8Bit>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) {
+    cudaGetLastError();
+    return TOPK_ERR_CUDA;
+  }
+  return launch(index_logits_kernel<k8Bit>, static_cast<const Params&>(p), p.slices, kThreads, smem, stream);
 }
 
 }  // namespace
@@ -73,14 +456,32 @@ extern "C" int topk_index_logits(const topk_index_logits_args* args, void* strea
       a.key_block_stride % piece || a.key_token_stride % piece || misaligned(a.weights, 4) ||
       misaligned(a.key_scales, 4) || misaligned(a.logits, 4) || misaligned(a.workspace, 16))
     return TOPK_ERR_MISALIGNED;
-  const int sms = num_sms();
-  if (sms < 1) return TOPK_ERR_CUDA;
-  LogitsParams p{};
+  int dev = 0;
+  topk_device_props props{};
+  if (cudaGetDevice(&dev) != cudaSuccess || topk_query_device(dev, &props) != TOPK_OK) {
+    cudaGetLastError();
+    return TOPK_ERR_CUDA;
+  }
+  Params p{};
   p.a = a;
   p.R = make_rows(a.rows, a.max_len, a.workspace);
-  const int64_t grid = a.rows.num_rows < sms * 2 ? a.rows.num_rows : sms * 2;
+  p.head_cols = (a.heads + 15) / 16 * 16;
+  const int fit = kMaxCols / p.head_cols;  // rows that a product takes
+  if (a.rows.row_request != nullptr) {
+    p.pack = fit;
+  } else {  // units that do not cross requests: the largest divisor of next_n that fits
+    p.pack = 1;
+    for (int d = 2; d <= fit; ++d)
+      if (a.rows.next_n % d == 0) p.pack = d;
+  }
+  if (p.pack > a.rows.num_rows) p.pack = static_cast<int32_t>(a.rows.num_rows);
+  p.units = (a.rows.num_rows + p.pack - 1) / p.pack;
+  p.row_bytes = a.dim * size;
+  p.chunks = (p.row_bytes + 127) / 128;
+  p.q_bytes = static_cast<uint32_t>(p.pack * p.head_cols * 128 * p.chunks);
+  const int64_t most = a.rows.num_rows * ((p.R.max_len + static_cast<int64_t>(kTile) - 1) / kTile);
+  p.slices = static_cast<int32_t>(most < props.num_sms ? most : props.num_sms);
+  p.inst = ltk::umma::instruction(a.dtype == TOPK_DTYPE_BF16 ? ltk::umma::kBF16 : ltk::umma::kF16, 0, false);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (size == 1) return launch(index_logits_kernel<__nv_fp8_e4m3>, p, grid, kThreads, 0, s);
-  if (a.dtype == TOPK_DTYPE_F16) return launch(index_logits_kernel<__half>, p, grid, kThreads, 0, s);
-  return launch(index_logits_kernel<__nv_bfloat16>, p, grid, kThreads, 0, s);
+  return size == 1 ? run<true>(p, props.max_smem_optin, s) : run<false>(p, props.max_smem_optin, s);
 }

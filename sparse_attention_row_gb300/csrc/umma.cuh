@@ -54,7 +54,7 @@ __device__ __forceinline__ uint64_t now_ns() {
   return t;
 }
 
-__device__ __noinline__ void mbar_wait_slow(uint32_t bar, uint32_t parity, volatile uint32_t* gave_up, uint32_t* status) {
+static __device__ __noinline__ void mbar_wait_slow(uint32_t bar, uint32_t parity, volatile uint32_t* gave_up, uint32_t* status) {
   const uint64_t t0 = now_ns();
   while (!mbar_try(bar, parity)) {
     if (*gave_up) return;
