@@ -19,7 +19,7 @@ LIB = os.path.join(HERE, "libtopk.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["topk_kernel.cu", "topk_kernel_pair.cu", "topk_kernel_small.cu", "topk_short.cu", "topk_short16.cu", "topk_sort.cu",
            "topk_api.cu",
-           "topk_static.cu", "kv_map.cu", "index_logits.cu", "paged_attention.cu", "planner.cpp"]
+           "topk_static.cu", "kv_map.cu", "cache_map.cu", "index_logits.cu", "paged_attention.cu", "planner.cpp"]
 
 
 def _nvcc() -> str:

@@ -18,6 +18,7 @@
 // 16-byte asynchronous copies (any page size and stride; zeros where there is no
 // token), 1 thread issues the products, two groups of 4 warps take the tiles in
 // turn, a thread per token.
+#include "cache_map.cuh"
 #include "paged.cuh"
 #include "umma.cuh"
 
@@ -39,6 +40,7 @@ constexpr int kSegmentSlots = 4;  // a segment's weights are written when at mos
 constexpr int kMaxCols = 256, kMaxRows = 16;
 
 struct Params {
+  CacheMap map;
   topk_index_logits_args a;
   Rows R;
   int32_t pack;      // rows of a unit
@@ -215,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1) index_logits_kernel(const __grid_
   const Guard guard{&sm.gave_up, p.R.status};
   if (tid == 0) {
     for (int i = 0; i < kMaxSlots; ++i) {
-      mbar_init(smem_addr(&sm.full[i]), kCopyThreads);
+      mbar_init(smem_addr(&sm.full[i]), kCopyWarps);
       mbar_init(smem_addr(&sm.empty[i]), 1);
     }
     mbar_init(smem_addr(&sm.q_full), kCopyThreads);
@@ -277,10 +279,10 @@ __global__ void __launch_bounds__(kThreads, 1) index_logits_kernel(const __grid_
 
   if (warp >= kSumWarps && warp < kMmaWarp) {
     // ---- copies -----------------------------------------------------------
-    const int me = tid - kSumWarps * 32, sub = lane >> 3, col = lane & 7;
+    const int me = tid - kSumWarps * 32, col = lane & 7;
     const char* q = static_cast<const char*>(p.a.q);
-    const char* keys = static_cast<const char*>(p.a.keys);
-    uint32_t tile = 0, segment = 0;
+    TokenRows rows;
+    uint32_t tile = 0, segment = 0, slot = 0, phase = 0;
     for (; walk.left > 0; walk.next(p), ++segment) {
       mbar_wait(smem_addr(&sm.q_empty), (segment & 1) ^ 1, guard);
       const int cols = walk.rows * p.head_cols;
@@ -321,28 +323,17 @@ __global__ void __launch_bounds__(kThreads, 1) index_logits_kernel(const __grid_
         const float next_scale = token_scale(position(t + 1), next_block);
         const bool here = in_cache(x, at_block);
         if (x < walk.longest && !here) atomicOr(p.R.status, TOPK_DEV_BAD_BLOCK);
-        const char* from = keys;
-        if (here) from += (at_block * p.a.key_block_stride + (x - column(x) * p.R.block_size) * p.a.key_token_stride) * elem;
-        const unsigned here_mask = __ballot_sync(~0u, here);
-        const int slot = tile % p.slots;
-        mbar_wait(smem_addr(&sm.empty[slot]), ((tile / p.slots) & 1) ^ 1, guard);
-        const uint32_t dst = ring + slot * slot_bytes;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int lane_from = i * 4 + sub, token = (warp - kSumWarps) * 32 + lane_from;
-          const char* src = reinterpret_cast<const char*>(__shfl_sync(~0u, reinterpret_cast<uint64_t>(from), lane_from));
-          const bool on = (here_mask >> lane_from) & 1;
-          const uint32_t to = dst + token * 128 + ((col ^ (token & 7)) << 4);
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            if (c < p.chunks) {
-              const int byte = c * 128 + col * 16;
-              const bool in = on && byte < p.row_bytes;
-              copy16(to + c * kChunk, in ? src + byte : keys, in ? 16 : 0);
-            }
-          }
+        const int place = x - column(x) * p.R.block_size;
+        if (p.map.run_rows && (walk.at + t + 1) * kTile <= walk.longest)  // before the pass's last tile
+          rows.set(run_row(p.map, here, at_block, place, 0), p.map.run_rows, lane);
+        else
+          rows.set(gather_row(p.map, here, at_block, place, 0), 0, lane);
+        mbar_wait(smem_addr(&sm.empty[0]) + slot * 8, phase ^ 1, guard);
+        rows.fetch(p.map, ring + slot * slot_bytes + (warp - kSumWarps) * 32 * 128, 0, p.chunks, smem_addr(&sm.full[0]) + slot * 8, lane);
+        if (++slot == static_cast<uint32_t>(p.slots)) {
+          slot = 0;
+          phase ^= 1;
         }
-        copies_arrive(smem_addr(&sm.full[slot]));
         sm.scale[tile % kTokenSlots][me] = scale;
         sm.found[tile % kTokenSlots][me] = here;
         mbar_arrive(smem_addr(&sm.token_full[tile % kTokenSlots]));
@@ -354,36 +345,42 @@ __global__ void __launch_bounds__(kThreads, 1) index_logits_kernel(const __grid_
     copies_wait_all();
   } else if (warp == kMmaWarp) {
     // ---- products ---------------------------------------------------------
-    if (lane == 0) {
-      uint32_t tile = 0, segment = 0;
-      const int steps = (p.row_bytes + 31) / 32;
-      for (; walk.left > 0; walk.next(p), ++segment) {
-        const uint32_t inst = p.inst | (static_cast<uint32_t>(walk.rows * p.head_cols >> 3) << 17);
-        mbar_wait(smem_addr(&sm.q_full), segment & 1, guard);
-        fence_async();
-        for (int t = 0; t < walk.count; ++t, ++tile) {
-          const int slot = tile % p.slots;
-          mbar_wait(smem_addr(&sm.full[slot]), (tile / p.slots) & 1, guard);
-          fence_async();
-          mbar_wait(smem_addr(&sm.s_empty[tile & 1]), ((tile >> 1) & 1) ^ 1, guard);
-          fence_after();
-          for (int k = 0; k < steps; ++k) {
-            const uint32_t off = (k & 3) * 32, ch = k >> 2;
-            const uint64_t a = operand(ring + slot * slot_bytes + ch * kChunk + off, 16);
-            const uint64_t b = operand(q_at + ch * (p.pack * p.head_cols * 128) + off, 16);
-            if (k8Bit)
-              mma8(tmem + (tile & 1) * kMaxCols, a, b, inst, k > 0);
-            else
-              mma16(tmem + (tile & 1) * kMaxCols, a, b, inst, k > 0);
-          }
-          commit(smem_addr(&sm.empty[slot]));
-          if (t + 1 == walk.count) commit(smem_addr(&sm.q_empty));
-          commit(smem_addr(&sm.s_full[tile & 1]));
+    const int chunks = p.row_bytes / 128, steps = (p.row_bytes % 128 + 31) / 32;  // whole chunks, and steps of 32 bytes after them
+    const uint32_t q_chunk = p.pack * p.head_cols * 128;
+    uint32_t tile = 0, segment = 0, slot = 0, phase = 0;
+    for (; walk.left > 0; walk.next(p), ++segment) {
+      const uint32_t inst = p.inst | (static_cast<uint32_t>(walk.rows * p.head_cols >> 3) << 17);
+      mbar_wait_warp(smem_addr(&sm.q_full), segment & 1, guard);
+      fence_async();
+      for (int t = 0; t < walk.count; ++t, ++tile) {
+        mbar_wait_warp(smem_addr(&sm.full[0]) + slot * 8, phase, guard);
+        mbar_wait_warp(smem_addr(&sm.s_empty[0]) + (tile & 1) * 8, ((tile >> 1) & 1) ^ 1, guard);
+        fence_after();
+        const uint32_t d = tmem + (tile & 1) * kMaxCols, k_at = ring + slot * slot_bytes;
+        int c = 0;
+        for (; c < chunks; ++c) {
+          if (k8Bit)
+            mma8_chunk(d, operand(k_at + c * kChunk, 16), operand(q_at + c * q_chunk, 16), inst, c > 0);
+          else
+            mma16_chunk(d, operand(k_at + c * kChunk, 16), operand(q_at + c * q_chunk, 16), inst, c > 0);
+        }
+        for (int i = 0; i < steps; ++i) {
+          if (k8Bit)
+            mma8_step(d, operand(k_at + c * kChunk + i * 32, 16), operand(q_at + c * q_chunk + i * 32, 16), inst, c + i > 0);
+          else
+            mma16_step(d, operand(k_at + c * kChunk + i * 32, 16), operand(q_at + c * q_chunk + i * 32, 16), inst, c + i > 0);
+        }
+        commit(smem_addr(&sm.empty[0]) + slot * 8);
+        if (t + 1 == walk.count) commit(smem_addr(&sm.q_empty));
+        commit(smem_addr(&sm.s_full[0]) + (tile & 1) * 8);
+        if (++slot == static_cast<uint32_t>(p.slots)) {
+          slot = 0;
+          phase ^= 1;
         }
       }
-      commit(smem_addr(&sm.all_done));
-      mbar_wait(smem_addr(&sm.all_done), 0, guard);
     }
+    commit(smem_addr(&sm.all_done));
+    mbar_wait_warp(smem_addr(&sm.all_done), 0, guard);
     __syncwarp();
   } else {
     // ---- sums -------------------------------------------------------------
@@ -413,6 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) index_logits_kernel(const __grid_
       }
     }
   }
+  settle(guard);
   fence_before();
   __syncthreads();
   fence_after();
@@ -465,6 +463,8 @@ extern "C" int topk_index_logits(const topk_index_logits_args* args, void* strea
   Params p{};
   p.a = a;
   p.R = make_rows(a.rows, a.max_len, a.workspace);
+  rc = make_cache_map(&p.map, a.keys, size, a.dtype, a.rows.num_blocks, a.rows.block_size, 1, a.dim, a.key_block_stride, a.key_token_stride, 0);
+  if (rc != TOPK_OK) return rc;
   p.head_cols = (a.heads + 15) / 16 * 16;
   const int fit = kMaxCols / p.head_cols;  // rows that a product takes
   if (a.rows.row_request != nullptr) {

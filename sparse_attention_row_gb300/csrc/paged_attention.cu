@@ -143,6 +143,14 @@ struct Walk {
   }
 };
 
+// A place in the ring of pieces, and the parity of its barrier's phase.
+struct Ring {
+  uint32_t slot = 0, phase = 0;
+  __device__ void step(uint32_t slots, uint32_t by = 1) {
+    for (slot += by; slot >= slots; slot -= slots) phase ^= 1;
+  }
+};
+
 // Reduces v[c] over the warp's lanes; lane i gets column i % N.
 template <int N, bool kMax>
 __device__ __forceinline__ float reduce_columns(const float (&v)[N], int lane) {
@@ -166,6 +174,44 @@ __device__ __forceinline__ float reduce_columns(const float (&v)[N], int lane) {
   }
   return t[0];
 }
+
+// A copying warp's part of a piece: 32 tokens, eight lanes to each 128 bytes, four tokens an instruction.
+struct Copies {
+  const char* from[8];
+  uint32_t seen;   // bit i: from[i] is to be read
+  uint32_t to[2];  // place in the tile of the even and odd instructions, whose tokens differ by four
+  int byte;        // of a 128-byte row
+  __device__ Copies(int warp, int lane) : seen(0) {
+    const int token = warp * 32 + (lane >> 3), col = lane & 7;
+    byte = col * 16;
+    to[0] = token * 128 + ((col ^ (token & 7)) << 4);
+    to[1] = (token + 4) * 128 + ((col ^ ((token + 4) & 7)) << 4);
+  }
+  // Each lane brings the address of its token, lane by lane in the order of the tile.
+  __device__ __forceinline__ void aim(const char* mine, bool on, int lane) {
+    const unsigned all = __ballot_sync(~0u, on);
+    seen = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int lane_from = i * 4 + (lane >> 3);
+      from[i] = reinterpret_cast<const char*>(__shfl_sync(~0u, reinterpret_cast<uint64_t>(mine), lane_from)) + byte;
+      seen |= ((all >> lane_from) & 1) << i;
+    }
+  }
+  // Up to 128 of the `dims` elements that there are from `first` on; zeros up to the end of a chunk of 64.
+  __device__ __forceinline__ void piece(uint32_t dst, int first, int dims, const void* anywhere) const {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      if (c * 64 >= dims) break;
+      const bool in = c * 128 + byte < dims * 2;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool on = in && ((seen >> i) & 1);
+        copy16(dst + c * kChunk + to[i & 1] + (i >> 1) * 1024, on ? from[i] + (first * 2 + c * 128) : anywhere, on ? 16 : 0);
+      }
+    }
+  }
+};
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -275,15 +321,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     walk.size();
   }
   const int k_ring = p.k_pieces - p.rest;                       // pieces of the keys in the ring
-  const int tile_pieces = k_ring + (p.latent ? 0 : p.v_pieces);  // ring pieces of a tile
   const uint32_t s_cols = static_cast<uint32_t>(p.v_pieces) * N;  // columns before the scores'
   const int block_cols = min(p.block_cols, p.cols - block * p.block_cols);
 
   if (warp >= kSoftmaxWarps && warp < kMmaWarp) {
     // ---- copies -----------------------------------------------------------
     const int me = tid - kSoftmaxWarps * 32;  // this thread's token of a tile
-    const int sub = lane >> 3, col = lane & 7;
-    uint32_t piece = 0;  // ring pieces begun
+    const int col = lane & 7;
+    const uint32_t full = smem_addr(&sm.full[0]), empty = smem_addr(&sm.empty[0]);
+    Ring at;
+    Copies copies(warp - kSoftmaxWarps, lane);
     uint32_t tile = 0, segment = 0;
     for (; walk.left > 0; walk.next(p), ++segment) {
       const int64_t row0 = walk.group * p.pack;
@@ -329,45 +376,33 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         sm.token[tile % kTokenSlots][me] = pos;
         mbar_arrive(smem_addr(&sm.token_full[tile % kTokenSlots]));
         const bool seen = pos != INT_MAX;
-        const uint16_t* kp = static_cast<const uint16_t*>(p.a.k);
-        const uint16_t* vp = static_cast<const uint16_t*>(p.a.v);
-        if (seen) {
-          kp += static_cast<int64_t>(at_block) * p.a.k_block_stride + place * p.a.k_token_stride + walk.kv_head * p.a.k_head_stride;
-          if (!p.latent) vp += static_cast<int64_t>(at_block) * p.a.v_block_stride + place * p.a.v_token_stride + walk.kv_head * p.a.v_head_stride;
-        }
+        const char* kp = static_cast<const char*>(p.a.k);
+        if (seen)
+          kp += 2 * (static_cast<int64_t>(at_block) * p.a.k_block_stride + place * p.a.k_token_stride + walk.kv_head * p.a.k_head_stride);
+        const char* vp = static_cast<const char*>(p.a.v);
+        if (seen && !p.latent)
+          vp += 2 * (static_cast<int64_t>(at_block) * p.a.v_block_stride + place * p.a.v_token_stride + walk.kv_head * p.a.v_head_stride);
         const int next_block = table_entry(next_token), later_token = listed(t + 2);
-        const unsigned seen_mask = __ballot_sync(~0u, seen);
-        const auto copy_piece = [&](const uint16_t* ptr, uint32_t dst, int chunk0, int chunks, int dims) {
-          const uint64_t mine = reinterpret_cast<uint64_t>(ptr);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int from = i * 4 + sub, token = (warp - kSoftmaxWarps) * 32 + from;
-            const char* src = reinterpret_cast<const char*>(__shfl_sync(~0u, mine, from));
-            const bool on = (seen_mask >> from) & 1;
-            const uint32_t to = dst + token * 128 + ((col ^ (token & 7)) << 4);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              if (c < chunks) {
-                const int dim = (chunk0 + c) * 64 + col * 8;
-                const bool in = on && dim < dims;
-                copy16(to + c * kChunk, in ? src + dim * 2 : static_cast<const char*>(p.a.k), in ? 16 : 0);
-              }
-            }
-          }
-        };
-        for (int u = 0; u < tile_pieces; ++u, ++piece) {
-          const int slot = piece % p.slots;
-          mbar_wait(smem_addr(&sm.empty[slot]), ((piece / p.slots) & 1) ^ 1, guard);
-          if (u < k_ring)
-            copy_piece(kp, ring + slot * kPiece, u * 2, min(2, p.k_chunks - u * 2), p.a.dk);
-          else
-            copy_piece(vp, ring + slot * kPiece, (u - k_ring) * 2, 2, p.a.dv);
-          copies_arrive(smem_addr(&sm.full[slot]));
+        copies.aim(kp, seen, lane);
+        for (int u = 0; u < k_ring; ++u) {
+          mbar_wait(empty + at.slot * 8, at.phase ^ 1, guard);
+          copies.piece(ring + at.slot * kPiece, u * 128, p.a.dk - u * 128, p.a.k);
+          copies_arrive(full + at.slot * 8);
+          at.step(p.slots);
         }
         if (p.rest) {
           mbar_wait(smem_addr(&sm.rest_empty), (tile & 1) ^ 1, guard);
-          copy_piece(kp, rest, k_ring * 2, 1, p.a.dk);
+          copies.piece(rest, k_ring * 128, p.a.dk - k_ring * 128, p.a.k);
           copies_arrive(smem_addr(&sm.rest_full));
+        }
+        if (!p.latent) {
+          copies.aim(vp, seen, lane);
+          for (int u = 0; u < p.v_pieces; ++u) {
+            mbar_wait(empty + at.slot * 8, at.phase ^ 1, guard);
+            copies.piece(ring + at.slot * kPiece, u * 128, p.a.dv - u * 128, p.a.v);
+            copies_arrive(full + at.slot * 8);
+            at.step(p.slots);
+          }
         }
         at_token = next_token;
         at_block = next_block;
@@ -377,67 +412,73 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     copies_wait_all();
   } else if (warp == kMmaWarp) {
     // ---- products ---------------------------------------------------------
-    if (lane == 0) {
-      constexpr uint32_t kInstS = instruction(kBf16 ? kBF16 : kF16, N, false);
-      constexpr uint32_t kInstO = instruction(kBf16 ? kBF16 : kF16, N, true);
-      uint32_t tile = 0, segment = 0;
-      // S^T of one tile, into one of its two places
-      const auto scores = [&](uint32_t tl) {
-        const uint32_t d = tmem + s_cols + (tl & 1) * N;
-        bool add = false;
-        for (int u = 0; u < p.k_pieces; ++u) {
-          uint32_t at, piece = 0;
-          if (u < k_ring) {
-            piece = tl * tile_pieces + u;
-            at = ring + (piece % p.slots) * kPiece;
-            mbar_wait(smem_addr(&sm.full[piece % p.slots]), (piece / p.slots) & 1, guard);
-          } else {
-            at = rest;
-            mbar_wait(smem_addr(&sm.rest_full), tl & 1, guard);
-          }
-          fence_async();
-          const int dims = min(p.a.dk - u * 128, 128);
-          for (int k = 0; k * 16 < dims; ++k) {
-            const uint32_t off = (k & 3) * 32, half = k >> 2;
-            mma16(d, operand(at + half * kChunk + off, 16), operand(q_at + (u * 2 + half) * (N * 128) + off, 16), kInstS, add);
-            add = true;
-          }
-          // keys that are no values are done with
-          if (u < k_ring && !(p.latent && u < p.v_pieces)) commit(smem_addr(&sm.empty[piece % p.slots]));
-          if (u >= k_ring && !p.rest_is_p) commit(smem_addr(&sm.rest_empty));
+    constexpr uint32_t kInstS = instruction(kBf16 ? kBF16 : kF16, N, false);
+    constexpr uint32_t kInstO = instruction(kBf16 ? kBF16 : kF16, N, true);
+    const uint32_t full = smem_addr(&sm.full[0]), empty = smem_addr(&sm.empty[0]);
+    Ring kr, vr;  // the pieces of keys and of values that come next
+    if (!p.latent) vr.step(p.slots, k_ring);
+    uint32_t scored = 0;                    // tiles whose scores have been taken
+    // S^T of the next tile, into one of its two places
+    const auto scores = [&]() {
+      const uint32_t d = tmem + s_cols + (scored & 1) * N;
+      for (int u = 0; u < p.k_pieces; ++u) {
+        uint32_t at = rest;
+        if (u < k_ring) {
+          at = ring + kr.slot * kPiece;
+          mbar_wait_warp(full + kr.slot * 8, kr.phase, guard);
+        } else {
+          mbar_wait_warp(smem_addr(&sm.rest_full), scored & 1, guard);
         }
-        commit(smem_addr(&sm.s_full[tl & 1]));
-      };
-      for (; walk.left > 0; walk.next(p), ++segment) {
-        mbar_wait(smem_addr(&sm.q_full), segment & 1, guard);
         fence_async();
-        if (p.ahead) scores(tile);
-        for (int t = 0; t < walk.count; ++t, ++tile) {
-          const bool last = t + 1 == walk.count;
-          if (!p.ahead) scores(tile);
-          if (p.ahead && !last) scores(tile + 1);
-          if (p.ahead ? t + 2 == walk.count || walk.count == 1 : last) commit(smem_addr(&sm.q_empty));
-          mbar_wait(smem_addr(&sm.p_full), tile & 1, guard);
-          fence_after();
-          for (int u = 0; u < p.v_pieces; ++u) {
-            const uint32_t piece = tile * tile_pieces + (p.latent ? u : k_ring + u), slot = piece % p.slots;
-            const uint32_t at = ring + slot * kPiece;
-            if (!p.latent) {
-              mbar_wait(smem_addr(&sm.full[slot]), (piece / p.slots) & 1, guard);
-              fence_async();
-            }
-#pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-              mma16(tmem + u * N, operand(at + k * 2048, kChunk), operand(p_at + k * 2048, 1024), kInstO, t > 0 || k > 0);
-            commit(smem_addr(&sm.empty[slot]));
-          }
-          if (p.rest && p.rest_is_p) commit(smem_addr(&sm.rest_empty));
-          commit(smem_addr(&sm.o_done));
+        const int dims = min(p.a.dk - u * 128, 128);
+        const uint32_t q_piece = q_at + u * 2 * (N * 128);
+        if (dims == 128) {
+          mma16_piece(d, operand(at, 16), operand(q_piece, 16), operand(q_piece + N * 128, 16), kInstS, u > 0);
+        } else {
+          int k = 0;
+          if (dims >= 64) mma16_chunk(d, operand(at, 16), operand(q_piece, 16), kInstS, u + k++ > 0);
+          for (int i = 0; k * 64 + i * 16 < dims; ++i)
+            mma16_step(d, operand(at + k * kChunk + i * 32, 16), operand(q_piece + k * (N * 128) + i * 32, 16), kInstS, u + k + i > 0);
+        }
+        // keys that are no values are done with
+        if (u < k_ring) {
+          if (!p.latent || u >= p.v_pieces) commit(empty + kr.slot * 8);
+          kr.step(p.slots);
+        } else if (!p.rest_is_p) {
+          commit(smem_addr(&sm.rest_empty));
         }
       }
-      commit(smem_addr(&sm.all_done));
-      mbar_wait(smem_addr(&sm.all_done), 0, guard);
+      if (!p.latent) kr.step(p.slots, p.v_pieces);
+      commit(smem_addr(&sm.s_full[scored & 1]));
+      ++scored;
+    };
+    uint32_t tile = 0, segment = 0;
+    for (; walk.left > 0; walk.next(p), ++segment) {
+      mbar_wait_warp(smem_addr(&sm.q_full), segment & 1, guard);
+      fence_async();
+      if (p.ahead) scores();
+      for (int t = 0; t < walk.count; ++t, ++tile) {
+        const bool last = t + 1 == walk.count;
+        if (p.ahead ? !last : true) scores();
+        if (p.ahead ? t + 2 == walk.count || walk.count == 1 : last) commit(smem_addr(&sm.q_empty));
+        mbar_wait_warp(smem_addr(&sm.p_full), tile & 1, guard);
+        fence_after();
+        for (int u = 0; u < p.v_pieces; ++u) {
+          if (!p.latent) {
+            mbar_wait_warp(full + vr.slot * 8, vr.phase, guard);
+            fence_async();
+          }
+          mma16_tokens(tmem + u * N, operand(ring + vr.slot * kPiece, kChunk), operand(p_at, 1024), kInstO, t > 0);
+          commit(empty + vr.slot * 8);
+          vr.step(p.slots);
+        }
+        vr.step(p.slots, p.latent ? k_ring - p.v_pieces : k_ring);
+        if (p.rest && p.rest_is_p) commit(smem_addr(&sm.rest_empty));
+        commit(smem_addr(&sm.o_done));
+      }
     }
+    commit(smem_addr(&sm.all_done));
+    mbar_wait_warp(smem_addr(&sm.all_done), 0, guard);
     __syncwarp();
   } else {
     // ---- softmax and output ------------------------------------------------
@@ -506,7 +547,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           s[i + 2] = exp2_fast(fmaf(s[i + 2], p.scale2, -u.z));
           s[i + 3] = exp2_fast(fmaf(s[i + 3], p.scale2, -u.w));
         }
-        // the last tile's product has read P and written O
         if (tile > 0) mbar_wait(smem_addr(&sm.o_done), (tile - 1) & 1, guard);
         fence_after();
         if (rescale) {  // the same for all warps of this half: they hold the same maxima
@@ -542,7 +582,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sm.p_full));
       }
-      // the segment's sums
       const float part_l = reduce_columns<H, false>(l, lane);
       if (lane < H) sm.column_sum[half][quarter][lane] = part_l;
       named_sync(1 + half, 128);
@@ -619,6 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       p.join[slice] = j;
     }
   }
+  settle(guard);
   fence_before();
   __syncthreads();
   fence_after();

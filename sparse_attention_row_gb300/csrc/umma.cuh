@@ -70,6 +70,20 @@ __device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, const G
   if (!mbar_try(bar, parity)) mbar_wait_slow(bar, parity, g.gave_up, g.status);
 }
 
+// Before a CTA that gave up ends: its copies and products in flight, of which no one waits for the end any more,
+// take microseconds; 2 ms are waited.
+__device__ __forceinline__ void settle(const Guard& g) {
+  if (!*g.gave_up) return;
+  const uint64_t t0 = now_ns();
+  while (now_ns() - t0 < 2000000) __nanosleep(1000);
+}
+
+// mbar_wait for a whole warp, which goes on in step.
+__device__ __forceinline__ void mbar_wait_warp(uint32_t bar, uint32_t parity, const Guard& g) {
+  mbar_wait(bar, parity, g);
+  __syncwarp();
+}
+
 // 16 bytes into shared memory; `bytes` 0 writes zeros and reads nothing.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -154,13 +168,11 @@ __device__ __forceinline__ void tmem_store8(uint32_t addr, const float* v) {
 
 // ---- products -------------------------------------------------------------
 
-// Descriptor of an operand tile at shared-memory address `addr` (16-byte aligned), 128-byte swizzle, groups of
-// eight rows 1024 bytes apart. `leading` matters to MN-major operands of more than 64 elements only: bytes
-// from one 128-byte column of the tile to the next.
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t leading) {
-  return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | (static_cast<uint64_t>((leading >> 4) & 0x3FFF) << 16) |
-         (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
-}
+// Descriptor of an operand tile, 128-byte swizzle, groups of eight rows 1024 bytes apart: its low word, from the
+// tile's shared-memory address (16-byte aligned). `leading` matters to MN-major operands of more than 64 elements
+// only: bytes from one 128-byte column of the tile to the next. The high word is the same for all.
+__device__ __forceinline__ uint32_t operand(uint32_t addr, uint32_t leading) { return (addr >> 4) | (leading >> 4 << 16); }
+constexpr uint32_t kOperandHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
 
 enum Format : uint32_t { kF16 = 0, kBF16 = 1, kE4M3 = 0 };
 
@@ -170,27 +182,131 @@ __host__ __device__ constexpr uint32_t instruction(uint32_t format, uint32_t n, 
          ((128u >> 4) << 24);
 }
 
-// One thread: D (tensor memory) = A B, or D += A B. K = 16 elements of two bytes.
-__device__ __forceinline__ void mma16(uint32_t d, uint64_t a, uint64_t b, uint32_t inst, bool add) {
+// The same value in every lane, and known to be: it can live in a uniform register.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(~0u, x, 0); }
+
+// Products, by a whole warp in step, of which one thread issues: D (tensor memory) = A B, or D += A B where `add`
+// (or a later step of the same call). Every lane of the warp runs the code around them, so that addresses stay in
+// uniform registers, which the instruction wants: one thread alone, with a register moved over for every operand, takes
+// about 120 cycles an instruction (N = 16 and N = 64 alike) where the tensor core takes 36 to 48.
+// 32 bytes of both K-major operands: 16 elements of two bytes.
+__device__ __forceinline__ void mma16_step(uint32_t d, uint32_t a, uint32_t b, uint32_t inst, bool add) {
+  d = uniform(d), a = uniform(a), b = uniform(b);
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(inst), "r"(static_cast<uint32_t>(add))
+      "{\n .reg .pred p, q, t;\n .reg .b32 x, y;\n .reg .b64 a, b;\n"
+      " setp.ne.u32 p, %5, 0;\n setp.eq.u32 t, 0, 0;\n elect.sync _|q, 0xffffffff;\n"
+      " add.u32 x, %1, 0; add.u32 y, %2, 0; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n"
+      "}" ::"r"(d), "r"(a), "r"(b), "r"(kOperandHigh), "r"(inst), "r"(static_cast<uint32_t>(add))
       : "memory");
 }
 
-// The same for 8-bit elements: K = 32.
-__device__ __forceinline__ void mma8(uint32_t d, uint64_t a, uint64_t b, uint32_t inst, bool add) {
+// 128 bytes of both: four such steps.
+__device__ __forceinline__ void mma16_chunk(uint32_t d, uint32_t a, uint32_t b, uint32_t inst, bool add) {
+  d = uniform(d), a = uniform(a), b = uniform(b);
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(inst), "r"(static_cast<uint32_t>(add))
+      "{\n .reg .pred p, q, t;\n .reg .b32 x, y;\n .reg .b64 a, b;\n"
+      " setp.ne.u32 p, %5, 0;\n setp.eq.u32 t, 0, 0;\n elect.sync _|q, 0xffffffff;\n"
+      " add.u32 x, %1, 0; add.u32 y, %2, 0; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n"
+      " add.u32 x, %1, 2; add.u32 y, %2, 2; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+      " add.u32 x, %1, 4; add.u32 y, %2, 4; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+      " add.u32 x, %1, 6; add.u32 y, %2, 6; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+      "}" ::"r"(d), "r"(a), "r"(b), "r"(kOperandHigh), "r"(inst), "r"(static_cast<uint32_t>(add))
       : "memory");
 }
 
-// One arrival on `bar` when every product that this thread has issued is done.
+// 256 bytes of both, in two chunks: A's 16 KB apart, B's at b and b2.
+__device__ __forceinline__ void mma16_piece(uint32_t d, uint32_t a, uint32_t b, uint32_t b2, uint32_t inst, bool add) {
+  d = uniform(d), a = uniform(a), b = uniform(b), b2 = uniform(b2);
+  asm volatile(
+      "{\n .reg .pred p, q, t;\n .reg .b32 x, y;\n .reg .b64 a, b;\n"
+      " setp.ne.u32 p, %5, 0;\n setp.eq.u32 t, 0, 0;\n elect.sync _|q, 0xffffffff;\n"
+      " add.u32 x, %1, 0; add.u32 y, %2, 0; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n"
+      " add.u32 x, %1, 2; add.u32 y, %2, 2; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+      " add.u32 x, %1, 4; add.u32 y, %2, 4; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+      " add.u32 x, %1, 6; add.u32 y, %2, 6; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+      " add.u32 x, %1, 1024; add.u32 y, %6, 0; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+      " add.u32 x, %1, 1026; add.u32 y, %6, 2; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+      " add.u32 x, %1, 1028; add.u32 y, %6, 4; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+      " add.u32 x, %1, 1030; add.u32 y, %6, 6; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+      "}" ::"r"(d), "r"(a), "r"(b), "r"(kOperandHigh), "r"(inst), "r"(static_cast<uint32_t>(add)), "r"(b2)
+      : "memory");
+}
+
+// MN-major operands, 128 rows: eight steps of 16 rows.
+__device__ __forceinline__ void mma16_tokens(uint32_t d, uint32_t a, uint32_t b, uint32_t inst, bool add) {
+  d = uniform(d), a = uniform(a), b = uniform(b);
+  asm volatile(
+      "{\n .reg .pred p, q, t;\n .reg .b32 x, y;\n .reg .b64 a, b;\n"
+      " setp.ne.u32 p, %5, 0;\n setp.eq.u32 t, 0, 0;\n elect.sync _|q, 0xffffffff;\n"
+      " add.u32 x, %1, 0; add.u32 y, %2, 0; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n"
+      " add.u32 x, %1, 128; add.u32 y, %2, 128; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+      " add.u32 x, %1, 256; add.u32 y, %2, 256; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+      " add.u32 x, %1, 384; add.u32 y, %2, 384; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+      " add.u32 x, %1, 512; add.u32 y, %2, 512; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+      " add.u32 x, %1, 640; add.u32 y, %2, 640; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+      " add.u32 x, %1, 768; add.u32 y, %2, 768; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+      " add.u32 x, %1, 896; add.u32 y, %2, 896; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+      "}" ::"r"(d), "r"(a), "r"(b), "r"(kOperandHigh), "r"(inst), "r"(static_cast<uint32_t>(add))
+      : "memory");
+}
+
+// 32 bytes of both K-major operands: 32 elements of one byte.
+__device__ __forceinline__ void mma8_step(uint32_t d, uint32_t a, uint32_t b, uint32_t inst, bool add) {
+  d = uniform(d), a = uniform(a), b = uniform(b);
+  asm volatile(
+      "{\n .reg .pred p, q, t;\n .reg .b32 x, y;\n .reg .b64 a, b;\n"
+      " setp.ne.u32 p, %5, 0;\n setp.eq.u32 t, 0, 0;\n elect.sync _|q, 0xffffffff;\n"
+      " add.u32 x, %1, 0; add.u32 y, %2, 0; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, p;\n"
+      "}" ::"r"(d), "r"(a), "r"(b), "r"(kOperandHigh), "r"(inst), "r"(static_cast<uint32_t>(add))
+      : "memory");
+}
+
+// 128 bytes of both.
+__device__ __forceinline__ void mma8_chunk(uint32_t d, uint32_t a, uint32_t b, uint32_t inst, bool add) {
+  d = uniform(d), a = uniform(a), b = uniform(b);
+  asm volatile(
+      "{\n .reg .pred p, q, t;\n .reg .b32 x, y;\n .reg .b64 a, b;\n"
+      " setp.ne.u32 p, %5, 0;\n setp.eq.u32 t, 0, 0;\n elect.sync _|q, 0xffffffff;\n"
+      " add.u32 x, %1, 0; add.u32 y, %2, 0; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, p;\n"
+      " add.u32 x, %1, 2; add.u32 y, %2, 2; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, t;\n"
+      " add.u32 x, %1, 4; add.u32 y, %2, 4; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, t;\n"
+      " add.u32 x, %1, 6; add.u32 y, %2, 6; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, t;\n"
+      "}" ::"r"(d), "r"(a), "r"(b), "r"(kOperandHigh), "r"(inst), "r"(static_cast<uint32_t>(add))
+      : "memory");
+}
+
+// One arrival on `bar` when every product that this warp has issued is done.
 __device__ __forceinline__ void commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar)
+      : "memory");
 }
 
 }  // namespace umma
