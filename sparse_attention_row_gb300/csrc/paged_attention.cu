@@ -52,6 +52,7 @@ constexpr int kMaxSlots = 6;
 constexpr int kMaxQk = 576, kMaxV = 512;
 constexpr int kMaxBlockCols = 64;
 constexpr int kJoinThreads = 128, kJoinCols = 8;
+constexpr int kMaxParts = 256;  // slices of a launch at most
 constexpr float kMoveAbove = 8.f;  // in powers of two
 
 struct Join {  // what the join kernel has to know of the unit that ends in a slice and began before it
@@ -146,7 +147,10 @@ struct Walk {
 // A place in the ring of pieces, and the parity of its barrier's phase.
 struct Ring {
   uint32_t slot = 0, phase = 0;
-  __device__ void step(uint32_t slots, uint32_t by = 1) {
+  __device__ __forceinline__ void step(uint32_t slots) {
+    if (++slot == slots) slot = 0, phase ^= 1;
+  }
+  __device__ __forceinline__ void step(uint32_t slots, uint32_t by) {
     for (slot += by; slot >= slots; slot -= slots) phase ^= 1;
   }
 };
@@ -230,7 +234,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   }
 }
 
-template <int N, bool kBf16>
+template <int N, bool kBf16, bool kLatent>
 __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(1024) uint8_t raw[];
   const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
@@ -380,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         if (seen)
           kp += 2 * (static_cast<int64_t>(at_block) * p.a.k_block_stride + place * p.a.k_token_stride + walk.kv_head * p.a.k_head_stride);
         const char* vp = static_cast<const char*>(p.a.v);
-        if (seen && !p.latent)
+        if (seen && !kLatent)
           vp += 2 * (static_cast<int64_t>(at_block) * p.a.v_block_stride + place * p.a.v_token_stride + walk.kv_head * p.a.v_head_stride);
         const int next_block = table_entry(next_token), later_token = listed(t + 2);
         copies.aim(kp, seen, lane);
@@ -390,12 +394,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           copies_arrive(full + at.slot * 8);
           at.step(p.slots);
         }
-        if (p.rest) {
+        if (kLatent && p.rest) {
           mbar_wait(smem_addr(&sm.rest_empty), (tile & 1) ^ 1, guard);
           copies.piece(rest, k_ring * 128, p.a.dk - k_ring * 128, p.a.k);
           copies_arrive(smem_addr(&sm.rest_full));
         }
-        if (!p.latent) {
+        if (!kLatent) {
           copies.aim(vp, seen, lane);
           for (int u = 0; u < p.v_pieces; ++u) {
             mbar_wait(empty + at.slot * 8, at.phase ^ 1, guard);
@@ -416,39 +420,49 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     constexpr uint32_t kInstO = instruction(kBf16 ? kBF16 : kF16, N, true);
     const uint32_t full = smem_addr(&sm.full[0]), empty = smem_addr(&sm.empty[0]);
     Ring kr, vr;  // the pieces of keys and of values that come next
-    if (!p.latent) vr.step(p.slots, k_ring);
+    if (!kLatent) vr.step(p.slots, k_ring);
     uint32_t scored = 0;                    // tiles whose scores have been taken
     // S^T of the next tile, into one of its two places
+    const int whole_pieces = p.a.dk / 128;
     const auto scores = [&]() {
       const uint32_t d = tmem + s_cols + (scored & 1) * N;
-      for (int u = 0; u < p.k_pieces; ++u) {
+      uint32_t q_piece = q_at;
+#pragma unroll 1
+      for (int u = 0; u < whole_pieces; ++u, q_piece += 2 * N * 128) {
+        mbar_wait_warp(full + kr.slot * 8, kr.phase, guard);
+        fence_async();
+        mma16_piece(d, operand(ring + kr.slot * kPiece, 16), operand(q_piece, 16), operand(q_piece + N * 128, 16), kInstS, u > 0);
+        if (!kLatent || u >= p.v_pieces) commit(empty + kr.slot * 8);  // keys that are no values are done with
+        kr.step(p.slots);
+      }
+      if (whole_pieces < p.k_pieces) {  // the last one is not whole
         uint32_t at = rest;
-        if (u < k_ring) {
+        if (kLatent && p.rest) {
+          mbar_wait_warp(smem_addr(&sm.rest_full), scored & 1, guard);
+        } else {
           at = ring + kr.slot * kPiece;
           mbar_wait_warp(full + kr.slot * 8, kr.phase, guard);
-        } else {
-          mbar_wait_warp(smem_addr(&sm.rest_full), scored & 1, guard);
         }
         fence_async();
-        const int dims = min(p.a.dk - u * 128, 128);
-        const uint32_t q_piece = q_at + u * 2 * (N * 128);
-        if (dims == 128) {
-          mma16_piece(d, operand(at, 16), operand(q_piece, 16), operand(q_piece + N * 128, 16), kInstS, u > 0);
-        } else {
-          int k = 0;
-          if (dims >= 64) mma16_chunk(d, operand(at, 16), operand(q_piece, 16), kInstS, u + k++ > 0);
-          for (int i = 0; k * 64 + i * 16 < dims; ++i)
-            mma16_step(d, operand(at + k * kChunk + i * 32, 16), operand(q_piece + k * (N * 128) + i * 32, 16), kInstS, u + k + i > 0);
+        int left = p.a.dk - whole_pieces * 128;
+        bool add = whole_pieces > 0;
+        if (left >= 64) {
+          mma16_chunk(d, operand(at, 16), operand(q_piece, 16), kInstS, add);
+          add = true;
+          left -= 64;
+          at += kChunk;
+          q_piece += N * 128;
         }
-        // keys that are no values are done with
-        if (u < k_ring) {
-          if (!p.latent || u >= p.v_pieces) commit(empty + kr.slot * 8);
+#pragma unroll 1
+        for (; left > 0; left -= 16, at += 32, q_piece += 32, add = true) mma16_step(d, operand(at, 16), operand(q_piece, 16), kInstS, add);
+        if (kLatent && p.rest) {
+          if (!p.rest_is_p) commit(smem_addr(&sm.rest_empty));
+        } else {
+          if (!kLatent || whole_pieces >= p.v_pieces) commit(empty + kr.slot * 8);
           kr.step(p.slots);
-        } else if (!p.rest_is_p) {
-          commit(smem_addr(&sm.rest_empty));
         }
       }
-      if (!p.latent) kr.step(p.slots, p.v_pieces);
+      if (!kLatent) kr.step(p.slots, p.v_pieces);
       commit(smem_addr(&sm.s_full[scored & 1]));
       ++scored;
     };
@@ -456,15 +470,26 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     for (; walk.left > 0; walk.next(p), ++segment) {
       mbar_wait_warp(smem_addr(&sm.q_full), segment & 1, guard);
       fence_async();
-      if (p.ahead) scores();
+      int to_score = walk.count;
+      if (p.ahead) {
+        scores();
+        --to_score;
+      }
+#pragma unroll 1
       for (int t = 0; t < walk.count; ++t, ++tile) {
-        const bool last = t + 1 == walk.count;
-        if (p.ahead ? !last : true) scores();
-        if (p.ahead ? t + 2 == walk.count || walk.count == 1 : last) commit(smem_addr(&sm.q_empty));
+        if (to_score > 0) {
+          scores();
+          --to_score;
+        }
+        if (to_score == 0) {  // once: the queries are done with
+          commit(smem_addr(&sm.q_empty));
+          --to_score;
+        }
         mbar_wait_warp(smem_addr(&sm.p_full), tile & 1, guard);
         fence_after();
+#pragma unroll 1
         for (int u = 0; u < p.v_pieces; ++u) {
-          if (!p.latent) {
+          if (!kLatent) {
             mbar_wait_warp(full + vr.slot * 8, vr.phase, guard);
             fence_async();
           }
@@ -472,8 +497,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           commit(empty + vr.slot * 8);
           vr.step(p.slots);
         }
-        vr.step(p.slots, p.latent ? k_ring - p.v_pieces : k_ring);
-        if (p.rest && p.rest_is_p) commit(smem_addr(&sm.rest_empty));
+        vr.step(p.slots, kLatent ? k_ring - p.v_pieces : k_ring);
+        if (kLatent && p.rest_is_p) commit(smem_addr(&sm.rest_empty));
         commit(smem_addr(&sm.o_done));
       }
     }
@@ -665,49 +690,102 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   if (warp == kMmaWarp) tmem_free(tmem, p.tmem_cols);
 }
 
-// Joins the parts of the units that fell into several slices: eight columns of a unit a CTA.
+// A load that stays where it is written: left to the compiler, the join's loads move to their uses, one latency each
+// (4 parts of eight loads a thread: 17 000 cycles against 4300).
+__device__ __forceinline__ float4 load_now(const float4* at) {
+  float4 v;
+  asm volatile("ld.global.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(at) : "memory");
+  return v;
+}
+
+// Joins the parts of the units that fell into several slices: eight columns of a unit a CTA. The parts' places and
+// weights are found once, 16 lanes to a column; then every thread sums its values over the parts.
 template <int N, bool kBf16>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Params p) {
+  __shared__ int32_t place[kMaxParts];  // [part]: its place in `part` and `stat`, in columns
+  __shared__ float weight[kMaxParts][kJoinCols];
+  __shared__ float inverse[kJoinCols];
+  const int per = N / kJoinCols, tid = threadIdx.x;
+  const int slice = blockIdx.x / (p.blocks * per), block = blockIdx.x / per % p.blocks, col0 = blockIdx.x % per * kJoinCols;
+  const int block_cols = min(p.block_cols, p.cols - block * p.block_cols);
   dependent_wait();
   dependent_launch();
-  const int per = N / kJoinCols;
-  const int slice = blockIdx.x / (p.blocks * per), block = blockIdx.x / per % p.blocks, col0 = blockIdx.x % per * kJoinCols;
   const Join jn = p.join[slice];
-  if (jn.last < 0) return;
-  const int width = p.v_pieces * 128;
-  const int block_cols = min(p.block_cols, p.cols - block * p.block_cols);
+  if (jn.last < 0 || col0 >= block_cols) return;
+  const int parts = jn.last - jn.first + 1, width = p.v_pieces * 128;
   const int64_t row0 = jn.rowgroup * p.pack;
-  for (int n = col0; n < min(col0 + kJoinCols, block_cols); ++n) {
-    float m = -INFINITY, sum = 0.f;
-    for (int s = jn.first; s <= jn.last; ++s) {
-      if (slice_begin(jn.tiles, p.slices, s) == slice_begin(jn.tiles, p.slices, s + 1)) continue;
-      const int64_t slot = ((static_cast<int64_t>(s) * 2 + (s == jn.first ? jn.first_slot : 0)) * p.blocks + block) * N;
-      const float2 st = p.stat[slot + n];
-      const float m2 = fmaxf(m, st.x), b = m2 == -INFINITY ? 0.f : m2;
-      sum = sum * exp2f(m - b) + st.y * exp2f(st.x - b);
-      m = m2;
-    }
-    const float b = m == -INFINITY ? 0.f : m, inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int c = block * p.block_cols + n, j = c / p.group;
-    const int64_t head = jn.kv_head * p.group + c - j * p.group;
-    if (p.a.lse && threadIdx.x == 0) p.a.lse[(row0 + j) * p.a.heads + head] = sum == 0.f ? -INFINITY : (b + log2f(sum)) * 0.69314718055994531f;
-    for (int d = threadIdx.x * 4; d < p.a.dv; d += kJoinThreads * 4) {
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int s = jn.first; s <= jn.last; ++s) {
-        if (slice_begin(jn.tiles, p.slices, s) == slice_begin(jn.tiles, p.slices, s + 1)) continue;
-        const int64_t slot = ((static_cast<int64_t>(s) * 2 + (s == jn.first ? jn.first_slot : 0)) * p.blocks + block) * N;
-        const float f = exp2f(p.stat[slot + n].x - b);
-        const float4 y = *reinterpret_cast<const float4*>(p.part + (slot + n) * width + d);
-        x.x += f * y.x;
-        x.y += f * y.y;
-        x.z += f * y.z;
-        x.w += f * y.w;
+  for (int i = tid; i < parts; i += kJoinThreads) {
+    const int s = jn.first + i;
+    const bool empty = slice_begin(jn.tiles, p.slices, s) == slice_begin(jn.tiles, p.slices, s + 1);
+    place[i] = empty ? -1 : ((s * 2 + (i == 0 ? jn.first_slot : 0)) * p.blocks + block) * N + col0;
+  }
+  __syncthreads();
+  {
+    const int col = tid >> 4, sub = tid & 15;
+    float m = -INFINITY;
+    for (int i = sub; i < parts; i += 16)
+      if (place[i] >= 0) m = fmaxf(m, p.stat[place[i] + col].x);
+#pragma unroll
+    for (int d = 8; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+    const float base = m == -INFINITY ? 0.f : m;
+    float sum = 0.f;
+    for (int i = sub; i < parts; i += 16) {
+      float w = 0.f;
+      if (place[i] >= 0) {
+        const float2 st = p.stat[place[i] + col];
+        w = exp2f(st.x - base);
+        sum += w * st.y;
       }
+      weight[i][col] = w;
+    }
+#pragma unroll
+    for (int d = 8; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+    if (sub == 0) {
+      inverse[col] = sum == 0.f ? 0.f : 1.f / sum;
+      const int n = col0 + col, c = block * p.block_cols + n, j = c / p.group;
+      if (p.a.lse && n < block_cols)
+        p.a.lse[(row0 + j) * p.a.heads + jn.kv_head * p.group + c - j * p.group] =
+            sum == 0.f ? -INFINITY : (base + log2f(sum)) * 0.69314718055994531f;
+    }
+  }
+  __syncthreads();
+  constexpr int kEach = kJoinCols * kMaxV / 4 / kJoinThreads;
+  float4 x[kEach];
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  int from_at[kEach], col_at[kEach];  // what is past the columns' end is read again from their last values, and not stored
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    from_at[k] = min(tid + k * kJoinThreads, kJoinCols * width / 4 - 1);
+    col_at[k] = from_at[k] * 4 / width;
+  }
+  for (int i = 0; i < parts; ++i) {
+    const float4* from = reinterpret_cast<const float4*>(p.part + static_cast<int64_t>(max(place[i], 0)) * width);
+    float4 y[kEach];
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) y[k] = load_now(from + from_at[k]);
+    if (place[i] < 0) continue;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const float w = weight[i][col_at[k]];
+      x[k].x += w * y[k].x;
+      x[k].y += w * y[k].y;
+      x[k].z += w * y[k].z;
+      x[k].w += w * y[k].w;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int e = (tid + k * kJoinThreads) * 4, col = e / width, d = e - col * width, n = col0 + col;
+    if (col < kJoinCols && n < block_cols && d < p.a.dv) {
+      const float f = inverse[col];
+      if (f == 0.f) x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      const int c = block * p.block_cols + n, j = c / p.group;
       uint2 packed;
-      if (sum == 0.f) x = make_float4(0.f, 0.f, 0.f, 0.f);
-      packed.x = pack2<kBf16>(x.x * inv, x.y * inv);
-      packed.y = pack2<kBf16>(x.z * inv, x.w * inv);
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.a.out) + (row0 + j) * p.a.out_row_stride + head * p.a.out_head_stride + d) = packed;
+      packed.x = pack2<kBf16>(x[k].x * f, x[k].y * f);
+      packed.y = pack2<kBf16>(x[k].z * f, x[k].w * f);
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.a.out) + (row0 + j) * p.a.out_row_stride +
+                                static_cast<int64_t>(jn.kv_head * p.group + c - j * p.group) * p.a.out_head_stride + d) = packed;
     }
   }
 }
@@ -724,7 +802,7 @@ size_t workspace_for(int sms) {
 
 static_assert(sizeof(Smem<64>) + 1024 + 9 * 64 * 128 + 4 * kPiece + kChunk <= 232448, "latent attention of 64 columns: four pieces of the ring");
 
-template <int N, bool kBf16>
+template <int N, bool kBf16, bool kLatent>
 int run(Params& p, int smem_limit, bool joins, cudaStream_t stream) {
   const int extra = static_cast<int>(sizeof(Smem<N>)) + 1024;
   p.q_bytes = p.k_chunks * N * 128;
@@ -742,13 +820,20 @@ int run(Params& p, int smem_limit, bool joins, cudaStream_t stream) {
   p.tmem_cols = 32;
   while (p.tmem_cols < static_cast<uint32_t>((p.v_pieces + 2) * N)) p.tmem_cols *= 2;
   const size_t smem = p.q_bytes + static_cast<size_t>(p.slots) * kPiece + (p.rest && !p.rest_is_p ? kChunk : 0) + kChunk + extra;
-  if (cudaFuncSetAttribute(attention_kernel<N, kBf16>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) {
+  if (cudaFuncSetAttribute(attention_kernel<N, kBf16, kLatent>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) {
     cudaGetLastError();
     return TOPK_ERR_CUDA;
   }
-  int rc = launch(attention_kernel<N, kBf16>, static_cast<const Params&>(p), static_cast<int64_t>(p.slices) * p.blocks, kThreads, smem, stream);
+  int rc = launch(attention_kernel<N, kBf16, kLatent>, static_cast<const Params&>(p), static_cast<int64_t>(p.slices) * p.blocks, kThreads, smem, stream);
   if (rc != TOPK_OK || !joins) return rc;
   return launch(join_kernel<N, kBf16>, static_cast<const Params&>(p), static_cast<int64_t>(p.slices) * p.blocks * (N / kJoinCols), kJoinThreads, 0, stream);
+}
+
+template <int N>
+int run_columns(Params& p, int smem_limit, bool joins, cudaStream_t stream) {
+  const bool bf16 = p.a.dtype == TOPK_DTYPE_BF16;
+  if (p.latent) return bf16 ? run<N, true, true>(p, smem_limit, joins, stream) : run<N, false, true>(p, smem_limit, joins, stream);
+  return bf16 ? run<N, true, false>(p, smem_limit, joins, stream) : run<N, false, false>(p, smem_limit, joins, stream);
 }
 
 }  // namespace
@@ -813,6 +898,7 @@ extern "C" int topk_paged_attention(const topk_attention_args* args, void* strea
   const int64_t most = units * (a.indices ? p.row_tiles : (p.R.max_len + kTile - 1) / kTile);
   int64_t slices = sms / p.blocks < 1 ? 1 : sms / p.blocks;
   if (slices > most) slices = most;
+  if (slices > kMaxParts) slices = kMaxParts;
   p.slices = static_cast<int32_t>(slices);
   bool joins = true;
   if (p.row_tiles) {  // every unit has as many tiles: the host can see whether a slice begins inside one
@@ -826,8 +912,7 @@ extern "C" int topk_paged_attention(const topk_attention_args* args, void* strea
   w += static_cast<size_t>(most_ctas(sms)) * 2 * kMaxBlockCols * sizeof(float2);
   p.part = reinterpret_cast<float*>(w);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool bf = a.dtype == TOPK_DTYPE_BF16;
-  if (p.block_cols <= 16) return bf ? run<16, true>(p, props.max_smem_optin, joins, s) : run<16, false>(p, props.max_smem_optin, joins, s);
-  if (p.block_cols <= 32) return bf ? run<32, true>(p, props.max_smem_optin, joins, s) : run<32, false>(p, props.max_smem_optin, joins, s);
-  return bf ? run<64, true>(p, props.max_smem_optin, joins, s) : run<64, false>(p, props.max_smem_optin, joins, s);
+  if (p.block_cols <= 16) return run_columns<16>(p, props.max_smem_optin, joins, s);
+  if (p.block_cols <= 32) return run_columns<32>(p, props.max_smem_optin, joins, s);
+  return run_columns<64>(p, props.max_smem_optin, joins, s);
 }

@@ -38,6 +38,17 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   return done != 0;
 }
 
+// The same, suspended for up to 20 us where the phase is not over yet.
+__device__ __forceinline__ bool mbar_try_long(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity), "r"(20000u)
+      : "memory");
+  return done != 0;
+}
+
 // A CTA's waits. One that runs out sets the flag, after which every wait of the CTA returns at once: the
 // loops run to their end without waiting, over memory that stays in bounds, and the launch's status says
 // that its results are void.
@@ -56,7 +67,7 @@ __device__ __forceinline__ uint64_t now_ns() {
 
 static __device__ __noinline__ void mbar_wait_slow(uint32_t bar, uint32_t parity, volatile uint32_t* gave_up, uint32_t* status) {
   const uint64_t t0 = now_ns();
-  while (!mbar_try(bar, parity)) {
+  while (!mbar_try_long(bar, parity)) {
     if (*gave_up) return;
     if (now_ns() - t0 > kWaitLimitNs) {
       *gave_up = 1;
