@@ -51,8 +51,9 @@ constexpr int kTokenSlots = 8;  // more than the tiles that the copies can be ah
 constexpr int kMaxSlots = 6;
 constexpr int kMaxQk = 576, kMaxV = 512;
 constexpr int kMaxBlockCols = 64;
-constexpr int kJoinThreads = 128, kJoinCols = 8;
+constexpr int kJoinThreads = 128, kJoinDims = 32;
 constexpr int kMaxParts = 256;  // slices of a launch at most
+constexpr int kSplitTiles = 4;
 constexpr float kMoveAbove = 8.f;  // in powers of two
 
 struct Join {  // what the join kernel has to know of the unit that ends in a slice and began before it
@@ -80,6 +81,7 @@ struct Params {
   int32_t ahead;         // 1: the next tile's scores are taken before this tile's values
   int32_t slices;
   int32_t row_tiles;     // tiles of every unit where index lists are given, else 0
+  int32_t whole;         // 1: slices begin between units only (index lists)
   int64_t row_groups;
   uint32_t tmem_cols;
   uint32_t q_bytes;
@@ -93,15 +95,16 @@ template <int N>
 struct Smem {  // behind the tiles
   static constexpr int kHalf = N / 2;
   int32_t token[kTokenSlots][kTile];  // position of each token of a tile, INT_MAX where nothing is to be seen
-  float column_max[2][2][4][kHalf];   // [parity][half][warp]
+  float column_max[2][4][kHalf];      // [half][warp]; a barrier stands between one tile's reads and the next one's writes
   float moved[kSoftmaxWarps][2][kHalf];  // maximum in use, factor of the old sums
   float column_sum[2][4][kHalf];
   int32_t limit[2][2][kHalf];  // [parity of the segment][half]: tokens that a column sees
+  int64_t out_at[2][2][kHalf];  // and where its output lies
   int32_t least[2][2];
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t q_full, q_empty, rest_full, rest_empty, s_full[2], p_full, o_done, token_full[kTokenSlots], all_done;
   int64_t scan[kThreads / 32];
-  int64_t start_group, tiles;
+  int64_t start_group, tiles, run_begin, run_end;
   int64_t start_at;
   uint32_t tmem;
   uint32_t gave_up;
@@ -120,8 +123,16 @@ __device__ __forceinline__ int group_tiles(const Params& p, int64_t g, bool repo
   return n == 0 ? 1 : (n + kTile - 1) / kTile;
 }
 
-__device__ __forceinline__ int64_t slice_begin(int64_t tiles, int slices, int s) { return tiles * s / slices; }
+// First tile of slice s, and the slice of tile x; in 32 bits where the products fit (a 64-bit division takes some
+// hundreds of cycles, and a launch starts with several).
+constexpr int64_t kSmallTiles = 1 << 22;
+__device__ __forceinline__ int64_t slice_begin(int64_t tiles, int slices, int s) {
+  if (tiles < kSmallTiles) return static_cast<uint32_t>(tiles) * static_cast<uint32_t>(s) / static_cast<uint32_t>(slices);
+  return tiles * s / slices;
+}
 __device__ __forceinline__ int slice_of(int64_t tiles, int slices, int64_t x) {
+  if (tiles < kSmallTiles)
+    return static_cast<int>((static_cast<uint32_t>(x + 1) * static_cast<uint32_t>(slices) - 1) / static_cast<uint32_t>(tiles));
   return static_cast<int>(((x + 1) * slices - 1) / tiles);
 }
 
@@ -270,10 +281,20 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   // where this slice's run begins
   if (p.row_tiles) {
     if (tid == 0) {
-      sm.tiles = p.row_groups * p.a.kv_heads * p.row_tiles;
-      const int64_t begin = slice_begin(sm.tiles, p.slices, slice), unit = begin / p.row_tiles;
-      sm.start_group = unit / p.a.kv_heads;
-      sm.start_at = begin - sm.start_group * p.a.kv_heads * p.row_tiles;
+      const int64_t units = p.row_groups * p.a.kv_heads;
+      sm.tiles = units * p.row_tiles;
+      if (p.whole) {
+        const int64_t unit = slice_begin(units, p.slices, slice);
+        sm.run_begin = unit * p.row_tiles;
+        sm.run_end = slice_begin(units, p.slices, slice + 1) * p.row_tiles;
+        sm.start_group = p.a.kv_heads == 1 ? unit : unit / p.a.kv_heads;
+      } else {
+        sm.run_begin = slice_begin(sm.tiles, p.slices, slice);
+        sm.run_end = slice_begin(sm.tiles, p.slices, slice + 1);
+        const int64_t per = static_cast<int64_t>(p.row_tiles) * p.a.kv_heads;
+        sm.start_group = sm.run_begin < kSmallTiles ? static_cast<uint32_t>(sm.run_begin) / static_cast<uint32_t>(per) : sm.run_begin / per;
+      }
+      sm.start_at = sm.run_begin - sm.start_group * p.a.kv_heads * p.row_tiles;
     }
   } else {
     const int64_t per = (p.row_groups + kThreads - 1) / kThreads;
@@ -307,21 +328,27 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         at += n;
       }
     }
-    if (tid == 0) sm.tiles = total;
+    if (tid == 0) {
+      sm.tiles = total;
+      sm.run_begin = begin;
+      sm.run_end = slice_begin(total, p.slices, slice + 1);
+    }
   }
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = sm.tmem;
-  const int64_t all_tiles = sm.tiles, run_begin = slice_begin(all_tiles, p.slices, slice);
+  const int64_t all_tiles = sm.tiles, run_begin = sm.run_begin;
   Walk walk;
-  walk.left = slice_begin(all_tiles, p.slices, slice + 1) - run_begin;
+  walk.left = sm.run_end - run_begin;
   walk.group = sm.start_group;
   walk.count = 0;
   if (walk.left > 0) {
     walk.tiles = group_tiles(p, walk.group, false);
-    walk.kv_head = static_cast<int>(sm.start_at / walk.tiles);
-    walk.at = static_cast<int>(sm.start_at % walk.tiles);
+    walk.kv_head = 0;
+    int64_t at = sm.start_at;
+    for (; at >= walk.tiles; at -= walk.tiles) ++walk.kv_head;
+    walk.at = static_cast<int>(at);
     walk.size();
   }
   const int k_ring = p.k_pieces - p.rest;                       // pieces of the keys in the ring
@@ -407,6 +434,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             copies_arrive(full + at.slot * 8);
             at.step(p.slots);
           }
+        }
+        // a latent tile's copies wait for the tile before it to leave the ring: until then, fetch its tokens into L2, the
+        // blocks of a unit a part of them each
+        if (kLatent && next_token >= 0 && next_token < length && next_block >= 0 && next_block < p.R.num_blocks) {
+          const char* next = static_cast<const char*>(p.a.k) +
+                             2 * (static_cast<int64_t>(next_block) * p.a.k_block_stride +
+                                  (next_token - column(next_token) * p.R.block_size) * p.a.k_token_stride + walk.kv_head * p.a.k_head_stride);
+          for (int line = block; line * 64 < p.a.dk; line += p.blocks) asm volatile("prefetch.global.L2 [%0];" ::"l"(next + line * 128));
         }
         at_token = next_token;
         at_block = next_block;
@@ -519,7 +554,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       if (quarter == 0) {  // what each column sees
         const int c = block * p.block_cols + my_col;
         int n = INT_MAX;
-        if (my_col < block_cols) n = row_length(p.R, row0 + c / p.group, p.row_tiles != 0 && block == 0);
+        if (my_col < block_cols) {
+          const int j = c / p.group;
+          n = row_length(p.R, row0 + j, p.row_tiles != 0 && block == 0);
+          if (lane < H)
+            sm.out_at[segment & 1][half][lane] = (row0 + j) * p.a.out_row_stride + static_cast<int64_t>(walk.kv_head * p.group + c - j * p.group) * p.a.out_head_stride;
+        }
         int least = n;
 #pragma unroll
         for (int d = 16; d; d >>= 1) least = min(least, __shfl_xor_sync(~0u, least, d));
@@ -528,7 +568,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       }
       named_sync(1 + half, 128);
       const int least = sm.least[segment & 1][half];
-      float m = -INFINITY, in_use = 0.f;  // of my_col, in powers of two
+      // of my_col, in powers of two: its maximum when that last moved, and what is taken off its scores; below every score
+      // until a finite one has come
+      float m = -INFINITY, in_use = -1e30f;
       float l[H];
 #pragma unroll
       for (int i = 0; i < H; ++i) l[i] = 0.f;
@@ -545,25 +587,40 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           for (int i = 0; i < H; ++i)
             if (pos >= sm.limit[segment & 1][half][i]) s[i] = -INFINITY;
         }
-        const float warp_max = reduce_columns<H, true>(s, lane);
-        if (lane < H) sm.column_max[tile & 1][half][quarter][lane] = warp_max;
-        named_sync(1 + half, 128);
-        float top = -INFINITY;
+        // does any score exceed the maximum in use by so much that it has to move?
+        bool move_any = t == 0;
+        if (t > 0) {
+          float x = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) top = fmaxf(top, sm.column_max[tile & 1][half][w][lane & (H - 1)]);
-        top *= p.scale2;
-        const bool move = top > m + kMoveAbove || (m == -INFINITY && top > m);
-        const bool rescale = __any_sync(~0u, move && m > -INFINITY);
-        const float factor = move && m > -INFINITY ? exp2_fast(m - top) : 1.f;
-        if (move) {
-          m = top;
-          in_use = m - kShift;
+          for (int i = 0; i < H; i += 4) {
+            const float4 u = *reinterpret_cast<const float4*>(&sm.moved[warp][0][i]);
+            x = fmaxf(x, fmaxf(fmaf(s[i], p.scale2, -u.x), fmaf(s[i + 1], p.scale2, -u.y)));
+            x = fmaxf(x, fmaxf(fmaf(s[i + 2], p.scale2, -u.z), fmaf(s[i + 3], p.scale2, -u.w)));
+          }
+          move_any = named_any(1 + half, 128, x > kMoveAbove + kShift);
         }
-        if (lane < H) {
-          sm.moved[warp][0][lane] = in_use;
-          sm.moved[warp][1][lane] = factor;
+        bool rescale = false;
+        if (move_any) {
+          const float warp_max = reduce_columns<H, true>(s, lane);
+          if (lane < H) sm.column_max[half][quarter][lane] = warp_max;
+          named_sync(1 + half, 128);
+          float top = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) top = fmaxf(top, sm.column_max[half][w][lane & (H - 1)]);
+          top *= p.scale2;
+          const bool move = top > m + kMoveAbove || (m == -INFINITY && top > m);
+          rescale = __any_sync(~0u, move && m > -INFINITY);
+          const float factor = move && m > -INFINITY ? exp2_fast(m - top) : 1.f;
+          if (move) {
+            m = top;
+            in_use = m - kShift;
+          }
+          if (lane < H) {
+            sm.moved[warp][0][lane] = in_use;
+            sm.moved[warp][1][lane] = factor;
+          }
+          __syncwarp();
         }
-        __syncwarp();
 #pragma unroll
         for (int i = 0; i < H; i += 4) {
           const float4 u = *reinterpret_cast<const float4*>(&sm.moved[warp][0][i]);
@@ -628,35 +685,33 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       __syncwarp();
       mbar_wait(smem_addr(&sm.o_done), (tile - 1) & 1, guard);
       fence_after();
+#pragma unroll 1
       for (int u = 0; u < p.v_pieces; ++u) {
         float o[H];
         tmem_load(tmem + lanes + u * N + half * H, o);
         load_wait(o);
         const int dim = u * 128 + token;
 #pragma unroll
-        for (int i = 0; i < H; ++i) {
-          const float f = sm.moved[warp][0][i];
-          o[i] = f == 0.f ? 0.f : o[i] * f;
+        for (int i = 0; i < H; i += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(&sm.moved[warp][0][i]);
+          o[i] = f.x == 0.f ? 0.f : o[i] * f.x;
+          o[i + 1] = f.y == 0.f ? 0.f : o[i + 1] * f.y;
+          o[i + 2] = f.z == 0.f ? 0.f : o[i + 2] * f.z;
+          o[i + 3] = f.w == 0.f ? 0.f : o[i + 3] * f.w;
         }
-        if (!whole) {
-          float* to = p.part + (slot + half * H) * (p.v_pieces * 128) + dim;
+        if (!whole) {  // [dim][column]: a thread's columns side by side
+          float4* to = reinterpret_cast<float4*>(p.part + slot * (p.v_pieces * 128) + dim * N + half * H);
 #pragma unroll
-          for (int i = 0; i < H; ++i)
-            if (half * H + i < block_cols) to[static_cast<int64_t>(i) * (p.v_pieces * 128)] = o[i];
+          for (int i = 0; i < H; i += 4) to[i / 4] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
         } else {
           // two columns at a time: neighbouring lanes exchange values and store pairs of dims
+          const int odd = lane & 1, d = dim - odd, real = d < p.a.dv ? block_cols - half * H - odd : 0;
+          const int64_t* out_at = sm.out_at[segment & 1][half] + odd;
+          uint16_t* out = static_cast<uint16_t*>(p.a.out) + d;
 #pragma unroll
           for (int i = 0; i < H; i += 2) {
-            const bool odd = lane & 1;
             const float other = __shfl_xor_sync(~0u, odd ? o[i] : o[i + 1], 1);
-            const int n = half * H + i + odd;
-            const int c = block * p.block_cols + n, j = c / p.group;
-            const int d = dim - odd;
-            if (n < block_cols && d < p.a.dv) {
-              uint16_t* to = static_cast<uint16_t*>(p.a.out) + (row0 + j) * p.a.out_row_stride +
-                             static_cast<int64_t>(walk.kv_head * p.group + c - j * p.group) * p.a.out_head_stride + d;
-              *reinterpret_cast<uint32_t*>(to) = odd ? pack2<kBf16>(other, o[i + 1]) : pack2<kBf16>(o[i], other);
-            }
+            if (i < real) *reinterpret_cast<uint32_t*>(out + out_at[i]) = odd ? pack2<kBf16>(other, o[i + 1]) : pack2<kBf16>(o[i], other);
           }
         }
       }
@@ -698,95 +753,101 @@ __device__ __forceinline__ float4 load_now(const float4* at) {
   return v;
 }
 
-// Joins the parts of the units that fell into several slices: eight columns of a unit a CTA. The parts' places and
-// weights are found once, 16 lanes to a column; then every thread sums its values over the parts.
+// Joins the parts of the units that fell into several slices: kJoinDims values of a unit's columns a CTA. Every thread
+// has four columns of some values and sums them over the parts, four parts' loads at a time; the sums go through shared
+// memory to be stored along the values.
 template <int N, bool kBf16>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Params p) {
-  __shared__ int32_t place[kMaxParts];  // [part]: its place in `part` and `stat`, in columns
-  __shared__ float weight[kMaxParts][kJoinCols];
-  __shared__ float inverse[kJoinCols];
-  const int per = N / kJoinCols, tid = threadIdx.x;
-  const int slice = blockIdx.x / (p.blocks * per), block = blockIdx.x / per % p.blocks, col0 = blockIdx.x % per * kJoinCols;
+  __shared__ int32_t place[kMaxParts];  // of each part, in columns; -1: the slice was empty
+  __shared__ float base[N], inverse[N];
+  __shared__ float sums[kJoinDims][N + 4];
+  const int tid = threadIdx.x, per = p.v_pieces * 128 / kJoinDims;
+  const int dim0 = blockIdx.x % per * kJoinDims, block = blockIdx.x / per % p.blocks, slice = blockIdx.x / per / p.blocks;
   const int block_cols = min(p.block_cols, p.cols - block * p.block_cols);
   dependent_wait();
   dependent_launch();
   const Join jn = p.join[slice];
-  if (jn.last < 0 || col0 >= block_cols) return;
+  if (jn.last < 0 || dim0 >= p.a.dv) return;
   const int parts = jn.last - jn.first + 1, width = p.v_pieces * 128;
   const int64_t row0 = jn.rowgroup * p.pack;
   for (int i = tid; i < parts; i += kJoinThreads) {
     const int s = jn.first + i;
     const bool empty = slice_begin(jn.tiles, p.slices, s) == slice_begin(jn.tiles, p.slices, s + 1);
-    place[i] = empty ? -1 : ((s * 2 + (i == 0 ? jn.first_slot : 0)) * p.blocks + block) * N + col0;
+    place[i] = empty ? -1 : ((s * 2 + (i == 0 ? jn.first_slot : 0)) * p.blocks + block) * N;
   }
   __syncthreads();
-  {
-    const int col = tid >> 4, sub = tid & 15;
-    float m = -INFINITY;
-    for (int i = sub; i < parts; i += 16)
-      if (place[i] >= 0) m = fmaxf(m, p.stat[place[i] + col].x);
-#pragma unroll
-    for (int d = 8; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-    const float base = m == -INFINITY ? 0.f : m;
-    float sum = 0.f;
-    for (int i = sub; i < parts; i += 16) {
-      float w = 0.f;
-      if (place[i] >= 0) {
-        const float2 st = p.stat[place[i] + col];
-        w = exp2f(st.x - base);
-        sum += w * st.y;
-      }
-      weight[i][col] = w;
+  {  // each column's maximum and sum, by kJoinThreads / N lanes
+    constexpr int kLanes = kJoinThreads / N;
+    const int col = tid / kLanes, sub = tid % kLanes;
+    float m = -INFINITY, sum = 0.f;
+    for (int i = sub; i < parts; i += kLanes) {
+      if (place[i] < 0) continue;
+      const float2 st = p.stat[place[i] + col];
+      const float top = fmaxf(m, st.x), b = top == -INFINITY ? 0.f : top;
+      sum = sum * exp2f(m - b) + st.y * exp2f(st.x - b);
+      m = top;
     }
 #pragma unroll
-    for (int d = 8; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+    for (int d = kLanes / 2; d; d >>= 1) {
+      const float m2 = __shfl_xor_sync(~0u, m, d), sum2 = __shfl_xor_sync(~0u, sum, d);
+      const float top = fmaxf(m, m2), b = top == -INFINITY ? 0.f : top;
+      sum = sum * exp2f(m - b) + sum2 * exp2f(m2 - b);
+      m = top;
+    }
     if (sub == 0) {
+      base[col] = m == -INFINITY ? 0.f : m;
       inverse[col] = sum == 0.f ? 0.f : 1.f / sum;
-      const int n = col0 + col, c = block * p.block_cols + n, j = c / p.group;
-      if (p.a.lse && n < block_cols)
-        p.a.lse[(row0 + j) * p.a.heads + jn.kv_head * p.group + c - j * p.group] =
-            sum == 0.f ? -INFINITY : (base + log2f(sum)) * 0.69314718055994531f;
+      const int c = block * p.block_cols + col, j = c / p.group;
+      if (p.a.lse && dim0 == 0 && col < block_cols)
+        p.a.lse[(row0 + j) * p.a.heads + jn.kv_head * p.group + c - j * p.group] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
     }
   }
   __syncthreads();
-  constexpr int kEach = kJoinCols * kMaxV / 4 / kJoinThreads;
+  constexpr int kRow = N / 4, kEach = kJoinDims * kRow / kJoinThreads, kAtOnce = 4;
+  const int col = tid % kRow * 4, dim = tid / kRow;  // and every kJoinThreads / kRow dims on
   float4 x[kEach];
 #pragma unroll
   for (int k = 0; k < kEach; ++k) x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  int from_at[kEach], col_at[kEach];  // what is past the columns' end is read again from their last values, and not stored
+  const float4 b = make_float4(base[col], base[col + 1], base[col + 2], base[col + 3]);
+  for (int i = 0; i < parts; i += kAtOnce) {
+    float4 y[kAtOnce][kEach], st[kAtOnce][2];
 #pragma unroll
-  for (int k = 0; k < kEach; ++k) {
-    from_at[k] = min(tid + k * kJoinThreads, kJoinCols * width / 4 - 1);
-    col_at[k] = from_at[k] * 4 / width;
-  }
-  for (int i = 0; i < parts; ++i) {
-    const float4* from = reinterpret_cast<const float4*>(p.part + static_cast<int64_t>(max(place[i], 0)) * width);
-    float4 y[kEach];
+    for (int a = 0; a < kAtOnce; ++a) {
+      const int at = max(i + a < parts ? place[i + a] : 0, 0);
+      st[a][0] = load_now(reinterpret_cast<const float4*>(p.stat + at + col));
+      st[a][1] = load_now(reinterpret_cast<const float4*>(p.stat + at + col) + 1);
 #pragma unroll
-    for (int k = 0; k < kEach; ++k) y[k] = load_now(from + from_at[k]);
-    if (place[i] < 0) continue;
+      for (int k = 0; k < kEach; ++k)
+        y[a][k] = load_now(reinterpret_cast<const float4*>(p.part + static_cast<int64_t>(at) * width + (dim0 + dim + k * (kJoinThreads / kRow)) * N + col));
+    }
 #pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-      const float w = weight[i][col_at[k]];
-      x[k].x += w * y[k].x;
-      x[k].y += w * y[k].y;
-      x[k].z += w * y[k].z;
-      x[k].w += w * y[k].w;
+    for (int a = 0; a < kAtOnce; ++a) {
+      if (i + a >= parts || place[i + a] < 0) continue;
+      const float4 w = make_float4(exp2f(st[a][0].x - b.x), exp2f(st[a][0].z - b.y), exp2f(st[a][1].x - b.z), exp2f(st[a][1].z - b.w));
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) {
+        x[k].x += w.x * y[a][k].x;
+        x[k].y += w.y * y[a][k].y;
+        x[k].z += w.z * y[a][k].z;
+        x[k].w += w.w * y[a][k].w;
+      }
     }
   }
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
-    const int e = (tid + k * kJoinThreads) * 4, col = e / width, d = e - col * width, n = col0 + col;
-    if (col < kJoinCols && n < block_cols && d < p.a.dv) {
-      const float f = inverse[col];
-      if (f == 0.f) x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      const int c = block * p.block_cols + n, j = c / p.group;
-      uint2 packed;
-      packed.x = pack2<kBf16>(x[k].x * f, x[k].y * f);
-      packed.y = pack2<kBf16>(x[k].z * f, x[k].w * f);
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.a.out) + (row0 + j) * p.a.out_row_stride +
-                                static_cast<int64_t>(jn.kv_head * p.group + c - j * p.group) * p.a.out_head_stride + d) = packed;
-    }
+    float* to = &sums[dim + k * (kJoinThreads / kRow)][col];
+    to[0] = inverse[col] == 0.f ? 0.f : x[k].x * inverse[col];
+    to[1] = inverse[col + 1] == 0.f ? 0.f : x[k].y * inverse[col + 1];
+    to[2] = inverse[col + 2] == 0.f ? 0.f : x[k].z * inverse[col + 2];
+    to[3] = inverse[col + 3] == 0.f ? 0.f : x[k].w * inverse[col + 3];
+  }
+  __syncthreads();
+  for (int e = tid; e < block_cols * (kJoinDims / 2); e += kJoinThreads) {
+    const int n = e / (kJoinDims / 2), d = e % (kJoinDims / 2) * 2, c = block * p.block_cols + n, j = c / p.group;
+    if (dim0 + d < p.a.dv)
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.a.out) + (row0 + j) * p.a.out_row_stride +
+                                   static_cast<int64_t>(jn.kv_head * p.group + c - j * p.group) * p.a.out_head_stride + dim0 + d) =
+          pack2<kBf16>(sums[d][n], sums[d + 1][n]);
   }
 }
 
@@ -826,7 +887,7 @@ int run(Params& p, int smem_limit, bool joins, cudaStream_t stream) {
   }
   int rc = launch(attention_kernel<N, kBf16, kLatent>, static_cast<const Params&>(p), static_cast<int64_t>(p.slices) * p.blocks, kThreads, smem, stream);
   if (rc != TOPK_OK || !joins) return rc;
-  return launch(join_kernel<N, kBf16>, static_cast<const Params&>(p), static_cast<int64_t>(p.slices) * p.blocks * (N / kJoinCols), kJoinThreads, 0, stream);
+  return launch(join_kernel<N, kBf16>, static_cast<const Params&>(p), static_cast<int64_t>(p.slices) * p.blocks * (p.v_pieces * 128 / kJoinDims), kJoinThreads, 0, stream);
 }
 
 template <int N>
@@ -901,9 +962,13 @@ extern "C" int topk_paged_attention(const topk_attention_args* args, void* strea
   if (slices > kMaxParts) slices = kMaxParts;
   p.slices = static_cast<int32_t>(slices);
   bool joins = true;
-  if (p.row_tiles) {  // every unit has as many tiles: the host can see whether a slice begins inside one
-    joins = false;
-    for (int s = 1; s < p.slices; ++s) joins = joins || (units * p.row_tiles * s / p.slices) % p.row_tiles != 0;
+  if (p.row_tiles) {  // every unit has as many tiles
+    // Whole units, if the longest run then takes no longer than an equal share with what a split costs: the parts' way
+    // through memory and the join take about as long as kSplitTiles tiles.
+    const int64_t equal = (units * p.row_tiles + p.slices - 1) / p.slices, even = (units + p.slices - 1) / p.slices * p.row_tiles;
+    p.whole = even <= equal + kSplitTiles;
+    if (p.whole && p.slices > units) p.slices = static_cast<int32_t>(units);
+    joins = !p.whole;
   }
   char* w = static_cast<char*>(a.workspace) + TOPK_PAGED_WORKSPACE_BYTES;
   p.join = reinterpret_cast<Join*>(w);

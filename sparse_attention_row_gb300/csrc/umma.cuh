@@ -114,6 +114,17 @@ __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+// Whether `x` holds for any of the threads that meet at the barrier.
+__device__ __forceinline__ bool named_any(int id, int threads, bool x) {
+  uint32_t any;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %3, 0;\n barrier.cta.red.or.pred q, %1, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(any)
+      : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(x))
+      : "memory");
+  return any != 0;
+}
+
 // ---- tensor memory --------------------------------------------------------
 
 __device__ __forceinline__ void tmem_alloc(uint32_t where, uint32_t columns) {  // a whole warp
