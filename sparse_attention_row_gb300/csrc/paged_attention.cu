@@ -53,7 +53,6 @@ constexpr int kMaxQk = 576, kMaxV = 512;
 constexpr int kMaxBlockCols = 64;
 constexpr int kJoinThreads = 128, kJoinDims = 32;
 constexpr int kMaxParts = 256;  // slices of a launch at most
-constexpr int kSplitTiles = 4;
 constexpr float kMoveAbove = 8.f;  // in powers of two
 
 struct Join {  // what the join kernel has to know of the unit that ends in a slice and began before it
@@ -362,6 +361,19 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     const uint32_t full = smem_addr(&sm.full[0]), empty = smem_addr(&sm.empty[0]);
     Ring at;
     Copies copies(warp - kSoftmaxWarps, lane);
+    // Whether the next slot is empty is asked before a piece's copies are issued: the answer of a later question would
+    // wait behind them (185 cycles a piece in which nothing is copied).
+    bool empty_next = true;
+    const auto next_slot = [&]() {
+      if (!empty_next) mbar_wait(empty + at.slot * 8, at.phase ^ 1, guard);
+      Ring then = at;
+      then.step(p.slots);
+      empty_next = mbar_test(empty + then.slot * 8, then.phase ^ 1);
+    };
+    const auto done_slot = [&]() {
+      copies_arrive(full + at.slot * 8);
+      at.step(p.slots);
+    };
     uint32_t tile = 0, segment = 0;
     for (; walk.left > 0; walk.next(p), ++segment) {
       const int64_t row0 = walk.group * p.pack;
@@ -414,25 +426,26 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         if (seen && !kLatent)
           vp += 2 * (static_cast<int64_t>(at_block) * p.a.v_block_stride + place * p.a.v_token_stride + walk.kv_head * p.a.v_head_stride);
         const int next_block = table_entry(next_token), later_token = listed(t + 2);
-        copies.aim(kp, seen, lane);
-        for (int u = 0; u < k_ring; ++u) {
-          mbar_wait(empty + at.slot * 8, at.phase ^ 1, guard);
-          copies.piece(ring + at.slot * kPiece, u * 128, p.a.dk - u * 128, p.a.k);
-          copies_arrive(full + at.slot * 8);
-          at.step(p.slots);
-        }
-        if (kLatent && p.rest) {
+        const auto copy_rest = [&]() {
           mbar_wait(smem_addr(&sm.rest_empty), (tile & 1) ^ 1, guard);
           copies.piece(rest, k_ring * 128, p.a.dk - k_ring * 128, p.a.k);
           copies_arrive(smem_addr(&sm.rest_full));
+        };
+        copies.aim(kp, seen, lane);
+        // the rest first where it has a buffer of its own, free since this tile's predecessor was scored
+        if (kLatent && p.rest && !p.rest_is_p) copy_rest();
+        for (int u = 0; u < k_ring; ++u) {
+          next_slot();
+          copies.piece(ring + at.slot * kPiece, u * 128, p.a.dk - u * 128, p.a.k);
+          done_slot();
         }
+        if (kLatent && p.rest && p.rest_is_p) copy_rest();
         if (!kLatent) {
           copies.aim(vp, seen, lane);
           for (int u = 0; u < p.v_pieces; ++u) {
-            mbar_wait(empty + at.slot * 8, at.phase ^ 1, guard);
+            next_slot();
             copies.piece(ring + at.slot * kPiece, u * 128, p.a.dv - u * 128, p.a.v);
-            copies_arrive(full + at.slot * 8);
-            at.step(p.slots);
+            done_slot();
           }
         }
         // a latent tile's copies wait for the tile before it to leave the ring: until then, fetch its tokens into L2, the
@@ -459,44 +472,51 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     uint32_t scored = 0;                    // tiles whose scores have been taken
     // S^T of the next tile, into one of its two places
     const int whole_pieces = p.a.dk / 128;
+    const bool rest_first = kLatent && p.rest && !p.rest_is_p;
+    // the keys' last dims where they fill no piece
+    const auto last_scores = [&](uint32_t d, bool add) {
+      uint32_t at = rest, q_piece = q_at + whole_pieces * 2 * N * 128;
+      if (kLatent && p.rest) {
+        mbar_wait_warp(smem_addr(&sm.rest_full), scored & 1, guard);
+      } else {
+        at = ring + kr.slot * kPiece;
+        mbar_wait_warp(full + kr.slot * 8, kr.phase, guard);
+      }
+      fence_async();
+      int left = p.a.dk - whole_pieces * 128;
+      if (left >= 64) {
+        mma16_chunk(d, operand(at, 16), operand(q_piece, 16), kInstS, add);
+        add = true;
+        left -= 64;
+        at += kChunk;
+        q_piece += N * 128;
+      }
+#pragma unroll 1
+      for (; left > 0; left -= 16, at += 32, q_piece += 32, add = true) mma16_step(d, operand(at, 16), operand(q_piece, 16), kInstS, add);
+      if (kLatent && p.rest) {
+        if (!p.rest_is_p) commit(smem_addr(&sm.rest_empty));
+      } else {
+        if (!kLatent || whole_pieces >= p.v_pieces) commit(empty + kr.slot * 8);
+        kr.step(p.slots);
+      }
+    };
     const auto scores = [&]() {
       const uint32_t d = tmem + s_cols + (scored & 1) * N;
       uint32_t q_piece = q_at;
+      if (rest_first) last_scores(d, false);
+      bool ready = false;
 #pragma unroll 1
       for (int u = 0; u < whole_pieces; ++u, q_piece += 2 * N * 128) {
-        mbar_wait_warp(full + kr.slot * 8, kr.phase, guard);
+        if (!ready) mbar_wait(full + kr.slot * 8, kr.phase, guard);
+        __syncwarp();
         fence_async();
-        mma16_piece(d, operand(ring + kr.slot * kPiece, 16), operand(q_piece, 16), operand(q_piece + N * 128, 16), kInstS, u > 0);
-        if (!kLatent || u >= p.v_pieces) commit(empty + kr.slot * 8);  // keys that are no values are done with
+        const Ring here = kr;
         kr.step(p.slots);
+        ready = mbar_test(full + kr.slot * 8, kr.phase);  // the answer comes while the products are issued
+        mma16_piece(d, operand(ring + here.slot * kPiece, 16), operand(q_piece, 16), operand(q_piece + N * 128, 16), kInstS, rest_first || u > 0);
+        if (!kLatent || u >= p.v_pieces) commit(empty + here.slot * 8);  // keys that are no values are done with
       }
-      if (whole_pieces < p.k_pieces) {  // the last one is not whole
-        uint32_t at = rest;
-        if (kLatent && p.rest) {
-          mbar_wait_warp(smem_addr(&sm.rest_full), scored & 1, guard);
-        } else {
-          at = ring + kr.slot * kPiece;
-          mbar_wait_warp(full + kr.slot * 8, kr.phase, guard);
-        }
-        fence_async();
-        int left = p.a.dk - whole_pieces * 128;
-        bool add = whole_pieces > 0;
-        if (left >= 64) {
-          mma16_chunk(d, operand(at, 16), operand(q_piece, 16), kInstS, add);
-          add = true;
-          left -= 64;
-          at += kChunk;
-          q_piece += N * 128;
-        }
-#pragma unroll 1
-        for (; left > 0; left -= 16, at += 32, q_piece += 32, add = true) mma16_step(d, operand(at, 16), operand(q_piece, 16), kInstS, add);
-        if (kLatent && p.rest) {
-          if (!p.rest_is_p) commit(smem_addr(&sm.rest_empty));
-        } else {
-          if (!kLatent || whole_pieces >= p.v_pieces) commit(empty + kr.slot * 8);
-          kr.step(p.slots);
-        }
-      }
+      if (!rest_first && whole_pieces < p.k_pieces) last_scores(d, whole_pieces > 0);
       if (!kLatent) kr.step(p.slots, p.v_pieces);
       commit(smem_addr(&sm.s_full[scored & 1]));
       ++scored;
@@ -964,9 +984,10 @@ extern "C" int topk_paged_attention(const topk_attention_args* args, void* strea
   bool joins = true;
   if (p.row_tiles) {  // every unit has as many tiles
     // Whole units, if the longest run then takes no longer than an equal share with what a split costs: the parts' way
-    // through memory and the join take about as long as kSplitTiles tiles.
+    // through memory and the join take about as long as a tile for every 16 columns.
+    const int split_tiles = (p.block_cols + 15) / 16;
     const int64_t equal = (units * p.row_tiles + p.slices - 1) / p.slices, even = (units + p.slices - 1) / p.slices * p.row_tiles;
-    p.whole = even <= equal + kSplitTiles;
+    p.whole = even <= equal + split_tiles;
     if (p.whole && p.slices > units) p.slices = static_cast<int32_t>(units);
     joins = !p.whole;
   }
