@@ -53,6 +53,7 @@ constexpr int kMaxQk = 576, kMaxV = 512;
 constexpr int kMaxBlockCols = 64;
 constexpr int kJoinThreads = 128, kJoinDims = 32;
 constexpr int kMaxParts = 256;  // slices of a launch at most
+constexpr int kFetchAhead = 3;  // tiles
 constexpr float kMoveAbove = 8.f;  // in powers of two
 
 struct Join {  // what the join kernel has to know of the unit that ends in a slice and began before it
@@ -377,6 +378,42 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     uint32_t tile = 0, segment = 0;
     for (; walk.left > 0; walk.next(p), ++segment) {
       const int64_t row0 = walk.group * p.pack;
+      const int length = group_length(p, walk.group, false);
+      const int64_t request = length > 0 ? row_request(p.R, row0) : 0;
+      const int32_t* list = p.a.indices ? p.a.indices + row0 * p.a.index_row_stride : nullptr;
+      // A tile's tokens are found in two steps, each a tile earlier than its result is used: the position (from
+      // the list), then the block (from the table).
+      const auto listed = [&](int t) {
+        const int i = (walk.at + t) * kTile + me;
+        if (t >= walk.count) return -1;
+        return !list ? i : (i < p.a.num_indices ? list[i] : -1);
+      };
+      const auto column = [&](int x) { return p.R.block_shift >= 0 ? x >> p.R.block_shift : x / p.R.block_size; };
+      const auto table_entry = [&](int x) {
+        return x >= 0 && x < length ? __ldg(p.R.block_table + request * p.R.table_stride + column(x)) : 0;
+      };
+      const auto address = [&](const void* cache, int x, int x_block, int64_t block_stride, int64_t token_stride, int64_t head_stride) {
+        return static_cast<const char*>(cache) + 2 * (static_cast<int64_t>(x_block) * block_stride +
+                                                      (x - column(x) * p.R.block_size) * token_stride + walk.kv_head * head_stride);
+      };
+      const auto in_cache = [&](int x, int x_block) { return x >= 0 && x < length && x_block >= 0 && x_block < p.R.num_blocks; };
+      // A latent tile's copies wait for the tile before it to leave the ring. So its tokens are fetched into L2 some tiles
+      // ahead, the blocks of a unit a part of them each.
+      const auto fetch = [&](int x, int x_block) {
+        if (!in_cache(x, x_block)) return;
+        const char* from = address(p.a.k, x, x_block, p.a.k_block_stride, p.a.k_token_stride, p.a.k_head_stride);
+        for (int line = block; line * 64 < p.a.dk; line += p.blocks) asm volatile("prefetch.global.L2 [%0];" ::"l"(from + line * 128));
+      };
+      int at_token = listed(0), next_token = listed(1);
+      if (kLatent) {
+        int x[kFetchAhead - 1], b[kFetchAhead - 1];
+#pragma unroll
+        for (int i = 0; i < kFetchAhead - 1; ++i) x[i] = listed(i + 1);
+#pragma unroll
+        for (int i = 0; i < kFetchAhead - 1; ++i) b[i] = table_entry(x[i]);
+#pragma unroll
+        for (int i = 0; i < kFetchAhead - 1; ++i) fetch(x[i], b[i]);
+      }
       // the segment's queries, zeros past the block's columns and past dk
       mbar_wait(smem_addr(&sm.q_empty), (segment & 1) ^ 1, guard);
       for (int n = me >> 3; n < N; n += kCopyThreads / 8) {
@@ -392,39 +429,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         }
       }
       copies_arrive(smem_addr(&sm.q_full));
-      const int length = group_length(p, walk.group, false);
-      const int64_t request = length > 0 ? row_request(p.R, row0) : 0;
-      const int32_t* list = p.a.indices ? p.a.indices + row0 * p.a.index_row_stride : nullptr;
-      // A tile's tokens are found in two steps, each a tile earlier than its result is used: the position (from
-      // the list), then the block (from the table).
-      const auto listed = [&](int t) {
-        const int i = (walk.at + t) * kTile + me;
-        if (t >= walk.count) return -1;
-        return !list ? i : (i < p.a.num_indices ? list[i] : -1);
-      };
-      const auto column = [&](int x) { return p.R.block_shift >= 0 ? x >> p.R.block_shift : x / p.R.block_size; };
-      const auto table_entry = [&](int x) {
-        return x >= 0 && x < length ? __ldg(p.R.block_table + request * p.R.table_stride + column(x)) : 0;
-      };
-      int at_token = listed(0), at_block = table_entry(at_token), next_token = listed(1);
+      int at_block = table_entry(at_token);
       for (int t = 0; t < walk.count; ++t, ++tile) {
-        int pos = INT_MAX, place = 0;
-        if (at_token >= 0 && at_token < length) {
-          place = at_token - column(at_token) * p.R.block_size;
-          if (at_block >= 0 && at_block < p.R.num_blocks)
-            pos = at_token;
-          else
-            atomicOr(p.R.status, TOPK_DEV_BAD_BLOCK);
-        }
-        sm.token[tile % kTokenSlots][me] = pos;
+        const bool seen = in_cache(at_token, at_block);
+        if (!seen && at_token >= 0 && at_token < length) atomicOr(p.R.status, TOPK_DEV_BAD_BLOCK);
+        sm.token[tile % kTokenSlots][me] = seen ? at_token : INT_MAX;
         mbar_arrive(smem_addr(&sm.token_full[tile % kTokenSlots]));
-        const bool seen = pos != INT_MAX;
-        const char* kp = static_cast<const char*>(p.a.k);
-        if (seen)
-          kp += 2 * (static_cast<int64_t>(at_block) * p.a.k_block_stride + place * p.a.k_token_stride + walk.kv_head * p.a.k_head_stride);
-        const char* vp = static_cast<const char*>(p.a.v);
-        if (seen && !kLatent)
-          vp += 2 * (static_cast<int64_t>(at_block) * p.a.v_block_stride + place * p.a.v_token_stride + walk.kv_head * p.a.v_head_stride);
+        const char *kp = static_cast<const char*>(p.a.k), *vp = static_cast<const char*>(p.a.v);
+        if (seen) {
+          kp = address(kp, at_token, at_block, p.a.k_block_stride, p.a.k_token_stride, p.a.k_head_stride);
+          if (!kLatent) vp = address(vp, at_token, at_block, p.a.v_block_stride, p.a.v_token_stride, p.a.v_head_stride);
+        }
         const int next_block = table_entry(next_token), later_token = listed(t + 2);
         const auto copy_rest = [&]() {
           mbar_wait(smem_addr(&sm.rest_empty), (tile & 1) ^ 1, guard);
@@ -448,13 +463,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             done_slot();
           }
         }
-        // a latent tile's copies wait for the tile before it to leave the ring: until then, fetch its tokens into L2, the
-        // blocks of a unit a part of them each
-        if (kLatent && next_token >= 0 && next_token < length && next_block >= 0 && next_block < p.R.num_blocks) {
-          const char* next = static_cast<const char*>(p.a.k) +
-                             2 * (static_cast<int64_t>(next_block) * p.a.k_block_stride +
-                                  (next_token - column(next_token) * p.R.block_size) * p.a.k_token_stride + walk.kv_head * p.a.k_head_stride);
-          for (int line = block; line * 64 < p.a.dk; line += p.blocks) asm volatile("prefetch.global.L2 [%0];" ::"l"(next + line * 128));
+        if (kLatent) {
+          const int x = listed(t + kFetchAhead);
+          fetch(x, table_entry(x));
         }
         at_token = next_token;
         at_block = next_block;
@@ -563,6 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   } else {
     // ---- softmax and output ------------------------------------------------
     constexpr int H = N / 2;
+    constexpr float kMostProbability = kBf16 ? 256.f : 32768.f;  // 2^(kMoveAbove + kShift)
     constexpr float kShift = kBf16 ? 0.f : 7.f;  // fp16: probabilities use the upper half of its range, at most 2^15
     const int half = warp >> 2, quarter = warp & 3, token = quarter * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
@@ -602,25 +614,40 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         float s[H];
         tmem_load(tmem + lanes + s_cols + (tile & 1) * N + half * H, s);
         load_wait(s);
-        if (pos >= least) {
+        const auto mask = [&]() {
+          if (pos >= least) {
 #pragma unroll
-          for (int i = 0; i < H; ++i)
-            if (pos >= sm.limit[segment & 1][half][i]) s[i] = -INFINITY;
-        }
-        // does any score exceed the maximum in use by so much that it has to move?
-        bool move_any = t == 0;
-        if (t > 0) {
-          float x = -INFINITY;
+            for (int i = 0; i < H; ++i)
+              if (pos >= sm.limit[segment & 1][half][i]) s[i] = -INFINITY;
+          }
+        };
+        const auto probabilities = [&]() {
 #pragma unroll
           for (int i = 0; i < H; i += 4) {
             const float4 u = *reinterpret_cast<const float4*>(&sm.moved[warp][0][i]);
-            x = fmaxf(x, fmaxf(fmaf(s[i], p.scale2, -u.x), fmaf(s[i + 1], p.scale2, -u.y)));
-            x = fmaxf(x, fmaxf(fmaf(s[i + 2], p.scale2, -u.z), fmaf(s[i + 3], p.scale2, -u.w)));
+            s[i] = exp2_fast(fmaf(s[i], p.scale2, -u.x));
+            s[i + 1] = exp2_fast(fmaf(s[i + 1], p.scale2, -u.y));
+            s[i + 2] = exp2_fast(fmaf(s[i + 2], p.scale2, -u.z));
+            s[i + 3] = exp2_fast(fmaf(s[i + 3], p.scale2, -u.w));
           }
-          move_any = named_any(1 + half, 128, x > kMoveAbove + kShift);
+        };
+        mask();
+        // With the maxima in use: is any of the probabilities so large that its column's has to move?
+        bool move_any = t == 0;
+        if (t > 0) {
+          probabilities();
+          float x = 0.f;
+#pragma unroll
+          for (int i = 0; i < H; i += 2) x = fmaxf(x, fmaxf(s[i], s[i + 1]));
+          move_any = named_any(1 + half, 128, x > kMostProbability);
         }
         bool rescale = false;
         if (move_any) {
+          if (t > 0) {
+            tmem_load(tmem + lanes + s_cols + (tile & 1) * N + half * H, s);
+            load_wait(s);
+            mask();
+          }
           const float warp_max = reduce_columns<H, true>(s, lane);
           if (lane < H) sm.column_max[half][quarter][lane] = warp_max;
           named_sync(1 + half, 128);
@@ -640,15 +667,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             sm.moved[warp][1][lane] = factor;
           }
           __syncwarp();
+          probabilities();
         }
-#pragma unroll
-        for (int i = 0; i < H; i += 4) {
-          const float4 u = *reinterpret_cast<const float4*>(&sm.moved[warp][0][i]);
-          s[i] = exp2_fast(fmaf(s[i], p.scale2, -u.x));
-          s[i + 1] = exp2_fast(fmaf(s[i + 1], p.scale2, -u.y));
-          s[i + 2] = exp2_fast(fmaf(s[i + 2], p.scale2, -u.z));
-          s[i + 3] = exp2_fast(fmaf(s[i + 3], p.scale2, -u.w));
-        }
+        // the last tile's product has read P and written O
         if (tile > 0) mbar_wait(smem_addr(&sm.o_done), (tile - 1) & 1, guard);
         fence_after();
         if (rescale) {  // the same for all warps of this half: they hold the same maxima
