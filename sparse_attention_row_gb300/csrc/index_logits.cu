@@ -418,16 +418,15 @@ __global__ void __launch_bounds__(kThreads, 1) index_logits_kernel(const __grid_
 }
 
 template <bool k8Bit>
-int run(Params& p, int smem_limit, cudaStream_t stream) {
+int run(Params& p, int device, int smem_limit, cudaStream_t stream) {
   const int extra = static_cast<int>(sizeof(Smem)) + 1024;
   const int slot = p.chunks * kChunk, room = smem_limit - extra - static_cast<int>(p.q_bytes);
   p.slots = room / slot < kMaxSlots ? room / slot : kMaxSlots;
   if (p.slots < 1) return TOPK_ERR_PLAN;
   const size_t smem = p.q_bytes + static_cast<size_t>(p.slots) * slot + extra;
-  if (cudaFuncSetAttribute(index_logits_kernel<k8Bit>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) {
-    cudaGetLastError();
-    return TOPK_ERR_CUDA;
-  }
+  static int granted[kMaxDevices];
+  const int rc = allow_smem(index_logits_kernel<k8Bit>, smem_limit, device, granted);
+  if (rc != TOPK_OK) return rc;
   return launch(index_logits_kernel<k8Bit>, static_cast<const Params&>(p), p.slices, kThreads, smem, stream);
 }
 
@@ -483,5 +482,5 @@ extern "C" int topk_index_logits(const topk_index_logits_args* args, void* strea
   p.slices = static_cast<int32_t>(most < props.num_sms ? most : props.num_sms);
   p.inst = ltk::umma::instruction(a.dtype == TOPK_DTYPE_BF16 ? ltk::umma::kBF16 : ltk::umma::kF16, 0, false);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return size == 1 ? run<true>(p, props.max_smem_optin, s) : run<false>(p, props.max_smem_optin, s);
+  return size == 1 ? run<true>(p, dev, props.max_smem_optin, s) : run<false>(p, dev, props.max_smem_optin, s);
 }

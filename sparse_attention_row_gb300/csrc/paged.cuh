@@ -127,6 +127,20 @@ inline int launch(void (*kernel)(Args), const Args& args, int64_t grid, int thre
   return TOPK_OK;
 }
 
+// Lets a kernel use `smem` bytes of shared memory. Asked of the runtime once for each kernel and device: `granted` (one
+// for each kernel, its own static array) holds what was granted.
+constexpr int kMaxDevices = 64;
+template <typename Kernel>
+inline int allow_smem(Kernel* kernel, size_t smem, int device, int* granted) {
+  if (device >= 0 && device < kMaxDevices && __atomic_load_n(&granted[device], __ATOMIC_ACQUIRE) >= static_cast<int>(smem)) return TOPK_OK;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) {
+    cudaGetLastError();
+    return TOPK_ERR_CUDA;
+  }
+  if (device >= 0 && device < kMaxDevices) __atomic_store_n(&granted[device], static_cast<int>(smem), __ATOMIC_RELEASE);
+  return TOPK_OK;
+}
+
 // SMs of the current device (cached); 0 if it cannot be queried.
 int num_sms();
 

@@ -905,7 +905,7 @@ size_t workspace_for(int sms) {
 static_assert(sizeof(Smem<64>) + 1024 + 9 * 64 * 128 + 4 * kPiece + kChunk <= 232448, "latent attention of 64 columns: four pieces of the ring");
 
 template <int N, bool kBf16, bool kLatent>
-int run(Params& p, int smem_limit, bool joins, cudaStream_t stream) {
+int run(Params& p, int device, int smem_limit, bool joins, cudaStream_t stream) {
   const int extra = static_cast<int>(sizeof(Smem<N>)) + 1024;
   p.q_bytes = p.k_chunks * N * 128;
   p.rest_is_p = 0;
@@ -922,20 +922,19 @@ int run(Params& p, int smem_limit, bool joins, cudaStream_t stream) {
   p.tmem_cols = 32;
   while (p.tmem_cols < static_cast<uint32_t>((p.v_pieces + 2) * N)) p.tmem_cols *= 2;
   const size_t smem = p.q_bytes + static_cast<size_t>(p.slots) * kPiece + (p.rest && !p.rest_is_p ? kChunk : 0) + kChunk + extra;
-  if (cudaFuncSetAttribute(attention_kernel<N, kBf16, kLatent>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) {
-    cudaGetLastError();
-    return TOPK_ERR_CUDA;
-  }
-  int rc = launch(attention_kernel<N, kBf16, kLatent>, static_cast<const Params&>(p), static_cast<int64_t>(p.slices) * p.blocks, kThreads, smem, stream);
+  static int granted[kMaxDevices];
+  int rc = allow_smem(attention_kernel<N, kBf16, kLatent>, smem_limit, device, granted);
+  if (rc != TOPK_OK) return rc;
+  rc = launch(attention_kernel<N, kBf16, kLatent>, static_cast<const Params&>(p), static_cast<int64_t>(p.slices) * p.blocks, kThreads, smem, stream);
   if (rc != TOPK_OK || !joins) return rc;
   return launch(join_kernel<N, kBf16>, static_cast<const Params&>(p), static_cast<int64_t>(p.slices) * p.blocks * (p.v_pieces * 128 / kJoinDims), kJoinThreads, 0, stream);
 }
 
 template <int N>
-int run_columns(Params& p, int smem_limit, bool joins, cudaStream_t stream) {
+int run_columns(Params& p, int device, int smem_limit, bool joins, cudaStream_t stream) {
   const bool bf16 = p.a.dtype == TOPK_DTYPE_BF16;
-  if (p.latent) return bf16 ? run<N, true, true>(p, smem_limit, joins, stream) : run<N, false, true>(p, smem_limit, joins, stream);
-  return bf16 ? run<N, true, false>(p, smem_limit, joins, stream) : run<N, false, false>(p, smem_limit, joins, stream);
+  if (p.latent) return bf16 ? run<N, true, true>(p, device, smem_limit, joins, stream) : run<N, false, true>(p, device, smem_limit, joins, stream);
+  return bf16 ? run<N, true, false>(p, device, smem_limit, joins, stream) : run<N, false, false>(p, device, smem_limit, joins, stream);
 }
 
 }  // namespace
@@ -1019,7 +1018,7 @@ extern "C" int topk_paged_attention(const topk_attention_args* args, void* strea
   w += static_cast<size_t>(most_ctas(sms)) * 2 * kMaxBlockCols * sizeof(float2);
   p.part = reinterpret_cast<float*>(w);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (p.block_cols <= 16) return run_columns<16>(p, props.max_smem_optin, joins, s);
-  if (p.block_cols <= 32) return run_columns<32>(p, props.max_smem_optin, joins, s);
-  return run_columns<64>(p, props.max_smem_optin, joins, s);
+  if (p.block_cols <= 16) return run_columns<16>(p, dev, props.max_smem_optin, joins, s);
+  if (p.block_cols <= 32) return run_columns<32>(p, dev, props.max_smem_optin, joins, s);
+  return run_columns<64>(p, dev, props.max_smem_optin, joins, s);
 }

@@ -2,7 +2,9 @@
 indexer's logits, and attention over the cache.
 
 Argument marshalling only, like the rest of the binding: shapes, strides and
-types are read from the tensors, checked, and handed to ``libtopk.so``.
+types are read from the tensors, checked, and handed to ``libtopk.so``. A decode
+step makes these calls back to back, so the checks are plain comparisons and the
+arguments are packed in one go: a call is enqueued in some 10 us of host time.
 """
 from __future__ import annotations
 
@@ -27,11 +29,6 @@ class KvMap(NamedTuple):
     token_start: "torch.Tensor"  # int32 [requests + 1]  # noqa: F821
 
 
-def _need(ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
-
-
 class PagedDecoder:
     """The paged calls on one device, with their workspace.
 
@@ -46,13 +43,18 @@ class PagedDecoder:
         self._torch = torch
         self.device = device
         self._dev = torch.device("cuda", device)
-        self._lib = _sar._load()
+        lib = _sar._load()
+        self._kv_map, self._index_logits, self._attention = lib.topk_kv_map, lib.topk_index_logits, lib.topk_paged_attention
+        self._f32, self._i32, self._i64 = torch.float32, torch.int32, torch.int64
         self._dtypes = {torch.float16: 1, torch.bfloat16: 2, torch.float8_e4m3fn: 3}
+        self._empty_tensor = torch.empty
+        self._get_device, self._get_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
         self.nbytes = _sar.topk_attention_workspace_size(device)
         if self.nbytes == 0:
             raise _sar.TopkError(_sar.TOPK_ERR_CUDA, "topk_attention_workspace_size")
         with torch.cuda.device(device):
             self.workspace = torch.empty(self.nbytes, dtype=torch.uint8, device=self._dev)
+            self._workspace_ptr = self.workspace.data_ptr()
             self.reset()
 
     def reset(self, stream=None) -> None:
@@ -68,81 +70,95 @@ class PagedDecoder:
             raise _sar.TopkError(rc, "topk_get_status")
         return word
 
-    def _on(self, t, what: str, dtype, dims: int):
-        _need(t.dtype == dtype and t.dim() == dims, f"{what} must be a {dims}-dimensional {dtype} tensor")
-        _need(t.device == self._dev, f"{what} must be on {self._dev}")
+    # Checks: each returns the tensor's address, or raises.
+
+    def _bad(self, what: str, t, need: str):
+        raise ValueError(f"{what} must be {need} on {self._dev}; got {tuple(t.shape)} {t.dtype}, strides {tuple(t.stride())}, on {t.device}")
+
+    def _ints(self, what: str, t, n: int):
+        """int32 [n], contiguous."""
+        if t.dtype is not self._i32 or t.dim() != 1 or t.numel() != n or t.get_device() != self.device or not t.is_contiguous():
+            self._bad(what, t, f"a contiguous int32 tensor with {n} entries")
         return t.data_ptr()
 
-    def _ints(self, t, what: str, n=None):
-        p = self._on(t, what, self._torch.int32, 1)
-        _need(t.is_contiguous() and (n is None or t.numel() == n), f"{what} must be contiguous" + ("" if n is None else f" with {n} entries"))
-        return p
+    def _matrix(self, what: str, t, dtype, rows: int):
+        """[rows, any], rows contiguous."""
+        if t.dtype is not dtype or t.dim() != 2 or t.shape[0] != rows or t.get_device() != self.device or (t.stride(1) != 1 and t.shape[1] != 1):
+            self._bad(what, t, f"a {dtype} tensor of {rows} contiguous rows")
+        return t.data_ptr()
+
+    def _vectors(self, what: str, t, dtype, dims: int):
+        """`dims` dimensions, the last one contiguous."""
+        if t.dtype is not dtype or t.dim() != dims or t.get_device() != self.device or (t.stride(-1) != 1 and t.shape[-1] != 1):
+            self._bad(what, t, f"a {dims}-dimensional {dtype} tensor with a contiguous last dimension")
+        return t.data_ptr()
 
     def _empty(self, shape, dtype, stream):
-        torch = self._torch
         if stream is None:
-            return torch.empty(shape, dtype=dtype, device=self._dev)
+            return self._empty_tensor(shape, dtype=dtype, device=self._dev)
+        torch = self._torch
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=self._dev)
         with torch.cuda.stream(stream):
             return torch.empty(shape, dtype=dtype, device=self._dev)
 
-    def _call(self, name: str, args: bytes, stream) -> None:
-        torch = self._torch
+    def _call(self, function, args: bytes, stream) -> None:
         if stream is None:
-            stream = torch.cuda.current_stream(self._dev)
-        if not isinstance(stream, int):
+            stream = self._get_stream(self.device)
+        elif not isinstance(stream, int):
             stream = stream.cuda_stream
-        if torch.cuda.current_device() == self.device:
-            rc = getattr(self._lib, name)(args, stream)
+        if self._get_device() == self.device:
+            rc = function(args, stream)
         else:
-            with torch.cuda.device(self.device):
-                rc = getattr(self._lib, name)(args, stream)
-        if rc != _sar.TOPK_OK:
-            raise _sar.TopkError(rc, name)
+            with self._torch.cuda.device(self.device):
+                rc = function(args, stream)
+        if rc != 0:
+            raise _sar.TopkError(rc, function.__name__)
 
     def kv_map(self, context_lens, new_lens, block_table, free_blocks, taken, block_size: int, max_tokens: int,
                taken_out=None, out: KvMap | None = None, stream=None) -> KvMap:
         """Gives the requests' new tokens their places: enters the blocks taken from ``free_blocks`` in
         ``block_table`` (int32 [requests, columns], in place), advances ``taken`` (int32 [1]; into
         ``taken_out`` if that is given) and lists slot, length and request of every new token."""
-        torch = self._torch
         n = context_lens.numel()
-        context, new = self._ints(context_lens, "context_lens"), self._ints(new_lens, "new_lens", n)
-        table = self._on(block_table, "block_table", torch.int32, 2)
-        _need(block_table.shape[0] == n and block_table.stride(1) == 1, "block_table must hold one contiguous row per request")
+        context, new = self._ints("context_lens", context_lens, n), self._ints("new_lens", new_lens, n)
+        table = self._matrix("block_table", block_table, self._i32, n)
+        columns = block_table.shape[1]
+        free = free_blocks.numel()
         if out is None:
-            out = KvMap(self._empty(max_tokens, torch.int64, stream), self._empty(max_tokens, torch.int32, stream),
-                        self._empty(max_tokens, torch.int32, stream), self._empty(n + 1, torch.int32, stream))
-        slots = self._on(out.slots, "out.slots", torch.int64, 1)
-        _need(out.slots.is_contiguous() and out.slots.numel() == max_tokens, "out.slots must be contiguous with max_tokens entries")
-        taken_ptr = self._ints(taken, "taken", 1)
-        self._call("topk_kv_map", _MAP.pack(
-            context, new, n, block_size, table, block_table.stride(0) if n > 1 else max(block_table.stride(0), block_table.shape[1]), block_table.shape[1],
-            self._ints(free_blocks, "free_blocks"), free_blocks.numel(), taken_ptr,
-            taken_ptr if taken_out is None else self._ints(taken_out, "taken_out", 1), slots,
-            self._ints(out.row_lens, "out.row_lens", max_tokens), self._ints(out.row_request, "out.row_request", max_tokens),
-            self._ints(out.token_start, "out.token_start", n + 1), max_tokens, self.workspace.data_ptr()), stream)
+            # one allocation: the int64 slots first, then the int32 lists
+            words = self._empty(2 * max_tokens + max_tokens + max_tokens + n + 1, self._i32, stream)
+            slots, lens, request, start = words.split_with_sizes((2 * max_tokens, max_tokens, max_tokens, n + 1))
+            out = KvMap(slots.view(self._i64), lens, request, start)
+            slots_ptr = words.data_ptr()
+            lens_ptr = slots_ptr + 8 * max_tokens
+            request_ptr = lens_ptr + 4 * max_tokens
+            start_ptr = request_ptr + 4 * max_tokens
+        else:
+            slots = out.slots
+            if slots.dtype is not self._i64 or slots.dim() != 1 or slots.numel() != max_tokens or slots.get_device() != self.device or not slots.is_contiguous():
+                self._bad("out.slots", slots, f"a contiguous int64 tensor with {max_tokens} entries")
+            slots_ptr = slots.data_ptr()
+            lens_ptr, request_ptr = self._ints("out.row_lens", out.row_lens, max_tokens), self._ints("out.row_request", out.row_request, max_tokens)
+            start_ptr = self._ints("out.token_start", out.token_start, n + 1)
+        taken_ptr = self._ints("taken", taken, 1)
+        stride = block_table.stride(0)
+        self._call(self._kv_map, _MAP.pack(
+            context, new, n, block_size, table, stride if n > 1 or stride >= columns else columns, columns, self._ints("free_blocks", free_blocks, free), free, taken_ptr,
+            taken_ptr if taken_out is None else self._ints("taken_out", taken_out, 1), slots_ptr, lens_ptr, request_ptr, start_ptr, max_tokens,
+            self._workspace_ptr), stream)
         return out
 
     def _rows(self, rows: int, lengths, block_table, num_blocks: int, block_size: int, next_n, row_request):
-        torch = self._torch
-        _need(lengths.dtype == torch.int32 and lengths.dim() in (1, 2) and lengths.is_contiguous() and lengths.device == self._dev,
-              f"lengths must be a contiguous int32 tensor with 1 or 2 dimensions on {self._dev}")
-        _need(lengths.numel() == rows, "lengths must hold one length per row")
+        if lengths.dtype is not self._i32 or lengths.numel() != rows or lengths.dim() not in (1, 2) or lengths.get_device() != self.device or not lengths.is_contiguous():
+            self._bad("lengths", lengths, f"a contiguous int32 tensor with 1 or 2 dimensions and {rows} entries")
         if next_n is None:
             next_n = lengths.shape[1] if lengths.dim() == 2 else 1
-        table = self._on(block_table, "block_table", torch.int32, 2)
         requests, columns = block_table.shape
-        _need(block_table.stride(1) == 1 or columns == 1, "block_table's rows must be contiguous")
+        stride = block_table.stride(0)
         return (rows, next_n, block_size, requests, num_blocks, lengths.data_ptr(),
-                None if row_request is None else self._ints(row_request, "row_request", rows), table,
-                max(block_table.stride(0), columns) if requests < 2 else block_table.stride(0), columns)
-
-    def _vectors(self, t, what: str, dtype, dims: int):
-        p = self._on(t, what, dtype, dims)
-        _need(t.stride(-1) == 1 or t.shape[-1] == 1, f"{what}'s last dimension must be contiguous")
-        return p
+                0 if row_request is None else self._ints("row_request", row_request, rows), self._matrix("block_table", block_table, self._i32, requests),
+                stride if requests > 1 or stride >= columns else columns, columns)
 
     def index_logits(self, q, weights, keys, block_table, lengths, key_scales=None, next_n: int | None = None,
                      row_request=None, max_len: int | None = None, out=None, stream=None):
@@ -150,27 +166,34 @@ class PagedDecoder:
         keys [blocks, block_size, dim] (fp16, bf16 or fp8 e4m3, as q), key_scales fp32 [blocks, block_size].
         Writes logits fp32 [rows, max_len] up to each row's length and leaves the rest of ``out`` as it is
         (what a new tensor holds there is undefined; the selection never uses it)."""
-        torch = self._torch
         rows, heads, dim = q.shape
-        _need(q.dtype in self._dtypes, f"q has an unsupported type {q.dtype}")
-        qp, kp = self._vectors(q, "q", q.dtype, 3), self._vectors(keys, "keys", q.dtype, 3)
-        wp = self._on(weights, "weights", torch.float32, 2)
-        _need(weights.shape == (rows, heads) and (weights.stride(1) == 1 or heads == 1), "weights must be [rows, heads] with contiguous rows")
-        _need(keys.shape[2] == dim, "q and keys must have the same last dimension")
-        sp, s0, s1 = None, 0, 0
+        dtype = q.dtype
+        kind = self._dtypes.get(dtype)
+        if kind is None:
+            raise ValueError(f"q has an unsupported type {dtype}")
+        qp, kp = self._vectors("q", q, dtype, 3), self._vectors("keys", keys, dtype, 3)
+        wp = self._matrix("weights", weights, self._f32, rows)
+        blocks, block_size, key_dim = keys.shape
+        if weights.shape[1] != heads or key_dim != dim:
+            raise ValueError("weights must have q's heads and keys its last dimension")
+        sp, s0, s1 = 0, 0, 0
         if key_scales is not None:
-            sp = self._on(key_scales, "key_scales", torch.float32, 2)
-            _need(key_scales.shape == keys.shape[:2], "key_scales must be [blocks, block_size]")
+            if key_scales.dtype is not self._f32 or key_scales.shape != keys.shape[:2] or key_scales.get_device() != self.device:
+                self._bad("key_scales", key_scales, "a float32 [blocks, block_size] tensor")
+            sp = key_scales.data_ptr()
             s0, s1 = key_scales.stride()
-        rows_args = self._rows(rows, lengths, block_table, keys.shape[0], keys.shape[1], next_n, row_request)
+        rows_args = self._rows(rows, lengths, block_table, blocks, block_size, next_n, row_request)
         if out is None:
-            out = self._empty((rows, block_table.shape[1] * keys.shape[1] if max_len is None else max_len), torch.float32, stream)
-        op = self._on(out, "out", torch.float32, 2)
-        _need(out.shape[0] == rows and (out.stride(1) == 1 or out.shape[1] == 1), "out must hold one contiguous row per row of q")
-        _need(max_len is None or max_len <= out.shape[1], "max_len must not exceed out's columns")
-        self._call("topk_index_logits", _LOGITS.pack(
-            *(x or 0 for x in rows_args), self._dtypes[q.dtype], heads, dim, qp, q.stride(0), q.stride(1), wp, weights.stride(0), kp, keys.stride(0), keys.stride(1),
-            sp or 0, s0, s1, op, out.stride(0), out.shape[1] if max_len is None else max_len, self.workspace.data_ptr()), stream)
+            out = self._empty((rows, block_table.shape[1] * block_size if max_len is None else max_len), self._f32, stream)
+        op = self._matrix("out", out, self._f32, rows)
+        width = out.shape[1]
+        if max_len is not None:
+            if max_len > width:
+                raise ValueError("max_len must not exceed out's columns")
+            width = max_len
+        self._call(self._index_logits, _LOGITS.pack(
+            *rows_args, kind, heads, dim, qp, q.stride(0), q.stride(1), wp, weights.stride(0), kp, keys.stride(0), keys.stride(1),
+            sp, s0, s1, op, out.stride(0), width, self._workspace_ptr), stream)
         return out
 
     def attention(self, q, k_cache, block_table, lengths, v_cache=None, v_dim: int | None = None, indices=None,
@@ -180,40 +203,51 @@ class PagedDecoder:
         the heads' dimension), over every token below each row's length or over ``indices``
         (int32 [rows, n], as the selection writes them). ``v_cache`` None: a token's value is the first
         ``v_dim`` elements of its key (latent attention). Returns out, or (out, lse)."""
-        torch = self._torch
+        rows, heads, dk = q.shape
+        dtype = q.dtype
+        kind = self._dtypes.get(dtype)
+        if kind is None:
+            raise ValueError(f"q has an unsupported type {dtype}")
         if k_cache.dim() == 3:
             k_cache = k_cache.unsqueeze(2)
-        if v_cache is not None and v_cache.dim() == 3:
-            v_cache = v_cache.unsqueeze(2)
-        rows, heads, dk = q.shape
-        _need(q.dtype in self._dtypes, f"q has an unsupported type {q.dtype}")
-        qp, kp = self._vectors(q, "q", q.dtype, 3), self._vectors(k_cache, "k_cache", q.dtype, 4)
-        blocks, block_size, kv_heads, _ = k_cache.shape
-        _need(k_cache.shape[3] == dk, "q and k_cache must have the same last dimension")
-        vp, vs = 0, (0, 0, 0, 0)
+        qp, kp = self._vectors("q", q, dtype, 3), self._vectors("k_cache", k_cache, dtype, 4)
+        blocks, block_size, kv_heads, key_dim = k_cache.shape
+        if key_dim != dk:
+            raise ValueError("q and k_cache must have the same last dimension")
+        k0, k1, k2, _ = k_cache.stride()
+        vp = v0 = v1 = v2 = 0
         if v_cache is not None:
-            vp, vs = self._vectors(v_cache, "v_cache", q.dtype, 4), v_cache.stride()
-            _need(v_cache.shape[:3] == k_cache.shape[:3] and v_dim in (None, v_cache.shape[3]), "v_cache must have k_cache's blocks and heads, and v_dim values")
+            if v_cache.dim() == 3:
+                v_cache = v_cache.unsqueeze(2)
+            vp = self._vectors("v_cache", v_cache, dtype, 4)
+            v0, v1, v2, _ = v_cache.stride()
+            if v_cache.shape[:3] != k_cache.shape[:3] or (v_dim is not None and v_dim != v_cache.shape[3]):
+                raise ValueError("v_cache must have k_cache's blocks and heads, and v_dim values")
             v_dim = v_cache.shape[3]
-        _need(v_dim is not None, "v_dim must be given where there is no v_cache")
-        ip, i0, topk = 0, 0, 0
+        elif v_dim is None:
+            raise ValueError("v_dim must be given where there is no v_cache")
+        ip = i0 = topk = 0
         if indices is not None:
-            ip = self._on(indices, "indices", torch.int32, 2)
-            _need(indices.shape[0] == rows and (indices.stride(1) == 1 or indices.shape[1] == 1), "indices must hold one contiguous row per row of q")
+            ip = self._matrix("indices", indices, self._i32, rows)
             i0, topk = indices.stride(0), indices.shape[1]
         rows_args = self._rows(rows, lengths, block_table, blocks, block_size, next_n, row_request)
         if out is None:
-            out = self._empty((rows, heads, v_dim), q.dtype, stream)
-        op = self._vectors(out, "out", q.dtype, 3)
-        _need(out.shape == (rows, heads, v_dim), "out must be [rows, heads, v_dim]")
-        if lse is None and return_lse:
-            lse = self._empty((rows, heads), torch.float32, stream)
+            out = self._empty((rows, heads, v_dim), dtype, stream)
+            op, o0, o1 = out.data_ptr(), heads * v_dim, v_dim
+        else:
+            op = self._vectors("out", out, dtype, 3)
+            if out.shape != (rows, heads, v_dim):
+                self._bad("out", out, f"a {(rows, heads, v_dim)} tensor")
+            o0, o1, _ = out.stride()
         lp = 0
         if lse is not None:
-            lp = self._on(lse, "lse", torch.float32, 2)
-            _need(lse.shape == (rows, heads) and lse.is_contiguous(), "lse must be a contiguous [rows, heads] tensor")
-        ks = k_cache.stride()
-        self._call("topk_paged_attention", _ATTENTION.pack(
-            *(x or 0 for x in rows_args), self._dtypes[q.dtype], heads, kv_heads, dk, v_dim, dk ** -0.5 if scale is None else scale, qp, q.stride(0), q.stride(1),
-            kp, ks[0], ks[1], ks[2], vp, vs[0], vs[1], vs[2], ip, i0, topk, op, out.stride(0), out.stride(1), lp, self.workspace.data_ptr(), self.nbytes), stream)
+            lp = self._matrix("lse", lse, self._f32, rows)
+            if lse.shape[1] != heads or not lse.is_contiguous():
+                self._bad("lse", lse, f"a contiguous {(rows, heads)} tensor")
+        elif return_lse:
+            lse = self._empty((rows, heads), self._f32, stream)
+            lp = lse.data_ptr()
+        self._call(self._attention, _ATTENTION.pack(
+            *rows_args, kind, heads, kv_heads, dk, v_dim, dk ** -0.5 if scale is None else scale, qp, q.stride(0), q.stride(1),
+            kp, k0, k1, k2, vp, v0, v1, v2, ip, i0, topk, op, o0, o1, lp, self._workspace_ptr, self.nbytes), stream)
         return (out, lse) if return_lse else out
