@@ -37,8 +37,9 @@ constexpr int kSumWarps = 16, kCopyWarps = 4;
 constexpr int kCopyThreads = kCopyWarps * 32;
 constexpr int kMmaWarp = kSumWarps + kCopyWarps;
 constexpr int kThreads = (kMmaWarp + 1) * 32;
-constexpr int kMaxSlots = 5;
-constexpr int kTokenSlots = 8;   // more than the steps that the copies can be ahead of the sums: ring slots + 2
+constexpr int kMaxSlots = 8;
+constexpr int kTokenSlots = 16;  // more than the steps that the copies can be ahead of the sums: ring slots + 2
+constexpr int kGroup = 4;        // steps whose blocks are looked up together
 constexpr int kSegmentSlots = 4;  // a segment's weights are written when at most two segments are still being summed
 constexpr int kMaxCols = 256, kMaxRows = 16;
 
@@ -157,58 +158,85 @@ struct Walk {
   }
 };
 
+// Where a pass's tokens lie: looked up by the copying warps, and by the summing ones for the scales.
+__device__ __forceinline__ int block_column(const Rows& R, int x) { return R.block_shift >= 0 ? x >> R.block_shift : x / R.block_size; }
+__device__ __forceinline__ int table_entry(const Params& p, const Walk& w, int x) {
+  return x < w.longest ? __ldg(p.R.block_table + w.request * p.R.table_stride + block_column(p.R, x)) : 0;
+}
+__device__ __forceinline__ bool in_cache(const Params& p, const Walk& w, int x, int b) {
+  return x < w.longest && b >= 0 && b < p.R.num_blocks;
+}
+
 __device__ __forceinline__ float relu(float x) {
   float y;
   asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
   return y;
 }
 
+// s += w * relu(x) for two columns at once.
+__device__ __forceinline__ void add_two(uint64_t* s, float w0, float w1, float x0, float x1) {
+  asm("{\n .reg .b64 w, x;\n mov.b64 w, {%1, %2};\n mov.b64 x, {%3, %4};\n fma.rn.f32x2 %0, w, x, %0;\n}"
+      : "+l"(*s)
+      : "f"(w0), "f"(w1), "f"(relu(x0)), "f"(relu(x1)));
+}
+__device__ __forceinline__ float sum_of_two(uint64_t s) {
+  float a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(s));
+  return a + b;
+}
+
 // The weighted sums of rows [row, row_end) of one tile for this thread's token, 16 columns at a time, the next ones on
-// their way meanwhile. `at`: the first row's columns.
+// their way meanwhile. `at`: the first row's columns. kWide: heads are a multiple of 32, so that no chunk of 32 columns is
+// part of two rows or has columns without a head.
+template <bool kWide>
 __device__ __forceinline__ void sum_tile(const Params& p, uint32_t at, const float* weight, const int32_t* length, int row, int row_end,
                                          int pos, float scale, bool found, int64_t row0) {
   constexpr int C = 16;
   if (row >= row_end) return;
   float v[2][C];
-  const int cols = (row_end - row) * p.head_cols;
+  const uint32_t end = at + (row_end - row) * p.head_cols;
   weight += row * p.head_cols;
+  float* out = p.a.logits + (row0 + row) * p.a.logits_row_stride + pos;
   tmem_load(at, v[0]);
   int in_row = 0;
-  float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-  const auto take = [&](float (&x)[C], int c) {
-    // columns past the heads hold zeros times a key: not numbers where the key is none
-    const int real = p.a.heads - in_row;
-    if (real >= C) {
+  uint64_t s0 = 0, s1 = 0;
+  const auto take = [&](float (&x)[C]) {
+    if (kWide || p.a.heads - in_row >= C) {
 #pragma unroll
       for (int i = 0; i < C; i += 4) {
-        const float4 w = *reinterpret_cast<const float4*>(weight + c + i);
-        s0 = fmaf(w.x, relu(x[i]), s0);
-        s1 = fmaf(w.y, relu(x[i + 1]), s1);
-        s2 = fmaf(w.z, relu(x[i + 2]), s2);
-        s3 = fmaf(w.w, relu(x[i + 3]), s3);
+        const float4 w = *reinterpret_cast<const float4*>(weight + i);
+        add_two(&s0, w.x, w.y, x[i], x[i + 1]);
+        add_two(&s1, w.z, w.w, x[i + 2], x[i + 3]);
       }
-    } else {
+    } else {  // columns past the heads hold zeros times a key: not numbers where the key is none
 #pragma unroll
       for (int i = 0; i < C; ++i)
-        if (i < real) s0 = fmaf(weight[c + i], relu(x[i]), s0);
+        if (i < p.a.heads - in_row) add_two(&s0, weight[i], 0.f, x[i], 0.f);
     }
+    weight += C;
     in_row += C;
-    if (in_row == p.head_cols) {
-      if (pos < length[row]) p.a.logits[(row0 + row) * p.a.logits_row_stride + pos] = found ? ((s0 + s1) + (s2 + s3)) * scale : -INFINITY;
-      ++row;
-      in_row = 0;
-      s0 = s1 = s2 = s3 = 0.f;
-    }
   };
-  for (int c = 0; c < cols; c += 2 * C) {
+  const auto row_done = [&]() {
+    if (in_row != p.head_cols) return;
+    if (pos < length[row]) *out = found ? (sum_of_two(s0) + sum_of_two(s1)) * scale : -INFINITY;
+    out += p.a.logits_row_stride;
+    ++row;
+    in_row = 0;
+    s0 = s1 = 0;
+  };
+#pragma unroll 1
+  while (true) {
     load_wait(v[0]);
-    if (c + C < cols) tmem_load(at + c + C, v[1]);
-    take(v[0], c);
-    if (c + C < cols) {
-      load_wait(v[1]);
-      if (c + 2 * C < cols) tmem_load(at + c + 2 * C, v[0]);
-      take(v[1], c + C);
-    }
+    if (kWide || at + C < end) tmem_load(at + C, v[1]);
+    take(v[0]);
+    if (!kWide) row_done();
+    if (!kWide && at + C >= end) break;
+    load_wait(v[1]);
+    at += 2 * C;
+    if (at < end) tmem_load(at, v[0]);
+    take(v[1]);
+    row_done();
+    if (at >= end) break;
   }
 }
 
@@ -222,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) index_logits_kernel(const __grid_
   const Guard guard{&sm.gave_up, p.R.status};
   if (tid == 0) {
     for (int i = 0; i < kMaxSlots; ++i) {
-      mbar_init(smem_addr(&sm.full[i]), kCopyWarps * p.tiles);
+      mbar_init(smem_addr(&sm.full[i]), kCopyWarps + (p.a.key_scales ? kCopyThreads : 0));
       mbar_init(smem_addr(&sm.empty[i]), 1);
     }
     mbar_init(smem_addr(&sm.q_full), kCopyThreads);
@@ -231,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1) index_logits_kernel(const __grid_
       mbar_init(smem_addr(&sm.s_full[i]), 1);
       mbar_init(smem_addr(&sm.s_empty[i]), kSumWarps / 2);
     }
-    for (int i = 0; i < kTokenSlots; ++i) mbar_init(smem_addr(&sm.token_full[i]), kCopyThreads);
+    for (int i = 0; i < kTokenSlots; ++i) mbar_init(smem_addr(&sm.token_full[i]), kCopyWarps);
     for (int i = 0; i < kSegmentSlots; ++i) mbar_init(smem_addr(&sm.segment_full[i]), kCopyThreads);
     mbar_init(smem_addr(&sm.all_done), 1);
     sm.gave_up = 0;
@@ -286,7 +314,6 @@ __global__ void __launch_bounds__(kThreads, 1) index_logits_kernel(const __grid_
     // ---- copies -----------------------------------------------------------
     const int me = tid - kSumWarps * 32, col = lane & 7;
     const char* q = static_cast<const char*>(p.a.q);
-    TokenRows rows;
     uint32_t step = 0, segment = 0, slot = 0, phase = 0;
     for (; walk.left > 0; walk.next(p), ++segment) {
       mbar_wait(smem_addr(&sm.q_empty), (segment & 1) ^ 1, guard);
@@ -309,67 +336,67 @@ __global__ void __launch_bounds__(kThreads, 1) index_logits_kernel(const __grid_
       }
       for (int j = me; j < walk.rows; j += kCopyThreads) sm.length[ss][j] = row_length(p.R, row0 + j, false);
       mbar_arrive(smem_addr(&sm.segment_full[ss]));
-      // A step's tokens (this thread's: one of each tile) are found in stages, each a step earlier than its result is
-      // used: the block, then the scale.
-      const auto position = [&](int t, int m) { return t < walk.count ? ((walk.at + t) * p.tiles + m) * kTile + me : INT_MAX; };
-      const auto column = [&](int x) { return p.R.block_shift >= 0 ? x >> p.R.block_shift : x / p.R.block_size; };
-      const auto table_entry = [&](int x) {
-        return x < walk.longest ? __ldg(p.R.block_table + walk.request * p.R.table_stride + column(x)) : 0;
-      };
-      const auto in_cache = [&](int x, int b) { return x < walk.longest && b >= 0 && b < p.R.num_blocks; };
-      const auto token_scale = [&](int x, int b) {
-        return p.a.key_scales && in_cache(x, b)
-                   ? __ldg(p.a.key_scales + b * p.a.scale_block_stride + (x - column(x) * p.R.block_size) * p.a.scale_token_stride)
-                   : 1.f;
-      };
-      int at_block[2], next_block[2], later_block[2];
-      float scale[2], next_scale[2];
+      // A warp fetches 32 or 64 of a step's tokens; each lane looks up one or two of them, a group of steps ahead.
+      const int warp_tokens = 32 * p.tiles, warp_first = (warp - kSumWarps) * warp_tokens;
+      const auto position = [&](int t, int h) { return t < walk.count && h < p.tiles ? (walk.at + t) * (kTile * p.tiles) + warp_first + h * 32 + lane : INT_MAX; };
+      int blocks[kGroup][2];
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        at_block[m] = next_block[m] = later_block[m] = 0;
-        scale[m] = next_scale[m] = 1.f;
-        if (m < p.tiles) {
-          at_block[m] = table_entry(position(0, m));
-          next_block[m] = table_entry(position(1, m));
-        }
-      }
+      for (int i = 0; i < kGroup * 2; ++i) blocks[i / 2][i % 2] = table_entry(p, walk, position(i / 2, i % 2));
+      for (int t0 = 0; t0 < walk.count; t0 += kGroup) {
+        int next[kGroup][2];
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
-        if (m < p.tiles) scale[m] = token_scale(position(0, m), at_block[m]);
-      for (int t = 0; t < walk.count; ++t, ++step) {
-        const uint32_t full = smem_addr(&sm.full[0]) + slot * 8, ts = step % kTokenSlots;
+        for (int i = 0; i < kGroup * 2; ++i) next[i / 2][i % 2] = table_entry(p, walk, position(t0 + kGroup + i / 2, i % 2));
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
-          if (m < p.tiles) {
-            later_block[m] = table_entry(position(t + 2, m));
-            next_scale[m] = token_scale(position(t + 1, m), next_block[m]);
+        for (int i = 0; i < kGroup; ++i) {
+          const int t = t0 + i;
+          if (t >= walk.count) break;
+          const uint32_t ts = step % kTokenSlots, full = smem_addr(&sm.full[0]) + slot * 8;
+          const bool runs = p.map.run_rows && (walk.at + t) * (kTile * p.tiles) + warp_first + warp_tokens <= walk.longest;
+          int row[2] = {0, 0};
+          mbar_wait(smem_addr(&sm.empty[0]) + slot * 8, phase ^ 1, guard);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (h < p.tiles) {
+              const int x = position(t, h), place = x - block_column(p.R, x) * p.R.block_size, b = blocks[i][h];
+              const bool here = in_cache(p, walk, x, b);
+              if (x < walk.longest && !here) atomicOr(p.R.status, TOPK_DEV_BAD_BLOCK);
+              row[h] = runs ? run_row(p.map, here, b, place) : gather_row(p.map, here, b, place);
+              const int token = warp_first + h * 32 + lane;
+              sm.found[ts][token] = here;
+              if (p.a.key_scales)
+                copy4(smem_addr(&sm.scale[ts][token]),
+                      here ? p.a.key_scales + b * p.a.scale_block_stride + place * p.a.scale_token_stride : p.a.key_scales, here ? 4 : 0);
+            }
+          if (p.a.key_scales) copies_arrive(full);
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_addr(&sm.token_full[ts]));
+            expect_bytes(full, warp_tokens * 128 * p.chunks);
           }
-        mbar_wait(smem_addr(&sm.empty[0]) + slot * 8, phase ^ 1, guard);
+          __syncwarp();
+          const uint32_t to = ring + slot * slot_bytes;
+          if (runs) {  // a lane for each run and column of 128 bytes
+            const int n = warp_tokens / p.map.run_rows, c = lane / n, from = (lane - c * n) * p.map.run_rows, token = warp_first + from;
+            const int r0 = __shfl_sync(~0u, row[0], from & 31), r1 = __shfl_sync(~0u, row[1], from & 31);
+            if (c < p.chunks) fetch_run(p.map, to + token / kTile * tile_bytes + c * kChunk + token % kTile * 128, c, from < 32 ? r0 : r1, full);
+          } else {  // a lane for each four tokens and column
+            const int n = warp_tokens / 4, c = lane / n, from = (lane - c * n) * 4, token = warp_first + from;
+            int r[4];
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
-          if (m < p.tiles) {
-            const int x = position(t, m), place = x - column(x) * p.R.block_size;
-            const bool here = in_cache(x, at_block[m]);
-            if (x < walk.longest && !here) atomicOr(p.R.status, TOPK_DEV_BAD_BLOCK);
-            if (p.map.run_rows && ((walk.at + t) * p.tiles + m + 1) * kTile <= walk.longest)  // before the pass's last tile
-              rows.set(run_row(p.map, here, at_block[m], place, 0), p.map.run_rows, lane);
-            else
-              rows.set(gather_row(p.map, here, at_block[m], place, 0), 0, lane);
-            rows.fetch(p.map, ring + slot * slot_bytes + m * tile_bytes + (warp - kSumWarps) * 32 * 128, 0, p.chunks, full, lane);
-            sm.scale[ts][m * kTile + me] = scale[m];
-            sm.found[ts][m * kTile + me] = here;
+            for (int j = 0; j < 4; ++j) {
+              const int r0 = __shfl_sync(~0u, row[0], (from + j) & 31), r1 = __shfl_sync(~0u, row[1], (from + j) & 31);
+              r[j] = from < 32 ? r0 : r1;
+            }
+            if (c < p.chunks) fetch_four(p.map, to + token / kTile * tile_bytes + c * kChunk + token % kTile * 128, c, r, full);
           }
-        mbar_arrive(smem_addr(&sm.token_full[ts]));
-        if (++slot == static_cast<uint32_t>(p.slots)) {
-          slot = 0;
-          phase ^= 1;
+          ++step;
+          if (++slot == static_cast<uint32_t>(p.slots)) {
+            slot = 0;
+            phase ^= 1;
+          }
         }
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          at_block[m] = next_block[m];
-          next_block[m] = later_block[m];
-          scale[m] = next_scale[m];
-        }
+        for (int i = 0; i < kGroup * 2; ++i) blocks[i / 2][i % 2] = next[i / 2][i % 2];
       }
     }
     copies_wait_all();
@@ -429,21 +456,24 @@ __global__ void __launch_bounds__(kThreads, 1) index_logits_kernel(const __grid_
       mbar_wait(smem_addr(&sm.segment_full[ss]), (segment / kSegmentSlots) & 1, guard);
       const int middle = (walk.rows + 1) / 2;
       const int row = p.tiles == 1 && part == 1 ? middle : 0, row_end = p.tiles == 1 && part == 0 ? middle : walk.rows;
-      for (int t = 0; t < walk.count; ++t, ++step) {
-        if ((step & 1) != turn) continue;
-        const uint32_t ts = step % kTokenSlots;
-        mbar_wait(smem_addr(&sm.token_full[ts]), (step / kTokenSlots) & 1, guard);
-        const float scale = sm.scale[ts][token];
-        const bool found = sm.found[ts][token];
-        mbar_wait(smem_addr(&sm.s_full[turn]), (step >> 1) & 1, guard);
-        fence_after();
+      for (int t = (step & 1) == turn ? 0 : 1; t < walk.count; t += 2) {
         const int pos = (walk.at + t) * p.tiles * kTile + token;
+        const uint32_t ts = (step + t) % kTokenSlots;
+        mbar_wait(smem_addr(&sm.token_full[ts]), ((step + t) / kTokenSlots) & 1, guard);
+        const bool found = sm.found[ts][token];
+        mbar_wait(smem_addr(&sm.s_full[turn]), ((step + t) >> 1) & 1, guard);
         __syncwarp();
-        sum_tile(p, at + row * p.head_cols, sm.weight[ss], sm.length[ss], row, row_end, pos, scale, found, walk.row0 + walk.first);
+        fence_after();
+        const float scale = p.a.key_scales ? sm.scale[ts][token] : 1.f;  // it came with the keys
+        if (p.a.heads % 32 == 0)
+          sum_tile<true>(p, at + row * p.head_cols, sm.weight[ss], sm.length[ss], row, row_end, pos, scale, found, walk.row0 + walk.first);
+        else
+          sum_tile<false>(p, at + row * p.head_cols, sm.weight[ss], sm.length[ss], row, row_end, pos, scale, found, walk.row0 + walk.first);
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sm.s_empty[turn]));
       }
+      step += walk.count;
     }
   }
   settle(guard);
@@ -498,8 +528,6 @@ extern "C" int topk_index_logits(const topk_index_logits_args* args, void* strea
   Params p{};
   p.a = a;
   p.R = make_rows(a.rows, a.max_len, a.workspace);
-  rc = make_cache_map(&p.map, a.keys, size, a.dtype, a.rows.num_blocks, a.rows.block_size, 1, a.dim, a.key_block_stride, a.key_token_stride, 0);
-  if (rc != TOPK_OK) return rc;
   p.head_cols = (a.heads + 15) / 16 * 16;
   const int fit = kMaxCols / p.head_cols;  // rows that a product takes
   if (a.rows.row_request != nullptr) {
@@ -510,11 +538,14 @@ extern "C" int topk_index_logits(const topk_index_logits_args* args, void* strea
       if (a.rows.next_n % d == 0) p.pack = d;
   }
   if (p.pack > a.rows.num_rows) p.pack = static_cast<int32_t>(a.rows.num_rows);
+  p.tiles = p.pack * p.head_cols <= kMaxCols / 2 ? 2 : 1;
   p.units = (a.rows.num_rows + p.pack - 1) / p.pack;
+  rc = make_cache_map(&p.map, a.keys, size, a.dtype, a.rows.num_blocks, a.rows.block_size, a.dim, a.key_block_stride, a.key_token_stride,
+                      32 * p.tiles);
+  if (rc != TOPK_OK) return rc;
   p.row_bytes = a.dim * size;
   p.chunks = (p.row_bytes + 127) / 128;
   p.q_bytes = static_cast<uint32_t>(p.pack * p.head_cols * 128 * p.chunks);
-  p.tiles = p.pack * p.head_cols <= kMaxCols / 2 ? 2 : 1;
   const int64_t step = p.tiles * kTile, most = a.rows.num_rows * ((p.R.max_len + step - 1) / step);
   p.slices = static_cast<int32_t>(most < props.num_sms ? most : props.num_sms);
   p.inst = ltk::umma::instruction(a.dtype == TOPK_DTYPE_BF16 ? ltk::umma::kBF16 : ltk::umma::kF16, 0, false);

@@ -32,6 +32,7 @@
 // when a tile's exceeds it by 2^8, which leaves the sums exact in fp32 and
 // spares nearly every rescaling of O^T in tensor memory.
 #include "paged.cuh"
+#include "token_copies.cuh"
 #include "umma.cuh"
 
 namespace ltk {
@@ -190,44 +191,6 @@ __device__ __forceinline__ float reduce_columns(const float (&v)[N], int lane) {
   return t[0];
 }
 
-// A copying warp's part of a piece: 32 tokens, eight lanes to each 128 bytes, four tokens an instruction.
-struct Copies {
-  const char* from[8];
-  uint32_t seen;   // bit i: from[i] is to be read
-  uint32_t to[2];  // place in the tile of the even and odd instructions, whose tokens differ by four
-  int byte;        // of a 128-byte row
-  __device__ Copies(int warp, int lane) : seen(0) {
-    const int token = warp * 32 + (lane >> 3), col = lane & 7;
-    byte = col * 16;
-    to[0] = token * 128 + ((col ^ (token & 7)) << 4);
-    to[1] = (token + 4) * 128 + ((col ^ ((token + 4) & 7)) << 4);
-  }
-  // Each lane brings the address of its token, lane by lane in the order of the tile.
-  __device__ __forceinline__ void aim(const char* mine, bool on, int lane) {
-    const unsigned all = __ballot_sync(~0u, on);
-    seen = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int lane_from = i * 4 + (lane >> 3);
-      from[i] = reinterpret_cast<const char*>(__shfl_sync(~0u, reinterpret_cast<uint64_t>(mine), lane_from)) + byte;
-      seen |= ((all >> lane_from) & 1) << i;
-    }
-  }
-  // Up to 128 of the `dims` elements that there are from `first` on; zeros up to the end of a chunk of 64.
-  __device__ __forceinline__ void piece(uint32_t dst, int first, int dims, const void* anywhere) const {
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      if (c * 64 >= dims) break;
-      const bool in = c * 128 + byte < dims * 2;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const bool on = in && ((seen >> i) & 1);
-        copy16(dst + c * kChunk + to[i & 1] + (i >> 1) * 1024, on ? from[i] + (first * 2 + c * 128) : anywhere, on ? 16 : 0);
-      }
-    }
-  }
-};
-
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -361,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     const int col = lane & 7;
     const uint32_t full = smem_addr(&sm.full[0]), empty = smem_addr(&sm.empty[0]);
     Ring at;
-    Copies copies(warp - kSoftmaxWarps, lane);
+    TokenCopies copies((warp - kSoftmaxWarps) * 32, lane);
     // Whether the next slot is empty is asked before a piece's copies are issued: the answer of a later question would
     // wait behind them (185 cycles a piece in which nothing is copied).
     bool empty_next = true;
@@ -443,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         const int next_block = table_entry(next_token), later_token = listed(t + 2);
         const auto copy_rest = [&]() {
           mbar_wait(smem_addr(&sm.rest_empty), (tile & 1) ^ 1, guard);
-          copies.piece(rest, k_ring * 128, p.a.dk - k_ring * 128, p.a.k);
+          copies.columns(rest, kChunk, k_ring * 256, p.a.dk * 2, p.a.k);
           copies_arrive(smem_addr(&sm.rest_full));
         };
         copies.aim(kp, seen, lane);
@@ -451,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         if (kLatent && p.rest && !p.rest_is_p) copy_rest();
         for (int u = 0; u < k_ring; ++u) {
           next_slot();
-          copies.piece(ring + at.slot * kPiece, u * 128, p.a.dk - u * 128, p.a.k);
+          copies.columns(ring + at.slot * kPiece, kChunk, u * 256, p.a.dk * 2, p.a.k);
           done_slot();
         }
         if (kLatent && p.rest && p.rest_is_p) copy_rest();
@@ -459,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           copies.aim(vp, seen, lane);
           for (int u = 0; u < p.v_pieces; ++u) {
             next_slot();
-            copies.piece(ring + at.slot * kPiece, u * 128, p.a.dv - u * 128, p.a.v);
+            copies.columns(ring + at.slot * kPiece, kChunk, u * 256, p.a.dv * 2, p.a.v);
             done_slot();
           }
         }
