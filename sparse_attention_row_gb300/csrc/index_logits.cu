@@ -18,7 +18,8 @@
 // sums up the rows' steps to find its run. Rows are independent over the tokens,
 // so nothing has to be joined.
 //
-// Roles in a CTA (21 warps): 4 fetch keys into a ring of steps by TMA (cache_map.cuh), a
+// Roles in a CTA (21 warps): 4 bring the queries, and one of them (all, where
+// pages are no multiples of 8 tokens) the keys by TMA into a ring of steps (cache_map.cuh), a
 // warp issues the products, four groups of 4 warps sum: two a step, which take a
 // tile each, or half of the rows of the one.
 #include "cache_map.cuh"
@@ -38,7 +39,6 @@ constexpr int kCopyThreads = kCopyWarps * 32;
 constexpr int kMmaWarp = kSumWarps + kCopyWarps;
 constexpr int kThreads = (kMmaWarp + 1) * 32;
 constexpr int kMaxSlots = 8;
-constexpr int kTokenSlots = 16;  // more than the steps that the copies can be ahead of the sums: ring slots + 2
 constexpr int kGroup = 4;        // steps whose blocks are looked up together
 constexpr int kSegmentSlots = 4;  // a segment's weights are written when at most two segments are still being summed
 constexpr int kMaxCols = 256, kMaxRows = 16;
@@ -60,12 +60,10 @@ struct Params {
 };
 
 struct Smem {
-  float scale[kTokenSlots][2 * kTile];
-  uint8_t found[kTokenSlots][2 * kTile];
   float weight[kSegmentSlots][kMaxCols];
   int32_t length[kSegmentSlots][kMaxRows];
   uint64_t full[kMaxSlots], empty[kMaxSlots];
-  uint64_t q_full, q_empty, s_full[2], s_empty[2], token_full[kTokenSlots], segment_full[kSegmentSlots], all_done;
+  uint64_t q_full, q_empty, s_full[2], s_empty[2], segment_full[kSegmentSlots], all_done;
   int64_t scan[kThreads / 32];
   int64_t start_unit, start_at, steps;
   uint32_t tmem, gave_up;
@@ -250,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) index_logits_kernel(const __grid_
   const Guard guard{&sm.gave_up, p.R.status};
   if (tid == 0) {
     for (int i = 0; i < kMaxSlots; ++i) {
-      mbar_init(smem_addr(&sm.full[i]), kCopyWarps + (p.a.key_scales ? kCopyThreads : 0));
+      mbar_init(smem_addr(&sm.full[i]), p.map.run_rows ? 1 : kCopyWarps);
       mbar_init(smem_addr(&sm.empty[i]), 1);
     }
     mbar_init(smem_addr(&sm.q_full), kCopyThreads);
@@ -259,7 +257,6 @@ __global__ void __launch_bounds__(kThreads, 1) index_logits_kernel(const __grid_
       mbar_init(smem_addr(&sm.s_full[i]), 1);
       mbar_init(smem_addr(&sm.s_empty[i]), kSumWarps / 2);
     }
-    for (int i = 0; i < kTokenSlots; ++i) mbar_init(smem_addr(&sm.token_full[i]), kCopyWarps);
     for (int i = 0; i < kSegmentSlots; ++i) mbar_init(smem_addr(&sm.segment_full[i]), kCopyThreads);
     mbar_init(smem_addr(&sm.all_done), 1);
     sm.gave_up = 0;
@@ -314,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1) index_logits_kernel(const __grid_
     // ---- copies -----------------------------------------------------------
     const int me = tid - kSumWarps * 32, col = lane & 7;
     const char* q = static_cast<const char*>(p.a.q);
-    uint32_t step = 0, segment = 0, slot = 0, phase = 0;
+    uint32_t segment = 0, slot = 0, phase = 0;
     for (; walk.left > 0; walk.next(p), ++segment) {
       mbar_wait(smem_addr(&sm.q_empty), (segment & 1) ^ 1, guard);
       const int cols = walk.rows * p.head_cols;
@@ -336,67 +333,67 @@ __global__ void __launch_bounds__(kThreads, 1) index_logits_kernel(const __grid_
       }
       for (int j = me; j < walk.rows; j += kCopyThreads) sm.length[ss][j] = row_length(p.R, row0 + j, false);
       mbar_arrive(smem_addr(&sm.segment_full[ss]));
-      // A warp fetches 32 or 64 of a step's tokens; each lane looks up one or two of them, a group of steps ahead.
-      const int warp_tokens = 32 * p.tiles, warp_first = (warp - kSumWarps) * warp_tokens;
-      const auto position = [&](int t, int h) { return t < walk.count && h < p.tiles ? (walk.at + t) * (kTile * p.tiles) + warp_first + h * 32 + lane : INT_MAX; };
-      int blocks[kGroup][2];
+      // The keys of a pass's last tokens and of what lies behind them come whole: a token's scores are its own.
+      const int step_tokens = kTile * p.tiles;
+      const auto place_of = [&](int token) { return ring + slot * slot_bytes + token / kTile * tile_bytes + token % kTile * 128; };
+      const auto row_of = [&](int x, int b) {
+        const bool here = in_cache(p, walk, x, b);
+        const int place = x - block_column(p.R, x) * p.R.block_size;
+        return p.map.run_rows ? run_row(p.map, here, b, place) : gather_row(p.map, here, b, place);
+      };
+      const auto next_slot = [&]() {
+        if (++slot == static_cast<uint32_t>(p.slots)) {
+          slot = 0;
+          phase ^= 1;
+        }
+      };
+      if (p.map.run_rows) {
+        // one warp, a lane for each run of tokens; the runs' blocks are looked up a group of steps ahead
+        if (warp == kSumWarps) {
+          const int token = lane * p.map.run_rows;
+          const auto position = [&](int t) { return t < walk.count && token < step_tokens ? (walk.at + t) * step_tokens + token : INT_MAX; };
+          int blocks[kGroup];
 #pragma unroll
-      for (int i = 0; i < kGroup * 2; ++i) blocks[i / 2][i % 2] = table_entry(p, walk, position(i / 2, i % 2));
-      for (int t0 = 0; t0 < walk.count; t0 += kGroup) {
-        int next[kGroup][2];
+          for (int i = 0; i < kGroup; ++i) blocks[i] = table_entry(p, walk, position(i));
+          for (int t0 = 0; t0 < walk.count; t0 += kGroup) {
+            int next[kGroup];
 #pragma unroll
-        for (int i = 0; i < kGroup * 2; ++i) next[i / 2][i % 2] = table_entry(p, walk, position(t0 + kGroup + i / 2, i % 2));
+            for (int i = 0; i < kGroup; ++i) next[i] = table_entry(p, walk, position(t0 + kGroup + i));
 #pragma unroll
-        for (int i = 0; i < kGroup; ++i) {
-          const int t = t0 + i;
-          if (t >= walk.count) break;
-          const uint32_t ts = step % kTokenSlots, full = smem_addr(&sm.full[0]) + slot * 8;
-          const bool runs = p.map.run_rows && (walk.at + t) * (kTile * p.tiles) + warp_first + warp_tokens <= walk.longest;
-          int row[2] = {0, 0};
-          mbar_wait(smem_addr(&sm.empty[0]) + slot * 8, phase ^ 1, guard);
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (h < p.tiles) {
-              const int x = position(t, h), place = x - block_column(p.R, x) * p.R.block_size, b = blocks[i][h];
-              const bool here = in_cache(p, walk, x, b);
-              if (x < walk.longest && !here) atomicOr(p.R.status, TOPK_DEV_BAD_BLOCK);
-              row[h] = runs ? run_row(p.map, here, b, place) : gather_row(p.map, here, b, place);
-              const int token = warp_first + h * 32 + lane;
-              sm.found[ts][token] = here;
-              if (p.a.key_scales)
-                copy4(smem_addr(&sm.scale[ts][token]),
-                      here ? p.a.key_scales + b * p.a.scale_block_stride + place * p.a.scale_token_stride : p.a.key_scales, here ? 4 : 0);
+            for (int i = 0; i < kGroup; ++i) {
+              if (t0 + i >= walk.count) break;
+              const uint32_t full = smem_addr(&sm.full[0]) + slot * 8;
+              const int row = row_of(position(t0 + i), blocks[i]);
+              mbar_wait(smem_addr(&sm.empty[0]) + slot * 8, phase ^ 1, guard);
+              if (lane == 0) expect_bytes(full, slot_bytes);
+              __syncwarp();
+              if (token < step_tokens)
+                for (int c = 0; c < p.chunks; ++c) fetch_run(p.map, place_of(token) + c * kChunk, c, row, full);
+              next_slot();
             }
-          if (p.a.key_scales) copies_arrive(full);
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(smem_addr(&sm.token_full[ts]));
-            expect_bytes(full, warp_tokens * 128 * p.chunks);
-          }
-          __syncwarp();
-          const uint32_t to = ring + slot * slot_bytes;
-          if (runs) {  // a lane for each run and column of 128 bytes
-            const int n = warp_tokens / p.map.run_rows, c = lane / n, from = (lane - c * n) * p.map.run_rows, token = warp_first + from;
-            const int r0 = __shfl_sync(~0u, row[0], from & 31), r1 = __shfl_sync(~0u, row[1], from & 31);
-            if (c < p.chunks) fetch_run(p.map, to + token / kTile * tile_bytes + c * kChunk + token % kTile * 128, c, from < 32 ? r0 : r1, full);
-          } else {  // a lane for each four tokens and column
-            const int n = warp_tokens / 4, c = lane / n, from = (lane - c * n) * 4, token = warp_first + from;
-            int r[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int r0 = __shfl_sync(~0u, row[0], (from + j) & 31), r1 = __shfl_sync(~0u, row[1], (from + j) & 31);
-              r[j] = from < 32 ? r0 : r1;
-            }
-            if (c < p.chunks) fetch_four(p.map, to + token / kTile * tile_bytes + c * kChunk + token % kTile * 128, c, r, full);
-          }
-          ++step;
-          if (++slot == static_cast<uint32_t>(p.slots)) {
-            slot = 0;
-            phase ^= 1;
+            for (int i = 0; i < kGroup; ++i) blocks[i] = next[i];
           }
         }
+      } else {
+        // pages of odd sizes: four warps, a lane for each four tokens
+        const int token = (warp - kSumWarps) * (step_tokens / kCopyWarps) + lane * 4;
+        const bool mine = lane * 4 < step_tokens / kCopyWarps;
+        for (int t = 0; t < walk.count; ++t) {
+          const uint32_t full = smem_addr(&sm.full[0]) + slot * 8;
+          int row[4];
 #pragma unroll
-        for (int i = 0; i < kGroup * 2; ++i) blocks[i / 2][i % 2] = next[i / 2][i % 2];
+          for (int j = 0; j < 4; ++j) {
+            const int x = (walk.at + t) * step_tokens + token + j;
+            row[j] = row_of(x, table_entry(p, walk, x));
+          }
+          mbar_wait(smem_addr(&sm.empty[0]) + slot * 8, phase ^ 1, guard);
+          if (lane == 0) expect_bytes(full, slot_bytes / kCopyWarps);
+          __syncwarp();
+          if (mine)
+            for (int c = 0; c < p.chunks; ++c) fetch_four(p.map, place_of(token) + c * kChunk, c, row, full);
+          next_slot();
+        }
       }
     }
     copies_wait_all();
@@ -456,15 +453,24 @@ __global__ void __launch_bounds__(kThreads, 1) index_logits_kernel(const __grid_
       mbar_wait(smem_addr(&sm.segment_full[ss]), (segment / kSegmentSlots) & 1, guard);
       const int middle = (walk.rows + 1) / 2;
       const int row = p.tiles == 1 && part == 1 ? middle : 0, row_end = p.tiles == 1 && part == 0 ? middle : walk.rows;
-      for (int t = (step & 1) == turn ? 0 : 1; t < walk.count; t += 2) {
-        const int pos = (walk.at + t) * p.tiles * kTile + token;
-        const uint32_t ts = (step + t) % kTokenSlots;
-        mbar_wait(smem_addr(&sm.token_full[ts]), ((step + t) / kTokenSlots) & 1, guard);
-        const bool found = sm.found[ts][token];
+      // the token's block and scale, looked up two and one of this group's steps ahead
+      const auto position = [&](int t) { return t < walk.count ? (walk.at + t) * p.tiles * kTile + token : INT_MAX; };
+      const auto token_scale = [&](int x, int b) {
+        return p.a.key_scales && in_cache(p, walk, x, b)
+                   ? __ldg(p.a.key_scales + b * p.a.scale_block_stride + (x - block_column(p.R, x) * p.R.block_size) * p.a.scale_token_stride)
+                   : 1.f;
+      };
+      int t = (step & 1) == turn ? 0 : 1;
+      int at_block = table_entry(p, walk, position(t)), next_block = table_entry(p, walk, position(t + 2));
+      float scale = token_scale(position(t), at_block);
+      for (; t < walk.count; t += 2) {
+        const int pos = position(t), later_block = table_entry(p, walk, position(t + 4));
+        const float next_scale = token_scale(position(t + 2), next_block);
+        const bool found = in_cache(p, walk, pos, at_block);
+        if (pos < walk.longest && !found) atomicOr(p.R.status, TOPK_DEV_BAD_BLOCK);
         mbar_wait(smem_addr(&sm.s_full[turn]), ((step + t) >> 1) & 1, guard);
         __syncwarp();
         fence_after();
-        const float scale = p.a.key_scales ? sm.scale[ts][token] : 1.f;  // it came with the keys
         if (p.a.heads % 32 == 0)
           sum_tile<true>(p, at + row * p.head_cols, sm.weight[ss], sm.length[ss], row, row_end, pos, scale, found, walk.row0 + walk.first);
         else
@@ -472,6 +478,9 @@ __global__ void __launch_bounds__(kThreads, 1) index_logits_kernel(const __grid_
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sm.s_empty[turn]));
+        at_block = next_block;
+        next_block = later_block;
+        scale = next_scale;
       }
       step += walk.count;
     }
@@ -541,7 +550,7 @@ extern "C" int topk_index_logits(const topk_index_logits_args* args, void* strea
   p.tiles = p.pack * p.head_cols <= kMaxCols / 2 ? 2 : 1;
   p.units = (a.rows.num_rows + p.pack - 1) / p.pack;
   rc = make_cache_map(&p.map, a.keys, size, a.dtype, a.rows.num_blocks, a.rows.block_size, a.dim, a.key_block_stride, a.key_token_stride,
-                      32 * p.tiles);
+                      64);
   if (rc != TOPK_OK) return rc;
   p.row_bytes = a.dim * size;
   p.chunks = (p.row_bytes + 127) / 128;
