@@ -41,13 +41,17 @@ namespace {
 
 using namespace ltk::umma;
 
-constexpr int kTile = 128;             // tokens
-constexpr int kChunk = 128 * 128;      // bytes of 128 tokens x 64 dims
-constexpr int kPiece = 2 * kChunk;     // a ring slot
+constexpr int kTile = 128;            // tokens
+constexpr int kChunk = kTile * 128;   // bytes of 64 dims
+constexpr int kPiece = 2 * kChunk;    // a ring slot: 128 dims
+// Places for P, and for the rest of the keys. A latent tile and the queries leave room for one; elsewhere the next tile's
+// probabilities need not wait until the last one's have been multiplied.
+template <bool kLatent>
+constexpr int places = kLatent ? 1 : 2;
 constexpr int kSoftmaxWarps = 8, kCopyWarps = 4;
 constexpr int kCopyThreads = kCopyWarps * 32;
-constexpr int kMmaWarp = kSoftmaxWarps + kCopyWarps;
-constexpr int kThreads = (kMmaWarp + 1) * 32;
+constexpr int kScoreWarp = kSoftmaxWarps + kCopyWarps, kValueWarp = kScoreWarp + 1;
+constexpr int kThreads = (kValueWarp + 1) * 32;
 constexpr int kTokenSlots = 8;  // more than the tiles that the copies can be ahead of the softmax: ring slots + 1
 constexpr int kMaxSlots = 6;
 constexpr int kMaxQk = 576, kMaxV = 512;
@@ -76,10 +80,9 @@ struct Params {
   int32_t k_chunks;      // of 64 dims
   int32_t k_pieces, v_pieces;
   int32_t latent;        // values are the first dims of the keys
-  int32_t rest;          // 1: the last half piece of the keys has a buffer of its own
+  int32_t rest;          // 1: the last 64 dims of the keys, which are no values, have two buffers of their own
   int32_t rest_is_p;     // 1: and P takes its place after it has been used
   int32_t slots;         // of the ring
-  int32_t ahead;         // 1: the next tile's scores are taken before this tile's values
   int32_t slices;
   int32_t row_tiles;     // tiles of every unit where index lists are given, else 0
   int32_t whole;         // 1: slices begin between units only (index lists)
@@ -87,7 +90,7 @@ struct Params {
   uint32_t tmem_cols;
   uint32_t q_bytes;
   float scale2;          // scale * log2(e)
-  float* part;           // [slices][2][blocks][N][v_pieces * 128]
+  float* part;           // [slices][2][blocks][v_pieces * 128][N]
   float2* stat;          // [slices][2][blocks][N]: maximum (in powers of two) and sum
   Join* join;            // [slices]
 };
@@ -95,7 +98,7 @@ struct Params {
 template <int N>
 struct Smem {  // behind the tiles
   static constexpr int kHalf = N / 2;
-  int32_t token[kTokenSlots][kTile];  // position of each token of a tile, INT_MAX where nothing is to be seen
+  int32_t token[kTokenSlots][128];  // position of each token of a tile, INT_MAX where nothing is to be seen
   float column_max[2][4][kHalf];      // [half][warp]; a barrier stands between one tile's reads and the next one's writes
   float moved[kSoftmaxWarps][2][kHalf];  // maximum in use, factor of the old sums
   float column_sum[2][4][kHalf];
@@ -103,7 +106,7 @@ struct Smem {  // behind the tiles
   int64_t out_at[2][2][kHalf];  // and where its output lies
   int32_t least[2][2];
   uint64_t full[kMaxSlots], empty[kMaxSlots];
-  uint64_t q_full, q_empty, rest_full, rest_empty, s_full[2], p_full, o_done, token_full[kTokenSlots], all_done;
+  uint64_t q_full, q_empty, rest_full[2], rest_empty[2], s_full[2], s_empty[2], p_full[2], o_done[2], token_full[kTokenSlots], all_done[2];
   int64_t scan[kThreads / 32];
   int64_t start_group, tiles, run_begin, run_end;
   int64_t start_at;
@@ -121,7 +124,7 @@ __device__ __forceinline__ int group_length(const Params& p, int64_t g, bool rep
 __device__ __forceinline__ int group_tiles(const Params& p, int64_t g, bool report) {
   if (p.row_tiles) return p.row_tiles;
   const int n = group_length(p, g, report);
-  return n == 0 ? 1 : (n + kTile - 1) / kTile;
+  return n == 0 ? 1 : static_cast<int>((n + kTile - 1u) / kTile);
 }
 
 // First tile of slice s, and the slice of tile x; in 32 bits where the products fit (a 64-bit division takes some
@@ -210,11 +213,12 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 
 template <int N, bool kBf16, bool kLatent>
 __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ Params p) {
+  constexpr int kPlaces = places<kLatent>;
   extern __shared__ __align__(1024) uint8_t raw[];
   const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
   const uint32_t q_at = base, ring = q_at + p.q_bytes, rest = ring + p.slots * kPiece;
-  const uint32_t p_at = rest + (p.rest && !p.rest_is_p ? kChunk : 0);
-  Smem<N>& sm = *reinterpret_cast<Smem<N>*>(raw + (p_at + kChunk - smem_addr(raw)));
+  const uint32_t p_at = rest + (p.rest && !p.rest_is_p ? kPlaces * kChunk : 0);
+  Smem<N>& sm = *reinterpret_cast<Smem<N>*>(raw + (p_at + kPlaces * kChunk - smem_addr(raw)));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int block = blockIdx.x % p.blocks, slice = blockIdx.x / p.blocks;
   const Guard guard{&sm.gave_up, p.R.status};
@@ -226,18 +230,20 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     }
     mbar_init(smem_addr(&sm.q_full), kCopyThreads);
     mbar_init(smem_addr(&sm.q_empty), 1);
-    mbar_init(smem_addr(&sm.rest_full), kCopyThreads);
-    mbar_init(smem_addr(&sm.rest_empty), 1);
-    mbar_init(smem_addr(&sm.s_full[0]), 1);
-    mbar_init(smem_addr(&sm.s_full[1]), 1);
-    mbar_init(smem_addr(&sm.p_full), kSoftmaxWarps);
-    mbar_init(smem_addr(&sm.o_done), 1);
-    mbar_init(smem_addr(&sm.all_done), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&sm.rest_full[i]), kCopyThreads);
+      mbar_init(smem_addr(&sm.rest_empty[i]), 1);
+      mbar_init(smem_addr(&sm.s_full[i]), 1);
+      mbar_init(smem_addr(&sm.s_empty[i]), kSoftmaxWarps);
+      mbar_init(smem_addr(&sm.p_full[i]), kSoftmaxWarps);
+      mbar_init(smem_addr(&sm.o_done[i]), 1);
+      mbar_init(smem_addr(&sm.all_done[i]), 1);
+    }
     for (int i = 0; i < kTokenSlots; ++i) mbar_init(smem_addr(&sm.token_full[i]), kCopyThreads);
     sm.gave_up = 0;
     fence_async();
   }
-  if (warp == kMmaWarp) tmem_alloc(smem_addr(&sm.tmem), p.tmem_cols);
+  if (warp == kScoreWarp) tmem_alloc(smem_addr(&sm.tmem), p.tmem_cols);
   dependent_wait();
   dependent_launch();
 
@@ -318,25 +324,23 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   const uint32_t s_cols = static_cast<uint32_t>(p.v_pieces) * N;  // columns before the scores'
   const int block_cols = min(p.block_cols, p.cols - block * p.block_cols);
 
-  if (warp >= kSoftmaxWarps && warp < kMmaWarp) {
+  if (warp >= kSoftmaxWarps && warp < kScoreWarp) {
     // ---- copies -----------------------------------------------------------
-    const int me = tid - kSoftmaxWarps * 32;  // this thread's token of a tile
-    const int col = lane & 7;
+    const int me = tid - kSoftmaxWarps * 32, col = lane & 7;  // a thread's token of a tile: `me`
     const uint32_t full = smem_addr(&sm.full[0]), empty = smem_addr(&sm.empty[0]);
     Ring at;
     TokenCopies copies((warp - kSoftmaxWarps) * 32, lane);
     // Whether the next slot is empty is asked before a piece's copies are issued: the answer of a later question would
-    // wait behind them (185 cycles a piece in which nothing is copied).
+    // wait behind them.
     bool empty_next = true;
-    const auto next_slot = [&]() {
+    const auto copy_slot = [&](int first, int bytes, const void* cache) {
       if (!empty_next) mbar_wait(empty + at.slot * 8, at.phase ^ 1, guard);
       Ring then = at;
       then.step(p.slots);
       empty_next = mbar_test(empty + then.slot * 8, then.phase ^ 1);
-    };
-    const auto done_slot = [&]() {
+      copies.columns(ring + at.slot * kPiece, kChunk, first, bytes, cache);
       copies_arrive(full + at.slot * 8);
-      at.step(p.slots);
+      at = then;
     };
     uint32_t tile = 0, segment = 0;
     for (; walk.left > 0; walk.next(p), ++segment) {
@@ -360,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                                                       (x - column(x) * p.R.block_size) * token_stride + walk.kv_head * head_stride);
       };
       const auto in_cache = [&](int x, int x_block) { return x >= 0 && x < length && x_block >= 0 && x_block < p.R.num_blocks; };
-      // A latent tile's copies wait for the tile before it to leave the ring. So its tokens are fetched into L2 some tiles
+      // A latent tile's copies wait for an earlier tile to leave the ring. So its tokens are fetched into L2 some tiles
       // ahead, the blocks of a unit a part of them each.
       const auto fetch = [&](int x, int x_block) {
         if (!in_cache(x, x_block)) return;
@@ -368,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         for (int line = block; line * 64 < p.a.dk; line += p.blocks) asm volatile("prefetch.global.L2 [%0];" ::"l"(from + line * 128));
       };
       int at_token = listed(0), next_token = listed(1);
-      if (kLatent) {
+      if constexpr (kLatent) {
         int x[kFetchAhead - 1], b[kFetchAhead - 1];
 #pragma unroll
         for (int i = 0; i < kFetchAhead - 1; ++i) x[i] = listed(i + 1);
@@ -404,29 +408,22 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           if (!kLatent) vp = address(vp, at_token, at_block, p.a.v_block_stride, p.a.v_token_stride, p.a.v_head_stride);
         }
         const int next_block = table_entry(next_token), later_token = listed(t + 2);
-        const auto copy_rest = [&]() {
-          mbar_wait(smem_addr(&sm.rest_empty), (tile & 1) ^ 1, guard);
-          copies.columns(rest, kChunk, k_ring * 256, p.a.dk * 2, p.a.k);
-          copies_arrive(smem_addr(&sm.rest_full));
-        };
         copies.aim(kp, seen, lane);
-        // the rest first where it has a buffer of its own, free since this tile's predecessor was scored
+        const auto copy_rest = [&]() {
+          const uint32_t b = tile & 1, before = tile - kPlaces;  // the tile that had this place
+          if (tile >= kPlaces) mbar_wait(smem_addr(&sm.rest_empty[before & 1]), (before >> 1) & 1, guard);
+          copies.columns(rest + (kPlaces == 2 ? b * kChunk : 0), kChunk, k_ring * 2 * 128, p.a.dk * 2, p.a.k);
+          copies_arrive(smem_addr(&sm.rest_full[b]));
+        };
+        // the rest first where it has buffers of its own, free since an earlier tile was scored
         if (kLatent && p.rest && !p.rest_is_p) copy_rest();
-        for (int u = 0; u < k_ring; ++u) {
-          next_slot();
-          copies.columns(ring + at.slot * kPiece, kChunk, u * 256, p.a.dk * 2, p.a.k);
-          done_slot();
-        }
+        for (int u = 0; u < k_ring; ++u) copy_slot(u * 2 * 128, p.a.dk * 2, p.a.k);
         if (kLatent && p.rest && p.rest_is_p) copy_rest();
-        if (!kLatent) {
+        if constexpr (!kLatent) {
           copies.aim(vp, seen, lane);
-          for (int u = 0; u < p.v_pieces; ++u) {
-            next_slot();
-            copies.columns(ring + at.slot * kPiece, kChunk, u * 256, p.a.dv * 2, p.a.v);
-            done_slot();
-          }
+          for (int u = 0; u < p.v_pieces; ++u) copy_slot(u * 2 * 128, p.a.dv * 2, p.a.v);
         }
-        if (kLatent) {
+        if constexpr (kLatent) {
           const int x = listed(t + kFetchAhead);
           fetch(x, table_entry(x));
         }
@@ -436,104 +433,100 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       }
     }
     copies_wait_all();
-  } else if (warp == kMmaWarp) {
-    // ---- products ---------------------------------------------------------
-    constexpr uint32_t kInstS = instruction(kBf16 ? kBF16 : kF16, N, false);
-    constexpr uint32_t kInstO = instruction(kBf16 ? kBF16 : kF16, N, true);
+  } else if (warp == kScoreWarp) {
+    // ---- S^T = K Q^T, into one of two places ---------------------------------
+    constexpr uint32_t kInst = instruction(kBf16 ? kBF16 : kF16, N, false);
     const uint32_t full = smem_addr(&sm.full[0]), empty = smem_addr(&sm.empty[0]);
-    Ring kr, vr;  // the pieces of keys and of values that come next
-    if (!kLatent) vr.step(p.slots, k_ring);
-    uint32_t scored = 0;                    // tiles whose scores have been taken
-    // S^T of the next tile, into one of its two places
-    const int whole_pieces = p.a.dk / 128;
+    const int whole_pieces = p.a.dk / (2 * 64);
     const bool rest_first = kLatent && p.rest && !p.rest_is_p;
-    // the keys' last dims where they fill no piece
-    const auto last_scores = [&](uint32_t d, bool add) {
-      uint32_t at = rest, q_piece = q_at + whole_pieces * 2 * N * 128;
-      if (kLatent && p.rest) {
-        mbar_wait_warp(smem_addr(&sm.rest_full), scored & 1, guard);
-      } else {
-        at = ring + kr.slot * kPiece;
-        mbar_wait_warp(full + kr.slot * 8, kr.phase, guard);
-      }
-      fence_async();
-      int left = p.a.dk - whole_pieces * 128;
-      if (left >= 64) {
-        mma16_chunk(d, operand(at, 16), operand(q_piece, 16), kInstS, add);
-        add = true;
-        left -= 64;
-        at += kChunk;
-        q_piece += N * 128;
-      }
-#pragma unroll 1
-      for (; left > 0; left -= 16, at += 32, q_piece += 32, add = true) mma16_step(d, operand(at, 16), operand(q_piece, 16), kInstS, add);
-      if (kLatent && p.rest) {
-        if (!p.rest_is_p) commit(smem_addr(&sm.rest_empty));
-      } else {
-        if (!kLatent || whole_pieces >= p.v_pieces) commit(empty + kr.slot * 8);
-        kr.step(p.slots);
-      }
-    };
-    const auto scores = [&]() {
-      const uint32_t d = tmem + s_cols + (scored & 1) * N;
-      uint32_t q_piece = q_at;
-      if (rest_first) last_scores(d, false);
-      bool ready = false;
-#pragma unroll 1
-      for (int u = 0; u < whole_pieces; ++u, q_piece += 2 * N * 128) {
-        if (!ready) mbar_wait(full + kr.slot * 8, kr.phase, guard);
-        __syncwarp();
-        fence_async();
-        const Ring here = kr;
-        kr.step(p.slots);
-        ready = mbar_test(full + kr.slot * 8, kr.phase);  // the answer comes while the products are issued
-        mma16_piece(d, operand(ring + here.slot * kPiece, 16), operand(q_piece, 16), operand(q_piece + N * 128, 16), kInstS, rest_first || u > 0);
-        if (!kLatent || u >= p.v_pieces) commit(empty + here.slot * 8);  // keys that are no values are done with
-      }
-      if (!rest_first && whole_pieces < p.k_pieces) last_scores(d, whole_pieces > 0);
-      if (!kLatent) kr.step(p.slots, p.v_pieces);
-      commit(smem_addr(&sm.s_full[scored & 1]));
-      ++scored;
-    };
+    Ring at;
     uint32_t tile = 0, segment = 0;
     for (; walk.left > 0; walk.next(p), ++segment) {
       mbar_wait_warp(smem_addr(&sm.q_full), segment & 1, guard);
       fence_async();
-      int to_score = walk.count;
-      if (p.ahead) {
-        scores();
-        --to_score;
-      }
 #pragma unroll 1
       for (int t = 0; t < walk.count; ++t, ++tile) {
-        if (to_score > 0) {
-          scores();
-          --to_score;
-        }
-        if (to_score == 0) {  // once: the queries are done with
-          commit(smem_addr(&sm.q_empty));
-          --to_score;
-        }
-        mbar_wait_warp(smem_addr(&sm.p_full), tile & 1, guard);
+        const uint32_t b = tile & 1, d = tmem + s_cols + b * N;
+        // the keys' last dims where they fill no piece
+        const auto last_dims = [&](bool add) {
+          uint32_t k_at, q_piece = q_at + whole_pieces * 2 * (N * 128);
+          if (kLatent && p.rest) {
+            k_at = rest + (kPlaces == 2 ? b * kChunk : 0);
+            mbar_wait_warp(smem_addr(&sm.rest_full[b]), (tile >> 1) & 1, guard);
+          } else {
+            k_at = ring + at.slot * kPiece;
+            mbar_wait_warp(full + at.slot * 8, at.phase, guard);
+          }
+          fence_async();
+          int left = p.a.dk - whole_pieces * (2 * 64);
+#pragma unroll 1
+          for (; left >= 64; left -= 64, k_at += kChunk, q_piece += N * 128, add = true)
+            mma16_chunk(d, operand(k_at, 16), operand(q_piece, 16), kInst, add);
+#pragma unroll 1
+          for (; left > 0; left -= 16, k_at += 32, q_piece += 32, add = true) mma16_step(d, operand(k_at, 16), operand(q_piece, 16), kInst, add);
+          if (kLatent && p.rest) {
+            if (!p.rest_is_p) commit(smem_addr(&sm.rest_empty[b]));
+          } else {
+            if (!kLatent || whole_pieces >= p.v_pieces) commit(empty + at.slot * 8);
+            at.step(p.slots);
+          }
+        };
+        mbar_wait_warp(smem_addr(&sm.s_empty[b]), ((tile >> 1) & 1) ^ 1, guard);
         fence_after();
+        if (rest_first) last_dims(false);
+        uint32_t q_piece = q_at;
+        bool ready = false;
+#pragma unroll 1
+        for (int u = 0; u < whole_pieces; ++u) {
+          if (!ready) mbar_wait(full + at.slot * 8, at.phase, guard);
+          __syncwarp();
+          fence_async();
+          const uint32_t slot = at.slot;
+          at.step(p.slots);
+          ready = mbar_test(full + at.slot * 8, at.phase);  // the answer comes while the products are issued
+          mma16_pair(d, operand(ring + slot * kPiece, 16), kChunk >> 4, operand(q_piece, 16), (N * 128) >> 4, kInst, rest_first || u > 0);
+          q_piece += 2 * N * 128;
+          if (!kLatent || u >= p.v_pieces) commit(empty + slot * 8);  // keys that are no values are done with
+        }
+        if (!rest_first && whole_pieces < p.k_pieces) last_dims(whole_pieces > 0);
+        if (!kLatent) at.step(p.slots, p.v_pieces);
+        commit(smem_addr(&sm.s_full[b]));
+      }
+      commit(smem_addr(&sm.q_empty));
+    }
+    commit(smem_addr(&sm.all_done[0]));
+    mbar_wait_warp(smem_addr(&sm.all_done[0]), 0, guard);
+  } else if (warp == kValueWarp) {
+    // ---- O^T += V^T P^T --------------------------------------------------------
+    constexpr uint32_t kInst = instruction(kBf16 ? kBF16 : kF16, N, true);
+    const uint32_t full = smem_addr(&sm.full[0]), empty = smem_addr(&sm.empty[0]);
+    Ring at;
+    uint32_t tile = 0;
+    for (; walk.left > 0; walk.next(p)) {
+#pragma unroll 1
+      for (int t = 0; t < walk.count; ++t, ++tile) {
+        const uint32_t b = tile & 1;
+        mbar_wait_warp(smem_addr(&sm.p_full[b]), (tile >> 1) & 1, guard);
+        fence_after();
+        if (!kLatent) at.step(p.slots, k_ring);
+        const uint32_t p_tile = operand(p_at + (kPlaces == 2 ? b * kChunk : 0), 1024);
 #pragma unroll 1
         for (int u = 0; u < p.v_pieces; ++u) {
           if (!kLatent) {
-            mbar_wait_warp(full + vr.slot * 8, vr.phase, guard);
+            mbar_wait_warp(full + at.slot * 8, at.phase, guard);
             fence_async();
           }
-          mma16_tokens(tmem + u * N, operand(ring + vr.slot * kPiece, kChunk), operand(p_at, 1024), kInstO, t > 0);
-          commit(empty + vr.slot * 8);
-          vr.step(p.slots);
+          mma16_tokens(tmem + u * N, operand(ring + at.slot * kPiece, kChunk), p_tile, kInst, t > 0);
+          commit(empty + at.slot * 8);
+          at.step(p.slots);
         }
-        vr.step(p.slots, kLatent ? k_ring - p.v_pieces : k_ring);
-        if (kLatent && p.rest_is_p) commit(smem_addr(&sm.rest_empty));
-        commit(smem_addr(&sm.o_done));
+        if (kLatent) at.step(p.slots, k_ring - p.v_pieces);
+        if (kLatent && p.rest_is_p) commit(smem_addr(&sm.rest_empty[b]));
+        commit(smem_addr(&sm.o_done[b]));
       }
     }
-    commit(smem_addr(&sm.all_done));
-    mbar_wait_warp(smem_addr(&sm.all_done), 0, guard);
-    __syncwarp();
+    commit(smem_addr(&sm.all_done[1]));
+    mbar_wait_warp(smem_addr(&sm.all_done[1]), 0, guard);
   } else {
     // ---- softmax and output ------------------------------------------------
     constexpr int H = N / 2;
@@ -632,10 +625,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           __syncwarp();
           probabilities();
         }
-        // the last tile's product has read P and written O
-        if (tile > 0) mbar_wait(smem_addr(&sm.o_done), (tile - 1) & 1, guard);
-        fence_after();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sm.s_empty[tile & 1]));
         if (rescale) {  // the same for all warps of this half: they hold the same maxima
+          mbar_wait(smem_addr(&sm.o_done[(tile & 1) ^ 1]), ((tile - 1) >> 1) & 1, guard);  // the tile before has been added
+          __syncwarp();
+          fence_after();
 #pragma unroll
           for (int i = 0; i < H; ++i) l[i] *= sm.moved[warp][1][i];
           for (int u = 0; u < p.v_pieces; ++u) {
@@ -652,21 +648,25 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           }
           store_wait();
         }
+        // the product that read this place of P is done
+        if (tile >= kPlaces) mbar_wait(smem_addr(&sm.o_done[(tile - kPlaces) & 1]), ((tile - kPlaces) >> 1) & 1, guard);
 #pragma unroll
         for (int i = 0; i < H; ++i) l[i] += s[i];
-        const uint32_t row = p_at + token * 128;
+        const uint32_t row = p_at + (kPlaces == 2 ? (tile & 1) * kChunk : 0) + token * 128;
+        {
 #pragma unroll
-        for (int i = 0; i < H; i += 8) {
-          const uint32_t at = row + ((((half * H + i) >> 3) ^ (token & 7)) << 4);
-          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(pack2<kBf16>(s[i], s[i + 1])),
-                       "r"(pack2<kBf16>(s[i + 2], s[i + 3])), "r"(pack2<kBf16>(s[i + 4], s[i + 5])),
-                       "r"(pack2<kBf16>(s[i + 6], s[i + 7]))
-                       : "memory");
+          for (int i = 0; i < H; i += 8) {
+            const uint32_t at = row + ((((half * H + i) >> 3) ^ (token & 7)) << 4);
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(pack2<kBf16>(s[i], s[i + 1])),
+                         "r"(pack2<kBf16>(s[i + 2], s[i + 3])), "r"(pack2<kBf16>(s[i + 4], s[i + 5])),
+                         "r"(pack2<kBf16>(s[i + 6], s[i + 7]))
+                         : "memory");
+          }
         }
         fence_async();
         fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&sm.p_full));
+        if (lane == 0) mbar_arrive(smem_addr(&sm.p_full[tile & 1]));
       }
       const float part_l = reduce_columns<H, false>(l, lane);
       if (lane < H) sm.column_sum[half][quarter][lane] = part_l;
@@ -687,7 +687,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         }
       }
       __syncwarp();
-      mbar_wait(smem_addr(&sm.o_done), (tile - 1) & 1, guard);
+      mbar_wait(smem_addr(&sm.o_done[(tile & 1) ^ 1]), ((tile - 1) >> 1) & 1, guard);
+      __syncwarp();
       fence_after();
 #pragma unroll 1
       for (int u = 0; u < p.v_pieces; ++u) {
@@ -746,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == kMmaWarp) tmem_free(tmem, p.tmem_cols);
+  if (warp == kScoreWarp) tmem_free(tmem, p.tmem_cols);
 }
 
 // A load that stays where it is written: left to the compiler, the join's loads move to their uses, one latency each
@@ -865,26 +866,26 @@ size_t workspace_for(int sms) {
   return TOPK_PAGED_WORKSPACE_BYTES + (most_ctas(sms) * kJoinBytes + 255) / 256 * 256 + slots * kMaxBlockCols * (kMaxV * sizeof(float) + sizeof(float2));
 }
 
-static_assert(sizeof(Smem<64>) + 1024 + 9 * 64 * 128 + 4 * kPiece + kChunk <= 232448, "latent attention of 64 columns: four pieces of the ring");
+static_assert(sizeof(Smem<64>) + 1024 + 9 * 64 * 128 + 4 * kPiece + kChunk <= 232448, "a latent tile beside 64 columns");
 
 template <int N, bool kBf16, bool kLatent>
 int run(Params& p, int device, int smem_limit, bool joins, cudaStream_t stream) {
   const int extra = static_cast<int>(sizeof(Smem<N>)) + 1024;
   p.q_bytes = p.k_chunks * N * 128;
   p.rest_is_p = 0;
-  int room = smem_limit - extra - static_cast<int>(p.q_bytes) - kChunk;  // for the ring and, where it is not P, the rest
+  constexpr int kExtra = places<kLatent> * kChunk;  // for P, and for the rest
+  int room = smem_limit - extra - static_cast<int>(p.q_bytes) - kExtra;  // for the ring and, where it is not P, the rest
   if (p.rest) {
-    // a buffer of its own for the rest lets the next tile's last keys come early, if the ring loses nothing by it
-    p.rest_is_p = (room - kChunk) / kPiece < room / kPiece;
-    if (!p.rest_is_p) room -= kChunk;
+    // buffers of its own for the rest let a later tile's last keys come early, if the ring loses nothing by it
+    p.rest_is_p = (room - kExtra) / kPiece < room / kPiece;
+    if (!p.rest_is_p) room -= kExtra;
   }
   p.slots = room / kPiece < kMaxSlots ? room / kPiece : kMaxSlots;
-  const int k_ring = p.k_pieces - p.rest, tile_pieces = k_ring + (p.latent ? 0 : p.v_pieces);
-  if (p.slots < (p.latent ? tile_pieces : 1)) return TOPK_ERR_PLAN;
-  p.ahead = !p.rest_is_p && p.slots >= tile_pieces + k_ring;
+  const int k_ring = p.k_pieces - p.rest;
+  if (p.slots < (p.latent && k_ring > 2 ? k_ring : 2)) return TOPK_ERR_PLAN;
   p.tmem_cols = 32;
   while (p.tmem_cols < static_cast<uint32_t>((p.v_pieces + 2) * N)) p.tmem_cols *= 2;
-  const size_t smem = p.q_bytes + static_cast<size_t>(p.slots) * kPiece + (p.rest && !p.rest_is_p ? kChunk : 0) + kChunk + extra;
+  const size_t smem = p.q_bytes + static_cast<size_t>(p.slots) * kPiece + (p.rest && !p.rest_is_p ? kExtra : 0) + kExtra + extra;
   static int granted[kMaxDevices];
   int rc = allow_smem(attention_kernel<N, kBf16, kLatent>, smem_limit, device, granted);
   if (rc != TOPK_OK) return rc;
@@ -951,15 +952,15 @@ extern "C" int topk_paged_attention(const topk_attention_args* args, void* strea
   p.blocks = (p.cols + kMaxBlockCols - 1) / kMaxBlockCols;
   p.block_cols = (p.cols + p.blocks - 1) / p.blocks;
   p.k_chunks = (a.dk + 63) / 64;
+  p.latent = a.v == nullptr;
   p.k_pieces = (p.k_chunks + 1) / 2;
   p.v_pieces = (a.dv + 127) / 128;
-  p.latent = a.v == nullptr;
   p.rest = p.latent && p.k_chunks % 2 == 1 && p.k_pieces > p.v_pieces;
   p.row_groups = a.rows.num_rows / p.pack;
   p.row_tiles = a.indices ? (a.num_indices + kTile - 1) / kTile : 0;
   p.scale2 = a.scale * 1.4426950408889634f;
   const int64_t units = p.row_groups * a.kv_heads;
-  const int64_t most = units * (a.indices ? p.row_tiles : (p.R.max_len + kTile - 1) / kTile);
+  const int64_t most = units * (a.indices ? p.row_tiles : (p.R.max_len + static_cast<int64_t>(kTile) - 1) / kTile);
   int64_t slices = sms / p.blocks < 1 ? 1 : sms / p.blocks;
   if (slices > most) slices = most;
   if (slices > kMaxParts) slices = kMaxParts;

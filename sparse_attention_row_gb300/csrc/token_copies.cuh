@@ -15,7 +15,8 @@ namespace paged {
 
 // A copying warp's 32 tokens of a tile: eight lanes to each 128 bytes, four tokens an instruction.
 struct TokenCopies {
-  const char* from[8];
+  static constexpr int kEach = 8, kColumns = 2;
+  const char* from[kEach];
   uint32_t seen;   // bit i: from[i] is to be read
   uint32_t to[2];  // place in the tile of the even and odd instructions, whose tokens differ by four
   int byte;        // of a 128-byte row
@@ -25,26 +26,26 @@ struct TokenCopies {
     to[0] = token * 128 + ((col ^ (token & 7)) << 4);
     to[1] = (token + 4) * 128 + ((col ^ ((token + 4) & 7)) << 4);
   }
-  // Each lane brings the address of its token, lane by lane in the order of the tile.
+  // Each lane brings the address of a token, lane by lane in the order of the tile.
   __device__ __forceinline__ void aim(const char* mine, bool on, int lane) {
     const unsigned all = __ballot_sync(~0u, on);
     seen = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kEach; ++i) {
       const int lane_from = i * 4 + (lane >> 3);
       from[i] = reinterpret_cast<const char*>(__shfl_sync(~0u, reinterpret_cast<uint64_t>(mine), lane_from)) + byte;
       seen |= ((all >> lane_from) & 1) << i;
     }
   }
-  // Up to 256 bytes of each token from `first` on, a token having `bytes` in all: 128-byte columns (swizzled tiles,
-  // `column` bytes apart), the last one filled up with zeros.
+  // Up to 256 bytes of each token from `first` on, a token having `bytes` in all: 128-byte columns (swizzled
+  // tiles, `column` bytes apart), the last one filled up with zeros.
   __device__ __forceinline__ void columns(uint32_t dst, uint32_t column, int first, int bytes, const void* anywhere) const {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
+    for (int c = 0; c < kColumns; ++c) {
       if (first + c * 128 >= bytes) break;
       const bool in = first + c * 128 + byte < bytes;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < kEach; ++i) {
         const bool on = in && ((seen >> i) & 1);
         umma::copy16(dst + c * column + to[i & 1] + (i >> 1) * 1024, on ? from[i] + (first + c * 128) : anywhere, on ? 16 : 0);
       }

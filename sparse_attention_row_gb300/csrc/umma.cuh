@@ -252,9 +252,9 @@ __device__ __forceinline__ void mma16_chunk(uint32_t d, uint32_t a, uint32_t b, 
       : "memory");
 }
 
-// 256 bytes of both, in two chunks: A's 16 KB apart, B's at b and b2.
-__device__ __forceinline__ void mma16_piece(uint32_t d, uint32_t a, uint32_t b, uint32_t b2, uint32_t inst, bool add) {
-  d = uniform(d), a = uniform(a), b = uniform(b), b2 = uniform(b2);
+// 256 bytes of both, in two chunks, the second ones `a_next` and `b_next` (in 16 bytes) behind the first.
+__device__ __forceinline__ void mma16_pair(uint32_t d, uint32_t a, uint32_t a_next, uint32_t b, uint32_t b_next, uint32_t inst, bool add) {
+  d = uniform(d), a = uniform(a), b = uniform(b);
   asm volatile(
       "{\n .reg .pred p, q, t;\n .reg .b32 x, y;\n .reg .b64 a, b;\n"
       " setp.ne.u32 p, %5, 0;\n setp.eq.u32 t, 0, 0;\n elect.sync _|q, 0xffffffff;\n"
@@ -266,15 +266,15 @@ __device__ __forceinline__ void mma16_piece(uint32_t d, uint32_t a, uint32_t b, 
       " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
       " add.u32 x, %1, 6; add.u32 y, %2, 6; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
       " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
-      " add.u32 x, %1, 1024; add.u32 y, %6, 0; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " add.u32 x, %6, 0; add.u32 y, %7, 0; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
       " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
-      " add.u32 x, %1, 1026; add.u32 y, %6, 2; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " add.u32 x, %6, 2; add.u32 y, %7, 2; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
       " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
-      " add.u32 x, %1, 1028; add.u32 y, %6, 4; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " add.u32 x, %6, 4; add.u32 y, %7, 4; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
       " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
-      " add.u32 x, %1, 1030; add.u32 y, %6, 6; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " add.u32 x, %6, 6; add.u32 y, %7, 6; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
       " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
-      "}" ::"r"(d), "r"(a), "r"(b), "r"(kOperandHigh), "r"(inst), "r"(static_cast<uint32_t>(add)), "r"(b2)
+      "}" ::"r"(d), "r"(a), "r"(b), "r"(kOperandHigh), "r"(inst), "r"(static_cast<uint32_t>(add)), "r"(a + a_next), "r"(b + b_next)
       : "memory");
 }
 
