@@ -5,7 +5,7 @@
 // Two exclusive sums over the requests (new tokens; blocks taken) place
 // everything. They are short (a few thousand requests at most), so every CTA
 // computes both from the start of the lists, a segment of requests at a time
-// in shared memory, and then writes its own slice of the token lists: one
+// in shared memory, and then writes its own chunks of the token lists: one
 // launch, nothing exchanged between CTAs but a ticket. A token finds its
 // request by a binary search in the segment's starts. A block taken in this
 // call always holds a new token at its first place, so the thread that lists
@@ -15,7 +15,7 @@
 // it, and the one that draws the last ticket writes taken_out (and sets the
 // ticket back to zero).
 //
-// Bound by latency: 16 bytes are written a token.
+// Bound by latency, and by the 16 bytes that are written a token.
 #include "paged.cuh"
 
 namespace ltk {
@@ -26,7 +26,7 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPer = 4;                    // requests a thread scans
 constexpr int kSegment = kThreads * kPer;  // requests of one segment
-constexpr int kSlice = 2048;               // tokens that make a CTA worth its scan
+constexpr int kChunk = 2048;               // consecutive tokens of a CTA; chunks are dealt to the CTAs in turn
 constexpr int kTicketWord = 8;             // of the workspace
 
 struct MapParams {
@@ -44,9 +44,9 @@ __device__ __forceinline__ int64_t context(const MapParams& p, int64_t r) {
   return p.a.context_lens[r] < 0 ? 0 : p.a.context_lens[r];
 }
 
-__global__ void __launch_bounds__(kThreads) kv_map_kernel(const MapParams p) {
-  __shared__ int64_t start[kSegment];      // first new token of each request of the segment
-  __shared__ int64_t first[kSegment];      // blocks taken before each
+__global__ void __launch_bounds__(kThreads, 3) kv_map_kernel(const MapParams p) {
+  __shared__ uint32_t start[kSegment];  // first new token of each request of the segment, from the segment's first
+  __shared__ uint32_t first[kSegment];  // blocks taken before each, likewise
   __shared__ int64_t warp_tokens[kWarps], warp_blocks[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const topk_kv_map_args& a = p.a;
@@ -54,9 +54,11 @@ __global__ void __launch_bounds__(kThreads) kv_map_kernel(const MapParams p) {
   dependent_wait();
   dependent_launch();
   const int64_t taken = *a.taken;
-  const int64_t slice = (a.max_tokens + gridDim.x - 1) / gridDim.x;  // tokens of this CTA: [t0, t1)
-  const int64_t t0 = slice * blockIdx.x;
-  const int64_t t1 = t0 + slice < a.max_tokens ? t0 + slice : a.max_tokens;
+  // this CTA's first chunk that ends after token x
+  const auto first_chunk = [&](int64_t x) {
+    const int64_t chunk = x / kChunk;
+    return (chunk + gridDim.x - 1 - blockIdx.x) / gridDim.x * gridDim.x + blockIdx.x;
+  };
   int64_t tokens = 0, blocks = 0;  // before the segment
   uint32_t flags = 0;
   for (int64_t r0 = 0; r0 < a.num_requests; r0 += kSegment) {
@@ -119,50 +121,68 @@ __global__ void __launch_bounds__(kThreads) kv_map_kernel(const MapParams p) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int j = tid * kPer + i;
-      start[j] = at;
-      first[j] = took;
+      start[j] = static_cast<uint32_t>(at - tokens);
+      first[j] = static_cast<uint32_t>(took - blocks);
       if (j < n && (r0 / kSegment) % gridDim.x == blockIdx.x) a.token_start[r0 + j] = static_cast<int32_t>(at);
       at += my_new[i];
       took += my_take[i];
     }
     __syncthreads();
-    const int64_t lo = t0 > tokens ? t0 : tokens, end = tokens + seg_tokens, hi = t1 < end ? t1 : end;
-    for (int64_t t = lo + tid; t < hi; t += kThreads) {
-      int j = 0;  // the last request whose start is at or before t: it holds t, since later ones start after it
+    const int64_t end = tokens + seg_tokens;
+    // Token numbers are below 2^31 and positions below 2^32, so 32 bits do from here on.
+    const uint32_t n_tokens = static_cast<uint32_t>(seg_tokens);
+    const int64_t taken_here = taken + blocks;
+    for (int64_t chunk = first_chunk(tokens); chunk * kChunk < end; chunk += gridDim.x) {
+      const int64_t chunk0 = chunk * kChunk - tokens;  // from the segment's first token
+#pragma unroll 2
+      for (int i = 0; i < kChunk; i += kThreads) {
+        const int64_t t64 = chunk0 + i + tid;
+        if (t64 < 0 || t64 >= n_tokens) continue;
+        const uint32_t t = static_cast<uint32_t>(t64);
+        uint32_t j = 0;  // the last request whose start is at or before t: it holds t, since later ones start after it
 #pragma unroll
-      for (int step = kSegment / 2; step > 0; step >>= 1)
-        if (start[j + step] <= t) j += step;
-      const int64_t r = r0 + j;
-      const int64_t c = context(p, r);
-      const int64_t pos = c + (t - start[j]);
-      const int64_t col = p.block_shift >= 0 ? pos >> p.block_shift : pos / a.block_size;
-      const int64_t place = pos - col * a.block_size;
-      const int64_t have = blocks_for(p, c);
-      int64_t block = -1;
-      if (col >= a.max_blocks) {
-        flags |= TOPK_DEV_TABLE_FULL;
-      } else if (col < have) {
-        block = a.block_table[r * a.table_stride + col];
-      } else {
-        const int64_t i = taken + first[j] + (col - have);
-        if (i >= 0 && i < a.num_free)
-          block = a.free_blocks[i];
-        else
-          flags |= TOPK_DEV_BLOCKS_EXHAUSTED;
-        if (place == 0) a.block_table[r * a.table_stride + col] = static_cast<int32_t>(block);
+        for (uint32_t step = kSegment / 2; step > 0; step >>= 1)
+          if (start[j + step] <= t) j += step;
+        const int32_t r = static_cast<int32_t>(r0) + static_cast<int32_t>(j);
+        const int32_t c = max(a.context_lens[r], 0);
+        const uint32_t pos = static_cast<uint32_t>(c) + (t - start[j]);
+        const uint32_t size = a.block_size, columns = static_cast<uint32_t>(a.max_blocks);
+        const uint32_t col = p.block_shift >= 0 ? pos >> p.block_shift : pos / size;
+        const uint32_t place = pos - col * size;
+        const uint32_t have = min(p.block_shift >= 0 ? (c + (size - 1)) >> p.block_shift : (c + (size - 1)) / size, columns);
+        int32_t* entry = a.block_table + r * a.table_stride + col;
+        int32_t block = -1;
+        if (col >= columns) {
+          flags |= TOPK_DEV_TABLE_FULL;
+        } else if (col < have) {
+          block = *entry;
+        } else {
+          const int64_t n = taken_here + first[j] + (col - have);
+          if (n >= 0 && n < a.num_free)
+            block = __ldg(a.free_blocks + n);
+          else
+            flags |= TOPK_DEV_BLOCKS_EXHAUSTED;
+          if (place == 0) *entry = block;
+        }
+        const int64_t at = tokens + t;
+        a.slots[at] = block < 0 ? -1 : static_cast<int64_t>(block) * size + place;
+        a.row_lens[at] = static_cast<int32_t>(min(pos, 0x7FFFFFFEu) + 1);
+        a.row_request[at] = r;
       }
-      a.slots[t] = block < 0 ? -1 : block * a.block_size + place;
-      a.row_lens[t] = static_cast<int32_t>(pos + 1 < INT32_MAX ? pos + 1 : INT32_MAX);
-      a.row_request[t] = static_cast<int32_t>(r);
     }
     tokens += seg_tokens;
     blocks += seg_blocks;
     __syncthreads();  // the next segment writes the starts again
   }
-  for (int64_t t = (t0 > tokens ? t0 : tokens) + tid; t < t1; t += kThreads) {
-    a.slots[t] = -1;
-    a.row_lens[t] = 0;
-    a.row_request[t] = -1;
+  for (int64_t chunk = first_chunk(tokens); chunk * kChunk < a.max_tokens; chunk += gridDim.x) {
+#pragma unroll
+    for (int i = 0; i < kChunk; i += kThreads) {
+      const int64_t t = chunk * kChunk + i + tid;
+      if (t < tokens || t >= a.max_tokens) continue;
+      a.slots[t] = -1;
+      a.row_lens[t] = 0;
+      a.row_request[t] = -1;
+    }
   }
   if (flags) atomicOr(status, flags);
   if (tid == 0) {
@@ -225,7 +245,7 @@ extern "C" int topk_kv_map(const topk_kv_map_args* args, void* stream) {
   p.block_shift = -1;
   for (int s = 0; s < 31; ++s)
     if ((1ll << s) == a.block_size) p.block_shift = s;
-  int64_t grid = (a.max_tokens + kSlice - 1) / kSlice;
-  grid = grid < 1 ? 1 : (grid > 2ll * sms ? 2ll * sms : grid);
+  int64_t grid = (a.max_tokens + kChunk - 1) / kChunk;
+  grid = grid < 1 ? 1 : (grid > 3ll * sms ? 3ll * sms : grid);
   return launch(kv_map_kernel, p, grid, kThreads, 0, static_cast<cudaStream_t>(stream));
 }
