@@ -73,26 +73,37 @@ __device__ __forceinline__ int steps_of(const Params& p, int length) { return (l
 
 // The rows of a unit: whether those that see anything have one request, and the unit's steps.
 struct Unit {
-  int64_t row0;
-  int rows;
+  int64_t row0, request;  // of those rows
+  int rows, longest;
   bool shared;
   int64_t steps;
-  __device__ Unit(const Params& p, int64_t u, bool report) {
+  __device__ Unit(const Params& p, int64_t u) {
     row0 = u * p.pack;
     rows = static_cast<int>(min(static_cast<int64_t>(p.pack), p.R.num_rows - row0));
     shared = true;
-    int most = 0;
-    int64_t sum = 0, request = -1;
-    for (int j = 0; j < rows; ++j) {
-      const int n = row_length(p.R, row0 + j, report);
-      if (n == 0) continue;
-      most = max(most, n);
-      sum += steps_of(p, n);
-      const int64_t b = row_request(p.R, row0 + j);
-      if (request >= 0 && b != request) shared = false;
-      request = b;
+    longest = 0;
+    request = -1;
+    int64_t sum = 0;
+    for (int j0 = 0; j0 < rows; j0 += 8) {  // eight rows' entries on their way at once
+      int32_t n[8];
+      int64_t b[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int64_t row = row0 + min(j0 + i, rows - 1);
+        n[i] = p.R.lengths[row];
+        b[i] = row_request(p.R, row);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = j0 + i < rows ? seen_tokens(p.R, n[i], b[i]) : 0;
+        if (c == 0) continue;
+        longest = max(longest, c);
+        sum += steps_of(p, c);
+        if (request >= 0 && b[i] != request) shared = false;
+        request = b[i];
+      }
     }
-    steps = shared ? steps_of(p, most) : sum;
+    steps = shared ? steps_of(p, longest) : sum;
   }
 };
 
@@ -105,36 +116,29 @@ struct Walk {
   int unit_rows;
   bool shared;
   int at, count, longest;
-  __device__ void pass(const Params& p, int from) {  // the pass that begins with the unit's row `from` or a later one
+  __device__ void pass(const Params& p, int from) {  // of a unit with several: the one of row `from` or a later one
     longest = 0;
-    first = from;
     rows = 0;
-    if (shared) {
-      if (from > 0) return;
-      rows = unit_rows;
-      for (int j = 0; j < rows; ++j) {
-        const int n = row_length(p.R, row0 + j, false);
-        if (n > 0) request = row_request(p.R, row0 + j);
-        longest = max(longest, n);
-      }
-    } else {
-      for (; first < unit_rows; ++first) {
-        longest = row_length(p.R, row0 + first, false);
-        if (longest > 0) {
-          rows = 1;
-          request = row_request(p.R, row0 + first);
-          return;
-        }
+    for (first = from; first < unit_rows; ++first) {
+      longest = row_length(p.R, row0 + first);
+      if (longest > 0) {
+        rows = 1;
+        request = row_request(p.R, row0 + first);
+        return;
       }
     }
   }
   __device__ void enter(const Params& p, int64_t u) {
-    const Unit x(p, u, false);
+    const Unit x(p, u);
     unit = u;
     row0 = x.row0;
     unit_rows = x.rows;
     shared = x.shared;
-    pass(p, 0);
+    first = 0;
+    rows = x.rows;
+    longest = x.longest;
+    request = x.request;
+    if (!shared) pass(p, 0);
   }
   __device__ void size(const Params& p) { count = static_cast<int>(min(static_cast<int64_t>(steps_of(p, longest) - at), left)); }
   __device__ void start(const Params& p, int64_t u, int64_t offset) {
@@ -150,7 +154,8 @@ struct Walk {
     left -= count;
     at = 0;
     if (left <= 0) return;
-    pass(p, shared ? 1 : first + 1);
+    longest = 0;
+    if (!shared) pass(p, first + 1);
     while (longest == 0) enter(p, unit + 1);  // there are steps left, so some later unit has them
     size(p);
   }
@@ -257,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1) index_logits_kernel(const __grid_
     const int64_t per = (p.units + kThreads - 1) / kThreads;
     const int64_t u0 = min(per * tid, p.units), u1 = min(u0 + per, p.units);
     int64_t mine = 0;
-    for (int64_t u = u0; u < u1; ++u) mine += Unit(p, u, slice == 0).steps;
+    for (int64_t u = u0; u < u1; ++u) mine += Unit(p, u).steps;
     int64_t pre = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -274,8 +279,12 @@ __global__ void __launch_bounds__(kThreads, 1) index_logits_kernel(const __grid_
     const int64_t begin = total * slice / p.slices;
     int64_t at = pre - mine;
     if (begin >= at && begin < pre) {
-      for (int64_t u = u0; u < u1; ++u) {
-        const int64_t n = Unit(p, u, false).steps;
+      if (u1 - u0 == 1) {
+        sm.start_unit = u0;
+        sm.start_at = begin - at;
+      }
+      for (int64_t u = u0; u1 - u0 > 1 && u < u1; ++u) {
+        const int64_t n = Unit(p, u).steps;
         if (begin < at + n) {
           sm.start_unit = u;
           sm.start_at = begin - at;
@@ -319,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) index_logits_kernel(const __grid_
         const int j = n / p.head_cols, h = n - j * p.head_cols;
         sm.weight[ss][n] = h < p.a.heads ? p.a.weights[(row0 + j) * p.a.weight_row_stride + h] : 0.f;
       }
-      for (int j = me; j < walk.rows; j += kCopyThreads) sm.length[ss][j] = row_length(p.R, row0 + j, false);
+      for (int j = me; j < walk.rows; j += kCopyThreads) sm.length[ss][j] = row_length(p.R, row0 + j);
       mbar_arrive(smem_addr(&sm.segment_full[ss]));
       // The keys of a pass's last tokens and of what lies behind them come whole: a token's scores are its own.
       const int step_tokens = kTile * p.tiles;
@@ -494,6 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) index_logits_kernel(const __grid_
       step += walk.count;
     }
   }
+  if (slice == 0) report_rows(p.R, tid, kThreads);
   settle(guard);
   fence_before();
   __syncthreads();

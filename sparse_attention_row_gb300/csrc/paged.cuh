@@ -36,31 +36,27 @@ __device__ __forceinline__ int64_t row_request(const Rows& R, int64_t row) {
   return R.row_request ? static_cast<int64_t>(R.row_request[row]) : row / R.next_n;
 }
 
-// Tokens that a row sees; 0 for a padding row (negative request).
-__device__ __forceinline__ int row_length(const Rows& R, int64_t row, bool report) {
-  if (R.row_request) {
-    const int32_t b = R.row_request[row];
-    if (b < 0) return 0;
-    if (b >= R.num_requests) {
-      if (report) atomicOr(R.status, TOPK_DEV_BAD_BLOCK);
-      return 0;
-    }
-  }
-  const int32_t n = R.lengths[row];
-  const int32_t c = n < 0 ? 0 : (n > R.max_len ? R.max_len : n);
-  if (report && c != n) atomicOr(R.status, TOPK_DEV_LENGTH_CLAMPED);
-  return c;
+// Tokens that a row sees, from its entry in `lengths` and its request; 0 for a padding row (negative request).
+__device__ __forceinline__ int seen_tokens(const Rows& R, int32_t n, int64_t request) {
+  if (request < 0 || request >= R.num_requests) return 0;
+  return n < 0 ? 0 : (n > R.max_len ? R.max_len : n);
 }
 
-// Block and place of token `pos` (0 <= pos < max_len) of a request; false where its block is outside the cache.
-__device__ __forceinline__ bool locate(const Rows& R, int64_t request, int pos, int64_t* block, int* place) {
-  const int col = R.block_shift >= 0 ? pos >> R.block_shift : pos / R.block_size;
-  *place = pos - col * R.block_size;
-  const int32_t b = __ldg(R.block_table + request * R.table_stride + col);
-  *block = b;
-  if (b >= 0 && b < R.num_blocks) return true;
-  atomicOr(R.status, TOPK_DEV_BAD_BLOCK);
-  return false;
+__device__ __forceinline__ int row_length(const Rows& R, int64_t row) {
+  const int32_t n = R.lengths[row];
+  return seen_tokens(R, n, row_request(R, row));
+}
+
+// Reports what was wrong with the rows: one CTA does it, when its work is done.
+__device__ __forceinline__ void report_rows(const Rows& R, int tid, int threads) {
+  uint32_t bits = 0;
+  for (int64_t row = tid; row < R.num_rows; row += threads) {
+    const int32_t n = R.lengths[row];
+    const int64_t b = row_request(R, row);
+    if (b >= R.num_requests) bits |= TOPK_DEV_BAD_BLOCK;
+    if (b >= 0 && b < R.num_requests && (n < 0 || n > R.max_len)) bits |= TOPK_DEV_LENGTH_CLAMPED;
+  }
+  if (bits) atomicOr(R.status, bits);
 }
 
 // Programmatic dependent launch: wait for the kernel before this one on the stream, before the first

@@ -114,16 +114,17 @@ struct Smem {  // behind the tiles
   uint32_t gave_up;
 };
 
-__device__ __forceinline__ int group_length(const Params& p, int64_t g, bool report) {
+__device__ __forceinline__ int group_length(const Params& p, int64_t g) {
   int most = 0;
-  for (int j = 0; j < p.pack; ++j) most = max(most, row_length(p.R, g * p.pack + j, report));
+#pragma unroll 4
+  for (int j = 0; j < p.pack; ++j) most = max(most, row_length(p.R, g * p.pack + j));
   return most;
 }
 
 // Tiles of a unit; one at least, so that every unit is met and its rows written.
-__device__ __forceinline__ int group_tiles(const Params& p, int64_t g, bool report) {
+__device__ __forceinline__ int group_tiles(const Params& p, int64_t g) {
   if (p.row_tiles) return p.row_tiles;
-  const int n = group_length(p, g, report);
+  const int n = group_length(p, g);
   return n == 0 ? 1 : static_cast<int>((n + kTile - 1u) / kTile);
 }
 
@@ -153,7 +154,7 @@ struct Walk {
     if (++kv_head == p.a.kv_heads) {
       kv_head = 0;
       ++group;
-      if (left > 0) tiles = group_tiles(p, group, false);
+      if (left > 0) tiles = group_tiles(p, group);
     }
     size();
   }
@@ -269,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     const int64_t per = (p.row_groups + kThreads - 1) / kThreads;
     const int64_t g0 = min(per * tid, p.row_groups), g1 = min(g0 + per, p.row_groups);
     int64_t mine = 0;
-    for (int64_t g = g0; g < g1; ++g) mine += group_tiles(p, g, blockIdx.x == 0);
+    for (int64_t g = g0; g < g1; ++g) mine += group_tiles(p, g);
     int64_t pre = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -287,8 +288,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     const int64_t begin = slice_begin(total, p.slices, slice);
     int64_t at = (pre - mine) * p.a.kv_heads;
     if (begin >= at && begin < pre * p.a.kv_heads) {
-      for (int64_t g = g0; g < g1; ++g) {
-        const int64_t n = static_cast<int64_t>(group_tiles(p, g, false)) * p.a.kv_heads;
+      if (g1 - g0 == 1) {
+        sm.start_group = g0;
+        sm.start_at = begin - at;
+      }
+      for (int64_t g = g0; g1 - g0 > 1 && g < g1; ++g) {
+        const int64_t n = static_cast<int64_t>(group_tiles(p, g)) * p.a.kv_heads;
         if (begin < at + n) {
           sm.start_group = g;
           sm.start_at = begin - at;
@@ -313,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   walk.group = sm.start_group;
   walk.count = 0;
   if (walk.left > 0) {
-    walk.tiles = group_tiles(p, walk.group, false);
+    walk.tiles = group_tiles(p, walk.group);
     walk.kv_head = 0;
     int64_t at = sm.start_at;
     for (; at >= walk.tiles; at -= walk.tiles) ++walk.kv_head;
@@ -345,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     uint32_t tile = 0, segment = 0;
     for (; walk.left > 0; walk.next(p), ++segment) {
       const int64_t row0 = walk.group * p.pack;
-      const int length = group_length(p, walk.group, false);
+      const int length = group_length(p, walk.group);
       const int64_t request = length > 0 ? row_request(p.R, row0) : 0;
       const int32_t* list = p.a.indices ? p.a.indices + row0 * p.a.index_row_stride : nullptr;
       // A tile's tokens are found in two steps, each a tile earlier than its result is used: the position (from
@@ -544,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         int n = INT_MAX;
         if (my_col < block_cols) {
           const int j = c / p.group;
-          n = row_length(p.R, row0 + j, p.row_tiles != 0 && block == 0);
+          n = row_length(p.R, row0 + j);
           if (lane < H)
             sm.out_at[segment & 1][half][lane] = (row0 + j) * p.a.out_row_stride + static_cast<int64_t>(walk.kv_head * p.group + c - j * p.group) * p.a.out_head_stride;
         }
@@ -743,6 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       p.join[slice] = j;
     }
   }
+  if (blockIdx.x == 0) report_rows(p.R, tid, kThreads);
   settle(guard);
   fence_before();
   __syncthreads();

@@ -298,6 +298,22 @@ def test_drafted_tokens(dec, next_n, heads, kv_heads, dk, dv, latent, topk):
     check_attention(dec, lengths, case, next_n, dv, 64)
 
 
+def test_more_columns_than_are_packed(dec):
+    # 3 rows of 512 heads over one key-value head: each row by itself, in eight blocks of 64 columns
+    lengths = [200, 201, 202, 40, 41, 42]
+    case = attention_case(26, lengths, 3, 512, 1, 64, 64, False, torch.float16, 16)
+    check_attention(dec, lengths, case, 3, 64, 16)
+
+
+@pytest.mark.parametrize("block", [8, 16, 24, 32, 48, 64, 128, 192])
+def test_logits_over_pages_of_any_size(dec, block):
+    lengths = [700, 129, 300, 1]
+    for dtype in (torch.bfloat16, F8):
+        case = logits_case(block, lengths, 1, 64, 128, dtype, block, scaled=True)
+        check_logits(dec, lengths, case, 1, block, 700)
+    ok(dec)
+
+
 def test_a_request_for_each_row(dec):
     req = [0] * 40 + [2] * 3 + [1] + [3, 0, 3]
     lengths = [200 + i for i in range(40)] + [0, 130, 600, 1, 77, 900, 2]
@@ -500,3 +516,20 @@ def test_binding_refuses(dec):
         dec.attention(q, k, t, ln, v_dim=72)
     with pytest.raises(ValueError):
         dec.index_logits(q, torch.zeros(2, 15, device="cuda"), k[:, :, 0], t, ln)
+
+
+# ---- together ----------------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kw", [dict(), dict(requests=1, prompt=40, topk=64, block=16, heads=128), dict(requests=9, prompt=300, topk=1, block=5, heads=40),
+                                dict(requests=3, prompt=2500, topk=2048, heads=64)])
+def test_example_of_sparse_decoding(dec, kw):
+    # map, logits, selection and attention, each call on the last one's output; bf16 outputs below 8, so half a unit in
+    # the last place of the largest (2^-6), as much for the probabilities' rounding, and the same again
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "sparse_decode.py")
+    spec = importlib.util.spec_from_file_location("sparse_decode", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    assert module.run(**kw) < 4 * 2.0 ** -6
