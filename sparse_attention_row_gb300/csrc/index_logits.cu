@@ -311,23 +311,26 @@ __global__ void __launch_bounds__(kThreads, 1) index_logits_kernel(const __grid_
     uint32_t segment = 0, slot = 0, phase = 0;
     for (; walk.left > 0; walk.next(p), ++segment) {
       mbar_wait(smem_addr(&sm.q_empty), (segment & 1) ^ 1, guard);
-      const int cols = walk.rows * p.head_cols;
       const int64_t row0 = walk.row0 + walk.first;
-      for (int n = me >> 3; n < cols; n += kCopyThreads / 8) {
-        const int j = n / p.head_cols, h = n - j * p.head_cols;
-        const char* from = q + ((row0 + j) * p.a.q_row_stride + h * p.a.q_head_stride) * elem;
-        for (int ch = 0; ch < p.chunks; ++ch) {
-          const int byte = ch * 128 + col * 16;
-          const bool in = h < p.a.heads && byte < p.row_bytes;
-          copy16(q_at + ch * (p.pack * p.head_cols * 128) + n * 128 + ((col ^ (n & 7)) << 4), in ? from + byte : q, in ? 16 : 0);
+      for (int j = 0; j < walk.rows; ++j) {
+        const char* row_q = q + (row0 + j) * p.a.q_row_stride * elem;
+#pragma unroll 4
+        for (int h = me >> 3; h < p.head_cols; h += kCopyThreads / 8) {
+          const char* from = row_q + h * p.a.q_head_stride * elem;
+          const int n = j * p.head_cols + h;
+          for (int ch = 0; ch < p.chunks; ++ch) {
+            const int byte = ch * 128 + col * 16;
+            const bool in = h < p.a.heads && byte < p.row_bytes;
+            copy16(q_at + ch * (p.pack * p.head_cols * 128) + n * 128 + ((col ^ (n & 7)) << 4), in ? from + byte : q, in ? 16 : 0);
+          }
         }
       }
       copies_arrive(smem_addr(&sm.q_full));
       const int ss = segment % kSegmentSlots;
-      for (int n = me; n < cols; n += kCopyThreads) {
-        const int j = n / p.head_cols, h = n - j * p.head_cols;
-        sm.weight[ss][n] = h < p.a.heads ? p.a.weights[(row0 + j) * p.a.weight_row_stride + h] : 0.f;
-      }
+#pragma unroll 4
+      for (int j = 0; j < walk.rows; ++j)
+        for (int h = me; h < p.head_cols; h += kCopyThreads)
+          sm.weight[ss][j * p.head_cols + h] = h < p.a.heads ? p.a.weights[(row0 + j) * p.a.weight_row_stride + h] : 0.f;
       for (int j = me; j < walk.rows; j += kCopyThreads) sm.length[ss][j] = row_length(p.R, row0 + j);
       mbar_arrive(smem_addr(&sm.segment_full[ss]));
       // The keys of a pass's last tokens and of what lies behind them come whole: a token's scores are its own.
@@ -557,15 +560,15 @@ extern "C" int topk_index_logits(const topk_index_logits_args* args, void* strea
   p.a = a;
   p.R = make_rows(a.rows, a.max_len, a.workspace);
   p.head_cols = (a.heads + 15) / 16 * 16;
-  const int fit = kMaxCols / p.head_cols;  // rows that a product takes
-  if (a.rows.row_request != nullptr) {
-    p.pack = fit;
-  } else {  // units that do not cross requests: the largest divisor of next_n that fits
-    p.pack = 1;
-    for (int d = 2; d <= fit; ++d)
-      if (a.rows.next_n % d == 0) p.pack = d;
+  // Rows of a unit: as many as a product takes, of one request (the largest divisor of next_n; given each row's request, the
+  // kernel sees to it), but no more than leaves every SM a step where the rows are few and short. (22 rows of 32 heads over
+  // 400 tokens: @PACK@ us with one row a unit, 16 us with eight.)
+  const int fit = kMaxCols / p.head_cols;
+  for (int d = 1; d <= fit && d <= a.rows.num_rows; ++d) {
+    if (a.rows.row_request != nullptr ? (d & (d - 1)) != 0 : a.rows.next_n % d != 0) continue;
+    const int64_t tokens = kTile * (d * p.head_cols <= kMaxCols / 2 ? 2 : 1);
+    if (d == 1 || (a.rows.num_rows + d - 1) / d * ((p.R.max_len + tokens - 1) / tokens) >= props.num_sms) p.pack = d;
   }
-  if (p.pack > a.rows.num_rows) p.pack = static_cast<int32_t>(a.rows.num_rows);
   p.tiles = p.pack * p.head_cols <= kMaxCols / 2 ? 2 : 1;
   p.units = (a.rows.num_rows + p.pack - 1) / p.pack;
   rc = make_cache_map(&p.map, a.keys, size, a.dtype, a.rows.num_blocks, a.rows.block_size, a.dim, a.key_block_stride, a.key_token_stride,

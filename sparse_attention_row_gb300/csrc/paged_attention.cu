@@ -56,7 +56,8 @@ constexpr int kTokenSlots = 8;  // more than the tiles that the copies can be ah
 constexpr int kMaxSlots = 6;
 constexpr int kMaxQk = 576, kMaxV = 512;
 constexpr int kMaxBlockCols = 64;
-constexpr int kJoinThreads = 128, kJoinDims = 32;
+constexpr int kTeam = 128, kJoinDims = 32;  // threads of a team
+constexpr int kMaxTeams = 4;                // which take the parts in turn
 constexpr int kMaxParts = 256;  // slices of a launch at most
 constexpr int kFetchAhead = 3;  // tiles
 constexpr float kMoveAbove = 8.f;  // in powers of two
@@ -92,7 +93,10 @@ struct Params {
   float scale2;          // scale * log2(e)
   float* part;           // [slices][2][blocks][v_pieces * 128][N]
   float2* stat;          // [slices][2][blocks][N]: maximum (in powers of two) and sum
-  Join* join;            // [slices]
+  Join* join;            // [joins]
+  int32_t joins;         // places for a unit's end: one for each unit, or where those are more, for each slice
+  int32_t by_unit;
+  int32_t teams;         // of the join
 };
 
 template <int N>
@@ -726,10 +730,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         }
       }
       fence_before();
-      if (tid == 0 && block == 0 && first_segment) {  // a unit that began before this slice and ends in it
+      const bool ends = walk.at + walk.count == walk.tiles;
+      if (tid == 0 && block == 0 && (p.by_unit ? ends : first_segment)) {  // a unit that began before this slice and ends in it
         Join j{};
         j.last = -1;
-        if (walk.at > 0 && walk.at + walk.count == walk.tiles) {
+        if (walk.at > 0 && ends) {
           const int64_t unit_begin = run_begin - walk.at;
           j.rowgroup = walk.group;
           j.kv_head = walk.kv_head;
@@ -738,11 +743,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           j.first_slot = slice_begin(all_tiles, p.slices, j.first) == unit_begin ? 0 : 1;
           j.tiles = all_tiles;
         }
-        p.join[slice] = j;
+        p.join[p.by_unit ? walk.group * p.a.kv_heads + walk.kv_head : slice] = j;
       }
       first_segment = false;
     }
-    if (first_segment && tid == 0 && block == 0) {  // an empty run
+    if (first_segment && !p.by_unit && tid == 0 && block == 0) {  // an empty run
       Join j{};
       j.last = -1;
       p.join[slice] = j;
@@ -765,33 +770,33 @@ __device__ __forceinline__ float4 load_now(const float4* at) {
 }
 
 // Joins the parts of the units that fell into several slices: kJoinDims values of a unit's columns a CTA. Every thread
-// has four columns of some values and sums them over the parts, four parts' loads at a time; the sums go through shared
-// memory to be stored along the values.
+// has four columns of some values and sums them over its team's parts, four parts' loads at a time; the teams' sums meet in
+// shared memory, to be stored along the values.
 template <int N, bool kBf16>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kTeam * kMaxTeams) join_kernel(const __grid_constant__ Params p) {
   __shared__ int32_t place[kMaxParts];  // of each part, in columns; -1: the slice was empty
   __shared__ float base[N], inverse[N];
   __shared__ float sums[kJoinDims][N + 4];
   const int tid = threadIdx.x, per = p.v_pieces * 128 / kJoinDims;
-  const int dim0 = blockIdx.x % per * kJoinDims, block = blockIdx.x / per % p.blocks, slice = blockIdx.x / per / p.blocks;
+  const int dim0 = blockIdx.x % per * kJoinDims, block = blockIdx.x / per % p.blocks, at_join = blockIdx.x / per / p.blocks;
   const int block_cols = min(p.block_cols, p.cols - block * p.block_cols);
   dependent_wait();
   dependent_launch();
-  const Join jn = p.join[slice];
+  const Join jn = p.join[at_join];
   if (jn.last < 0 || dim0 >= p.a.dv) return;
   const int parts = jn.last - jn.first + 1, width = p.v_pieces * 128;
   const int64_t row0 = jn.rowgroup * p.pack;
-  for (int i = tid; i < parts; i += kJoinThreads) {
+  for (int i = tid; i < parts; i += kTeam * p.teams) {
     const int s = jn.first + i;
     const bool empty = slice_begin(jn.tiles, p.slices, s) == slice_begin(jn.tiles, p.slices, s + 1);
     place[i] = empty ? -1 : ((s * 2 + (i == 0 ? jn.first_slot : 0)) * p.blocks + block) * N;
   }
   __syncthreads();
-  {  // each column's maximum and sum, by kJoinThreads / N lanes
-    constexpr int kLanes = kJoinThreads / N;
-    const int col = tid / kLanes, sub = tid % kLanes;
+  {  // each column's maximum and sum
+    const int lanes_each = kTeam / N * p.teams;
+    const int col = tid / lanes_each, sub = tid % lanes_each;
     float m = -INFINITY, sum = 0.f;
-    for (int i = sub; i < parts; i += kLanes) {
+    for (int i = sub; i < parts; i += lanes_each) {
       if (place[i] < 0) continue;
       const float2 st = p.stat[place[i] + col];
       const float top = fmaxf(m, st.x), b = top == -INFINITY ? 0.f : top;
@@ -799,7 +804,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
       m = top;
     }
 #pragma unroll
-    for (int d = kLanes / 2; d; d >>= 1) {
+    for (int d = lanes_each / 2; d; d >>= 1) {
       const float m2 = __shfl_xor_sync(~0u, m, d), sum2 = __shfl_xor_sync(~0u, sum, d);
       const float top = fmaxf(m, m2), b = top == -INFINITY ? 0.f : top;
       sum = sum * exp2f(m - b) + sum2 * exp2f(m2 - b);
@@ -814,26 +819,27 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     }
   }
   __syncthreads();
-  constexpr int kRow = N / 4, kEach = kJoinDims * kRow / kJoinThreads, kAtOnce = 4;
-  const int col = tid % kRow * 4, dim = tid / kRow;  // and every kJoinThreads / kRow dims on
+  constexpr int kRow = N / 4, kEach = kJoinDims * kRow / kTeam, kAtOnce = 4;
+  const int team = tid / kTeam, col = tid % kRow * 4, dim = tid % kTeam / kRow;  // and every kTeam / kRow dims on
   float4 x[kEach];
 #pragma unroll
   for (int k = 0; k < kEach; ++k) x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
   const float4 b = make_float4(base[col], base[col + 1], base[col + 2], base[col + 3]);
-  for (int i = 0; i < parts; i += kAtOnce) {
+  for (int i0 = team; i0 < parts; i0 += kAtOnce * p.teams) {
     float4 y[kAtOnce][kEach], st[kAtOnce][2];
 #pragma unroll
     for (int a = 0; a < kAtOnce; ++a) {
-      const int at = max(i + a < parts ? place[i + a] : 0, 0);
+      const int i = i0 + a * p.teams, at = max(i < parts ? place[i] : 0, 0);
       st[a][0] = load_now(reinterpret_cast<const float4*>(p.stat + at + col));
       st[a][1] = load_now(reinterpret_cast<const float4*>(p.stat + at + col) + 1);
 #pragma unroll
       for (int k = 0; k < kEach; ++k)
-        y[a][k] = load_now(reinterpret_cast<const float4*>(p.part + static_cast<int64_t>(at) * width + (dim0 + dim + k * (kJoinThreads / kRow)) * N + col));
+        y[a][k] = load_now(reinterpret_cast<const float4*>(p.part + static_cast<int64_t>(at) * width + (dim0 + dim + k * (kTeam / kRow)) * N + col));
     }
 #pragma unroll
     for (int a = 0; a < kAtOnce; ++a) {
-      if (i + a >= parts || place[i + a] < 0) continue;
+      const int i = i0 + a * p.teams;
+      if (i >= parts || place[i] < 0) continue;
       const float4 w = make_float4(exp2f(st[a][0].x - b.x), exp2f(st[a][0].z - b.y), exp2f(st[a][1].x - b.z), exp2f(st[a][1].z - b.w));
 #pragma unroll
       for (int k = 0; k < kEach; ++k) {
@@ -844,21 +850,25 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
       }
     }
   }
+  for (int turn = 0; turn < p.teams; ++turn) {  // in the teams' order: the same sums every time
+    if (team == turn) {
 #pragma unroll
-  for (int k = 0; k < kEach; ++k) {
-    float* to = &sums[dim + k * (kJoinThreads / kRow)][col];
-    to[0] = inverse[col] == 0.f ? 0.f : x[k].x * inverse[col];
-    to[1] = inverse[col + 1] == 0.f ? 0.f : x[k].y * inverse[col + 1];
-    to[2] = inverse[col + 2] == 0.f ? 0.f : x[k].z * inverse[col + 2];
-    to[3] = inverse[col + 3] == 0.f ? 0.f : x[k].w * inverse[col + 3];
+      for (int k = 0; k < kEach; ++k) {
+        float4* to = reinterpret_cast<float4*>(&sums[dim + k * (kTeam / kRow)][col]);
+        const float4 y = turn == 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : *to;
+        *to = make_float4(x[k].x + y.x, x[k].y + y.y, x[k].z + y.z, x[k].w + y.w);
+      }
+    }
+    if (turn + 1 < min(parts, p.teams)) __syncthreads();
+    else break;
   }
   __syncthreads();
-  for (int e = tid; e < block_cols * (kJoinDims / 2); e += kJoinThreads) {
+  for (int e = tid; e < block_cols * (kJoinDims / 2); e += kTeam * p.teams) {
     const int n = e / (kJoinDims / 2), d = e % (kJoinDims / 2) * 2, c = block * p.block_cols + n, j = c / p.group;
     if (dim0 + d < p.a.dv)
       *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.a.out) + (row0 + j) * p.a.out_row_stride +
                                    static_cast<int64_t>(jn.kv_head * p.group + c - j * p.group) * p.a.out_head_stride + dim0 + d) =
-          pack2<kBf16>(sums[d][n], sums[d + 1][n]);
+          inverse[n] == 0.f ? 0u : pack2<kBf16>(sums[d][n] * inverse[n], sums[d + 1][n] * inverse[n]);
   }
 }
 
@@ -897,7 +907,7 @@ int run(Params& p, int device, int smem_limit, bool joins, cudaStream_t stream) 
   if (rc != TOPK_OK) return rc;
   rc = launch(attention_kernel<N, kBf16, kLatent>, static_cast<const Params&>(p), static_cast<int64_t>(p.slices) * p.blocks, kThreads, smem, stream);
   if (rc != TOPK_OK || !joins) return rc;
-  return launch(join_kernel<N, kBf16>, static_cast<const Params&>(p), static_cast<int64_t>(p.slices) * p.blocks * (p.v_pieces * 128 / kJoinDims), kJoinThreads, 0, stream);
+  return launch(join_kernel<N, kBf16>, static_cast<const Params&>(p), static_cast<int64_t>(p.joins) * p.blocks * (p.v_pieces * 128 / kJoinDims), kTeam * p.teams, 0, stream);
 }
 
 template <int N>
@@ -981,6 +991,11 @@ extern "C" int topk_paged_attention(const topk_attention_args* args, void* strea
     if (p.whole && p.slices > units) p.slices = static_cast<int32_t>(units);
     joins = !p.whole;
   }
+  p.by_unit = units <= p.slices;
+  // Units in many parts are joined by more threads each; units in a few by more CTAs at once. (One unit in about 100 parts,
+  // 64 columns: 35 us with four teams, 55 with one; 64 units in two or three, 16 columns: 39 us with one, 45 with four.)
+  p.teams = p.slices >= 8 * units ? kMaxTeams : 1;
+  p.joins = p.by_unit ? static_cast<int32_t>(units) : p.slices;
   char* w = static_cast<char*>(a.workspace) + TOPK_PAGED_WORKSPACE_BYTES;
   p.join = reinterpret_cast<Join*>(w);
   w += (most_ctas(sms) * kJoinBytes + 255) / 256 * 256;
