@@ -84,17 +84,17 @@ struct Unit {
     longest = 0;
     request = -1;
     int64_t sum = 0;
-    for (int j0 = 0; j0 < rows; j0 += 8) {  // eight rows' entries on their way at once
-      int32_t n[8];
-      int64_t b[8];
+    for (int j0 = 0; j0 < rows; j0 += 4) {  // four rows' entries on their way at once
+      int32_t n[4];
+      int64_t b[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 4; ++i) {
         const int64_t row = row0 + min(j0 + i, rows - 1);
         n[i] = p.R.lengths[row];
         b[i] = row_request(p.R, row);
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 4; ++i) {
         const int c = j0 + i < rows ? seen_tokens(p.R, n[i], b[i]) : 0;
         if (c == 0) continue;
         longest = max(longest, c);
@@ -162,7 +162,6 @@ struct Walk {
 };
 
 // Where a pass's tokens lie: looked up by the copying warps, and by the summing ones for the scales.
-__device__ __forceinline__ int block_column(const Rows& R, int x) { return R.block_shift >= 0 ? x >> R.block_shift : x / R.block_size; }
 __device__ __forceinline__ int table_entry(const Params& p, const Walk& w, int x) {
   return x < w.longest ? __ldg(p.R.block_table + w.request * p.R.table_stride + block_column(p.R, x)) : 0;
 }

@@ -27,13 +27,18 @@ struct Rows {
   const int32_t* block_table;
   int32_t next_n;
   int32_t block_size;
-  int32_t block_shift;  // log2(block_size), -1 where it is no power of two
+  uint32_t block_mul, block_shift;  // x / block_size = (high word of x * block_mul + x) >> block_shift, 0 <= x < 2^31
   int32_t max_len;
   uint32_t* status;
 };
 
 __device__ __forceinline__ int64_t row_request(const Rows& R, int64_t row) {
   return R.row_request ? static_cast<int64_t>(R.row_request[row]) : row / R.next_n;
+}
+
+// The table's column of a token (division by an invariant, Granlund and Montgomery 1994).
+__device__ __forceinline__ int block_column(const Rows& R, int x) {
+  return static_cast<int>((__umulhi(static_cast<uint32_t>(x), R.block_mul) + static_cast<uint32_t>(x)) >> R.block_shift);
 }
 
 // Tokens that a row sees, from its entry in `lengths` and its request; 0 for a padding row (negative request).
@@ -95,9 +100,8 @@ inline Rows make_rows(const topk_paged_rows& r, int64_t columns, void* workspace
   R.block_table = r.block_table;
   R.next_n = r.next_n;
   R.block_size = r.block_size;
-  R.block_shift = -1;
-  for (int s = 0; s < 31; ++s)
-    if ((1ll << s) == r.block_size) R.block_shift = s;
+  while ((1ull << R.block_shift) < static_cast<uint64_t>(r.block_size)) ++R.block_shift;
+  R.block_mul = static_cast<uint32_t>(((1ull << 32) * ((1ull << R.block_shift) - r.block_size)) / r.block_size + 1);
   const int64_t held = r.max_blocks > INT32_MAX / r.block_size ? INT32_MAX : r.max_blocks * r.block_size;
   R.max_len = static_cast<int32_t>(held < columns ? held : columns);
   R.status = static_cast<uint32_t*>(workspace);

@@ -59,7 +59,6 @@ constexpr int kMaxBlockCols = 64;
 constexpr int kTeam = 128, kJoinDims = 32;  // threads of a team
 constexpr int kMaxTeams = 4;                // which take the parts in turn
 constexpr int kMaxParts = 256;  // slices of a launch at most
-constexpr int kFetchAhead = 3;  // tiles
 constexpr float kMoveAbove = 8.f;  // in powers of two
 
 struct Join {  // what the join kernel has to know of the unit that ends in a slice and began before it
@@ -118,9 +117,11 @@ struct Smem {  // behind the tiles
   uint32_t gave_up;
 };
 
-__device__ __forceinline__ int group_length(const Params& p, int64_t g) {
+// Out of line: seven copies of it in a kernel that is already longer than the instruction caches like cost 3 to 5 % (and
+// fetching tokens into L2 ahead of their copies, which was tried, cost more than it brought).
+static __device__ __noinline__ int group_length(const Params& p, int64_t g) {
   int most = 0;
-#pragma unroll 4
+#pragma unroll 1
   for (int j = 0; j < p.pack; ++j) most = max(most, row_length(p.R, g * p.pack + j));
   return most;
 }
@@ -339,17 +340,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     const uint32_t full = smem_addr(&sm.full[0]), empty = smem_addr(&sm.empty[0]);
     Ring at;
     TokenCopies copies((warp - kSoftmaxWarps) * 32, lane);
-    // Whether the next slot is empty is asked before a piece's copies are issued: the answer of a later question would
-    // wait behind them.
-    bool empty_next = true;
     const auto copy_slot = [&](int first, int bytes, const void* cache) {
-      if (!empty_next) mbar_wait(empty + at.slot * 8, at.phase ^ 1, guard);
-      Ring then = at;
-      then.step(p.slots);
-      empty_next = mbar_test(empty + then.slot * 8, then.phase ^ 1);
+      mbar_wait(empty + at.slot * 8, at.phase ^ 1, guard);
       copies.columns(ring + at.slot * kPiece, kChunk, first, bytes, cache);
       copies_arrive(full + at.slot * 8);
-      at = then;
+      at.step(p.slots);
     };
     uint32_t tile = 0, segment = 0;
     for (; walk.left > 0; walk.next(p), ++segment) {
@@ -364,32 +359,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         if (t >= walk.count) return -1;
         return !list ? i : (i < p.a.num_indices ? list[i] : -1);
       };
-      const auto column = [&](int x) { return p.R.block_shift >= 0 ? x >> p.R.block_shift : x / p.R.block_size; };
       const auto table_entry = [&](int x) {
-        return x >= 0 && x < length ? __ldg(p.R.block_table + request * p.R.table_stride + column(x)) : 0;
+        return x >= 0 && x < length ? __ldg(p.R.block_table + request * p.R.table_stride + block_column(p.R, x)) : 0;
       };
       const auto address = [&](const void* cache, int x, int x_block, int64_t block_stride, int64_t token_stride, int64_t head_stride) {
         return static_cast<const char*>(cache) + 2 * (static_cast<int64_t>(x_block) * block_stride +
-                                                      (x - column(x) * p.R.block_size) * token_stride + walk.kv_head * head_stride);
+                                                      (x - block_column(p.R, x) * p.R.block_size) * token_stride + walk.kv_head * head_stride);
       };
       const auto in_cache = [&](int x, int x_block) { return x >= 0 && x < length && x_block >= 0 && x_block < p.R.num_blocks; };
-      // A latent tile's copies wait for an earlier tile to leave the ring. So its tokens are fetched into L2 some tiles
-      // ahead, the blocks of a unit a part of them each.
-      const auto fetch = [&](int x, int x_block) {
-        if (!in_cache(x, x_block)) return;
-        const char* from = address(p.a.k, x, x_block, p.a.k_block_stride, p.a.k_token_stride, p.a.k_head_stride);
-        for (int line = block; line * 64 < p.a.dk; line += p.blocks) asm volatile("prefetch.global.L2 [%0];" ::"l"(from + line * 128));
-      };
       int at_token = listed(0), next_token = listed(1);
-      if constexpr (kLatent) {
-        int x[kFetchAhead - 1], b[kFetchAhead - 1];
-#pragma unroll
-        for (int i = 0; i < kFetchAhead - 1; ++i) x[i] = listed(i + 1);
-#pragma unroll
-        for (int i = 0; i < kFetchAhead - 1; ++i) b[i] = table_entry(x[i]);
-#pragma unroll
-        for (int i = 0; i < kFetchAhead - 1; ++i) fetch(x[i], b[i]);
-      }
       // the segment's queries, zeros past the block's columns and past dk
       mbar_wait(smem_addr(&sm.q_empty), (segment & 1) ^ 1, guard);
       for (int n = me >> 3; n < N; n += kCopyThreads / 8) {
@@ -431,10 +409,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         if constexpr (!kLatent) {
           copies.aim(vp, seen, lane);
           for (int u = 0; u < p.v_pieces; ++u) copy_slot(u * 2 * 128, p.a.dv * 2, p.a.v);
-        }
-        if constexpr (kLatent) {
-          const int x = listed(t + kFetchAhead);
-          fetch(x, table_entry(x));
         }
         at_token = next_token;
         at_block = next_block;
@@ -484,15 +458,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         fence_after();
         if (rest_first) last_dims(false);
         uint32_t q_piece = q_at;
-        bool ready = false;
 #pragma unroll 1
         for (int u = 0; u < whole_pieces; ++u) {
-          if (!ready) mbar_wait(full + at.slot * 8, at.phase, guard);
-          __syncwarp();
+          mbar_wait_warp(full + at.slot * 8, at.phase, guard);
           fence_async();
           const uint32_t slot = at.slot;
           at.step(p.slots);
-          ready = mbar_test(full + at.slot * 8, at.phase);  // the answer comes while the products are issued
           mma16_pair(d, operand(ring + slot * kPiece, 16), kChunk >> 4, operand(q_piece, 16), (N * 128) >> 4, kInst, rest_first || u > 0);
           q_piece += 2 * N * 128;
           if (!kLatent || u >= p.v_pieces) commit(empty + slot * 8);  // keys that are no values are done with
@@ -644,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 #pragma unroll
           for (int i = 0; i < H; ++i) l[i] *= sm.moved[warp][1][i];
           for (int u = 0; u < p.v_pieces; ++u) {
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < H; i += 8) {
               float o[8];
               const uint32_t at = tmem + lanes + u * N + half * H + i;
