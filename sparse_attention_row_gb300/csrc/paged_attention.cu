@@ -109,7 +109,7 @@ struct Smem {  // behind the tiles
   int64_t out_at[2][2][kHalf];  // and where its output lies
   int32_t least[2][2];
   uint64_t full[kMaxSlots], empty[kMaxSlots];
-  uint64_t q_full, q_empty, rest_full[2], rest_empty[2], s_full[2], s_empty[2], p_full[2], o_done[2], token_full[kTokenSlots], all_done[2];
+  uint64_t q_first, q_full, q_empty, rest_full[2], rest_empty[2], s_full[2], s_empty[2], p_full[2], o_done[2], token_full[kTokenSlots], all_done[2];
   int64_t scan[kThreads / 32];
   int64_t start_group, tiles, run_begin, run_end;
   int64_t start_at;
@@ -217,6 +217,28 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   }
 }
 
+// A segment's queries [N][dk] into their K-major tiles, by `threads` threads (a multiple of 8); zeros past the block's columns
+// and past dk.
+template <int N>
+__device__ __noinline__ void copy_queries(const Params& p, uint32_t q_at, int64_t row0, int kv_head, int block, int block_cols, int me,
+                                          int threads) {
+  const int col = me & 7;
+#pragma unroll 1
+  for (int n = me >> 3; n < N; n += threads >> 3) {
+    const int c = block * p.block_cols + n, j = c / p.group;
+    const uint16_t* q = static_cast<const uint16_t*>(p.a.q);
+    const bool real = n < block_cols;
+    if (real) q += (row0 + j) * p.a.q_row_stride + static_cast<int64_t>(kv_head * p.group + c - j * p.group) * p.a.q_head_stride;
+    const uint32_t dst = q_at + n * 128 + ((col ^ (n & 7)) << 4);
+#pragma unroll 3
+    for (int ch = 0; ch < p.k_chunks; ++ch) {
+      const int dim = ch * 64 + col * 8;
+      const bool in = real && dim < p.a.dk;
+      copy16(dst + ch * (N * 128), in ? q + dim : static_cast<const uint16_t*>(p.a.q), in ? 16 : 0);
+    }
+  }
+}
+
 template <int N, bool kBf16, bool kLatent>
 __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ Params p) {
   constexpr int kPlaces = places<kLatent>;
@@ -234,6 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       mbar_init(smem_addr(&sm.full[i]), kCopyThreads);
       mbar_init(smem_addr(&sm.empty[i]), 1);
     }
+    mbar_init(smem_addr(&sm.q_first), kSoftmaxWarps * 32);
     mbar_init(smem_addr(&sm.q_full), kCopyThreads);
     mbar_init(smem_addr(&sm.q_empty), 1);
     for (int i = 0; i < 2; ++i) {
@@ -334,9 +357,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   const uint32_t s_cols = static_cast<uint32_t>(p.v_pieces) * N;  // columns before the scores'
   const int block_cols = min(p.block_cols, p.cols - block * p.block_cols);
 
+  // the first segment's queries, by the warps that have nothing to do yet
+  if (walk.left > 0 && warp < kSoftmaxWarps) {
+    copy_queries<N>(p, q_at, walk.group * p.pack, walk.kv_head, block, block_cols, tid, kSoftmaxWarps * 32);
+    copies_arrive(smem_addr(&sm.q_first));
+  }
   if (warp >= kSoftmaxWarps && warp < kScoreWarp) {
     // ---- copies -----------------------------------------------------------
-    const int me = tid - kSoftmaxWarps * 32, col = lane & 7;  // a thread's token of a tile: `me`
+    const int me = tid - kSoftmaxWarps * 32;  // a thread's token of a tile
     const uint32_t full = smem_addr(&sm.full[0]), empty = smem_addr(&sm.empty[0]);
     Ring at;
     TokenCopies copies((warp - kSoftmaxWarps) * 32, lane);
@@ -368,22 +396,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       };
       const auto in_cache = [&](int x, int x_block) { return x >= 0 && x < length && x_block >= 0 && x_block < p.R.num_blocks; };
       int at_token = listed(0), next_token = listed(1);
-      // the segment's queries, zeros past the block's columns and past dk
-      mbar_wait(smem_addr(&sm.q_empty), (segment & 1) ^ 1, guard);
-      for (int n = me >> 3; n < N; n += kCopyThreads / 8) {
-        const int c = block * p.block_cols + n, j = c / p.group;
-        const uint16_t* q = static_cast<const uint16_t*>(p.a.q);
-        const bool real = n < block_cols;
-        if (real) q += (row0 + j) * p.a.q_row_stride + static_cast<int64_t>(walk.kv_head * p.group + c - j * p.group) * p.a.q_head_stride;
-        const uint32_t dst = q_at + n * 128 + ((col ^ (n & 7)) << 4);
-        for (int ch = 0; ch < p.k_chunks; ++ch) {
-          const int dim = ch * 64 + col * 8;
-          const bool in = real && dim < p.a.dk;
-          copy16(dst + ch * (N * 128), in ? q + dim : static_cast<const uint16_t*>(p.a.q), in ? 16 : 0);
-        }
-      }
-      copies_arrive(smem_addr(&sm.q_full));
       int at_block = table_entry(at_token);
+      asm volatile("" ::"r"(at_block) : "memory");  // here, before any copies are issued: a load waits behind those
+      if (segment > 0) {  // the first one's are copied by the softmax warps
+        mbar_wait(smem_addr(&sm.q_empty), (segment & 1) ^ 1, guard);
+        copy_queries<N>(p, q_at, row0, walk.kv_head, block, block_cols, me, kCopyThreads);
+        copies_arrive(smem_addr(&sm.q_full));
+      }
       for (int t = 0; t < walk.count; ++t, ++tile) {
         const bool seen = in_cache(at_token, at_block);
         if (!seen && at_token >= 0 && at_token < length) atomicOr(p.R.status, TOPK_DEV_BAD_BLOCK);
@@ -425,7 +444,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     Ring at;
     uint32_t tile = 0, segment = 0;
     for (; walk.left > 0; walk.next(p), ++segment) {
-      mbar_wait_warp(smem_addr(&sm.q_full), segment & 1, guard);
+      if (segment == 0)
+        mbar_wait_warp(smem_addr(&sm.q_first), 0, guard);
+      else
+        mbar_wait_warp(smem_addr(&sm.q_full), (segment & 1) ^ 1, guard);
       fence_async();
 #pragma unroll 1
       for (int t = 0; t < walk.count; ++t, ++tile) {
@@ -656,7 +678,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       for (int w = 0; w < 4; ++w) sum += sm.column_sum[half][w][lane & (H - 1)];
       const bool whole = walk.count == walk.tiles;
       const int64_t slot = ((static_cast<int64_t>(slice) * 2 + (first_segment ? 0 : 1)) * p.blocks + block) * N;
-      if (lane < H) sm.moved[warp][0][lane] = sum == 0.f ? 0.f : (whole ? 1.f / sum : 1.f);
+      const float inverse = sum == 0.f ? 0.f : 1.f / sum;
+      const bool blank = __any_sync(~0u, sum == 0.f);  // some column saw nothing: its values are zeros, whatever stands in O
+      if (lane < H) sm.moved[warp][0][lane] = inverse;
       if (quarter == 0 && lane < H) {
         if (!whole) {
           p.stat[slot + my_col] = make_float2(m == -INFINITY ? -INFINITY : in_use, sum);
@@ -676,27 +700,27 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         tmem_load(tmem + lanes + u * N + half * H, o);
         load_wait(o);
         const int dim = u * 128 + token;
+        if (blank) {
 #pragma unroll
-        for (int i = 0; i < H; i += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(&sm.moved[warp][0][i]);
-          o[i] = f.x == 0.f ? 0.f : o[i] * f.x;
-          o[i + 1] = f.y == 0.f ? 0.f : o[i + 1] * f.y;
-          o[i + 2] = f.z == 0.f ? 0.f : o[i + 2] * f.z;
-          o[i + 3] = f.w == 0.f ? 0.f : o[i + 3] * f.w;
+          for (int i = 0; i < H; ++i)
+            if (sm.moved[warp][0][i] == 0.f) o[i] = 0.f;
         }
         if (!whole) {  // [dim][column]: a thread's columns side by side
           float4* to = reinterpret_cast<float4*>(p.part + slot * (p.v_pieces * 128) + dim * N + half * H);
 #pragma unroll
           for (int i = 0; i < H; i += 4) to[i / 4] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
         } else {
-          // two columns at a time: neighbouring lanes exchange values and store pairs of dims
+          // two columns at a time: neighbouring lanes exchange them and store pairs of dims
           const int odd = lane & 1, d = dim - odd, real = d < p.a.dv ? block_cols - half * H - odd : 0;
           const int64_t* out_at = sm.out_at[segment & 1][half] + odd;
           uint16_t* out = static_cast<uint16_t*>(p.a.out) + d;
 #pragma unroll
           for (int i = 0; i < H; i += 2) {
-            const float other = __shfl_xor_sync(~0u, odd ? o[i] : o[i + 1], 1);
-            if (i < real) *reinterpret_cast<uint32_t*>(out + out_at[i]) = odd ? pack2<kBf16>(other, o[i + 1]) : pack2<kBf16>(o[i], other);
+            const float2 f = *reinterpret_cast<const float2*>(&sm.moved[warp][0][i]);
+            const uint32_t mine = pack2<kBf16>(o[i] * f.x, o[i + 1] * f.y), other = __shfl_xor_sync(~0u, mine, 1);
+            // the even lane has this column of both dims, the odd lane the next one
+            const uint32_t both = odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
+            if (i < real) *reinterpret_cast<uint32_t*>(out + out_at[i]) = both;
           }
         }
       }
