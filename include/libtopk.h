@@ -401,6 +401,10 @@ typedef struct {
  * lies outside the cache scores -inf (TOPK_DEV_BAD_BLOCK).
  * heads 1..128, dim 8..128 (multiples of 8; of 16 for 8-bit types). q and keys are
  * read in pieces of 16 bytes: their addresses and strides are multiples of that.
+ * Any block_size is taken; keys stream fastest where it is a multiple of 64, and
+ * about four times slower where it is none of 8. TOPK_ERR_UNSUPPORTED also where the
+ * strides of keys are negative, or so small a common divisor apart that the cache has
+ * 2^31 rows of it.
  */
 typedef struct {
   topk_paged_rows rows;

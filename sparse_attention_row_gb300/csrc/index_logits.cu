@@ -10,9 +10,7 @@
 // that the weighted sum over the heads is one thread's own: no exchange at all.
 // A step is two such tiles where N <= 128 and one where it is more: 256 columns of
 // tensor memory, of which there are two places, so that one step's sums run while the
-// next is multiplied. (One tile a step, and half as many warps for the sums: what a
-// step costs beside its data, 1700 to 2000 cycles of waits and hand-overs, was all that
-// the batch over 8-bit keys took.)
+// next is multiplied.
 //
 // The units' steps are dealt in equal runs to the CTAs, one on each SM; every CTA
 // sums up the rows' steps to find its run. Rows are independent over the tokens,
@@ -22,6 +20,15 @@
 // pages are no multiples of 8 tokens) the keys by TMA into a ring of steps (cache_map.cuh), a
 // warp issues the products, four groups of 4 warps sum: two a step, which take a
 // tile each, or half of the rows of the one.
+//
+// What bounds it. Decoding reads every key once: 32 requests of two rows of 64 heads
+// over 100 K to 160 K tokens take 174 us (6.3 TB/s, bf16), 64 rows over 8 K to 32 K
+// 8-bit keys 39 us (4.6 TB/s: a step of 32 KB costs some 1400 cycles of hand-overs between
+// its warps, about what its data takes). A prompt's piece is bounded by the sums: one maximum
+// and half a fused multiply-add a token, row and head, 512 rows of 64 heads over 16 K
+// tokens in 126 us (1070 TFLOP/s). All of it depends on short loops: each spilled register
+// and each unrolled look-up in them showed (8-bit keys: 57 us with 80 registers a thread, 42
+// with 96).
 #include "cache_map.cuh"
 #include "paged.cuh"
 #include "umma.cuh"
@@ -561,7 +568,7 @@ extern "C" int topk_index_logits(const topk_index_logits_args* args, void* strea
   p.head_cols = (a.heads + 15) / 16 * 16;
   // Rows of a unit: as many as a product takes, of one request (the largest divisor of next_n; given each row's request, the
   // kernel sees to it), but no more than leaves every SM a step where the rows are few and short. (22 rows of 32 heads over
-  // 400 tokens: @PACK@ us with one row a unit, 16 us with eight.)
+  // 400 tokens: 9 us with one row a unit, 16 us with eight.)
   const int fit = kMaxCols / p.head_cols;
   for (int d = 1; d <= fit && d <= a.rows.num_rows; ++d) {
     if (a.rows.row_request != nullptr ? (d & (d - 1)) != 0 : a.rows.next_n % d != 0) continue;

@@ -22,15 +22,28 @@
 // run. With more than 64 columns, neighbouring CTAs take the column blocks of one
 // run and meet its tokens in L2.
 //
-// Roles in a CTA (13 warps): 4 copy tokens into a ring of 32 KB pieces (128
+// Roles in a CTA (14 warps): 4 copy tokens into a ring of 32 KB pieces (128
 // tokens x 128 dims) with 16-byte asynchronous copies, which take any page size,
 // stride and index list and write zeros for what is masked (whatever the cache
-// holds there); 1 thread issues the products; 8 warps do the softmax, a thread
-// per token and half of the columns. A column's maximum runs over the tokens,
-// that is over threads: a butterfly of shuffles in each warp, then four
-// numbers per column through shared memory. The maximum in use is moved only
-// when a tile's exceeds it by 2^8, which leaves the sums exact in fp32 and
-// spares nearly every rescaling of O^T in tensor memory.
+// holds there); one warp issues the scores' products and one the values'; 8 warps do
+// the softmax, a thread per token and half of the columns. A column's maximum
+// runs over the tokens, that is over threads: a butterfly of shuffles in each
+// warp, then four numbers per column through shared memory. It is taken for a
+// unit's first tile, and later only where a probability comes out above 2^8: then the
+// maximum in use is moved, and the sums and O^T are scaled. Everything is held in fp32
+// but P, which is rounded to the input type for the second product (for fp16, scaled
+// by 2^7, so that small probabilities keep their bits).
+//
+// What bounds it. Grouped heads read every byte once: 64 rows of 32 heads over 4
+// key-value heads and 8 K to 32 K tokens run at the speed of the memory (375 us, 7.1 TB/s).
+// Latent attention reads shared memory: a tile's products at N = 64 read 555 KB there at
+// 128 bytes a cycle, 48 to 50 cycles an instruction (39 to 42 at N = 16), and its copies
+// write 147 KB at 72 bytes a cycle, 5400 cycles a tile; a tile takes about 6000, since tiles of
+// 72 KB of keys and a queries' block of the same size leave no room for two: 1024 rows of
+// 64 heads over 2048 tokens each take 365 us (800 TFLOP/s). Tiles of 64 tokens, of which
+// two fit, took 540: the products read more a token, and two tiles' copies and products
+// meet in shared memory all the time. N = 16 is bounded the same way by the copies and the
+// waits between a tile's steps: 64 rows of 16 heads over 1024 scattered tokens take 30 us.
 #include "paged.cuh"
 #include "token_copies.cuh"
 #include "umma.cuh"
