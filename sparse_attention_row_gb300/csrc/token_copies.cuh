@@ -20,7 +20,8 @@ struct TokenCopies {
   uint32_t seen;   // bit i: from[i] is to be read
   uint32_t to[2];  // place in the tile of the even and odd instructions, whose tokens differ by four
   int byte;        // of a 128-byte row
-  __device__ TokenCopies(int first_token, int lane) : seen(0) {
+  bool all;        // every one of the warp's tokens is to be read
+  __device__ TokenCopies(int first_token, int lane) : seen(0), all(false) {
     const int token = first_token + (lane >> 3), col = lane & 7;
     byte = col * 16;
     to[0] = token * 128 + ((col ^ (token & 7)) << 4);
@@ -28,19 +29,30 @@ struct TokenCopies {
   }
   // Each lane brings the address of a token, lane by lane in the order of the tile.
   __device__ __forceinline__ void aim(const char* mine, bool on, int lane) {
-    const unsigned all = __ballot_sync(~0u, on);
+    const unsigned who = __ballot_sync(~0u, on);
+    all = who == ~0u;
     seen = 0;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
       const int lane_from = i * 4 + (lane >> 3);
       from[i] = reinterpret_cast<const char*>(__shfl_sync(~0u, reinterpret_cast<uint64_t>(mine), lane_from)) + byte;
-      seen |= ((all >> lane_from) & 1) << i;
+      seen |= ((who >> lane_from) & 1) << i;
     }
   }
   // Up to 256 bytes of each token from `first` on, a token having `bytes` in all: 128-byte columns (swizzled
   // tiles, `column` bytes apart), the last one filled up with zeros.
   __device__ __forceinline__ void columns(uint32_t dst, uint32_t column, int first, int bytes, const void* anywhere) const {
+    if (all && first + kColumns * 128 <= bytes) {  // nearly always: no selections, a third of the instructions
+      const uint32_t even = dst + to[0], odd = dst + to[1];
 #pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const char* at = from[i] + first;
+#pragma unroll
+        for (int c = 0; c < kColumns; ++c) umma::copy16((i & 1 ? odd : even) + c * column + (i >> 1) * 1024, at + c * 128, 16);
+      }
+      return;
+    }
+#pragma unroll 1
     for (int c = 0; c < kColumns; ++c) {
       if (first + c * 128 >= bytes) break;
       const bool in = first + c * 128 + byte < bytes;

@@ -97,7 +97,7 @@ __device__ __forceinline__ void mbar_wait_warp(uint32_t bar, uint32_t parity, co
 
 // 16 bytes into shared memory; `bytes` 0 writes zeros and reads nothing.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
 // One arrival on `bar` when every copy that this thread has begun has landed.
