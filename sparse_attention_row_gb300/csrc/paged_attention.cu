@@ -665,8 +665,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         }
         // the product that read this place of P is done
         if (tile >= kPlaces) mbar_wait(smem_addr(&sm.o_done[(tile - kPlaces) & 1]), ((tile - kPlaces) >> 1) & 1, guard);
-#pragma unroll
-        for (int i = 0; i < H; ++i) l[i] += s[i];
         const uint32_t row = p_at + (kPlaces == 2 ? (tile & 1) * kChunk : 0) + token * 128;
         {
 #pragma unroll
@@ -682,6 +680,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sm.p_full[tile & 1]));
+#pragma unroll
+        for (int i = 0; i < H; ++i) l[i] += s[i];
       }
       const float part_l = reduce_columns<H, false>(l, lane);
       if (lane < H) sm.column_sum[half][quarter][lane] = part_l;
