@@ -35,15 +35,16 @@
 // by 2^7, so that small probabilities keep their bits).
 //
 // What bounds it. Grouped heads read every byte once: 64 rows of 32 heads over 4
-// key-value heads and 8 K to 32 K tokens run at the speed of the memory (375 us, 7.1 TB/s).
-// Latent attention reads shared memory: a tile's products at N = 64 read 555 KB there at
-// 128 bytes a cycle, 48 to 50 cycles an instruction (39 to 42 at N = 16), and its copies
-// write 147 KB at 72 bytes a cycle, 5400 cycles a tile; a tile takes about 6000, since tiles of
-// 72 KB of keys and a queries' block of the same size leave no room for two: 1024 rows of
-// 64 heads over 2048 tokens each take 365 us (800 TFLOP/s). Tiles of 64 tokens, of which
-// two fit, took 540: the products read more a token, and two tiles' copies and products
-// meet in shared memory all the time. N = 16 is bounded the same way by the copies and the
-// waits between a tile's steps: 64 rows of 16 heads over 1024 scattered tokens take 30 us.
+// key-value heads and 8 K to 32 K tokens run at the speed of the memory (370 to 380 us, 7.1
+// TB/s). Latent attention is bounded by the chain of a tile's steps. Its 147 KB of keys and
+// 64 columns' queries fill shared memory, so the next tile's keys can only come while this
+// one's values are multiplied and leave the ring: at N = 64 some 1850 cycles for the values'
+// products, 1500 until the last keys are there, 950 for the scores that wait for them and
+// 1150 for the softmax, 6000 in all, of which the products read shared memory for 3260 (48 to
+// 50 cycles an instruction, 39 to 42 at N = 16). 1024 rows of 64 heads over 2048 tokens each
+// take 365 us (800 TFLOP/s), 64 rows of 128 heads over 2048 of 8 K to 32 K tokens 63 us. Tiles of
+// 64 tokens, of which two fit, were slower (540 and 90 us): their products read more shared
+// memory a token, and copies and products meet there all the time.
 #include "paged.cuh"
 #include "token_copies.cuh"
 #include "umma.cuh"
