@@ -275,7 +275,7 @@ def test_latent(dec, dtype, heads, topk, block):
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("heads, kv_heads, dk, dv", [(32, 4, 128, 128), (8, 8, 64, 64), (8, 2, 256, 256), (6, 2, 80, 96), (64, 1, 192, 128), (71, 1, 64, 64),
-                                                     (24, 3, 8, 8), (48, 4, 128, 64), (256, 2, 128, 128), (12, 4, 512, 512), (5, 1, 576, 256)])
+                                                     (24, 3, 8, 8), (48, 4, 128, 64), (256, 2, 128, 128), (12, 4, 512, 512), (5, 1, 576, 256), (64, 1, 576, 512), (40, 1, 520, 320)])
 def test_grouped(dec, dtype, heads, kv_heads, dk, dv):
     case = attention_case(heads + dk, LENGTHS, 1, heads, kv_heads, dk, dv, False, dtype, 16)
     check_attention(dec, LENGTHS, case, 1, dv, 16)
