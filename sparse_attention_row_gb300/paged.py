@@ -125,15 +125,10 @@ class PagedDecoder:
         table = self._matrix("block_table", block_table, self._i32, n)
         columns = block_table.shape[1]
         free = free_blocks.numel()
-        if out is None:
-            # one allocation: the int64 slots first, then the int32 lists
-            words = self._empty(2 * max_tokens + max_tokens + max_tokens + n + 1, self._i32, stream)
-            slots, lens, request, start = words.split_with_sizes((2 * max_tokens, max_tokens, max_tokens, n + 1))
-            out = KvMap(slots.view(self._i64), lens, request, start)
-            slots_ptr = words.data_ptr()
-            lens_ptr = slots_ptr + 8 * max_tokens
-            request_ptr = lens_ptr + 4 * max_tokens
-            start_ptr = request_ptr + 4 * max_tokens
+        if out is None:  # four allocations, 6 us of host time; one, cut into views, takes 10
+            out = KvMap(self._empty(max_tokens, self._i64, stream), self._empty(max_tokens, self._i32, stream),
+                        self._empty(max_tokens, self._i32, stream), self._empty(n + 1, self._i32, stream))
+            slots_ptr, lens_ptr, request_ptr, start_ptr = (x.data_ptr() for x in out)
         else:
             slots = out.slots
             if slots.dtype is not self._i64 or slots.dim() != 1 or slots.numel() != max_tokens or slots.get_device() != self.device or not slots.is_contiguous():
