@@ -76,7 +76,7 @@ struct Smem {
   uint32_t tmem, gave_up;
 };
 
-__device__ __forceinline__ int steps_of(const Params& p, int length) { return (length + p.tiles * kTile - 1) / (p.tiles * kTile); }
+__device__ __forceinline__ int steps_of(const Params& p, int length) { return static_cast<int>((length + (p.tiles * kTile - 1u)) / (p.tiles * kTile)); }
 
 // The rows of a unit: whether those that see anything have one request, and the unit's steps.
 struct Unit {

@@ -33,7 +33,7 @@ struct Rows {
 };
 
 __device__ __forceinline__ int64_t row_request(const Rows& R, int64_t row) {
-  return R.row_request ? static_cast<int64_t>(R.row_request[row]) : row / R.next_n;
+  return R.row_request ? static_cast<int64_t>(R.row_request[row]) : static_cast<uint32_t>(row) / static_cast<uint32_t>(R.next_n);  // rows are below 2^31
 }
 
 // The table's column of a token (division by an invariant, Granlund and Montgomery 1994).

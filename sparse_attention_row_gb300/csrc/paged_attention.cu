@@ -42,7 +42,7 @@
 // products, 1500 until the last keys are there, 950 for the scores that wait for them and
 // 1150 for the softmax, 6000 in all, of which the products read shared memory for 3260 (48 to
 // 50 cycles an instruction, 39 to 42 at N = 16). 1024 rows of 64 heads over 2048 tokens each
-// take 365 us (800 TFLOP/s), 64 rows of 128 heads over 2048 of 8 K to 32 K tokens 63 us. Tiles of
+// take 365 us (800 TFLOP/s), 64 rows of 128 heads over 2048 of 8 K to 32 K tokens 64 us. Tiles of
 // 64 tokens, of which two fit, were slower (540 and 90 us): their products read more shared
 // memory a token, and copies and products meet there all the time.
 #include "paged.cuh"
@@ -115,13 +115,12 @@ struct Params {
 template <int N>
 struct Smem {  // behind the tiles
   static constexpr int kHalf = N / 2;
-  int32_t token[kTokenSlots][128];  // position of each token of a tile, INT_MAX where nothing is to be seen
+  int32_t seen_by[kTokenSlots][128];  // of each token of a tile: a row of the group, kEveryRow, or kNoRow
   float column_max[2][4][kHalf];      // [half][warp]; a barrier stands between one tile's reads and the next one's writes
   float moved[kSoftmaxWarps][2][kHalf];  // maximum in use, factor of the old sums
   float column_sum[2][4][kHalf];
-  int32_t limit[2][2][kHalf];  // [parity of the segment][half]: tokens that a column sees
+  int32_t row_of[2][2][kHalf];  // [parity of the segment][half]: a column's row in the group, or kSeesNothing
   int64_t out_at[2][2][kHalf];  // and where its output lies
-  int32_t least[2][2];
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t q_first, q_full, q_empty, rest_full[2], rest_empty[2], s_full[2], s_empty[2], p_full[2], o_done[2], token_full[kTokenSlots], all_done[2];
   int64_t scan[kThreads / 32];
@@ -131,20 +130,64 @@ struct Smem {  // behind the tiles
   uint32_t gave_up;
 };
 
-// Out of line: seven copies of it in a kernel that is already longer than the instruction caches like cost 3 to 5 % (and
-// fetching tokens into L2 ahead of their copies, which was tried, cost more than it brought).
-static __device__ __noinline__ int group_length(const Params& p, int64_t g) {
-  int most = 0;
-#pragma unroll 1
-  for (int j = 0; j < p.pack; ++j) most = max(most, row_length(p.R, g * p.pack + j));
-  return most;
+__device__ __forceinline__ int length_in_group(const Params& p, int64_t g, int j) {
+  if (p.pack == 1) return row_length(p.R, g);
+  const int32_t n = p.R.lengths[g * p.pack + j];  // the request is the group's number, and within the table
+  return n < 0 ? 0 : (n > p.R.max_len ? p.R.max_len : n);
 }
 
-// Tiles of a unit; one at least, so that every unit is met and its rows written.
-__device__ __forceinline__ int group_tiles(const Params& p, int64_t g) {
-  if (p.row_tiles) return p.row_tiles;
-  const int n = group_length(p, g);
-  return n == 0 ? 1 : static_cast<int>((n + kTile - 1u) / kTile);
+__device__ __forceinline__ int tiles_for(int tokens) { return static_cast<int>((tokens + (kTile - 1u)) / kTile); }
+
+// A unit's tiles. Rows whose lengths differ share those tiles that all of them see whole (rows that see nothing aside: their
+// sums are dropped). From there on every row has tiles of its own, in which the others' columns are masked and
+// tokens that only others see are zeros: a probability of zero does not keep a NaN or an infinity of theirs out of a
+// product. That is a tile or two more a row of a group. The functions on groups are out of line: seven copies in a kernel that
+// is already longer than the instruction caches like cost 3 to 5 % (and fetching tokens into L2 ahead of their copies, which
+// was tried, cost more than it brought).
+struct GroupSize {
+  int most;    // tokens of the longest row
+  int common;  // tiles that its rows share
+  int tiles;   // in all; one at least, so that every unit is met and its rows written
+};
+static __device__ __noinline__ GroupSize group_size(const Params& p, int64_t g) {
+  int most = 0, least = INT_MAX, own = 0, some = 0;
+#pragma unroll 1
+  for (int j = 0; j < p.pack; ++j) {
+    const int n = length_in_group(p, g, j);
+    if (n == 0) continue;
+    most = max(most, n);
+    least = min(least, n);
+    own += tiles_for(n);
+    ++some;
+  }
+  GroupSize x;
+  x.most = most;
+  x.common = least >= most ? tiles_for(most) : least / kTile;
+  x.tiles = least >= most ? max(x.common, 1) : own - (some - 1) * x.common;
+  return x;
+}
+
+__device__ __forceinline__ int group_tiles(const Params& p, int64_t g) { return p.row_tiles ? p.row_tiles : group_size(p, g).tiles; }
+
+// The tiles from a unit's number `at` on that the same rows see.
+constexpr int kEveryRow = -1, kNoRow = INT_MAX, kSeesNothing = -2;
+struct Pass {
+  int tile, end;  // of the tokens
+  int limit;      // tokens seen
+  int who;        // the group's row that sees them, or kEveryRow
+};
+static __device__ __noinline__ Pass find_pass(const Params& p, int64_t g, int at) {
+  const GroupSize size = group_size(p, g);
+  if (at < size.common) return {at, size.common, size.most, kEveryRow};
+  at -= size.common;
+#pragma unroll 1
+  for (int j = 0; j < p.pack; ++j) {
+    const int n = length_in_group(p, g, j), own = tiles_for(n) - size.common;
+    if (own <= 0) continue;
+    if (at < own) return {size.common + at, size.common + own, n, j};
+    at -= own;
+  }
+  return {0, 1, 0, kEveryRow};  // no row sees anything
 }
 
 // First tile of slice s, and the slice of tile x; in 32 bits where the products fit (a 64-bit division takes some
@@ -391,15 +434,19 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     uint32_t tile = 0, segment = 0;
     for (; walk.left > 0; walk.next(p), ++segment) {
       const int64_t row0 = walk.group * p.pack;
-      const int length = group_length(p, walk.group);
+      const int length = p.pack == 1 ? row_length(p.R, row0) : group_size(p, walk.group).most;
       const int64_t request = length > 0 ? row_request(p.R, row0) : 0;
       const int32_t* list = p.a.indices ? p.a.indices + row0 * p.a.index_row_stride : nullptr;
       // A tile's tokens are found in two steps, each a tile earlier than its result is used: the position (from
       // the list), then the block (from the table).
-      const auto listed = [&](int t) {
-        const int i = (walk.at + t) * kTile + me;
+      Pass pass{walk.at, p.pack == 1 ? INT_MAX : walk.at, list ? p.a.num_indices : length, kEveryRow};
+      const auto listed = [&](int t, int* who) {  // for t = 0, 1, 2, ...
         if (t >= walk.count) return -1;
-        return !list ? i : (i < p.a.num_indices ? list[i] : -1);
+        if (pass.tile == pass.end) pass = find_pass(p, walk.group, walk.at + t);
+        *who = pass.who;
+        const int i = pass.tile++ * kTile + me;
+        if (i >= pass.limit) return -1;
+        return list ? list[i] : i;
       };
       const auto table_entry = [&](int x) {
         return x >= 0 && x < length ? __ldg(p.R.block_table + request * p.R.table_stride + block_column(p.R, x)) : 0;
@@ -409,7 +456,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                                                       (x - block_column(p.R, x) * p.R.block_size) * token_stride + walk.kv_head * head_stride);
       };
       const auto in_cache = [&](int x, int x_block) { return x >= 0 && x < length && x_block >= 0 && x_block < p.R.num_blocks; };
-      int at_token = listed(0), next_token = listed(1);
+      int at_who = kEveryRow, next_who = kEveryRow, later_who = kEveryRow;
+      int at_token = listed(0, &at_who), next_token = listed(1, &next_who);
       int at_block = table_entry(at_token);
       asm volatile("" ::"r"(at_block) : "memory");  // here, before any copies are issued: a load waits behind those
       if (segment > 0) {  // the first one's are copied by the softmax warps
@@ -420,14 +468,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       for (int t = 0; t < walk.count; ++t, ++tile) {
         const bool seen = in_cache(at_token, at_block);
         if (!seen && at_token >= 0 && at_token < length) atomicOr(p.R.status, TOPK_DEV_BAD_BLOCK);
-        sm.token[tile % kTokenSlots][me] = seen ? at_token : INT_MAX;
+        sm.seen_by[tile % kTokenSlots][me] = seen ? at_who : kNoRow;
         mbar_arrive(smem_addr(&sm.token_full[tile % kTokenSlots]));
         const char *kp = static_cast<const char*>(p.a.k), *vp = static_cast<const char*>(p.a.v);
         if (seen) {
           kp = address(kp, at_token, at_block, p.a.k_block_stride, p.a.k_token_stride, p.a.k_head_stride);
           if (!kLatent) vp = address(vp, at_token, at_block, p.a.v_block_stride, p.a.v_token_stride, p.a.v_head_stride);
         }
-        const int next_block = table_entry(next_token), later_token = listed(t + 2);
+        const int next_block = table_entry(next_token), later_token = listed(t + 2, &later_who);
         copies.aim(kp, seen, lane);
         const auto copy_rest = [&]() {
           const uint32_t b = tile & 1, before = tile - kPlaces;  // the tile that had this place
@@ -446,6 +494,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         at_token = next_token;
         at_block = next_block;
         next_token = later_token;
+        at_who = next_who;
+        next_who = later_who;
       }
     }
     copies_wait_all();
@@ -555,23 +605,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     bool first_segment = true;
     for (; walk.left > 0; walk.next(p), ++segment) {
       const int64_t row0 = walk.group * p.pack;
-      if (quarter == 0) {  // what each column sees
+      if (quarter == 0 && lane < H) {  // whose each column is
         const int c = block * p.block_cols + my_col;
-        int n = INT_MAX;
+        int row = kSeesNothing;
         if (my_col < block_cols) {
           const int j = c / p.group;
-          n = row_length(p.R, row0 + j);
-          if (lane < H)
-            sm.out_at[segment & 1][half][lane] = (row0 + j) * p.a.out_row_stride + static_cast<int64_t>(walk.kv_head * p.group + c - j * p.group) * p.a.out_head_stride;
+          if (length_in_group(p, walk.group, j) > 0) row = j;
+          sm.out_at[segment & 1][half][lane] = (row0 + j) * p.a.out_row_stride + static_cast<int64_t>(walk.kv_head * p.group + c - j * p.group) * p.a.out_head_stride;
         }
-        int least = n;
-#pragma unroll
-        for (int d = 16; d; d >>= 1) least = min(least, __shfl_xor_sync(~0u, least, d));
-        if (lane < H) sm.limit[segment & 1][half][lane] = n == INT_MAX ? 0 : n;
-        if (lane == 0) sm.least[segment & 1][half] = least;
+        sm.row_of[segment & 1][half][lane] = row;
       }
       named_sync(1 + half, 128);
-      const int least = sm.least[segment & 1][half];
       // of my_col, in powers of two: its maximum when that last moved, and what is taken off its scores; below every score
       // until a finite one has come
       float m = -INFINITY, in_use = -1e30f;
@@ -580,17 +624,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       for (int i = 0; i < H; ++i) l[i] = 0.f;
       for (int t = 0; t < walk.count; ++t, ++tile) {
         mbar_wait(smem_addr(&sm.token_full[tile % kTokenSlots]), (tile / kTokenSlots) & 1, guard);
-        const int pos = sm.token[tile % kTokenSlots][token];
+        const int who = sm.seen_by[tile % kTokenSlots][token];
         mbar_wait(smem_addr(&sm.s_full[tile & 1]), (tile >> 1) & 1, guard);
         fence_after();
         float s[H];
         tmem_load(tmem + lanes + s_cols + (tile & 1) * N + half * H, s);
         load_wait(s);
         const auto mask = [&]() {
-          if (pos >= least) {
+          if (who != kEveryRow) {
 #pragma unroll
             for (int i = 0; i < H; ++i)
-              if (pos >= sm.limit[segment & 1][half][i]) s[i] = -INFINITY;
+              if (who != sm.row_of[segment & 1][half][i]) s[i] = -INFINITY;
           }
         };
         const auto probabilities = [&]() {
@@ -690,6 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       float sum = 0.f;
 #pragma unroll
       for (int w = 0; w < 4; ++w) sum += sm.column_sum[half][w][lane & (H - 1)];
+      if (sm.row_of[segment & 1][half][lane & (H - 1)] == kSeesNothing) sum = 0.f, m = -INFINITY;
       const bool whole = walk.count == walk.tiles;
       const int64_t slot = ((static_cast<int64_t>(slice) * 2 + (first_segment ? 0 : 1)) * p.blocks + block) * N;
       const float inverse = sum == 0.f ? 0.f : 1.f / sum;
@@ -971,8 +1016,11 @@ extern "C" int topk_paged_attention(const topk_attention_args* args, void* strea
   p.a = a;
   p.R = make_rows(a.rows, INT32_MAX, a.workspace);
   p.group = a.heads / a.kv_heads;
-  // the rows of a request share its tokens, unless index lists tell them apart
-  p.pack = a.indices == nullptr && a.rows.row_request == nullptr && a.rows.next_n * static_cast<int64_t>(p.group) <= 1024 ? a.rows.next_n : 1;
+  // The rows of a request share its tokens, unless index lists tell them apart. (Even where that makes no fewer column blocks:
+  // 16 requests of two rows of 128 heads over 8 K to 32 K tokens take 248 us, each row by itself 255.)
+  const bool together = a.indices == nullptr && a.rows.row_request == nullptr && a.rows.next_n * static_cast<int64_t>(p.group) <= 1024 &&
+                        a.rows.next_n * (static_cast<int64_t>(p.R.max_len) / kTile + 1) <= INT32_MAX;  // a unit's tiles
+  p.pack = together ? a.rows.next_n : 1;
   p.cols = p.pack * p.group;
   p.blocks = (p.cols + kMaxBlockCols - 1) / kMaxBlockCols;
   p.block_cols = (p.cols + p.blocks - 1) / p.blocks;

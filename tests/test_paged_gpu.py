@@ -384,6 +384,30 @@ def test_nan_in_a_seen_token_shows(dec):
     assert out[0].isfinite().all() and out[1].isnan().all()
 
 
+@pytest.mark.parametrize("heads, kv_heads, dk, dv, latent", [(16, 1, 576, 512, True), (8, 2, 128, 128, False), (128, 1, 576, 512, True)])
+def test_tokens_of_later_rows_only(dec, heads, kv_heads, dk, dv, latent):
+    # what a request's last row alone sees shows there, whatever it is, and in no other row
+    next_n, last = 3, [300, 128, 3, 2000, 129]
+    lengths = [max(0, n + j - 2 if i != 3 else (700, 0, n)[j]) for i, n in enumerate(last) for j in range(next_n)]
+    q, k, v, table, req, _ = attention_case(24, lengths, next_n, heads, kv_heads, dk, dv, latent, torch.bfloat16, 64)
+    for i, n in enumerate(last):
+        b, o = pu.tokens(table, i, torch.tensor([n - 1]), 64)
+        (k if latent else v)[b, o, 0, 5] = (math.nan, math.inf, -math.inf)[i % 3]
+    want = pu.attention64(q, k, v, dv, table, lengths, req, 64, dk ** -0.5)
+    i32 = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    out, lse = dec.attention(q.cuda(), k.cuda(), table.cuda(), i32, v_cache=None if v is None else v.cuda(), v_dim=dv, next_n=next_n, return_lse=True)
+    ok(dec)
+    early = torch.tensor([r for r in range(len(lengths)) if r % next_n != next_n - 1])
+    pu.check_attention(out[early.cuda()], lse[early.cuda()], [x[early] for x in want], torch.bfloat16)
+    # where the token's weight is not zero (a score of minus infinity makes it so)
+    late, group = out[next_n - 1::next_n].cpu(), heads // kv_heads
+    shown = want[1][next_n - 1::next_n, :group].isfinite().logical_not() if latent else torch.ones(len(last), group, dtype=torch.bool)
+    assert shown.any(1).all() and late[:, :group, 5][shown].isfinite().logical_not().all()
+    if not latent:
+        late[:, :group, 5] = 0
+        assert late.isfinite().all()
+
+
 def test_rising_scores_over_many_tiles(dec):
     # each tile's maximum is far above the last one's: sums have to be scaled down on the way
     lengths = [1500, 1400]
