@@ -42,7 +42,7 @@
 // products, 1500 until the last keys are there, 950 for the scores that wait for them and
 // 1150 for the softmax, 6000 in all, of which the products read shared memory for 3260 (48 to
 // 50 cycles an instruction, 39 to 42 at N = 16). 1024 rows of 64 heads over 2048 tokens each
-// take 365 us (800 TFLOP/s), 64 rows of 128 heads over 2048 of 8 K to 32 K tokens 64 us. Tiles of
+// take 369 us (790 TFLOP/s), 64 rows of 128 heads over 2048 of 8 K to 32 K tokens 63 us. Tiles of
 // 64 tokens, of which two fit, were slower (540 and 90 us): their products read more shared
 // memory a token, and copies and products meet there all the time.
 #include "paged.cuh"
@@ -115,12 +115,14 @@ struct Params {
 template <int N>
 struct Smem {  // behind the tiles
   static constexpr int kHalf = N / 2;
-  int32_t seen_by[kTokenSlots][128];  // of each token of a tile: a row of the group, kEveryRow, or kNoRow
+  int32_t token[kTokenSlots][128];  // position of each token of a tile, INT_MAX where nothing is to be seen
   float column_max[2][4][kHalf];      // [half][warp]; a barrier stands between one tile's reads and the next one's writes
   float moved[kSoftmaxWarps][2][kHalf];  // maximum in use, factor of the old sums
   float column_sum[2][4][kHalf];
-  int32_t row_of[2][2][kHalf];  // [parity of the segment][half]: a column's row in the group, or kSeesNothing
+  int32_t limit[2][2][kHalf];  // [parity of the segment][half]: tokens that a column sees
   int64_t out_at[2][2][kHalf];  // and where its output lies
+  int32_t least[2][2], split[2][2];  // of those; and from where on not all of the unit's rows that see anything see a token
+  uint32_t kept;                // 1 + the last of the tiles that begin a segment but add to what O holds
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t q_first, q_full, q_empty, rest_full[2], rest_empty[2], s_full[2], s_empty[2], p_full[2], o_done[2], token_full[kTokenSlots], all_done[2];
   int64_t scan[kThreads / 32];
@@ -130,64 +132,20 @@ struct Smem {  // behind the tiles
   uint32_t gave_up;
 };
 
-__device__ __forceinline__ int length_in_group(const Params& p, int64_t g, int j) {
-  if (p.pack == 1) return row_length(p.R, g);
-  const int32_t n = p.R.lengths[g * p.pack + j];  // the request is the group's number, and within the table
-  return n < 0 ? 0 : (n > p.R.max_len ? p.R.max_len : n);
+// Out of line: seven copies of it in a kernel that is already longer than the instruction caches like cost 3 to 5 % (and
+// fetching tokens into L2 ahead of their copies, which was tried, cost more than it brought).
+static __device__ __noinline__ int group_length(const Params& p, int64_t g) {
+  int most = 0;
+#pragma unroll 1
+  for (int j = 0; j < p.pack; ++j) most = max(most, row_length(p.R, g * p.pack + j));
+  return most;
 }
 
-__device__ __forceinline__ int tiles_for(int tokens) { return static_cast<int>((tokens + (kTile - 1u)) / kTile); }
-
-// A unit's tiles. Rows whose lengths differ share those tiles that all of them see whole (rows that see nothing aside: their
-// sums are dropped). From there on every row has tiles of its own, in which the others' columns are masked and
-// tokens that only others see are zeros: a probability of zero does not keep a NaN or an infinity of theirs out of a
-// product. That is a tile or two more a row of a group. The functions on groups are out of line: seven copies in a kernel that
-// is already longer than the instruction caches like cost 3 to 5 % (and fetching tokens into L2 ahead of their copies, which
-// was tried, cost more than it brought).
-struct GroupSize {
-  int most;    // tokens of the longest row
-  int common;  // tiles that its rows share
-  int tiles;   // in all; one at least, so that every unit is met and its rows written
-};
-static __device__ __noinline__ GroupSize group_size(const Params& p, int64_t g) {
-  int most = 0, least = INT_MAX, own = 0, some = 0;
-#pragma unroll 1
-  for (int j = 0; j < p.pack; ++j) {
-    const int n = length_in_group(p, g, j);
-    if (n == 0) continue;
-    most = max(most, n);
-    least = min(least, n);
-    own += tiles_for(n);
-    ++some;
-  }
-  GroupSize x;
-  x.most = most;
-  x.common = least >= most ? tiles_for(most) : least / kTile;
-  x.tiles = least >= most ? max(x.common, 1) : own - (some - 1) * x.common;
-  return x;
-}
-
-__device__ __forceinline__ int group_tiles(const Params& p, int64_t g) { return p.row_tiles ? p.row_tiles : group_size(p, g).tiles; }
-
-// The tiles from a unit's number `at` on that the same rows see.
-constexpr int kEveryRow = -1, kNoRow = INT_MAX, kSeesNothing = -2;
-struct Pass {
-  int tile, end;  // of the tokens
-  int limit;      // tokens seen
-  int who;        // the group's row that sees them, or kEveryRow
-};
-static __device__ __noinline__ Pass find_pass(const Params& p, int64_t g, int at) {
-  const GroupSize size = group_size(p, g);
-  if (at < size.common) return {at, size.common, size.most, kEveryRow};
-  at -= size.common;
-#pragma unroll 1
-  for (int j = 0; j < p.pack; ++j) {
-    const int n = length_in_group(p, g, j), own = tiles_for(n) - size.common;
-    if (own <= 0) continue;
-    if (at < own) return {size.common + at, size.common + own, n, j};
-    at -= own;
-  }
-  return {0, 1, 0, kEveryRow};  // no row sees anything
+// Tiles of a unit; one at least, so that every unit is met and its rows written.
+__device__ __forceinline__ int group_tiles(const Params& p, int64_t g) {
+  if (p.row_tiles) return p.row_tiles;
+  const int n = group_length(p, g);
+  return n == 0 ? 1 : static_cast<int>((n + kTile - 1u) / kTile);
 }
 
 // First tile of slice s, and the slice of tile x; in 32 bits where the products fit (a 64-bit division takes some
@@ -296,6 +254,116 @@ __device__ __noinline__ void copy_queries(const Params& p, uint32_t q_at, int64_
   }
 }
 
+// Tokens that only some of a unit's rows see. For the other rows' columns their probability is zero, which does not keep a value
+// that is NaN or infinite out of the product. Such values are looked for in these tokens, a unit's last few, and
+// where there are any, they are added to O for the columns that see them, and replaced by zeros for the product. (The look
+// costs a unit less than 1 us; a thread to each token, not a warp, cost 10 of 246 us with 16 requests of two rows. Tiles of
+// their own for each row's last tokens would not do: they end in the same O.)
+template <bool kBf16>
+__device__ __forceinline__ bool no_number(uint32_t bits) {
+  constexpr uint32_t kExponent = kBf16 ? 0x7F80 : 0x7C00;
+  return (bits & kExponent) == kExponent;
+}
+
+struct Values {  // a tile's, in the ring
+  uint32_t ring, full, piece, slots;  // the first piece, counted from the launch's first
+  int dv;
+  __device__ __forceinline__ uint32_t chunk(int c) const { return ring + (piece + c / 2) % slots * kPiece + c % 2 * kChunk; }
+};
+
+// Whether one of the tokens `who` of the warp's 32 has such a value; all lanes look at one token at a time. With `clear`, zeros
+// take their places.
+template <bool kBf16, bool kClear>
+static __device__ __noinline__ bool find_no_numbers(Values v, int first_token, uint32_t who) {
+  constexpr uint32_t kExponents = kBf16 ? 0x7F807F80 : 0x7C007C00, kLowest = kBf16 ? 0x00800080 : 0x04000400;
+  const int lane = threadIdx.x & 31;
+  uint32_t found = 0;
+#pragma unroll 1
+  for (; who; who &= who - 1) {
+    const int token = first_token + __ffs(who) - 1;
+#pragma unroll 1
+    for (int c = lane >> 3; c * 64 < v.dv; c += 4) {
+      const uint32_t at = v.chunk(c) + token * 128 + (lane & 7) * 16;
+      uint32_t x[4];
+      asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at) : "memory");
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t bad = ((x[i] & kExponents) + kLowest) & 0x80008000;  // an exponent of all ones carries
+        found |= bad;
+        if (kClear) x[i] &= ~((bad >> 15) * 0xFFFF);
+      }
+      if (kClear) asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]) : "memory");
+    }
+  }
+  return found != 0;
+}
+
+// Adds them to O in this thread's lane: value `dim` of each piece, `columns` columns from `o` on, which see as many tokens as
+// `limit` says.
+template <bool kBf16, int kColumns>
+static __device__ __noinline__ void add_no_numbers(Values v, uint32_t o, uint32_t n, int v_pieces, int dim, const int32_t* position, int split,
+                                                   const int32_t* limit) {
+#pragma unroll 1
+  for (int token = 0; token < kTile; ++token) {
+    const int pos = position[token];
+    if (pos < split || pos == INT_MAX) continue;
+#pragma unroll 1
+    for (int u = 0; u < v_pieces; ++u) {
+      uint16_t bits;
+      asm volatile("ld.shared.u16 %0, [%1];"
+                   : "=h"(bits)
+                   : "r"(v.chunk(u * 2 + (dim >> 6)) + token * 128 + ((((dim & 63) >> 3) ^ (token & 7)) << 4) + (dim & 7) * 2)
+                   : "memory");
+      const bool mine = u * 128 + dim < v.dv && no_number<kBf16>(bits);
+      if (!__any_sync(~0u, mine)) continue;
+      const float x = !mine ? 0.f : (kBf16 ? __bfloat162float(__ushort_as_bfloat16(bits)) : __half2float(__ushort_as_half(bits)));
+#pragma unroll 1
+      for (int i = 0; i < kColumns; i += 8) {
+        float y[8];
+        tmem_load(o + u * n + i, y);
+        load_wait(y);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] += pos < limit[i + j] ? x : 0.f;
+        tmem_store8(o + u * n + i, y);
+        store_wait();
+      }
+    }
+  }
+}
+
+// The softmax warps call it for a tile of such tokens, which has been scored and not yet been multiplied with its values.
+template <int N, bool kBf16, bool kLatent>
+static __device__ __noinline__ void protect(const Params& p, Smem<N>& sm, uint32_t ring, uint32_t tile, uint32_t segment, bool first, uint32_t tmem) {
+  const int half = threadIdx.x >> 7, token = threadIdx.x & 127, split = sm.split[segment & 1][half];
+  const int32_t* position = sm.token[tile % kTokenSlots];
+  const Guard guard{&sm.gave_up, p.R.status};
+  const uint32_t k_ring = p.k_pieces - p.rest;
+  const Values v{ring, smem_addr(&sm.full[0]), tile * (k_ring + (kLatent ? 0 : p.v_pieces)) + (kLatent ? 0 : k_ring), static_cast<uint32_t>(p.slots), p.a.dv};
+  const uint32_t who = __ballot_sync(~0u, position[token] >= split && position[token] != INT_MAX);
+#pragma unroll 1
+  for (int u = 0; u < p.v_pieces; ++u) mbar_wait(v.full + (v.piece + u) % v.slots * 8, (v.piece + u) / v.slots & 1, guard);
+  __syncwarp();
+  // both halves of the warps, of which the first looks, decide the same
+  if (!named_any(3, kSoftmaxWarps * 32, half == 0 && find_no_numbers<kBf16, false>(v, token & ~31, who))) return;
+  const uint32_t o = tmem + ((token & ~31u) << 16) + half * (N / 2);
+  __syncwarp();
+  if (!first) {
+    mbar_wait(smem_addr(&sm.o_done[(tile & 1) ^ 1]), ((tile - 1) >> 1) & 1, guard);
+    __syncwarp();
+    fence_after();
+  } else {
+    const float zeros[8] = {};
+    for (int u = 0; u < p.v_pieces; ++u)
+      for (int i = 0; i < N / 2; i += 8) tmem_store8(o + u * N + i, zeros);
+    store_wait();
+    if (threadIdx.x == 0) sm.kept = tile + 1;
+  }
+  add_no_numbers<kBf16, N / 2>(v, o, N, p.v_pieces, token, position, split, sm.limit[segment & 1][half]);
+  named_sync(3, kSoftmaxWarps * 32);
+  if (half == 0) find_no_numbers<kBf16, true>(v, token & ~31, who);
+  __syncwarp();
+}
+
 template <int N, bool kBf16, bool kLatent>
 __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ Params p) {
   constexpr int kPlaces = places<kLatent>;
@@ -327,6 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     }
     for (int i = 0; i < kTokenSlots; ++i) mbar_init(smem_addr(&sm.token_full[i]), kCopyThreads);
     sm.gave_up = 0;
+    sm.kept = 0;
     fence_async();
   }
   if (warp == kScoreWarp) tmem_alloc(smem_addr(&sm.tmem), p.tmem_cols);
@@ -434,19 +503,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     uint32_t tile = 0, segment = 0;
     for (; walk.left > 0; walk.next(p), ++segment) {
       const int64_t row0 = walk.group * p.pack;
-      const int length = p.pack == 1 ? row_length(p.R, row0) : group_size(p, walk.group).most;
+      const int length = group_length(p, walk.group);
       const int64_t request = length > 0 ? row_request(p.R, row0) : 0;
       const int32_t* list = p.a.indices ? p.a.indices + row0 * p.a.index_row_stride : nullptr;
       // A tile's tokens are found in two steps, each a tile earlier than its result is used: the position (from
       // the list), then the block (from the table).
-      Pass pass{walk.at, p.pack == 1 ? INT_MAX : walk.at, list ? p.a.num_indices : length, kEveryRow};
-      const auto listed = [&](int t, int* who) {  // for t = 0, 1, 2, ...
+      const auto listed = [&](int t) {
+        const int i = (walk.at + t) * kTile + me;
         if (t >= walk.count) return -1;
-        if (pass.tile == pass.end) pass = find_pass(p, walk.group, walk.at + t);
-        *who = pass.who;
-        const int i = pass.tile++ * kTile + me;
-        if (i >= pass.limit) return -1;
-        return list ? list[i] : i;
+        return !list ? i : (i < p.a.num_indices ? list[i] : -1);
       };
       const auto table_entry = [&](int x) {
         return x >= 0 && x < length ? __ldg(p.R.block_table + request * p.R.table_stride + block_column(p.R, x)) : 0;
@@ -456,8 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                                                       (x - block_column(p.R, x) * p.R.block_size) * token_stride + walk.kv_head * head_stride);
       };
       const auto in_cache = [&](int x, int x_block) { return x >= 0 && x < length && x_block >= 0 && x_block < p.R.num_blocks; };
-      int at_who = kEveryRow, next_who = kEveryRow, later_who = kEveryRow;
-      int at_token = listed(0, &at_who), next_token = listed(1, &next_who);
+      int at_token = listed(0), next_token = listed(1);
       int at_block = table_entry(at_token);
       asm volatile("" ::"r"(at_block) : "memory");  // here, before any copies are issued: a load waits behind those
       if (segment > 0) {  // the first one's are copied by the softmax warps
@@ -468,14 +532,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       for (int t = 0; t < walk.count; ++t, ++tile) {
         const bool seen = in_cache(at_token, at_block);
         if (!seen && at_token >= 0 && at_token < length) atomicOr(p.R.status, TOPK_DEV_BAD_BLOCK);
-        sm.seen_by[tile % kTokenSlots][me] = seen ? at_who : kNoRow;
+        sm.token[tile % kTokenSlots][me] = seen ? at_token : INT_MAX;
         mbar_arrive(smem_addr(&sm.token_full[tile % kTokenSlots]));
         const char *kp = static_cast<const char*>(p.a.k), *vp = static_cast<const char*>(p.a.v);
         if (seen) {
           kp = address(kp, at_token, at_block, p.a.k_block_stride, p.a.k_token_stride, p.a.k_head_stride);
           if (!kLatent) vp = address(vp, at_token, at_block, p.a.v_block_stride, p.a.v_token_stride, p.a.v_head_stride);
         }
-        const int next_block = table_entry(next_token), later_token = listed(t + 2, &later_who);
+        const int next_block = table_entry(next_token), later_token = listed(t + 2);
         copies.aim(kp, seen, lane);
         const auto copy_rest = [&]() {
           const uint32_t b = tile & 1, before = tile - kPlaces;  // the tile that had this place
@@ -494,8 +558,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         at_token = next_token;
         at_block = next_block;
         next_token = later_token;
-        at_who = next_who;
-        next_who = later_who;
       }
     }
     copies_wait_all();
@@ -575,6 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         mbar_wait_warp(smem_addr(&sm.p_full[b]), (tile >> 1) & 1, guard);
         fence_after();
         if (!kLatent) at.step(p.slots, k_ring);
+        const bool add = t > 0 || *const_cast<volatile uint32_t*>(&sm.kept) == tile + 1;
         const uint32_t p_tile = operand(p_at + (kPlaces == 2 ? b * kChunk : 0), 1024);
 #pragma unroll 1
         for (int u = 0; u < p.v_pieces; ++u) {
@@ -582,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             mbar_wait_warp(full + at.slot * 8, at.phase, guard);
             fence_async();
           }
-          mma16_tokens(tmem + u * N, operand(ring + at.slot * kPiece, kChunk), p_tile, kInst, t > 0);
+          mma16_tokens(tmem + u * N, operand(ring + at.slot * kPiece, kChunk), p_tile, kInst, add);
           commit(empty + at.slot * 8);
           at.step(p.slots);
         }
@@ -605,17 +668,36 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     bool first_segment = true;
     for (; walk.left > 0; walk.next(p), ++segment) {
       const int64_t row0 = walk.group * p.pack;
-      if (quarter == 0 && lane < H) {  // whose each column is
+      if (quarter == 0) {  // what each column sees
         const int c = block * p.block_cols + my_col;
-        int row = kSeesNothing;
+        int n = INT_MAX;
         if (my_col < block_cols) {
           const int j = c / p.group;
-          if (length_in_group(p, walk.group, j) > 0) row = j;
-          sm.out_at[segment & 1][half][lane] = (row0 + j) * p.a.out_row_stride + static_cast<int64_t>(walk.kv_head * p.group + c - j * p.group) * p.a.out_head_stride;
+          n = row_length(p.R, row0 + j);
+          if (lane < H)
+            sm.out_at[segment & 1][half][lane] = (row0 + j) * p.a.out_row_stride + static_cast<int64_t>(walk.kv_head * p.group + c - j * p.group) * p.a.out_head_stride;
         }
-        sm.row_of[segment & 1][half][lane] = row;
+        int least = n, split = INT_MAX;
+        if (p.pack > 1) {
+#pragma unroll 1
+          for (int j = lane; j < p.pack; j += 32) {
+            const int seen = row_length(p.R, row0 + j);
+            if (seen > 0) split = min(split, seen);
+          }
+        }
+#pragma unroll
+        for (int d = 16; d; d >>= 1) {
+          least = min(least, __shfl_xor_sync(~0u, least, d));
+          split = min(split, __shfl_xor_sync(~0u, split, d));
+        }
+        if (lane < H) sm.limit[segment & 1][half][lane] = n == INT_MAX ? 0 : n;
+        if (lane == 0) {
+          sm.least[segment & 1][half] = least;
+          sm.split[segment & 1][half] = split;
+        }
       }
       named_sync(1 + half, 128);
+      const int least = sm.least[segment & 1][half], split_at = sm.split[segment & 1][half] / kTile - walk.at;
       // of my_col, in powers of two: its maximum when that last moved, and what is taken off its scores; below every score
       // until a finite one has come
       float m = -INFINITY, in_use = -1e30f;
@@ -624,17 +706,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       for (int i = 0; i < H; ++i) l[i] = 0.f;
       for (int t = 0; t < walk.count; ++t, ++tile) {
         mbar_wait(smem_addr(&sm.token_full[tile % kTokenSlots]), (tile / kTokenSlots) & 1, guard);
-        const int who = sm.seen_by[tile % kTokenSlots][token];
+        const int pos = sm.token[tile % kTokenSlots][token];
         mbar_wait(smem_addr(&sm.s_full[tile & 1]), (tile >> 1) & 1, guard);
         fence_after();
+        if (t >= split_at) protect<N, kBf16, kLatent>(p, sm, ring, tile, segment, t == 0, tmem);
         float s[H];
         tmem_load(tmem + lanes + s_cols + (tile & 1) * N + half * H, s);
         load_wait(s);
         const auto mask = [&]() {
-          if (who != kEveryRow) {
+          if (pos >= least) {
 #pragma unroll
             for (int i = 0; i < H; ++i)
-              if (who != sm.row_of[segment & 1][half][i]) s[i] = -INFINITY;
+              if (pos >= sm.limit[segment & 1][half][i]) s[i] = -INFINITY;
           }
         };
         const auto probabilities = [&]() {
@@ -734,7 +817,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       float sum = 0.f;
 #pragma unroll
       for (int w = 0; w < 4; ++w) sum += sm.column_sum[half][w][lane & (H - 1)];
-      if (sm.row_of[segment & 1][half][lane & (H - 1)] == kSeesNothing) sum = 0.f, m = -INFINITY;
       const bool whole = walk.count == walk.tiles;
       const int64_t slot = ((static_cast<int64_t>(slice) * 2 + (first_segment ? 0 : 1)) * p.blocks + block) * N;
       const float inverse = sum == 0.f ? 0.f : 1.f / sum;
@@ -1017,10 +1099,8 @@ extern "C" int topk_paged_attention(const topk_attention_args* args, void* strea
   p.R = make_rows(a.rows, INT32_MAX, a.workspace);
   p.group = a.heads / a.kv_heads;
   // The rows of a request share its tokens, unless index lists tell them apart. (Even where that makes no fewer column blocks:
-  // 16 requests of two rows of 128 heads over 8 K to 32 K tokens take 248 us, each row by itself 255.)
-  const bool together = a.indices == nullptr && a.rows.row_request == nullptr && a.rows.next_n * static_cast<int64_t>(p.group) <= 1024 &&
-                        a.rows.next_n * (static_cast<int64_t>(p.R.max_len) / kTile + 1) <= INT32_MAX;  // a unit's tiles
-  p.pack = together ? a.rows.next_n : 1;
+  // 16 requests of two rows of 128 heads over 8 K to 32 K tokens take 247 us, each row by itself 255.)
+  p.pack = a.indices == nullptr && a.rows.row_request == nullptr && a.rows.next_n * static_cast<int64_t>(p.group) <= 1024 ? a.rows.next_n : 1;
   p.cols = p.pack * p.group;
   p.blocks = (p.cols + kMaxBlockCols - 1) / kMaxBlockCols;
   p.block_cols = (p.cols + p.blocks - 1) / p.blocks;

@@ -384,11 +384,12 @@ def test_nan_in_a_seen_token_shows(dec):
     assert out[0].isfinite().all() and out[1].isnan().all()
 
 
-@pytest.mark.parametrize("heads, kv_heads, dk, dv, latent", [(16, 1, 576, 512, True), (8, 2, 128, 128, False), (128, 1, 576, 512, True)])
-def test_tokens_of_later_rows_only(dec, heads, kv_heads, dk, dv, latent):
+@pytest.mark.parametrize("heads, kv_heads, dk, dv, latent, times", [(16, 1, 576, 512, True, 1), (8, 2, 128, 128, False, 1), (128, 1, 576, 512, True, 1),
+                                                                    (16, 1, 576, 512, True, 30), (4, 2, 72, 136, False, 60), (32, 1, 128, 256, False, 30)])
+def test_tokens_of_later_rows_only(dec, heads, kv_heads, dk, dv, latent, times):
     # what a request's last row alone sees shows there, whatever it is, and in no other row
-    next_n, last = 3, [300, 128, 3, 2000, 129]
-    lengths = [max(0, n + j - 2 if i != 3 else (700, 0, n)[j]) for i, n in enumerate(last) for j in range(next_n)]
+    next_n, last = 3, [300, 128, 3, 2000, 129] * times
+    lengths = [max(0, n + j - 2 if i % 5 != 3 else (700, 0, n)[j]) for i, n in enumerate(last) for j in range(next_n)]
     q, k, v, table, req, _ = attention_case(24, lengths, next_n, heads, kv_heads, dk, dv, latent, torch.bfloat16, 64)
     for i, n in enumerate(last):
         b, o = pu.tokens(table, i, torch.tensor([n - 1]), 64)
