@@ -603,6 +603,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           }
         };
         mbar_wait_warp(smem_addr(&sm.s_empty[b]), ((tile >> 1) & 1) ^ 1, guard);
+        // This warp does not wait for the values' pieces. Where they fill the ring, its next slot may still be waiting for one, and a
+        // parity tells no phase from the second one after it: the values have to be through.
+        if (!kLatent && tile > 0 && p.slots <= p.v_pieces) mbar_wait_warp(smem_addr(&sm.o_done[b ^ 1]), ((tile - 1) >> 1) & 1, guard);
         fence_after();
         if (rest_first) last_dims(false);
         uint32_t q_piece = q_at;
@@ -1034,7 +1037,7 @@ int run(Params& p, int device, int smem_limit, bool joins, cudaStream_t stream) 
   }
   p.slots = room / kPiece < kMaxSlots ? room / kPiece : kMaxSlots;
   const int k_ring = p.k_pieces - p.rest;
-  if (p.slots < (p.latent && k_ring > 2 ? k_ring : 2)) return TOPK_ERR_PLAN;
+  if (p.slots < (p.latent && k_ring > 2 ? k_ring : 2) || (!p.latent && p.pack > 1 && p.slots < p.v_pieces)) return TOPK_ERR_PLAN;
   p.tmem_cols = 32;
   while (p.tmem_cols < static_cast<uint32_t>((p.v_pieces + 2) * N)) p.tmem_cols *= 2;
   const size_t smem = p.q_bytes + static_cast<size_t>(p.slots) * kPiece + (p.rest && !p.rest_is_p ? kExtra : 0) + kExtra + extra;
@@ -1100,14 +1103,19 @@ extern "C" int topk_paged_attention(const topk_attention_args* args, void* strea
   p.group = a.heads / a.kv_heads;
   // The rows of a request share its tokens, unless index lists tell them apart. (Even where that makes no fewer column blocks:
   // 16 requests of two rows of 128 heads over 8 K to 32 K tokens take 247 us, each row by itself 255.)
-  p.pack = a.indices == nullptr && a.rows.row_request == nullptr && a.rows.next_n * static_cast<int64_t>(p.group) <= 1024 ? a.rows.next_n : 1;
+  // Not where a tile's values are more pieces than the ring may hold, which have to be there together before the product of
+  // tokens that only some rows see.
+  p.latent = a.v == nullptr;
+  p.k_chunks = (a.dk + 63) / 64;
+  p.v_pieces = (a.dv + 127) / 128;
+  const int held = (props.max_smem_optin - static_cast<int>(sizeof(Smem<64>)) - 1024 - p.k_chunks * 64 * 128 - 2 * kChunk) / kPiece;
+  const bool together = a.indices == nullptr && a.rows.row_request == nullptr && a.rows.next_n * static_cast<int64_t>(p.group) <= 1024 &&
+                        (p.latent || p.v_pieces <= held);
+  p.pack = together ? a.rows.next_n : 1;
   p.cols = p.pack * p.group;
   p.blocks = (p.cols + kMaxBlockCols - 1) / kMaxBlockCols;
   p.block_cols = (p.cols + p.blocks - 1) / p.blocks;
-  p.k_chunks = (a.dk + 63) / 64;
-  p.latent = a.v == nullptr;
   p.k_pieces = (p.k_chunks + 1) / 2;
-  p.v_pieces = (a.dv + 127) / 128;
   p.rest = p.latent && p.k_chunks % 2 == 1 && p.k_pieces > p.v_pieces;
   p.row_groups = a.rows.num_rows / p.pack;
   p.row_tiles = a.indices ? (a.num_indices + kTile - 1) / kTile : 0;

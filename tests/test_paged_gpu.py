@@ -385,7 +385,8 @@ def test_nan_in_a_seen_token_shows(dec):
 
 
 @pytest.mark.parametrize("heads, kv_heads, dk, dv, latent, times", [(16, 1, 576, 512, True, 1), (8, 2, 128, 128, False, 1), (128, 1, 576, 512, True, 1),
-                                                                    (16, 1, 576, 512, True, 30), (4, 2, 72, 136, False, 60), (32, 1, 128, 256, False, 30)])
+                                                                    (16, 1, 576, 512, True, 30), (4, 2, 72, 136, False, 60), (32, 1, 128, 256, False, 30),
+                                                                    (40, 1, 576, 512, False, 1), (40, 1, 448, 392, False, 20), (64, 2, 384, 512, False, 1)])
 def test_tokens_of_later_rows_only(dec, heads, kv_heads, dk, dv, latent, times):
     # what a request's last row alone sees shows there, whatever it is, and in no other row
     next_n, last = 3, [300, 128, 3, 2000, 129] * times
@@ -407,6 +408,14 @@ def test_tokens_of_later_rows_only(dec, heads, kv_heads, dk, dv, latent, times):
     if not latent:
         late[:, :group, 5] = 0
         assert late.isfinite().all()
+
+
+@pytest.mark.parametrize("dk, dv", [(384, 512), (576, 512), (512, 384), (448, 392)])
+def test_values_that_fill_the_ring(dec, dk, dv):
+    # 64 query heads' tiles leave room for as few pieces of the cache as a tile's values have; several tiles a CTA
+    lengths = [300 + 7 * i for i in range(100)]
+    case = attention_case(dk, lengths, 1, 64, 1, dk, dv, False, torch.bfloat16, 64)
+    check_attention(dec, lengths, case, 1, dv, 64)
 
 
 def test_rising_scores_over_many_tiles(dec):
