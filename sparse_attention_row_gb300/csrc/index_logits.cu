@@ -212,7 +212,6 @@ __device__ __forceinline__ void sum_tile(const Params& p, uint32_t at, const flo
   for (; at < end; at += C) {
     float x[C];
     tmem_load(at, x);
-    load_wait(x);
     if (kWide || p.a.heads - in_row >= C) {
 #pragma unroll
       for (int i = 0; i < C; i += 4) {

@@ -321,7 +321,6 @@ static __device__ __noinline__ void add_no_numbers(Values v, uint32_t o, uint32_
       for (int i = 0; i < kColumns; i += 8) {
         float y[8];
         tmem_load(o + u * n + i, y);
-        load_wait(y);
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] += pos < limit[i + j] ? x : 0.f;
         tmem_store8(o + u * n + i, y);
@@ -715,7 +714,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         if (t >= split_at) protect<N, kBf16, kLatent>(p, sm, ring, tile, segment, t == 0, tmem);
         float s[H];
         tmem_load(tmem + lanes + s_cols + (tile & 1) * N + half * H, s);
-        load_wait(s);
         const auto mask = [&]() {
           if (pos >= least) {
 #pragma unroll
@@ -747,7 +745,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         if (move_any) {
           if (t > 0) {
             tmem_load(tmem + lanes + s_cols + (tile & 1) * N + half * H, s);
-            load_wait(s);
             mask();
           }
           const float warp_max = reduce_columns<H, true>(s, lane);
@@ -786,7 +783,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
               float o[8];
               const uint32_t at = tmem + lanes + u * N + half * H + i;
               tmem_load(at, o);
-              load_wait(o);
 #pragma unroll
               for (int j = 0; j < 8; ++j) o[j] *= sm.moved[warp][1][i + j];
               tmem_store8(at, o);
@@ -842,7 +838,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       for (int u = 0; u < p.v_pieces; ++u) {
         float o[H];
         tmem_load(tmem + lanes + u * N + half * H, o);
-        load_wait(o);
         const int dim = u * 128 + token;
         if (blank) {
 #pragma unroll
