@@ -120,12 +120,17 @@ struct Smem {  // behind the tiles
   float moved[kSoftmaxWarps][2][kHalf];  // maximum in use, factor of the old sums
   float column_sum[2][4][kHalf];
   int32_t limit[2][2][kHalf];  // [parity of the segment][half]: tokens that a column sees
-  int64_t out_at[2][2][kHalf];  // and where its output lies
+  union {
+    int64_t out_at[2][2][kHalf];  // and where its output lies
+    int64_t scan[kThreads / 32];  // before the first segment
+  };
   int32_t least[2][2], split[2][2];  // of those; and from where on not all of the unit's rows that see anything see a token
   uint32_t kept;                // 1 + the last of the tiles that begin a segment but add to what O holds
-  uint64_t full[kMaxSlots], empty[kMaxSlots];
+  // A slot of the ring is free (`empty`, by slots), or a piece has come: the keys' pieces by their number, and the values'.
+  // Each is waited for by one warp, one after another: a parity tells no phase from the second one before it, so no wait may
+  // skip a phase, and copies of later pieces do not say that the arrivals of earlier ones have been counted.
+  uint64_t key_come[kMaxSlots], value_come[kMaxSlots], empty[kMaxSlots];
   uint64_t q_first, q_full, q_empty, rest_full[2], rest_empty[2], s_full[2], s_empty[2], p_full[2], o_done[2], token_full[kTokenSlots], all_done[2];
-  int64_t scan[kThreads / 32];
   int64_t start_group, tiles, run_begin, run_end;
   int64_t start_at;
   uint32_t tmem;
@@ -180,7 +185,7 @@ struct Walk {
   }
 };
 
-// A place in the ring of pieces, and the parity of its barrier's phase.
+// A place in the ring of pieces, or among barriers that are taken in turn, and the parity of its phase.
 struct Ring {
   uint32_t slot = 0, phase = 0;
   __device__ __forceinline__ void step(uint32_t slots) {
@@ -266,7 +271,7 @@ __device__ __forceinline__ bool no_number(uint32_t bits) {
 }
 
 struct Values {  // a tile's, in the ring
-  uint32_t ring, full, piece, slots;  // the first piece, counted from the launch's first
+  uint32_t ring, piece, slots;  // the first piece, counted from the launch's first
   int dv;
   __device__ __forceinline__ uint32_t chunk(int c) const { return ring + (piece + c / 2) % slots * kPiece + c % 2 * kChunk; }
 };
@@ -337,18 +342,19 @@ static __device__ __noinline__ void protect(const Params& p, Smem<N>& sm, uint32
   const int32_t* position = sm.token[tile % kTokenSlots];
   const Guard guard{&sm.gave_up, p.R.status};
   const uint32_t k_ring = p.k_pieces - p.rest;
-  const Values v{ring, smem_addr(&sm.full[0]), tile * (k_ring + (kLatent ? 0 : p.v_pieces)) + (kLatent ? 0 : k_ring), static_cast<uint32_t>(p.slots), p.a.dv};
+  const Values v{ring, tile * (k_ring + (kLatent ? 0 : p.v_pieces)) + (kLatent ? 0 : k_ring), static_cast<uint32_t>(p.slots), p.a.dv};
+  const uint32_t come = smem_addr(kLatent ? &sm.key_come[0] : &sm.value_come[0]), number = tile * (kLatent ? k_ring : p.v_pieces);
   const uint32_t who = __ballot_sync(~0u, position[token] >= split && position[token] != INT_MAX);
+  // the last tile's values are through, so that what is waited for is this tile's
+  if (!first) mbar_wait(smem_addr(&sm.o_done[(tile & 1) ^ 1]), ((tile - 1) >> 1) & 1, guard);
 #pragma unroll 1
-  for (int u = 0; u < p.v_pieces; ++u) mbar_wait(v.full + (v.piece + u) % v.slots * 8, (v.piece + u) / v.slots & 1, guard);
+  for (int u = 0; u < p.v_pieces; ++u) mbar_wait(come + (number + u) % kMaxSlots * 8, (number + u) / kMaxSlots & 1, guard);
   __syncwarp();
   // both halves of the warps, of which the first looks, decide the same
   if (!named_any(3, kSoftmaxWarps * 32, half == 0 && find_no_numbers<kBf16, false>(v, token & ~31, who))) return;
   const uint32_t o = tmem + ((token & ~31u) << 16) + half * (N / 2);
   __syncwarp();
   if (!first) {
-    mbar_wait(smem_addr(&sm.o_done[(tile & 1) ^ 1]), ((tile - 1) >> 1) & 1, guard);
-    __syncwarp();
     fence_after();
   } else {
     const float zeros[8] = {};
@@ -377,7 +383,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 
   if (tid == 0) {
     for (int i = 0; i < kMaxSlots; ++i) {
-      mbar_init(smem_addr(&sm.full[i]), kCopyThreads);
+      mbar_init(smem_addr(&sm.key_come[i]), kCopyThreads);
+      mbar_init(smem_addr(&sm.value_come[i]), kCopyThreads);
       mbar_init(smem_addr(&sm.empty[i]), 1);
     }
     mbar_init(smem_addr(&sm.q_first), kSoftmaxWarps * 32);
@@ -490,14 +497,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   if (warp >= kSoftmaxWarps && warp < kScoreWarp) {
     // ---- copies -----------------------------------------------------------
     const int me = tid - kSoftmaxWarps * 32;  // a thread's token of a tile
-    const uint32_t full = smem_addr(&sm.full[0]), empty = smem_addr(&sm.empty[0]);
-    Ring at;
+    const uint32_t empty = smem_addr(&sm.empty[0]);
+    Ring at, keys, values;
     TokenCopies copies((warp - kSoftmaxWarps) * 32, lane);
-    const auto copy_slot = [&](int first, int bytes, const void* cache) {
+    const auto copy_slot = [&](int first, int bytes, const void* cache, uint64_t* come, Ring& number) {
       mbar_wait(empty + at.slot * 8, at.phase ^ 1, guard);
       copies.columns(ring + at.slot * kPiece, kChunk, first, bytes, cache);
-      copies_arrive(full + at.slot * 8);
+      copies_arrive(smem_addr(come + number.slot));
       at.step(p.slots);
+      number.step(kMaxSlots);
     };
     uint32_t tile = 0, segment = 0;
     for (; walk.left > 0; walk.next(p), ++segment) {
@@ -548,11 +556,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         };
         // the rest first where it has buffers of its own, free since an earlier tile was scored
         if (kLatent && p.rest && !p.rest_is_p) copy_rest();
-        for (int u = 0; u < k_ring; ++u) copy_slot(u * 2 * 128, p.a.dk * 2, p.a.k);
+        for (int u = 0; u < k_ring; ++u) copy_slot(u * 2 * 128, p.a.dk * 2, p.a.k, sm.key_come, keys);
         if (kLatent && p.rest && p.rest_is_p) copy_rest();
         if constexpr (!kLatent) {
           copies.aim(vp, seen, lane);
-          for (int u = 0; u < p.v_pieces; ++u) copy_slot(u * 2 * 128, p.a.dv * 2, p.a.v);
+          for (int u = 0; u < p.v_pieces; ++u) copy_slot(u * 2 * 128, p.a.dv * 2, p.a.v, sm.value_come, values);
         }
         at_token = next_token;
         at_block = next_block;
@@ -563,10 +571,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   } else if (warp == kScoreWarp) {
     // ---- S^T = K Q^T, into one of two places ---------------------------------
     constexpr uint32_t kInst = instruction(kBf16 ? kBF16 : kF16, N, false);
-    const uint32_t full = smem_addr(&sm.full[0]), empty = smem_addr(&sm.empty[0]);
+    const uint32_t come = smem_addr(&sm.key_come[0]), empty = smem_addr(&sm.empty[0]);
     const int whole_pieces = p.a.dk / (2 * 64);
     const bool rest_first = kLatent && p.rest && !p.rest_is_p;
-    Ring at;
+    Ring at, keys;
     uint32_t tile = 0, segment = 0;
     for (; walk.left > 0; walk.next(p), ++segment) {
       if (segment == 0)
@@ -585,7 +593,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             mbar_wait_warp(smem_addr(&sm.rest_full[b]), (tile >> 1) & 1, guard);
           } else {
             k_at = ring + at.slot * kPiece;
-            mbar_wait_warp(full + at.slot * 8, at.phase, guard);
+            mbar_wait_warp(come + keys.slot * 8, keys.phase, guard);
+            keys.step(kMaxSlots);
           }
           fence_async();
           int left = p.a.dk - whole_pieces * (2 * 64);
@@ -602,15 +611,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           }
         };
         mbar_wait_warp(smem_addr(&sm.s_empty[b]), ((tile >> 1) & 1) ^ 1, guard);
-        // This warp does not wait for the values' pieces. Where they fill the ring, its next slot may still be waiting for one, and a
-        // parity tells no phase from the second one after it: the values have to be through.
-        if (!kLatent && tile > 0 && p.slots <= p.v_pieces) mbar_wait_warp(smem_addr(&sm.o_done[b ^ 1]), ((tile - 1) >> 1) & 1, guard);
         fence_after();
         if (rest_first) last_dims(false);
         uint32_t q_piece = q_at;
 #pragma unroll 1
         for (int u = 0; u < whole_pieces; ++u) {
-          mbar_wait_warp(full + at.slot * 8, at.phase, guard);
+          mbar_wait_warp(come + keys.slot * 8, keys.phase, guard);
+          keys.step(kMaxSlots);
           fence_async();
           const uint32_t slot = at.slot;
           at.step(p.slots);
@@ -629,8 +636,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   } else if (warp == kValueWarp) {
     // ---- O^T += V^T P^T --------------------------------------------------------
     constexpr uint32_t kInst = instruction(kBf16 ? kBF16 : kF16, N, true);
-    const uint32_t full = smem_addr(&sm.full[0]), empty = smem_addr(&sm.empty[0]);
-    Ring at;
+    const uint32_t come = smem_addr(&sm.value_come[0]), empty = smem_addr(&sm.empty[0]);
+    Ring at, values;
     uint32_t tile = 0;
     for (; walk.left > 0; walk.next(p)) {
 #pragma unroll 1
@@ -644,7 +651,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 #pragma unroll 1
         for (int u = 0; u < p.v_pieces; ++u) {
           if (!kLatent) {
-            mbar_wait_warp(full + at.slot * 8, at.phase, guard);
+            mbar_wait_warp(come + values.slot * 8, values.phase, guard);
+            values.step(kMaxSlots);
             fence_async();
           }
           mma16_tokens(tmem + u * N, operand(ring + at.slot * kPiece, kChunk), p_tile, kInst, add);
