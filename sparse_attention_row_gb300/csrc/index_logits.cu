@@ -170,7 +170,7 @@ struct Walk {
 
 // Where a pass's tokens lie: looked up by the copying warps, and by the summing ones for the scales.
 __device__ __forceinline__ int table_entry(const Params& p, const Walk& w, int x) {
-  return x < w.longest ? __ldg(p.R.block_table + w.request * p.R.table_stride + block_column(p.R, x)) : 0;
+  return x < w.longest ? p.R.block_table[w.request * p.R.table_stride + block_column(p.R, x)] : 0;
 }
 __device__ __forceinline__ bool in_cache(const Params& p, const Walk& w, int x, int b) {
   return x < w.longest && b >= 0 && b < p.R.num_blocks;
@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) index_logits_kernel(const __grid_
       const auto position = [&](int t) { return t < walk.count ? (walk.at + t) * p.tiles * kTile + token : INT_MAX; };
       const auto token_scale = [&](int x, int b) {
         return p.a.key_scales && in_cache(p, walk, x, b)
-                   ? __ldg(p.a.key_scales + b * p.a.scale_block_stride + (x - block_column(p.R, x) * p.R.block_size) * p.a.scale_token_stride)
+                   ? p.a.key_scales[b * p.a.scale_block_stride + (x - block_column(p.R, x) * p.R.block_size) * p.a.scale_token_stride]
                    : 1.f;
       };
       const int t_first = (step & 1) == turn ? 0 : 1;

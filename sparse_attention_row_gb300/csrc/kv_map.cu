@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv_map_kernel(const MapParams p) 
         } else {
           const int64_t n = taken_here + first[j] + (col - have);
           if (n >= 0 && n < a.num_free)
-            block = __ldg(a.free_blocks + n);
+            block = a.free_blocks[n];
           else
             flags |= TOPK_DEV_BLOCKS_EXHAUSTED;
           if (place == 0) *entry = block;

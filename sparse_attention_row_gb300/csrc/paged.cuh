@@ -65,7 +65,8 @@ __device__ __forceinline__ void report_rows(const Rows& R, int tid, int threads)
 }
 
 // Programmatic dependent launch: wait for the kernel before this one on the stream, before the first
-// access to global memory; and let the next one start early in the same way.
+// access to global memory; and let the next one start early in the same way. A kernel that has begun before the
+// last one has ended may not use loads of data that nothing writes while it runs (__ldg): what they read is what it waits for.
 __device__ __forceinline__ void dependent_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void dependent_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         return !list ? i : (i < p.a.num_indices ? list[i] : -1);
       };
       const auto table_entry = [&](int x) {
-        return x >= 0 && x < length ? __ldg(p.R.block_table + request * p.R.table_stride + block_column(p.R, x)) : 0;
+        return x >= 0 && x < length ? p.R.block_table[request * p.R.table_stride + block_column(p.R, x)] : 0;
       };
       const auto address = [&](const void* cache, int x, int x_block, int64_t block_stride, int64_t token_stride, int64_t head_stride) {
         return static_cast<const char*>(cache) + 2 * (static_cast<int64_t>(x_block) * block_stride +

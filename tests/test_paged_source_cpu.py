@@ -42,3 +42,10 @@ def test_instructions_of_a_whole_warp_bring_it_together_first():
 @pytest.mark.parametrize("name", [n for n in PAGED if n != "umma.cuh"])
 def test_kernels_use_the_wrappers(name):
     assert not ALIGNED.search(source(name))
+
+
+@pytest.mark.parametrize("name", PAGED)
+def test_no_loads_for_data_that_nothing_writes(name):
+    # ld.global.nc, which __ldg() is, wants memory that is constant while the kernel runs. These kernels begin before the one
+    # that writes their block table, lengths and scales has ended.
+    assert not re.search(r"__ldg|ld\.global\.nc|__restrict__", source(name))
