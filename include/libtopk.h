@@ -70,7 +70,9 @@ typedef enum {
 #define TOPK_DEV_BLOCKS_EXHAUSTED 0x10u /* topk_kv_map: free_blocks ran out; the tokens concerned got slot -1 */
 #define TOPK_DEV_TABLE_FULL 0x20u       /* topk_kv_map: a request outgrew its row of the table; slot -1 */
 #define TOPK_DEV_TOKENS_DROPPED 0x40u   /* topk_kv_map: more new tokens than max_tokens; the rest got no block and are not listed */
-#define TOPK_DEV_BAD_BLOCK 0x80u        /* a valid token's block, or a row's request, lies outside the cache or the table */
+#define TOPK_DEV_BAD_BLOCK 0x80u        /* a valid token's block, or a row's request, lies outside the cache or the table;
+                                         * topk_kv_map: a new token's page is a negative one, as after a step without
+                                         * enough free blocks: slot -1 */
 #define TOPK_DEV_PIPELINE_TIMEOUT 0x100u /* a wait between the warps of a CTA gave up: the launch's results are void */
 
 /* Tuning and test knobs for topk_ragged_ex. Zero-initialise, then set fields.

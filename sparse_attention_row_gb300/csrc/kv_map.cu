@@ -154,18 +154,22 @@ __global__ void __launch_bounds__(kThreads, 3) kv_map_kernel(const MapParams p) 
         const uint32_t have = min(p.block_shift >= 0 ? (c + (size - 1)) >> p.block_shift : (c + (size - 1)) / size, columns);
         int32_t* entry = a.block_table + r * a.table_stride + col;
         int32_t block = -1;
+        bool had = false;  // whether the table or the free list names a block
         if (col >= columns) {
           flags |= TOPK_DEV_TABLE_FULL;
         } else if (col < have) {
           block = *entry;
+          had = true;
         } else {
           const int64_t n = taken_here + first[j] + (col - have);
-          if (n >= 0 && n < a.num_free)
+          had = n >= 0 && n < a.num_free;
+          if (had)
             block = a.free_blocks[n];
           else
             flags |= TOPK_DEV_BLOCKS_EXHAUSTED;
           if (place == 0) *entry = block;
         }
+        if (had && block < 0) flags |= TOPK_DEV_BAD_BLOCK;  // where an earlier step ran out of blocks, for one
         const int64_t at = tokens + t;
         a.slots[at] = block < 0 ? -1 : static_cast<int64_t>(block) * size + place;
         a.row_lens[at] = static_cast<int32_t>(min(pos, 0x7FFFFFFEu) + 1);

@@ -1,0 +1,45 @@
+"""The paged calls where they went wrong once."""
+import pytest
+import torch
+
+import sparse_attention_row_gb300 as sar
+from tests.gpu_util import require_cuda
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dec():
+    require_cuda()
+    return sar.PagedDecoder(0)
+
+
+@pytest.fixture(autouse=True)
+def _clear(request):
+    yield
+    if "dec" in request.fixturenames:
+        request.getfixturevalue("dec").reset()
+
+
+def dev(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def test_map_reports_tokens_on_a_page_that_an_earlier_step_did_not_get(dec):
+    # the free list ends within request 0's new tokens; the next step's token falls into the page that was entered as -1
+    table, free, taken = dev([[-1] * 4, [9, 8, -1, -1]]), dev([5, 6]), dev([0])
+    first = dec.kv_map(dev([0, 20]), dev([40, 1]), table, free, taken, 16, 41)
+    assert table.tolist() == [[5, 6, -1, -1], [9, 8, -1, -1]] and int(taken) == 2
+    assert first.slots.tolist() == list(range(80, 112)) + [-1] * 8 + [8 * 16 + 4]
+    assert dec.status() == sar.TOPK_DEV_BLOCKS_EXHAUSTED
+    dec.reset()
+    second = dec.kv_map(dev([40, 21]), dev([1, 1]), table, free, taken, 16, 2)
+    assert second.slots.tolist() == [-1, 8 * 16 + 5]
+    assert dec.status() == sar.TOPK_DEV_BAD_BLOCK
+
+
+def test_map_reports_a_negative_block_on_the_free_list(dec):
+    table = dev([[-1] * 2])
+    m = dec.kv_map(dev([0]), dev([20]), table, dev([3, -7]), dev([0]), 16, 20)
+    assert m.slots.tolist() == list(range(48, 64)) + [-1] * 4 and table.tolist() == [[3, -7]]
+    assert dec.status() == sar.TOPK_DEV_BAD_BLOCK
