@@ -57,15 +57,23 @@ class PagedDecoder:
             self._workspace_ptr = self.workspace.data_ptr()
             self.reset()
 
+    def _on_stream(self, function, stream, *args):
+        """function(*args, stream) with the decoder's device current, on the stream that its calls run on."""
+        stream = self._get_stream(self.device) if stream is None else stream
+        if self._get_device() == self.device:
+            return function(*args, stream)
+        with self._torch.cuda.device(self.device):
+            return function(*args, stream)
+
     def reset(self, stream=None) -> None:
         """Clears the status word (stream-ordered)."""
-        rc = _sar.topk_workspace_init(self.workspace, _sar.TOPK_PAGED_WORKSPACE_BYTES, stream)
+        rc = self._on_stream(_sar.topk_workspace_init, stream, self.workspace, _sar.TOPK_PAGED_WORKSPACE_BYTES)
         if rc != _sar.TOPK_OK:
             raise _sar.TopkError(rc, "topk_workspace_init")
 
     def status(self, stream=None) -> int:
         """The sticky TOPK_DEV_* bits; synchronises the stream."""
-        rc, word = _sar.topk_get_status(self.workspace, stream)
+        rc, word = self._on_stream(_sar.topk_get_status, stream, self.workspace)
         if rc != _sar.TOPK_OK:
             raise _sar.TopkError(rc, "topk_get_status")
         return word
