@@ -34,7 +34,9 @@ class PagedDecoder:
 
     Calls that may overlap on the GPU need separate PagedDecoders. ``stream`` is a torch
     stream (default: the current one); tensors that were made on another stream must be
-    ready there, and outlive the call, as with any kernel. Outputs made here belong to it.
+    ready there, and outlive the call, as with any kernel, and so must the decoder with its
+    workspace. Outputs made here belong to that stream. Making a decoder waits for the current
+    stream, so that its workspace is cleared before a call on another.
     """
 
     def __init__(self, device: int = 0):
@@ -56,6 +58,9 @@ class PagedDecoder:
             self.workspace = torch.empty(self.nbytes, dtype=torch.uint8, device=self._dev)
             self._workspace_ptr = self.workspace.data_ptr()
             self.reset()
+            # cleared before a first call on whichever stream (a capture runs nothing that could be waited for)
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()
 
     def _on_stream(self, function, stream, *args):
         """function(*args, stream) with the decoder's device current, on the stream that its calls run on."""

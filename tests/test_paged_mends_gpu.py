@@ -43,3 +43,21 @@ def test_map_reports_a_negative_block_on_the_free_list(dec):
     m = dec.kv_map(dev([0]), dev([20]), table, dev([3, -7]), dev([0]), 16, 20)
     assert m.slots.tolist() == list(range(48, 64)) + [-1] * 4 and table.tolist() == [[3, -7]]
     assert dec.status() == sar.TOPK_DEV_BAD_BLOCK
+
+
+def test_a_new_decoder_is_ready_on_another_stream(dec):
+    # its workspace comes dirty from the allocator, and the stream that it is made on has work to do; the call is made on
+    # another stream at once
+    requests, each, block = 64, 100, 16
+    context, new, table = dev([0] * requests), dev([each] * requests), dev([[-1] * 7] * requests)
+    free, taken, after, side = dev(list(range(7 * requests))), dev([0]), dev([0]), torch.cuda.Stream()
+    junk = torch.full((dec.nbytes,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    del junk
+    torch.cuda._sleep(200_000_000)
+    fresh = sar.PagedDecoder(0)
+    fresh.kv_map(context, new, table, free, taken, block, requests * each, taken_out=after, stream=side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert int(after) == 7 * requests
+    assert fresh.status() == 0
