@@ -45,6 +45,8 @@
 // take 369 us (790 TFLOP/s), 64 rows of 128 heads over 2048 of 8 K to 32 K tokens 63 us. Tiles of
 // 64 tokens, of which two fit, were slower (540 and 90 us): their products read more shared
 // memory a token, and copies and products meet there all the time.
+#include <cfloat>
+
 #include "paged.cuh"
 #include "token_copies.cuh"
 #include "umma.cuh"
@@ -708,9 +710,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       }
       named_sync(1 + half, 128);
       const int least = sm.least[segment & 1][half], split_at = sm.split[segment & 1][half] / kTile - walk.at;
-      // of my_col, in powers of two: its maximum when that last moved, and what is taken off its scores; below every score
-      // until a finite one has come
-      float m = -INFINITY, in_use = -1e30f;
+      // of my_col, in powers of two: its maximum when that last moved, and what is taken off its scores; the lowest
+      // number until a finite one has come, so that any such score makes the maximum move
+      float m = -INFINITY, in_use = -FLT_MAX;
       float l[H];
 #pragma unroll
       for (int i = 0; i < H; ++i) l[i] = 0.f;

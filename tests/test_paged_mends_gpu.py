@@ -61,3 +61,30 @@ def test_a_new_decoder_is_ready_on_another_stream(dec):
     torch.cuda.synchronize()
     assert int(after) == 7 * requests
     assert fresh.status() == 0
+
+
+@pytest.mark.parametrize("listed", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_finite_scores_far_below_zero_after_scores_of_minus_infinity(dec, dtype, listed):
+    # a row's first 128 tokens score -inf, the others all the same: a finite number, for bf16 far below -1e30. 160 rows, so
+    # that both tiles of a row are one run's, of 16 heads, so that no column is left over. Probabilities are one; their sums
+    # and the values' are exact but for the last steps: the mean of 64 values of half a unit, three roundings of the
+    # log-sum and two of its constants.
+    heads, dk, tokens, block, scale = 16, 64, 192, 64, 0.125
+    q = torch.full((160, heads, dk), 2.0 ** (60 if dtype == torch.bfloat16 else 6), dtype=dtype)
+    k = torch.zeros(3, block, 1, dk, dtype=dtype)
+    k[:2, :, 0, 5] = -float("inf")
+    k[2, :, 0, 7] = -2.0 ** (50 if dtype == torch.bfloat16 else 8)
+    v = torch.randn(3, block, 1, dk, generator=torch.Generator().manual_seed(1)).to(dtype)
+    table = torch.arange(3, dtype=torch.int32).repeat(160, 1)
+    indices = torch.arange(tokens, dtype=torch.int32).repeat(160, 1) if listed else None
+    score = scale * float(q[0, 0, 0]) * float(k[2, 0, 0, 7])
+    out, lse = dec.attention(q.cuda(), k.cuda(), table.cuda(), dev([tokens] * 160), v_cache=v.cuda(), scale=scale, return_lse=True,
+                             indices=None if indices is None else indices.cuda())
+    assert dec.status() == 0
+    want = v[2, :, 0].double().mean(0)
+    half = 2.0 ** (-11 if dtype == torch.float16 else -8)
+    room = want.abs() * half * 1.01 + v[2].double().abs().mean() * 64 * 2.0 ** -22
+    assert ((out.cpu().double() - want).abs() <= room).all()
+    log_sum = score + 4.1588830833596715  # ln 64
+    assert ((lse.cpu().double() - log_sum).abs() <= abs(log_sum) * 2.0 ** -21).all()
