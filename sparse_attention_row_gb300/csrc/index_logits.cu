@@ -2,15 +2,15 @@
 // (topk_index_logits), on the tensor cores:
 //   logits[r, t] = s_t * sum_h w[r, h] * max(0, q[r, h, :] . k[t, :]).
 //
-// A unit is a few consecutive rows; where they belong to one request (drafted
-// tokens, a prompt's piece) they share a pass over its keys, otherwise each has a
-// pass of its own. A product takes 128 tokens,
+// A unit is a few consecutive rows; those that belong to one request (drafted
+// tokens, a prompt's piece) share a pass over its keys. A product takes 128 tokens,
 //   S^T [128 tokens x N] = K [128 x dim] . Q^T [dim x N],  N = rows x heads <= 256,
 // and puts a token's scores for all rows and heads in one lane of tensor memory, so
 // that the weighted sum over the heads is one thread's own: no exchange at all.
-// A step is two such tiles where N <= 128 and one where it is more: 256 columns of
-// tensor memory, of which there are two places, so that one step's sums run while the
-// next is multiplied.
+// There are two places of 256 columns, so that one's sums run while the next is
+// multiplied. Two tiles share a place where N <= 128. A step, what is copied at once, is
+// two tiles, or one where all passes are wider; where each row brings its request, the
+// kernel finds the passes, and a wide one multiplies a step's two tiles one after the other.
 //
 // The units' steps are dealt in equal runs to the CTAs, one on each SM; every CTA
 // sums up the rows' steps to find its run. Rows are independent over the tokens,
@@ -78,81 +78,72 @@ struct Smem {
 
 __device__ __forceinline__ int steps_of(const Params& p, int length) { return static_cast<int>((length + (p.tiles * kTile - 1u)) / (p.tiles * kTile)); }
 
-// The rows of a unit: whether those that see anything have one request, and the unit's steps.
-struct Unit {
-  int64_t row0, request;  // of those rows
-  int rows, longest;
-  bool shared;
-  int64_t steps;
-  __device__ Unit(const Params& p, int64_t u) {
-    row0 = u * p.pack;
-    rows = static_cast<int>(min(static_cast<int64_t>(p.pack), p.R.num_rows - row0));
-    shared = true;
-    longest = 0;
-    request = -1;
-    int64_t sum = 0;
-    for (int j0 = 0; j0 < rows; j0 += 4) {  // four rows' entries on their way at once
-      int32_t n[4];
-      int64_t b[4];
+// Steps of a unit: those of its passes, each a run of rows of one request (rows that see nothing do not part one).
+__device__ __forceinline__ int64_t unit_steps(const Params& p, int64_t u) {
+  const int64_t row0 = u * p.pack;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(p.pack), p.R.num_rows - row0));
+  int longest = 0;
+  int64_t request = -1, steps = 0;
+  for (int j0 = 0; j0 < rows; j0 += 4) {  // four rows' entries on their way at once
+    int32_t n[4];
+    int64_t b[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t row = row0 + min(j0 + i, rows - 1);
-        n[i] = p.R.lengths[row];
-        b[i] = row_request(p.R, row);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = j0 + i < rows ? seen_tokens(p.R, n[i], b[i]) : 0;
-        if (c == 0) continue;
-        longest = max(longest, c);
-        sum += steps_of(p, c);
-        if (request >= 0 && b[i] != request) shared = false;
-        request = b[i];
-      }
+    for (int i = 0; i < 4; ++i) {
+      const int64_t row = row0 + min(j0 + i, rows - 1);
+      n[i] = p.R.lengths[row];
+      b[i] = row_request(p.R, row);
     }
-    steps = shared ? steps_of(p, longest) : sum;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = j0 + i < rows ? seen_tokens(p.R, n[i], b[i]) : 0;
+      if (c == 0) continue;
+      if (b[i] != request) {
+        steps += steps_of(p, longest);
+        longest = 0;
+      }
+      request = b[i];
+      longest = max(longest, c);
+    }
   }
-};
+  return steps + steps_of(p, longest);
+}
 
-// A slice's run of steps, segment by segment (a segment: the steps of one pass in the run).
+// A slice's run of steps, walked by whole warps segment by segment (a segment: the steps of one pass in the run).
 struct Walk {
   int64_t unit, left;
   int64_t row0;      // of the pass
   int64_t request;
   int first, rows;   // the pass's rows within the unit
-  int unit_rows;
-  bool shared;
   int at, count, longest;
-  __device__ void pass(const Params& p, int from) {  // of a unit with several: the one of row `from` or a later one
-    longest = 0;
-    rows = 0;
-    for (first = from; first < unit_rows; ++first) {
-      longest = row_length(p.R, row0 + first);
-      if (longest > 0) {
-        rows = 1;
-        request = row_request(p.R, row0 + first);
-        return;
-      }
+  __device__ void pass(const Params& p, int from) {  // the one of row `from` or of a later one; none: longest is 0
+    const int lane = threadIdx.x & 31, unit_rows = static_cast<int>(min(static_cast<int64_t>(p.pack), p.R.num_rows - row0));
+    int n = 0, b = 0;
+    if (lane >= from && lane < unit_rows) {
+      const int64_t of = row_request(p.R, row0 + lane);
+      n = seen_tokens(p.R, p.R.lengths[row0 + lane], of);
+      b = static_cast<int>(of);
     }
+    const unsigned seen = __ballot_sync(~0u, n > 0);
+    first = seen ? __ffs(seen) - 1 : unit_rows;
+    b = n > 0 ? b : -1;
+    const int mine = __shfl_sync(~0u, b, first & 31);
+    const unsigned others = __ballot_sync(~0u, n > 0 && b != mine);
+    const unsigned run = others ? seen & ((1u << (__ffs(others) - 1)) - 1) : seen;
+    rows = run ? 32 - __clz(run) - first : 0;
+    longest = __reduce_max_sync(~0u, (run >> lane) & 1 ? n : 0);
+    request = mine;
   }
   __device__ void enter(const Params& p, int64_t u) {
-    const Unit x(p, u);
     unit = u;
-    row0 = x.row0;
-    unit_rows = x.rows;
-    shared = x.shared;
-    first = 0;
-    rows = x.rows;
-    longest = x.longest;
-    request = x.request;
-    if (!shared) pass(p, 0);
+    row0 = u * p.pack;
+    pass(p, 0);
   }
   __device__ void size(const Params& p) { count = static_cast<int>(min(static_cast<int64_t>(steps_of(p, longest) - at), left)); }
   __device__ void start(const Params& p, int64_t u, int64_t offset) {
     enter(p, u);
     while (offset >= steps_of(p, longest)) {
       offset -= steps_of(p, longest);
-      pass(p, first + 1);
+      pass(p, first + rows);
     }
     at = static_cast<int>(offset);
     size(p);
@@ -161,11 +152,12 @@ struct Walk {
     left -= count;
     at = 0;
     if (left <= 0) return;
-    longest = 0;
-    if (!shared) pass(p, first + 1);
+    pass(p, first + rows);
     while (longest == 0) enter(p, unit + 1);  // there are steps left, so some later unit has them
     size(p);
   }
+  // A product of the pass: both tiles of a step where their columns fit a place of tensor memory side by side, else one.
+  __device__ int product_tiles(const Params& p) const { return p.tiles == 2 && rows * p.head_cols <= kMaxCols / 2 ? 2 : 1; }
 };
 
 // Where a pass's tokens lie: looked up by the copying warps, and by the summing ones for the scales.
@@ -267,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1) index_logits_kernel(const __grid_
     const int64_t per = (p.units + kThreads - 1) / kThreads;
     const int64_t u0 = min(per * tid, p.units), u1 = min(u0 + per, p.units);
     int64_t mine = 0;
-    for (int64_t u = u0; u < u1; ++u) mine += Unit(p, u).steps;
+    for (int64_t u = u0; u < u1; ++u) mine += unit_steps(p, u);
     int64_t pre = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -289,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1) index_logits_kernel(const __grid_
         sm.start_at = begin - at;
       }
       for (int64_t u = u0; u1 - u0 > 1 && u < u1; ++u) {
-        const int64_t n = Unit(p, u).steps;
+        const int64_t n = unit_steps(p, u);
         if (begin < at + n) {
           sm.start_unit = u;
           sm.start_at = begin - at;
@@ -409,32 +401,38 @@ __global__ void __launch_bounds__(kThreads, 1) index_logits_kernel(const __grid_
     uint32_t step = 0, segment = 0, slot = 0, phase = 0;
     for (; walk.left > 0; walk.next(p), ++segment) {
       const uint32_t inst = p.inst | (static_cast<uint32_t>(walk.rows * p.head_cols >> 3) << 17);
+      const int at_once = walk.product_tiles(p);
       mbar_wait_warp(smem_addr(&sm.q_full), segment & 1, guard);
       fence_async();
-      for (int t = 0; t < walk.count; ++t, ++step) {
-        mbar_wait_warp(smem_addr(&sm.s_empty[0]) + (step & 1) * 8, ((step >> 1) & 1) ^ 1, guard);
-        mbar_wait_warp(smem_addr(&sm.full[0]) + slot * 8, phase, guard);
-        fence_after();
+      for (int t = 0; t < walk.count; ++t) {
+        int from = 0;  // of the step's tiles
+        do {
+          mbar_wait_warp(smem_addr(&sm.s_empty[0]) + (step & 1) * 8, ((step >> 1) & 1) ^ 1, guard);
+          if (from == 0) mbar_wait_warp(smem_addr(&sm.full[0]) + slot * 8, phase, guard);
+          fence_after();
 #pragma unroll 1
-        for (int m = 0; m < p.tiles; ++m) {
-          const uint32_t d = tmem + (step & 1) * kMaxCols + m * (kMaxCols / 2), k_at = ring + slot * slot_bytes + m * tile_bytes;
-          int c = 0;
+          for (int m = 0; m < at_once; ++m) {
+            const uint32_t d = tmem + (step & 1) * kMaxCols + m * (kMaxCols / 2), k_at = ring + slot * slot_bytes + (from + m) * tile_bytes;
+            int c = 0;
 #pragma unroll 1
-          for (; c < chunks; ++c) {
-            if (k8Bit)
-              mma8_chunk(d, operand(k_at + c * kChunk, 16), operand(q_at + c * q_chunk, 16), inst, c > 0);
-            else
-              mma16_chunk(d, operand(k_at + c * kChunk, 16), operand(q_at + c * q_chunk, 16), inst, c > 0);
+            for (; c < chunks; ++c) {
+              if (k8Bit)
+                mma8_chunk(d, operand(k_at + c * kChunk, 16), operand(q_at + c * q_chunk, 16), inst, c > 0);
+              else
+                mma16_chunk(d, operand(k_at + c * kChunk, 16), operand(q_at + c * q_chunk, 16), inst, c > 0);
+            }
+#pragma unroll 1
+            for (int i = 0; i < rest; ++i) {
+              if (k8Bit)
+                mma8_step(d, operand(k_at + c * kChunk + i * 32, 16), operand(q_at + c * q_chunk + i * 32, 16), inst, c + i > 0);
+              else
+                mma16_step(d, operand(k_at + c * kChunk + i * 32, 16), operand(q_at + c * q_chunk + i * 32, 16), inst, c + i > 0);
+            }
           }
-#pragma unroll 1
-          for (int i = 0; i < rest; ++i) {
-            if (k8Bit)
-              mma8_step(d, operand(k_at + c * kChunk + i * 32, 16), operand(q_at + c * q_chunk + i * 32, 16), inst, c + i > 0);
-            else
-              mma16_step(d, operand(k_at + c * kChunk + i * 32, 16), operand(q_at + c * q_chunk + i * 32, 16), inst, c + i > 0);
-          }
-        }
-        commit(smem_addr(&sm.s_full[0]) + (step & 1) * 8);
+          commit(smem_addr(&sm.s_full[0]) + (step & 1) * 8);
+          ++step;
+          from += at_once;
+        } while (from < p.tiles && ((walk.at + t) * p.tiles + from) * kTile < walk.longest);
         commit(smem_addr(&sm.empty[0]) + slot * 8);
         if (t + 1 == walk.count) commit(smem_addr(&sm.q_empty));
         if (++slot == static_cast<uint32_t>(p.slots)) {
@@ -448,20 +446,26 @@ __global__ void __launch_bounds__(kThreads, 1) index_logits_kernel(const __grid_
     __syncwarp();
   } else {
     // ---- sums -------------------------------------------------------------
-    const uint32_t turn = warp >> 3;     // every second step
+    const uint32_t turn = warp >> 3;     // every second product
     const int part = (warp >> 2) & 1;    // its tile, or its half of the rows
-    const int quarter = warp & 3, token = (p.tiles == 2 ? part * kTile : 0) + quarter * 32 + lane;
-    const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + turn * kMaxCols + (p.tiles == 2 ? part * (kMaxCols / 2) : 0);
+    const int quarter = warp & 3;
     uint32_t step = 0, segment = 0;
     for (; walk.left > 0; walk.next(p), ++segment) {
       const int ss = segment % kSegmentSlots;
       mbar_wait(smem_addr(&sm.segment_full[ss]), (segment / kSegmentSlots) & 1, guard);
+      const bool both = walk.product_tiles(p) == 2;
+      const int tokens = both ? 2 * kTile : kTile;  // of a product
+      const int token = (both ? part * kTile : 0) + quarter * 32 + lane;
+      const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + turn * kMaxCols + (both ? part * (kMaxCols / 2) : 0);
       const int middle = (walk.rows + 1) / 2;
-      const int row = p.tiles == 1 && part == 1 ? middle : 0, row_end = p.tiles == 1 && part == 0 ? middle : walk.rows;
+      const int row = !both && part == 1 ? middle : 0, row_end = !both && part == 0 ? middle : walk.rows;
+      // the segment's products
+      const int first = walk.at * (p.tiles * kTile / tokens);
+      const int count = min((walk.at + walk.count) * (p.tiles * kTile / tokens), static_cast<int>((walk.longest + (tokens - 1u)) / tokens)) - first;
       // The token's blocks and scales, two of this group's steps at a time: a group of two is looked up while the one before
       // it is summed, its blocks one earlier still. (Looked up a step ahead, the scales of 8-bit keys were waited for: they
       // come from HBM, behind a stream of keys.)
-      const auto position = [&](int t) { return t < walk.count ? (walk.at + t) * p.tiles * kTile + token : INT_MAX; };
+      const auto position = [&](int t) { return t < count ? (first + t) * tokens + token : INT_MAX; };
       const auto token_scale = [&](int x, int b) {
         return p.a.key_scales && in_cache(p, walk, x, b)
                    ? p.a.key_scales[b * p.a.scale_block_stride + (x - block_column(p.R, x) * p.R.block_size) * p.a.scale_token_stride]
@@ -476,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) index_logits_kernel(const __grid_
       for (int i = 0; i < 2; ++i) b1[i] = table_entry(p, walk, position(t_first + 4 + i * 2));
 #pragma unroll
       for (int i = 0; i < 2; ++i) s0[i] = token_scale(position(t_first + i * 2), b0[i]);
-      for (int t0 = t_first; t0 < walk.count; t0 += 4) {
+      for (int t0 = t_first; t0 < count; t0 += 4) {
         int b2[2];
         float s1[2];
 #pragma unroll
@@ -486,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) index_logits_kernel(const __grid_
 #pragma unroll 1
         for (int i = 0; i < 2; ++i) {
           const int t = t0 + i * 2, pos = position(t);
-          if (t >= walk.count) break;
+          if (t >= count) break;
           const bool found = in_cache(p, walk, pos, i ? b0[1] : b0[0]);
           const float scale = i ? s0[1] : s0[0];
           if (pos < walk.longest && !found) atomicOr(p.R.status, TOPK_DEV_BAD_BLOCK);
@@ -508,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) index_logits_kernel(const __grid_
           s0[i] = s1[i];
         }
       }
-      step += walk.count;
+      step += count;
     }
   }
   if (slice == 0) report_rows(p.R, tid, kThreads);
@@ -574,7 +578,9 @@ extern "C" int topk_index_logits(const topk_index_logits_args* args, void* strea
     const int64_t tokens = kTile * (d * p.head_cols <= kMaxCols / 2 ? 2 : 1);
     if (d == 1 || (a.rows.num_rows + d - 1) / d * ((p.R.max_len + tokens - 1) / tokens) >= props.num_sms) p.pack = d;
   }
-  p.tiles = p.pack * p.head_cols <= kMaxCols / 2 ? 2 : 1;
+  // Two tiles a step where a unit's columns leave room for both in a place, and where rows bring their requests: passes may
+  // then be of fewer rows. One of more columns multiplies a step's tiles one after the other.
+  p.tiles = a.rows.row_request != nullptr || p.pack * p.head_cols <= kMaxCols / 2 ? 2 : 1;
   p.units = (a.rows.num_rows + p.pack - 1) / p.pack;
   rc = make_cache_map(&p.map, a.keys, size, a.dtype, a.rows.num_blocks, a.rows.block_size, a.dim, a.key_block_stride, a.key_token_stride,
                       64);

@@ -3,6 +3,7 @@ import pytest
 import torch
 
 import sparse_attention_row_gb300 as sar
+from tests import paged_util as pu
 from tests.gpu_util import require_cuda
 
 pytestmark = pytest.mark.gpu
@@ -88,3 +89,83 @@ def test_finite_scores_far_below_zero_after_scores_of_minus_infinity(dec, dtype,
     assert ((out.cpu().double() - want).abs() <= room).all()
     log_sum = score + 4.1588830833596715  # ln 64
     assert ((lse.cpu().double() - log_sum).abs() <= abs(log_sum) * 2.0 ** -21).all()
+
+
+def graph_us(call, passes=20, replays=10):
+    """The least device time of a pass in a graph of them."""
+    for _ in range(3):
+        call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(passes):
+            call()
+    graph.replay()
+    best = float("inf")
+    for _ in range(replays):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        graph.replay()
+        b.record()
+        b.synchronize()
+        best = min(best, a.elapsed_time(b) * 1e3 / passes)
+    return best
+
+
+@pytest.mark.parametrize("next_n, dtype, room", [(1, torch.float8_e4m3fn, 1.15), (2, torch.float8_e4m3fn, 1.2), (2, torch.bfloat16, 1.2)])
+def test_logits_of_rows_with_requests_take_no_longer(dec, next_n, dtype, room):
+    # the same rows by next_n and by row_request: a request's keys are read once either way. (When each row of a unit with
+    # more than one request read them for itself, in steps of half as many tokens: 1.16, 1.49 and 1.31 times as long.)
+    requests, heads, dim, block, tokens = 64 // next_n, 64, 128, 64, 40000
+    g = torch.Generator(device="cuda").manual_seed(2)
+    columns = tokens // block + 1
+    table = torch.randperm(requests * columns, generator=g, device="cuda").int().view(requests, columns)
+    lengths = (tokens - torch.randint(0, tokens // 2, (requests, 1), generator=g, device="cuda") + torch.arange(next_n, device="cuda")).int().view(-1)
+    rows = len(lengths)
+    q = torch.randn((rows, heads, dim), generator=g, device="cuda").to(dtype)
+    keys = torch.randn((requests * columns, block, dim), generator=g, device="cuda", dtype=torch.float16).to(dtype)
+    w = torch.randn((rows, heads), generator=g, device="cuda")
+    scales = torch.rand((requests * columns, block), generator=g, device="cuda")
+    out, other = torch.zeros((2, rows, columns * block), device="cuda")
+    request = (torch.arange(rows, device="cuda") // next_n).int()
+    for _ in range(3):  # another user's work beside it may spoil a measurement, not three
+        by_next_n = graph_us(lambda: dec.index_logits(q, w, keys, table, lengths, key_scales=scales, next_n=next_n, out=out))
+        by_request = graph_us(lambda: dec.index_logits(q, w, keys, table, lengths, key_scales=scales, row_request=request, out=other))
+        if by_request <= room * by_next_n:
+            break
+    assert dec.status() == 0 and torch.equal(out, other)
+    assert by_request <= room * by_next_n, f"{by_request:.1f} us against {by_next_n:.1f}"
+
+
+@pytest.mark.parametrize("heads", [8, 33, 64, 128])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float8_e4m3fn])
+def test_logits_of_runs_of_any_length(dec, heads, dtype):
+    # runs of rows of one request that begin and end anywhere in a unit, with rows that see nothing and padding rows among
+    # them, and lengths around the ends of tiles and pairs of tiles
+    counts, ends = [1, 2, 3, 4, 5, 9, 16, 1, 1, 33], [127, 128, 129, 255, 256, 257, 383, 384, 385, 513, 641, 1]
+    request, lengths = [], []
+    for r, n in enumerate(counts):
+        for j in range(n):
+            request.append(r)
+            lengths.append(0 if (r + j) % 7 == 6 else ends[(3 * r + j) % len(ends)])
+            if (r + j) % 5 == 4:
+                request.append(-1)
+                lengths.append(77)
+    # a long prompt's piece, so that units hold as many rows as they may
+    request += [len(counts)] * 70
+    lengths += [20000 + j for j in range(70)]
+    seen = [0 if b < 0 else n for n, b in zip(lengths, request)]
+    rq = [max(b, 0) for b in request]
+    g = torch.Generator().manual_seed(heads)
+    longest = [max([n for n, b in zip(seen, rq) if b == i]) for i in range(len(counts) + 1)]
+    table, blocks = pu.block_table(g, longest, 16)
+    q = torch.randn(len(rq), heads, 128, generator=g).to(dtype)
+    keys = pu.poisoned(torch.randn(blocks, 16, 128, generator=g).to(dtype), table, longest, 16)
+    w, scales = torch.randn(len(rq), heads, generator=g), 0.5 + torch.rand(blocks, 16, generator=g)
+    width = max(longest)
+    want, tol = pu.logits64(q, w, keys, scales, table, seen, rq, 16, width)
+    out = torch.full((len(rq), width), 7.25, device="cuda")
+    got = dec.index_logits(q.cuda(), w.cuda(), keys.cuda(), table.cuda(), dev(lengths), key_scales=scales.cuda(), row_request=dev(request), out=out).cpu().double()
+    past = want.isnan()
+    assert (got[past] == 7.25).all() and ((got - want).abs()[~past] <= tol[~past]).all()
+    assert dec.status() == 0
