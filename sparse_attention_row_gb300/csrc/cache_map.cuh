@@ -2,10 +2,11 @@
 //
 // The cache is a list of rows, one token each, whose addresses are base + row * step;
 // `step` is the largest one that the strides of blocks and tokens are multiples of, so
-// that any of them fits. Where tokens follow one another in a block, up to 64 of them
-// are fetched at once; elsewhere, and where some are masked, four rows by their
-// numbers (tile::gather4). A masked token's row number is one past the last, which
-// reads as zeros. Either way 128 bytes of each token at a time, swizzled.
+// that any of them fits. Where a block's tokens come in runs of 8 to 64 (its size is a
+// multiple of that, and its stride one of the tokens'), a run is fetched at once;
+// elsewhere four rows by their numbers (tile::gather4). What is masked has a row number
+// past the last, which reads as zeros; of a run that begins in the cache the tokens past
+// the length are fetched with it. Either way 128 bytes of each token at a time, swizzled.
 //
 // This is for streams of whole pages. An instruction takes its warp 70 cycles for 512
 // bytes and 180 for 8 KB, so scattered tokens are better copied by cp.async

@@ -590,7 +590,8 @@ extern "C" int topk_index_logits(const topk_index_logits_args* args, void* strea
   p.q_bytes = static_cast<uint32_t>(p.pack * p.head_cols * 128 * p.chunks);
   const int64_t step = p.tiles * kTile, most = a.rows.num_rows * ((p.R.max_len + step - 1) / step);
   p.slices = static_cast<int32_t>(most < props.num_sms ? most : props.num_sms);
-  p.inst = ltk::umma::instruction(a.dtype == TOPK_DTYPE_BF16 ? ltk::umma::kBF16 : ltk::umma::kF16, 0, false);
+  using namespace ltk::umma;
+  p.inst = instruction(size == 1 ? kE4M3 : a.dtype == TOPK_DTYPE_BF16 ? kBF16 : kF16, 0, false);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return size == 1 ? run<true>(p, dev, props.max_smem_optin, s) : run<false>(p, dev, props.max_smem_optin, s);
 }

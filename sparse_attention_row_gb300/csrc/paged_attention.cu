@@ -60,8 +60,8 @@ using namespace ltk::umma;
 constexpr int kTile = 128;            // tokens
 constexpr int kChunk = kTile * 128;   // bytes of 64 dims
 constexpr int kPiece = 2 * kChunk;    // a ring slot: 128 dims
-// Places for P, and for the rest of the keys. A latent tile and the queries leave room for one; elsewhere the next tile's
-// probabilities need not wait until the last one's have been multiplied.
+// Places for P. A latent tile and the queries leave room for one; elsewhere the next tile's probabilities need not wait
+// until the last one's have been multiplied.
 template <bool kLatent>
 constexpr int places = kLatent ? 1 : 2;
 constexpr int kSoftmaxWarps = 8, kCopyWarps = 4;
@@ -96,8 +96,8 @@ struct Params {
   int32_t k_chunks;      // of 64 dims
   int32_t k_pieces, v_pieces;
   int32_t latent;        // values are the first dims of the keys
-  int32_t rest;          // 1: the last 64 dims of the keys, which are no values, have two buffers of their own
-  int32_t rest_is_p;     // 1: and P takes its place after it has been used
+  int32_t rest;          // 1: the last 64 dims of latent keys, which are no values, have a buffer of their own
+  int32_t rest_is_p;     // 1: which is P's, who takes it after it has been used
   int32_t slots;         // of the ring
   int32_t slices;
   int32_t row_tiles;     // tiles of every unit where index lists are given, else 0
@@ -132,7 +132,7 @@ struct Smem {  // behind the tiles
   // Each is waited for by one warp, one after another: a parity tells no phase from the second one before it, so no wait may
   // skip a phase, and copies of later pieces do not say that the arrivals of earlier ones have been counted.
   uint64_t key_come[kMaxSlots], value_come[kMaxSlots], empty[kMaxSlots];
-  uint64_t q_first, q_full, q_empty, rest_full[2], rest_empty[2], s_full[2], s_empty[2], p_full[2], o_done[2], token_full[kTokenSlots], all_done[2];
+  uint64_t q_first, q_full, q_empty, rest_full, rest_empty, s_full[2], s_empty[2], p_full[2], o_done[2], token_full[kTokenSlots], all_done[2];
   int64_t start_group, tiles, run_begin, run_end;
   int64_t start_at;
   uint32_t tmem;
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   extern __shared__ __align__(1024) uint8_t raw[];
   const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
   const uint32_t q_at = base, ring = q_at + p.q_bytes, rest = ring + p.slots * kPiece;
-  const uint32_t p_at = rest + (p.rest && !p.rest_is_p ? kPlaces * kChunk : 0);
+  const uint32_t p_at = rest + (p.rest && !p.rest_is_p ? kChunk : 0);
   Smem<N>& sm = *reinterpret_cast<Smem<N>*>(raw + (p_at + kPlaces * kChunk - smem_addr(raw)));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int block = blockIdx.x % p.blocks, slice = blockIdx.x / p.blocks;
@@ -392,9 +392,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     mbar_init(smem_addr(&sm.q_first), kSoftmaxWarps * 32);
     mbar_init(smem_addr(&sm.q_full), kCopyThreads);
     mbar_init(smem_addr(&sm.q_empty), 1);
+    mbar_init(smem_addr(&sm.rest_full), kCopyThreads);
+    mbar_init(smem_addr(&sm.rest_empty), 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_addr(&sm.rest_full[i]), kCopyThreads);
-      mbar_init(smem_addr(&sm.rest_empty[i]), 1);
       mbar_init(smem_addr(&sm.s_full[i]), 1);
       mbar_init(smem_addr(&sm.s_empty[i]), kSoftmaxWarps);
       mbar_init(smem_addr(&sm.p_full[i]), kSoftmaxWarps);
@@ -551,12 +551,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         const int next_block = table_entry(next_token), later_token = listed(t + 2);
         copies.aim(kp, seen, lane);
         const auto copy_rest = [&]() {
-          const uint32_t b = tile & 1, before = tile - kPlaces;  // the tile that had this place
-          if (tile >= kPlaces) mbar_wait(smem_addr(&sm.rest_empty[before & 1]), (before >> 1) & 1, guard);
-          copies.columns(rest + (kPlaces == 2 ? b * kChunk : 0), kChunk, k_ring * 2 * 128, p.a.dk * 2, p.a.k);
-          copies_arrive(smem_addr(&sm.rest_full[b]));
+          mbar_wait(smem_addr(&sm.rest_empty), (tile & 1) ^ 1, guard);
+          copies.columns(rest, kChunk, k_ring * 2 * 128, p.a.dk * 2, p.a.k);
+          copies_arrive(smem_addr(&sm.rest_full));
         };
-        // the rest first where it has buffers of its own, free since an earlier tile was scored
+        // the rest first where its buffer is free since the last tile was scored
         if (kLatent && p.rest && !p.rest_is_p) copy_rest();
         for (int u = 0; u < k_ring; ++u) copy_slot(u * 2 * 128, p.a.dk * 2, p.a.k, sm.key_come, keys);
         if (kLatent && p.rest && p.rest_is_p) copy_rest();
@@ -591,8 +590,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         const auto last_dims = [&](bool add) {
           uint32_t k_at, q_piece = q_at + whole_pieces * 2 * (N * 128);
           if (kLatent && p.rest) {
-            k_at = rest + (kPlaces == 2 ? b * kChunk : 0);
-            mbar_wait_warp(smem_addr(&sm.rest_full[b]), (tile >> 1) & 1, guard);
+            k_at = rest;
+            mbar_wait_warp(smem_addr(&sm.rest_full), tile & 1, guard);
           } else {
             k_at = ring + at.slot * kPiece;
             mbar_wait_warp(come + keys.slot * 8, keys.phase, guard);
@@ -606,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 #pragma unroll 1
           for (; left > 0; left -= 16, k_at += 32, q_piece += 32, add = true) mma16_step(d, operand(k_at, 16), operand(q_piece, 16), kInst, add);
           if (kLatent && p.rest) {
-            if (!p.rest_is_p) commit(smem_addr(&sm.rest_empty[b]));
+            if (!p.rest_is_p) commit(smem_addr(&sm.rest_empty));
           } else {
             if (!kLatent || whole_pieces >= p.v_pieces) commit(empty + at.slot * 8);
             at.step(p.slots);
@@ -662,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           at.step(p.slots);
         }
         if (kLatent) at.step(p.slots, k_ring - p.v_pieces);
-        if (kLatent && p.rest_is_p) commit(smem_addr(&sm.rest_empty[b]));
+        if (kLatent && p.rest_is_p) commit(smem_addr(&sm.rest_empty));
         commit(smem_addr(&sm.o_done[b]));
       }
     }
@@ -1033,19 +1032,19 @@ int run(Params& p, int device, int smem_limit, bool joins, cudaStream_t stream) 
   const int extra = static_cast<int>(sizeof(Smem<N>)) + 1024;
   p.q_bytes = p.k_chunks * N * 128;
   p.rest_is_p = 0;
-  constexpr int kExtra = places<kLatent> * kChunk;  // for P, and for the rest
-  int room = smem_limit - extra - static_cast<int>(p.q_bytes) - kExtra;  // for the ring and, where it is not P, the rest
+  constexpr int kPBytes = places<kLatent> * kChunk;
+  int room = smem_limit - extra - static_cast<int>(p.q_bytes) - kPBytes;  // for the ring and, where it is not P, the rest
   if (p.rest) {
-    // buffers of its own for the rest let a later tile's last keys come early, if the ring loses nothing by it
-    p.rest_is_p = (room - kExtra) / kPiece < room / kPiece;
-    if (!p.rest_is_p) room -= kExtra;
+    // a buffer of its own for the rest lets the next tile's last keys come early, if the ring loses nothing by it
+    p.rest_is_p = (room - kChunk) / kPiece < room / kPiece;
+    if (!p.rest_is_p) room -= kChunk;
   }
   p.slots = room / kPiece < kMaxSlots ? room / kPiece : kMaxSlots;
   const int k_ring = p.k_pieces - p.rest;
   if (p.slots < (p.latent && k_ring > 2 ? k_ring : 2) || (!p.latent && p.pack > 1 && p.slots < p.v_pieces)) return TOPK_ERR_PLAN;
   p.tmem_cols = 32;
   while (p.tmem_cols < static_cast<uint32_t>((p.v_pieces + 2) * N)) p.tmem_cols *= 2;
-  const size_t smem = p.q_bytes + static_cast<size_t>(p.slots) * kPiece + (p.rest && !p.rest_is_p ? kExtra : 0) + kExtra + extra;
+  const size_t smem = p.q_bytes + static_cast<size_t>(p.slots) * kPiece + (p.rest && !p.rest_is_p ? kChunk : 0) + kPBytes + extra;
   static int granted[kMaxDevices];
   int rc = allow_smem(attention_kernel<N, kBf16, kLatent>, smem_limit, device, granted);
   if (rc != TOPK_OK) return rc;
