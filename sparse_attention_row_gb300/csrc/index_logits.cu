@@ -24,11 +24,12 @@
 // What bounds it. Decoding reads every key once: 32 requests of two rows of 64 heads
 // over 100 K to 160 K tokens take 174 us (6.3 TB/s, bf16), 64 rows over 8 K to 32 K
 // 8-bit keys 39 us (4.6 TB/s: a step of 32 KB costs some 1400 cycles of hand-overs between
-// its warps, about what its data takes). A prompt's piece is bounded by the sums: one maximum
-// and half a fused multiply-add a token, row and head, 512 rows of 64 heads over 16 K
-// tokens in 126 us (1070 TFLOP/s). All of it depends on short loops: each spilled register
-// and each unrolled look-up in them showed (8-bit keys: 57 us with 80 registers a thread, 42
-// with 96).
+// its warps, about what its data takes). A prompt's piece keeps no unit busy (tensor pipe
+// 44%, issue 48%): a place of 256 columns is multiplied in 1024 cycles, in which the
+// warps that are to sum it wait, and summed while the other place is multiplied. 512
+// rows of 64 heads over 16 K tokens take 122 us (1110 TFLOP/s). All of it depends on short
+// loops: spills and unrolled look-ups in them showed (8-bit keys: 57 us with 80 registers
+// a thread, 42 with 96, at which 20 bytes a thread are still spilled).
 #include "cache_map.cuh"
 #include "paged.cuh"
 #include "umma.cuh"

@@ -15,7 +15,7 @@
 // it, and the one that draws the last ticket writes taken_out (and sets the
 // ticket back to zero).
 //
-// Bound by latency (4.5 us for 64 requests with a token each), and by the 16 bytes that
+// Bound by latency (4.8 us for 64 requests with a token each), and by the 16 bytes that
 // are written a token: lists for two million tokens, half of them new ones of 512 requests,
 // take 16 us (2 TB/s).
 #include "paged.cuh"

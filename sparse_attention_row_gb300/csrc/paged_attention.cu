@@ -35,14 +35,14 @@
 // by 2^7, so that small probabilities keep their bits).
 //
 // What bounds it. Grouped heads read every byte once: 64 rows of 32 heads over 4
-// key-value heads and 8 K to 32 K tokens run at the speed of the memory (370 to 380 us, 7.1
-// TB/s). Latent attention is bounded by the chain of a tile's steps. Its 147 KB of keys and
+// key-value heads and 8 K to 32 K tokens run at the speed of the memory (380 us on the
+// device, 392 a call among others: 7.1 and 6.8 TB/s). Latent attention is bounded by the chain of a tile's steps. Its 147 KB of keys and
 // 64 columns' queries fill shared memory, so the next tile's keys can only come while this
 // one's values are multiplied and leave the ring: at N = 64 some 1850 cycles for the values'
 // products, 1500 until the last keys are there, 950 for the scores that wait for them and
 // 1150 for the softmax, 6000 in all, of which the products read shared memory for 3260 (48 to
 // 50 cycles an instruction, 39 to 42 at N = 16). 1024 rows of 64 heads over 2048 tokens each
-// take 369 us (790 TFLOP/s), 64 rows of 128 heads over 2048 of 8 K to 32 K tokens 63 us. Tiles of
+// take 372 us (786 TFLOP/s), 64 rows of 128 heads over 2048 of 8 K to 32 K tokens 64 us. Tiles of
 // 64 tokens, of which two fit, were slower (540 and 90 us): their products read more shared
 // memory a token, and copies and products meet there all the time.
 #include <cfloat>
