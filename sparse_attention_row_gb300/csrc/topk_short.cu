@@ -189,7 +189,9 @@ __device__ __noinline__ bool wait_piece(unsigned long long* bar, uint32_t parity
 // until that kernel has completed and its writes are visible (at once when
 // there is none, or when the launch did not allow the early start). The signal
 // that follows lets the next kernel on the stream start early in the same way:
-// that kernel waits for this one's completion before it reads its output.
+// that kernel waits for this one's completion before it reads its output. Lengths
+// and logits are read by plain loads: __ldg wants memory that nothing writes while
+// the kernel runs, and their producer may still be running when it begins.
 __device__ __forceinline__ void wait_previous_grid() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -357,12 +359,12 @@ struct Src {
 
 __device__ __forceinline__ float4 load_group(const Smem& s, const Src& src, int v) {
   if (src.ring0 >= 0) return reinterpret_cast<const float4*>(s.row)[(src.ring0 + v) % kRingF4];
-  if (src.cs == 1) return __ldg(reinterpret_cast<const float4*>(src.g) + v);
+  if (src.cs == 1) return reinterpret_cast<const float4*>(src.g)[v];
   float f[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int e = 4 * v + j;
-    f[j] = (e < src.len) ? __ldg(src.g + static_cast<int64_t>(e) * src.cs) : 0.0f;
+    f[j] = (e < src.len) ? src.g[static_cast<int64_t>(e) * src.cs] : 0.0f;
   }
   return make_float4(f[0], f[1], f[2], f[3]);
 }
@@ -760,9 +762,9 @@ __global__ void __launch_bounds__(kThreads, 1) topk_short_kernel(const Params p)
   // when the first length is in, warp 1 issues the rest of the blind pieces
   // and then the row's own window up to a ring's worth, so the seed's piece is
   // queued behind none of them and few pieces are fetched past the row.
-  const int32_t len_raw0 = __ldg(p.lengths + r);
+  const int32_t len_raw0 = p.lengths[r];
   // thread 0 holds the raw length of the next row, loaded a row ahead of its use
-  int32_t nl_raw = (tid == 0 && r + gridDim.x < p.num_rows) ? __ldg(p.lengths + r + gridDim.x) : 0;
+  int32_t nl_raw = (tid == 0 && r + gridDim.x < p.num_rows) ? p.lengths[r + gridDim.x] : 0;
   int blind = 0;  // pieces of the first row in flight before its length is known
   if (bulk) blind = min(make_win(p, r, static_cast<int>(p.max_len)).np, kBlind);  // the same in every thread
   if (warp == 0) {
@@ -804,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1) topk_short_kernel(const Params p)
     if (tid == 0) {
       s.len_next = (rn < p.num_rows) ? clamp_len(p, nl_raw, true) : 0;
       const int64_t rnn = rn + gridDim.x;
-      nl_raw = (rnn < p.num_rows) ? __ldg(p.lengths + rnn) : 0;
+      nl_raw = (rnn < p.num_rows) ? p.lengths[rnn] : 0;
     }
     const Win w = make_win(p, r, len);
     int32_t* o = p.out + r * static_cast<int64_t>(K);
@@ -828,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1) topk_short_kernel(const Params p)
       if (!bulk) {
         // strided rows: every thread loads its elements into the window
         const int64_t cs = p.col_stride;
-        for (int e = tid; e < len; e += kThreads) s.row[e] = __ldg(w.rowp + static_cast<int64_t>(e) * cs);
+        for (int e = tid; e < len; e += kThreads) s.row[e] = w.rowp[static_cast<int64_t>(e) * cs];
         __syncthreads();
       }
       // ---- seed: the top 12 key bits of piece 0 (slot S) and its largest key. Warp 0
@@ -1532,7 +1534,7 @@ __global__ void __launch_bounds__(kThreads, 1) topk_short_cluster_kernel(const P
   // last slot, so that every CTA finds the same threshold from the same bytes
   // without waiting for CTA 0; its own piece kRing - 1 follows once the seed
   // is read.
-  const int32_t len_raw = __ldg(p.lengths + r);
+  const int32_t len_raw = p.lengths[r];
   const Win wmax = make_win(p, r, static_cast<int>(p.max_len));
   const int blind = min(wmax.np > me ? (wmax.np - me + C - 1) / C : 0, kBlind);
   const int S = me == 0 ? 0 : kRing - 1;  // the seed sample's slot

@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kThreads) topk_sort_kernel(const SortParams p)
       if (i < K) {
         const int32_t x = row_idx[i];
         if (x >= 0 && x < p.max_len) {
-          const uint32_t vk = value_key(__ldg(row + static_cast<int64_t>(x) * p.col_stride));
+          const uint32_t vk = value_key(row[static_cast<int64_t>(x) * p.col_stride]);
           k = (static_cast<unsigned long long>(~vk) << 32) | static_cast<uint32_t>(x);
         }
       }
@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kThreads) topk_sort_kernel(const SortParams p)
       const unsigned long long k = keys[i];
       const int32_t x = (k == ~0ull) ? -1 : static_cast<int32_t>(k & 0xFFFFFFFFull);
       if (p.sort) row_idx[i] = x;
-      if (row_val) row_val[i] = (x >= 0) ? __ldg(row + static_cast<int64_t>(x) * p.col_stride)
+      if (row_val) row_val[i] = (x >= 0) ? row[static_cast<int64_t>(x) * p.col_stride]
                                          : -__int_as_float(0x7F800000);
     }
     __syncthreads();  // the next row reuses the keys

@@ -169,3 +169,38 @@ def test_logits_of_runs_of_any_length(dec, heads, dtype):
     past = want.isnan()
     assert (got[past] == 7.25).all() and ((got - want).abs()[~past] <= tol[~past]).all()
     assert dec.status() == 0
+
+
+@pytest.mark.parametrize("tokens", [3000, 40000])
+def test_the_selection_reads_the_logits_that_were_just_written(dec, tokens):
+    # map, logits and selection back to back into the same buffers, the queries and lengths in turn: each selection is that of
+    # its own logits, whose kernel lets the next begin early
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rows, block, topk, selector = 12, 64, 512, sar.Selector(0)
+    columns = -(-tokens // block)
+    table = torch.randperm(rows * columns, generator=g, device="cuda").int().view(rows, columns)
+    keys = torch.randn((rows * columns, block, 128), generator=g, device="cuda", dtype=torch.float16)
+    sets = [(torch.randn((rows, 32, 128), generator=g, device="cuda", dtype=torch.float16), torch.randn((rows, 32), generator=g, device="cuda"),
+             torch.randint(tokens // 2 // block, tokens // block, (rows,), generator=g, device="cuda").int() * block + 1 + i) for i in range(3)]
+    new, free, taken, after = torch.ones_like(sets[0][2]), torch.arange(rows, device="cuda", dtype=torch.int32), dev([0]), dev([0])
+    logits = torch.zeros((rows, columns * block), device="cuda")
+    made = sar.KvMap(torch.zeros(rows, dtype=torch.int64, device="cuda"), dev([0] * rows), dev([0] * rows), dev([0] * (rows + 1)))
+    want = []
+    for q, w, context in sets:
+        torch.cuda.synchronize()
+        logits.fill_(float("-inf"))
+        dec.index_logits(q, w, keys, table, context + 1, out=logits)
+        torch.cuda.synchronize()
+        # a set of indices, by value: ties are not expected among so few
+        want.append(torch.topk(logits, topk, dim=1).indices.sort(1).values)
+    got = []
+    torch.cuda.synchronize()
+    for i in range(30):
+        q, w, context = sets[i % 3]
+        dec.kv_map(context, new, table, free, taken, block, rows, taken_out=after, out=made)
+        dec.index_logits(q, w, keys, table, made.row_lens, out=logits)
+        got.append((i % 3, selector(logits, made.row_lens, topk)))
+    torch.cuda.synchronize()
+    for i, picked in got:
+        assert torch.equal(picked.long().sort(1).values, want[i])
+    assert dec.status() == 0 and selector.status() == 0
