@@ -97,7 +97,7 @@ struct Params {
   int32_t k_pieces, v_pieces;
   int32_t latent;        // values are the first dims of the keys
   int32_t rest;          // 1: the last 64 dims of latent keys, which are no values, have a buffer of their own
-  int32_t rest_is_p;     // 1: which is P's, who takes it after it has been used
+  int32_t rest_is_p;     // 1: which is P's place, free until the tile's probabilities are written
   int32_t slots;         // of the ring
   int32_t slices;
   int32_t row_tiles;     // tiles of every unit where index lists are given, else 0
