@@ -474,6 +474,232 @@ size_t topk_attention_workspace_size(int device);
 
 int topk_paged_attention(const topk_attention_args* args, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Blocks that a cheap score selects. A block is a page of the cache, and its score
+ * for a row's key-value head is the product of the head's queries with the mean key
+ * of the page. A step is
+ *   topk_block_means      the means of the pages that the step wrote to,
+ *   topk_block_scores     a score for every block that a row sees, and how many it sees,
+ *   topk_ragged           the selection: its rows are the (row, key-value head) pairs,
+ *   topk_block_attention  attention over the tokens of the selected blocks.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * means[b, g, :] = mean over the tokens held by page b of k[b, t, g, :], for every page in
+ * which one of the requests has got new tokens: request r, which had context_lens[r]
+ * tokens, has new_lens[r] more (negative reads as 0), and the last page counts the tokens that it
+ * holds. Other pages' means are left as they are. Sums are in fp32 and rounded once. A page
+ * outside the cache, or past the table's last column, is skipped (TOPK_DEV_BAD_BLOCK, TOPK_DEV_TABLE_FULL).
+ * Types f16 and bf16; dk 8..576 in multiples of 8, kv_heads 1..1024; k and means are accessed in pieces of
+ * 16 bytes: addresses and strides are multiples of that.
+ */
+typedef struct {
+  const int32_t* context_lens; /* [num_requests] */
+  const int32_t* new_lens;     /* [num_requests] */
+  int64_t num_requests;        /* 0..2^31-1; 1024 rows of the table, or all of them, have fewer than 2^32 entries */
+  int block_size;              /* >= 1 */
+  int dtype;                   /* TOPK_DTYPE_F16 or TOPK_DTYPE_BF16: of k and means */
+  const int32_t* block_table;  /* [num_requests, max_blocks] */
+  int64_t table_stride;        /* >= max_blocks */
+  int64_t max_blocks;          /* columns of the table, >= 1 */
+  int64_t num_blocks;          /* pages of the cache */
+  int kv_heads, dk;
+  const void* k; /* [num_blocks, block_size, kv_heads, dk], strides in elements, the last one 1 */
+  int64_t k_block_stride, k_token_stride, k_head_stride;
+  void* means; /* [num_blocks, kv_heads, dk] */
+  int64_t mean_block_stride, mean_head_stride;
+  void* workspace; /* TOPK_PAGED_WORKSPACE_BYTES, 16-byte aligned */
+} topk_block_means_args;
+
+int topk_block_means(const topk_block_means_args* args, void* stream);
+
+/*
+ * scores[r, g, j] = (sum of q[r, h, :] over the heads h of group g) . means[page of block j, g, :]
+ * for every block j < n_r = ceil(len_r / block_size) of the row, and score_lens[r, g] = n_r: the logits and the
+ * lengths with which topk_ragged selects each (row, head)'s blocks. The row's first sink_blocks and last
+ * recent_blocks blocks score +inf, so that they are selected first. Entries from n_r on are not
+ * written. Sums and products are in fp32. A block whose page lies outside the cache scores -inf
+ * (TOPK_DEV_BAD_BLOCK), and its mean is not read.
+ * heads 1..1024, dk 8..576 in multiples of 8; types f16 and bf16; q and means are read in pieces of 16 bytes.
+ */
+typedef struct {
+  topk_paged_rows rows;
+  int dtype; /* of q and means */
+  int heads, kv_heads, dk;
+  int sink_blocks, recent_blocks; /* >= 0 */
+  const void* q;                  /* [num_rows, heads, dk], strides in elements, the last one 1 */
+  int64_t q_row_stride, q_head_stride;
+  const void* means; /* [num_blocks, kv_heads, dk] */
+  int64_t mean_block_stride, mean_head_stride;
+  float* scores; /* [num_rows, kv_heads, max_columns] */
+  int64_t score_row_stride, score_head_stride;
+  int64_t max_columns; /* blocks past them are not scored, nor counted in score_lens (TOPK_DEV_LENGTH_CLAMPED) */
+  int32_t* score_lens; /* [num_rows, kv_heads], contiguous */
+  void* workspace;     /* TOPK_PAGED_WORKSPACE_BYTES, 16-byte aligned */
+} topk_block_scores_args;
+
+int topk_block_scores(const topk_block_scores_args* args, void* stream);
+
+/*
+ * topk_paged_attention of each row's key-value heads over blocks of their own: the heads of
+ * group g of row r see the tokens t < len_r of the blocks that blocks[r, g, :] names (columns of the request's row of
+ * the table). Blocks may stand in any order; one that the row does not have is skipped (the -1 padding
+ * of topk_ragged), a repeated one counts as often as it stands there. `attention.indices` is NULL;
+ * everything else is as in topk_paged_attention.
+ */
+typedef struct {
+  topk_attention_args attention;
+  const int32_t* blocks; /* [num_rows, kv_heads, num_chosen] */
+  int64_t block_row_stride, block_head_stride; /* >= 0; a head stride of 0: one list for all heads of a row */
+  int64_t num_chosen;                          /* >= 1; num_chosen * block_size < 2^30 */
+} topk_block_attention_args;
+
+int topk_block_attention(const topk_block_attention_args* args, void* stream);
+
+/*
+ * topk_paged_attention over everything cached (`attention.indices` is NULL), for requests of which some
+ * begin with the same pages: request b begins with the first prefix_lens[prefix_of[b]] tokens of the
+ * pages in prefix_table's row prefix_of[b]. The whole pages among those are read once for all rows, next to
+ * each other, that begin with them, and not through the requests' own rows of the table. Lengths
+ * count all tokens, the prefix's among them. A request whose prefix_of is negative begins with nothing shared; so
+ * does, whatever it names, one of which some row sees fewer tokens than those whole pages hold.
+ * The results are those of topk_paged_attention where the requests' own rows of the table name the same pages,
+ * but that the part behind the prefix is rounded to the type of `out` before both are joined.
+ * `attention.lse` must be given: it holds the statistics of that part meanwhile.
+ */
+typedef struct {
+  topk_attention_args attention;
+  const int32_t* prefix_of;    /* [num_requests] */
+  int64_t num_prefixes;        /* 0..2^31-1; a prefix_of at or above it: TOPK_DEV_BAD_BLOCK, nothing shared */
+  const int32_t* prefix_lens;  /* [num_prefixes] tokens; clamped into [0, prefix_blocks * block_size] */
+  const int32_t* prefix_table; /* [num_prefixes, prefix_blocks] */
+  int64_t prefix_stride;       /* elements between its rows, >= prefix_blocks */
+  int64_t prefix_blocks;       /* >= 1 */
+  void* scratch;               /* 16-byte aligned; nothing in it outlives the call */
+  size_t scratch_bytes;        /* at least topk_shared_attention_scratch_size */
+} topk_shared_attention_args;
+
+/* Scratch that topk_shared_attention needs on `device` for this many rows; 0 if the device cannot be queried. */
+size_t topk_shared_attention_scratch_size(int device, int64_t num_rows);
+
+int topk_shared_attention(const topk_shared_attention_args* args, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The pages themselves. Tables, the list of free pages and `taken` are topk_kv_map's: free_blocks[taken ..
+ * num_free) may be handed out, and what comes back is put in front of them. `shares` counts, for each
+ * page, its holders beyond the first: rows of the table that name it, less one; 0 for a page with one holder or none.
+ * So topk_kv_map need not know of it. A row of the table names a page at most once, and holds -1 where it has none.
+ * All results are the same every time; calls on the same tables and lists are made on one stream.
+ * Each is one launch; num_blocks, num_free and num_requests * max_blocks are below 2^31.
+ * ------------------------------------------------------------------------ */
+
+/* What the calls work on. */
+typedef struct {
+  int32_t* block_table; /* [num_requests, max_blocks] */
+  int64_t num_requests;
+  int64_t table_stride; /* >= max_blocks */
+  int64_t max_blocks;   /* >= 1 */
+  int32_t* shares;      /* [num_blocks] */
+  int64_t num_blocks;
+  int32_t* free_blocks; /* [num_free] */
+  int64_t num_free;
+  int32_t* taken;  /* [1] */
+  void* workspace; /* TOPK_PAGED_WORKSPACE_BYTES, 16-byte aligned */
+} topk_page_pool;
+
+/*
+ * Forks requests: the i-th child gets the first kept_lens[i] tokens of its parent. It shares the
+ * parent's whole pages; if tokens are left, it gets a page of its own for them, the next free one, and the copy
+ * parent's page -> new page is listed. The child's row is written in full (-1 behind), whatever it held: free
+ * what a child holds first. Lists that name a child twice, or a child as parent, are not allowed (the
+ * call stays within its memory; the result is unspecified).
+ * A parent or child outside the table: nothing is done for the pair (TOPK_DEV_BAD_BLOCK). Where the
+ * parent has no page, or one outside the pool, or where no free page is left, the child's entry is -1
+ * (TOPK_DEV_BAD_BLOCK, TOPK_DEV_BLOCKS_EXHAUSTED). Lengths are clamped into the table's width.
+ */
+typedef struct {
+  topk_page_pool pool;
+  const int32_t* parents;   /* [num_forks] rows of the table */
+  const int32_t* children;  /* [num_forks] */
+  const int32_t* kept_lens; /* [num_forks] tokens */
+  int64_t num_forks;        /* 0..2^31-1 */
+  int block_size;           /* >= 1 */
+  int32_t* source;          /* [num_forks] page to copy from, -1: nothing to copy */
+  int32_t* target;          /* [num_forks] page to copy to */
+} topk_page_fork_args;
+
+int topk_page_fork(const topk_page_fork_args* args, void* stream);
+
+/*
+ * Frees requests: each page of their rows loses a holder, and the rows are set to -1. A page without holders goes
+ * back on the list: those of the call together in front of the others, in the order in which the requests are
+ * listed and of their columns. A request outside the table is skipped (TOPK_DEV_BAD_BLOCK), as is an entry outside the pool; one
+ * that is listed twice has nothing the second time. Pages for which the list has no room in front (more come back than
+ * were taken) are dropped (TOPK_DEV_BLOCKS_EXHAUSTED).
+ */
+typedef struct {
+  topk_page_pool pool;
+  const int32_t* requests; /* [num_freed] rows of the table */
+  int64_t num_freed;       /* 0..2^20; num_freed * max_blocks < 2^31 - 2^16 */
+} topk_page_free_args;
+
+int topk_page_free(const topk_page_free_args* args, void* stream);
+
+/*
+ * Compacts the pool: pages that the table names move to lower numbers. The highest of them takes the place of the lowest free
+ * page, the second highest that of the second lowest, and so on, while that lowers a number and `max_copies` moves
+ * are not yet made. Lists the moves, whose contents topk_page_copy then brings over; writes the table and the shares
+ * with the pages' new numbers, and the free pages in rising order to free_blocks[taken ..). Pages that
+ * neither the table nor the list names stay where they are. A free page that the table names as well is taken off
+ * the list, one that is listed twice, or is none of the pool, likewise (TOPK_DEV_BAD_BLOCK; taken rises). Outputs may be the inputs themselves;
+ * entries free_blocks_out[0 .. taken_out) are copied from free_blocks.
+ * `scratch`: 12 * num_blocks bytes, 16-byte aligned; nothing in it outlives the call.
+ */
+typedef struct {
+  topk_page_pool pool;
+  int64_t max_copies; /* 0..2^31-1 */
+  int32_t* source;    /* [max_copies] page to copy from, -1 behind the last move */
+  int32_t* target;    /* [max_copies] page to copy to */
+  int32_t* block_table_out; /* [num_requests, max_blocks], stride table_out_stride */
+  int64_t table_out_stride;
+  int32_t* shares_out;      /* [num_blocks] */
+  int32_t* free_blocks_out; /* [num_free] */
+  int32_t* taken_out;       /* [1] */
+  void* scratch;
+  size_t scratch_bytes;
+} topk_page_compact_args;
+
+int topk_page_compact(const topk_page_compact_args* args, void* stream);
+
+/* A cache whose pages are copied: page b holds n0 * n1 runs of run_bytes, at base + b * block_stride + i * stride0 + j * stride1
+ * (in bytes, i < n0, j < n1). */
+typedef struct {
+  void* base;
+  int64_t num_blocks;
+  int64_t block_stride, stride0, stride1;
+  int32_t n0, n1;
+  int64_t run_bytes;
+} topk_page_cache;
+
+#define TOPK_MAX_PAGE_CACHES 256
+
+/*
+ * Copies page source[i] to page target[i] in every one of the caches (layers' keys, values, scales, means), for i < num_copies.
+ * Pairs with a negative page are skipped; so are pairs with a page outside a cache, in that cache (TOPK_DEV_BAD_BLOCK). A page may be
+ * the source of several pairs; no target is listed twice, or as a source. Pieces are as wide as addresses,
+ * strides and run_bytes of a cache allow, 16 bytes at most.
+ */
+typedef struct {
+  const int32_t* source; /* [num_copies] */
+  const int32_t* target;
+  int64_t num_copies;            /* 0..2^31-1 */
+  const topk_page_cache* caches; /* HOST array [num_caches], read before the call returns */
+  int num_caches;                /* 0..TOPK_MAX_PAGE_CACHES */
+  void* workspace;               /* TOPK_PAGED_WORKSPACE_BYTES, 16-byte aligned */
+} topk_page_copy_args;
+
+int topk_page_copy(const topk_page_copy_args* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -22,7 +22,11 @@ __all__ = [
     "topk_get_status", "topk_status_string", "topk_query_device", "topk_make_plan",
     "topk_kv_map", "topk_index_logits", "topk_paged_attention", "topk_attention_workspace_size",
     "TopkPagedRows", "TopkKvMapArgs", "TopkIndexLogitsArgs", "TopkAttentionArgs",
-    "library_path", "Selector", "PagedDecoder", "KvMap",
+    "topk_block_means", "topk_block_scores", "topk_block_attention", "topk_shared_attention", "topk_shared_attention_scratch_size",
+    "topk_page_fork", "topk_page_free", "topk_page_compact", "topk_page_copy",
+    "TopkBlockMeansArgs", "TopkBlockScoresArgs", "TopkBlockAttentionArgs", "TopkSharedAttentionArgs", "TopkPagePool",
+    "TopkPageForkArgs", "TopkPageFreeArgs", "TopkPageCompactArgs", "TopkPageCache", "TopkPageCopyArgs",
+    "library_path", "Selector", "PagedDecoder", "KvMap", "PageCopies", "PageCaches",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -66,11 +70,14 @@ TOPK_DTYPE_BF16 = 2
 TOPK_DTYPE_F8E4M3 = 3
 
 TOPK_PAGED_WORKSPACE_BYTES = 256
+TOPK_MAX_PAGE_CACHES = 256
 
 EXPORTED = ("topk_workspace_size", "topk_workspace_init", "topk_ragged", "topk_ragged_ex", "topk_ragged_static",
             "topk_ragged_strided", "topk_gather_sort", "topk_get_status", "topk_status_string",
             "topk_query_device", "topk_make_plan", "topk_kv_map", "topk_index_logits", "topk_paged_attention",
-            "topk_attention_workspace_size")
+            "topk_attention_workspace_size", "topk_block_means", "topk_block_scores", "topk_block_attention",
+            "topk_shared_attention", "topk_shared_attention_scratch_size", "topk_page_fork", "topk_page_free",
+            "topk_page_compact", "topk_page_copy")
 
 
 class TopkError(RuntimeError):
@@ -158,6 +165,71 @@ class TopkAttentionArgs(ctypes.Structure):
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
+class TopkBlockMeansArgs(ctypes.Structure):
+    _fields_ = [("context_lens", ctypes.c_void_p), ("new_lens", ctypes.c_void_p), ("num_requests", ctypes.c_int64),
+                ("block_size", ctypes.c_int), ("dtype", ctypes.c_int), ("block_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("max_blocks", ctypes.c_int64), ("num_blocks", ctypes.c_int64),
+                ("kv_heads", ctypes.c_int), ("dk", ctypes.c_int), ("k", ctypes.c_void_p),
+                ("k_block_stride", ctypes.c_int64), ("k_token_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+                ("means", ctypes.c_void_p), ("mean_block_stride", ctypes.c_int64), ("mean_head_stride", ctypes.c_int64),
+                ("workspace", ctypes.c_void_p)]
+
+
+class TopkBlockScoresArgs(ctypes.Structure):
+    _fields_ = [("rows", TopkPagedRows), ("dtype", ctypes.c_int), ("heads", ctypes.c_int), ("kv_heads", ctypes.c_int),
+                ("dk", ctypes.c_int), ("sink_blocks", ctypes.c_int), ("recent_blocks", ctypes.c_int), ("q", ctypes.c_void_p),
+                ("q_row_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64), ("means", ctypes.c_void_p),
+                ("mean_block_stride", ctypes.c_int64), ("mean_head_stride", ctypes.c_int64), ("scores", ctypes.c_void_p),
+                ("score_row_stride", ctypes.c_int64), ("score_head_stride", ctypes.c_int64),
+                ("max_columns", ctypes.c_int64), ("score_lens", ctypes.c_void_p), ("workspace", ctypes.c_void_p)]
+
+
+class TopkBlockAttentionArgs(ctypes.Structure):
+    _fields_ = [("attention", TopkAttentionArgs), ("blocks", ctypes.c_void_p), ("block_row_stride", ctypes.c_int64),
+                ("block_head_stride", ctypes.c_int64), ("num_chosen", ctypes.c_int64)]
+
+
+class TopkSharedAttentionArgs(ctypes.Structure):
+    _fields_ = [("attention", TopkAttentionArgs), ("prefix_of", ctypes.c_void_p), ("num_prefixes", ctypes.c_int64),
+                ("prefix_lens", ctypes.c_void_p), ("prefix_table", ctypes.c_void_p), ("prefix_stride", ctypes.c_int64),
+                ("prefix_blocks", ctypes.c_int64), ("scratch", ctypes.c_void_p), ("scratch_bytes", ctypes.c_size_t)]
+
+
+class TopkPagePool(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("num_requests", ctypes.c_int64), ("table_stride", ctypes.c_int64),
+                ("max_blocks", ctypes.c_int64), ("shares", ctypes.c_void_p), ("num_blocks", ctypes.c_int64),
+                ("free_blocks", ctypes.c_void_p), ("num_free", ctypes.c_int64), ("taken", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p)]
+
+
+class TopkPageForkArgs(ctypes.Structure):
+    _fields_ = [("pool", TopkPagePool), ("parents", ctypes.c_void_p), ("children", ctypes.c_void_p),
+                ("kept_lens", ctypes.c_void_p), ("num_forks", ctypes.c_int64), ("block_size", ctypes.c_int),
+                ("source", ctypes.c_void_p), ("target", ctypes.c_void_p)]
+
+
+class TopkPageFreeArgs(ctypes.Structure):
+    _fields_ = [("pool", TopkPagePool), ("requests", ctypes.c_void_p), ("num_freed", ctypes.c_int64)]
+
+
+class TopkPageCompactArgs(ctypes.Structure):
+    _fields_ = [("pool", TopkPagePool), ("max_copies", ctypes.c_int64), ("source", ctypes.c_void_p),
+                ("target", ctypes.c_void_p), ("block_table_out", ctypes.c_void_p), ("table_out_stride", ctypes.c_int64),
+                ("shares_out", ctypes.c_void_p), ("free_blocks_out", ctypes.c_void_p), ("taken_out", ctypes.c_void_p),
+                ("scratch", ctypes.c_void_p), ("scratch_bytes", ctypes.c_size_t)]
+
+
+class TopkPageCache(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("num_blocks", ctypes.c_int64), ("block_stride", ctypes.c_int64),
+                ("stride0", ctypes.c_int64), ("stride1", ctypes.c_int64), ("n0", ctypes.c_int32), ("n1", ctypes.c_int32),
+                ("run_bytes", ctypes.c_int64)]
+
+
+class TopkPageCopyArgs(ctypes.Structure):
+    _fields_ = [("source", ctypes.c_void_p), ("target", ctypes.c_void_p), ("num_copies", ctypes.c_int64),
+                ("caches", ctypes.c_void_p), ("num_caches", ctypes.c_int), ("workspace", ctypes.c_void_p)]
+
+
 def library_path() -> str:
     return _LIB_PATH
 
@@ -198,11 +270,15 @@ def _load():
         lib.topk_make_plan.restype = i32
         lib.topk_make_plan.argtypes = [ctypes.POINTER(TopkDeviceProps), i64, i64, i32, i32,
                                        ctypes.POINTER(TopkOptions), ctypes.POINTER(TopkPlan)]
-        for name in ("topk_kv_map", "topk_index_logits", "topk_paged_attention"):
+        for name in ("topk_kv_map", "topk_index_logits", "topk_paged_attention", "topk_block_means", "topk_block_scores",
+                     "topk_block_attention", "topk_shared_attention", "topk_page_fork", "topk_page_free", "topk_page_compact",
+                     "topk_page_copy"):
             getattr(lib, name).restype = i32
             getattr(lib, name).argtypes = [vp, vp]
         lib.topk_attention_workspace_size.restype = ctypes.c_size_t
         lib.topk_attention_workspace_size.argtypes = [i32]
+        lib.topk_shared_attention_scratch_size.restype = ctypes.c_size_t
+        lib.topk_shared_attention_scratch_size.argtypes = [i32, i64]
         _lib = lib
         return lib
 
@@ -323,6 +399,42 @@ def topk_attention_workspace_size(device: int) -> int:
     return int(_load().topk_attention_workspace_size(device))
 
 
+def topk_block_means(args: TopkBlockMeansArgs, stream=None) -> int:
+    return int(_load().topk_block_means(ctypes.byref(args), _stream(stream)))
+
+
+def topk_block_scores(args: TopkBlockScoresArgs, stream=None) -> int:
+    return int(_load().topk_block_scores(ctypes.byref(args), _stream(stream)))
+
+
+def topk_block_attention(args: TopkBlockAttentionArgs, stream=None) -> int:
+    return int(_load().topk_block_attention(ctypes.byref(args), _stream(stream)))
+
+
+def topk_shared_attention(args: TopkSharedAttentionArgs, stream=None) -> int:
+    return int(_load().topk_shared_attention(ctypes.byref(args), _stream(stream)))
+
+
+def topk_page_fork(args: TopkPageForkArgs, stream=None) -> int:
+    return int(_load().topk_page_fork(ctypes.byref(args), _stream(stream)))
+
+
+def topk_page_free(args: TopkPageFreeArgs, stream=None) -> int:
+    return int(_load().topk_page_free(ctypes.byref(args), _stream(stream)))
+
+
+def topk_page_compact(args: TopkPageCompactArgs, stream=None) -> int:
+    return int(_load().topk_page_compact(ctypes.byref(args), _stream(stream)))
+
+
+def topk_page_copy(args: TopkPageCopyArgs, stream=None) -> int:
+    return int(_load().topk_page_copy(ctypes.byref(args), _stream(stream)))
+
+
+def topk_shared_attention_scratch_size(device: int, num_rows: int) -> int:
+    return int(_load().topk_shared_attention_scratch_size(device, num_rows))
+
+
 class Selector:
     """Owns one workspace on one device and runs calls on a stream.
 
@@ -390,4 +502,4 @@ class Selector:
             raise TopkError(rc, "topk_workspace_init")
 
 
-from .paged import KvMap, PagedDecoder  # noqa: E402
+from .paged import KvMap, PageCaches, PageCopies, PagedDecoder  # noqa: E402

@@ -1,0 +1,81 @@
+// The forms of the attention kernel (paged_attention.cu), and what each of them is given beside the call's arguments.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "libtopk.h"
+#include "paged.cuh"
+
+namespace ltk {
+namespace paged {
+
+enum class Form {
+  kPlain,   // topk_paged_attention
+  kBlocks,  // topk_block_attention: index lists name blocks, one list for each row and key-value head
+  kTail,    // topk_shared_attention, the tokens behind the prefixes: rows begin at a page of their own
+  kShared,  // topk_shared_attention, the prefixes: units are runs of rows that share one
+};
+
+// Neighbouring rows that share a prefix.
+struct SharedRun {
+  int32_t row0, rows;
+  int32_t prefix;  // row of the prefixes' table
+  int32_t length;  // tokens shared: whole pages
+};
+
+struct FormArgs {
+  // kBlocks
+  const int32_t* blocks;
+  int64_t block_row_stride, block_head_stride;
+  int64_t num_chosen;
+  // kTail
+  const int32_t* skip;  // [rows] columns of the request's table before the row's first token
+  // kShared
+  const SharedRun* runs;
+  const int32_t* run_count;
+  const int32_t* prefix_table;
+  int64_t prefix_stride;
+  int64_t prefix_most;  // tokens of a prefix at most
+  float* tail_lse;      // [slices][2][column blocks][columns]: of what is behind the prefix, for the join
+};
+
+int attend_plain(const topk_attention_args& a, const FormArgs& f, void* stream);
+int attend_blocks(const topk_attention_args& a, const FormArgs& f, void* stream);
+int attend_tail(const topk_attention_args& a, const FormArgs& f, void* stream);
+int attend_shared(const topk_attention_args& a, const FormArgs& f, void* stream);
+
+constexpr int kMaxQk = 576, kMaxV = 512;
+
+// What all forms refuse; of pointers only where there are rows.
+inline int check_attention(const topk_attention_args& a) {
+  int rc = check_rows(a.rows);
+  if (rc != TOPK_OK) return rc;
+  if (!(a.scale > 0.f) || a.scale > 3.4e38f || a.heads < 1 || a.kv_heads < 1 || a.heads % a.kv_heads != 0)
+    return TOPK_ERR_INVALID_ARG;
+  if (a.indices != nullptr && (a.num_indices < 1 || a.num_indices > (1 << 20) || a.index_row_stride < 0))
+    return TOPK_ERR_INVALID_ARG;
+  if ((a.dtype != TOPK_DTYPE_F16 && a.dtype != TOPK_DTYPE_BF16) || a.heads > 1024 || a.dk < 8 || a.dk > kMaxQk || a.dk % 8 ||
+      a.dv < 8 || a.dv > kMaxV || a.dv % 8 || (a.v == nullptr && a.dv > a.dk))
+    return TOPK_ERR_UNSUPPORTED;
+  if (a.rows.num_rows == 0) return TOPK_OK;
+  rc = check_row_pointers(a.rows);
+  if (rc != TOPK_OK) return rc;
+  if (a.q == nullptr || a.k == nullptr || a.out == nullptr || a.workspace == nullptr) return TOPK_ERR_INVALID_ARG;
+  if (misaligned(a.q, 16) || a.q_row_stride % 8 || a.q_head_stride % 8 || misaligned(a.k, 16) || a.k_block_stride % 8 ||
+      a.k_token_stride % 8 || a.k_head_stride % 8 || misaligned(a.out, 16) || a.out_row_stride % 8 || a.out_head_stride % 8 ||
+      misaligned(a.indices, 4) || misaligned(a.lse, 4) || misaligned(a.workspace, 16) ||
+      (a.v && (misaligned(a.v, 16) || a.v_block_stride % 8 || a.v_token_stride % 8 || a.v_head_stride % 8)))
+    return TOPK_ERR_MISALIGNED;
+  return TOPK_OK;
+}
+
+// Columns (rows and heads) of a unit at most, where rows share a prefix; and the rows of a run: what fills them.
+constexpr int kSharedCols = 64;
+inline int rows_of_run(const topk_attention_args& a) {
+  const int group = a.heads / a.kv_heads, rows = group >= kSharedCols ? 1 : kSharedCols / group;
+  return rows < a.rows.num_rows ? rows : static_cast<int>(a.rows.num_rows);
+}
+
+}  // namespace paged
+}  // namespace ltk

@@ -45,15 +45,29 @@
 // take 372 us (786 TFLOP/s), 64 rows of 128 heads over 2048 of 8 K to 32 K tokens 64 us. Tiles of
 // 64 tokens, of which two fit, were slower (540 and 90 us): their products read more shared
 // memory a token, and copies and products meet there all the time.
+//
+// Forms. The kernel is compiled once more for each form of the call (attention_forms.cuh says what they
+// are for): kBlocks, whose index lists name blocks, one list for each row and key-value head; kTail, whose
+// rows begin at a page of their own; kShared, whose units are runs of rows that share a prefix, and whose results are joined
+// with what kTail left in `out` and `lse`. A translation unit each, in which kForm is a constant.
 #include <cfloat>
 
+#include "attention_forms.cuh"
 #include "paged.cuh"
 #include "token_copies.cuh"
 #include "umma.cuh"
 
+#ifndef LTK_ATTENTION_FORM
+#define LTK_ATTENTION_PLAIN
+#define LTK_ATTENTION_FORM kPlain
+#define LTK_ATTENTION_CALL attend_plain
+#endif
+
 namespace ltk {
 namespace paged {
 namespace {
+
+constexpr Form kForm = Form::LTK_ATTENTION_FORM;
 
 using namespace ltk::umma;
 
@@ -70,7 +84,6 @@ constexpr int kScoreWarp = kSoftmaxWarps + kCopyWarps, kValueWarp = kScoreWarp +
 constexpr int kThreads = (kValueWarp + 1) * 32;
 constexpr int kTokenSlots = 8;  // more than the tiles that the copies can be ahead of the softmax: ring slots + 1
 constexpr int kMaxSlots = 6;
-constexpr int kMaxQk = 576, kMaxV = 512;
 constexpr int kMaxBlockCols = 64;
 constexpr int kTeam = 128, kJoinDims = 32;  // threads of a team
 constexpr int kMaxTeams = 4;                // which take the parts in turn
@@ -112,6 +125,7 @@ struct Params {
   int32_t joins;         // places for a unit's end: one for each unit, or where those are more, for each slice
   int32_t by_unit;
   int32_t teams;         // of the join
+  FormArgs f;
 };
 
 template <int N>
@@ -142,11 +156,17 @@ struct Smem {  // behind the tiles
 // Out of line: seven copies of it in a kernel that is already longer than the instruction caches like cost 3 to 5 % (and
 // fetching tokens into L2 ahead of their copies, which was tried, cost more than it brought).
 static __device__ __noinline__ int group_length(const Params& p, int64_t g) {
+  if constexpr (kForm == Form::kShared) return p.f.runs[g].length;
   int most = 0;
 #pragma unroll 1
   for (int j = 0; j < p.pack; ++j) most = max(most, row_length(p.R, g * p.pack + j));
   return most;
 }
+
+// First row of a group of rows, and the columns that it has.
+__device__ __forceinline__ int64_t group_row(const Params& p, int64_t g) { return kForm == Form::kShared ? p.f.runs[g].row0 : g * p.pack; }
+__device__ __forceinline__ int group_cols(const Params& p, int64_t g) { return kForm == Form::kShared ? p.f.runs[g].rows * p.group : p.cols; }
+__device__ __forceinline__ int columns_of_block(const Params& p, int64_t g, int block) { return min(p.block_cols, group_cols(p, g) - block * p.block_cols); }
 
 // Tiles of a unit; one at least, so that every unit is met and its rows written.
 __device__ __forceinline__ int group_tiles(const Params& p, int64_t g) {
@@ -237,6 +257,29 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     const __half2 x = __floats2half2_rn(lo, hi);
     return reinterpret_cast<const uint32_t&>(x);
   }
+}
+
+// What a prefix and the tokens behind it weigh in the whole: from the logarithms of their sums, the prefix's in powers of
+// two, the other's a natural one.
+struct Weights {
+  float prefix, tail, lse;
+};
+__device__ __forceinline__ Weights weigh(float prefix2, float tail_lse) {
+  const float tail2 = tail_lse * 1.4426950408889634f, top = fmaxf(prefix2, tail2), b = top == -INFINITY ? 0.f : top;
+  const float x = exp2f(prefix2 - b), y = exp2f(tail2 - b), sum = x + y, r = sum == 0.f ? 0.f : 1.f / sum;
+  return {x * r, y * r, sum == 0.f ? -INFINITY : (b + log2f(sum)) * 0.69314718055994531f};
+}
+
+// Two values of a row and `weight` times those behind the prefix, which stand at `at`.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t add_tail(float lo, float hi, const uint16_t* at, float weight) {
+  const uint32_t bits = *reinterpret_cast<const uint32_t*>(at);
+  float2 t;
+  if constexpr (kBf16)
+    t = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162&>(bits));
+  else
+    t = __half22float2(reinterpret_cast<const __half2&>(bits));
+  return pack2<kBf16>(lo + weight * t.x, hi + weight * t.y);
 }
 
 // A segment's queries [N][dk] into their K-major tiles, by `threads` threads (a multiple of 8); zeros past the block's columns
@@ -429,8 +472,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       sm.start_at = sm.run_begin - sm.start_group * p.a.kv_heads * p.row_tiles;
     }
   } else {
-    const int64_t per = (p.row_groups + kThreads - 1) / kThreads;
-    const int64_t g0 = min(per * tid, p.row_groups), g1 = min(g0 + per, p.row_groups);
+    const int64_t row_groups = kForm == Form::kShared ? *p.f.run_count : p.row_groups;
+    const int64_t per = (row_groups + kThreads - 1) / kThreads;
+    const int64_t g0 = min(per * tid, row_groups), g1 = min(g0 + per, row_groups);
     int64_t mine = 0;
     for (int64_t g = g0; g < g1; ++g) mine += group_tiles(p, g);
     int64_t pre = mine;
@@ -489,11 +533,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   }
   const int k_ring = p.k_pieces - p.rest;                       // pieces of the keys in the ring
   const uint32_t s_cols = static_cast<uint32_t>(p.v_pieces) * N;  // columns before the scores'
-  const int block_cols = min(p.block_cols, p.cols - block * p.block_cols);
+  const int most_cols = min(p.block_cols, p.cols - block * p.block_cols);
+  // a shared prefix's last group may have fewer rows than the others
+  const auto block_columns = [&]() { return kForm == Form::kShared ? columns_of_block(p, walk.group, block) : most_cols; };
 
   // the first segment's queries, by the warps that have nothing to do yet
   if (walk.left > 0 && warp < kSoftmaxWarps) {
-    copy_queries<N>(p, q_at, walk.group * p.pack, walk.kv_head, block, block_cols, tid, kSoftmaxWarps * 32);
+    copy_queries<N>(p, q_at, group_row(p, walk.group), walk.kv_head, block, block_columns(), tid, kSoftmaxWarps * 32);
     copies_arrive(smem_addr(&sm.q_first));
   }
   if (warp >= kSoftmaxWarps && warp < kScoreWarp) {
@@ -511,18 +557,30 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     };
     uint32_t tile = 0, segment = 0;
     for (; walk.left > 0; walk.next(p), ++segment) {
-      const int64_t row0 = walk.group * p.pack;
+      const int64_t row0 = group_row(p, walk.group);
       const int length = group_length(p, walk.group);
-      const int64_t request = length > 0 ? row_request(p.R, row0) : 0;
-      const int32_t* list = p.a.indices ? p.a.indices + row0 * p.a.index_row_stride : nullptr;
+      const int64_t request = length > 0 && kForm != Form::kShared ? row_request(p.R, row0) : 0;
+      const int32_t* pages = kForm == Form::kShared ? p.f.prefix_table + p.f.runs[walk.group].prefix * p.f.prefix_stride
+                             : kForm == Form::kTail ? p.R.block_table + request * p.R.table_stride + (length > 0 ? p.f.skip[row0] : 0)
+                                                    : nullptr;
+      const int32_t* list = kForm == Form::kBlocks ? p.f.blocks + row0 * p.f.block_row_stride + walk.kv_head * p.f.block_head_stride
+                            : p.a.indices          ? p.a.indices + row0 * p.a.index_row_stride
+                                                   : nullptr;
       // A tile's tokens are found in two steps, each a tile earlier than its result is used: the position (from
       // the list), then the block (from the table).
       const auto listed = [&](int t) {
         const int i = (walk.at + t) * kTile + me;
         if (t >= walk.count) return -1;
+        if constexpr (kForm == Form::kBlocks) {
+          const int e = block_column(p.R, i);
+          const int column = e < p.f.num_chosen ? list[e] : -1;
+          const int64_t x = static_cast<int64_t>(column) * p.R.block_size + (i - e * p.R.block_size);
+          return column >= 0 && x < length ? static_cast<int>(x) : -1;
+        }
         return !list ? i : (i < p.a.num_indices ? list[i] : -1);
       };
       const auto table_entry = [&](int x) {
+        if constexpr (kForm == Form::kTail || kForm == Form::kShared) return x >= 0 && x < length ? pages[block_column(p.R, x)] : 0;
         return x >= 0 && x < length ? p.R.block_table[request * p.R.table_stride + block_column(p.R, x)] : 0;
       };
       const auto address = [&](const void* cache, int x, int x_block, int64_t block_stride, int64_t token_stride, int64_t head_stride) {
@@ -535,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       asm volatile("" ::"r"(at_block) : "memory");  // here, before any copies are issued: a load waits behind those
       if (segment > 0) {  // the first one's are copied by the softmax warps
         mbar_wait(smem_addr(&sm.q_empty), (segment & 1) ^ 1, guard);
-        copy_queries<N>(p, q_at, row0, walk.kv_head, block, block_cols, me, kCopyThreads);
+        copy_queries<N>(p, q_at, row0, walk.kv_head, block, block_columns(), me, kCopyThreads);
         copies_arrive(smem_addr(&sm.q_full));
       }
       for (int t = 0; t < walk.count; ++t, ++tile) {
@@ -678,18 +736,19 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     uint32_t tile = 0, segment = 0;
     bool first_segment = true;
     for (; walk.left > 0; walk.next(p), ++segment) {
-      const int64_t row0 = walk.group * p.pack;
+      const int64_t row0 = group_row(p, walk.group);
+      const int block_cols = block_columns();
       if (quarter == 0) {  // what each column sees
         const int c = block * p.block_cols + my_col;
         int n = INT_MAX;
         if (my_col < block_cols) {
           const int j = c / p.group;
-          n = row_length(p.R, row0 + j);
+          n = kForm == Form::kShared ? group_length(p, walk.group) : row_length(p.R, row0 + j);
           if (lane < H)
             sm.out_at[segment & 1][half][lane] = (row0 + j) * p.a.out_row_stride + static_cast<int64_t>(walk.kv_head * p.group + c - j * p.group) * p.a.out_head_stride;
         }
         int least = n, split = INT_MAX;
-        if (p.pack > 1) {
+        if (kForm != Form::kShared && p.pack > 1) {
 #pragma unroll 1
           for (int j = lane; j < p.pack; j += 32) {
             const int seen = row_length(p.R, row0 + j);
@@ -821,6 +880,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       }
       const float part_l = reduce_columns<H, false>(l, lane);
       if (lane < H) sm.column_sum[half][quarter][lane] = part_l;
+      // of my_col: the logarithm of the sum behind the prefix, read by every warp before the first one writes the whole sum's
+      float tail = -INFINITY;
+      if constexpr (kForm == Form::kShared) {
+        if (my_col < block_cols) {
+          const int c = block * p.block_cols + my_col, j = c / p.group;
+          tail = p.a.lse[(row0 + j) * p.a.heads + walk.kv_head * p.group + c - j * p.group];
+        }
+      }
       named_sync(1 + half, 128);
       float sum = 0.f;
 #pragma unroll
@@ -829,14 +896,19 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       const int64_t slot = ((static_cast<int64_t>(slice) * 2 + (first_segment ? 0 : 1)) * p.blocks + block) * N;
       const float inverse = sum == 0.f ? 0.f : 1.f / sum;
       const bool blank = __any_sync(~0u, sum == 0.f);  // some column saw nothing: its values are zeros, whatever stands in O
-      if (lane < H) sm.moved[warp][0][lane] = inverse;
+      const Weights both = kForm == Form::kShared ? weigh(sum == 0.f ? -INFINITY : in_use + log2f(sum), tail) : Weights{};
+      if (lane < H) {
+        sm.moved[warp][0][lane] = kForm == Form::kShared ? inverse * both.prefix : inverse;
+        if (kForm == Form::kShared) sm.moved[warp][1][lane] = both.tail;
+      }
       if (quarter == 0 && lane < H) {
         if (!whole) {
           p.stat[slot + my_col] = make_float2(m == -INFINITY ? -INFINITY : in_use, sum);
+          if (kForm == Form::kShared) p.f.tail_lse[slot + my_col] = tail;
         } else if (p.a.lse && my_col < block_cols) {
           const int c = block * p.block_cols + my_col, j = c / p.group;
           p.a.lse[(row0 + j) * p.a.heads + walk.kv_head * p.group + c - j * p.group] =
-              sum == 0.f ? -INFINITY : (in_use + log2f(sum)) * 0.69314718055994531f;
+              kForm == Form::kShared ? both.lse : sum == 0.f ? -INFINITY : (in_use + log2f(sum)) * 0.69314718055994531f;
         }
       }
       __syncwarp();
@@ -865,6 +937,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 #pragma unroll
           for (int i = 0; i < H; i += 2) {
             const float2 f = *reinterpret_cast<const float2*>(&sm.moved[warp][0][i]);
+            if constexpr (kForm == Form::kShared) {
+              const float x = o[i] * f.x, y = o[i + 1] * f.y, other = __shfl_xor_sync(~0u, odd ? x : y, 1);
+              if (i < real) *reinterpret_cast<uint32_t*>(out + out_at[i]) = add_tail<kBf16>(odd ? other : x, odd ? y : other, out + out_at[i], sm.moved[warp][1][i + odd]);
+              continue;
+            }
             const uint32_t mine = pack2<kBf16>(o[i] * f.x, o[i + 1] * f.y), other = __shfl_xor_sync(~0u, mine, 1);
             // the even lane has this column of both dims, the odd lane the next one
             const uint32_t both = odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
@@ -896,7 +973,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       p.join[slice] = j;
     }
   }
-  if (blockIdx.x == 0) report_rows(p.R, tid, kThreads);
+  if (kForm != Form::kShared && blockIdx.x == 0) report_rows(p.R, tid, kThreads);
   settle(guard);
   fence_before();
   __syncthreads();
@@ -918,17 +995,16 @@ __device__ __forceinline__ float4 load_now(const float4* at) {
 template <int N, bool kBf16>
 __global__ void __launch_bounds__(kTeam * kMaxTeams) join_kernel(const __grid_constant__ Params p) {
   __shared__ int32_t place[kMaxParts];  // of each part, in columns; -1: the slice was empty
-  __shared__ float base[N], inverse[N];
+  __shared__ float base[N], inverse[N], tail[kForm == Form::kShared ? N : 1];
   __shared__ float sums[kJoinDims][N + 4];
   const int tid = threadIdx.x, per = p.v_pieces * 128 / kJoinDims;
   const int dim0 = blockIdx.x % per * kJoinDims, block = blockIdx.x / per % p.blocks, at_join = blockIdx.x / per / p.blocks;
-  const int block_cols = min(p.block_cols, p.cols - block * p.block_cols);
   dependent_wait();
   dependent_launch();
   const Join jn = p.join[at_join];
   if (jn.last < 0 || dim0 >= p.a.dv) return;
-  const int parts = jn.last - jn.first + 1, width = p.v_pieces * 128;
-  const int64_t row0 = jn.rowgroup * p.pack;
+  const int parts = jn.last - jn.first + 1, width = p.v_pieces * 128, block_cols = columns_of_block(p, jn.rowgroup, block);
+  const int64_t row0 = group_row(p, jn.rowgroup);
   for (int i = tid; i < parts; i += kTeam * p.teams) {
     const int s = jn.first + i;
     const bool empty = slice_begin(jn.tiles, p.slices, s) == slice_begin(jn.tiles, p.slices, s + 1);
@@ -957,8 +1033,15 @@ __global__ void __launch_bounds__(kTeam * kMaxTeams) join_kernel(const __grid_co
       base[col] = m == -INFINITY ? 0.f : m;
       inverse[col] = sum == 0.f ? 0.f : 1.f / sum;
       const int c = block * p.block_cols + col, j = c / p.group;
+      Weights both{};
+      if constexpr (kForm == Form::kShared) {
+        both = weigh(sum == 0.f ? -INFINITY : m + log2f(sum), p.f.tail_lse[place[0] + col]);
+        inverse[col] *= both.prefix;
+        tail[col] = both.tail;
+      }
       if (p.a.lse && dim0 == 0 && col < block_cols)
-        p.a.lse[(row0 + j) * p.a.heads + jn.kv_head * p.group + c - j * p.group] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
+        p.a.lse[(row0 + j) * p.a.heads + jn.kv_head * p.group + c - j * p.group] =
+            kForm == Form::kShared ? both.lse : sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
     }
   }
   __syncthreads();
@@ -1008,10 +1091,14 @@ __global__ void __launch_bounds__(kTeam * kMaxTeams) join_kernel(const __grid_co
   __syncthreads();
   for (int e = tid; e < block_cols * (kJoinDims / 2); e += kTeam * p.teams) {
     const int n = e / (kJoinDims / 2), d = e % (kJoinDims / 2) * 2, c = block * p.block_cols + n, j = c / p.group;
-    if (dim0 + d < p.a.dv)
-      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.a.out) + (row0 + j) * p.a.out_row_stride +
-                                   static_cast<int64_t>(jn.kv_head * p.group + c - j * p.group) * p.a.out_head_stride + dim0 + d) =
-          inverse[n] == 0.f ? 0u : pack2<kBf16>(sums[d][n] * inverse[n], sums[d + 1][n] * inverse[n]);
+    if (dim0 + d < p.a.dv) {
+      uint16_t* to = static_cast<uint16_t*>(p.a.out) + (row0 + j) * p.a.out_row_stride +
+                     static_cast<int64_t>(jn.kv_head * p.group + c - j * p.group) * p.a.out_head_stride + dim0 + d;
+      if constexpr (kForm == Form::kShared)
+        *reinterpret_cast<uint32_t*>(to) = add_tail<kBf16>(inverse[n] == 0.f ? 0.f : sums[d][n] * inverse[n], inverse[n] == 0.f ? 0.f : sums[d + 1][n] * inverse[n], to, tail[n]);
+      else
+        *reinterpret_cast<uint32_t*>(to) = inverse[n] == 0.f ? 0u : pack2<kBf16>(sums[d][n] * inverse[n], sums[d + 1][n] * inverse[n]);
+    }
   }
 }
 
@@ -1041,7 +1128,7 @@ int run(Params& p, int device, int smem_limit, bool joins, cudaStream_t stream) 
   }
   p.slots = room / kPiece < kMaxSlots ? room / kPiece : kMaxSlots;
   const int k_ring = p.k_pieces - p.rest;
-  if (p.slots < (p.latent && k_ring > 2 ? k_ring : 2) || (!p.latent && p.pack > 1 && p.slots < p.v_pieces)) return TOPK_ERR_PLAN;
+  if (p.slots < (p.latent && k_ring > 2 ? k_ring : 2) || (kForm != Form::kShared && !p.latent && p.pack > 1 && p.slots < p.v_pieces)) return TOPK_ERR_PLAN;
   p.tmem_cols = 32;
   while (p.tmem_cols < static_cast<uint32_t>((p.v_pieces + 2) * N)) p.tmem_cols *= 2;
   const size_t smem = p.q_bytes + static_cast<size_t>(p.slots) * kPiece + (p.rest && !p.rest_is_p ? kChunk : 0) + kPBytes + extra;
@@ -1060,38 +1147,10 @@ int run_columns(Params& p, int device, int smem_limit, bool joins, cudaStream_t 
   return bf16 ? run<N, true, false>(p, device, smem_limit, joins, stream) : run<N, false, false>(p, device, smem_limit, joins, stream);
 }
 
-}  // namespace
-}  // namespace paged
-}  // namespace ltk
-
-extern "C" size_t topk_attention_workspace_size(int device) {
-  topk_device_props p{};
-  if (topk_query_device(device, &p) != TOPK_OK) return 0;
-  return ltk::paged::workspace_for(p.num_sms);
-}
-
-extern "C" int topk_paged_attention(const topk_attention_args* args, void* stream) {
-  using namespace ltk::paged;
-  if (args == nullptr) return TOPK_ERR_INVALID_ARG;
-  const topk_attention_args& a = *args;
-  int rc = check_rows(a.rows);
-  if (rc != TOPK_OK) return rc;
-  if (!(a.scale > 0.f) || a.scale > 3.4e38f || a.heads < 1 || a.kv_heads < 1 || a.heads % a.kv_heads != 0)
-    return TOPK_ERR_INVALID_ARG;
-  if (a.indices != nullptr && (a.num_indices < 1 || a.num_indices > (1 << 20) || a.index_row_stride < 0))
-    return TOPK_ERR_INVALID_ARG;
-  if ((a.dtype != TOPK_DTYPE_F16 && a.dtype != TOPK_DTYPE_BF16) || a.heads > 1024 || a.dk < 8 || a.dk > kMaxQk || a.dk % 8 ||
-      a.dv < 8 || a.dv > kMaxV || a.dv % 8 || (a.v == nullptr && a.dv > a.dk))
-    return TOPK_ERR_UNSUPPORTED;
-  if (a.rows.num_rows == 0) return TOPK_OK;
-  rc = check_row_pointers(a.rows);
-  if (rc != TOPK_OK) return rc;
-  if (a.q == nullptr || a.k == nullptr || a.out == nullptr || a.workspace == nullptr) return TOPK_ERR_INVALID_ARG;
-  if (misaligned(a.q, 16) || a.q_row_stride % 8 || a.q_head_stride % 8 || misaligned(a.k, 16) || a.k_block_stride % 8 ||
-      a.k_token_stride % 8 || a.k_head_stride % 8 || misaligned(a.out, 16) || a.out_row_stride % 8 || a.out_head_stride % 8 ||
-      misaligned(a.indices, 4) || misaligned(a.lse, 4) || misaligned(a.workspace, 16) ||
-      (a.v && (misaligned(a.v, 16) || a.v_block_stride % 8 || a.v_token_stride % 8 || a.v_head_stride % 8)))
-    return TOPK_ERR_MISALIGNED;
+// The call of this form, after the checks that all forms share.
+int attend(const topk_attention_args& a, const FormArgs& f, void* stream) {
+  int rc = check_attention(a);
+  if (rc != TOPK_OK || a.rows.num_rows == 0) return rc;
   int dev = 0;
   topk_device_props props{};
   if (cudaGetDevice(&dev) != cudaSuccess || topk_query_device(dev, &props) != TOPK_OK) {
@@ -1103,6 +1162,7 @@ extern "C" int topk_paged_attention(const topk_attention_args* args, void* strea
 
   Params p{};
   p.a = a;
+  p.f = f;
   p.R = make_rows(a.rows, INT32_MAX, a.workspace);
   p.group = a.heads / a.kv_heads;
   // The rows of a request share its tokens, unless index lists tell them apart. (Even where that makes no fewer column blocks:
@@ -1113,19 +1173,25 @@ extern "C" int topk_paged_attention(const topk_attention_args* args, void* strea
   p.k_chunks = (a.dk + 63) / 64;
   p.v_pieces = (a.dv + 127) / 128;
   const int held = (props.max_smem_optin - static_cast<int>(sizeof(Smem<64>)) - 1024 - p.k_chunks * 64 * 128 - 2 * kChunk) / kPiece;
-  const bool together = a.indices == nullptr && a.rows.row_request == nullptr && a.rows.next_n * static_cast<int64_t>(p.group) <= 1024 &&
+  const bool lists = kForm == Form::kBlocks || a.indices != nullptr;
+  const bool together = !lists && a.rows.row_request == nullptr && a.rows.next_n * static_cast<int64_t>(p.group) <= 1024 &&
                         (p.latent || p.v_pieces <= held);
   p.pack = together ? a.rows.next_n : 1;
+  if (kForm == Form::kShared) p.pack = rows_of_run(a);
   p.cols = p.pack * p.group;
   p.blocks = (p.cols + kMaxBlockCols - 1) / kMaxBlockCols;
   p.block_cols = (p.cols + p.blocks - 1) / p.blocks;
   p.k_pieces = (p.k_chunks + 1) / 2;
   p.rest = p.latent && p.k_chunks % 2 == 1 && p.k_pieces > p.v_pieces;
   p.row_groups = a.rows.num_rows / p.pack;
-  p.row_tiles = a.indices ? (a.num_indices + kTile - 1) / kTile : 0;
+  p.row_tiles = kForm == Form::kBlocks ? static_cast<int32_t>((f.num_chosen * a.rows.block_size + kTile - 1) / kTile)
+                : a.indices            ? (a.num_indices + kTile - 1) / kTile
+                                       : 0;
   p.scale2 = a.scale * 1.4426950408889634f;
-  const int64_t units = p.row_groups * a.kv_heads;
-  const int64_t most = units * (a.indices ? p.row_tiles : (p.R.max_len + static_cast<int64_t>(kTile) - 1) / kTile);
+  // (Of a shared prefix: what one prefix for all rows has. There may be more units, up to one for each row and head.)
+  const int64_t units = kForm == Form::kShared ? (a.rows.num_rows + p.pack - 1) / p.pack * a.kv_heads : p.row_groups * a.kv_heads;
+  const int64_t longest = kForm == Form::kShared ? f.prefix_most : p.R.max_len;
+  const int64_t most = (kForm == Form::kShared ? a.rows.num_rows * a.kv_heads : units) * (lists ? p.row_tiles : (longest + kTile - 1) / kTile);
   int64_t slices = sms / p.blocks < 1 ? 1 : sms / p.blocks;
   if (slices > most) slices = most;
   if (slices > kMaxParts) slices = kMaxParts;
@@ -1140,7 +1206,7 @@ extern "C" int topk_paged_attention(const topk_attention_args* args, void* strea
     if (p.whole && p.slices > units) p.slices = static_cast<int32_t>(units);
     joins = !p.whole;
   }
-  p.by_unit = units <= p.slices;
+  p.by_unit = kForm != Form::kShared && units <= p.slices;
   // Units in many parts are joined by more threads each; units in a few by more CTAs at once. (One unit in about 100 parts,
   // 64 columns: 35 us with four teams, 55 with one; 64 units in two or three, 16 columns: 39 us with one, 45 with four.)
   p.teams = p.slices >= 8 * units ? kMaxTeams : 1;
@@ -1156,3 +1222,23 @@ extern "C" int topk_paged_attention(const topk_attention_args* args, void* strea
   if (p.block_cols <= 32) return run_columns<32>(p, dev, props.max_smem_optin, joins, s);
   return run_columns<64>(p, dev, props.max_smem_optin, joins, s);
 }
+
+}  // namespace
+
+int LTK_ATTENTION_CALL(const topk_attention_args& a, const FormArgs& f, void* stream) { return attend(a, f, stream); }
+
+}  // namespace paged
+}  // namespace ltk
+
+#ifdef LTK_ATTENTION_PLAIN
+extern "C" size_t topk_attention_workspace_size(int device) {
+  topk_device_props p{};
+  if (topk_query_device(device, &p) != TOPK_OK) return 0;
+  return ltk::paged::workspace_for(p.num_sms);
+}
+
+extern "C" int topk_paged_attention(const topk_attention_args* args, void* stream) {
+  if (args == nullptr) return TOPK_ERR_INVALID_ARG;
+  return ltk::paged::attend_plain(*args, ltk::paged::FormArgs{}, stream);
+}
+#endif

@@ -1,0 +1,649 @@
+// The pages of a pool: forking and freeing requests, compacting the pool, and copying pages.
+//
+// Forking and freeing change three things that have to agree: rows of the table, the holders of each page beyond its first, and
+// the stack of free pages whose pointer is `taken`. What comes out has to be the same every time, so nothing is handed out or
+// handed back in the order of atomics: places come from exclusive sums over the lists, as in the map (kv_map.cu).
+//
+//   fork     a CTA has some of the forks and counts the new pages of all before them; its threads go along the rows.
+//   free     a page that several of the call's rows hold goes back once, at the first of its places. Three steps, a cluster's
+//            barrier between them: every place takes a holder off; of a page without holders, the places
+//            meet in its word of `shares` by their number's minimum; and the places whose number stands there are counted, summed up
+//            and written.
+//   compact  marks of what the table and the list name; the free pages in rising and the named ones in falling order by
+//            sums over the pool; their pairs are the moves, as long as they lower a number.
+//   copy     every cache's pages in pieces of 16 KB over all CTAs, 16 bytes a thread and four loads at a time: bound by HBM.
+//
+// Free and compact are one cluster of eight CTAs, whose barrier in hardware takes the place of further launches. They are bound by
+// latency up to some 100 000 entries of the table (a step is 1 to 2 us) and by eight SMs' loads above.
+#include "paged.cuh"
+
+namespace ltk {
+namespace paged {
+namespace {
+
+constexpr int kTicketWord = 8;  // of the workspace, as in the map
+
+// ---- fork -------------------------------------------------------------------
+
+constexpr int kForkThreads = 256;
+
+struct ForkParams {
+  topk_page_fork_args a;
+  Rows R;  // for the division by block_size
+};
+
+struct Fork {
+  int64_t parent, child;  // rows of the table
+  int32_t whole;          // pages shared
+  int32_t source;         // page of what is left, -1: nothing
+};
+
+__device__ __forceinline__ Fork read_fork(const ForkParams& p, int64_t i, uint32_t* flags) {
+  const topk_page_pool& t = p.a.pool;
+  Fork f{p.a.parents[i], p.a.children[i], 0, -1};
+  if (f.parent < 0 || f.parent >= t.num_requests || f.child < 0 || f.child >= t.num_requests) {
+    *flags |= TOPK_DEV_BAD_BLOCK;
+    f.child = -1;
+    return f;
+  }
+  const int n = min(max(p.a.kept_lens[i], 0), p.R.max_len);
+  f.whole = block_column(p.R, n);
+  if (n > f.whole * p.R.block_size) {
+    f.source = t.block_table[f.parent * t.table_stride + f.whole];
+    if (f.source < 0 || f.source >= t.num_blocks) {
+      *flags |= TOPK_DEV_BAD_BLOCK;
+      f.source = -1;
+    }
+  }
+  return f;
+}
+
+__global__ void __launch_bounds__(kForkThreads) fork_kernel(const __grid_constant__ ForkParams p) {
+  __shared__ Fork forks[kForkThreads];
+  __shared__ int32_t rank[kForkThreads], warp_sum[kForkThreads / 32], all_before;
+  const topk_page_fork_args& a = p.a;
+  const topk_page_pool& t = a.pool;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint32_t flags = 0, none = 0;
+  dependent_wait();
+  dependent_launch();
+  const int64_t taken = *t.taken;
+  const int64_t per = (a.num_forks + gridDim.x - 1) / gridDim.x;
+  const int64_t i0 = min(per * blockIdx.x, a.num_forks), i1 = min(i0 + per, a.num_forks);
+  if (tid == 0) all_before = 0;
+  __syncthreads();
+  int32_t count = 0;
+  for (int64_t i = tid; i < i0; i += kForkThreads) count += read_fork(p, i, &none).source >= 0;
+  for (int d = 16; d; d >>= 1) count += __shfl_xor_sync(~0u, count, d);
+  if (lane == 0 && count > 0) atomicAdd(&all_before, count);  // a sum of whole numbers: any order
+  __syncthreads();
+  int64_t before = all_before;
+  for (int64_t base = i0; base < i1; base += kForkThreads) {
+    const int here = static_cast<int>(min(i1 - base, static_cast<int64_t>(kForkThreads)));
+    Fork f{0, -1, 0, -1};
+    if (tid < here) f = read_fork(p, base + tid, &flags);
+    const unsigned who = __ballot_sync(~0u, f.source >= 0);
+    if (lane == 0) warp_sum[warp] = __popc(who);
+    __syncthreads();
+    int32_t at = __popc(who & ((1u << lane) - 1)), total = 0;
+    for (int w = 0; w < kForkThreads / 32; ++w) {
+      if (w < warp) at += warp_sum[w];
+      total += warp_sum[w];
+    }
+    forks[tid] = f;
+    rank[tid] = at;
+    __syncthreads();
+    for (int k = 0; k < here; ++k) {
+      const Fork g = forks[k];
+      const int64_t n = taken + before + rank[k];
+      int32_t target = -1;
+      if (g.source >= 0) {
+        if (n >= 0 && n < t.num_free) target = t.free_blocks[n];
+        if (target < 0) flags |= TOPK_DEV_BLOCKS_EXHAUSTED;
+      }
+      if (tid == 0) {
+        a.source[base + k] = target < 0 ? -1 : g.source;
+        a.target[base + k] = target;
+      }
+      if (g.child < 0) continue;
+      const int32_t* from = t.block_table + g.parent * t.table_stride;
+      int32_t* to = t.block_table + g.child * t.table_stride;
+      for (int64_t c = tid; c < t.max_blocks; c += kForkThreads) {
+        int32_t page = c == g.whole ? target : -1;
+        if (c < g.whole) {
+          page = from[c];
+          if (page >= 0 && page < t.num_blocks) {
+            atomicAdd(t.shares + page, 1);
+          } else {
+            page = -1;
+            flags |= TOPK_DEV_BAD_BLOCK;
+          }
+        }
+        to[c] = page;
+      }
+    }
+    before += total;
+    __syncthreads();  // the next forks are written
+  }
+  if (flags) atomicOr(p.R.status, flags);
+  // the CTA with the last forks knows how many pages went; it is the last to have read `taken` if all others have drawn their
+  // tickets, and the last one writes what that CTA left
+  __shared__ bool last;
+  uint32_t* ticket = p.R.status + kTicketWord;
+  if (tid == 0) {
+    if (blockIdx.x == gridDim.x - 1) ticket[1] = static_cast<uint32_t>(before);
+    __threadfence();
+    last = gridDim.x == 1 || atomicAdd(ticket, 1u) + 1 == gridDim.x;
+    if (last) {
+      __threadfence();
+      const int64_t after = taken + static_cast<int64_t>(*const_cast<volatile uint32_t*>(ticket + 1));
+      ticket[0] = 0;
+      ticket[1] = 0;
+      *t.taken = static_cast<int32_t>(after < t.num_free ? after : (taken > t.num_free ? taken : t.num_free));
+    }
+  }
+}
+
+// ---- one cluster ------------------------------------------------------------
+
+constexpr int kCluster = 8;
+constexpr int kPageThreads = 1024;
+constexpr int kPageWarps = kPageThreads / 32;
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+// All threads of the cluster meet; what they wrote before is seen behind it.
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ int32_t read_peer(const int32_t* mine, uint32_t rank) {
+  const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
+  uint32_t there;
+  int32_t v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(there) : "memory");
+  return v;
+}
+
+// What other CTAs of the cluster wrote: from L2.
+__device__ __forceinline__ int32_t look(const int32_t* at) { return __ldcg(at); }
+
+// Sums of a CTA: `x` summed up over its threads.
+__device__ __forceinline__ int32_t sum_of_cta(int32_t x, int32_t (&warp_sum)[kPageWarps], int lane, int warp) {
+  for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(~0u, x, d);
+  __syncthreads();
+  if (lane == 0) warp_sum[warp] = x;
+  __syncthreads();
+  int32_t all = 0;
+  for (int w = 0; w < kPageWarps; ++w) all += warp_sum[w];
+  return all;
+}
+
+// Where this thread's `x` (0 or 1) stands among those of the CTA, and how many there are.
+__device__ __forceinline__ int32_t place_in_cta(bool x, int32_t* all, int32_t (&warp_sum)[kPageWarps], int lane, int warp) {
+  const unsigned who = __ballot_sync(~0u, x);
+  __syncthreads();
+  if (lane == 0) warp_sum[warp] = __popc(who);
+  __syncthreads();
+  int32_t at = __popc(who & ((1u << lane) - 1)), total = 0;
+  for (int w = 0; w < kPageWarps; ++w) {
+    if (w < warp) at += warp_sum[w];
+    total += warp_sum[w];
+  }
+  *all = total;
+  return at;
+}
+
+// Sums over the cluster of what each CTA has in *mine: those before this one, and all.
+__device__ __forceinline__ void sum_of_cluster(const int32_t* mine, int64_t* before, int64_t* all) {
+  *before = *all = 0;
+  const uint32_t me = cluster_rank();
+  for (uint32_t r = 0; r < kCluster; ++r) {
+    const int32_t x = read_peer(mine, r);
+    if (r < me) *before += x;
+    *all += x;
+  }
+}
+
+// ---- free -------------------------------------------------------------------
+
+constexpr int64_t kMostFreed = 1 << 20;  // requests of a call
+constexpr int kOnceWords = kMostFreed / kCluster / 32 + 2;
+
+struct FreeParams {
+  topk_page_free_args a;
+  uint32_t* status;
+};
+
+__global__ void __launch_bounds__(kPageThreads, 1) free_kernel(const __grid_constant__ FreeParams p) {
+  __shared__ int32_t warp_sum[kPageWarps], mine;
+  __shared__ uint32_t again[kOnceWords];  // bits of the requests of this CTA that were listed before
+  const topk_page_free_args& a = p.a;
+  const topk_page_pool& t = a.pool;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint32_t flags = 0;
+  dependent_wait();
+  dependent_launch();
+  const int64_t taken = min(max(static_cast<int64_t>(*t.taken), int64_t{0}), t.num_free);
+  // this CTA's requests, and places: a request's columns in order
+  const int64_t per = (a.num_freed + kCluster - 1) / kCluster, i0 = min(per * cluster_rank(), a.num_freed), i1 = min(i0 + per, a.num_freed);
+  for (int i = tid; i < kOnceWords; i += kPageThreads) again[i] = 0;
+  __syncthreads();
+  for (int64_t i = i0 + warp; i < i1; i += kPageWarps) {
+    const int32_t request = a.requests[i];
+    bool found = false;
+    for (int64_t j = lane; j < i; j += 32) found |= a.requests[j] == request;
+    if (__any_sync(~0u, found) && lane == 0) atomicOr(&again[(i - i0) >> 5], 1u << ((i - i0) & 31));
+  }
+  __syncthreads();
+  const int64_t places = (i1 - i0) * t.max_blocks;
+  const uint32_t columns = static_cast<uint32_t>(t.max_blocks);
+  // the page at a place, -1 where there is none; and its entry in the table
+  const auto page_at = [&](int64_t place, int32_t** entry) -> int32_t {
+    const uint32_t i = static_cast<uint32_t>(place) / columns, c = static_cast<uint32_t>(place) - i * columns;
+    if (again[i >> 5] >> (i & 31) & 1) return -1;
+    const int64_t request = a.requests[i0 + i];
+    if (request < 0 || request >= t.num_requests) {
+      flags |= TOPK_DEV_BAD_BLOCK;
+      return -1;
+    }
+    *entry = t.block_table + request * t.table_stride + c;
+    const int32_t page = **entry;
+    if (page >= t.num_blocks) flags |= TOPK_DEV_BAD_BLOCK;
+    return page < t.num_blocks ? page : -1;
+  };
+  const auto number = [&](int64_t place) { return INT32_MIN + static_cast<int32_t>(i0 * t.max_blocks + place); };
+  int32_t* entry = nullptr;
+  for (int64_t x = tid; x < places; x += kPageThreads) {
+    const int32_t page = page_at(x, &entry);
+    if (page >= 0) atomicSub(t.shares + page, 1);
+  }
+  cluster_sync();
+  for (int64_t x = tid; x < places; x += kPageThreads) {
+    const int32_t page = page_at(x, &entry);
+    if (page >= 0 && look(t.shares + page) < 0) atomicMin(t.shares + page, number(x));
+  }
+  cluster_sync();
+  int32_t count = 0;
+  for (int64_t x = tid; x < places; x += kPageThreads) {
+    const int32_t page = page_at(x, &entry);
+    count += page >= 0 && look(t.shares + page) == number(x);
+  }
+  count = sum_of_cta(count, warp_sum, lane, warp);
+  if (tid == 0) mine = count;
+  cluster_sync();
+  int64_t before, all;
+  sum_of_cluster(&mine, &before, &all);
+  const int64_t first = taken - all;  // where the pages go, in front of the others
+  if (first < 0) flags |= TOPK_DEV_BLOCKS_EXHAUSTED;
+  for (int64_t x0 = 0; x0 < places; x0 += kPageThreads) {
+    const int64_t x = x0 + tid;
+    int32_t* at = nullptr;
+    const int32_t page = x < places ? page_at(x, &at) : -1;
+    const bool back = page >= 0 && look(t.shares + page) == number(x);
+    int32_t here;
+    const int64_t to = first + before + place_in_cta(back, &here, warp_sum, lane, warp);
+    if (back) {
+      if (to >= 0) t.free_blocks[to] = page;
+      t.shares[page] = 0;  // the page's other places find another number here, as they did before
+    }
+    if (at != nullptr) *at = -1;
+    before += here;
+  }
+  if (flags) atomicOr(p.status, flags);
+  cluster_sync();  // no CTA leaves before its sums are read; and `taken` has been read by all
+  if (cluster_rank() == 0 && tid == 0) *t.taken = static_cast<int32_t>(first > 0 ? first : 0);
+}
+
+// ---- compact ----------------------------------------------------------------
+
+enum Mark : int32_t { kNothing = 0, kNamed = 1, kFree = 2, kBoth = 3, kArrived = 4 };  // and ~target for a page that moves
+
+struct CompactParams {
+  topk_page_compact_args a;
+  uint32_t* status;
+};
+
+__global__ void __launch_bounds__(kPageThreads, 1) compact_kernel(const __grid_constant__ CompactParams p) {
+  __shared__ int32_t warp_sum[kPageWarps], mine[3];
+  const topk_page_compact_args& a = p.a;
+  const topk_page_pool& t = a.pool;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t rank = cluster_rank(), all_threads = kCluster * kPageThreads, me = rank * kPageThreads + tid;
+  int32_t* mark = static_cast<int32_t*>(a.scratch);
+  int32_t *low = mark + t.num_blocks, *high = low + t.num_blocks;
+  uint32_t flags = 0;
+  dependent_wait();
+  dependent_launch();
+  const int64_t taken = min(max(static_cast<int64_t>(*t.taken), int64_t{0}), t.num_free);
+  const int64_t entries = t.num_requests * t.max_blocks;
+  const uint32_t columns = static_cast<uint32_t>(t.max_blocks);
+  for (int64_t b = me; b < t.num_blocks; b += all_threads) mark[b] = kNothing;
+  cluster_sync();
+  for (int64_t e = me; e < entries; e += all_threads) {
+    const uint32_t r = static_cast<uint32_t>(e) / columns, c = static_cast<uint32_t>(e) - r * columns;
+    const int32_t page = t.block_table[r * t.table_stride + c];
+    if (page >= 0 && page < t.num_blocks) mark[page] = kNamed;
+    if (page >= t.num_blocks) flags |= TOPK_DEV_BAD_BLOCK;
+  }
+  cluster_sync();
+  for (int64_t f = taken + me; f < t.num_free; f += all_threads) {
+    const int32_t page = t.free_blocks[f];
+    if (page < 0 || page >= t.num_blocks || atomicOr(mark + page, static_cast<int32_t>(kFree)) != kNothing) flags |= TOPK_DEV_BAD_BLOCK;
+  }
+  cluster_sync();
+  // this CTA's pages
+  const int64_t per = (t.num_blocks + kCluster - 1) / kCluster, b0 = min(per * rank, t.num_blocks), b1 = min(b0 + per, t.num_blocks);
+  int32_t free_count = 0, named_count = 0;
+  for (int64_t b = b0 + tid; b < b1; b += kPageThreads) {
+    const int32_t m = look(mark + b);
+    free_count += m == kFree;
+    named_count += (m & kNamed) != 0;
+  }
+  free_count = sum_of_cta(free_count, warp_sum, lane, warp);
+  named_count = sum_of_cta(named_count, warp_sum, lane, warp);
+  if (tid == 0) {
+    mine[0] = free_count;
+    mine[1] = named_count;
+  }
+  cluster_sync();
+  int64_t free_before, free_all, named_before, named_all;
+  sum_of_cluster(&mine[0], &free_before, &free_all);
+  sum_of_cluster(&mine[1], &named_before, &named_all);
+  for (int64_t x = b0; x < b1; x += kPageThreads) {
+    const int64_t b = x + tid;
+    const int32_t m = b < b1 ? look(mark + b) : kNothing;
+    const bool is_free = m == kFree, is_named = (m & kNamed) != 0;
+    int32_t n;
+    const int64_t at = free_before + place_in_cta(is_free, &n, warp_sum, lane, warp);
+    if (is_free) low[at] = static_cast<int32_t>(b);
+    free_before += n;
+    const int64_t from_top = named_all - 1 - (named_before + place_in_cta(is_named, &n, warp_sum, lane, warp));
+    if (is_named) high[from_top] = static_cast<int32_t>(b);
+    named_before += n;
+  }
+  cluster_sync();
+  const int64_t pairs = min(free_all, named_all);
+  for (int64_t i = me; i < a.max_copies; i += all_threads) {
+    const int32_t from = i < pairs ? look(high + i) : -1, to = i < pairs ? look(low + i) : -1;
+    const bool moves = to < from;
+    const int32_t source = moves ? from : -1, target = moves ? to : -1;
+    a.source[i] = source;
+    a.target[i] = target;
+    if (moves) {
+      const int32_t n = t.shares[source];
+      mark[source] = ~target;
+      mark[target] = kArrived;
+      a.shares_out[target] = n;
+      a.shares_out[source] = 0;
+    }
+  }
+  cluster_sync();
+  for (int64_t e = me; e < entries; e += all_threads) {
+    const uint32_t r = static_cast<uint32_t>(e) / columns, c = static_cast<uint32_t>(e) - r * columns;
+    int32_t page = t.block_table[r * t.table_stride + c];
+    if (page >= 0 && page < t.num_blocks) {
+      const int32_t m = look(mark + page);
+      if (m < 0) page = ~m;
+    }
+    a.block_table_out[r * a.table_out_stride + c] = page;
+  }
+  int32_t count = 0;
+  for (int64_t b = b0 + tid; b < b1; b += kPageThreads) {
+    const int32_t m = look(mark + b);
+    count += m == kFree || m < 0;
+    if (m >= 0 && m != kArrived) a.shares_out[b] = t.shares[b];
+  }
+  count = sum_of_cta(count, warp_sum, lane, warp);
+  if (tid == 0) mine[2] = count;
+  cluster_sync();
+  int64_t before, all;
+  sum_of_cluster(&mine[2], &before, &all);
+  const int64_t taken_out = t.num_free - all;  // the list holds every free page once, so there are no more than it has places
+  for (int64_t x = b0; x < b1; x += kPageThreads) {
+    const int64_t b = x + tid;
+    const int32_t m = b < b1 ? look(mark + b) : kNothing;
+    const bool is_free = m == kFree || m < 0;
+    int32_t n;
+    const int64_t at = taken_out + before + place_in_cta(is_free, &n, warp_sum, lane, warp);
+    if (is_free) a.free_blocks_out[at] = static_cast<int32_t>(b);
+    before += n;
+  }
+  if (a.free_blocks_out != t.free_blocks)
+    for (int64_t f = me; f < taken_out; f += all_threads) a.free_blocks_out[f] = t.free_blocks[f];
+  if (flags) atomicOr(p.status, flags);
+  cluster_sync();  // no CTA leaves before its sums are read
+  if (me == 0) *a.taken_out = static_cast<int32_t>(taken_out);
+}
+
+template <typename Args>
+int launch_cluster(void (*kernel)(Args), const Args& args, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kCluster);
+  cfg.blockDim = dim3(kPageThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kCluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = dependent_launch_default() ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args) != cudaSuccess) {
+    cudaGetLastError();
+    return TOPK_ERR_CUDA;
+  }
+  return TOPK_OK;
+}
+
+// ---- copy -------------------------------------------------------------------
+
+constexpr int kCopyThreads = 256;
+constexpr int kAtOnce = 4;  // loads of a thread
+constexpr int kFewCaches = 16;
+
+struct Cache {
+  char* base;
+  int64_t block_stride, stride0, stride1;
+  int32_t num_blocks, n1;
+  uint32_t pieces;      // of a page
+  uint32_t run_pieces;  // of a run
+  uint32_t first;       // chunk of a pair at which this cache's begin
+  int32_t shift;        // a piece is 2^shift bytes
+};
+
+template <int kCaches>
+struct CopyParams {
+  const int32_t *source, *target;
+  int64_t num_copies;
+  uint32_t* status;
+  int32_t num_caches;
+  uint32_t chunks;  // of a pair
+  Cache cache[kCaches];
+};
+
+// One piece of each of kAtOnce places of a page; T has the piece's size.
+template <typename T>
+__device__ __forceinline__ void copy_chunk(const Cache& c, int64_t source, int64_t target, uint32_t x0) {
+  const char* from = c.base + source * c.block_stride;
+  char* to = c.base + target * c.block_stride;
+  T v[kAtOnce];
+  int64_t at[kAtOnce];
+#pragma unroll
+  for (int i = 0; i < kAtOnce; ++i) {
+    const uint32_t x = x0 + i * kCopyThreads;
+    if (x >= c.pieces) continue;
+    if (c.run_pieces == c.pieces) {
+      at[i] = static_cast<int64_t>(x) * sizeof(T);
+    } else {
+      const uint32_t run = x / c.run_pieces, n0 = run / c.n1;
+      at[i] = n0 * c.stride0 + (run - n0 * c.n1) * c.stride1 + static_cast<int64_t>(x - run * c.run_pieces) * sizeof(T);
+    }
+    v[i] = *reinterpret_cast<const T*>(from + at[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < kAtOnce; ++i)
+    if (x0 + i * kCopyThreads < c.pieces) *reinterpret_cast<T*>(to + at[i]) = v[i];
+}
+
+template <int kCaches>
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyParams<kCaches> p) {
+  dependent_wait();
+  dependent_launch();
+  uint32_t flags = 0;
+  for (int64_t u = blockIdx.x; u < p.num_copies * p.chunks; u += gridDim.x) {
+    const int64_t pair = u / p.chunks;
+    const uint32_t chunk = static_cast<uint32_t>(u - pair * p.chunks);
+    const int32_t source = p.source[pair], target = p.target[pair];
+    if (source < 0 || target < 0) continue;
+    int k = 0;  // the last cache whose first chunk is at or before this one
+    for (int step = kCaches / 2; step > 0; step >>= 1)
+      if (k + step < p.num_caches && p.cache[k + step].first <= chunk) k += step;
+    const Cache& c = p.cache[k];
+    if (source >= c.num_blocks || target >= c.num_blocks) {
+      flags |= TOPK_DEV_BAD_BLOCK;
+      continue;
+    }
+    const uint32_t x0 = (chunk - c.first) * (kCopyThreads * kAtOnce) + threadIdx.x;
+    switch (c.shift) {
+      case 4: copy_chunk<uint4>(c, source, target, x0); break;
+      case 3: copy_chunk<uint2>(c, source, target, x0); break;
+      case 2: copy_chunk<uint32_t>(c, source, target, x0); break;
+      case 1: copy_chunk<uint16_t>(c, source, target, x0); break;
+      default: copy_chunk<uint8_t>(c, source, target, x0);
+    }
+  }
+  if (flags && threadIdx.x == 0) atomicOr(p.status, flags);
+}
+
+template <int kCaches>
+int run_copy(const topk_page_copy_args& a, const Cache* caches, uint32_t chunks, int sms, cudaStream_t stream) {
+  CopyParams<kCaches> p{};
+  p.source = a.source;
+  p.target = a.target;
+  p.num_copies = a.num_copies;
+  p.status = static_cast<uint32_t*>(a.workspace);
+  p.num_caches = a.num_caches;
+  p.chunks = chunks;
+  for (int i = 0; i < a.num_caches; ++i) p.cache[i] = caches[i];
+  const int64_t units = a.num_copies * chunks, most = 8ll * sms;
+  return launch(copy_kernel<kCaches>, static_cast<const CopyParams<kCaches>&>(p), units < most ? units : most, kCopyThreads, 0, stream);
+}
+
+int check_pool(const topk_page_pool& t) {
+  if (t.num_requests < 0 || t.num_requests > INT32_MAX || t.max_blocks < 1 || t.max_blocks > INT32_MAX || t.table_stride < t.max_blocks ||
+      t.num_blocks < 0 || t.num_blocks > INT32_MAX || t.num_free < 0 || t.num_free > INT32_MAX || t.num_requests * t.max_blocks > INT32_MAX)
+    return TOPK_ERR_INVALID_ARG;
+  if (t.taken == nullptr || t.workspace == nullptr || (t.num_requests > 0 && t.block_table == nullptr) || (t.num_blocks > 0 && t.shares == nullptr) ||
+      (t.num_free > 0 && t.free_blocks == nullptr))
+    return TOPK_ERR_INVALID_ARG;
+  if (misaligned(t.block_table, 4) || misaligned(t.shares, 4) || misaligned(t.free_blocks, 4) || misaligned(t.taken, 4) || misaligned(t.workspace, 16))
+    return TOPK_ERR_MISALIGNED;
+  return TOPK_OK;
+}
+
+}  // namespace
+}  // namespace paged
+}  // namespace ltk
+
+extern "C" int topk_page_fork(const topk_page_fork_args* args, void* stream) {
+  using namespace ltk::paged;
+  if (args == nullptr) return TOPK_ERR_INVALID_ARG;
+  const topk_page_fork_args& a = *args;
+  const int rc = check_pool(a.pool);
+  if (rc != TOPK_OK) return rc;
+  if (a.num_forks < 0 || a.num_forks > INT32_MAX || a.block_size < 1) return TOPK_ERR_INVALID_ARG;
+  if (a.num_forks == 0) return TOPK_OK;
+  if (a.parents == nullptr || a.children == nullptr || a.kept_lens == nullptr || a.source == nullptr || a.target == nullptr) return TOPK_ERR_INVALID_ARG;
+  if (misaligned(a.parents, 4) || misaligned(a.children, 4) || misaligned(a.kept_lens, 4) || misaligned(a.source, 4) || misaligned(a.target, 4))
+    return TOPK_ERR_MISALIGNED;
+  const int sms = num_sms();
+  if (sms < 1) return TOPK_ERR_CUDA;
+  ForkParams p{};
+  p.a = a;
+  topk_paged_rows rows{};
+  rows.block_size = a.block_size;
+  rows.max_blocks = a.pool.max_blocks;
+  p.R = make_rows(rows, INT32_MAX, a.pool.workspace);
+  const int64_t grid = a.num_forks < 2ll * sms ? a.num_forks : 2ll * sms;
+  return launch(fork_kernel, static_cast<const ForkParams&>(p), grid, kForkThreads, 0, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int topk_page_free(const topk_page_free_args* args, void* stream) {
+  using namespace ltk::paged;
+  if (args == nullptr) return TOPK_ERR_INVALID_ARG;
+  const topk_page_free_args& a = *args;
+  const int rc = check_pool(a.pool);
+  if (rc != TOPK_OK) return rc;
+  if (a.num_freed < 0 || a.num_freed > kMostFreed || a.num_freed * a.pool.max_blocks >= INT32_MAX - 65536) return TOPK_ERR_INVALID_ARG;
+  if (a.num_freed == 0) return TOPK_OK;
+  if (a.requests == nullptr) return TOPK_ERR_INVALID_ARG;
+  if (misaligned(a.requests, 4)) return TOPK_ERR_MISALIGNED;
+  FreeParams p{};
+  p.a = a;
+  p.status = static_cast<uint32_t*>(a.pool.workspace);
+  return launch_cluster(free_kernel, static_cast<const FreeParams&>(p), static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int topk_page_compact(const topk_page_compact_args* args, void* stream) {
+  using namespace ltk::paged;
+  if (args == nullptr) return TOPK_ERR_INVALID_ARG;
+  const topk_page_compact_args& a = *args;
+  const int rc = check_pool(a.pool);
+  if (rc != TOPK_OK) return rc;
+  const topk_page_pool& t = a.pool;
+  if (a.max_copies < 0 || a.max_copies > INT32_MAX || a.table_out_stride < t.max_blocks) return TOPK_ERR_INVALID_ARG;
+  if ((a.max_copies > 0 && (a.source == nullptr || a.target == nullptr)) || (t.num_requests > 0 && a.block_table_out == nullptr) ||
+      (t.num_blocks > 0 && (a.shares_out == nullptr || a.scratch == nullptr)) || (t.num_free > 0 && a.free_blocks_out == nullptr) || a.taken_out == nullptr)
+    return TOPK_ERR_INVALID_ARG;
+  if (misaligned(a.source, 4) || misaligned(a.target, 4) || misaligned(a.block_table_out, 4) || misaligned(a.shares_out, 4) ||
+      misaligned(a.free_blocks_out, 4) || misaligned(a.taken_out, 4) || misaligned(a.scratch, 16))
+    return TOPK_ERR_MISALIGNED;
+  if (a.scratch_bytes < static_cast<size_t>(t.num_blocks) * 3 * sizeof(int32_t)) return TOPK_ERR_WORKSPACE_TOO_SMALL;
+  CompactParams p{};
+  p.a = a;
+  p.status = static_cast<uint32_t*>(t.workspace);
+  return launch_cluster(compact_kernel, static_cast<const CompactParams&>(p), static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int topk_page_copy(const topk_page_copy_args* args, void* stream) {
+  using namespace ltk::paged;
+  if (args == nullptr) return TOPK_ERR_INVALID_ARG;
+  const topk_page_copy_args& a = *args;
+  if (a.num_copies < 0 || a.num_copies > INT32_MAX || a.num_caches < 0 || a.num_caches > TOPK_MAX_PAGE_CACHES || (a.num_caches > 0 && a.caches == nullptr))
+    return TOPK_ERR_INVALID_ARG;
+  Cache caches[TOPK_MAX_PAGE_CACHES];
+  int64_t chunks = 0;
+  for (int i = 0; i < a.num_caches; ++i) {
+    const topk_page_cache& c = a.caches[i];
+    if (c.num_blocks < 0 || c.num_blocks > INT32_MAX || c.n0 < 1 || c.n1 < 1 || c.run_bytes < 1 || (c.num_blocks > 0 && c.base == nullptr)) return TOPK_ERR_INVALID_ARG;
+    const uint64_t all = reinterpret_cast<uint64_t>(c.base) | static_cast<uint64_t>(c.block_stride) | static_cast<uint64_t>(c.run_bytes) |
+                         (c.n0 > 1 ? static_cast<uint64_t>(c.stride0) : 0) | (c.n1 > 1 ? static_cast<uint64_t>(c.stride1) : 0);
+    int shift = 0;
+    while (shift < 4 && !(all >> shift & 1)) ++shift;
+    const int64_t run = c.run_bytes >> shift;
+    if (run > INT32_MAX || run * c.n0 > INT32_MAX || run * c.n0 * c.n1 > INT32_MAX - kCopyThreads * kAtOnce) return TOPK_ERR_UNSUPPORTED;
+    const int64_t pieces = run * c.n0 * c.n1;
+    caches[i] = Cache{static_cast<char*>(c.base), c.block_stride, c.stride0, c.stride1, static_cast<int32_t>(c.num_blocks), c.n1,
+                      static_cast<uint32_t>(pieces), static_cast<uint32_t>(run), static_cast<uint32_t>(chunks), shift};
+    chunks += (pieces + kCopyThreads * kAtOnce - 1) / (kCopyThreads * kAtOnce);
+    if (chunks > INT32_MAX) return TOPK_ERR_UNSUPPORTED;
+  }
+  if (a.num_copies == 0 || a.num_caches == 0) return TOPK_OK;
+  if (a.source == nullptr || a.target == nullptr || a.workspace == nullptr) return TOPK_ERR_INVALID_ARG;
+  if (misaligned(a.source, 4) || misaligned(a.target, 4) || misaligned(a.workspace, 16)) return TOPK_ERR_MISALIGNED;
+  const int sms = num_sms();
+  if (sms < 1) return TOPK_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return a.num_caches <= kFewCaches ? run_copy<kFewCaches>(a, caches, static_cast<uint32_t>(chunks), sms, s)
+                                    : run_copy<TOPK_MAX_PAGE_CACHES>(a, caches, static_cast<uint32_t>(chunks), sms, s);
+}

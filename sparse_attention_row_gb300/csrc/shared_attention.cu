@@ -1,0 +1,204 @@
+// topk_shared_attention: attention over everything cached, for requests of which some begin with the same pages.
+//
+//   softmax over a row's tokens, split in two:  out = w_p out_p + w_t out_t,  w = exp(lse - log(exp(lse_p) + exp(lse_t)))
+//
+// for the prefix's tokens p and those behind it, t. Three steps, in order on the stream:
+//   plan    which rows share what, from the rows' lengths and requests, on the device: a run is as many neighbouring rows
+//           with the same prefix as fill a unit's columns, and every row gets its length behind the prefix.
+//   tails   attention over what is behind the prefixes, each request by itself (kTail): bound by HBM. Its results stand in
+//           `out` and `lse`.
+//   prefix  attention over the prefixes, a run of rows at a time (kShared), which reads a prefix once for 64 columns or more, and
+//           joins its results with those of the tails as it writes them.
+#include "attention_forms.cuh"
+#include "paged.cuh"
+
+namespace ltk {
+namespace paged {
+namespace {
+
+constexpr int kThreads = 1024;
+
+struct PlanParams {
+  Rows R;
+  const int32_t* prefix_of;
+  int64_t num_prefixes;
+  const int32_t* prefix_lens;
+  int64_t prefix_most;  // tokens of a prefix's row of the table
+  int32_t run_rows;     // of a run at most
+  int32_t* tail_lengths;
+  int32_t* skip;
+  SharedRun* runs;
+  int32_t* run_count;
+};
+
+// Tokens of a row's prefix, whole pages; 0: nothing shared. `prefix`: which one.
+__device__ __forceinline__ int shared_tokens(const PlanParams& p, int64_t request, int32_t* prefix) {
+  if (request < 0 || request >= p.R.num_requests) return 0;
+  *prefix = p.prefix_of[request];
+  if (*prefix < 0 || *prefix >= p.num_prefixes) return 0;
+  const int64_t n = p.prefix_lens[*prefix];
+  if (n <= 0) return 0;
+  const int held = static_cast<int>(n < p.prefix_most ? n : p.prefix_most);
+  return block_column(p.R, held) * p.R.block_size;
+}
+
+// What row `row` shares, and with whom: 0 where one of its request's rows, which read the rest together, sees less.
+__device__ __forceinline__ int row_shares(const PlanParams& p, int64_t row, int32_t* prefix) {
+  const int64_t request = row_request(p.R, row);
+  const int n = shared_tokens(p, request, prefix);
+  if (n == 0) return 0;
+  if (p.R.row_request) return seen_tokens(p.R, p.R.lengths[row], request) >= n ? n : 0;
+  for (int j = 0; j < p.R.next_n; ++j)
+    if (seen_tokens(p.R, p.R.lengths[request * p.R.next_n + j], request) < n) return 0;
+  return n;
+}
+
+// One CTA: rows 1024 at a time, with the start of the run that the last segment ended in.
+__global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
+  __shared__ int64_t key[kThreads + 2];  // prefix and tokens of each row of the segment, and of its neighbours
+  __shared__ int32_t warp_start[kThreads / 32], warp_ends[kThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  dependent_wait();
+  dependent_launch();
+  const auto key_of = [&](int64_t row) -> int64_t {
+    int32_t prefix = -1;
+    if (row < 0 || row >= p.R.num_rows) return -1;
+    const int n = row_shares(p, row, &prefix);
+    return n == 0 ? -1 : static_cast<int64_t>(prefix) << 32 | n;
+  };
+  uint32_t bits = 0;
+  int64_t start = 0;  // of the run so far
+  int32_t count = 0;  // runs listed
+  for (int64_t row0 = 0; row0 < p.R.num_rows; row0 += kThreads) {
+    const int64_t row = row0 + tid;
+    const bool real = row < p.R.num_rows;
+    const int64_t mine = key_of(row);
+    key[tid + 1] = mine;
+    if (tid == 0) key[0] = key_of(row0 - 1);
+    if (tid == kThreads - 1) key[kThreads + 1] = key_of(row + 1);
+    if (real) {
+      const int64_t request = row_request(p.R, row);
+      const int32_t n = p.R.lengths[row];
+      if (request >= p.R.num_requests) bits |= TOPK_DEV_BAD_BLOCK;
+      if (request >= 0 && request < p.R.num_requests) {
+        if (n < 0 || n > p.R.max_len) bits |= TOPK_DEV_LENGTH_CLAMPED;
+        if (p.prefix_of[request] >= p.num_prefixes) bits |= TOPK_DEV_BAD_BLOCK;
+      }
+      const int shared = mine < 0 ? 0 : static_cast<int32_t>(mine);
+      p.tail_lengths[row] = seen_tokens(p.R, n, request) - shared;
+      p.skip[row] = block_column(p.R, shared);
+    }
+    __syncthreads();
+    // the start of each row's run: the last row at or before it whose key is another than the row's before
+    int32_t from = real && key[tid] != mine ? tid : -1;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int32_t x = __shfl_up_sync(~0u, from, d);
+      if (lane >= d) from = max(from, x);
+    }
+    if (lane == 31) warp_start[warp] = from;
+    __syncthreads();
+    int32_t before = -1;
+    for (int w = 0; w < warp; ++w) before = max(before, warp_start[w]);
+    from = max(from, before);
+    const int64_t run_start = from >= 0 ? row0 + from : start;
+    const int64_t at = row - run_start;
+    const bool ends = real && mine >= 0 && (key[tid + 2] != mine || at % p.run_rows == p.run_rows - 1);
+    const unsigned who = __ballot_sync(~0u, ends);
+    if (lane == 0) warp_ends[warp] = __popc(who);
+    __syncthreads();
+    int32_t place = count + __popc(who & ((1u << lane) - 1)), total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) place += warp_ends[w];
+      total += warp_ends[w];
+    }
+    if (ends) {
+      const int rows = static_cast<int>(at % p.run_rows) + 1;
+      p.runs[place] = SharedRun{static_cast<int32_t>(row - rows + 1), rows, static_cast<int32_t>(mine >> 32), static_cast<int32_t>(mine)};
+    }
+    count += total;
+    int32_t last = -1;
+    for (int w = 0; w < kThreads / 32; ++w) last = max(last, warp_start[w]);
+    if (last >= 0) start = row0 + last;
+    __syncthreads();  // the next segment writes the sums again
+  }
+  if (tid == 0) *p.run_count = count;
+  if (bits) atomicOr(p.R.status, bits);
+}
+
+size_t round_up(size_t n) { return (n + 255) / 256 * 256; }
+
+// Scratch: the number of runs, the runs, rows' lengths behind the prefix and their first columns, the tails' statistics.
+struct Scratch {
+  size_t runs, lengths, skip, tail_lse, end;
+  Scratch(int sms, int64_t rows) {
+    runs = 256;
+    lengths = runs + round_up(sizeof(SharedRun) * rows);
+    skip = lengths + round_up(sizeof(int32_t) * rows);
+    tail_lse = skip + round_up(sizeof(int32_t) * rows);
+    end = tail_lse + static_cast<size_t>(sms > 16 ? sms : 16) * 2 * kSharedCols * sizeof(float);
+  }
+};
+
+}  // namespace
+}  // namespace paged
+}  // namespace ltk
+
+extern "C" size_t topk_shared_attention_scratch_size(int device, int64_t num_rows) {
+  topk_device_props p{};
+  if (topk_query_device(device, &p) != TOPK_OK) return 0;
+  return ltk::paged::Scratch(p.num_sms, num_rows < 0 ? 0 : num_rows).end;
+}
+
+extern "C" int topk_shared_attention(const topk_shared_attention_args* args, void* stream) {
+  using namespace ltk::paged;
+  if (args == nullptr) return TOPK_ERR_INVALID_ARG;
+  const topk_shared_attention_args& s = *args;
+  const topk_attention_args& a = s.attention;
+  if (a.indices != nullptr || s.num_prefixes < 0 || s.num_prefixes > INT32_MAX || s.prefix_blocks < 1 || s.prefix_blocks > INT32_MAX ||
+      s.prefix_stride < s.prefix_blocks)
+    return TOPK_ERR_INVALID_ARG;
+  int rc = check_attention(a);
+  if (rc != TOPK_OK || a.rows.num_rows == 0) return rc;
+  if (a.lse == nullptr || s.prefix_of == nullptr || s.scratch == nullptr || (s.num_prefixes > 0 && (s.prefix_lens == nullptr || s.prefix_table == nullptr)))
+    return TOPK_ERR_INVALID_ARG;
+  if (misaligned(s.prefix_of, 4) || misaligned(s.prefix_lens, 4) || misaligned(s.prefix_table, 4) || misaligned(s.scratch, 16)) return TOPK_ERR_MISALIGNED;
+  int device = 0;
+  topk_device_props props{};
+  if (cudaGetDevice(&device) != cudaSuccess || topk_query_device(device, &props) != TOPK_OK) {
+    cudaGetLastError();
+    return TOPK_ERR_CUDA;
+  }
+  const Scratch at(props.num_sms, a.rows.num_rows);
+  if (s.scratch_bytes < at.end || a.workspace_bytes < topk_attention_workspace_size(device)) return TOPK_ERR_WORKSPACE_TOO_SMALL;
+  char* scratch = static_cast<char*>(s.scratch);
+  const int64_t held = s.prefix_blocks > INT32_MAX / a.rows.block_size ? INT32_MAX : s.prefix_blocks * a.rows.block_size;
+
+  PlanParams p{};
+  p.R = make_rows(a.rows, INT32_MAX, a.workspace);
+  p.prefix_of = s.prefix_of;
+  p.num_prefixes = s.num_prefixes;
+  p.prefix_lens = s.prefix_lens;
+  p.prefix_most = held;
+  p.run_rows = rows_of_run(a);
+  p.tail_lengths = reinterpret_cast<int32_t*>(scratch + at.lengths);
+  p.skip = reinterpret_cast<int32_t*>(scratch + at.skip);
+  p.runs = reinterpret_cast<SharedRun*>(scratch + at.runs);
+  p.run_count = reinterpret_cast<int32_t*>(scratch);
+  rc = launch(plan_kernel, p, 1, kThreads, 0, static_cast<cudaStream_t>(stream));
+  if (rc != TOPK_OK) return rc;
+
+  FormArgs f{};
+  f.skip = p.skip;
+  topk_attention_args tail = a;
+  tail.rows.lengths = p.tail_lengths;
+  rc = attend_tail(tail, f, stream);
+  if (rc != TOPK_OK || s.num_prefixes == 0) return rc;
+  f.runs = p.runs;
+  f.run_count = p.run_count;
+  f.prefix_table = s.prefix_table;
+  f.prefix_stride = s.prefix_stride;
+  f.prefix_most = held;
+  f.tail_lse = reinterpret_cast<float*>(scratch + at.tail_lse);
+  return attend_shared(tail, f, stream);
+}

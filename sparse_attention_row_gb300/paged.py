@@ -1,5 +1,6 @@
 """The calls around the selection, for torch tensors: a paged cache's map, the
-indexer's logits, and attention over the cache.
+indexer's logits, attention over the cache (over chosen blocks of it, and over
+prefixes that requests share), the blocks' means and scores, and the pages themselves.
 
 Argument marshalling only, like the rest of the binding: shapes, strides and
 types are read from the tensors, checked, and handed to ``libtopk.so``. A decode
@@ -8,6 +9,7 @@ arguments are packed in one go: a call with its outputs given is enqueued in 7 t
 """
 from __future__ import annotations
 
+import ctypes
 import struct
 from typing import NamedTuple
 
@@ -18,7 +20,18 @@ import sparse_attention_row_gb300 as _sar
 _ROWS = "qiiqqPPPqq"
 _MAP = struct.Struct("@PPqiPqqPqPPPPPPqP")
 _LOGITS = struct.Struct("@" + _ROWS + "iiiPqqPqPqqPqqPqqP")
-_ATTENTION = struct.Struct("@" + _ROWS + "iiiiifPqqPqqqPqqqPqiPqqPPN")
+_ATTEND = _ROWS + "iiiiifPqqPqqqPqqqPqiPqqPPN"
+_POOL = "PqqqPqPqPP"
+_ATTENTION = struct.Struct("@" + _ATTEND)
+_MEANS = struct.Struct("@PPqiiPqqqiiPqqqPqqP")
+_SCORES = struct.Struct("@" + _ROWS + "iiiiiiPqqPqqPqqqPP")
+_BLOCKS = struct.Struct("@" + _ATTEND + "Pqqq")
+_SHARED = struct.Struct("@" + _ATTEND + "PqPPqqPN")
+_FORK = struct.Struct("@" + _POOL + "PPPqiPP")
+_FREE = struct.Struct("@" + _POOL + "Pq")
+_COMPACT = struct.Struct("@" + _POOL + "qPPPqPPPPN")
+_CACHE = struct.Struct("@PqqqqiiQ")
+_COPY = struct.Struct("@PPqPiP")
 
 
 class KvMap(NamedTuple):
@@ -27,6 +40,20 @@ class KvMap(NamedTuple):
     row_lens: "torch.Tensor"     # int32 [max_tokens], position + 1: the rows' lengths  # noqa: F821
     row_request: "torch.Tensor"  # int32 [max_tokens], -1 past the last token  # noqa: F821
     token_start: "torch.Tensor"  # int32 [requests + 1]  # noqa: F821
+
+
+class PageCopies(NamedTuple):
+    """Pages to copy: what ``PagedDecoder.fork_pages`` and ``compact_pages`` list and ``copy_pages`` does; -1 where there is nothing to copy."""
+    source: "torch.Tensor"  # int32 [copies]  # noqa: F821
+    target: "torch.Tensor"  # int32 [copies]  # noqa: F821
+
+
+class PageCaches:
+    """Caches whose pages are copied together, read once: made by ``PagedDecoder.page_caches``."""
+
+    def __init__(self, tensors, packed: bytes):
+        self.tensors, self.packed, self.address = tensors, ctypes.create_string_buffer(packed, max(len(packed), 1)), 0
+        self.address = ctypes.addressof(self.packed)
 
 
 class PagedDecoder:
@@ -47,7 +74,11 @@ class PagedDecoder:
         self._dev = torch.device("cuda", device)
         lib = _sar._load()
         self._kv_map, self._index_logits, self._attention = lib.topk_kv_map, lib.topk_index_logits, lib.topk_paged_attention
-        self._f32, self._i32, self._i64 = torch.float32, torch.int32, torch.int64
+        self._block_means, self._block_scores, self._block_attention = lib.topk_block_means, lib.topk_block_scores, lib.topk_block_attention
+        self._shared_attention = lib.topk_shared_attention
+        self._fork, self._free, self._compact, self._copy = lib.topk_page_fork, lib.topk_page_free, lib.topk_page_compact, lib.topk_page_copy
+        self._f32, self._i32, self._i64, self._u8 = torch.float32, torch.int32, torch.int64, torch.uint8
+        self._scratch = {}  # bytes that shared_attention needs, by the number of rows
         self._dtypes = {torch.float16: 1, torch.bfloat16: 2, torch.float8_e4m3fn: 3}
         self._empty_tensor = torch.empty
         self._get_device, self._get_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
@@ -212,13 +243,8 @@ class PagedDecoder:
             *rows_args, kind, heads, dim, qp, q0, q1, wp, w0, kp, k0, k1, sp, s0, s1, op, o0, width, self._workspace_ptr), stream)
         return out
 
-    def attention(self, q, k_cache, block_table, lengths, v_cache=None, v_dim: int | None = None, indices=None,
-                  scale: float | None = None, next_n: int | None = None, row_request=None, out=None, lse=None,
-                  return_lse: bool = False, stream=None):
-        """Attention of q [rows, heads, dk] over a paged cache [blocks, block_size, kv_heads, dk] (or without
-        the heads' dimension), over every token below each row's length or over ``indices``
-        (int32 [rows, n], as the selection writes them). ``v_cache`` None: a token's value is the first
-        ``v_dim`` elements of its key (latent attention). Returns out, or (out, lse)."""
+    def _attend(self, q, k_cache, block_table, lengths, v_cache, v_dim, indices, scale, next_n, row_request, out, lse, return_lse, stream):
+        """Checks an attention call's tensors: (its packed arguments' values, out, lse)."""
         rows, heads, dk = q.shape
         dtype = q.dtype
         kind = self._dtypes.get(dtype)
@@ -256,7 +282,192 @@ class PagedDecoder:
         elif return_lse:
             lse = self._empty((rows, heads), self._f32, stream)
             lp = lse.data_ptr()
-        self._call(self._attention, _ATTENTION.pack(
-            *rows_args, kind, heads, kv_heads, dk, v_dim, dk ** -0.5 if scale is None else scale, qp, q0, q1,
-            kp, k0, k1, k2, vp, v0, v1, v2, ip, i0, topk, op, o0, o1, lp, self._workspace_ptr, self.nbytes), stream)
+        return (*rows_args, kind, heads, kv_heads, dk, v_dim, dk ** -0.5 if scale is None else scale, qp, q0, q1,
+                kp, k0, k1, k2, vp, v0, v1, v2, ip, i0, topk, op, o0, o1, lp, self._workspace_ptr, self.nbytes), out, lse
+
+    def attention(self, q, k_cache, block_table, lengths, v_cache=None, v_dim: int | None = None, indices=None,
+                  scale: float | None = None, next_n: int | None = None, row_request=None, out=None, lse=None,
+                  return_lse: bool = False, stream=None):
+        """Attention of q [rows, heads, dk] over a paged cache [blocks, block_size, kv_heads, dk] (or without
+        the heads' dimension), over every token below each row's length or over ``indices``
+        (int32 [rows, n], as the selection writes them). ``v_cache`` None: a token's value is the first
+        ``v_dim`` elements of its key (latent attention). Returns out, or (out, lse)."""
+        args, out, lse = self._attend(q, k_cache, block_table, lengths, v_cache, v_dim, indices, scale, next_n, row_request, out, lse, return_lse, stream)
+        self._call(self._attention, _ATTENTION.pack(*args), stream)
         return (out, lse) if return_lse else out
+
+    # ---- blocks chosen by a cheap score ----
+
+    def block_means(self, k_cache, block_table, context_lens, new_lens, means, stream=None):
+        """Brings ``means`` ([blocks, kv_heads, dk], of k_cache's type, in place) up to date after a step in which the requests
+        got ``new_lens`` tokens behind ``context_lens`` (int32 [requests]): the mean key of every page that holds one of them."""
+        dtype, n = k_cache.dtype, len(block_table)
+        kind = self._dtypes.get(dtype)
+        if kind is None:
+            raise ValueError(f"k_cache has an unsupported type {dtype}")
+        kp, k0, k1, k2, (blocks, block_size, kv_heads), dk = self._cache("k_cache", k_cache, dtype)
+        mp, (m0, m1, _) = self._vectors("means", means, dtype, 3)
+        if means.shape != (blocks, kv_heads, dk):
+            self._bad("means", means, f"a {(blocks, kv_heads, dk)} tensor")
+        table, stride, columns = self._matrix("block_table", block_table, self._i32, n)
+        self._call(self._block_means, _MEANS.pack(
+            self._ints("context_lens", context_lens, n), self._ints("new_lens", new_lens, n), n, block_size, kind, table,
+            stride if n > 1 or stride >= columns else columns, columns, blocks, kv_heads, dk, kp, k0, k1, k2, mp, m0, m1, self._workspace_ptr), stream)
+        return means
+
+    def block_scores(self, q, means, block_table, lengths, block_size: int, sink_blocks: int = 0, recent_blocks: int = 0,
+                     next_n: int | None = None, row_request=None, out=None, lens=None, stream=None):
+        """Scores of every block (page) that a row sees, for each key-value head: the sum of the head's queries
+        (q [rows, heads, dk]) times the page's mean key (``means`` [blocks, kv_heads, dk]); +inf for the first ``sink_blocks`` and the
+        last ``recent_blocks``. Returns (fp32 [rows, kv_heads, columns], int32 [rows, kv_heads]: the blocks that each sees), which
+        is what the selection takes: ``selector(scores.flatten(0, 1), lens.flatten(), n)``. Scores past them are left as they are."""
+        rows, heads, dk = q.shape
+        dtype = q.dtype
+        kind = self._dtypes.get(dtype)
+        if kind is None:
+            raise ValueError(f"q has an unsupported type {dtype}")
+        (qp, (q0, q1, _)), (mp, (m0, m1, _)) = self._vectors("q", q, dtype, 3), self._vectors("means", means, dtype, 3)
+        blocks, kv_heads, mean_dim = means.shape
+        if mean_dim != dk:
+            raise ValueError("q and means must have the same last dimension")
+        rows_args = self._rows(rows, lengths, block_table, blocks, block_size, next_n, row_request)
+        if out is None:
+            out = self._empty((rows, kv_heads, block_table.shape[1]), self._f32, stream)
+        op, (o0, o1, _) = self._vectors("out", out, self._f32, 3)
+        if out.shape[:2] != (rows, kv_heads):
+            self._bad("out", out, f"a {(rows, kv_heads)} x columns tensor")
+        if lens is None:
+            lens = self._empty((rows, kv_heads), self._i32, stream)
+        lp, _, lens_heads = self._matrix("lens", lens, self._i32, rows)
+        if lens_heads != kv_heads or not lens.is_contiguous():
+            self._bad("lens", lens, f"a contiguous {(rows, kv_heads)} tensor")
+        self._call(self._block_scores, _SCORES.pack(
+            *rows_args, kind, heads, kv_heads, dk, sink_blocks, recent_blocks, qp, q0, q1, mp, m0, m1, op, o0, o1, out.shape[2], lp, self._workspace_ptr), stream)
+        return out, lens
+
+    def block_attention(self, q, k_cache, block_table, lengths, blocks, v_cache=None, v_dim: int | None = None, scale: float | None = None,
+                        next_n: int | None = None, row_request=None, out=None, lse=None, return_lse: bool = False, stream=None):
+        """``attention`` over the tokens of chosen blocks: ``blocks`` int32 [rows, kv_heads, n], a list for each key-value head, or
+        [rows, n], one for all heads of a row; columns of the row's request in the table, -1 where there is none."""
+        args, out, lse = self._attend(q, k_cache, block_table, lengths, v_cache, v_dim, None, scale, next_n, row_request, out, lse, return_lse, stream)
+        rows, kv_heads = q.shape[0], args[12]
+        bp, strides = self._vectors("blocks", blocks, self._i32, blocks.dim() if blocks.dim() in (2, 3) else 3)
+        if blocks.shape[0] != rows or (len(strides) == 3 and blocks.shape[1] != kv_heads):
+            self._bad("blocks", blocks, f"a {(rows, kv_heads)} x n or {rows} x n tensor")
+        self._call(self._block_attention, _BLOCKS.pack(*args, bp, strides[0], strides[1] if len(strides) == 3 else 0, blocks.shape[-1]), stream)
+        return (out, lse) if return_lse else out
+
+    # ---- a prefix that requests share ----
+
+    def shared_attention(self, q, k_cache, block_table, lengths, prefix_of, prefix_lens, prefix_table, v_cache=None, v_dim: int | None = None,
+                         scale: float | None = None, next_n: int | None = None, row_request=None, out=None, lse=None,
+                         return_lse: bool = False, stream=None):
+        """``attention`` over everything cached, for requests of which some begin with the same pages: request b with the first
+        ``prefix_lens[prefix_of[b]]`` tokens of the pages in ``prefix_table[prefix_of[b]]`` (int32 [requests], negative: nothing shared;
+        [prefixes]; [prefixes, columns]). Their whole pages are read once for all neighbouring rows that begin with them. Lengths count the
+        prefix, and the rows of ``block_table`` have its pages' columns."""
+        args, out, lse = self._attend(q, k_cache, block_table, lengths, v_cache, v_dim, None, scale, next_n, row_request, out, lse, True, stream)
+        prefixes = len(prefix_table)
+        table, stride, columns = self._matrix("prefix_table", prefix_table, self._i32, prefixes)
+        rows = q.shape[0]
+        need = self._scratch.get(rows)
+        if need is None:
+            need = self._scratch[rows] = _sar.topk_shared_attention_scratch_size(self.device, rows)
+        scratch = self._empty(need, self._u8, stream)
+        self._call(self._shared_attention, _SHARED.pack(
+            *args, self._ints("prefix_of", prefix_of, len(block_table)), prefixes, self._ints("prefix_lens", prefix_lens, prefixes), table,
+            stride if prefixes > 1 or stride >= columns else columns, columns, scratch.data_ptr(), need), stream)
+        return (out, lse) if return_lse else out
+
+    # ---- the pages ----
+
+    def _pool(self, block_table, shares, free_blocks, taken):
+        requests, blocks, free = len(block_table), shares.numel(), free_blocks.numel()
+        table, stride, columns = self._matrix("block_table", block_table, self._i32, requests)
+        return (table, requests, stride if requests > 1 or stride >= columns else columns, columns, self._ints("shares", shares, blocks), blocks,
+                self._ints("free_blocks", free_blocks, free), free, self._ints("taken", taken, 1), self._workspace_ptr)
+
+    def _copies(self, out, n: int, stream):
+        if out is None:
+            out = PageCopies(self._empty(n, self._i32, stream), self._empty(n, self._i32, stream))
+        return out, self._ints("out.source", out.source, n), self._ints("out.target", out.target, n)
+
+    def fork_pages(self, parents, children, kept_lens, block_table, shares, free_blocks, taken, block_size: int,
+                   out: PageCopies | None = None, stream=None) -> PageCopies:
+        """Gives each of ``children`` (rows of the table, int32) the first ``kept_lens`` tokens of its parent: it shares the parent's whole
+        pages (``shares``: int32 [blocks], holders beyond the first), and gets a page of its own from ``free_blocks`` for what is left
+        (``taken`` advances, as in ``kv_map``). Returns the copies into those, for ``copy_pages``. All in place; free what a child holds first."""
+        n = parents.numel()
+        pool = self._pool(block_table, shares, free_blocks, taken)
+        out, source, target = self._copies(out, n, stream)
+        self._call(self._fork, _FORK.pack(*pool, self._ints("parents", parents, n), self._ints("children", children, n), self._ints("kept_lens", kept_lens, n), n, block_size, source, target), stream)
+        return out
+
+    def free_pages(self, requests, block_table, shares, free_blocks, taken, stream=None) -> None:
+        """Takes the pages of ``requests`` (rows of the table, int32) back, in place: those that no other row holds are put in front of
+        the free ones (``taken`` goes down), in the order of requests and columns; the rows are set to -1."""
+        n = requests.numel()
+        self._call(self._free, _FREE.pack(*self._pool(block_table, shares, free_blocks, taken), self._ints("requests", requests, n), n), stream)
+
+    def compact_pages(self, block_table, shares, free_blocks, taken, max_copies: int, table_out=None, shares_out=None, free_out=None,
+                      taken_out=None, out: PageCopies | None = None, stream=None) -> PageCopies:
+        """Moves the highest pages that the table names to the lowest free numbers, ``max_copies`` of them at most, and sorts the free
+        ones. In place, or into the tensors that are given. Returns the moves; ``copy_pages`` brings the contents over."""
+        pool = self._pool(block_table, shares, free_blocks, taken)
+        requests, columns, blocks, free = pool[1], pool[3], pool[5], pool[7]
+        table, stride = pool[0], pool[2]
+        if table_out is not None:
+            table, stride, wide = self._matrix("table_out", table_out, self._i32, requests)
+            if wide != columns:
+                self._bad("table_out", table_out, f"a {(requests, columns)} tensor")
+            stride = stride if requests > 1 or stride >= columns else columns
+        out, source, target = self._copies(out, max_copies, stream)
+        scratch = self._empty(12 * blocks, self._u8, stream)
+        self._call(self._compact, _COMPACT.pack(
+            *pool, max_copies, source, target, table, stride, pool[4] if shares_out is None else self._ints("shares_out", shares_out, blocks),
+            pool[6] if free_out is None else self._ints("free_out", free_out, free), pool[8] if taken_out is None else self._ints("taken_out", taken_out, 1),
+            scratch.data_ptr(), 12 * blocks), stream)
+        return out
+
+    def page_caches(self, caches) -> PageCaches:
+        """Reads caches ([blocks, ...] each, any type and strides whose pages are at most two loops over runs of bytes) for ``copy_pages``, to be
+        kept by programs that copy among the same ones again."""
+        caches = list(caches)
+        if len(caches) > _sar.TOPK_MAX_PAGE_CACHES:
+            raise ValueError(f"at most {_sar.TOPK_MAX_PAGE_CACHES} caches at a time")
+        return PageCaches(caches, b"".join([self._page_cache(t) for t in caches]))
+
+    def _page_cache(self, t) -> bytes:
+        if t.dim() < 1 or t.get_device() != self.device or t.dim() > 1 and 0 in t.shape[1:]:
+            self._bad("a cache", t, "a [blocks, ...] tensor")
+        size, strides, shape = t.element_size(), t.stride(), t.shape
+        if t.is_contiguous():
+            run, loops = t[0].numel() if shape[0] else 1, []
+        else:
+            # the loops over a page, the inner ones first; those that follow one another in memory are one
+            run, loops = 1, []
+            for stride, n in sorted((stride, n) for stride, n in zip(strides[1:], shape[1:]) if n > 1):
+                if not loops and stride == run:
+                    run *= n
+                elif loops and stride == loops[-1][0] * loops[-1][1]:
+                    loops[-1][1] *= n
+                else:
+                    loops.append([stride, n])
+            ends = run
+            for stride, n in loops:
+                if stride < ends:
+                    self._bad("a cache", t, "a tensor whose elements do not overlap")
+                ends = stride * (n - 1) + ends
+            if len(loops) > 2 or (shape[0] > 1 and strides[0] == 0):
+                self._bad("a cache", t, "a tensor whose pages are at most two loops over runs of memory")
+        (s0, n0), (s1, n1) = (loops[::-1] + [[0, 1], [0, 1]])[:2]
+        return _CACHE.pack(t.data_ptr(), shape[0], strides[0] * size, s0 * size, s1 * size, n0, n1, run * size)
+
+    def copy_pages(self, caches, copies: PageCopies, stream=None) -> None:
+        """Copies page ``copies.source[i]`` to ``copies.target[i]`` in every one of ``caches`` (tensors [blocks, ...]: layers' keys, values,
+        scales, means; or what ``page_caches`` made of them); pairs with a -1 are skipped. No target may be listed twice, or as a source."""
+        if not isinstance(caches, PageCaches):
+            caches = self.page_caches(caches)
+        n = copies.source.numel()
+        self._call(self._copy, _COPY.pack(self._ints("source", copies.source, n), self._ints("target", copies.target, n), n, caches.address,
+                                          len(caches.tensors), self._workspace_ptr), stream)
