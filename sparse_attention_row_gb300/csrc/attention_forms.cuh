@@ -70,10 +70,21 @@ inline int check_attention(const topk_attention_args& a) {
   return TOPK_OK;
 }
 
-// Columns (rows and heads) of a unit at most, where rows share a prefix; and the rows of a run: what fills them.
-constexpr int kSharedCols = 64;
+// Columns (rows and heads) of a unit at most, where rows share a prefix: kWideCols in wide_prefix.cu, which takes keys and values
+// of up to 128 dims that are not one, kSharedCols in the kernel of all forms.
+constexpr int kSharedCols = 64, kWideCols = 256;
+
+int attend_wide(const topk_attention_args& a, const FormArgs& f, void* scratch, void* stream);
+size_t wide_scratch(int sms);
+
+inline bool takes_wide(const topk_attention_args& a) {
+  const int group = a.heads / a.kv_heads;
+  return a.v != nullptr && a.dk <= 128 && a.dv <= 128 && group <= kWideCols && a.rows.num_rows * group > kSharedCols;
+}
+
+// Rows of a run: what fills a unit's columns.
 inline int rows_of_run(const topk_attention_args& a) {
-  const int group = a.heads / a.kv_heads, rows = group >= kSharedCols ? 1 : kSharedCols / group;
+  const int group = a.heads / a.kv_heads, cols = takes_wide(a) ? kWideCols : kSharedCols, rows = group >= cols ? 1 : cols / group;
   return rows < a.rows.num_rows ? rows : static_cast<int>(a.rows.num_rows);
 }
 

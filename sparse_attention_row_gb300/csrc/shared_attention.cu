@@ -7,8 +7,8 @@
 //           with the same prefix as fill a unit's columns, and every row gets its length behind the prefix.
 //   tails   attention over what is behind the prefixes, each request by itself (kTail): bound by HBM. Its results stand in
 //           `out` and `lse`.
-//   prefix  attention over the prefixes, a run of rows at a time (kShared), which reads a prefix once for 64 columns or more, and
-//           joins its results with those of the tails as it writes them.
+//   prefix  attention over the prefixes, a run of rows at a time, which joins its results with those of the tails as it writes
+//           them: wide_prefix.cu, 256 columns a run, or kShared of the kernel of all forms, 64.
 #include "attention_forms.cuh"
 #include "paged.cuh"
 
@@ -128,7 +128,8 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
 
 size_t round_up(size_t n) { return (n + 255) / 256 * 256; }
 
-// Scratch: the number of runs, the runs, rows' lengths behind the prefix and their first columns, the tails' statistics.
+// Scratch: the number of runs, the runs, rows' lengths behind the prefix and their first columns, the tails' statistics or the
+// parts of the wide kernel.
 struct Scratch {
   size_t runs, lengths, skip, tail_lse, end;
   Scratch(int sms, int64_t rows) {
@@ -136,7 +137,8 @@ struct Scratch {
     lengths = runs + round_up(sizeof(SharedRun) * rows);
     skip = lengths + round_up(sizeof(int32_t) * rows);
     tail_lse = skip + round_up(sizeof(int32_t) * rows);
-    end = tail_lse + static_cast<size_t>(sms > 16 ? sms : 16) * 2 * kSharedCols * sizeof(float);
+    const size_t few = static_cast<size_t>(sms > 16 ? sms : 16) * 2 * kSharedCols * sizeof(float), many = wide_scratch(sms);
+    end = tail_lse + (few > many ? few : many);
   }
 };
 
@@ -200,5 +202,5 @@ extern "C" int topk_shared_attention(const topk_shared_attention_args* args, voi
   f.prefix_stride = s.prefix_stride;
   f.prefix_most = held;
   f.tail_lse = reinterpret_cast<float*>(scratch + at.tail_lse);
-  return attend_shared(tail, f, stream);
+  return takes_wide(a) ? attend_wide(tail, f, f.tail_lse, stream) : attend_shared(tail, f, stream);
 }

@@ -178,6 +178,19 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[N]) {
   for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));  // used from here on, not before
 }
 
+// 32 columns of two values each, or of what else fills 32 bits.
+__device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t* v) {
+  __syncwarp();
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+      "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]),
+      "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]),
+      "r"(v[31])
+      : "memory");
+}
+
 __device__ __forceinline__ void tmem_store8(uint32_t addr, const float* v) {
   __syncwarp();
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "f"(v[0]), "f"(v[1]),
@@ -200,6 +213,9 @@ __host__ __device__ constexpr uint32_t instruction(uint32_t format, uint32_t n, 
   return (1u << 4) | (format << 7) | (format << 10) | (mn_major ? (1u << 15) | (1u << 16) : 0u) | ((n >> 3) << 17) |
          ((128u >> 4) << 24);
 }
+
+// The same with B alone MN-major.
+__host__ __device__ constexpr uint32_t instruction_b_mn(uint32_t format, uint32_t n) { return instruction(format, n, false) | (1u << 16); }
 
 // The same value in every lane, and known to be: it can live in a uniform register.
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(~0u, x, 0); }
@@ -286,6 +302,32 @@ __device__ __forceinline__ void mma16_tokens(uint32_t d, uint32_t a, uint32_t b,
       " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
       " add.u32 x, %1, 896; add.u32 y, %2, 896; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
       " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+      "}" ::"r"(d), "r"(a), "r"(b), "r"(kOperandHigh), "r"(inst), "r"(static_cast<uint32_t>(add))
+      : "memory");
+}
+
+// A in tensor memory, 128 rows by 128 columns of two bytes (64 of its columns); B MN-major, 128 rows: eight steps of 16.
+__device__ __forceinline__ void mma16_held(uint32_t d, uint32_t a, uint32_t b, uint32_t inst, bool add) {
+  d = uniform(d), a = uniform(a), b = uniform(b);
+  asm volatile(
+      "{\n .reg .pred p, q, t;\n .reg .b32 w, y;\n .reg .b64 b;\n"
+      " setp.ne.u32 p, %5, 0;\n setp.eq.u32 t, 0, 0;\n elect.sync _|q, 0xffffffff;\n"
+      " add.u32 w, %1, 0; add.u32 y, %2, 0; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [w], b, %4, p;\n"
+      " add.u32 w, %1, 8; add.u32 y, %2, 128; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [w], b, %4, t;\n"
+      " add.u32 w, %1, 16; add.u32 y, %2, 256; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [w], b, %4, t;\n"
+      " add.u32 w, %1, 24; add.u32 y, %2, 384; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [w], b, %4, t;\n"
+      " add.u32 w, %1, 32; add.u32 y, %2, 512; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [w], b, %4, t;\n"
+      " add.u32 w, %1, 40; add.u32 y, %2, 640; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [w], b, %4, t;\n"
+      " add.u32 w, %1, 48; add.u32 y, %2, 768; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [w], b, %4, t;\n"
+      " add.u32 w, %1, 56; add.u32 y, %2, 896; mov.b64 b, {y, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [w], b, %4, t;\n"
       "}" ::"r"(d), "r"(a), "r"(b), "r"(kOperandHigh), "r"(inst), "r"(static_cast<uint32_t>(add))
       : "memory");
 }

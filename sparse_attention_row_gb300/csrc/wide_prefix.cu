@@ -1,0 +1,683 @@
+// Attention over a prefix that many columns share (topk_shared_attention), joined with what rows see behind it.
+//
+// A unit is a run of rows that share a prefix and one key-value head: up to 256 columns (row, head), as two halves of 128.
+// Unlike in paged_attention.cu, whose columns are few, the columns are the long side of both products, M = 128:
+//   S [128 columns x 128 tokens]  = Q [128 x dk] . K^T
+//   O [128 columns x dv]         += P [128 x 128 tokens] . V
+// so that both run at the tensor core's full rate (N = 128: 64 cycles for 16 of the inner dimension), and a column's
+// scores lie in one thread: its maximum and sum need no exchange. P goes back into the tensor memory that its scores stood
+// in, and is the second product's A operand there. The two halves take turns: while the softmax of one is at work, the other's
+// products run. Tensor memory holds S and O of both: all of its 512 columns.
+//
+// Order of the products: for each tile P_a V, Q_a K' of the next tile, P_b V, Q_b K'. A half's next scores are written over its
+// probabilities; the tensor core takes products in the order in which one thread has issued them.
+//
+// Split: as in paged_attention.cu the units' tiles of 128 tokens, in order, are dealt in equal runs to the CTAs, one on
+// each SM; parts of units go through the workspace and a second kernel.
+//
+// Roles (13 warps): 4 softmax warps to each half, a thread to a column; 4 copy keys and values (and the queries of
+// later units) with 16-byte asynchronous copies, two places each; one issues the products.
+//
+// A column's maximum is taken from a unit's first tile; later the probabilities are taken with the maximum in use, and where one
+// comes out above 2^8, that is moved and O scaled (a warp at a time, for its own 32 columns). Statistics and O are in fp32; P
+// is rounded to the input type for the second product (fp16: scaled by 2^7 first).
+#include <cfloat>
+
+#include "attention_forms.cuh"
+#include "attention_parts.cuh"
+#include "paged.cuh"
+#include "token_copies.cuh"
+#include "umma.cuh"
+
+namespace ltk {
+namespace paged {
+namespace {
+
+using namespace ltk::umma;
+
+constexpr int kTile = 128;           // tokens
+constexpr int kChunk = kTile * 128;  // bytes of 64 dims
+constexpr int kPiece = 2 * kChunk;   // of a tile's keys or values: up to 128 dims
+constexpr int kHalf = 128;           // columns
+constexpr int kCols = 2 * kHalf;
+constexpr int kSoftmaxWarps = 8, kCopyWarps = 4, kCopyThreads = kCopyWarps * 32;
+constexpr int kMmaWarp = kSoftmaxWarps + kCopyWarps;
+constexpr int kThreads = (kMmaWarp + 1) * 32;
+constexpr int kSeenSlots = 4;  // tiles that the copies can be ahead of the softmax, and one
+constexpr int kMaxDim = 128;
+static_assert(kCols == kWideCols);
+
+struct Params {
+  topk_attention_args a;
+  Rows R;
+  FormArgs f;
+  int32_t group;   // heads a key-value head
+  int32_t v_cols;  // dv, rounded up to 16
+  int32_t slices;
+  float scale2;    // scale * log2(e)
+  float4* part;    // [slices][2][v_cols / 4][kCols]
+  float2* stat;    // [slices][2][kCols]: maximum (in powers of two) and sum
+  float* tail;     // [slices][2][kCols]: the logarithm of the sum behind the prefix
+  Join* join;      // [slices]
+};
+
+struct Smem {
+  uint32_t seen[kSeenSlots][kCopyWarps];  // tokens of a tile that are there
+  uint64_t key_full[2], key_empty[2], value_full[2], value_empty[2];
+  uint64_t seen_full[2][kSeenSlots];  // for each half, by the tiles that it takes part in
+  uint64_t q_first, q_full, q_empty, s_full[2], p_full[2], o_done[2], all_done;
+  int64_t scan[kThreads / 32];
+  int64_t start_group, start_at, tiles, run_begin, run_end;
+  uint32_t tmem, gave_up;
+};
+
+// A slice's run of tiles, walked segment by segment (a segment: the tiles of one unit in the run).
+struct Walk {
+  int64_t group, left;     // tiles of the run from here on
+  int kv_head, at, tiles;  // the unit, the segment's first tile, the unit's tiles
+  int count;               // tiles of the segment
+  __device__ void size() { count = static_cast<int>(min(static_cast<int64_t>(tiles - at), left)); }
+};
+
+__device__ __forceinline__ int run_tiles(const Params& p, int64_t g) { return (p.f.runs[g].length + kTile - 1) / kTile; }
+
+__device__ __forceinline__ void next_segment(const Params& p, Walk& w) {
+  w.left -= w.count;
+  w.at = 0;
+  if (++w.kv_head == p.a.kv_heads) {
+    w.kv_head = 0;
+    ++w.group;
+    if (w.left > 0) w.tiles = run_tiles(p, w.group);
+  }
+  w.size();
+}
+
+// A unit's queries into their K-major tiles, a half after the other; zeros past its columns and past dk.
+__device__ __noinline__ void copy_queries(const Params& p, uint32_t q_at, int64_t row0, int kv_head, int cols, int me, int threads) {
+  const int piece = me & 7;
+  const int halves = cols > kHalf ? 2 : 1, chunks = (p.a.dk + 63) / 64;
+#pragma unroll 1
+  for (int n = me >> 3; n < halves * kHalf; n += threads >> 3) {
+    const int j = n / p.group, row = n & (kHalf - 1);
+    const uint16_t* q = static_cast<const uint16_t*>(p.a.q);
+    const bool real = n < cols;
+    if (real) q += (row0 + j) * p.a.q_row_stride + static_cast<int64_t>(kv_head * p.group + n - j * p.group) * p.a.q_head_stride;
+    const uint32_t dst = q_at + (n / kHalf) * kPiece + row * 128 + ((piece ^ (row & 7)) << 4);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      if (c >= chunks) break;
+      const int dim = c * 64 + piece * 8;
+      const bool in = real && dim < p.a.dk;
+      copy16(dst + c * kChunk, in ? q + dim : static_cast<const uint16_t*>(p.a.q), in ? 16 : 0);
+    }
+  }
+}
+
+// S = Q K^T of a half: steps of 16 dims.
+__device__ __forceinline__ void multiply_keys(uint32_t d, uint32_t q, uint32_t k, int dk, uint32_t inst) {
+  if (dk == 128) {
+    mma16_pair(d, operand(q, 16), kChunk >> 4, operand(k, 16), kChunk >> 4, inst, false);
+    return;
+  }
+  bool add = false;
+  int left = dk;
+#pragma unroll 1
+  for (; left >= 64; left -= 64, q += kChunk, k += kChunk, add = true) mma16_chunk(d, operand(q, 16), operand(k, 16), inst, add);
+#pragma unroll 1
+  for (; left > 0; left -= 16, q += 32, k += 32, add = true) mma16_step(d, operand(q, 16), operand(k, 16), inst, add);
+}
+
+__device__ __forceinline__ uint64_t two(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 apart(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// The larger of two pairs of values of the input type, none of them negative.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (kBf16)
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+template <bool kBf16>
+__device__ __forceinline__ float2 unpack2(uint32_t x) {
+  if constexpr (kBf16) return __bfloat1622float2(reinterpret_cast<const __nv_bfloat162&>(x));
+  else return __half22float2(reinterpret_cast<const __half2&>(x));
+}
+
+// A tile's probabilities of a column, packed; their sum in `sum`, and whether one is larger than `most`.
+template <bool kBf16>
+__device__ __forceinline__ bool probabilities(uint32_t s_at, float scale2, float in_use, const uint32_t* seen, float most, uint32_t (&out)[kTile / 2],
+                                              float* sum) {
+  const bool all = (seen[0] & seen[1] & seen[2] & seen[3]) == ~0u;
+  const uint64_t scale = two(scale2, scale2), base = two(-in_use, -in_use);
+  uint64_t l = 0;
+  uint32_t top = 0;
+#pragma unroll
+  for (int c = 0; c < kTile; c += 32) {
+    float s[32];
+    tmem_load(s_at + c, s);
+    if (!all) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (!(seen[c / 32] >> i & 1)) s[i] = -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const float2 x = apart(fma2(two(s[i], s[i + 1]), scale, base));
+      const float y = exp2_fast(x.x), z = exp2_fast(x.y);
+      l = add2(l, two(y, z));
+      out[(c + i) / 2] = pack2<kBf16>(y, z);
+      top = larger<kBf16>(top, out[(c + i) / 2]);
+    }
+  }
+  const float2 both = apart(l), tops = unpack2<kBf16>(top);
+  *sum = both.x + both.y;
+  return fmaxf(tops.x, tops.y) > most;
+}
+
+template <bool kBf16>
+__global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_constant__ Params p) {
+  extern __shared__ __align__(1024) uint8_t raw[];
+  const uint32_t q_at = (smem_addr(raw) + 1023) & ~1023u, key_at = q_at + 2 * kPiece, value_at = key_at + 2 * kPiece;
+  Smem& sm = *reinterpret_cast<Smem*>(raw + (value_at + 2 * kPiece - smem_addr(raw)));
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, slice = blockIdx.x;
+  const Guard guard{&sm.gave_up, p.R.status};
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&sm.key_full[i]), kCopyThreads);
+      mbar_init(smem_addr(&sm.key_empty[i]), 1);
+      mbar_init(smem_addr(&sm.value_full[i]), kCopyThreads);
+      mbar_init(smem_addr(&sm.value_empty[i]), 1);
+      for (int j = 0; j < kSeenSlots; ++j) mbar_init(smem_addr(&sm.seen_full[i][j]), kCopyWarps);
+      mbar_init(smem_addr(&sm.s_full[i]), 1);
+      mbar_init(smem_addr(&sm.p_full[i]), kSoftmaxWarps / 2);
+      mbar_init(smem_addr(&sm.o_done[i]), 1);
+    }
+    mbar_init(smem_addr(&sm.q_first), kSoftmaxWarps * 32);
+    mbar_init(smem_addr(&sm.q_full), kCopyThreads);
+    mbar_init(smem_addr(&sm.q_empty), 1);
+    mbar_init(smem_addr(&sm.all_done), 1);
+    sm.gave_up = 0;
+    fence_async();
+  }
+  if (warp == kMmaWarp) tmem_alloc(smem_addr(&sm.tmem), 512);
+  dependent_wait();
+  dependent_launch();
+
+  // where this slice's run begins
+  {
+    const int64_t groups = *p.f.run_count, per = (groups + kThreads - 1) / kThreads;
+    const int64_t g0 = min(per * tid, groups), g1 = min(g0 + per, groups);
+    int64_t mine = 0;
+    for (int64_t g = g0; g < g1; ++g) mine += run_tiles(p, g);
+    int64_t pre = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t x = __shfl_up_sync(~0u, pre, d);
+      if (lane >= d) pre += x;
+    }
+    if (lane == 31) sm.scan[warp] = pre;
+    __syncthreads();
+    int64_t total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) pre += sm.scan[w];
+      total += sm.scan[w];
+    }
+    total *= p.a.kv_heads;
+    const int64_t begin = slice_begin(total, p.slices, slice);
+    int64_t at = (pre - mine) * p.a.kv_heads;
+    if (begin >= at && begin < pre * p.a.kv_heads) {
+      for (int64_t g = g0; g < g1; ++g) {
+        const int64_t n = static_cast<int64_t>(run_tiles(p, g)) * p.a.kv_heads;
+        if (begin < at + n) {
+          sm.start_group = g;
+          sm.start_at = begin - at;
+          break;
+        }
+        at += n;
+      }
+    }
+    if (tid == 0) {
+      sm.tiles = total;
+      sm.run_begin = begin;
+      sm.run_end = slice_begin(total, p.slices, slice + 1);
+    }
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = sm.tmem;
+  const int64_t run_begin = sm.run_begin;
+  Walk walk{};
+  walk.left = sm.run_end - run_begin;
+  if (walk.left > 0) {
+    walk.group = sm.start_group;
+    walk.tiles = run_tiles(p, walk.group);
+    int64_t at = sm.start_at;
+    for (; at >= walk.tiles; at -= walk.tiles) ++walk.kv_head;
+    walk.at = static_cast<int>(at);
+    walk.size();
+  }
+  const auto columns = [&]() { return p.f.runs[walk.group].rows * p.group; };
+
+  // the first segment's queries, by the warps that have nothing to do yet
+  if (walk.left > 0 && warp < kSoftmaxWarps) {
+    copy_queries(p, q_at, p.f.runs[walk.group].row0, walk.kv_head, columns(), tid, kSoftmaxWarps * 32);
+    copies_arrive(smem_addr(&sm.q_first));
+  }
+  if (warp >= kSoftmaxWarps && warp < kMmaWarp) {
+    // ---- copies -----------------------------------------------------------
+    const int me = tid - kSoftmaxWarps * 32;  // a thread's token of a tile
+    TokenCopies copies((warp - kSoftmaxWarps) * 32, lane);
+    uint32_t tile = 0, second = 0, segment = 0;  // second: tiles of which the second half takes part
+    for (; walk.left > 0; next_segment(p, walk), ++segment) {
+      const SharedRun run = p.f.runs[walk.group];
+      const int cols = run.rows * p.group;
+      const int32_t* pages = p.f.prefix_table + run.prefix * p.f.prefix_stride;
+      const auto place = [&](int t) { return t < walk.count ? (walk.at + t) * kTile + me : INT_MAX; };
+      const auto page_of = [&](int x) { return x < run.length ? pages[block_column(p.R, x)] : 0; };
+      int x = place(0), page = page_of(x);
+      asm volatile("" ::"r"(page) : "memory");  // here, before any copies are issued: a load waits behind those
+      if (segment > 0) {                        // the first one's are copied by the softmax warps
+        mbar_wait(smem_addr(&sm.q_empty), (segment & 1) ^ 1, guard);
+        copy_queries(p, q_at, run.row0, walk.kv_head, cols, me, kCopyThreads);
+        copies_arrive(smem_addr(&sm.q_full));
+      }
+      for (int t = 0; t < walk.count; ++t, ++tile) {
+        const bool seen = x < run.length && page >= 0 && page < p.R.num_blocks;
+        if (!seen && x < run.length) atomicOr(p.R.status, TOPK_DEV_BAD_BLOCK);
+        const uint32_t who = __ballot_sync(~0u, seen);
+        if (lane == 0) {
+          sm.seen[tile % kSeenSlots][warp - kSoftmaxWarps] = who;
+          mbar_arrive(smem_addr(&sm.seen_full[0][tile % kSeenSlots]));
+          if (cols > kHalf) mbar_arrive(smem_addr(&sm.seen_full[1][second % kSeenSlots]));
+        }
+        second += cols > kHalf;
+        const char *kp = static_cast<const char*>(p.a.k), *vp = static_cast<const char*>(p.a.v);
+        if (seen) {
+          const int in_page = x - block_column(p.R, x) * p.R.block_size;
+          kp += 2 * (static_cast<int64_t>(page) * p.a.k_block_stride + in_page * p.a.k_token_stride + walk.kv_head * p.a.k_head_stride);
+          vp += 2 * (static_cast<int64_t>(page) * p.a.v_block_stride + in_page * p.a.v_token_stride + walk.kv_head * p.a.v_head_stride);
+        }
+        x = place(t + 1);
+        page = page_of(x);
+        const uint32_t slot = tile & 1, phase = ((tile >> 1) & 1) ^ 1;
+        copies.aim(kp, seen, lane);
+        mbar_wait(smem_addr(&sm.key_empty[slot]), phase, guard);
+        copies.columns(key_at + slot * kPiece, kChunk, 0, p.a.dk * 2, p.a.k);
+        copies_arrive(smem_addr(&sm.key_full[slot]));
+        copies.aim(vp, seen, lane);
+        mbar_wait(smem_addr(&sm.value_empty[slot]), phase, guard);
+        copies.columns(value_at + slot * kPiece, kChunk, 0, p.a.dv * 2, p.a.v);
+        copies_arrive(smem_addr(&sm.value_full[slot]));
+      }
+    }
+    copies_wait_all();
+  } else if (warp == kMmaWarp) {
+    // ---- products -----------------------------------------------------------
+    constexpr uint32_t kKeys = instruction(kBf16 ? kBF16 : kF16, kTile, false);
+    const uint32_t values = instruction_b_mn(kBf16 ? kBF16 : kF16, p.v_cols);
+    uint32_t tile = 0, second = 0, segment = 0;
+    const auto scores = [&](int half, uint32_t t) {
+      multiply_keys(tmem + half * kTile, q_at + half * kPiece, key_at + (t & 1) * kPiece, p.a.dk, kKeys);
+      commit(smem_addr(&sm.s_full[half]));
+    };
+    const auto outputs = [&](int half, uint32_t t, bool add) {
+      mma16_held(tmem + kCols + half * kMaxDim, tmem + half * kTile, operand(value_at + (t & 1) * kPiece, kChunk), values, add);
+      commit(smem_addr(&sm.o_done[half]));
+    };
+    const auto keys_come = [&](uint32_t t) {
+      mbar_wait_warp(smem_addr(&sm.key_full[t & 1]), (t >> 1) & 1, guard);
+      fence_async();
+    };
+    for (; walk.left > 0; next_segment(p, walk), ++segment) {
+      const bool both = columns() > kHalf;
+      if (segment == 0)
+        mbar_wait_warp(smem_addr(&sm.q_first), 0, guard);
+      else
+        mbar_wait_warp(smem_addr(&sm.q_full), (segment & 1) ^ 1, guard);
+      keys_come(tile);
+      scores(0, tile);
+      if (both) scores(1, tile);
+      commit(smem_addr(&sm.key_empty[tile & 1]));
+#pragma unroll 1
+      for (int t = 0; t < walk.count; ++t, ++tile) {
+        const bool more = t + 1 < walk.count;
+        mbar_wait_warp(smem_addr(&sm.p_full[0]), tile & 1, guard);
+        fence_after();
+        mbar_wait_warp(smem_addr(&sm.value_full[tile & 1]), (tile >> 1) & 1, guard);
+        fence_async();
+        outputs(0, tile, t > 0);
+        if (more) {
+          keys_come(tile + 1);
+          scores(0, tile + 1);
+        }
+        if (both) {
+          mbar_wait_warp(smem_addr(&sm.p_full[1]), second & 1, guard);
+          fence_after();
+          outputs(1, tile, t > 0);
+          ++second;
+        }
+        commit(smem_addr(&sm.value_empty[tile & 1]));
+        if (more) {
+          if (both) scores(1, tile + 1);
+          commit(smem_addr(&sm.key_empty[(tile + 1) & 1]));
+        }
+      }
+      commit(smem_addr(&sm.q_empty));
+    }
+    commit(smem_addr(&sm.all_done));
+    mbar_wait_warp(smem_addr(&sm.all_done), 0, guard);
+  } else {
+    // ---- softmax and output ---------------------------------------------------
+    constexpr float kShift = kBf16 ? 0.f : 7.f;  // fp16: probabilities use the upper half of its range, at most 2^15
+    constexpr float kMostProbability = kBf16 ? 256.f : 32768.f;  // 2^(kMoveAbove + kShift)
+    const int half = warp >> 2, column = tid;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_at = tmem + lanes + half * kTile, o_at = tmem + lanes + kCols + half * kMaxDim;
+    uint32_t tile = 0, turn = 0;  // turn: tiles that this half took part in
+    bool first_segment = true;
+    for (; walk.left > 0; next_segment(p, walk)) {
+      const SharedRun run = p.f.runs[walk.group];
+      const int cols = run.rows * p.group;
+      if (half == 1 && cols <= kHalf) {
+        tile += walk.count;
+        first_segment = false;
+        continue;
+      }
+      const int j = column / p.group, head = walk.kv_head * p.group + column - j * p.group;
+      const bool real = column < cols;
+      // in powers of two: the maximum when it last moved, and what is taken off the scores; the lowest number until a finite
+      // one has come, so that any such score makes the maximum move
+      float m = -INFINITY, in_use = -FLT_MAX, l = 0.f;
+      for (int t = 0; t < walk.count; ++t, ++tile, ++turn) {
+        mbar_wait(smem_addr(&sm.seen_full[half][turn % kSeenSlots]), (turn / kSeenSlots) & 1, guard);
+        uint32_t seen[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) seen[i] = sm.seen[tile % kSeenSlots][i];
+        mbar_wait_warp(smem_addr(&sm.s_full[half]), turn & 1, guard);
+        fence_after();
+        uint32_t out[kTile / 2];
+        float sum = 0.f;
+        bool move_any = t == 0;
+        if (t > 0) move_any = __any_sync(~0u, probabilities<kBf16>(s_at, p.scale2, in_use, seen, kMostProbability, out, &sum));
+        if (move_any) {
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < kTile; c += 32) {
+            float s[32];
+            tmem_load(s_at + c, s);
+            const uint32_t who = c == 0 ? seen[0] : c == 32 ? seen[1] : c == 64 ? seen[2] : seen[3];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) top = fmaxf(top, who >> i & 1 ? s[i] : -INFINITY);
+          }
+          top *= p.scale2;
+          const bool move = top > m + kMoveAbove || (m == -INFINITY && top > m);
+          const bool rescale = __any_sync(~0u, move && m > -INFINITY);
+          const float factor = move && m > -INFINITY ? exp2_fast(m - top) : 1.f;
+          if (move) {
+            m = top;
+            in_use = m - kShift;
+          }
+          if (rescale) {
+            mbar_wait_warp(smem_addr(&sm.o_done[half]), (turn & 1) ^ 1, guard);  // the tile before has been added
+            fence_after();
+            l *= factor;
+#pragma unroll 1
+            for (int c = 0; c < p.v_cols; c += 16) {
+              float o[16];
+              tmem_load(o_at + c, o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] *= factor;
+              tmem_store8(o_at + c, o);
+              tmem_store8(o_at + c + 8, o + 8);
+            }
+            store_wait();
+          }
+          probabilities<kBf16>(s_at, p.scale2, in_use, seen, kMostProbability, out, &sum);
+        }
+        l += sum;
+        tmem_store32(s_at, out);
+        tmem_store32(s_at + 32, out + 32);
+        store_wait();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sm.p_full[half]));
+      }
+      // the whole unit, or a part of it
+      const bool whole = walk.count == walk.tiles;
+      const int64_t slot = static_cast<int64_t>(slice) * 2 + (first_segment ? 0 : 1);
+      float* lse = real ? p.a.lse + (run.row0 + j) * p.a.heads + head : nullptr;
+      const float tail = real ? *lse : -INFINITY;
+      const Weights both = weigh(l == 0.f ? -INFINITY : in_use + log2f(l), tail);
+      const float factor = l == 0.f ? 0.f : both.prefix / l;
+      if (whole) {
+        if (real) *lse = both.lse;
+      } else {
+        p.stat[slot * kCols + column] = make_float2(m == -INFINITY ? -INFINITY : in_use, l);
+        p.tail[slot * kCols + column] = tail;
+      }
+      mbar_wait_warp(smem_addr(&sm.o_done[half]), (turn & 1) ^ 1, guard);
+      fence_after();
+      uint16_t* out = static_cast<uint16_t*>(p.a.out) + (real ? (run.row0 + j) * p.a.out_row_stride + head * p.a.out_head_stride : 0);
+#pragma unroll 1
+      for (int c = 0; c < p.v_cols; c += 16) {
+        float o[16];
+        tmem_load(o_at + c, o);
+        if (l == 0.f) {  // nothing seen: zeros, whatever stands in O
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = 0.f;
+        }
+        if (!whole) {
+          float4* to = p.part + (slot * (p.v_cols / 4) + c / 4) * kCols + column;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) to[i * kCols] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        } else if (real) {
+#pragma unroll
+          for (int i = 0; i < 16; i += 8) {
+            if (c + i >= p.a.dv) break;
+            uint4* at = reinterpret_cast<uint4*>(out + c + i);
+            const uint4 x = *at;
+            const uint32_t old[4] = {x.x, x.y, x.z, x.w};
+            uint32_t y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = unpack2<kBf16>(old[e]);
+              y[e] = pack2<kBf16>(o[i + 2 * e] * factor + both.tail * f.x, o[i + 2 * e + 1] * factor + both.tail * f.y);
+            }
+            *at = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        }
+      }
+      fence_before();
+      if (first_segment && tid == 0) {  // a unit that began before this slice and ends in it
+        Join j{};
+        j.last = -1;
+        if (walk.at > 0 && walk.at + walk.count == walk.tiles) {
+          const int64_t unit_begin = run_begin - walk.at;
+          j.rowgroup = walk.group;
+          j.kv_head = walk.kv_head;
+          j.first = slice_of(sm.tiles, p.slices, unit_begin);
+          j.last = slice;
+          j.first_slot = slice_begin(sm.tiles, p.slices, j.first) == unit_begin ? 0 : 1;
+          j.tiles = sm.tiles;
+        }
+        p.join[slice] = j;
+      }
+      first_segment = false;
+    }
+    if (first_segment && tid == 0) {  // an empty run
+      Join j{};
+      j.last = -1;
+      p.join[slice] = j;
+    }
+  }
+  settle(guard);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == kMmaWarp) tmem_free(tmem, 512);
+}
+
+// Joins the parts of the units that fell into several slices: 32 columns of a unit a CTA, lanes along the columns, four values a
+// thread at a time.
+constexpr int kJoinCols = 32, kJoinWarps = 8, kMaxParts = 160;
+static_assert(kMaxParts <= kJoinWarps * 32);
+
+template <bool kBf16>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ Params p) {
+  __shared__ int32_t place[kMaxParts];  // of each part
+  __shared__ int32_t warp_parts[kJoinWarps];
+  __shared__ float weight[kMaxParts][kJoinCols];
+  __shared__ float4 sums[kJoinCols][kMaxDim / 4 + 1];
+  __shared__ float of_tail[kJoinCols];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int col0 = blockIdx.x % (kCols / kJoinCols) * kJoinCols, at_join = blockIdx.x / (kCols / kJoinCols);
+  dependent_wait();
+  dependent_launch();
+  const Join jn = p.join[at_join];
+  if (jn.last < 0) return;
+  const SharedRun run = p.f.runs[jn.rowgroup];
+  const int cols = run.rows * p.group, spanned = jn.last - jn.first + 1;
+  if (col0 >= cols) return;
+  int parts = 0;  // in order, without the slices that have no tiles
+  {
+    const int s = jn.first + tid;
+    const bool is = tid < spanned && slice_begin(jn.tiles, p.slices, s) != slice_begin(jn.tiles, p.slices, s + 1);
+    const unsigned who = __ballot_sync(~0u, is);
+    if (lane == 0) warp_parts[warp] = __popc(who);
+    __syncthreads();
+    int at = __popc(who & ((1u << lane) - 1));
+    for (int w = 0; w < kJoinWarps; ++w) {
+      if (w < warp) at += warp_parts[w];
+      parts += warp_parts[w];
+    }
+    if (is) place[at] = s * 2 + (tid == 0 ? jn.first_slot : 0);
+  }
+  __syncthreads();
+  // a column's maximum and sum, in the order of the parts; and each part's weight in the whole
+  if (warp == 0) {
+    const int col = col0 + lane;
+    float m = -INFINITY, sum = 0.f;
+    for (int i = 0; i < parts; ++i) {
+      const float2 st = p.stat[place[i] * kCols + col];
+      const float top = fmaxf(m, st.x), b = top == -INFINITY ? 0.f : top;
+      sum = sum * exp2f(m - b) + st.y * exp2f(st.x - b);
+      m = top;
+    }
+    const Weights both = weigh(sum == 0.f ? -INFINITY : m + log2f(sum), p.tail[place[0] * kCols + col]);
+    const float base = m == -INFINITY ? 0.f : m, factor = sum == 0.f ? 0.f : both.prefix / sum;
+    for (int i = 0; i < parts; ++i) weight[i][lane] = factor == 0.f ? 0.f : exp2f(p.stat[place[i] * kCols + col].x - base) * factor;
+    of_tail[lane] = both.tail;
+    if (col < cols) {
+      const int j = col / p.group;
+      p.a.lse[(run.row0 + j) * p.a.heads + jn.kv_head * p.group + col - j * p.group] = both.lse;
+    }
+  }
+  __syncthreads();
+  const int quads = p.v_cols / 4;
+  for (int d = warp; d < quads; d += kJoinWarps) {
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4* part = p.part + static_cast<int64_t>(d) * kCols + col0 + lane;
+    constexpr int kAtOnce = 8;
+    for (int i0 = 0; i0 < parts; i0 += kAtOnce) {
+      float4 y[kAtOnce];
+#pragma unroll
+      for (int a = 0; a < kAtOnce; ++a) y[a] = load_now(part + static_cast<int64_t>(place[min(i0 + a, parts - 1)]) * quads * kCols);
+#pragma unroll
+      for (int a = 0; a < kAtOnce; ++a) {
+        if (i0 + a >= parts) break;
+        const float w = weight[i0 + a][lane];
+        x.x += w * y[a].x;
+        x.y += w * y[a].y;
+        x.z += w * y[a].z;
+        x.w += w * y[a].w;
+      }
+    }
+    sums[lane][d] = x;
+  }
+  __syncthreads();
+  // along the values: four a thread
+  for (int e = tid; e < kJoinCols * quads; e += kJoinWarps * 32) {
+    const int n = e / quads, d = e - n * quads, col = col0 + n, j = col / p.group;
+    if (col >= cols || d * 4 >= p.a.dv) continue;
+    uint2* at = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.a.out) + (run.row0 + j) * p.a.out_row_stride +
+                                         static_cast<int64_t>(jn.kv_head * p.group + col - j * p.group) * p.a.out_head_stride + d * 4);
+    const uint2 old = *at;
+    const float2 f = unpack2<kBf16>(old.x), g = unpack2<kBf16>(old.y);
+    const float4 x = sums[n][d];
+    const float w = of_tail[n];
+    *at = make_uint2(pack2<kBf16>(x.x + w * f.x, x.y + w * f.y), pack2<kBf16>(x.z + w * g.x, x.w + w * g.y));
+  }
+}
+
+constexpr size_t kSmem = 6 * kPiece + sizeof(Smem) + 1024;
+static_assert(kSmem <= 232448, "keys, values and queries of 256 columns");
+
+size_t parts_of(int sms) { return static_cast<size_t>(sms) * 2; }
+
+template <bool kBf16>
+int run_wide(const Params& p, int device, cudaStream_t stream) {
+  static int granted[kMaxDevices];
+  int rc = allow_smem(prefix_kernel<kBf16>, kSmem, device, granted);
+  if (rc != TOPK_OK) return rc;
+  rc = launch(prefix_kernel<kBf16>, p, p.slices, kThreads, kSmem, stream);
+  if (rc != TOPK_OK) return rc;
+  return launch(join_kernel<kBf16>, p, static_cast<int64_t>(p.slices) * (kCols / kJoinCols), kJoinWarps * 32, 0, stream);
+}
+
+}  // namespace
+
+size_t wide_scratch(int sms) { return parts_of(sms) * kCols * (kMaxDim * sizeof(float) + sizeof(float2) + sizeof(float)) + static_cast<size_t>(sms) * sizeof(Join); }
+
+int attend_wide(const topk_attention_args& a, const FormArgs& f, void* scratch, void* stream) {
+  int device = 0;
+  topk_device_props props{};
+  if (cudaGetDevice(&device) != cudaSuccess || topk_query_device(device, &props) != TOPK_OK) {
+    cudaGetLastError();
+    return TOPK_ERR_CUDA;
+  }
+  Params p{};
+  p.a = a;
+  p.f = f;
+  p.R = make_rows(a.rows, INT32_MAX, a.workspace);
+  p.group = a.heads / a.kv_heads;
+  p.v_cols = (a.dv + 15) / 16 * 16;
+  p.scale2 = a.scale * 1.4426950408889634f;
+  const int64_t most = a.rows.num_rows * a.kv_heads * ((f.prefix_most + kTile - 1) / kTile);
+  int64_t slices = props.num_sms < kMaxParts ? props.num_sms : kMaxParts;
+  p.slices = static_cast<int32_t>(slices < most ? slices : most);
+  char* w = static_cast<char*>(scratch);
+  const size_t parts = parts_of(props.num_sms) * kCols;
+  p.part = reinterpret_cast<float4*>(w);
+  p.stat = reinterpret_cast<float2*>(w + parts * kMaxDim * sizeof(float));
+  p.tail = reinterpret_cast<float*>(p.stat + parts);
+  p.join = reinterpret_cast<Join*>(p.tail + parts);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return a.dtype == TOPK_DTYPE_BF16 ? run_wide<true>(p, device, s) : run_wide<false>(p, device, s);
+}
+
+}  // namespace paged
+}  // namespace ltk

@@ -257,3 +257,70 @@ def test_as_attention_of_every_request_by_itself(dec):
     alone, alone_lse = dec.attention(q, k, whole, ints(lengths), v_cache=v, return_lse=True)
     # both round their probabilities and results: four half steps of bf16 of the mean |v|, which is below 2 here
     assert (out.double() - alone.double()).abs().max() <= 4 * 2.0 ** -8 * 2 and (lse - alone_lse).abs().max() <= 1e-4
+
+
+# ---- runs of many columns -----------------------------------------------------------------------------------------
+
+WIDE = [(32, 8, 128, 128), (8, 1, 64, 64), (24, 2, 72, 40), (64, 4, 128, 64), (5, 1, 8, 8), (200, 1, 64, 128), (3, 3, 104, 120), (256, 1, 16, 96)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("heads, kv, dk, dv", WIDE)
+@pytest.mark.parametrize("rows", [17, 70, 129])
+def test_many_columns(dec, dtype, heads, kv, dk, dv, rows):
+    # one run, runs of which the last has a few columns, half a unit and whole ones; lengths that end inside a tile
+    prefix_of = [0] * (rows - 5) + [1] * 5
+    lengths = [(517 if p == 0 else 100) + (5 * i) % 33 for i, p in enumerate(prefix_of)]
+    case = make(20, [517, 100], prefix_of, lengths, list(range(rows)), heads, kv, dk, dv, False, dtype, 11)
+    check(dec, case, [517, 100], prefix_of, lengths, list(range(rows)), dv, 11)
+
+
+@pytest.mark.parametrize("each", [3, 40, 130])
+def test_many_columns_of_several_prefixes(dec, each):
+    # more units than CTAs with short prefixes; runs of few and many columns in turn, so that the second half joins in and rests
+    prefixes = [130, 16, 400, 128, 0, 256, 1000]
+    counts = [each, 1, each, 2, 3, 1, each]
+    prefix_of = [p for p, n in enumerate(counts) for _ in range(n)] + [-1] * 4
+    lengths = [max(prefixes[p], 1) + 3 * i if p >= 0 else 40 for i, p in enumerate(prefix_of)]
+    requests = list(range(len(lengths)))
+    case = make(21, prefixes, prefix_of, lengths, requests, 32, 4, 64, 64, False, torch.bfloat16, 16)
+    check(dec, case, prefixes, prefix_of, lengths, requests, 64, 16)
+
+
+def test_many_columns_with_scores_that_grow(dec):
+    # scores that rise along the prefix, so that maxima move often, for some of the columns
+    n = 40
+    prefix_of, lengths = [0] * n, [1500 + i for i in range(n)]
+    for dtype in (torch.float16, torch.bfloat16):
+        case = make(22, [1500], prefix_of, lengths, list(range(n)), 8, 1, 64, 64, False, dtype, 20)
+        q, k, v, hidden, whole, prefix_table = case
+        rise = torch.arange(1500).float() / 10
+        k[prefix_table[0].long(), :, 0, 0] = rise.view(75, 20).to(dtype)
+        q[::2, ::3, 0], q[1::2, ::3, 0] = 8.0, -8.0
+        check(dec, case, [1500], prefix_of, lengths, list(range(n)), 64, 20)
+        k[prefix_table[0, :40].long(), :, 0, 1] = -math.inf
+        q[:, :, 1] = q[:, :, 1].abs()
+        check(dec, case, [1500], prefix_of, lengths, list(range(n)), 64, 20)
+
+
+def test_many_columns_and_pages_outside_the_cache(dec):
+    n = 30
+    prefix_of, lengths = [0] * n, [300 + i for i in range(n)]
+    case = make(23, [300], prefix_of, lengths, list(range(n)), 16, 2, 64, 64, False, torch.float16, 10)
+    q, k, v, hidden, whole, prefix_table = case
+    bad = prefix_table.clone()
+    bad[0, 3], bad[0, 17], bad[0, 29] = -1, k.shape[0], 2 ** 31 - 1
+    out, lse = dec.shared_attention(q.cuda(), k.cuda(), hidden.cuda(), ints(lengths), ints(prefix_of), ints([300]), bad.cuda(), v_cache=v.cuda(), return_lse=True)
+    keep = torch.tensor([t for t in range(329) if t // 10 not in (3, 17, 29)], dtype=torch.int32)
+    want = pu.attention64(q, k, v, 64, whole, lengths, list(range(n)), 10, 64 ** -0.5, indices=keep.expand(n, -1))
+    pu.check_attention(out, lse, (want[0], want[1], want[2] * 2.1, want[3] + 1e-5), torch.float16)
+    assert dec.status() == sar.TOPK_DEV_BAD_BLOCK
+
+
+def test_many_columns_of_latent_and_wide_heads_and_drafted_tokens(dec):
+    for heads, kv, dk, dv, latent in [(16, 1, 576, 512, True), (16, 2, 256, 128, False), (8, 2, 128, 128, False), (16, 1, 128, 64, True)]:
+        prefix_of = [0] * 30
+        lengths = [b + j for b in range(400, 430) for j in range(3)]
+        requests = [r // 3 for r in range(90)]
+        case = make(24, [400], prefix_of, lengths, requests, heads, kv, dk, dv, latent, torch.float16, 16)
+        check(dec, case, [400], prefix_of, lengths, requests, dv, 16, next_n=3)
