@@ -4,16 +4,15 @@
 //
 // The sum over a group's heads comes first, so that a score is one product of dk elements whatever the group's size.
 //
-// Means. A unit is a page that got tokens. Its keys are a matrix, tokens by (head, dim); a thread sums 16 bytes of a
-// token's row over every so many tokens, eight loads at a time, and the threads of one column meet in shared memory, in
+// Means. The keys of a page are a matrix, tokens by (head, dim), and a unit is 512 bytes of its width; a thread sums 16 bytes of
+// a token's row over every fourth token, eight loads at a time, and the threads of one column meet in shared memory, in
 // a fixed order. Units are found as the map finds its tokens: every CTA sums the requests' pages up. Bound by HBM for
 // prompts, by latency for the page or so that a decode step touches of each request.
 //
-// Scores. A thread has one block of one head and up to 16 rows of a request: it reads the block's mean once, 16 bytes at
-// a time, and the rows' queries from shared memory, where all threads of a warp read the same words. So the
-// means, which are all there is to read for a few rows, stream from HBM (a warp's 32 rows of 2 dk bytes use every line
-// that they touch), and many rows of one request are bound by the fused multiply-adds. Consecutive threads have consecutive
-// blocks: scores are stored in whole lines.
+// Scores. A warp has 32 blocks of one head and up to eight rows of a request: eight lanes read a mean, 128 bytes at a time,
+// and multiply it with the rows' queries, whose sums over the group stand in shared memory. (A thread to each mean would read
+// the same bytes, but 16 of every line at a time: 52 us against LEAVE for 64 rows.) The means, which are all there
+// is to read for a few rows, stream from HBM; many rows of one request are bound by the fused multiply-adds.
 #include "paged.cuh"
 
 namespace ltk {
@@ -23,15 +22,26 @@ namespace {
 constexpr int kMaxDk = 576;
 
 template <bool kBf16>
+__device__ __forceinline__ float2 widen2(uint32_t x) {
+  if constexpr (kBf16)
+    return __bfloat1622float2(reinterpret_cast<const __nv_bfloat162&>(x));
+  else
+    return __half22float2(reinterpret_cast<const __half2&>(x));
+}
+
+// A load that stays where it is written, among others that are under way at the same time.
+__device__ __forceinline__ uint4 fetch(const uint16_t* at) {
+  uint4 v;
+  asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(at) : "memory");
+  return v;
+}
+
+template <bool kBf16>
 __device__ __forceinline__ void widen(const uint4& x, float (&v)[8]) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float2 f;
-    if constexpr (kBf16)
-      f = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162&>(w[i]));
-    else
-      f = __half22float2(reinterpret_cast<const __half2&>(w[i]));
+    const float2 f = widen2<kBf16>(w[i]);
     v[2 * i] = f.x;
     v[2 * i + 1] = f.y;
   }
@@ -50,13 +60,16 @@ __device__ __forceinline__ uint32_t narrow(float lo, float hi) {
 
 // ---- means ------------------------------------------------------------------
 
-constexpr int kMeanThreads = 256;
+constexpr int kMeanThreads = 128;
+constexpr int kMeanColumns = 32;  // of 16 bytes: a unit is so much of a page's width
+constexpr int kTeams = kMeanThreads / kMeanColumns;  // which take its tokens in turn
 constexpr int kSegment = 1024;  // requests whose pages are summed up at a time
 
 struct MeanParams {
   topk_block_means_args a;
   Rows R;           // for the division by block_size
   int32_t columns;  // of 16 bytes in a token's row of keys
+  int32_t widths;   // units of a page
 };
 
 // New pages of a request: the first one's column, and how many.
@@ -114,9 +127,11 @@ __global__ void __launch_bounds__(kMeanThreads) means_kernel(const __grid_consta
     }
     __syncthreads();
     // this CTA's first unit of the segment
-    const int64_t skipped = (before + gridDim.x - 1 - blockIdx.x) / gridDim.x * gridDim.x + blockIdx.x - before;
-    for (int64_t u64 = skipped; u64 < all; u64 += gridDim.x) {
-      const uint32_t u = static_cast<uint32_t>(u64);
+    const int64_t units = static_cast<int64_t>(all) * p.widths, done = before * p.widths;
+    const int64_t skipped = (done + gridDim.x - 1 - blockIdx.x) / gridDim.x * gridDim.x + blockIdx.x - done;
+    for (int64_t v = skipped; v < units; v += gridDim.x) {
+      const uint32_t u = static_cast<uint32_t>(v / p.widths);
+      const int c = static_cast<int>(v - static_cast<int64_t>(u) * p.widths) * kMeanColumns + lane;
       uint32_t j = 0;  // the last request whose start is at or before u
 #pragma unroll
       for (uint32_t step = kSegment / 2; step > 0; step >>= 1)
@@ -132,50 +147,41 @@ __global__ void __launch_bounds__(kMeanThreads) means_kernel(const __grid_consta
       }
       const int64_t left = total - static_cast<int64_t>(column) * a.block_size;
       const int held = static_cast<int>(left < a.block_size ? left : a.block_size);
-      for (int c0 = 0; c0 < p.columns; c0 += kMeanThreads) {
-        const int here = min(kMeanThreads, p.columns - c0), teams = kMeanThreads / here;
-        const int team = tid / here, c = c0 + tid - team * here;
-        const int per_head = a.dk / 8, head = c / per_head, d = (c - head * per_head) * 8;
-        float s[8] = {};
-        if (team < teams) {
-          const uint16_t* k = static_cast<const uint16_t*>(a.k) + page * a.k_block_stride + head * a.k_head_stride + d;
-          constexpr int kAtOnce = 8;
-          int t = team;
-          for (; t + (kAtOnce - 1) * teams < held; t += kAtOnce * teams) {
-            uint4 x[kAtOnce];
+      const int per_head = a.dk / 8, head = c / per_head, d = (c - head * per_head) * 8;
+      float s[8] = {};
+      if (c < p.columns) {
+        const uint16_t* k = static_cast<const uint16_t*>(a.k) + page * a.k_block_stride + head * a.k_head_stride + d;
+        constexpr int kAtOnce = 8;
+        for (int t = warp; t < held; t += kAtOnce * kTeams) {
+          uint4 x[kAtOnce];
 #pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) x[i] = *reinterpret_cast<const uint4*>(k + (t + i * teams) * a.k_token_stride);
+          for (int i = 0; i < kAtOnce; ++i) x[i] = fetch(k + static_cast<int64_t>(min(t + i * kTeams, held - 1)) * a.k_token_stride);
 #pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) {
-              float v[8];
-              widen<kBf16>(x[i], v);
+          for (int i = 0; i < kAtOnce; ++i) {
+            if (t + i * kTeams >= held) break;
+            float v8[8];
+            widen<kBf16>(x[i], v8);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) s[e] += v[e];
-            }
+            for (int e = 0; e < 8; ++e) s[e] += v8[e];
           }
-          for (; t < held; t += teams) {
-            float v[8];
-            widen<kBf16>(*reinterpret_cast<const uint4*>(k + t * a.k_token_stride), v);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s[e] += v[e];
-          }
-          part[tid][0] = make_float4(s[0], s[1], s[2], s[3]);
-          part[tid][1] = make_float4(s[4], s[5], s[6], s[7]);
         }
-        __syncthreads();
-        if (team == 0) {
-          for (int i = 1; i < teams; ++i) {
-            const float4 x = part[tid + i * here][0], y = part[tid + i * here][1];
-            s[0] += x.x, s[1] += x.y, s[2] += x.z, s[3] += x.w;
-            s[4] += y.x, s[5] += y.y, s[6] += y.z, s[7] += y.w;
-          }
-          const float n = static_cast<float>(held);
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.means) + page * a.mean_block_stride + head * a.mean_head_stride + d) =
-              make_uint4(narrow<kBf16>(s[0] / n, s[1] / n), narrow<kBf16>(s[2] / n, s[3] / n), narrow<kBf16>(s[4] / n, s[5] / n),
-                         narrow<kBf16>(s[6] / n, s[7] / n));
-        }
-        __syncthreads();  // the next column or page writes the parts again
       }
+      part[tid][0] = make_float4(s[0], s[1], s[2], s[3]);
+      part[tid][1] = make_float4(s[4], s[5], s[6], s[7]);
+      __syncthreads();
+      if (warp == 0 && c < p.columns) {
+#pragma unroll
+        for (int i = 1; i < kTeams; ++i) {
+          const float4 x = part[tid + i * kMeanColumns][0], y = part[tid + i * kMeanColumns][1];
+          s[0] += x.x, s[1] += x.y, s[2] += x.z, s[3] += x.w;
+          s[4] += y.x, s[5] += y.y, s[6] += y.z, s[7] += y.w;
+        }
+        const float n = static_cast<float>(held);
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.means) + page * a.mean_block_stride + head * a.mean_head_stride + d) =
+            make_uint4(narrow<kBf16>(s[0] / n, s[1] / n), narrow<kBf16>(s[2] / n, s[3] / n), narrow<kBf16>(s[4] / n, s[5] / n),
+                       narrow<kBf16>(s[6] / n, s[7] / n));
+      }
+      __syncthreads();  // the next unit writes the parts again
     }
     before += all;
     __syncthreads();  // the next segment writes the starts again
@@ -185,7 +191,10 @@ __global__ void __launch_bounds__(kMeanThreads) means_kernel(const __grid_consta
 
 // ---- scores -----------------------------------------------------------------
 
-constexpr int kScoreThreads = 128;  // blocks of a chunk
+constexpr int kScoreThreads = 256;
+constexpr int kScoreWarps = kScoreThreads / 32;
+constexpr int kTileRows = 8;
+constexpr int kQueryBytes = 48 * 1024;  // queries of a tile's rows and some of its heads
 
 struct ScoreParams {
   topk_block_scores_args a;
@@ -194,7 +203,9 @@ struct ScoreParams {
   int32_t tile_rows;      // rows of a tile: of one request where next_n says whose they are, else neighbours
   int32_t request_tiles;  // tiles of a request, 0: of all rows
   int64_t tiles;
-  int32_t splits;  // CTAs that share a tile's chunks
+  int32_t heads;    // of a window: those whose queries are held at a time
+  int32_t windows;  // of the heads
+  int32_t splits;   // CTAs that share a tile's blocks
 };
 
 __device__ __forceinline__ int seen_blocks(const ScoreParams& p, int tokens) {
@@ -202,13 +213,16 @@ __device__ __forceinline__ int seen_blocks(const ScoreParams& p, int tokens) {
 }
 
 template <int kRows, bool kBf16>
-__global__ void __launch_bounds__(kScoreThreads) scores_kernel(const __grid_constant__ ScoreParams p) {
-  extern __shared__ __align__(16) float q_sum[];  // [kRows][dk]
+__global__ void __launch_bounds__(kScoreThreads, 2) scores_kernel(const __grid_constant__ ScoreParams p) {
+  constexpr int kAtOnce = kRows > 2 ? 1 : 2;  // pieces of each mean
+  constexpr int kMeans = kRows > 2 ? 4 : 8;
+  extern __shared__ __align__(16) float q_sum[];  // [kRows][heads of the window][dk]
   __shared__ int32_t seen[kRows];
   const topk_block_scores_args& a = p.a;
-  const int tid = threadIdx.x;
-  const int split = blockIdx.x % p.splits, head = blockIdx.x / p.splits % a.kv_heads;
-  const int64_t tile = blockIdx.x / p.splits / a.kv_heads;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, sub = lane & 7, four = lane >> 3;
+  const int split = blockIdx.x % p.splits, window = blockIdx.x / p.splits % p.windows;
+  const int64_t tile = blockIdx.x / p.splits / p.windows;
+  const int head0 = window * p.heads, heads = min(p.heads, a.kv_heads - head0), pieces = a.dk / 8;
   dependent_wait();
   dependent_launch();
   int64_t row0, row_end;  // of the tile
@@ -230,17 +244,14 @@ __global__ void __launch_bounds__(kScoreThreads) scores_kernel(const __grid_cons
     if (tid < kRows) {
       const int n = tid < rows ? seen_tokens(p.R, p.R.lengths[row0 + tid], request) : 0;
       seen[tid] = seen_blocks(p, n);
-      if (tid < rows) {
-        if (split == 0) a.score_lens[(row0 + tid) * a.kv_heads + head] = seen[tid];
-        if (n > 0 && block_column(p.R, n - 1) >= a.max_columns) flags |= TOPK_DEV_LENGTH_CLAMPED;
-      }
+      if (tid < rows && n > 0 && block_column(p.R, n - 1) >= a.max_columns) flags |= TOPK_DEV_LENGTH_CLAMPED;
     }
-    for (int i = tid; i < kRows * (a.dk / 8); i += kScoreThreads) {
-      const int r = i / (a.dk / 8), d = (i - r * (a.dk / 8)) * 8;
+    for (int i = tid; i < kRows * heads * pieces; i += kScoreThreads) {
+      const int at = i / pieces, d = (i - at * pieces) * 8, r = at / heads, head = head0 + at - r * heads;
       float s[8] = {};
       if (r < rows) {
         const uint16_t* q = static_cast<const uint16_t*>(a.q) + (row0 + r) * a.q_row_stride + static_cast<int64_t>(head * p.group) * a.q_head_stride + d;
-#pragma unroll 4
+#pragma unroll 8
         for (int h = 0; h < p.group; ++h) {
           float v[8];
           widen<kBf16>(*reinterpret_cast<const uint4*>(q + h * a.q_head_stride), v);
@@ -248,7 +259,7 @@ __global__ void __launch_bounds__(kScoreThreads) scores_kernel(const __grid_cons
           for (int e = 0; e < 8; ++e) s[e] += v[e];
         }
       }
-      float4* to = reinterpret_cast<float4*>(q_sum + r * a.dk + d);
+      float4* to = reinterpret_cast<float4*>(q_sum + static_cast<int64_t>(at) * a.dk + d);
       to[0] = make_float4(s[0], s[1], s[2], s[3]);
       to[1] = make_float4(s[4], s[5], s[6], s[7]);
     }
@@ -256,33 +267,80 @@ __global__ void __launch_bounds__(kScoreThreads) scores_kernel(const __grid_cons
     int most = 0;
 #pragma unroll
     for (int r = 0; r < kRows; ++r) most = max(most, seen[r]);
-    for (int64_t chunk = split; chunk * kScoreThreads < most; chunk += p.splits) {
-      const int j = static_cast<int>(chunk) * kScoreThreads + tid;
-      if (j >= most) continue;
-      const int64_t page = p.R.block_table[request * p.R.table_stride + j];
+    if (split == 0)
+      for (int i = tid; i < rows * heads; i += kScoreThreads) a.score_lens[(row0 + i / heads) * a.kv_heads + head0 + i % heads] = seen[i / heads];
+    // a warp's turn: 32 blocks of a head; neighbouring warps have the same blocks' next heads, which lie side by side
+    const int turns = (most + 31) / 32 * heads;
+    for (int turn = split * kScoreWarps + warp; turn < turns; turn += p.splits * kScoreWarps) {
+      const int block0 = turn / heads * 32, at = turn - turn / heads * heads, head = head0 + at;
+      int64_t page = -1;
+      if (block0 + lane < most) page = p.R.block_table[request * p.R.table_stride + block0 + lane];
       const bool in = page >= 0 && page < p.R.num_blocks;
-      if (!in) flags |= TOPK_DEV_BAD_BLOCK;
-      const uint16_t* mean = static_cast<const uint16_t*>(a.means) + (in ? page : 0) * a.mean_block_stride + head * a.mean_head_stride;
-      float s[kRows] = {};
-      if (in) {
-#pragma unroll(kRows > 4 ? 4 : 8)
-        for (int d = 0; d < a.dk; d += 8) {
-          float v[8];
-          widen<kBf16>(*reinterpret_cast<const uint4*>(mean + d), v);
+      if (!in && block0 + lane < most) flags |= TOPK_DEV_BAD_BLOCK;
+      const unsigned there = __ballot_sync(~0u, in);
+      const uint16_t* mine = static_cast<const uint16_t*>(a.means) + (in ? page : 0) * a.mean_block_stride + head * a.mean_head_stride;
+      // eight lanes to a mean, four means at a time: block 4 c + four in step c
+      float s[8][kRows] = {};
+#pragma unroll 1
+      for (int piece0 = 0; piece0 < pieces; piece0 += 8 * kAtOnce) {
+        uint4 x[8][kAtOnce];
 #pragma unroll
-          for (int r = 0; r < kRows; ++r) {
-            const float4 x = *reinterpret_cast<const float4*>(q_sum + r * a.dk + d), y = *reinterpret_cast<const float4*>(q_sum + r * a.dk + d + 4);
-            s[r] = fmaf(v[0], x.x, fmaf(v[1], x.y, fmaf(v[2], x.z, fmaf(v[3], x.w, s[r]))));
-            s[r] = fmaf(v[4], y.x, fmaf(v[5], y.y, fmaf(v[6], y.z, fmaf(v[7], y.w, s[r]))));
+        for (int c = 0; c < 8; ++c) {
+          const int from = c * 4 + four;
+          const uint16_t* mean = reinterpret_cast<const uint16_t*>(__shfl_sync(~0u, reinterpret_cast<uint64_t>(mine), from));
+#pragma unroll
+          for (int i = 0; i < kAtOnce; ++i) {
+            const int piece = piece0 + i * 8 + sub;
+            x[c][i] = (there >> from & 1) && piece < pieces ? *reinterpret_cast<const uint4*>(mean + piece * 8) : make_uint4(0, 0, 0, 0);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+          const int piece = piece0 + i * 8 + sub;
+          if (piece >= pieces) break;
+          const float* q = q_sum + at * a.dk + piece * 8;
+          // four dims of some means at a time, for which every row's queries are read once
+#pragma unroll
+          for (int e = 0; e < 8; e += 4) {
+#pragma unroll
+            for (int c = 0; c < 8; c += kMeans) {
+              float2 lo[kMeans], hi[kMeans];
+#pragma unroll
+              for (int k = 0; k < kMeans; ++k) {
+                lo[k] = widen2<kBf16>(e == 0 ? x[c + k][i].x : x[c + k][i].z);
+                hi[k] = widen2<kBf16>(e == 0 ? x[c + k][i].y : x[c + k][i].w);
+              }
+#pragma unroll
+              for (int r = 0; r < kRows; ++r) {
+                const float4 y = *reinterpret_cast<const float4*>(q + r * heads * a.dk + e);
+#pragma unroll
+                for (int k = 0; k < kMeans; ++k) s[c + k][r] = fmaf(lo[k].x, y.x, fmaf(lo[k].y, y.y, fmaf(hi[k].x, y.z, fmaf(hi[k].y, y.w, s[c + k][r]))));
+              }
+            }
           }
         }
       }
+      // sums over the eight lanes, of which lane `sub` ends with step c = sub's: block 4 sub + four
+      const int j = block0 + 4 * sub + four;
+      const bool read = there >> (4 * sub + four) & 1;
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
+        float t[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) t[c] = s[c][r];
+#pragma unroll
+        for (int w = 4; w > 0; w >>= 1) {
+          const bool up = sub & w;
+#pragma unroll
+          for (int i = 0; i < w; ++i) {
+            const float keep = up ? t[i + w] : t[i], send = up ? t[i] : t[i + w];
+            t[i] = keep + __shfl_xor_sync(~0u, send, w);
+          }
+        }
         const int n = seen[r];
         if (r >= rows || j >= n) continue;
         const bool kept = j < a.sink_blocks || j >= n - a.recent_blocks;
-        a.scores[(row0 + r) * a.score_row_stride + head * a.score_head_stride + j] = !in ? -INFINITY : kept ? INFINITY : s[r];
+        a.scores[(row0 + r) * a.score_row_stride + head * a.score_head_stride + j] = !read ? -INFINITY : kept ? INFINITY : t[0];
       }
     }
     row0 += rows;
@@ -292,21 +350,30 @@ __global__ void __launch_bounds__(kScoreThreads) scores_kernel(const __grid_cons
 }
 
 template <int kRows, bool kBf16>
-int launch_scores(const ScoreParams& p, cudaStream_t stream) {
-  return launch(scores_kernel<kRows, kBf16>, p, p.tiles * p.a.kv_heads * p.splits, kScoreThreads, sizeof(float) * kRows * p.a.dk, stream);
+int launch_scores(ScoreParams& p, int sms, cudaStream_t stream) {
+  const topk_block_scores_args& a = p.a;
+  const int fit = kQueryBytes / (kRows * a.dk * static_cast<int>(sizeof(float)));
+  p.heads = fit < kScoreWarps ? (fit < a.kv_heads ? fit : a.kv_heads) : (kScoreWarps < a.kv_heads ? kScoreWarps : a.kv_heads);
+  p.windows = (a.kv_heads + p.heads - 1) / p.heads;
+  // CTAs for some rounds of the GPU, if there are blocks for as many: lengths are not known here, and those of a tile that reach
+  // past its blocks end at once.
+  const int64_t columns = a.rows.max_blocks < a.max_columns ? a.rows.max_blocks : a.max_columns;
+  const int64_t units = p.tiles * p.windows, turns = (columns + 31) / 32 * p.heads, most = (turns + kScoreWarps - 1) / kScoreWarps;
+  const int64_t wanted = (16ll * sms + units - 1) / units;
+  p.splits = static_cast<int32_t>(wanted < most ? wanted : most);
+  if (units * p.splits > INT32_MAX) return TOPK_ERR_UNSUPPORTED;
+  return launch(scores_kernel<kRows, kBf16>, static_cast<const ScoreParams&>(p), units * p.splits, kScoreThreads, sizeof(float) * kRows * p.heads * a.dk, stream);
 }
 
 template <bool kBf16>
-int run_scores(const ScoreParams& p, cudaStream_t stream) {
-  if (p.tile_rows <= 1) return launch_scores<1, kBf16>(p, stream);
-  if (p.tile_rows <= 2) return launch_scores<2, kBf16>(p, stream);
-  if (p.tile_rows <= 4) return launch_scores<4, kBf16>(p, stream);
-  if (p.tile_rows <= 8) return launch_scores<8, kBf16>(p, stream);
-  return launch_scores<16, kBf16>(p, stream);
+int run_scores(ScoreParams& p, int sms, cudaStream_t stream) {
+  if (p.tile_rows <= 1) return launch_scores<1, kBf16>(p, sms, stream);
+  if (p.tile_rows <= 2) return launch_scores<2, kBf16>(p, sms, stream);
+  if (p.tile_rows <= 4) return launch_scores<4, kBf16>(p, sms, stream);
+  return launch_scores<8, kBf16>(p, sms, stream);
 }
 
-constexpr int kTileRows = 16;
-static_assert(kTileRows * kMaxDk * sizeof(float) <= 48 * 1024, "queries of a tile");
+static_assert(kTileRows * kMaxDk * sizeof(float) <= kQueryBytes, "queries of a tile");
 
 bool two_bytes(int dtype) { return dtype == TOPK_DTYPE_F16 || dtype == TOPK_DTYPE_BF16; }
 
@@ -340,8 +407,9 @@ extern "C" int topk_block_means(const topk_block_means_args* args, void* stream)
   rows.max_blocks = a.max_blocks;
   p.R = make_rows(rows, INT32_MAX, a.workspace);
   p.columns = a.kv_heads * (a.dk / 8);
-  // Pages are not known here: as many CTAs as the SMs hold, each with every so manieth.
-  const int64_t grid = sms * 8;
+  p.widths = (p.columns + kMeanColumns - 1) / kMeanColumns;
+  // Pages are not known here: as many CTAs as the SMs hold, each with every so manieth unit.
+  const int64_t grid = sms * 10;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return a.dtype == TOPK_DTYPE_BF16 ? launch(means_kernel<true>, static_cast<const MeanParams&>(p), grid, kMeanThreads, 0, s)
                                     : launch(means_kernel<false>, static_cast<const MeanParams&>(p), grid, kMeanThreads, 0, s);
@@ -382,12 +450,6 @@ extern "C" int topk_block_scores(const topk_block_scores_args* args, void* strea
   } else {
     p.tiles = (rows + p.tile_rows - 1) / p.tile_rows;
   }
-  // CTAs for about four rounds of the GPU, if there are blocks for as many: lengths are not known here, and those of a tile
-  // that reach past its blocks end at once.
-  const int64_t columns = a.rows.max_blocks < a.max_columns ? a.rows.max_blocks : a.max_columns;
-  const int64_t chunks = (columns + kScoreThreads - 1) / kScoreThreads, wanted = (64ll * sms + p.tiles * a.kv_heads - 1) / (p.tiles * a.kv_heads);
-  p.splits = static_cast<int32_t>(wanted < chunks ? wanted : chunks);
-  if (p.tiles * a.kv_heads * p.splits > INT32_MAX) return TOPK_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return a.dtype == TOPK_DTYPE_BF16 ? run_scores<true>(p, s) : run_scores<false>(p, s);
+  return a.dtype == TOPK_DTYPE_BF16 ? run_scores<true>(p, sms, s) : run_scores<false>(p, sms, s);
 }

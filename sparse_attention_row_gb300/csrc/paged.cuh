@@ -134,7 +134,8 @@ constexpr int kMaxDevices = 64;
 template <typename Kernel>
 inline int allow_smem(Kernel* kernel, size_t smem, int device, int* granted) {
   if (device >= 0 && device < kMaxDevices && __atomic_load_n(&granted[device], __ATOMIC_ACQUIRE) >= static_cast<int>(smem)) return TOPK_OK;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) {
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess ||
+      cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) != cudaSuccess) {
     cudaGetLastError();
     return TOPK_ERR_CUDA;
   }

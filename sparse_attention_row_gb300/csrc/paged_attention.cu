@@ -79,6 +79,15 @@ constexpr int kPiece = 2 * kChunk;    // a ring slot: 128 dims
 // until the last one's have been multiplied.
 template <bool kLatent>
 constexpr int places = kLatent ? 1 : 2;
+// Places for the queries: with two, the copies need not wait for a unit's last scores before they go on to the next one. (Tails of 1
+// to 2048 tokens of 256 rows, 32 heads over 8, with their prefix of 32 K: 313 us, with one place 321.)
+template <bool kLatent>
+constexpr int most_query_places = !kLatent && (kForm == Form::kTail || kForm == Form::kBlocks) ? 2 : 1;
+// CTAs that an SM can hold: two, where lists of blocks make many short units of few columns, whose tokens come from L2. (1024
+// rows of one request, 32 heads over 4, 16 blocks of 64 tokens each: 219 us, with one CTA 250. A warp that looks tokens up for the
+// copies, or four more that copy the values, brought less, 235.)
+template <int N, bool kLatent>
+constexpr int ctas_per_sm = !kLatent && N == 16 && kForm == Form::kBlocks ? 2 : 1;
 constexpr int kSoftmaxWarps = 8, kCopyWarps = 4;
 constexpr int kCopyThreads = kCopyWarps * 32;
 constexpr int kScoreWarp = kSoftmaxWarps + kCopyWarps, kValueWarp = kScoreWarp + 1;
@@ -88,7 +97,7 @@ constexpr int kMaxSlots = 6;
 constexpr int kMaxBlockCols = 64;
 constexpr int kTeam = 128, kJoinDims = 32;  // threads of a team
 constexpr int kMaxTeams = 4;                // which take the parts in turn
-constexpr int kMaxParts = 256;  // slices of a launch at most
+constexpr int kMaxParts = 512;  // slices of a launch at most
 
 struct Params {
   topk_attention_args a;
@@ -110,6 +119,8 @@ struct Params {
   int64_t row_groups;
   uint32_t tmem_cols;
   uint32_t q_bytes;
+  int32_t query_places;
+  int32_t ctas;          // on an SM
   float scale2;          // scale * log2(e)
   float* part;           // [slices][2][blocks][v_pieces * 128][N]
   float2* stat;          // [slices][2][blocks][N]: maximum (in powers of two) and sum
@@ -138,7 +149,7 @@ struct Smem {  // behind the tiles
   // Each is waited for by one warp, one after another: a parity tells no phase from the second one before it, so no wait may
   // skip a phase, and copies of later pieces do not say that the arrivals of earlier ones have been counted.
   uint64_t key_come[kMaxSlots], value_come[kMaxSlots], empty[kMaxSlots];
-  uint64_t q_first, q_full, q_empty, rest_full, rest_empty, s_full[2], s_empty[2], p_full[2], o_done[2], token_full[kTokenSlots], all_done[2];
+  uint64_t q_first, q_full[2], q_empty[2], rest_full, rest_empty, s_full[2], s_empty[2], p_full[2], o_done[2], token_full[kTokenSlots], all_done[2];
   int64_t start_group, tiles, run_begin, run_end;
   int64_t start_at;
   uint32_t tmem;
@@ -354,11 +365,12 @@ static __device__ __noinline__ void protect(const Params& p, Smem<N>& sm, uint32
 }
 
 template <int N, bool kBf16, bool kLatent>
-__global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm<N, kLatent>) attention_kernel(const __grid_constant__ Params p) {
   constexpr int kPlaces = places<kLatent>;
   extern __shared__ __align__(1024) uint8_t raw[];
   const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
-  const uint32_t q_at = base, ring = q_at + p.q_bytes, rest = ring + p.slots * kPiece;
+  const int query_places = most_query_places<kLatent> == 2 ? p.query_places : 1;
+  const uint32_t q_at = base, ring = q_at + query_places * p.q_bytes, rest = ring + p.slots * kPiece;
   const uint32_t p_at = rest + (p.rest && !p.rest_is_p ? kChunk : 0);
   Smem<N>& sm = *reinterpret_cast<Smem<N>*>(raw + (p_at + kPlaces * kChunk - smem_addr(raw)));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -372,8 +384,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       mbar_init(smem_addr(&sm.empty[i]), 1);
     }
     mbar_init(smem_addr(&sm.q_first), kSoftmaxWarps * 32);
-    mbar_init(smem_addr(&sm.q_full), kCopyThreads);
-    mbar_init(smem_addr(&sm.q_empty), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&sm.q_full[i]), kCopyThreads);
+      mbar_init(smem_addr(&sm.q_empty[i]), 1);
+    }
     mbar_init(smem_addr(&sm.rest_full), kCopyThreads);
     mbar_init(smem_addr(&sm.rest_empty), 1);
     for (int i = 0; i < 2; ++i) {
@@ -531,9 +545,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       int at_block = table_entry(at_token);
       asm volatile("" ::"r"(at_block) : "memory");  // here, before any copies are issued: a load waits behind those
       if (segment > 0) {  // the first one's are copied by the softmax warps
-        mbar_wait(smem_addr(&sm.q_empty), (segment & 1) ^ 1, guard);
-        copy_queries<N>(p, q_at, row0, walk.kv_head, block, block_columns(), me, kCopyThreads);
-        copies_arrive(smem_addr(&sm.q_full));
+        // what stood in the place before: the last segment's or, of two places, the one's before
+        const uint32_t q = query_places == 2 ? segment & 1 : 0;
+        if (query_places == 1 || segment > 1) mbar_wait(smem_addr(&sm.q_empty[q]), ((query_places == 2 ? segment >> 1 : segment) & 1) ^ 1, guard);
+        copy_queries<N>(p, q_at + q * p.q_bytes, row0, walk.kv_head, block, block_columns(), me, kCopyThreads);
+        copies_arrive(smem_addr(&sm.q_full[q]));
       }
       for (int t = 0; t < walk.count; ++t, ++tile) {
         const bool seen = in_cache(at_token, at_block);
@@ -575,17 +591,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     Ring at, keys;
     uint32_t tile = 0, segment = 0;
     for (; walk.left > 0; walk.next(p), ++segment) {
+      const uint32_t q = query_places == 2 ? segment & 1 : 0, queries = q_at + q * p.q_bytes;
       if (segment == 0)
         mbar_wait_warp(smem_addr(&sm.q_first), 0, guard);
       else
-        mbar_wait_warp(smem_addr(&sm.q_full), (segment & 1) ^ 1, guard);
+        mbar_wait_warp(smem_addr(&sm.q_full[q]), query_places == 1 ? (segment & 1) ^ 1 : (segment >> 1 & 1) ^ (q ^ 1), guard);
       fence_async();
 #pragma unroll 1
       for (int t = 0; t < walk.count; ++t, ++tile) {
         const uint32_t b = tile & 1, d = tmem + s_cols + b * N;
         // the keys' last dims where they fill no piece
         const auto last_dims = [&](bool add) {
-          uint32_t k_at, q_piece = q_at + whole_pieces * 2 * (N * 128);
+          uint32_t k_at, q_piece = queries + whole_pieces * 2 * (N * 128);
           if (kLatent && p.rest) {
             k_at = rest;
             mbar_wait_warp(smem_addr(&sm.rest_full), tile & 1, guard);
@@ -611,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         mbar_wait_warp(smem_addr(&sm.s_empty[b]), ((tile >> 1) & 1) ^ 1, guard);
         fence_after();
         if (rest_first) last_dims(false);
-        uint32_t q_piece = q_at;
+        uint32_t q_piece = queries;
 #pragma unroll 1
         for (int u = 0; u < whole_pieces; ++u) {
           mbar_wait_warp(come + keys.slot * 8, keys.phase, guard);
@@ -627,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         if (!kLatent) at.step(p.slots, p.v_pieces);
         commit(smem_addr(&sm.s_full[b]));
       }
-      commit(smem_addr(&sm.q_empty));
+      commit(smem_addr(&sm.q_empty[q]));
     }
     commit(smem_addr(&sm.all_done[0]));
     mbar_wait_warp(smem_addr(&sm.all_done[0]), 0, guard);
@@ -1037,10 +1054,11 @@ constexpr size_t kJoinBytes = sizeof(Join);
 
 // CTAs of a launch: one on each SM, or one for each column block where there are more of those.
 int most_ctas(int sms) { return sms > 16 ? sms : 16; }
+constexpr int kMostCtasPerSm = 2;  // of which each has half the columns then
 
 size_t workspace_for(int sms) {
   const size_t slots = static_cast<size_t>(most_ctas(sms)) * 2;
-  return TOPK_PAGED_WORKSPACE_BYTES + (most_ctas(sms) * kJoinBytes + 255) / 256 * 256 + slots * kMaxBlockCols * (kMaxV * sizeof(float) + sizeof(float2));
+  return TOPK_PAGED_WORKSPACE_BYTES + (most_ctas(sms) * kMostCtasPerSm * kJoinBytes + 255) / 256 * 256 + slots * kMaxBlockCols * (kMaxV * sizeof(float) + sizeof(float2));
 }
 
 static_assert(sizeof(Smem<64>) + 1024 + 9 * 64 * 128 + 4 * kPiece + kChunk <= 232448, "a latent tile beside 64 columns");
@@ -1051,20 +1069,29 @@ int run(Params& p, int device, int smem_limit, bool joins, cudaStream_t stream) 
   p.q_bytes = p.k_chunks * N * 128;
   p.rest_is_p = 0;
   constexpr int kPBytes = places<kLatent> * kChunk;
+  const int most_smem = smem_limit;
+  // two CTAs on an SM, of which each keeps 1 KB for itself, if both have room for a tile
+  if (p.ctas == 2) {
+    if (smem_limit / 2 - 1024 - extra - static_cast<int>(p.q_bytes) - kPBytes >= (p.k_pieces + p.v_pieces) * kPiece)
+      smem_limit = smem_limit / 2 - 1024;
+  }
   int room = smem_limit - extra - static_cast<int>(p.q_bytes) - kPBytes;  // for the ring and, where it is not P, the rest
   if (p.rest) {
     // a buffer of its own for the rest lets the next tile's last keys come early, if the ring loses nothing by it
     p.rest_is_p = (room - kChunk) / kPiece < room / kPiece;
     if (!p.rest_is_p) room -= kChunk;
   }
+  // a second place for the queries, if four pieces or more remain, and a tile's values among them
+  p.query_places = most_query_places<kLatent> == 2 && (room - static_cast<int>(p.q_bytes)) / kPiece >= (p.ctas == 2 ? 2 : 4) ? 2 : 1;
+  if (p.query_places == 2) room -= static_cast<int>(p.q_bytes);
   p.slots = room / kPiece < kMaxSlots ? room / kPiece : kMaxSlots;
   const int k_ring = p.k_pieces - p.rest;
   if (p.slots < (p.latent && k_ring > 2 ? k_ring : 2) || (kForm != Form::kShared && !p.latent && p.pack > 1 && p.slots < p.v_pieces)) return TOPK_ERR_PLAN;
   p.tmem_cols = 32;
   while (p.tmem_cols < static_cast<uint32_t>((p.v_pieces + 2) * N)) p.tmem_cols *= 2;
-  const size_t smem = p.q_bytes + static_cast<size_t>(p.slots) * kPiece + (p.rest && !p.rest_is_p ? kChunk : 0) + kPBytes + extra;
+  const size_t smem = static_cast<size_t>(p.query_places) * p.q_bytes + static_cast<size_t>(p.slots) * kPiece + (p.rest && !p.rest_is_p ? kChunk : 0) + kPBytes + extra;
   static int granted[kMaxDevices];
-  int rc = allow_smem(attention_kernel<N, kBf16, kLatent>, smem_limit, device, granted);
+  int rc = allow_smem(attention_kernel<N, kBf16, kLatent>, most_smem, device, granted);
   if (rc != TOPK_OK) return rc;
   rc = launch(attention_kernel<N, kBf16, kLatent>, static_cast<const Params&>(p), static_cast<int64_t>(p.slices) * p.blocks, kThreads, smem, stream);
   if (rc != TOPK_OK || !joins) return rc;
@@ -1123,7 +1150,9 @@ int attend(const topk_attention_args& a, const FormArgs& f, void* stream) {
   const int64_t units = kForm == Form::kShared ? (a.rows.num_rows + p.pack - 1) / p.pack * a.kv_heads : p.row_groups * a.kv_heads;
   const int64_t longest = kForm == Form::kShared ? f.prefix_most : p.R.max_len;
   const int64_t most = (kForm == Form::kShared ? a.rows.num_rows * a.kv_heads : units) * (lists ? p.row_tiles : (longest + kTile - 1) / kTile);
-  int64_t slices = sms / p.blocks < 1 ? 1 : sms / p.blocks;
+  // two CTAs on an SM where a tile is two pieces and each has some units (64 rows of 64 heads over 8, 32 blocks: 94 us with one, 96 with two)
+  p.ctas = kForm == Form::kBlocks && !p.latent && p.block_cols <= 16 && p.k_pieces + p.v_pieces == 2 && units >= 8ll * sms ? 2 : 1;
+  int64_t slices = sms * p.ctas / p.blocks < 1 ? 1 : sms * p.ctas / p.blocks;
   if (slices > most) slices = most;
   if (slices > kMaxParts) slices = kMaxParts;
   p.slices = static_cast<int32_t>(slices);
@@ -1144,7 +1173,7 @@ int attend(const topk_attention_args& a, const FormArgs& f, void* stream) {
   p.joins = p.by_unit ? static_cast<int32_t>(units) : p.slices;
   char* w = static_cast<char*>(a.workspace) + TOPK_PAGED_WORKSPACE_BYTES;
   p.join = reinterpret_cast<Join*>(w);
-  w += (most_ctas(sms) * kJoinBytes + 255) / 256 * 256;
+  w += (most_ctas(sms) * kMostCtasPerSm * kJoinBytes + 255) / 256 * 256;
   p.stat = reinterpret_cast<float2*>(w);
   w += static_cast<size_t>(most_ctas(sms)) * 2 * kMaxBlockCols * sizeof(float2);
   p.part = reinterpret_cast<float*>(w);
