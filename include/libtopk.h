@@ -496,7 +496,8 @@ int topk_paged_attention(const topk_attention_args* args, void* stream);
 typedef struct {
   const int32_t* context_lens; /* [num_requests] */
   const int32_t* new_lens;     /* [num_requests] */
-  int64_t num_requests;        /* 0..2^31-1; 1024 rows of the table, or all of them, have fewer than 2^32 entries */
+  int64_t num_requests;        /* 0..2^31-1; 1024 rows of the table, or all where there are fewer, have fewer than
+                                * 2^31 entries times 512-byte columns of a token's keys */
   int block_size;              /* >= 1 */
   int dtype;                   /* TOPK_DTYPE_F16 or TOPK_DTYPE_BF16: of k and means */
   const int32_t* block_table;  /* [num_requests, max_blocks] */
@@ -653,7 +654,7 @@ int topk_page_free(const topk_page_free_args* args, void* stream);
  * neither the table nor the list names stay where they are. A free page that the table names as well is taken off
  * the list, one that is listed twice, or is none of the pool, likewise (TOPK_DEV_BAD_BLOCK; taken rises). Outputs may be the inputs themselves;
  * entries free_blocks_out[0 .. taken_out) are copied from free_blocks.
- * `scratch`: 12 * num_blocks bytes, 16-byte aligned; nothing in it outlives the call.
+ * `scratch`: 12 * num_blocks + 16 bytes, 16-byte aligned; nothing in it outlives the call.
  */
 typedef struct {
   topk_page_pool pool;

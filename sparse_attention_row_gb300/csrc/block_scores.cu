@@ -13,7 +13,10 @@
 // and multiply it with the rows' queries, whose sums over the group stand in shared memory. (A thread to each mean would read
 // the same bytes, but 16 of every line at a time: 52 us against LEAVE for 64 rows.) The means, which are all there
 // is to read for a few rows, stream from HBM; many rows of one request are bound by the fused multiply-adds.
+#include "attention_parts.cuh"
 #include "paged.cuh"
+#include "token_copies.cuh"
+#include "umma.cuh"
 
 namespace ltk {
 namespace paged {
@@ -69,7 +72,7 @@ struct MeanParams {
   topk_block_means_args a;
   Rows R;           // for the division by block_size
   int32_t columns;  // of 16 bytes in a token's row of keys
-  int32_t widths;   // units of a page
+  uint32_t widths;  // units of a page
 };
 
 // New pages of a request: the first one's column, and how many.
@@ -81,7 +84,7 @@ __device__ __forceinline__ int touched(const MeanParams& p, int64_t r, int32_t* 
 }
 
 template <bool kBf16>
-__global__ void __launch_bounds__(kMeanThreads) means_kernel(const __grid_constant__ MeanParams p) {
+__global__ void __launch_bounds__(kMeanThreads, 5) means_kernel(const __grid_constant__ MeanParams p) {
   __shared__ uint32_t start[kSegment + 1];
   __shared__ uint32_t warp_sum[kMeanThreads / 32];
   __shared__ float4 part[kMeanThreads][2];
@@ -91,9 +94,8 @@ __global__ void __launch_bounds__(kMeanThreads) means_kernel(const __grid_consta
   dependent_wait();
   dependent_launch();
   uint32_t flags = 0;
-  int64_t before = 0;  // pages of earlier segments
   for (int64_t r0 = 0; r0 < a.num_requests; r0 += kSegment) {
-    // the segment's new pages, and each request's first among them (32 bits do: they are entries of the table)
+    // the segment's new pages, and each request's first among them
     uint32_t mine[kPer], sum = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -126,12 +128,9 @@ __global__ void __launch_bounds__(kMeanThreads) means_kernel(const __grid_consta
       at += mine[i];
     }
     __syncthreads();
-    // this CTA's first unit of the segment
-    const int64_t units = static_cast<int64_t>(all) * p.widths, done = before * p.widths;
-    const int64_t skipped = (done + gridDim.x - 1 - blockIdx.x) / gridDim.x * gridDim.x + blockIdx.x - done;
-    for (int64_t v = skipped; v < units; v += gridDim.x) {
-      const uint32_t u = static_cast<uint32_t>(v / p.widths);
-      const int c = static_cast<int>(v - static_cast<int64_t>(u) * p.widths) * kMeanColumns + lane;
+    for (uint32_t v = blockIdx.x; v < all * p.widths; v += gridDim.x) {
+      const uint32_t u = v / p.widths;
+      const int c = static_cast<int>(v - u * p.widths) * kMeanColumns + lane;
       uint32_t j = 0;  // the last request whose start is at or before u
 #pragma unroll
       for (uint32_t step = kSegment / 2; step > 0; step >>= 1)
@@ -151,18 +150,22 @@ __global__ void __launch_bounds__(kMeanThreads) means_kernel(const __grid_consta
       float s[8] = {};
       if (c < p.columns) {
         const uint16_t* k = static_cast<const uint16_t*>(a.k) + page * a.k_block_stride + head * a.k_head_stride + d;
-        constexpr int kAtOnce = 8;
-        for (int t = warp; t < held; t += kAtOnce * kTeams) {
+        constexpr int kAtOnce = 16;
+        const int64_t step = kTeams * a.k_token_stride;
+        k += warp * a.k_token_stride;
+        for (int t = warp; t < held; t += kAtOnce * kTeams, k += kAtOnce * step) {
           uint4 x[kAtOnce];
+          const int here = (held - t + kTeams - 1) / kTeams;  // tokens left of this team's
 #pragma unroll
-          for (int i = 0; i < kAtOnce; ++i) x[i] = fetch(k + static_cast<int64_t>(min(t + i * kTeams, held - 1)) * a.k_token_stride);
+          for (int i = 0; i < kAtOnce; ++i) x[i] = fetch(i < here ? k + i * step : k);
 #pragma unroll
           for (int i = 0; i < kAtOnce; ++i) {
-            if (t + i * kTeams >= held) break;
             float v8[8];
             widen<kBf16>(x[i], v8);
+            if (i < here) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s[e] += v8[e];
+              for (int e = 0; e < 8; ++e) s[e] += v8[e];
+            }
           }
         }
       }
@@ -183,18 +186,12 @@ __global__ void __launch_bounds__(kMeanThreads) means_kernel(const __grid_consta
       }
       __syncthreads();  // the next unit writes the parts again
     }
-    before += all;
     __syncthreads();  // the next segment writes the starts again
   }
   if (flags) atomicOr(p.R.status, flags);
 }
 
 // ---- scores -----------------------------------------------------------------
-
-constexpr int kScoreThreads = 256;
-constexpr int kScoreWarps = kScoreThreads / 32;
-constexpr int kTileRows = 8;
-constexpr int kQueryBytes = 48 * 1024;  // queries of a tile's rows and some of its heads
 
 struct ScoreParams {
   topk_block_scores_args a;
@@ -205,175 +202,460 @@ struct ScoreParams {
   int64_t tiles;
   int32_t heads;    // of a window: those whose queries are held at a time
   int32_t windows;  // of the heads
-  int32_t splits;   // CTAs that share a tile's blocks
+  int32_t slices;
 };
 
 __device__ __forceinline__ int seen_blocks(const ScoreParams& p, int tokens) {
   return tokens == 0 ? 0 : static_cast<int>(min(static_cast<int64_t>(block_column(p.R, tokens - 1)) + 1, p.a.max_columns));
 }
 
+// The rows [row0, end) of a tile, and within them runs of rows of the same request: those from row0 on.
+struct TileRows {
+  int64_t row0, end;
+  __device__ __forceinline__ TileRows(const ScoreParams& p, int64_t tile) {
+    if (p.request_tiles > 0) {
+      const int64_t request = p.request_tiles == 1 ? tile : tile / p.request_tiles;
+      row0 = request * p.R.next_n + (tile - request * p.request_tiles) * p.tile_rows;
+      end = min(row0 + p.tile_rows, (request + 1) * p.R.next_n);
+    } else {
+      row0 = tile * p.tile_rows;
+      end = min(row0 + p.tile_rows, p.R.num_rows);
+    }
+  }
+  // Length of the run at row0, its request, and the blocks that its rows see at most.
+  __device__ __forceinline__ int run(const ScoreParams& p, int64_t* request, int* most) const {
+    *request = row_request(p.R, row0);
+    *most = 0;
+    if (p.request_tiles > 0) {  // all rows of the tile; loads that do not wait for one another
+      const int n = static_cast<int>(end - row0);
+      int32_t longest = 0;
+#pragma unroll 8
+      for (int i = 0; i < n; ++i) longest = max(longest, p.R.lengths[row0 + i]);
+      *most = seen_blocks(p, seen_tokens(p.R, longest, *request));
+      return n;
+    }
+    int n = 0;
+    for (; row0 + n < end; ++n) {
+      if (n > 0 && row_request(p.R, row0 + n) != *request) break;
+      *most = max(*most, seen_blocks(p, seen_tokens(p.R, p.R.lengths[row0 + n], *request)));
+    }
+    return n;
+  }
+  // Steps of `size` blocks for all runs.
+  __device__ __forceinline__ int64_t steps(const ScoreParams& p, int size) const {
+    TileRows t = *this;
+    int64_t sum = 0, request;
+    int most;
+    while (t.row0 < t.end) {
+      t.row0 += t.run(p, &request, &most);
+      sum += (most + size - 1) / size;
+    }
+    return sum;
+  }
+};
+
+// A CTA's share of all tiles' steps, which are dealt to the slices in equal numbers, in order.
+struct Share {
+  int64_t tile, skip, left;  // the first step: so many steps into that tile; and how many there are
+};
+
+template <int kThreads>
+__device__ __forceinline__ Share find_share(const ScoreParams& p, int slice, int size, int times) {
+  __shared__ int64_t sums[kThreads / 32];
+  __shared__ Share share;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t per = (p.tiles + kThreads - 1) / kThreads, t0 = min(per * tid, p.tiles), t1 = min(t0 + per, p.tiles);
+  int64_t mine = 0;
+  for (int64_t t = t0; t < t1; ++t) mine += TileRows(p, t).steps(p, size) * times;
+  int64_t pre = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t x = __shfl_up_sync(~0u, pre, d);
+    if (lane >= d) pre += x;
+  }
+  if (lane == 31) sums[warp] = pre;
+  if (tid == 0) share = Share{0, 0, 0};
+  __syncthreads();
+  int64_t total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) pre += sums[w];
+    total += sums[w];
+  }
+  const int64_t begin = slice_begin(total, p.slices, slice);
+  int64_t at = pre - mine;
+  if (begin >= at && begin < pre) {
+    for (int64_t t = t0; t < t1; ++t) {
+      const int64_t n = TileRows(p, t).steps(p, size) * times;
+      if (begin < at + n) {
+        share = Share{t, begin - at, slice_begin(total, p.slices, slice + 1) - begin};
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  return share;
+}
+
+// Every row's number of blocks, and what was wrong with the rows.
+__device__ __forceinline__ void write_lens(const ScoreParams& p) {
+  uint32_t bits = 0;
+  const int64_t all = p.R.num_rows * p.a.kv_heads;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < all; i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const int64_t row = i / p.a.kv_heads, request = row_request(p.R, row);
+    const int32_t given = p.R.lengths[row], n = seen_tokens(p.R, given, request);
+    if (request >= p.R.num_requests) bits |= TOPK_DEV_BAD_BLOCK;
+    if (request >= 0 && request < p.R.num_requests && (given < 0 || given > p.R.max_len)) bits |= TOPK_DEV_LENGTH_CLAMPED;
+    if (n > 0 && block_column(p.R, n - 1) >= p.a.max_columns) bits |= TOPK_DEV_LENGTH_CLAMPED;
+    p.a.score_lens[i] = seen_blocks(p, n);
+  }
+  if (bits) atomicOr(p.R.status, bits);
+}
+
+// What stands for a block's score: those that are always selected, and those that cannot be.
+__device__ __forceinline__ float final_score(const ScoreParams& p, float score, bool read, int block, int blocks) {
+  return !read ? -INFINITY : block < p.a.sink_blocks || block >= blocks - p.a.recent_blocks ? INFINITY : score;
+}
+
+// -- few rows
+
+constexpr int kFewThreads = 256;
+constexpr int kFewWarps = kFewThreads / 32;
+constexpr int kFewRows = 4;
+constexpr int kQueryBytes = 48 * 1024;  // queries of a tile's rows and some of its heads
+constexpr int kTurnBlocks = 32;
+
 template <int kRows, bool kBf16>
-__global__ void __launch_bounds__(kScoreThreads, 2) scores_kernel(const __grid_constant__ ScoreParams p) {
+__global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const __grid_constant__ ScoreParams p) {
   constexpr int kAtOnce = kRows > 2 ? 1 : 2;  // pieces of each mean
   constexpr int kMeans = kRows > 2 ? 4 : 8;
   extern __shared__ __align__(16) float q_sum[];  // [kRows][heads of the window][dk]
   __shared__ int32_t seen[kRows];
   const topk_block_scores_args& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, sub = lane & 7, four = lane >> 3;
-  const int split = blockIdx.x % p.splits, window = blockIdx.x / p.splits % p.windows;
-  const int64_t tile = blockIdx.x / p.splits / p.windows;
+  const int window = blockIdx.x % p.windows, slice = blockIdx.x / p.windows;
   const int head0 = window * p.heads, heads = min(p.heads, a.kv_heads - head0), pieces = a.dk / 8;
   dependent_wait();
   dependent_launch();
-  int64_t row0, row_end;  // of the tile
-  if (p.request_tiles > 0) {
-    const int64_t request = tile / p.request_tiles;
-    row0 = request * p.R.next_n + (tile - request * p.request_tiles) * p.tile_rows;
-    row_end = min(row0 + p.tile_rows, (request + 1) * p.R.next_n);
-  } else {
-    row0 = tile * p.tile_rows;
-    row_end = min(row0 + p.tile_rows, p.R.num_rows);
-  }
+  write_lens(p);
+  const Share share = find_share<kFewThreads>(p, slice, kTurnBlocks, 1);
   uint32_t flags = 0;
-  while (row0 < row_end) {
-    // the rows from here on that have the same request
-    const int64_t request = row_request(p.R, row0);
-    int rows = 1;
-    while (row0 + rows < row_end && row_request(p.R, row0 + rows) == request) ++rows;
-    __syncthreads();  // the last rows' queries have been read
-    if (tid < kRows) {
-      const int n = tid < rows ? seen_tokens(p.R, p.R.lengths[row0 + tid], request) : 0;
-      seen[tid] = seen_blocks(p, n);
-      if (tid < rows && n > 0 && block_column(p.R, n - 1) >= a.max_columns) flags |= TOPK_DEV_LENGTH_CLAMPED;
-    }
-    for (int i = tid; i < kRows * heads * pieces; i += kScoreThreads) {
-      const int at = i / pieces, d = (i - at * pieces) * 8, r = at / heads, head = head0 + at - r * heads;
-      float s[8] = {};
-      if (r < rows) {
-        const uint16_t* q = static_cast<const uint16_t*>(a.q) + (row0 + r) * a.q_row_stride + static_cast<int64_t>(head * p.group) * a.q_head_stride + d;
-#pragma unroll 8
-        for (int h = 0; h < p.group; ++h) {
-          float v[8];
-          widen<kBf16>(*reinterpret_cast<const uint4*>(q + h * a.q_head_stride), v);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) s[e] += v[e];
-        }
+  int64_t tile = share.tile, skip = share.skip, left = share.left;
+  for (; left > 0; ++tile) {
+    TileRows t(p, tile);
+    while (left > 0 && t.row0 < t.end) {
+      int64_t request;
+      int most;
+      const int64_t row0 = t.row0;
+      const int rows = t.run(p, &request, &most), groups = (most + kTurnBlocks - 1) / kTurnBlocks;
+      t.row0 += rows;
+      if (skip >= groups) {
+        skip -= groups;
+        continue;
       }
-      float4* to = reinterpret_cast<float4*>(q_sum + static_cast<int64_t>(at) * a.dk + d);
-      to[0] = make_float4(s[0], s[1], s[2], s[3]);
-      to[1] = make_float4(s[4], s[5], s[6], s[7]);
-    }
-    __syncthreads();
-    int most = 0;
+      const int first = static_cast<int>(skip), count = static_cast<int>(min(static_cast<int64_t>(groups - first), left));
+      skip = 0;
+      left -= count;
+      __syncthreads();  // the last rows' queries have been read
+      if (tid < kRows) seen[tid] = tid < rows ? seen_blocks(p, seen_tokens(p.R, p.R.lengths[row0 + tid], request)) : 0;
+      for (int i = tid; i < kRows * heads * pieces; i += kFewThreads) {
+        const int at = i / pieces, d = (i - at * pieces) * 8, r = at / heads, head = head0 + at - r * heads;
+        float s[8] = {};
+        if (r < rows) {
+          const uint16_t* q = static_cast<const uint16_t*>(a.q) + (row0 + r) * a.q_row_stride + static_cast<int64_t>(head * p.group) * a.q_head_stride + d;
+#pragma unroll 8
+          for (int h = 0; h < p.group; ++h) {
+            float v[8];
+            widen<kBf16>(*reinterpret_cast<const uint4*>(q + h * a.q_head_stride), v);
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) most = max(most, seen[r]);
-    if (split == 0)
-      for (int i = tid; i < rows * heads; i += kScoreThreads) a.score_lens[(row0 + i / heads) * a.kv_heads + head0 + i % heads] = seen[i / heads];
-    // a warp's turn: 32 blocks of a head; neighbouring warps have the same blocks' next heads, which lie side by side
-    const int turns = (most + 31) / 32 * heads;
-    for (int turn = split * kScoreWarps + warp; turn < turns; turn += p.splits * kScoreWarps) {
-      const int block0 = turn / heads * 32, at = turn - turn / heads * heads, head = head0 + at;
-      int64_t page = -1;
-      if (block0 + lane < most) page = p.R.block_table[request * p.R.table_stride + block0 + lane];
-      const bool in = page >= 0 && page < p.R.num_blocks;
-      if (!in && block0 + lane < most) flags |= TOPK_DEV_BAD_BLOCK;
-      const unsigned there = __ballot_sync(~0u, in);
-      const uint16_t* mine = static_cast<const uint16_t*>(a.means) + (in ? page : 0) * a.mean_block_stride + head * a.mean_head_stride;
-      // eight lanes to a mean, four means at a time: block 4 c + four in step c
-      float s[8][kRows] = {};
+            for (int e = 0; e < 8; ++e) s[e] += v[e];
+          }
+        }
+        float4* to = reinterpret_cast<float4*>(q_sum + static_cast<int64_t>(at) * a.dk + d);
+        to[0] = make_float4(s[0], s[1], s[2], s[3]);
+        to[1] = make_float4(s[4], s[5], s[6], s[7]);
+      }
+      // a warp's turn: 32 blocks of a head; neighbouring warps have the same blocks' next heads, which lie side by side
+      const int turns = count * heads;
+      const int32_t* table = p.R.block_table + request * p.R.table_stride;
+      const auto page_of = [&](int turn) {
+        const int j = (first + turn / heads) * kTurnBlocks + lane;
+        return turn < turns && j < most ? table[j] : -1;
+      };
+      int32_t next = page_of(warp);
+      __syncthreads();
+      for (int turn = warp; turn < turns; turn += kFewWarps) {
+        const int block0 = (first + turn / heads) * kTurnBlocks, at = turn - turn / heads * heads, head = head0 + at;
+        const int32_t page = next;
+        next = page_of(turn + kFewWarps);
+        const bool in = page >= 0 && page < p.R.num_blocks;
+        if (!in && block0 + lane < most) flags |= TOPK_DEV_BAD_BLOCK;
+        const unsigned there = __ballot_sync(~0u, in);
+        const uint16_t* mine = static_cast<const uint16_t*>(a.means) + static_cast<int64_t>(in ? page : 0) * a.mean_block_stride + head * a.mean_head_stride;
+        // eight lanes to a mean, four means at a time: block 4 c + four in step c
+        float s[8][kRows] = {};
 #pragma unroll 1
-      for (int piece0 = 0; piece0 < pieces; piece0 += 8 * kAtOnce) {
-        uint4 x[8][kAtOnce];
+        for (int piece0 = 0; piece0 < pieces; piece0 += 8 * kAtOnce) {
+          uint4 x[8][kAtOnce];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const int from = c * 4 + four;
-          const uint16_t* mean = reinterpret_cast<const uint16_t*>(__shfl_sync(~0u, reinterpret_cast<uint64_t>(mine), from));
+          for (int c = 0; c < 8; ++c) {
+            const int from = c * 4 + four;
+            const uint16_t* mean = reinterpret_cast<const uint16_t*>(__shfl_sync(~0u, reinterpret_cast<uint64_t>(mine), from));
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+              const int piece = piece0 + i * 8 + sub;
+              x[c][i] = (there >> from & 1) && piece < pieces ? *reinterpret_cast<const uint4*>(mean + piece * 8) : make_uint4(0, 0, 0, 0);
+            }
+          }
 #pragma unroll
           for (int i = 0; i < kAtOnce; ++i) {
             const int piece = piece0 + i * 8 + sub;
-            x[c][i] = (there >> from & 1) && piece < pieces ? *reinterpret_cast<const uint4*>(mean + piece * 8) : make_uint4(0, 0, 0, 0);
-          }
-        }
+            if (piece >= pieces) break;
+            const float* q = q_sum + at * a.dk + piece * 8;
+            // four dims of some means at a time, for which every row's queries are read once
 #pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-          const int piece = piece0 + i * 8 + sub;
-          if (piece >= pieces) break;
-          const float* q = q_sum + at * a.dk + piece * 8;
-          // four dims of some means at a time, for which every row's queries are read once
+            for (int e = 0; e < 8; e += 4) {
 #pragma unroll
-          for (int e = 0; e < 8; e += 4) {
+              for (int c = 0; c < 8; c += kMeans) {
+                float2 lo[kMeans], hi[kMeans];
 #pragma unroll
-            for (int c = 0; c < 8; c += kMeans) {
-              float2 lo[kMeans], hi[kMeans];
+                for (int k = 0; k < kMeans; ++k) {
+                  lo[k] = widen2<kBf16>(e == 0 ? x[c + k][i].x : x[c + k][i].z);
+                  hi[k] = widen2<kBf16>(e == 0 ? x[c + k][i].y : x[c + k][i].w);
+                }
 #pragma unroll
-              for (int k = 0; k < kMeans; ++k) {
-                lo[k] = widen2<kBf16>(e == 0 ? x[c + k][i].x : x[c + k][i].z);
-                hi[k] = widen2<kBf16>(e == 0 ? x[c + k][i].y : x[c + k][i].w);
-              }
+                for (int r = 0; r < kRows; ++r) {
+                  const float4 y = *reinterpret_cast<const float4*>(q + r * heads * a.dk + e);
 #pragma unroll
-              for (int r = 0; r < kRows; ++r) {
-                const float4 y = *reinterpret_cast<const float4*>(q + r * heads * a.dk + e);
-#pragma unroll
-                for (int k = 0; k < kMeans; ++k) s[c + k][r] = fmaf(lo[k].x, y.x, fmaf(lo[k].y, y.y, fmaf(hi[k].x, y.z, fmaf(hi[k].y, y.w, s[c + k][r]))));
+                  for (int k = 0; k < kMeans; ++k) s[c + k][r] = fmaf(lo[k].x, y.x, fmaf(lo[k].y, y.y, fmaf(hi[k].x, y.z, fmaf(hi[k].y, y.w, s[c + k][r]))));
+                }
               }
             }
           }
         }
-      }
-      // sums over the eight lanes, of which lane `sub` ends with step c = sub's: block 4 sub + four
-      const int j = block0 + 4 * sub + four;
-      const bool read = there >> (4 * sub + four) & 1;
+        // sums over the eight lanes, of which lane `sub` ends with step c = sub's: block 4 sub + four
+        const int j = block0 + 4 * sub + four;
+        const bool read = there >> (4 * sub + four) & 1;
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        float t[8];
+        for (int r = 0; r < kRows; ++r) {
+          float t8[8];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) t[c] = s[c][r];
+          for (int c = 0; c < 8; ++c) t8[c] = s[c][r];
 #pragma unroll
-        for (int w = 4; w > 0; w >>= 1) {
-          const bool up = sub & w;
+          for (int w = 4; w > 0; w >>= 1) {
+            const bool up = sub & w;
 #pragma unroll
-          for (int i = 0; i < w; ++i) {
-            const float keep = up ? t[i + w] : t[i], send = up ? t[i] : t[i + w];
-            t[i] = keep + __shfl_xor_sync(~0u, send, w);
+            for (int i = 0; i < w; ++i) {
+              const float keep = up ? t8[i + w] : t8[i], send = up ? t8[i] : t8[i + w];
+              t8[i] = keep + __shfl_xor_sync(~0u, send, w);
+            }
           }
+          const int n = seen[r];
+          if (r < rows && j < n) a.scores[(row0 + r) * a.score_row_stride + head * a.score_head_stride + j] = final_score(p, t8[0], read, j, n);
         }
-        const int n = seen[r];
-        if (r >= rows || j >= n) continue;
-        const bool kept = j < a.sink_blocks || j >= n - a.recent_blocks;
-        a.scores[(row0 + r) * a.score_row_stride + head * a.score_head_stride + j] = !read ? -INFINITY : kept ? INFINITY : t[0];
       }
     }
-    row0 += rows;
+    skip = 0;
   }
-  if (blockIdx.x == 0) report_rows(p.R, tid, kScoreThreads);
   if (flags) atomicOr(p.R.status, flags);
 }
 
 template <int kRows, bool kBf16>
-int launch_scores(ScoreParams& p, int sms, cudaStream_t stream) {
+int launch_few(ScoreParams& p, int sms, cudaStream_t stream) {
   const topk_block_scores_args& a = p.a;
   const int fit = kQueryBytes / (kRows * a.dk * static_cast<int>(sizeof(float)));
-  p.heads = fit < kScoreWarps ? (fit < a.kv_heads ? fit : a.kv_heads) : (kScoreWarps < a.kv_heads ? kScoreWarps : a.kv_heads);
+  p.heads = fit < kFewWarps ? (fit < a.kv_heads ? fit : a.kv_heads) : (kFewWarps < a.kv_heads ? kFewWarps : a.kv_heads);
   p.windows = (a.kv_heads + p.heads - 1) / p.heads;
-  // CTAs for some rounds of the GPU, if there are blocks for as many: lengths are not known here, and those of a tile that reach
-  // past its blocks end at once.
   const int64_t columns = a.rows.max_blocks < a.max_columns ? a.rows.max_blocks : a.max_columns;
-  const int64_t units = p.tiles * p.windows, turns = (columns + 31) / 32 * p.heads, most = (turns + kScoreWarps - 1) / kScoreWarps;
-  const int64_t wanted = (16ll * sms + units - 1) / units;
-  p.splits = static_cast<int32_t>(wanted < most ? wanted : most);
-  if (units * p.splits > INT32_MAX) return TOPK_ERR_UNSUPPORTED;
-  return launch(scores_kernel<kRows, kBf16>, static_cast<const ScoreParams&>(p), units * p.splits, kScoreThreads, sizeof(float) * kRows * p.heads * a.dk, stream);
+  const int64_t most = a.rows.num_rows * ((columns + kTurnBlocks - 1) / kTurnBlocks), ctas = (2ll * sms + p.windows - 1) / p.windows;
+  p.slices = static_cast<int32_t>(ctas < most ? ctas : most);
+  return launch(few_kernel<kRows, kBf16>, static_cast<const ScoreParams&>(p), static_cast<int64_t>(p.slices) * p.windows, kFewThreads, sizeof(float) * kRows * p.heads * a.dk, stream);
+}
+
+// -- many rows
+
+constexpr int kManyThreads = 128;
+constexpr int kManyDk = 256;
+constexpr int kTile = 128;           // blocks, and columns (row, head) at most
+constexpr int kChunk = kTile * 128;  // bytes of 64 dims
+
+// kGroup: heads of a group, 0: any number.
+template <int kGroup, bool kBf16>
+__global__ void __launch_bounds__(kManyThreads) many_kernel(const __grid_constant__ ScoreParams p) {
+  using namespace umma;
+  extern __shared__ __align__(1024) uint8_t raw[];
+  const topk_block_scores_args& a = p.a;
+  const int chunks = (a.dk + 63) / 64, pieces = (chunks + 1) / 2;
+  const uint32_t q_at = (smem_addr(raw) + 1023) & ~1023u, means_at = q_at + chunks * kChunk, step_bytes = chunks * kChunk;
+  __shared__ int32_t seen[kTile];
+  __shared__ uint64_t done;
+  __shared__ uint32_t tmem_at, gave_up;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = kGroup > 0 ? kGroup : p.group;
+  const Guard guard{&gave_up, p.R.status};
+  if (tid == 0) {
+    mbar_init(smem_addr(&done), 1);
+    gave_up = 0;
+    fence_async();
+  }
+  if (warp == 0) tmem_alloc(smem_addr(&tmem_at), kTile);
+  dependent_wait();
+  dependent_launch();
+  write_lens(p);
+  const Share share = find_share<kManyThreads>(p, blockIdx.x, kTile, a.kv_heads);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_at;
+  constexpr uint32_t kFormat = kBf16 ? kBF16 : kF16;
+  uint32_t flags = 0, products = 0, buffer = 0;
+  int64_t skip = share.skip, left = share.left;
+  TokenCopies copies(warp * 32, lane);
+  for (int64_t tile = share.tile; left > 0; ++tile) {
+    TileRows t(p, tile);
+    while (left > 0 && t.row0 < t.end) {
+      int64_t request;
+      int most;
+      const int64_t row0 = t.row0;
+      const int rows = t.run(p, &request, &most), steps = (most + kTile - 1) / kTile;
+      t.row0 += rows;
+      if (skip >= static_cast<int64_t>(steps) * a.kv_heads) {
+        skip -= static_cast<int64_t>(steps) * a.kv_heads;
+        continue;
+      }
+      if (tid < rows) seen[tid] = seen_blocks(p, seen_tokens(p.R, p.R.lengths[row0 + tid], request));
+      const int cols = rows * group;
+      const uint32_t inst = instruction(kFormat, (cols + 15) / 16 * 16, false);
+      const int32_t* table = p.R.block_table + request * p.R.table_stride;
+      for (int head = static_cast<int>(skip / steps); left > 0 && head < a.kv_heads; ++head) {
+        const int first = static_cast<int>(skip % steps), count = static_cast<int>(min(static_cast<int64_t>(steps - first), left));
+        skip = 0;
+        left -= count;
+        // queries of the head's columns
+        for (int n = tid >> 3; n < (cols + 15) / 16 * 16; n += kManyThreads / 8) {
+          const int r = n / group;
+          const bool real = n < cols;
+          const uint16_t* q = static_cast<const uint16_t*>(a.q);
+          if (real) q += (row0 + r) * a.q_row_stride + static_cast<int64_t>(head * group + n - r * group) * a.q_head_stride;
+          for (int c = 0; c < chunks; ++c) {
+            const int dim = c * 64 + (tid & 7) * 8;
+            const bool in = real && dim < a.dk;
+            copy16(q_at + c * kChunk + n * 128 + (((tid & 7) ^ (n & 7)) << 4), in ? q + dim : static_cast<const uint16_t*>(a.q), in ? 16 : 0);
+          }
+        }
+        // a step's means; `in`: whether this thread's block has one
+        const auto copy_means = [&](int step, uint32_t to, int32_t page) {
+          const int j = step * kTile + tid;
+          const bool in = j < most && page >= 0 && page < p.R.num_blocks;
+          if (!in && j < most) flags |= TOPK_DEV_BAD_BLOCK;
+          copies.aim(static_cast<const char*>(a.means) + 2 * (static_cast<int64_t>(in ? page : 0) * a.mean_block_stride + head * a.mean_head_stride), in, lane);
+          for (int u = 0; u < pieces; ++u) copies.columns(to + u * 2 * kChunk, kChunk, u * 256, a.dk * 2, a.means);
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          return in;
+        };
+        const auto page_of = [&](int step) { return step < first + count && step * kTile + tid < most ? table[step * kTile + tid] : -1; };
+        int32_t page = page_of(first), next_page = page_of(first + 1);
+        asm volatile("" ::"r"(page), "r"(next_page) : "memory");  // before the copies: a load waits behind those
+        bool in = copy_means(first, means_at + buffer * step_bytes, page);
+        for (int step = first; step < first + count; ++step) {
+          const bool more = step + 1 < first + count;
+          bool next_in = false;
+          if (more) {
+            page = next_page;
+            next_page = page_of(step + 2);
+            next_in = copy_means(step + 1, means_at + (buffer ^ 1) * step_bytes, page);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+          } else {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+          }
+          fence_async();
+          __syncthreads();
+          if (warp == 0) {
+            fence_after();
+            uint32_t k = means_at + buffer * step_bytes, q = q_at;
+            int dims = a.dk;
+            bool add = false;
+#pragma unroll 1
+            for (; dims >= 64; dims -= 64, k += kChunk, q += kChunk, add = true) mma16_chunk(tmem, operand(k, 16), operand(q, 16), inst, add);
+#pragma unroll 1
+            for (; dims > 0; dims -= 16, k += 32, q += 32, add = true) mma16_step(tmem, operand(k, 16), operand(q, 16), inst, add);
+            commit(smem_addr(&done));
+          }
+          mbar_wait_warp(smem_addr(&done), products++ & 1, guard);
+          fence_after();
+          const int j = step * kTile + tid;
+          float* to = a.scores + row0 * a.score_row_stride + head * a.score_head_stride + j;
+          const uint32_t from = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+          int r = 0, held = 0;
+          float sum = 0.f;
+#pragma unroll 1
+          for (int c = 0; c < cols; c += 32) {
+            float v[32];
+            tmem_load(from + c, v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              sum += v[i];
+              const bool ends = kGroup > 0 ? (kGroup <= 32 ? i % (kGroup <= 32 ? kGroup : 1) == kGroup - 1 : false) : ++held == group;
+              if (ends) {
+                if (r < rows) {
+                  const int n = seen[r];
+                  if (j < n) *to = final_score(p, sum, in, j, n);
+                }
+                to += a.score_row_stride;
+                ++r;
+                held = 0;
+                sum = 0.f;
+              }
+            }
+          }
+          fence_before();
+          __syncthreads();  // the sums have been read, and the means' place may be filled again
+          in = next_in;
+          buffer ^= 1;
+        }
+      }
+    }
+    skip = 0;
+  }
+  if (flags) atomicOr(p.R.status, flags);
+  settle(guard);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 0) tmem_free(tmem, kTile);
+}
+
+template <int kGroup, bool kBf16>
+int launch_many(ScoreParams& p, int device, const topk_device_props& props, cudaStream_t stream) {
+  static int granted[kMaxDevices];
+  const topk_block_scores_args& a = p.a;
+  const size_t smem = 3 * ((a.dk + 63) / 64) * static_cast<size_t>(kChunk) + 1024;
+  const int rc = allow_smem(many_kernel<kGroup, kBf16>, 3 * (kManyDk / 64) * static_cast<size_t>(kChunk) + 1024, device, granted);
+  if (rc != TOPK_OK) return rc;
+  const int64_t columns = a.rows.max_blocks < a.max_columns ? a.rows.max_blocks : a.max_columns;
+  const int64_t most = a.rows.num_rows * a.kv_heads * ((columns + kTile - 1) / kTile);
+  const int64_t held = props.max_smem_optin / (smem + 2048), ctas = props.num_sms * (held < 1 ? 1 : (held > 4 ? 4 : held));  // 4: of 512 columns of tensor memory
+  p.slices = static_cast<int32_t>(ctas < most ? ctas : most);
+  return launch(many_kernel<kGroup, kBf16>, static_cast<const ScoreParams&>(p), p.slices, kManyThreads, smem, stream);
 }
 
 template <bool kBf16>
-int run_scores(ScoreParams& p, int sms, cudaStream_t stream) {
-  if (p.tile_rows <= 1) return launch_scores<1, kBf16>(p, sms, stream);
-  if (p.tile_rows <= 2) return launch_scores<2, kBf16>(p, sms, stream);
-  if (p.tile_rows <= 4) return launch_scores<4, kBf16>(p, sms, stream);
-  return launch_scores<8, kBf16>(p, sms, stream);
+int run_scores(ScoreParams& p, int device, const topk_device_props& props, cudaStream_t stream) {
+  if (p.tile_rows > kFewRows) {
+    switch (p.group) {
+      case 1: return launch_many<1, kBf16>(p, device, props, stream);
+      case 2: return launch_many<2, kBf16>(p, device, props, stream);
+      case 4: return launch_many<4, kBf16>(p, device, props, stream);
+      case 8: return launch_many<8, kBf16>(p, device, props, stream);
+      case 16: return launch_many<16, kBf16>(p, device, props, stream);
+      default: return launch_many<0, kBf16>(p, device, props, stream);
+    }
+  }
+  if (p.tile_rows <= 1) return launch_few<1, kBf16>(p, props.num_sms, stream);
+  if (p.tile_rows <= 2) return launch_few<2, kBf16>(p, props.num_sms, stream);
+  return launch_few<4, kBf16>(p, props.num_sms, stream);
 }
 
-static_assert(kTileRows * kMaxDk * sizeof(float) <= kQueryBytes, "queries of a tile");
+static_assert(kFewRows * kMaxDk * sizeof(float) <= kQueryBytes, "queries of a tile");
 
 bool two_bytes(int dtype) { return dtype == TOPK_DTYPE_F16 || dtype == TOPK_DTYPE_BF16; }
 
@@ -389,7 +671,8 @@ extern "C" int topk_block_means(const topk_block_means_args* args, void* stream)
       a.table_stride < a.max_blocks || a.num_blocks < 0 || a.num_blocks > INT32_MAX || a.kv_heads < 1)
     return TOPK_ERR_INVALID_ARG;
   if (!two_bytes(a.dtype) || a.kv_heads > 1024 || a.dk < 8 || a.dk > kMaxDk || a.dk % 8) return TOPK_ERR_UNSUPPORTED;
-  if ((a.num_requests < kSegment ? a.num_requests : kSegment) * a.max_blocks > UINT32_MAX) return TOPK_ERR_UNSUPPORTED;
+  const int64_t widths = (a.kv_heads * (a.dk / 8) + kMeanColumns - 1) / kMeanColumns;
+  if ((a.num_requests < kSegment ? a.num_requests : kSegment) * a.max_blocks > INT32_MAX / widths) return TOPK_ERR_UNSUPPORTED;
   if (a.num_requests == 0) return TOPK_OK;
   if (a.context_lens == nullptr || a.new_lens == nullptr || a.block_table == nullptr || a.k == nullptr || a.means == nullptr ||
       a.workspace == nullptr)
@@ -407,9 +690,9 @@ extern "C" int topk_block_means(const topk_block_means_args* args, void* stream)
   rows.max_blocks = a.max_blocks;
   p.R = make_rows(rows, INT32_MAX, a.workspace);
   p.columns = a.kv_heads * (a.dk / 8);
-  p.widths = (p.columns + kMeanColumns - 1) / kMeanColumns;
+  p.widths = static_cast<uint32_t>(widths);
   // Pages are not known here: as many CTAs as the SMs hold, each with every so manieth unit.
-  const int64_t grid = sms * 10;
+  const int64_t grid = sms * 5;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return a.dtype == TOPK_DTYPE_BF16 ? launch(means_kernel<true>, static_cast<const MeanParams&>(p), grid, kMeanThreads, 0, s)
                                     : launch(means_kernel<false>, static_cast<const MeanParams&>(p), grid, kMeanThreads, 0, s);
@@ -432,18 +715,24 @@ extern "C" int topk_block_scores(const topk_block_scores_args* args, void* strea
   if (misaligned(a.q, 16) || a.q_row_stride % 8 || a.q_head_stride % 8 || misaligned(a.means, 16) || a.mean_block_stride % 8 ||
       a.mean_head_stride % 8 || misaligned(a.scores, 4) || misaligned(a.score_lens, 4) || misaligned(a.workspace, 16))
     return TOPK_ERR_MISALIGNED;
-  const int sms = num_sms();
-  if (sms < 1) return TOPK_ERR_CUDA;
+  int device = 0;
+  topk_device_props props{};
+  if (cudaGetDevice(&device) != cudaSuccess || topk_query_device(device, &props) != TOPK_OK) {
+    cudaGetLastError();
+    return TOPK_ERR_CUDA;
+  }
   ScoreParams p{};
   p.a = a;
   p.R = make_rows(a.rows, INT32_MAX, a.workspace);
   p.group = a.heads / a.kv_heads;
   const int64_t rows = a.rows.num_rows;
   // Rows that read the same means share them: the rows of a request; where each row brings its request, as many
-  // neighbours as a request has rows on average.
+  // neighbours as a request has rows on average. More than kFewRows of them go to the tensor cores, as many as fill 128 columns.
   int64_t share = a.rows.next_n;
   if (a.rows.row_request != nullptr) share = a.rows.num_requests > 0 ? (rows + a.rows.num_requests - 1) / a.rows.num_requests : 1;
-  p.tile_rows = static_cast<int32_t>(share < kTileRows ? share : kTileRows);
+  const int fill = kTile / p.group;
+  const int most = a.dk <= kManyDk && fill > kFewRows && share > kFewRows ? fill : kFewRows;
+  p.tile_rows = static_cast<int32_t>(share < most ? share : most);
   if (a.rows.row_request == nullptr) {
     p.request_tiles = (a.rows.next_n + p.tile_rows - 1) / p.tile_rows;
     p.tiles = rows / a.rows.next_n * p.request_tiles;
@@ -451,5 +740,5 @@ extern "C" int topk_block_scores(const topk_block_scores_args* args, void* strea
     p.tiles = (rows + p.tile_rows - 1) / p.tile_rows;
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return a.dtype == TOPK_DTYPE_BF16 ? run_scores<true>(p, sms, s) : run_scores<false>(p, sms, s);
+  return a.dtype == TOPK_DTYPE_BF16 ? run_scores<true>(p, device, props, s) : run_scores<false>(p, device, props, s);
 }

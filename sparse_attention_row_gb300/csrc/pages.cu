@@ -175,30 +175,36 @@ __device__ __forceinline__ int32_t read_peer(const int32_t* mine, uint32_t rank)
 // What other CTAs of the cluster wrote: from L2.
 __device__ __forceinline__ int32_t look(const int32_t* at) { return __ldcg(at); }
 
-// Sums of a CTA: `x` summed up over its threads.
-__device__ __forceinline__ int32_t sum_of_cta(int32_t x, int32_t (&warp_sum)[kPageWarps], int lane, int warp) {
-  for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(~0u, x, d);
-  __syncthreads();
-  if (lane == 0) warp_sum[warp] = x;
-  __syncthreads();
-  int32_t all = 0;
-  for (int w = 0; w < kPageWarps; ++w) all += warp_sum[w];
-  return all;
-}
+__device__ __forceinline__ int4 look4(const int32_t* at) { return __ldcg(reinterpret_cast<const int4*>(at)); }
 
-// Where this thread's `x` (0 or 1) stands among those of the CTA, and how many there are.
-__device__ __forceinline__ int32_t place_in_cta(bool x, int32_t* all, int32_t (&warp_sum)[kPageWarps], int lane, int warp) {
-  const unsigned who = __ballot_sync(~0u, x);
-  __syncthreads();
-  if (lane == 0) warp_sum[warp] = __popc(who);
-  __syncthreads();
-  int32_t at = __popc(who & ((1u << lane) - 1)), total = 0;
-  for (int w = 0; w < kPageWarps; ++w) {
-    if (w < warp) at += warp_sum[w];
-    total += warp_sum[w];
+// Of two counts of every thread: those of the threads before it in `a` and `b`, and the CTA's in `all_a` and `all_b`.
+struct Counts {
+  int32_t a, b, all_a, all_b;
+};
+__device__ __forceinline__ Counts count_before(int32_t a, int32_t b, int2 (&warp_sum)[kPageWarps]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int32_t x = a, y = b;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int32_t u = __shfl_up_sync(~0u, x, d), v = __shfl_up_sync(~0u, y, d);
+    if (lane >= d) x += u, y += v;
   }
-  *all = total;
-  return at;
+  __syncthreads();  // the last sums have been read
+  if (lane == 31) warp_sum[warp] = make_int2(x, y);
+  __syncthreads();
+  int2 mine = warp_sum[lane];  // every warp sums them up for itself
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int32_t u = __shfl_up_sync(~0u, mine.x, d), v = __shfl_up_sync(~0u, mine.y, d);
+    if (lane >= d) mine.x += u, mine.y += v;
+  }
+  Counts c;
+  c.all_a = __shfl_sync(~0u, mine.x, 31);
+  c.all_b = __shfl_sync(~0u, mine.y, 31);
+  const int32_t before_a = __shfl_sync(~0u, mine.x, warp ? warp - 1 : 0), before_b = __shfl_sync(~0u, mine.y, warp ? warp - 1 : 0);
+  c.a = x - a + (warp ? before_a : 0);
+  c.b = y - b + (warp ? before_b : 0);
+  return c;
 }
 
 // Sums over the cluster of what each CTA has in *mine: those before this one, and all.
@@ -216,6 +222,8 @@ __device__ __forceinline__ void sum_of_cluster(const int32_t* mine, int64_t* bef
 
 constexpr int64_t kMostFreed = 1 << 20;  // requests of a call
 constexpr int kOnceWords = kMostFreed / kCluster / 32 + 2;
+constexpr int kEach = 8;                       // places of a thread at a time, side by side
+constexpr int kRound = kEach * kPageThreads;  // places of a CTA
 
 struct FreeParams {
   topk_page_free_args a;
@@ -223,79 +231,119 @@ struct FreeParams {
 };
 
 __global__ void __launch_bounds__(kPageThreads, 1) free_kernel(const __grid_constant__ FreeParams p) {
-  __shared__ int32_t warp_sum[kPageWarps], mine;
+  __shared__ int2 warp_sum[kPageWarps];
+  __shared__ int32_t mine;
   __shared__ uint32_t again[kOnceWords];  // bits of the requests of this CTA that were listed before
   const topk_page_free_args& a = p.a;
   const topk_page_pool& t = a.pool;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t flags = 0;
+  // this CTA's requests, and places: a request's columns in order
+  const int64_t per = (a.num_freed + kCluster - 1) / kCluster, i0 = min(per * cluster_rank(), a.num_freed), i1 = min(i0 + per, a.num_freed);
+  for (int i = tid; i < (i1 - i0 + 31) / 32; i += kPageThreads) again[i] = 0;
   dependent_wait();
   dependent_launch();
   const int64_t taken = min(max(static_cast<int64_t>(*t.taken), int64_t{0}), t.num_free);
-  // this CTA's requests, and places: a request's columns in order
-  const int64_t per = (a.num_freed + kCluster - 1) / kCluster, i0 = min(per * cluster_rank(), a.num_freed), i1 = min(i0 + per, a.num_freed);
-  for (int i = tid; i < kOnceWords; i += kPageThreads) again[i] = 0;
   __syncthreads();
   for (int64_t i = i0 + warp; i < i1; i += kPageWarps) {
     const int32_t request = a.requests[i];
     bool found = false;
+#pragma unroll 8
     for (int64_t j = lane; j < i; j += 32) found |= a.requests[j] == request;
     if (__any_sync(~0u, found) && lane == 0) atomicOr(&again[(i - i0) >> 5], 1u << ((i - i0) & 31));
   }
   __syncthreads();
   const int64_t places = (i1 - i0) * t.max_blocks;
   const uint32_t columns = static_cast<uint32_t>(t.max_blocks);
-  // the page at a place, -1 where there is none; and its entry in the table
-  const auto page_at = [&](int64_t place, int32_t** entry) -> int32_t {
-    const uint32_t i = static_cast<uint32_t>(place) / columns, c = static_cast<uint32_t>(place) - i * columns;
-    if (again[i >> 5] >> (i & 31) & 1) return -1;
-    const int64_t request = a.requests[i0 + i];
-    if (request < 0 || request >= t.num_requests) {
-      flags |= TOPK_DEV_BAD_BLOCK;
-      return -1;
+  // The pages at this thread's places of a round, -1 where there is none. They stay in registers where there is one round only.
+  int32_t page[kEach];
+  const auto read = [&](int64_t round) {
+    const int64_t first = round * kRound + tid * kEach;
+    uint32_t i = static_cast<uint32_t>(first) / columns, c = static_cast<uint32_t>(first) - i * columns;
+    int64_t entry[kEach];
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      entry[k] = -1;
+      if (first + k < places && !(again[i >> 5] >> (i & 31) & 1)) {
+        const int64_t request = a.requests[i0 + i];
+        if (request < 0 || request >= t.num_requests)
+          flags |= TOPK_DEV_BAD_BLOCK;
+        else
+          entry[k] = request * t.table_stride + c;
+      }
+      if (++c == columns) c = 0, ++i;
     }
-    *entry = t.block_table + request * t.table_stride + c;
-    const int32_t page = **entry;
-    if (page >= t.num_blocks) flags |= TOPK_DEV_BAD_BLOCK;
-    return page < t.num_blocks ? page : -1;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) page[k] = entry[k] >= 0 ? t.block_table[entry[k]] : -1;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      if (page[k] >= t.num_blocks) {
+        flags |= TOPK_DEV_BAD_BLOCK;
+        page[k] = -1;
+      }
+    }
   };
-  const auto number = [&](int64_t place) { return INT32_MIN + static_cast<int32_t>(i0 * t.max_blocks + place); };
-  int32_t* entry = nullptr;
-  for (int64_t x = tid; x < places; x += kPageThreads) {
-    const int32_t page = page_at(x, &entry);
-    if (page >= 0) atomicSub(t.shares + page, 1);
+  const auto number = [&](int64_t round, int k) { return INT32_MIN + static_cast<int32_t>(i0 * t.max_blocks + round * kRound + tid * kEach + k); };
+  // Bits of the places whose pages go back: those whose number their page's word holds.
+  const auto going_back = [&](int64_t round) {
+    int32_t word[kEach];
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) word[k] = page[k] >= 0 ? look(t.shares + page[k]) : 0;
+    uint32_t back = 0;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) back |= (page[k] >= 0 && word[k] == number(round, k) ? 1u : 0u) << k;
+    return back;
+  };
+  const int64_t rounds = (places + kRound - 1) / kRound;
+  for (int64_t r = 0; r < rounds; ++r) {
+    read(r);
+#pragma unroll
+    for (int k = 0; k < kEach; ++k)
+      if (page[k] >= 0) atomicSub(t.shares + page[k], 1);
   }
   cluster_sync();
-  for (int64_t x = tid; x < places; x += kPageThreads) {
-    const int32_t page = page_at(x, &entry);
-    if (page >= 0 && look(t.shares + page) < 0) atomicMin(t.shares + page, number(x));
+  for (int64_t r = 0; r < rounds; ++r) {
+    if (rounds > 1) read(r);
+    int32_t word[kEach];
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) word[k] = page[k] >= 0 ? look(t.shares + page[k]) : 0;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k)
+      if (word[k] < 0) atomicMin(t.shares + page[k], number(r, k));
   }
   cluster_sync();
   int32_t count = 0;
-  for (int64_t x = tid; x < places; x += kPageThreads) {
-    const int32_t page = page_at(x, &entry);
-    count += page >= 0 && look(t.shares + page) == number(x);
+  for (int64_t r = 0; r < rounds; ++r) {
+    if (rounds > 1) read(r);
+    count += __popc(going_back(r));
   }
-  count = sum_of_cta(count, warp_sum, lane, warp);
-  if (tid == 0) mine = count;
+  const Counts sums = count_before(count, 0, warp_sum);
+  if (tid == 0) mine = sums.all_a;
   cluster_sync();
   int64_t before, all;
   sum_of_cluster(&mine, &before, &all);
   const int64_t first = taken - all;  // where the pages go, in front of the others
   if (first < 0) flags |= TOPK_DEV_BLOCKS_EXHAUSTED;
-  for (int64_t x0 = 0; x0 < places; x0 += kPageThreads) {
-    const int64_t x = x0 + tid;
-    int32_t* at = nullptr;
-    const int32_t page = x < places ? page_at(x, &at) : -1;
-    const bool back = page >= 0 && look(t.shares + page) == number(x);
-    int32_t here;
-    const int64_t to = first + before + place_in_cta(back, &here, warp_sum, lane, warp);
-    if (back) {
-      if (to >= 0) t.free_blocks[to] = page;
-      t.shares[page] = 0;  // the page's other places find another number here, as they did before
+  for (int64_t r = 0; r < rounds; ++r) {
+    if (rounds > 1) read(r);
+    // (a page's word, once cleared here, is no place's number, as it was none of its other places' before)
+    const uint32_t back = going_back(r);
+    const Counts here = count_before(__popc(back), 0, warp_sum);
+    int64_t to = first + before + here.a;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      if (!(back >> k & 1)) continue;
+      if (to >= 0) t.free_blocks[to] = page[k];
+      t.shares[page[k]] = 0;
+      ++to;
     }
-    if (at != nullptr) *at = -1;
-    before += here;
+    before += here.all_a;
+  }
+  // the rows hold nothing any more
+  for (int64_t i = i0; i < i1; ++i) {
+    const int64_t request = a.requests[i];
+    if (request < 0 || request >= t.num_requests || (again[(i - i0) >> 5] >> ((i - i0) & 31) & 1)) continue;
+    for (int64_t c = tid; c < t.max_blocks; c += kPageThreads) t.block_table[request * t.table_stride + c] = -1;
   }
   if (flags) atomicOr(p.status, flags);
   cluster_sync();  // no CTA leaves before its sums are read; and `taken` has been read by all
@@ -311,22 +359,36 @@ struct CompactParams {
   uint32_t* status;
 };
 
+// Pages of a CTA at a time: four side by side for each thread.
+constexpr int kPages = 4 * kPageThreads;
+
+__device__ __forceinline__ void count4(const int4& m, bool (*is)(int32_t), bool (&hit)[4]) {
+  hit[0] = is(m.x), hit[1] = is(m.y), hit[2] = is(m.z), hit[3] = is(m.w);
+}
+__device__ __forceinline__ bool is_free_now(int32_t m) { return m == kFree; }
+__device__ __forceinline__ bool is_named(int32_t m) { return (m & kNamed) != 0; }
+__device__ __forceinline__ bool is_free_after(int32_t m) { return m == kFree || m < 0; }
+__device__ __forceinline__ int32_t ones(const bool (&hit)[4]) { return hit[0] + hit[1] + hit[2] + hit[3]; }
+
 __global__ void __launch_bounds__(kPageThreads, 1) compact_kernel(const __grid_constant__ CompactParams p) {
-  __shared__ int32_t warp_sum[kPageWarps], mine[3];
+  __shared__ int2 warp_sum[kPageWarps];
+  __shared__ int32_t mine[3];
   const topk_page_compact_args& a = p.a;
   const topk_page_pool& t = a.pool;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x;
   const int64_t rank = cluster_rank(), all_threads = kCluster * kPageThreads, me = rank * kPageThreads + tid;
+  const int64_t padded = (t.num_blocks + 3) / 4 * 4;  // marks are read four at a time; those past the last page are kNothing
   int32_t* mark = static_cast<int32_t*>(a.scratch);
-  int32_t *low = mark + t.num_blocks, *high = low + t.num_blocks;
+  int32_t *low = mark + padded, *high = low + t.num_blocks;
   uint32_t flags = 0;
   dependent_wait();
   dependent_launch();
   const int64_t taken = min(max(static_cast<int64_t>(*t.taken), int64_t{0}), t.num_free);
   const int64_t entries = t.num_requests * t.max_blocks;
   const uint32_t columns = static_cast<uint32_t>(t.max_blocks);
-  for (int64_t b = me; b < t.num_blocks; b += all_threads) mark[b] = kNothing;
+  for (int64_t b = me * 4; b < padded; b += all_threads * 4) *reinterpret_cast<int4*>(mark + b) = make_int4(kNothing, kNothing, kNothing, kNothing);
   cluster_sync();
+#pragma unroll 4
   for (int64_t e = me; e < entries; e += all_threads) {
     const uint32_t r = static_cast<uint32_t>(e) / columns, c = static_cast<uint32_t>(e) - r * columns;
     const int32_t page = t.block_table[r * t.table_stride + c];
@@ -334,43 +396,52 @@ __global__ void __launch_bounds__(kPageThreads, 1) compact_kernel(const __grid_c
     if (page >= t.num_blocks) flags |= TOPK_DEV_BAD_BLOCK;
   }
   cluster_sync();
+#pragma unroll 4
   for (int64_t f = taken + me; f < t.num_free; f += all_threads) {
     const int32_t page = t.free_blocks[f];
     if (page < 0 || page >= t.num_blocks || atomicOr(mark + page, static_cast<int32_t>(kFree)) != kNothing) flags |= TOPK_DEV_BAD_BLOCK;
   }
   cluster_sync();
   // this CTA's pages
-  const int64_t per = (t.num_blocks + kCluster - 1) / kCluster, b0 = min(per * rank, t.num_blocks), b1 = min(b0 + per, t.num_blocks);
+  const int64_t per = (padded / 4 + kCluster - 1) / kCluster * 4, b0 = min(per * rank, padded), b1 = min(b0 + per, padded);
+  const auto marks = [&](int64_t x) { return x + tid * 4 < b1 ? look4(mark + x + tid * 4) : make_int4(kNothing, kNothing, kNothing, kNothing); };
   int32_t free_count = 0, named_count = 0;
-  for (int64_t b = b0 + tid; b < b1; b += kPageThreads) {
-    const int32_t m = look(mark + b);
-    free_count += m == kFree;
-    named_count += (m & kNamed) != 0;
+  for (int64_t x = b0; x < b1; x += kPages) {
+    const int4 m = marks(x);
+    bool hit[4];
+    count4(m, is_free_now, hit);
+    free_count += ones(hit);
+    count4(m, is_named, hit);
+    named_count += ones(hit);
   }
-  free_count = sum_of_cta(free_count, warp_sum, lane, warp);
-  named_count = sum_of_cta(named_count, warp_sum, lane, warp);
+  const Counts sums = count_before(free_count, named_count, warp_sum);
   if (tid == 0) {
-    mine[0] = free_count;
-    mine[1] = named_count;
+    mine[0] = sums.all_a;
+    mine[1] = sums.all_b;
   }
   cluster_sync();
   int64_t free_before, free_all, named_before, named_all;
   sum_of_cluster(&mine[0], &free_before, &free_all);
   sum_of_cluster(&mine[1], &named_before, &named_all);
-  for (int64_t x = b0; x < b1; x += kPageThreads) {
-    const int64_t b = x + tid;
-    const int32_t m = b < b1 ? look(mark + b) : kNothing;
-    const bool is_free = m == kFree, is_named = (m & kNamed) != 0;
-    int32_t n;
-    const int64_t at = free_before + place_in_cta(is_free, &n, warp_sum, lane, warp);
-    if (is_free) low[at] = static_cast<int32_t>(b);
-    free_before += n;
-    const int64_t from_top = named_all - 1 - (named_before + place_in_cta(is_named, &n, warp_sum, lane, warp));
-    if (is_named) high[from_top] = static_cast<int32_t>(b);
-    named_before += n;
+  for (int64_t x = b0; x < b1; x += kPages) {
+    const int4 m = marks(x);
+    bool is_free[4], named[4];
+    count4(m, is_free_now, is_free);
+    count4(m, is_named, named);
+    const Counts here = count_before(ones(is_free), ones(named), warp_sum);
+    int64_t at = free_before + here.a, from_top = named_all - 1 - (named_before + here.b);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int32_t b = static_cast<int32_t>(x + tid * 4 + k);
+      if (is_free[k]) low[at++] = b;
+      if (named[k]) high[from_top--] = b;
+    }
+    free_before += here.all_a;
+    named_before += here.all_b;
   }
   cluster_sync();
   const int64_t pairs = min(free_all, named_all);
+#pragma unroll 2
   for (int64_t i = me; i < a.max_copies; i += all_threads) {
     const int32_t from = i < pairs ? look(high + i) : -1, to = i < pairs ? look(low + i) : -1;
     const bool moves = to < from;
@@ -386,6 +457,7 @@ __global__ void __launch_bounds__(kPageThreads, 1) compact_kernel(const __grid_c
     }
   }
   cluster_sync();
+#pragma unroll 4
   for (int64_t e = me; e < entries; e += all_threads) {
     const uint32_t r = static_cast<uint32_t>(e) / columns, c = static_cast<uint32_t>(e) - r * columns;
     int32_t page = t.block_table[r * t.table_stride + c];
@@ -396,25 +468,36 @@ __global__ void __launch_bounds__(kPageThreads, 1) compact_kernel(const __grid_c
     a.block_table_out[r * a.table_out_stride + c] = page;
   }
   int32_t count = 0;
-  for (int64_t b = b0 + tid; b < b1; b += kPageThreads) {
-    const int32_t m = look(mark + b);
-    count += m == kFree || m < 0;
-    if (m >= 0 && m != kArrived) a.shares_out[b] = t.shares[b];
+  for (int64_t x = b0; x < b1; x += kPages) {
+    const int4 m = marks(x);
+    bool hit[4];
+    count4(m, is_free_after, hit);
+    count += ones(hit);
+    if (a.shares_out != t.shares) {
+      const int32_t word[4] = {m.x, m.y, m.z, m.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t b = x + tid * 4 + k;
+        if (b < min(b1, t.num_blocks) && word[k] >= 0 && word[k] != kArrived) a.shares_out[b] = t.shares[b];
+      }
+    }
   }
-  count = sum_of_cta(count, warp_sum, lane, warp);
-  if (tid == 0) mine[2] = count;
+  const Counts left = count_before(count, 0, warp_sum);
+  if (tid == 0) mine[2] = left.all_a;
   cluster_sync();
   int64_t before, all;
   sum_of_cluster(&mine[2], &before, &all);
   const int64_t taken_out = t.num_free - all;  // the list holds every free page once, so there are no more than it has places
-  for (int64_t x = b0; x < b1; x += kPageThreads) {
-    const int64_t b = x + tid;
-    const int32_t m = b < b1 ? look(mark + b) : kNothing;
-    const bool is_free = m == kFree || m < 0;
-    int32_t n;
-    const int64_t at = taken_out + before + place_in_cta(is_free, &n, warp_sum, lane, warp);
-    if (is_free) a.free_blocks_out[at] = static_cast<int32_t>(b);
-    before += n;
+  for (int64_t x = b0; x < b1; x += kPages) {
+    const int4 m = marks(x);
+    bool hit[4];
+    count4(m, is_free_after, hit);
+    const Counts here = count_before(ones(hit), 0, warp_sum);
+    int64_t at = taken_out + before + here.a;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (hit[k]) a.free_blocks_out[at++] = static_cast<int32_t>(x + tid * 4 + k);
+    before += here.all_a;
   }
   if (a.free_blocks_out != t.free_blocks)
     for (int64_t f = me; f < taken_out; f += all_threads) a.free_blocks_out[f] = t.free_blocks[f];
@@ -608,7 +691,7 @@ extern "C" int topk_page_compact(const topk_page_compact_args* args, void* strea
   if (misaligned(a.source, 4) || misaligned(a.target, 4) || misaligned(a.block_table_out, 4) || misaligned(a.shares_out, 4) ||
       misaligned(a.free_blocks_out, 4) || misaligned(a.taken_out, 4) || misaligned(a.scratch, 16))
     return TOPK_ERR_MISALIGNED;
-  if (a.scratch_bytes < static_cast<size_t>(t.num_blocks) * 3 * sizeof(int32_t)) return TOPK_ERR_WORKSPACE_TOO_SMALL;
+  if (a.scratch_bytes < static_cast<size_t>(t.num_blocks) * 3 * sizeof(int32_t) + 16) return TOPK_ERR_WORKSPACE_TOO_SMALL;
   CompactParams p{};
   p.a = a;
   p.status = static_cast<uint32_t*>(t.workspace);

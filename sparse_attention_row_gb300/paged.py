@@ -422,11 +422,12 @@ class PagedDecoder:
                 self._bad("table_out", table_out, f"a {(requests, columns)} tensor")
             stride = stride if requests > 1 or stride >= columns else columns
         out, source, target = self._copies(out, max_copies, stream)
-        scratch = self._empty(12 * blocks, self._u8, stream)
+        need = 12 * blocks + 16
+        scratch = self._empty(need, self._u8, stream)
         self._call(self._compact, _COMPACT.pack(
             *pool, max_copies, source, target, table, stride, pool[4] if shares_out is None else self._ints("shares_out", shares_out, blocks),
             pool[6] if free_out is None else self._ints("free_out", free_out, free), pool[8] if taken_out is None else self._ints("taken_out", taken_out, 1),
-            scratch.data_ptr(), 12 * blocks), stream)
+            scratch.data_ptr(), need), stream)
         return out
 
     def page_caches(self, caches) -> PageCaches:
@@ -442,7 +443,7 @@ class PagedDecoder:
             self._bad("a cache", t, "a [blocks, ...] tensor")
         size, strides, shape = t.element_size(), t.stride(), t.shape
         if t.is_contiguous():
-            run, loops = t[0].numel() if shape[0] else 1, []
+            run, loops = t.numel() // shape[0] if shape[0] else 1, []
         else:
             # the loops over a page, the inner ones first; those that follow one another in memory are one
             run, loops = 1, []

@@ -180,6 +180,44 @@ def test_scores_of_rows_of_a_request(dec, next_n):
     ok(dec)
 
 
+@pytest.mark.parametrize("heads, kv, dk", [(6, 2, 128), (24, 1, 64), (25, 1, 256), (75, 3, 40), (64, 4, 128), (4, 4, 8), (2, 1, 248), (26, 1, 64), (16, 2, 264)])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_scores_of_many_rows_of_a_request(dec, heads, kv, dk, dtype):
+    # groups that fill the columns and that do not, pages that there are none of, rows that see nothing among others
+    rows = 150
+    lengths = [0 if r % 11 == 5 else 300 + 7 * r for r in range(rows)]
+    case = scores_case(8, lengths, [0] * rows, heads, kv, dk, dtype, 2)
+    check_scores(dec, case, lengths, [0] * rows, 2, sinks=2, recent=3, next_n=rows)
+    requests = [0] * 70 + [1] * 3 + [2] * 77
+    case = scores_case(9, lengths, requests, heads, kv, dk, dtype, 4)
+    check_scores(dec, case, lengths, requests, 4, recent=1, row_request=True)
+    ok(dec)
+    q, means, table = case
+    table = table.clone()
+    bad = [3, 7, 130]
+    table[0, 3], table[0, 7], table[2, 130] = -5, means.shape[0], 2 ** 31 - 1
+    good = table.clamp(0, means.shape[0] - 1)
+    want, tol, _ = scores64(q, torch.nan_to_num(means.float()).to(dtype), good, lengths, requests, 4, 0, 0, table.shape[1])
+    got, _ = dec.block_scores(q.cuda(), means.cuda(), table.cuda(), ints(lengths), 4, row_request=ints(requests))
+    got = got.cpu().double()
+    for r, b in enumerate(requests):
+        n = -(-lengths[r] // 4)
+        off = torch.tensor([bool((table[b, j] < 0) | (table[b, j] >= means.shape[0])) for j in range(n)], dtype=torch.bool)
+        assert (got[r, :, :n][:, off] == -math.inf).all()
+        assert ((got[r, :, :n] - want[r, :, :n]).abs() <= tol[r, :, :n])[:, ~off].all()
+    assert dec.status() == sar.TOPK_DEV_BAD_BLOCK
+
+
+def test_scores_that_are_no_numbers_stay_in_their_blocks(dec):
+    for rows in (1, 9):
+        means = torch.zeros(300, 1, 64).half()
+        means[5, 0, 0], means[130, 0, 1], means[131, 0, 2] = math.inf, math.nan, -math.inf
+        got, _ = dec.block_scores(torch.ones(rows, 4, 64).half().cuda(), means.cuda(), torch.arange(300, dtype=torch.int32, device="cuda")[None], ints([300] * rows), 1, next_n=rows)
+        got = got.cpu()[:, 0]
+        assert (got[:, 5] == math.inf).all() and got[:, 130].isnan().all() and (got[:, 131] == -math.inf).all()
+        assert (got[:, [i for i in range(300) if i not in (5, 130, 131)]] == 0).all()
+
+
 def test_scores_with_a_request_for_each_row(dec):
     requests = [0] * 9 + [2] * 3 + [1] + [2] * 2 + [3, 0, 3]
     lengths = [200 + i for i in range(9)] + [0, 130, 600, 1, 128, 129, 77, 900, 2]

@@ -180,7 +180,7 @@ def test_free_refusals(code, change):
 
 @pytest.mark.parametrize("code, change", POOL + [
     (BAD, dict(max_copies=-1)), (BAD, dict(table_out_stride=7)), (BAD, dict(source=None)), (BAD, dict(target=None)), (BAD, dict(block_table_out=None)), (BAD, dict(shares_out=None)),
-    (BAD, dict(free_blocks_out=None)), (BAD, dict(taken_out=None)), (BAD, dict(scratch=None)), (SMALL, dict(scratch_bytes=119)), (MIS, dict(scratch=FAKE + 4)), (MIS, dict(taken_out=FAKE + 2))])
+    (BAD, dict(free_blocks_out=None)), (BAD, dict(taken_out=None)), (BAD, dict(scratch=None)), (SMALL, dict(scratch_bytes=135)), (MIS, dict(scratch=FAKE + 4)), (MIS, dict(taken_out=FAKE + 2))])
 def test_compact_refusals(code, change):
     assert sar.topk_page_compact(compact_args(**change), 0) == code
 

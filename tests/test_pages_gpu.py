@@ -186,6 +186,28 @@ def test_many_requests_freed_at_once_the_same_every_time(dec):
     ok(dec)
 
 
+def test_wide_tables_freed_in_several_rounds(dec):
+    rng = random.Random(6)
+    pool = Pool(400, 700, 60000, 1, rng)
+    for r in range(100):
+        pool.grow(r, rng.randrange(300, 500))
+    parents = [rng.randrange(100) for _ in range(300)]
+    kept = [rng.randrange(sum(p >= 0 for p in pool.table[a]) + 1) for a in parents]
+    state = pool.device()
+    dec.fork_pages(ints(parents), ints(list(range(100, 400))), ints(kept), *state, 1)
+    pool.fork(parents, list(range(100, 400)), kept)
+    pool.same(state)
+    gone = rng.sample(range(400), 380)
+    gone.insert(200, gone[3])
+    dec.free_pages(ints(gone), *state)
+    pool.release(gone)
+    pool.same(state)
+    dec.compact_pages(*state, 100000)
+    pool.compact(100000)
+    pool.same(state)
+    ok(dec)
+
+
 def test_fork_limits(dec):
     # no free page left; rows outside the table; a parent without the page; more tokens than the table is wide
     table = ints([[4, 5, 6], [7, -1, 90], [-1, -1, -1], [-1, -1, -1], [-1, -1, -1], [9, 9, 9]])
