@@ -20,7 +20,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["topk_kernel.cu", "topk_kernel_pair.cu", "topk_kernel_small.cu", "topk_short.cu", "topk_short16.cu", "topk_sort.cu",
            "topk_api.cu",
            "topk_static.cu", "kv_map.cu", "cache_map.cu", "index_logits.cu", "paged_attention.cu", "block_attention.cu", "tail_attention.cu",
-           "prefix_attention.cu", "shared_attention.cu", "wide_prefix.cu", "block_scores.cu", "pages.cu", "planner.cpp"]
+           "prefix_attention.cu", "whole_attention.cu", "shared_attention.cu", "wide_prefix.cu", "block_scores.cu", "pages.cu", "planner.cpp"]
 
 
 def _nvcc() -> str:

@@ -15,6 +15,7 @@ enum class Form {
   kBlocks,  // topk_block_attention: index lists name blocks, one list for each row and key-value head
   kTail,    // topk_shared_attention, the tokens behind the prefixes: rows begin at a page of their own
   kShared,  // topk_shared_attention, the prefixes: units are runs of rows that share one
+  kWhole,   // topk_shared_attention, each row by itself: the prefix's pages are found in its row of their table
 };
 
 // Neighbouring rows that share a prefix.
@@ -23,6 +24,36 @@ struct SharedRun {
   int32_t prefix;  // row of the prefixes' table
   int32_t length;  // tokens shared: whole pages
 };
+
+// What requests begin with.
+struct Prefixes {
+  const int32_t* of;  // [requests]
+  const int32_t* lens;
+  const int32_t* table;
+  int64_t count, stride;
+  int64_t most;  // tokens of a row of the table
+};
+
+// Tokens of a request's prefix, whole pages; 0: nothing shared. `prefix`: which one.
+__device__ __forceinline__ int prefix_tokens(const Prefixes& p, const Rows& R, int64_t request, int32_t* prefix) {
+  if (request < 0 || request >= R.num_requests) return 0;
+  *prefix = p.of[request];
+  if (*prefix < 0 || *prefix >= p.count) return 0;
+  const int64_t n = p.lens[*prefix];
+  if (n <= 0) return 0;
+  return block_column(R, static_cast<int>(n < p.most ? n : p.most)) * R.block_size;
+}
+
+// The same for a row: 0 also where one of its request's rows, which read what follows together, sees less.
+__device__ __forceinline__ int row_prefix_tokens(const Prefixes& p, const Rows& R, int64_t row, int32_t* prefix) {
+  const int64_t request = row_request(R, row);
+  const int n = prefix_tokens(p, R, request, prefix);
+  if (n == 0) return 0;
+  if (R.row_request) return seen_tokens(R, R.lengths[row], request) >= n ? n : 0;
+  for (int j = 0; j < R.next_n; ++j)
+    if (seen_tokens(R, R.lengths[request * R.next_n + j], request) < n) return 0;
+  return n;
+}
 
 struct FormArgs {
   // kBlocks
@@ -34,16 +65,15 @@ struct FormArgs {
   // kShared
   const SharedRun* runs;
   const int32_t* run_count;
-  const int32_t* prefix_table;
-  int64_t prefix_stride;
-  int64_t prefix_most;  // tokens of a prefix at most
-  float* tail_lse;      // [slices][2][column blocks][columns]: of what is behind the prefix, for the join
+  Prefixes prefixes;  // and kWhole
+  float* tail_lse;    // [slices][2][column blocks][columns]: of what is behind the prefix, for the join
 };
 
 int attend_plain(const topk_attention_args& a, const FormArgs& f, void* stream);
 int attend_blocks(const topk_attention_args& a, const FormArgs& f, void* stream);
 int attend_tail(const topk_attention_args& a, const FormArgs& f, void* stream);
 int attend_shared(const topk_attention_args& a, const FormArgs& f, void* stream);
+int attend_whole(const topk_attention_args& a, const FormArgs& f, void* stream);
 
 constexpr int kMaxQk = 576, kMaxV = 512;
 

@@ -8,8 +8,6 @@
 namespace ltk {
 namespace paged {
 
-constexpr float kMoveAbove = 8.f;  // in powers of two: how far scores may rise above a row's maximum before that is moved
-
 struct Join {  // what a join has to know of the unit that ends in a slice and began before it
   int64_t rowgroup;
   int32_t kv_head;

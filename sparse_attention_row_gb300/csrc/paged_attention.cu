@@ -48,7 +48,7 @@
 //
 // Forms. The kernel is compiled once more for each form of the call (attention_forms.cuh says what they
 // are for): kBlocks, whose index lists name blocks, one list for each row and key-value head; kTail, whose
-// rows begin at a page of their own; kShared, whose units are runs of rows that share a prefix, and whose results are joined
+// rows begin at a page of their own; kWhole, whose rows find their first pages in another table; kShared, whose units are runs of rows that share a prefix, and whose results are joined
 // with what kTail left in `out` and `lse`. A translation unit each, in which kForm is a constant.
 #include <cfloat>
 
@@ -97,6 +97,7 @@ constexpr int kMaxSlots = 6;
 constexpr int kMaxBlockCols = 64;
 constexpr int kTeam = 128, kJoinDims = 32;  // threads of a team
 constexpr int kMaxTeams = 4;                // which take the parts in turn
+constexpr float kMoveAbove = 8.f;  // in powers of two
 constexpr int kMaxParts = 512;  // slices of a launch at most
 
 struct Params {
@@ -513,9 +514,15 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<N, kLatent>) attention_k
       const int64_t row0 = group_row(p, walk.group);
       const int length = group_length(p, walk.group);
       const int64_t request = length > 0 && kForm != Form::kShared ? row_request(p.R, row0) : 0;
-      const int32_t* pages = kForm == Form::kShared ? p.f.prefix_table + p.f.runs[walk.group].prefix * p.f.prefix_stride
+      const int32_t* pages = kForm == Form::kShared ? p.f.prefixes.table + p.f.runs[walk.group].prefix * p.f.prefixes.stride
                              : kForm == Form::kTail ? p.R.block_table + request * p.R.table_stride + (length > 0 ? p.f.skip[row0] : 0)
                                                     : nullptr;
+      int prefix = 0;  // tokens that are found in the prefix's row of its table
+      if constexpr (kForm == Form::kWhole) {
+        int32_t which = 0;
+        if (length > 0) prefix = row_prefix_tokens(p.f.prefixes, p.R, row0, &which);
+        pages = p.f.prefixes.table + static_cast<int64_t>(prefix > 0 ? which : 0) * p.f.prefixes.stride;
+      }
       const int32_t* list = kForm == Form::kBlocks ? p.f.blocks + row0 * p.f.block_row_stride + walk.kv_head * p.f.block_head_stride
                             : p.a.indices          ? p.a.indices + row0 * p.a.index_row_stride
                                                    : nullptr;
@@ -534,6 +541,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<N, kLatent>) attention_k
       };
       const auto table_entry = [&](int x) {
         if constexpr (kForm == Form::kTail || kForm == Form::kShared) return x >= 0 && x < length ? pages[block_column(p.R, x)] : 0;
+        if (kForm == Form::kWhole && x >= 0 && x < prefix) return pages[block_column(p.R, x)];
         return x >= 0 && x < length ? p.R.block_table[request * p.R.table_stride + block_column(p.R, x)] : 0;
       };
       const auto address = [&](const void* cache, int x, int x_block, int64_t block_stride, int64_t token_stride, int64_t head_stride) {
@@ -930,6 +938,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<N, kLatent>) attention_k
     }
   }
   if (kForm != Form::kShared && blockIdx.x == 0) report_rows(p.R, tid, kThreads);
+  if (kForm == Form::kWhole && blockIdx.x == 0) {
+    for (int64_t r = tid; r < p.R.num_requests; r += kThreads)
+      if (p.f.prefixes.of[r] >= p.f.prefixes.count) atomicOr(p.R.status, TOPK_DEV_BAD_BLOCK);
+  }
   settle(guard);
   fence_before();
   __syncthreads();
@@ -1148,7 +1160,7 @@ int attend(const topk_attention_args& a, const FormArgs& f, void* stream) {
   p.scale2 = a.scale * 1.4426950408889634f;
   // (Of a shared prefix: what one prefix for all rows has. There may be more units, up to one for each row and head.)
   const int64_t units = kForm == Form::kShared ? (a.rows.num_rows + p.pack - 1) / p.pack * a.kv_heads : p.row_groups * a.kv_heads;
-  const int64_t longest = kForm == Form::kShared ? f.prefix_most : p.R.max_len;
+  const int64_t longest = kForm == Form::kShared ? f.prefixes.most : p.R.max_len;
   const int64_t most = (kForm == Form::kShared ? a.rows.num_rows * a.kv_heads : units) * (lists ? p.row_tiles : (longest + kTile - 1) / kTile);
   // two CTAs on an SM where a tile is two pieces and each has some units (64 rows of 64 heads over 8, 32 blocks: 94 us with one, 96 with two)
   p.ctas = kForm == Form::kBlocks && !p.latent && p.block_cols <= 16 && p.k_pieces + p.v_pieces == 2 && units >= 8ll * sms ? 2 : 1;

@@ -13,8 +13,8 @@
 //            sums over the pool; their pairs are the moves, as long as they lower a number.
 //   copy     every cache's pages in pieces of 16 KB over all CTAs, 16 bytes a thread and four loads at a time: bound by HBM.
 //
-// Free and compact are one cluster of eight CTAs, whose barrier in hardware takes the place of further launches. They are bound by
-// latency up to some 100 000 entries of the table (a step is 1 to 2 us) and by eight SMs' loads above.
+// Free and compact are one cluster of 16 CTAs, whose barrier in hardware takes the place of further launches. They are bound by
+// latency up to some 100 000 entries of the table (a step is 1 to 2 us) and by 16 SMs' loads and atomics above.
 #include "paged.cuh"
 
 namespace ltk {
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const __grid_constan
 
 // ---- one cluster ------------------------------------------------------------
 
-constexpr int kCluster = 8;
+constexpr int kCluster = 16;  // CTAs at most; 8 where the device takes no more
 constexpr int kPageThreads = 1024;
 constexpr int kPageWarps = kPageThreads / 32;
 
@@ -154,6 +154,12 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
+}
+
+__device__ __forceinline__ uint32_t cluster_ctas() {
+  uint32_t n;
+  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+  return n;
 }
 
 // All threads of the cluster meet; what they wrote before is seen behind it.
@@ -210,18 +216,21 @@ __device__ __forceinline__ Counts count_before(int32_t a, int32_t b, int2 (&warp
 // Sums over the cluster of what each CTA has in *mine: those before this one, and all.
 __device__ __forceinline__ void sum_of_cluster(const int32_t* mine, int64_t* before, int64_t* all) {
   *before = *all = 0;
-  const uint32_t me = cluster_rank();
+  const uint32_t me = cluster_rank(), ctas = cluster_ctas();
+  int32_t x[kCluster];
+#pragma unroll
+  for (uint32_t r = 0; r < kCluster; ++r) x[r] = r < ctas ? read_peer(mine, r) : 0;
+#pragma unroll
   for (uint32_t r = 0; r < kCluster; ++r) {
-    const int32_t x = read_peer(mine, r);
-    if (r < me) *before += x;
-    *all += x;
+    if (r < me) *before += x[r];
+    *all += x[r];
   }
 }
 
 // ---- free -------------------------------------------------------------------
 
 constexpr int64_t kMostFreed = 1 << 20;  // requests of a call
-constexpr int kOnceWords = kMostFreed / kCluster / 32 + 2;
+constexpr int kOnceWords = kMostFreed / 8 / 32 + 2;
 constexpr int kEach = 8;                       // places of a thread at a time, side by side
 constexpr int kRound = kEach * kPageThreads;  // places of a CTA
 
@@ -239,7 +248,7 @@ __global__ void __launch_bounds__(kPageThreads, 1) free_kernel(const __grid_cons
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t flags = 0;
   // this CTA's requests, and places: a request's columns in order
-  const int64_t per = (a.num_freed + kCluster - 1) / kCluster, i0 = min(per * cluster_rank(), a.num_freed), i1 = min(i0 + per, a.num_freed);
+  const int64_t per = (a.num_freed + cluster_ctas() - 1) / cluster_ctas(), i0 = min(per * cluster_rank(), a.num_freed), i1 = min(i0 + per, a.num_freed);
   for (int i = tid; i < (i1 - i0 + 31) / 32; i += kPageThreads) again[i] = 0;
   dependent_wait();
   dependent_launch();
@@ -340,10 +349,11 @@ __global__ void __launch_bounds__(kPageThreads, 1) free_kernel(const __grid_cons
     before += here.all_a;
   }
   // the rows hold nothing any more
-  for (int64_t i = i0; i < i1; ++i) {
-    const int64_t request = a.requests[i];
-    if (request < 0 || request >= t.num_requests || (again[(i - i0) >> 5] >> ((i - i0) & 31) & 1)) continue;
-    for (int64_t c = tid; c < t.max_blocks; c += kPageThreads) t.block_table[request * t.table_stride + c] = -1;
+#pragma unroll 4
+  for (int64_t x = tid; x < places; x += kPageThreads) {
+    const uint32_t i = static_cast<uint32_t>(x) / columns, c = static_cast<uint32_t>(x) - i * columns;
+    const int64_t request = a.requests[i0 + i];
+    if (request >= 0 && request < t.num_requests && !(again[i >> 5] >> (i & 31) & 1)) t.block_table[request * t.table_stride + c] = -1;
   }
   if (flags) atomicOr(p.status, flags);
   cluster_sync();  // no CTA leaves before its sums are read; and `taken` has been read by all
@@ -376,7 +386,7 @@ __global__ void __launch_bounds__(kPageThreads, 1) compact_kernel(const __grid_c
   const topk_page_compact_args& a = p.a;
   const topk_page_pool& t = a.pool;
   const int tid = threadIdx.x;
-  const int64_t rank = cluster_rank(), all_threads = kCluster * kPageThreads, me = rank * kPageThreads + tid;
+  const int64_t rank = cluster_rank(), all_threads = cluster_ctas() * kPageThreads, me = rank * kPageThreads + tid;
   const int64_t padded = (t.num_blocks + 3) / 4 * 4;  // marks are read four at a time; those past the last page are kNothing
   int32_t* mark = static_cast<int32_t*>(a.scratch);
   int32_t *low = mark + padded, *high = low + t.num_blocks;
@@ -403,7 +413,7 @@ __global__ void __launch_bounds__(kPageThreads, 1) compact_kernel(const __grid_c
   }
   cluster_sync();
   // this CTA's pages
-  const int64_t per = (padded / 4 + kCluster - 1) / kCluster * 4, b0 = min(per * rank, padded), b1 = min(b0 + per, padded);
+  const int64_t per = (padded / 4 + cluster_ctas() - 1) / cluster_ctas() * 4, b0 = min(per * rank, padded), b1 = min(b0 + per, padded);
   const auto marks = [&](int64_t x) { return x + tid * 4 < b1 ? look4(mark + x + tid * 4) : make_int4(kNothing, kNothing, kNothing, kNothing); };
   int32_t free_count = 0, named_count = 0;
   for (int64_t x = b0; x < b1; x += kPages) {
@@ -506,21 +516,51 @@ __global__ void __launch_bounds__(kPageThreads, 1) compact_kernel(const __grid_c
   if (me == 0) *a.taken_out = static_cast<int32_t>(taken_out);
 }
 
+// A cluster of `ctas` for this kernel, as a launch without its stream.
 template <typename Args>
-int launch_cluster(void (*kernel)(Args), const Args& args, cudaStream_t stream) {
+cudaLaunchConfig_t cluster_config(void (*kernel)(Args), int ctas, cudaLaunchAttribute (&attr)[2]) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kCluster);
+  cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kPageThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kCluster;
+  attr[0].val.clusterDim.x = ctas;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = dependent_launch_default() ? 2 : 1;
+  return cfg;
+}
+
+// CTAs of the cluster: 16 where the device can hold one of those, else 8. Asked for once for each kernel and device.
+template <typename Args>
+int cluster_size(void (*kernel)(Args), int* known) {
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  if (device < kMaxDevices && __atomic_load_n(&known[device], __ATOMIC_ACQUIRE) > 0) return known[device];
+  int size = 8, clusters = 0;
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = cluster_config(kernel, kCluster, attr);
+  cfg.numAttrs = 1;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+      cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) == cudaSuccess && clusters > 0)
+    size = kCluster;
+  cudaGetLastError();
+  if (device < kMaxDevices) __atomic_store_n(&known[device], size, __ATOMIC_RELEASE);
+  return size;
+}
+
+template <typename Args>
+int launch_cluster(void (*kernel)(Args), const Args& args, bool large, int* known, cudaStream_t stream) {
+  const int ctas = large ? cluster_size(kernel, known) : 8;
+  if (ctas == 0) return TOPK_ERR_CUDA;
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = cluster_config(kernel, ctas, attr);
+  cfg.stream = stream;
   if (cudaLaunchKernelEx(&cfg, kernel, args) != cudaSuccess) {
     cudaGetLastError();
     return TOPK_ERR_CUDA;
@@ -674,7 +714,8 @@ extern "C" int topk_page_free(const topk_page_free_args* args, void* stream) {
   FreeParams p{};
   p.a = a;
   p.status = static_cast<uint32_t*>(a.pool.workspace);
-  return launch_cluster(free_kernel, static_cast<const FreeParams&>(p), static_cast<cudaStream_t>(stream));
+  static int known[kMaxDevices];
+  return launch_cluster(free_kernel, static_cast<const FreeParams&>(p), true, known, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int topk_page_compact(const topk_page_compact_args* args, void* stream) {
@@ -695,7 +736,10 @@ extern "C" int topk_page_compact(const topk_page_compact_args* args, void* strea
   CompactParams p{};
   p.a = a;
   p.status = static_cast<uint32_t*>(t.workspace);
-  return launch_cluster(compact_kernel, static_cast<const CompactParams&>(p), static_cast<cudaStream_t>(stream));
+  static int known[kMaxDevices];
+  // (18 K pages, 16 K entries: 21 us with 8 CTAs, 23 with 16, whose barriers take longer)
+  const bool large = t.num_blocks + t.num_requests * t.max_blocks > (1 << 18);
+  return launch_cluster(compact_kernel, static_cast<const CompactParams&>(p), large, known, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int topk_page_copy(const topk_page_copy_args* args, void* stream) {

@@ -9,6 +9,9 @@
 //           `out` and `lse`.
 //   prefix  attention over the prefixes, a run of rows at a time, which joins its results with those of the tails as it writes
 //           them: wide_prefix.cu, 256 columns a run, or kShared of the kernel of all forms, 64.
+// Small calls take none of them, but one launch in which every row finds the prefix's pages in their table (kWhole).
+#include <cfloat>
+
 #include "attention_forms.cuh"
 #include "paged.cuh"
 
@@ -20,38 +23,13 @@ constexpr int kThreads = 1024;
 
 struct PlanParams {
   Rows R;
-  const int32_t* prefix_of;
-  int64_t num_prefixes;
-  const int32_t* prefix_lens;
-  int64_t prefix_most;  // tokens of a prefix's row of the table
+  Prefixes prefixes;
   int32_t run_rows;     // of a run at most
   int32_t* tail_lengths;
   int32_t* skip;
   SharedRun* runs;
   int32_t* run_count;
 };
-
-// Tokens of a row's prefix, whole pages; 0: nothing shared. `prefix`: which one.
-__device__ __forceinline__ int shared_tokens(const PlanParams& p, int64_t request, int32_t* prefix) {
-  if (request < 0 || request >= p.R.num_requests) return 0;
-  *prefix = p.prefix_of[request];
-  if (*prefix < 0 || *prefix >= p.num_prefixes) return 0;
-  const int64_t n = p.prefix_lens[*prefix];
-  if (n <= 0) return 0;
-  const int held = static_cast<int>(n < p.prefix_most ? n : p.prefix_most);
-  return block_column(p.R, held) * p.R.block_size;
-}
-
-// What row `row` shares, and with whom: 0 where one of its request's rows, which read the rest together, sees less.
-__device__ __forceinline__ int row_shares(const PlanParams& p, int64_t row, int32_t* prefix) {
-  const int64_t request = row_request(p.R, row);
-  const int n = shared_tokens(p, request, prefix);
-  if (n == 0) return 0;
-  if (p.R.row_request) return seen_tokens(p.R, p.R.lengths[row], request) >= n ? n : 0;
-  for (int j = 0; j < p.R.next_n; ++j)
-    if (seen_tokens(p.R, p.R.lengths[request * p.R.next_n + j], request) < n) return 0;
-  return n;
-}
 
 // One CTA: rows 1024 at a time, with the start of the run that the last segment ended in.
 __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
@@ -63,7 +41,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
   const auto key_of = [&](int64_t row) -> int64_t {
     int32_t prefix = -1;
     if (row < 0 || row >= p.R.num_rows) return -1;
-    const int n = row_shares(p, row, &prefix);
+    const int n = row_prefix_tokens(p.prefixes, p.R, row, &prefix);
     return n == 0 ? -1 : static_cast<int64_t>(prefix) << 32 | n;
   };
   uint32_t bits = 0;
@@ -82,7 +60,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
       if (request >= p.R.num_requests) bits |= TOPK_DEV_BAD_BLOCK;
       if (request >= 0 && request < p.R.num_requests) {
         if (n < 0 || n > p.R.max_len) bits |= TOPK_DEV_LENGTH_CLAMPED;
-        if (p.prefix_of[request] >= p.num_prefixes) bits |= TOPK_DEV_BAD_BLOCK;
+        if (p.prefixes.of[request] >= p.prefixes.count) bits |= TOPK_DEV_BAD_BLOCK;
       }
       const int shared = mine < 0 ? 0 : static_cast<int32_t>(mine);
       p.tail_lengths[row] = seen_tokens(p.R, n, request) - shared;
@@ -124,6 +102,14 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
   }
   if (tid == 0) *p.run_count = count;
   if (bits) atomicOr(p.R.status, bits);
+}
+
+// Bytes that all rows together read up to which each reads the prefix for itself, out of L2. (32 heads over 8: 134 MB 25 to 28 us,
+// shared 31 to 36; 537 MB 62 to 77 us, shared 36 to 56. 16 latent heads: 151 MB 29 to 35 us, shared 55 to 61; 604 MB 74 to 77 us,
+// shared 69 to 73. 128 latent heads fill the columns by themselves: 604 MB 194 us, shared 221.)
+double read_alone(const topk_attention_args& a) {
+  if (takes_wide(a)) return 256e6;
+  return a.heads / a.kv_heads >= kSharedCols ? DBL_MAX : 512e6;
 }
 
 size_t round_up(size_t n) { return (n + 255) / 256 * 256; }
@@ -176,12 +162,15 @@ extern "C" int topk_shared_attention(const topk_shared_attention_args* args, voi
   char* scratch = static_cast<char*>(s.scratch);
   const int64_t held = s.prefix_blocks > INT32_MAX / a.rows.block_size ? INT32_MAX : s.prefix_blocks * a.rows.block_size;
 
+  FormArgs f{};
+  f.prefixes = Prefixes{s.prefix_of, s.prefix_lens, s.prefix_table, s.num_prefixes, s.prefix_stride, held};
+  // Of the prefixes' lengths the host knows what their table can hold.
+  const double bytes = 2.0 * a.rows.num_rows * held * a.kv_heads * (a.dk + (a.v != nullptr ? a.dv : 0));
+  if (bytes <= read_alone(a)) return attend_whole(a, f, stream);
+
   PlanParams p{};
   p.R = make_rows(a.rows, INT32_MAX, a.workspace);
-  p.prefix_of = s.prefix_of;
-  p.num_prefixes = s.num_prefixes;
-  p.prefix_lens = s.prefix_lens;
-  p.prefix_most = held;
+  p.prefixes = f.prefixes;
   p.run_rows = rows_of_run(a);
   p.tail_lengths = reinterpret_cast<int32_t*>(scratch + at.lengths);
   p.skip = reinterpret_cast<int32_t*>(scratch + at.skip);
@@ -190,7 +179,6 @@ extern "C" int topk_shared_attention(const topk_shared_attention_args* args, voi
   rc = launch(plan_kernel, p, 1, kThreads, 0, static_cast<cudaStream_t>(stream));
   if (rc != TOPK_OK) return rc;
 
-  FormArgs f{};
   f.skip = p.skip;
   topk_attention_args tail = a;
   tail.rows.lengths = p.tail_lengths;
@@ -198,9 +186,6 @@ extern "C" int topk_shared_attention(const topk_shared_attention_args* args, voi
   if (rc != TOPK_OK || s.num_prefixes == 0) return rc;
   f.runs = p.runs;
   f.run_count = p.run_count;
-  f.prefix_table = s.prefix_table;
-  f.prefix_stride = s.prefix_stride;
-  f.prefix_most = held;
   f.tail_lse = reinterpret_cast<float*>(scratch + at.tail_lse);
   return takes_wide(a) ? attend_wide(tail, f, f.tail_lse, stream) : attend_shared(tail, f, stream);
 }

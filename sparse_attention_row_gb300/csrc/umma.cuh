@@ -178,6 +178,17 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[N]) {
   for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));  // used from here on, not before
 }
 
+// 64 columns, for which is waited once.
+__device__ __forceinline__ void tmem_load64(uint32_t addr, float (&v)[64]) {
+  __syncwarp();
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31]), "=f"(v[32]), "=f"(v[33]), "=f"(v[34]), "=f"(v[35]), "=f"(v[36]), "=f"(v[37]), "=f"(v[38]), "=f"(v[39]), "=f"(v[40]), "=f"(v[41]), "=f"(v[42]), "=f"(v[43]), "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47]), "=f"(v[48]), "=f"(v[49]), "=f"(v[50]), "=f"(v[51]), "=f"(v[52]), "=f"(v[53]), "=f"(v[54]), "=f"(v[55]), "=f"(v[56]), "=f"(v[57]), "=f"(v[58]), "=f"(v[59]), "=f"(v[60]), "=f"(v[61]), "=f"(v[62]), "=f"(v[63])
+               : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 64; ++i) asm volatile("" : "+f"(v[i]));  // used from here on, not before
+}
+
 // 32 columns of two values each, or of what else fills 32 bits.
 __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t* v) {
   __syncwarp();
@@ -306,7 +317,7 @@ __device__ __forceinline__ void mma16_tokens(uint32_t d, uint32_t a, uint32_t b,
       : "memory");
 }
 
-// A in tensor memory, 128 rows by 128 columns of two bytes (64 of its columns); B MN-major, 128 rows: eight steps of 16.
+// A in tensor memory, 128 rows by 64 columns of two bytes (32 of its columns); B MN-major, 64 rows: four steps of 16.
 __device__ __forceinline__ void mma16_held(uint32_t d, uint32_t a, uint32_t b, uint32_t inst, bool add) {
   d = uniform(d), a = uniform(a), b = uniform(b);
   asm volatile(
@@ -319,14 +330,6 @@ __device__ __forceinline__ void mma16_held(uint32_t d, uint32_t a, uint32_t b, u
       " add.u32 w, %1, 16; add.u32 y, %2, 256; mov.b64 b, {y, %3};\n"
       " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [w], b, %4, t;\n"
       " add.u32 w, %1, 24; add.u32 y, %2, 384; mov.b64 b, {y, %3};\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [w], b, %4, t;\n"
-      " add.u32 w, %1, 32; add.u32 y, %2, 512; mov.b64 b, {y, %3};\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [w], b, %4, t;\n"
-      " add.u32 w, %1, 40; add.u32 y, %2, 640; mov.b64 b, {y, %3};\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [w], b, %4, t;\n"
-      " add.u32 w, %1, 48; add.u32 y, %2, 768; mov.b64 b, {y, %3};\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [w], b, %4, t;\n"
-      " add.u32 w, %1, 56; add.u32 y, %2, 896; mov.b64 b, {y, %3};\n"
       " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [w], b, %4, t;\n"
       "}" ::"r"(d), "r"(a), "r"(b), "r"(kOperandHigh), "r"(inst), "r"(static_cast<uint32_t>(add))
       : "memory");

@@ -9,7 +9,8 @@
 // in, and is the second product's A operand there. The two halves take turns: while the softmax of one is at work, the other's
 // products run. Tensor memory holds S and O of both: all of its 512 columns.
 //
-// Order of the products: for each tile P_a V, Q_a K' of the next tile, P_b V, Q_b K'. A half's next scores are written over its
+// Order of the products: for each tile P_a V in two steps of 64 tokens, each as soon as its probabilities stand, Q_a K' of the
+// next tile, P_b V, Q_b K'. A half's next scores are written over its
 // probabilities; the tensor core takes products in the order in which one thread has issued them.
 //
 // Split: as in paged_attention.cu the units' tiles of 128 tokens, in order, are dealt in equal runs to the CTAs, one on
@@ -18,9 +19,9 @@
 // Roles (13 warps): 4 softmax warps to each half, a thread to a column; 4 copy keys and values (and the queries of
 // later units) with 16-byte asynchronous copies, two places each; one issues the products.
 //
-// A column's maximum is taken from a unit's first tile; later the probabilities are taken with the maximum in use, and where one
-// comes out above 2^8, that is moved and O scaled (a warp at a time, for its own 32 columns). Statistics and O are in fp32; P
-// is rounded to the input type for the second product (fp16: scaled by 2^7 first).
+// A column's maximum is taken from a unit's first 64 tokens; later the probabilities are taken with the maximum in use, and only
+// where their sum comes out too large is that moved and O scaled (a warp at a time, for its own 32 columns). Statistics and O
+// are in fp32; P is rounded to the input type for the second product (fp16: scaled by 2^7 first, sums of 64 below 2^15).
 #include <cfloat>
 
 #include "attention_forms.cuh"
@@ -38,6 +39,7 @@ using namespace ltk::umma;
 constexpr int kTile = 128;           // tokens
 constexpr int kChunk = kTile * 128;  // bytes of 64 dims
 constexpr int kPiece = 2 * kChunk;   // of a tile's keys or values: up to 128 dims
+constexpr int kStep = 64;            // tokens whose probabilities are handed over at a time
 constexpr int kHalf = 128;           // columns
 constexpr int kCols = 2 * kHalf;
 constexpr int kSoftmaxWarps = 8, kCopyWarps = 4, kCopyThreads = kCopyWarps * 32;
@@ -65,7 +67,10 @@ struct Smem {
   uint32_t seen[kSeenSlots][kCopyWarps];  // tokens of a tile that are there
   uint64_t key_full[2], key_empty[2], value_full[2], value_empty[2];
   uint64_t seen_full[2][kSeenSlots];  // for each half, by the tiles that it takes part in
-  uint64_t q_first, q_full, q_empty, s_full[2], p_full[2], o_done[2], all_done;
+  uint64_t q_first, q_full, q_empty, s_full[2], all_done;
+  // For each half and step, by the tiles that the half takes part in: a parity tells no phase from the second one before it, so
+  // the steps of a tile, which may both come before the first is waited for, have barriers of their own.
+  uint64_t p_full[2][2], o_done[2][2];
   int64_t scan[kThreads / 32];
   int64_t start_group, start_at, tiles, run_begin, run_end;
   uint32_t tmem, gave_up;
@@ -148,52 +153,34 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// The larger of two pairs of values of the input type, none of them negative.
-template <bool kBf16>
-__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
-  uint32_t r;
-  if constexpr (kBf16)
-    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  else
-    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
 template <bool kBf16>
 __device__ __forceinline__ float2 unpack2(uint32_t x) {
   if constexpr (kBf16) return __bfloat1622float2(reinterpret_cast<const __nv_bfloat162&>(x));
   else return __half22float2(reinterpret_cast<const __half2&>(x));
 }
 
-// A tile's probabilities of a column, packed; their sum in `sum`, and whether one is larger than `most`.
+// The probabilities of a column for half a tile's tokens, packed, and their sum. All scores are loaded at once: with a wait for
+// every 16 or 32 of them, each part's chain of latencies stands by itself (1700 cycles a tile against 1200).
 template <bool kBf16>
-__device__ __forceinline__ bool probabilities(uint32_t s_at, float scale2, float in_use, const uint32_t* seen, float most, uint32_t (&out)[kTile / 2],
-                                              float* sum) {
-  const bool all = (seen[0] & seen[1] & seen[2] & seen[3]) == ~0u;
+__device__ __forceinline__ float probabilities(uint32_t s_at, float scale2, float in_use, uint32_t seen0, uint32_t seen1, uint32_t (&out)[kStep / 2]) {
   const uint64_t scale = two(scale2, scale2), base = two(-in_use, -in_use);
-  uint64_t l = 0;
-  uint32_t top = 0;
+  float s[kStep];
+  tmem_load64(s_at, s);
+  if ((seen0 & seen1) != ~0u) {
 #pragma unroll
-  for (int c = 0; c < kTile; c += 32) {
-    float s[32];
-    tmem_load(s_at + c, s);
-    if (!all) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (!(seen[c / 32] >> i & 1)) s[i] = -INFINITY;
-    }
-#pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      const float2 x = apart(fma2(two(s[i], s[i + 1]), scale, base));
-      const float y = exp2_fast(x.x), z = exp2_fast(x.y);
-      l = add2(l, two(y, z));
-      out[(c + i) / 2] = pack2<kBf16>(y, z);
-      top = larger<kBf16>(top, out[(c + i) / 2]);
-    }
+    for (int i = 0; i < kStep; ++i)
+      if (!((i < 32 ? seen0 : seen1) >> (i & 31) & 1)) s[i] = -INFINITY;
   }
-  const float2 both = apart(l), tops = unpack2<kBf16>(top);
-  *sum = both.x + both.y;
-  return fmaxf(tops.x, tops.y) > most;
+  uint64_t l[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < kStep; i += 2) {
+    const float2 y = apart(fma2(two(s[i], s[i + 1]), scale, base));
+    const float u = exp2_fast(y.x), v = exp2_fast(y.y);
+    l[i / 2 & 3] = add2(l[i / 2 & 3], two(u, v));
+    out[i / 2] = pack2<kBf16>(u, v);
+  }
+  const float2 both = apart(add2(add2(l[0], l[1]), add2(l[2], l[3])));
+  return both.x + both.y;
 }
 
 template <bool kBf16>
@@ -212,8 +199,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
       mbar_init(smem_addr(&sm.value_empty[i]), 1);
       for (int j = 0; j < kSeenSlots; ++j) mbar_init(smem_addr(&sm.seen_full[i][j]), kCopyWarps);
       mbar_init(smem_addr(&sm.s_full[i]), 1);
-      mbar_init(smem_addr(&sm.p_full[i]), kSoftmaxWarps / 2);
-      mbar_init(smem_addr(&sm.o_done[i]), 1);
+      for (int j = 0; j < 2; ++j) {
+        mbar_init(smem_addr(&sm.p_full[i][j]), kSoftmaxWarps / 2);
+        mbar_init(smem_addr(&sm.o_done[i][j]), 1);
+      }
     }
     mbar_init(smem_addr(&sm.q_first), kSoftmaxWarps * 32);
     mbar_init(smem_addr(&sm.q_full), kCopyThreads);
@@ -295,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     for (; walk.left > 0; next_segment(p, walk), ++segment) {
       const SharedRun run = p.f.runs[walk.group];
       const int cols = run.rows * p.group;
-      const int32_t* pages = p.f.prefix_table + run.prefix * p.f.prefix_stride;
+      const int32_t* pages = p.f.prefixes.table + run.prefix * p.f.prefixes.stride;
       const auto place = [&](int t) { return t < walk.count ? (walk.at + t) * kTile + me : INT_MAX; };
       const auto page_of = [&](int x) { return x < run.length ? pages[block_column(p.R, x)] : 0; };
       int x = place(0), page = page_of(x);
@@ -344,9 +333,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
       multiply_keys(tmem + half * kTile, q_at + half * kPiece, key_at + (t & 1) * kPiece, p.a.dk, kKeys);
       commit(smem_addr(&sm.s_full[half]));
     };
-    const auto outputs = [&](int half, uint32_t t, bool add) {
-      mma16_held(tmem + kCols + half * kMaxDim, tmem + half * kTile, operand(value_at + (t & 1) * kPiece, kChunk), values, add);
-      commit(smem_addr(&sm.o_done[half]));
+    const auto outputs = [&](int half, uint32_t t, uint32_t turn, bool add) {
+#pragma unroll
+      for (int step = 0; step < 2; ++step) {
+        mbar_wait_warp(smem_addr(&sm.p_full[half][step]), turn & 1, guard);
+        fence_after();
+        mma16_held(tmem + kCols + half * kMaxDim, tmem + half * kTile + step * (kStep / 2), operand(value_at + (t & 1) * kPiece + step * kStep * 128, kChunk),
+                   values, add || step > 0);
+        commit(smem_addr(&sm.o_done[half][step]));
+      }
     };
     const auto keys_come = [&](uint32_t t) {
       mbar_wait_warp(smem_addr(&sm.key_full[t & 1]), (t >> 1) & 1, guard);
@@ -365,19 +360,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
 #pragma unroll 1
       for (int t = 0; t < walk.count; ++t, ++tile) {
         const bool more = t + 1 < walk.count;
-        mbar_wait_warp(smem_addr(&sm.p_full[0]), tile & 1, guard);
-        fence_after();
         mbar_wait_warp(smem_addr(&sm.value_full[tile & 1]), (tile >> 1) & 1, guard);
         fence_async();
-        outputs(0, tile, t > 0);
+        outputs(0, tile, tile, t > 0);
         if (more) {
           keys_come(tile + 1);
           scores(0, tile + 1);
         }
         if (both) {
-          mbar_wait_warp(smem_addr(&sm.p_full[1]), second & 1, guard);
-          fence_after();
-          outputs(1, tile, t > 0);
+          outputs(1, tile, second, t > 0);
           ++second;
         }
         commit(smem_addr(&sm.value_empty[tile & 1]));
@@ -393,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   } else {
     // ---- softmax and output ---------------------------------------------------
     constexpr float kShift = kBf16 ? 0.f : 7.f;  // fp16: probabilities use the upper half of its range, at most 2^15
-    constexpr float kMostProbability = kBf16 ? 256.f : 32768.f;  // 2^(kMoveAbove + kShift)
+    constexpr float kMostSum = kBf16 ? 1048576.f : 32768.f;  // of 64 probabilities, above which the maximum moves
     const int half = warp >> 2, column = tid;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + half * kTile, o_at = tmem + lanes + kCols + half * kMaxDim;
@@ -414,57 +405,58 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
       float m = -INFINITY, in_use = -FLT_MAX, l = 0.f;
       for (int t = 0; t < walk.count; ++t, ++tile, ++turn) {
         mbar_wait(smem_addr(&sm.seen_full[half][turn % kSeenSlots]), (turn / kSeenSlots) & 1, guard);
-        uint32_t seen[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) seen[i] = sm.seen[tile % kSeenSlots][i];
         mbar_wait_warp(smem_addr(&sm.s_full[half]), turn & 1, guard);
         fence_after();
-        uint32_t out[kTile / 2];
-        float sum = 0.f;
-        bool move_any = t == 0;
-        if (t > 0) move_any = __any_sync(~0u, probabilities<kBf16>(s_at, p.scale2, in_use, seen, kMostProbability, out, &sum));
-        if (move_any) {
-          float top = -INFINITY;
 #pragma unroll 1
-          for (int c = 0; c < kTile; c += 32) {
-            float s[32];
-            tmem_load(s_at + c, s);
-            const uint32_t who = c == 0 ? seen[0] : c == 32 ? seen[1] : c == 64 ? seen[2] : seen[3];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) top = fmaxf(top, who >> i & 1 ? s[i] : -INFINITY);
-          }
-          top *= p.scale2;
-          const bool move = top > m + kMoveAbove || (m == -INFINITY && top > m);
-          const bool rescale = __any_sync(~0u, move && m > -INFINITY);
-          const float factor = move && m > -INFINITY ? exp2_fast(m - top) : 1.f;
-          if (move) {
-            m = top;
-            in_use = m - kShift;
-          }
-          if (rescale) {
-            mbar_wait_warp(smem_addr(&sm.o_done[half]), (turn & 1) ^ 1, guard);  // the tile before has been added
-            fence_after();
-            l *= factor;
+        for (int step = 0; step < 2; ++step) {
+          const uint32_t from = s_at + step * kStep, seen0 = sm.seen[tile % kSeenSlots][step * 2], seen1 = sm.seen[tile % kSeenSlots][step * 2 + 1];
+          uint32_t out[kStep / 2];
+          float sum = 0.f;
+          // with the maximum in use, unless there is none yet or the probabilities come out too large: then that is moved first
+          for (bool move_first = t == 0 && step == 0;; move_first = true) {
+            if (move_first) {
+              float top = -INFINITY;
 #pragma unroll 1
-            for (int c = 0; c < p.v_cols; c += 16) {
-              float o[16];
-              tmem_load(o_at + c, o);
+              for (int c = 0; c < kStep; c += 16) {
+                float x[16];
+                tmem_load(from + c, x);
+                const uint32_t who = (c < 32 ? seen0 : seen1) >> (c & 16);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] *= factor;
-              tmem_store8(o_at + c, o);
-              tmem_store8(o_at + c + 8, o + 8);
+                for (int i = 0; i < 16; ++i) top = fmaxf(top, who >> i & 1 ? x[i] : -INFINITY);
+              }
+              top *= p.scale2;
+              const bool move = top > m, rescale = __any_sync(~0u, move && m > -INFINITY);
+              const float factor = move && m > -INFINITY ? exp2_fast(m - top) : 1.f;
+              if (move) {
+                m = top;
+                in_use = m - kShift;
+              }
+              if (rescale) {
+                mbar_wait_warp(smem_addr(&sm.o_done[half][step ^ 1]), (turn & 1) ^ (step ^ 1), guard);  // the step before has been added
+                fence_after();
+                l *= factor;
+#pragma unroll 1
+                for (int c = 0; c < p.v_cols; c += 16) {
+                  float o[16];
+                  tmem_load(o_at + c, o);
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) o[i] *= factor;
+                  tmem_store8(o_at + c, o);
+                  tmem_store8(o_at + c + 8, o + 8);
+                }
+                store_wait();
+              }
             }
-            store_wait();
+            sum = probabilities<kBf16>(from, p.scale2, in_use, seen0, seen1, out);
+            if (!__any_sync(~0u, !(sum <= kMostSum)) || move_first) break;
           }
-          probabilities<kBf16>(s_at, p.scale2, in_use, seen, kMostProbability, out, &sum);
+          l += sum;
+          tmem_store32(s_at + step * (kStep / 2), out);  // where scores stood that have been read
+          store_wait();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&sm.p_full[half][step]));
         }
-        l += sum;
-        tmem_store32(s_at, out);
-        tmem_store32(s_at + 32, out + 32);
-        store_wait();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&sm.p_full[half]));
       }
       // the whole unit, or a part of it
       const bool whole = walk.count == walk.tiles;
@@ -479,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         p.stat[slot * kCols + column] = make_float2(m == -INFINITY ? -INFINITY : in_use, l);
         p.tail[slot * kCols + column] = tail;
       }
-      mbar_wait_warp(smem_addr(&sm.o_done[half]), (turn & 1) ^ 1, guard);
+      mbar_wait_warp(smem_addr(&sm.o_done[half][1]), (turn & 1) ^ 1, guard);
       fence_after();
       uint16_t* out = static_cast<uint16_t*>(p.a.out) + (real ? (run.row0 + j) * p.a.out_row_stride + head * p.a.out_head_stride : 0);
 #pragma unroll 1
@@ -553,6 +545,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
   __shared__ float weight[kMaxParts][kJoinCols];
   __shared__ float4 sums[kJoinCols][kMaxDim / 4 + 1];
   __shared__ float of_tail[kJoinCols];
+  __shared__ float2 stats[kJoinWarps][kJoinCols];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int col0 = blockIdx.x % (kCols / kJoinCols) * kJoinCols, at_join = blockIdx.x / (kCols / kJoinCols);
   dependent_wait();
@@ -577,46 +570,77 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     if (is) place[at] = s * 2 + (tid == 0 ? jn.first_slot : 0);
   }
   __syncthreads();
-  // a column's maximum and sum, in the order of the parts; and each part's weight in the whole
-  if (warp == 0) {
+  // each column's maximum and sum: a warp's parts, then the warps' in order; and from them each part's weight in the whole
+  {
     const int col = col0 + lane;
     float m = -INFINITY, sum = 0.f;
-    for (int i = 0; i < parts; ++i) {
-      const float2 st = p.stat[place[i] * kCols + col];
+    constexpr int kAtOnce = 4;
+    for (int i0 = warp; i0 < parts; i0 += kAtOnce * kJoinWarps) {
+      float2 st[kAtOnce];
+#pragma unroll
+      for (int a = 0; a < kAtOnce; ++a) st[a] = p.stat[place[min(i0 + a * kJoinWarps, parts - 1)] * kCols + col];
+#pragma unroll
+      for (int a = 0; a < kAtOnce; ++a) {
+        const int i = i0 + a * kJoinWarps;
+        if (i >= parts) break;
+        weight[i][lane] = st[a].x;
+        const float top = fmaxf(m, st[a].x), b = top == -INFINITY ? 0.f : top;
+        sum = sum * exp2f(m - b) + st[a].y * exp2f(st[a].x - b);
+        m = top;
+      }
+    }
+    stats[warp][lane] = make_float2(m, sum);
+    const float tail = p.tail[place[0] * kCols + col];
+    __syncthreads();
+    m = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      const float2 st = stats[w][lane];
       const float top = fmaxf(m, st.x), b = top == -INFINITY ? 0.f : top;
       sum = sum * exp2f(m - b) + st.y * exp2f(st.x - b);
       m = top;
     }
-    const Weights both = weigh(sum == 0.f ? -INFINITY : m + log2f(sum), p.tail[place[0] * kCols + col]);
+    const Weights both = weigh(sum == 0.f ? -INFINITY : m + log2f(sum), tail);
     const float base = m == -INFINITY ? 0.f : m, factor = sum == 0.f ? 0.f : both.prefix / sum;
-    for (int i = 0; i < parts; ++i) weight[i][lane] = factor == 0.f ? 0.f : exp2f(p.stat[place[i] * kCols + col].x - base) * factor;
-    of_tail[lane] = both.tail;
-    if (col < cols) {
-      const int j = col / p.group;
-      p.a.lse[(run.row0 + j) * p.a.heads + jn.kv_head * p.group + col - j * p.group] = both.lse;
+    for (int i = warp; i < parts; i += kJoinWarps) weight[i][lane] = factor == 0.f ? 0.f : exp2f(weight[i][lane] - base) * factor;
+    if (warp == 0) {
+      of_tail[lane] = both.tail;
+      if (col < cols) {
+        const int j = col / p.group;
+        p.a.lse[(run.row0 + j) * p.a.heads + jn.kv_head * p.group + col - j * p.group] = both.lse;
+      }
     }
   }
   __syncthreads();
   const int quads = p.v_cols / 4;
-  for (int d = warp; d < quads; d += kJoinWarps) {
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float4* part = p.part + static_cast<int64_t>(d) * kCols + col0 + lane;
-    constexpr int kAtOnce = 8;
-    for (int i0 = 0; i0 < parts; i0 += kAtOnce) {
-      float4 y[kAtOnce];
+  {
+    constexpr int kAtOnce = 4, kQuads = kMaxDim / 4 / kJoinWarps;
+    float4 x[kQuads];
 #pragma unroll
-      for (int a = 0; a < kAtOnce; ++a) y[a] = load_now(part + static_cast<int64_t>(place[min(i0 + a, parts - 1)]) * quads * kCols);
+    for (int k = 0; k < kQuads; ++k) x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < parts; i0 += kAtOnce) {
+      float4 y[kAtOnce][kQuads];
+#pragma unroll
+      for (int a = 0; a < kAtOnce; ++a)
+#pragma unroll
+        for (int k = 0; k < kQuads; ++k)
+          y[a][k] = load_now(p.part + (static_cast<int64_t>(place[min(i0 + a, parts - 1)]) * quads + min(warp + k * kJoinWarps, quads - 1)) * kCols + col0 + lane);
 #pragma unroll
       for (int a = 0; a < kAtOnce; ++a) {
-        if (i0 + a >= parts) break;
-        const float w = weight[i0 + a][lane];
-        x.x += w * y[a].x;
-        x.y += w * y[a].y;
-        x.z += w * y[a].z;
-        x.w += w * y[a].w;
+        const float w = i0 + a < parts ? weight[i0 + a][lane] : 0.f;
+        if (w == 0.f) continue;  // nothing seen, whatever stands there
+#pragma unroll
+        for (int k = 0; k < kQuads; ++k) {
+          x[k].x += w * y[a][k].x;
+          x[k].y += w * y[a][k].y;
+          x[k].z += w * y[a][k].z;
+          x[k].w += w * y[a][k].w;
+        }
       }
     }
-    sums[lane][d] = x;
+#pragma unroll
+    for (int k = 0; k < kQuads; ++k)
+      if (warp + k * kJoinWarps < quads) sums[lane][warp + k * kJoinWarps] = x[k];
   }
   __syncthreads();
   // along the values: four a thread
@@ -666,7 +690,7 @@ int attend_wide(const topk_attention_args& a, const FormArgs& f, void* scratch, 
   p.group = a.heads / a.kv_heads;
   p.v_cols = (a.dv + 15) / 16 * 16;
   p.scale2 = a.scale * 1.4426950408889634f;
-  const int64_t most = a.rows.num_rows * a.kv_heads * ((f.prefix_most + kTile - 1) / kTile);
+  const int64_t most = a.rows.num_rows * a.kv_heads * ((f.prefixes.most + kTile - 1) / kTile);
   int64_t slices = props.num_sms < kMaxParts ? props.num_sms : kMaxParts;
   p.slices = static_cast<int32_t>(slices < most ? slices : most);
   char* w = static_cast<char*>(scratch);

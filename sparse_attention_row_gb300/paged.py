@@ -439,28 +439,32 @@ class PagedDecoder:
         return PageCaches(caches, b"".join([self._page_cache(t) for t in caches]))
 
     def _page_cache(self, t) -> bytes:
-        if t.dim() < 1 or t.get_device() != self.device or t.dim() > 1 and 0 in t.shape[1:]:
+        shape = t.shape
+        if not shape or t.get_device() != self.device:
             self._bad("a cache", t, "a [blocks, ...] tensor")
-        size, strides, shape = t.element_size(), t.stride(), t.shape
-        if t.is_contiguous():
-            run, loops = t.numel() // shape[0] if shape[0] else 1, []
-        else:
-            # the loops over a page, the inner ones first; those that follow one another in memory are one
-            run, loops = 1, []
-            for stride, n in sorted((stride, n) for stride, n in zip(strides[1:], shape[1:]) if n > 1):
-                if not loops and stride == run:
-                    run *= n
-                elif loops and stride == loops[-1][0] * loops[-1][1]:
-                    loops[-1][1] *= n
-                else:
-                    loops.append([stride, n])
-            ends = run
-            for stride, n in loops:
-                if stride < ends:
-                    self._bad("a cache", t, "a tensor whose elements do not overlap")
-                ends = stride * (n - 1) + ends
-            if len(loops) > 2 or (shape[0] > 1 and strides[0] == 0):
-                self._bad("a cache", t, "a tensor whose pages are at most two loops over runs of memory")
+        if t.is_contiguous() and shape[0] > 0:
+            run = t.numel() // shape[0] * t.element_size()
+            if run > 0:
+                return _CACHE.pack(t.data_ptr(), shape[0], run, 0, 0, 1, 1, run)
+        if 0 in shape[1:]:
+            self._bad("a cache", t, "a tensor whose pages hold something")
+        size, strides = t.element_size(), t.stride()
+        # the loops over a page, the inner ones first; those that follow one another in memory are one
+        run, loops = 1, []
+        for stride, n in sorted((stride, n) for stride, n in zip(strides[1:], shape[1:]) if n > 1):
+            if not loops and stride == run:
+                run *= n
+            elif loops and stride == loops[-1][0] * loops[-1][1]:
+                loops[-1][1] *= n
+            else:
+                loops.append([stride, n])
+        ends = run
+        for stride, n in loops:
+            if stride < ends:
+                self._bad("a cache", t, "a tensor whose elements do not overlap")
+            ends = stride * (n - 1) + ends
+        if len(loops) > 2 or (shape[0] > 1 and strides[0] == 0):
+            self._bad("a cache", t, "a tensor whose pages are at most two loops over runs of memory")
         (s0, n0), (s1, n1) = (loops[::-1] + [[0, 1], [0, 1]])[:2]
         return _CACHE.pack(t.data_ptr(), shape[0], strides[0] * size, s0 * size, s1 * size, n0, n1, run * size)
 

@@ -246,7 +246,7 @@ def test_caches_that_are_refused(dec, make):
 
 # ---- the sources -------------------------------------------------------------------------------------------------
 
-NEW = ["attention_forms.cuh", "block_attention.cu", "tail_attention.cu", "prefix_attention.cu", "shared_attention.cu", "block_scores.cu"]
+NEW = ["attention_forms.cuh", "block_attention.cu", "tail_attention.cu", "prefix_attention.cu", "whole_attention.cu", "shared_attention.cu", "wide_prefix.cu", "attention_parts.cuh", "block_scores.cu"]
 
 
 @pytest.mark.parametrize("name", NEW)

@@ -80,12 +80,32 @@ def want64(case, lengths, requests, dv, block, scale):
     return out, lse, tol * (2 + 2.0 ** -6 + room[..., None] * 2.0 ** -9), ltol + 2.0 ** -20 * (1 + room)
 
 
+READ_ALONE = 520e6  # bytes, up to which every row reads the prefix for itself: of the prefix's table's width, the only bound that the host knows
+
+
+def widened(table, rows, kv, dims, block):
+    """The prefixes' table with columns that no one uses, so that even few rows share what they begin with."""
+    columns = max(table.shape[1], int(READ_ALONE / (2 * rows * kv * dims * block)) + 2)
+    wide = torch.full((table.shape[0], columns), -7, dtype=torch.int32, device=table.device)
+    wide[:, :table.shape[1]] = table
+    return wide
+
+
+def tables(q, k, v, dv, prefix_table, block):
+    """Both ways through the call."""
+    yield prefix_table
+    if prefix_table.shape[0]:
+        yield widened(prefix_table, q.shape[0], k.shape[2], k.shape[3] + (0 if v is None else dv), block)
+
+
 def check(dec, case, prefixes, prefix_of, lengths, requests, dv, block, scale=None, allowed=0, **kw):
     q, k, v, hidden, whole, prefix_table = case
     c = lambda x: None if x is None else x.cuda()  # noqa: E731
-    out, lse = dec.shared_attention(c(q), c(k), c(hidden), ints(lengths), ints(prefix_of), ints(prefixes), c(prefix_table), v_cache=c(v), v_dim=dv, scale=scale, return_lse=True, **kw)
-    ok(dec, allowed)
-    pu.check_attention(out, lse, want64(case, lengths, requests, dv, block, q.shape[2] ** -0.5 if scale is None else scale), q.dtype)
+    want = want64(case, lengths, requests, dv, block, q.shape[2] ** -0.5 if scale is None else scale)
+    for table in tables(q, k, v, dv, prefix_table, block):
+        out, lse = dec.shared_attention(c(q), c(k), c(hidden), ints(lengths), ints(prefix_of), ints(prefixes), c(table), v_cache=c(v), v_dim=dv, scale=scale, return_lse=True, **kw)
+        ok(dec, allowed)
+        pu.check_attention(out, lse, want, q.dtype)
     return out, lse
 
 
@@ -170,10 +190,10 @@ def test_strided_views_and_outputs(dec):
     kk.copy_(k.cuda())
     vv.copy_(v.cuda())
     out = torch.full((3, 12, 64), 9.0).half().cuda()
-    wide_table, wide_prefix = torch.full((3, 40), -3, dtype=torch.int32, device="cuda"), torch.full((1, 9), -3, dtype=torch.int32, device="cuda")
+    wide_table, wide_prefix = torch.full((3, 40), -3, dtype=torch.int32, device="cuda"), torch.full((1, 20000), -3, dtype=torch.int32, device="cuda")
     wide_table[:, 5:5 + hidden.shape[1]], wide_prefix[:, 2:2 + prefix_table.shape[1]] = hidden.cuda(), prefix_table.cuda()
     lse = torch.empty(3, 6, device="cuda")
-    got, got_lse = dec.shared_attention(q.cuda(), kk, wide_table[:, 5:5 + hidden.shape[1]], ints(lengths), ints(prefix_of), ints([80]), wide_prefix[:, 2:2 + prefix_table.shape[1]],
+    got, got_lse = dec.shared_attention(q.cuda(), kk, wide_table[:, 5:5 + hidden.shape[1]], ints(lengths), ints(prefix_of), ints([80]), wide_prefix[:, 2:19000],
                                         v_cache=vv, out=out[:, 1::2, 8:56], lse=lse, return_lse=True)
     assert got_lse is lse
     pu.check_attention(got, lse, want64(case, lengths, requests, 48, 16, 64 ** -0.5), torch.float16)
@@ -188,23 +208,22 @@ def test_padding_rows_bad_prefixes_and_pages(dec):
     # a prefix that there is none of: the request is done by itself, and reported
     check(dec, case, [64], prefix_of, lengths, [0, 1, 2, 3], 64, 16, allowed=sar.TOPK_DEV_BAD_BLOCK)
     assert dec.status() == sar.TOPK_DEV_BAD_BLOCK
-    dec.reset()
-    # rows of no request, and one of a length that is cut to the table's width
-    out, lse = dec.shared_attention(q.cuda(), k.cuda(), hidden.cuda(), ints([100, 77, 2 ** 31 - 1, 50]), ints([0, 0, -1, 0]), ints([64]), prefix_table.cuda(), v_cache=v.cuda(),
-                                    row_request=ints([0, -1, 2, -4]), return_lse=True)
-    assert (out[1::2] == 0).all() and (lse[1::2] == -math.inf).all() and dec.status() == sar.TOPK_DEV_LENGTH_CLAMPED
-    dec.reset()
-    # a page of the prefix outside the cache is skipped
-    bad = prefix_table.clone()
-    bad[0, 2] = k.shape[0]
-    out, lse = dec.shared_attention(q.cuda(), k.cuda(), hidden.cuda(), ints(lengths), ints([0, 0, -1, 0]), ints([64]), bad.cuda(), v_cache=v.cuda(), return_lse=True)
-    keep = torch.tensor([t for t in range(100) if not 32 <= t < 48])
-    index = torch.stack([keep.int() if i != 2 else torch.cat([torch.arange(84), torch.arange(84, 84)]).int() for i in range(4)])
-    index[2] = torch.arange(84).int()
-    want = pu.attention64(q, k, v, 64, whole, lengths, [0, 1, 2, 3], 16, 64 ** -0.5, indices=index)
-    rows = [0, 1, 3]
-    pu.check_attention(out[rows], lse[rows], tuple(x[rows] * (2.1 if i == 2 else 1) + (1e-5 if i == 3 else 0) for i, x in enumerate(want)), torch.float16)
-    assert dec.status() == sar.TOPK_DEV_BAD_BLOCK
+    for table in tables(q, k, v, 64, prefix_table, 16):
+        dec.reset()
+        # rows of no request, and one of a length that is cut to the table's width
+        out, lse = dec.shared_attention(q.cuda(), k.cuda(), hidden.cuda(), ints([100, 77, 2 ** 31 - 1, 50]), ints([0, 0, -1, 0]), ints([64]), table.cuda(), v_cache=v.cuda(),
+                                        row_request=ints([0, -1, 2, -4]), return_lse=True)
+        assert (out[1::2] == 0).all() and (lse[1::2] == -math.inf).all() and dec.status() == sar.TOPK_DEV_LENGTH_CLAMPED
+        dec.reset()
+        # a page of the prefix outside the cache is skipped
+        bad = table.clone()
+        bad[0, 2] = k.shape[0]
+        out, lse = dec.shared_attention(q.cuda(), k.cuda(), hidden.cuda(), ints(lengths), ints([0, 0, -1, 0]), ints([64]), bad.cuda(), v_cache=v.cuda(), return_lse=True)
+        keep = torch.tensor([t for t in range(100) if not 32 <= t < 48], dtype=torch.int32)
+        want = pu.attention64(q, k, v, 64, whole, lengths, [0, 1, 2, 3], 16, 64 ** -0.5, indices=keep.expand(4, -1))
+        rows = [0, 1, 3]
+        pu.check_attention(out[rows], lse[rows], tuple(x[rows] * (2.1 if i == 2 else 1) + (1e-5 if i == 3 else 0) for i, x in enumerate(want)), torch.float16)
+        assert dec.status() == sar.TOPK_DEV_BAD_BLOCK
 
 
 def test_no_prefixes_and_no_rows(dec):
@@ -216,11 +235,14 @@ def test_no_prefixes_and_no_rows(dec):
     assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
 
 
-def test_the_same_every_time_on_a_stream_and_in_a_graph(dec):
+@pytest.mark.parametrize("wide", [False, True])
+def test_the_same_every_time_on_a_stream_and_in_a_graph(dec, wide):
     n = 30
     lengths, prefix_of = [700 + 13 * i for i in range(n)], [0] * 20 + [1] * 10
     case = make(10, [700, 300], prefix_of, lengths, list(range(n)), 16, 4, 128, 128, False, torch.bfloat16, 32)
     q, k, v, _, whole, prefix_table = (x.cuda() for x in case)
+    if wide:
+        prefix_table = widened(prefix_table, n, 4, 256, 32)
     ln, of, pl = ints(lengths), ints(prefix_of), ints([700, 300])
     call = lambda **kw: dec.shared_attention(q, k, whole, ln, of, pl, prefix_table, v_cache=v, return_lse=True, **kw)  # noqa: E731
     first = call()
@@ -253,7 +275,7 @@ def test_as_attention_of_every_request_by_itself(dec):
     lengths, prefix_of = [2100 + 50 * i for i in range(24)], [0] * 24
     case = make(11, [2100], prefix_of, lengths, list(range(24)), 32, 8, 128, 128, False, torch.bfloat16, 64)
     q, k, v, hidden, whole, prefix_table = (x.cuda() for x in case)
-    out, lse = dec.shared_attention(q, k, hidden, ints(lengths), ints(prefix_of), ints([2100]), prefix_table, v_cache=v, return_lse=True)
+    out, lse = dec.shared_attention(q, k, hidden, ints(lengths), ints(prefix_of), ints([2100]), widened(prefix_table, 24, 8, 256, 64), v_cache=v, return_lse=True)
     alone, alone_lse = dec.attention(q, k, whole, ints(lengths), v_cache=v, return_lse=True)
     # both round their probabilities and results: four half steps of bf16 of the mean |v|, which is below 2 here
     assert (out.double() - alone.double()).abs().max() <= 4 * 2.0 ** -8 * 2 and (lse - alone_lse).abs().max() <= 1e-4
@@ -310,11 +332,13 @@ def test_many_columns_and_pages_outside_the_cache(dec):
     q, k, v, hidden, whole, prefix_table = case
     bad = prefix_table.clone()
     bad[0, 3], bad[0, 17], bad[0, 29] = -1, k.shape[0], 2 ** 31 - 1
-    out, lse = dec.shared_attention(q.cuda(), k.cuda(), hidden.cuda(), ints(lengths), ints(prefix_of), ints([300]), bad.cuda(), v_cache=v.cuda(), return_lse=True)
     keep = torch.tensor([t for t in range(329) if t // 10 not in (3, 17, 29)], dtype=torch.int32)
     want = pu.attention64(q, k, v, 64, whole, lengths, list(range(n)), 10, 64 ** -0.5, indices=keep.expand(n, -1))
-    pu.check_attention(out, lse, (want[0], want[1], want[2] * 2.1, want[3] + 1e-5), torch.float16)
-    assert dec.status() == sar.TOPK_DEV_BAD_BLOCK
+    for table in tables(q, k, v, 64, bad, 10):
+        out, lse = dec.shared_attention(q.cuda(), k.cuda(), hidden.cuda(), ints(lengths), ints(prefix_of), ints([300]), table.cuda(), v_cache=v.cuda(), return_lse=True)
+        pu.check_attention(out, lse, (want[0], want[1], want[2] * 2.1, want[3] + 1e-5), torch.float16)
+        assert dec.status() == sar.TOPK_DEV_BAD_BLOCK
+        dec.reset()
 
 
 def test_many_columns_of_latent_and_wide_heads_and_drafted_tokens(dec):
