@@ -44,14 +44,32 @@ __device__ __forceinline__ int prefix_tokens(const Prefixes& p, const Rows& R, i
   return block_column(R, static_cast<int>(n < p.most ? n : p.most)) * R.block_size;
 }
 
-// The same for a row: 0 also where one of its request's rows, which read what follows together, sees less.
+// The same for a row: 0 also where one of its request's rows, which read what follows together, sees less. By a whole
+// warp, each lane with a row of its own (or past the last one): requests of many rows are looked through by all lanes.
 __device__ __forceinline__ int row_prefix_tokens(const Prefixes& p, const Rows& R, int64_t row, int32_t* prefix) {
-  const int64_t request = row_request(R, row);
-  const int n = prefix_tokens(p, R, request, prefix);
-  if (n == 0) return 0;
-  if (R.row_request) return seen_tokens(R, R.lengths[row], request) >= n ? n : 0;
-  for (int j = 0; j < R.next_n; ++j)
-    if (seen_tokens(R, R.lengths[request * R.next_n + j], request) < n) return 0;
+  const bool real = row >= 0 && row < R.num_rows;
+  const int64_t request = real ? row_request(R, row) : -1;
+  int n = prefix_tokens(p, R, request, prefix);
+  if (R.row_request) return n > 0 && seen_tokens(R, R.lengths[row], request) >= n ? n : 0;
+  constexpr int kFew = 4;
+  if (R.next_n <= kFew) {
+    for (int j = 0; j < R.next_n; ++j)
+      if (n > 0 && seen_tokens(R, R.lengths[request * R.next_n + j], request) < n) n = 0;
+    return n;
+  }
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+  for (unsigned todo = __ballot_sync(~0u, n > 0); todo;) {
+    const int first = __ffs(todo) - 1;
+    const int64_t which = __shfl_sync(~0u, request, first);
+    const int need = __shfl_sync(~0u, n, first);
+    bool less = false;
+    for (int j = lane; j < R.next_n; j += 32) less |= seen_tokens(R, R.lengths[which * R.next_n + j], which) < need;
+    less = __any_sync(~0u, less);
+    const bool mine = request == which;
+    if (mine && less) n = 0;
+    todo &= ~__ballot_sync(~0u, mine);
+  }
   return n;
 }
 

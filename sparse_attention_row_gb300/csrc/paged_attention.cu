@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<N, kLatent>) attention_k
       int prefix = 0;  // tokens that are found in the prefix's row of its table
       if constexpr (kForm == Form::kWhole) {
         int32_t which = 0;
-        if (length > 0) prefix = row_prefix_tokens(p.f.prefixes, p.R, row0, &which);
+        prefix = row_prefix_tokens(p.f.prefixes, p.R, row0, &which);
         pages = p.f.prefixes.table + static_cast<int64_t>(prefix > 0 ? which : 0) * p.f.prefixes.stride;
       }
       const int32_t* list = kForm == Form::kBlocks ? p.f.blocks + row0 * p.f.block_row_stride + walk.kv_head * p.f.block_head_stride

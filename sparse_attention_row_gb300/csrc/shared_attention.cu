@@ -40,7 +40,6 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
   dependent_launch();
   const auto key_of = [&](int64_t row) -> int64_t {
     int32_t prefix = -1;
-    if (row < 0 || row >= p.R.num_rows) return -1;
     const int n = row_prefix_tokens(p.prefixes, p.R, row, &prefix);
     return n == 0 ? -1 : static_cast<int64_t>(prefix) << 32 | n;
   };
@@ -52,8 +51,15 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
     const bool real = row < p.R.num_rows;
     const int64_t mine = key_of(row);
     key[tid + 1] = mine;
-    if (tid == 0) key[0] = key_of(row0 - 1);
-    if (tid == kThreads - 1) key[kThreads + 1] = key_of(row + 1);
+    // the neighbours' keys, by a warp each, as every key is found
+    if (warp == 0) {
+      const int64_t k = key_of(row0 - 1);
+      if (lane == 0) key[0] = k;
+    }
+    if (warp == kThreads / 32 - 1) {
+      const int64_t k = key_of(row0 + kThreads);
+      if (lane == 0) key[kThreads + 1] = k;
+    }
     if (real) {
       const int64_t request = row_request(p.R, row);
       const int32_t n = p.R.lengths[row];

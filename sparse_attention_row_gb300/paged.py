@@ -243,8 +243,8 @@ class PagedDecoder:
             *rows_args, kind, heads, dim, qp, q0, q1, wp, w0, kp, k0, k1, sp, s0, s1, op, o0, width, self._workspace_ptr), stream)
         return out
 
-    def _attend(self, q, k_cache, block_table, lengths, v_cache, v_dim, indices, scale, next_n, row_request, out, lse, return_lse, stream):
-        """Checks an attention call's tensors: (its packed arguments' values, out, lse)."""
+    def _attend(self, function, packer, more, q, k_cache, block_table, lengths, v_cache, v_dim, indices, scale, next_n, row_request, out, lse, return_lse, stream):
+        """Checks an attention call's tensors and makes the call, `more` being its arguments behind them: (out, lse)."""
         rows, heads, dk = q.shape
         dtype = q.dtype
         kind = self._dtypes.get(dtype)
@@ -282,8 +282,10 @@ class PagedDecoder:
         elif return_lse:
             lse = self._empty((rows, heads), self._f32, stream)
             lp = lse.data_ptr()
-        return (*rows_args, kind, heads, kv_heads, dk, v_dim, dk ** -0.5 if scale is None else scale, qp, q0, q1,
-                kp, k0, k1, k2, vp, v0, v1, v2, ip, i0, topk, op, o0, o1, lp, self._workspace_ptr, self.nbytes), out, lse
+        self._call(function, packer.pack(
+            *rows_args, kind, heads, kv_heads, dk, v_dim, dk ** -0.5 if scale is None else scale, qp, q0, q1,
+            kp, k0, k1, k2, vp, v0, v1, v2, ip, i0, topk, op, o0, o1, lp, self._workspace_ptr, self.nbytes, *more), stream)
+        return out, lse
 
     def attention(self, q, k_cache, block_table, lengths, v_cache=None, v_dim: int | None = None, indices=None,
                   scale: float | None = None, next_n: int | None = None, row_request=None, out=None, lse=None,
@@ -292,9 +294,8 @@ class PagedDecoder:
         the heads' dimension), over every token below each row's length or over ``indices``
         (int32 [rows, n], as the selection writes them). ``v_cache`` None: a token's value is the first
         ``v_dim`` elements of its key (latent attention). Returns out, or (out, lse)."""
-        args, out, lse = self._attend(q, k_cache, block_table, lengths, v_cache, v_dim, indices, scale, next_n, row_request, out, lse, return_lse, stream)
-        self._call(self._attention, _ATTENTION.pack(*args), stream)
-        return (out, lse) if return_lse else out
+        both = self._attend(self._attention, _ATTENTION, (), q, k_cache, block_table, lengths, v_cache, v_dim, indices, scale, next_n, row_request, out, lse, return_lse, stream)
+        return both if return_lse else both[0]
 
     # ---- blocks chosen by a cheap score ----
 
@@ -349,13 +350,13 @@ class PagedDecoder:
                         next_n: int | None = None, row_request=None, out=None, lse=None, return_lse: bool = False, stream=None):
         """``attention`` over the tokens of chosen blocks: ``blocks`` int32 [rows, kv_heads, n], a list for each key-value head, or
         [rows, n], one for all heads of a row; columns of the row's request in the table, -1 where there is none."""
-        args, out, lse = self._attend(q, k_cache, block_table, lengths, v_cache, v_dim, None, scale, next_n, row_request, out, lse, return_lse, stream)
-        rows, kv_heads = q.shape[0], args[12]
+        rows, kv_heads = q.shape[0], k_cache.shape[2] if k_cache.dim() == 4 else 1
         bp, strides = self._vectors("blocks", blocks, self._i32, blocks.dim() if blocks.dim() in (2, 3) else 3)
         if blocks.shape[0] != rows or (len(strides) == 3 and blocks.shape[1] != kv_heads):
             self._bad("blocks", blocks, f"a {(rows, kv_heads)} x n or {rows} x n tensor")
-        self._call(self._block_attention, _BLOCKS.pack(*args, bp, strides[0], strides[1] if len(strides) == 3 else 0, blocks.shape[-1]), stream)
-        return (out, lse) if return_lse else out
+        more = bp, strides[0], strides[1] if len(strides) == 3 else 0, blocks.shape[-1]
+        both = self._attend(self._block_attention, _BLOCKS, more, q, k_cache, block_table, lengths, v_cache, v_dim, None, scale, next_n, row_request, out, lse, return_lse, stream)
+        return both if return_lse else both[0]
 
     # ---- a prefix that requests share ----
 
@@ -366,7 +367,6 @@ class PagedDecoder:
         ``prefix_lens[prefix_of[b]]`` tokens of the pages in ``prefix_table[prefix_of[b]]`` (int32 [requests], negative: nothing shared;
         [prefixes]; [prefixes, columns]). Their whole pages are read once for all neighbouring rows that begin with them. Lengths count the
         prefix, and the rows of ``block_table`` have its pages' columns."""
-        args, out, lse = self._attend(q, k_cache, block_table, lengths, v_cache, v_dim, None, scale, next_n, row_request, out, lse, True, stream)
         prefixes = len(prefix_table)
         table, stride, columns = self._matrix("prefix_table", prefix_table, self._i32, prefixes)
         rows = q.shape[0]
@@ -374,10 +374,10 @@ class PagedDecoder:
         if need is None:
             need = self._scratch[rows] = _sar.topk_shared_attention_scratch_size(self.device, rows)
         scratch = self._empty(need, self._u8, stream)
-        self._call(self._shared_attention, _SHARED.pack(
-            *args, self._ints("prefix_of", prefix_of, len(block_table)), prefixes, self._ints("prefix_lens", prefix_lens, prefixes), table,
-            stride if prefixes > 1 or stride >= columns else columns, columns, scratch.data_ptr(), need), stream)
-        return (out, lse) if return_lse else out
+        more = (self._ints("prefix_of", prefix_of, len(block_table)), prefixes, self._ints("prefix_lens", prefix_lens, prefixes), table,
+                stride if prefixes > 1 or stride >= columns else columns, columns, scratch.data_ptr(), need)
+        both = self._attend(self._shared_attention, _SHARED, more, q, k_cache, block_table, lengths, v_cache, v_dim, None, scale, next_n, row_request, out, lse, True, stream)
+        return both if return_lse else both[0]
 
     # ---- the pages ----
 

@@ -392,3 +392,17 @@ def test_a_prompt_forked_decoded_freed_and_compacted(dec):
     release(list(range(rows)))
     assert int(taken) == 0 and sorted(free.tolist()) == list(range(pages)) and not shares.any() and (table == -1).all()
     ok(dec)
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(prompts=3, samples=9, tokens=700, heads=32, kv_heads=8, dim=128, block=64, topk=4), dict(prompts=1, samples=1, tokens=40, steps=1, heads=1, kv_heads=1, block=33),
+                                dict(prompts=4, samples=2, tokens=129, block=1, heads=6, kv_heads=3, topk=40)])
+def test_example_of_shared_prompts(dec, kw):
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "shared_prompts.py")
+    spec = importlib.util.spec_from_file_location("shared_prompts", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    # half steps of bf16 for the probabilities, the part behind the prefix and the result, of values below 5
+    assert example.run(**kw) < 3 * 2.0 ** -8 * 5

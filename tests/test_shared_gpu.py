@@ -149,6 +149,17 @@ def test_drafted_tokens(dec, next_n, latent):
     check(dec, by_row, [256, 128], prefix_of[:6] + [-1], lengths, requests, dv, 32, row_request=ints(requests))
 
 
+@pytest.mark.parametrize("next_n, heads, kv, dk, dv, latent", [(5, 4, 1, 64, 64, False), (40, 32, 4, 64, 64, False), (150, 16, 1, 576, 512, True), (33, 128, 1, 576, 512, True)])
+def test_many_rows_of_a_request(dec, next_n, heads, kv, dk, dv, latent):
+    # pieces of prompts behind a prefix; one row of the third request sees less than its prefix, and one of the last sees nothing
+    prefix_of, base = [0, 0, 0, -1, 1, 0], [100, 96, 100, 5, 64, 300]
+    lengths = [b + j for b in base for j in range(next_n)]
+    lengths[2 * next_n + next_n // 2], lengths[-1] = 95, 0
+    requests = [r // next_n for r in range(len(lengths))]
+    case = make(13, [100, 64], prefix_of, lengths, requests, heads, kv, dk, dv, latent, torch.bfloat16, 16)
+    check(dec, case, [100, 64], prefix_of, lengths, requests, dv, 16, next_n=next_n)
+
+
 def test_many_rows(dec):
     # more rows than are planned at a time, runs across that border, and more than one run for each prefix
     n = 2500
