@@ -17,8 +17,8 @@
 //
 //   many rows: tensor cores, which take the heads one by one, since a sum of them would not fit the input type: S [128 blocks x 128
 //   columns] = means . Q^T, a thread a block, which sums a row's heads up as it reads them from tensor memory. Bound by the chain of
-//   a tile's copy, product and sums, of which two or more CTAs on an SM overlap: 1024 rows of one request, 32 heads over 4, 32 K
-//   tokens take 21 us (41 by fused multiply-adds).
+//   a tile's copy, product and sums, which the CTAs on an SM overlap (three with one place for the means and 128 dims: 1024 rows
+//   of one request, 32 heads over 4, 32 K tokens take 18 us, 4096 rows 49; two with two places 21 and 56; fused multiply-adds 41).
 #include "attention_parts.cuh"
 #include "paged.cuh"
 #include "token_copies.cuh"
@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(kManyThreads) many_kernel(const __grid_constan
   extern __shared__ __align__(1024) uint8_t raw[];
   const topk_block_scores_args& a = p.a;
   const int chunks = (a.dk + 63) / 64, pieces = (chunks + 1) / 2;
-  const uint32_t q_at = (smem_addr(raw) + 1023) & ~1023u, means_at = q_at + chunks * kChunk, step_bytes = chunks * kChunk;
+  const uint32_t q_at = (smem_addr(raw) + 1023) & ~1023u, means_at = q_at + chunks * kChunk;
   __shared__ int32_t seen[kTile];
   __shared__ uint64_t done;
   __shared__ uint32_t tmem_at, gave_up;
@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(kManyThreads) many_kernel(const __grid_constan
   fence_after();
   const uint32_t tmem = tmem_at;
   constexpr uint32_t kFormat = kBf16 ? kBF16 : kF16;
-  uint32_t flags = 0, products = 0, buffer = 0;
+  uint32_t flags = 0, products = 0;
   int64_t skip = share.skip, left = share.left;
   TokenCopies copies(warp * 32, lane);
   for (int64_t tile = share.tile; left > 0; ++tile) {
@@ -561,23 +561,15 @@ __global__ void __launch_bounds__(kManyThreads) many_kernel(const __grid_constan
         const auto page_of = [&](int step) { return step < first + count && step * kTile + tid < most ? table[step * kTile + tid] : -1; };
         int32_t page = page_of(first), next_page = page_of(first + 1);
         asm volatile("" ::"r"(page), "r"(next_page) : "memory");  // before the copies: a load waits behind those
-        bool in = copy_means(first, means_at + buffer * step_bytes, page);
+        bool in = copy_means(first, means_at, page);
         for (int step = first; step < first + count; ++step) {
           const bool more = step + 1 < first + count;
-          bool next_in = false;
-          if (more) {
-            page = next_page;
-            next_page = page_of(step + 2);
-            next_in = copy_means(step + 1, means_at + (buffer ^ 1) * step_bytes, page);
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-          } else {
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-          }
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
           fence_async();
           __syncthreads();
           if (warp == 0) {
             fence_after();
-            uint32_t k = means_at + buffer * step_bytes, q = q_at;
+            uint32_t k = means_at, q = q_at;
             int dims = a.dk;
             bool add = false;
 #pragma unroll 1
@@ -615,8 +607,11 @@ __global__ void __launch_bounds__(kManyThreads) many_kernel(const __grid_constan
           }
           fence_before();
           __syncthreads();  // the sums have been read, and the means' place may be filled again
-          in = next_in;
-          buffer ^= 1;
+          if (more) {
+            page = next_page;
+            next_page = page_of(step + 2);
+            in = copy_means(step + 1, means_at, page);
+          }
         }
       }
     }
@@ -634,7 +629,7 @@ template <int kGroup, bool kBf16>
 int launch_many(ScoreParams& p, int device, const topk_device_props& props, cudaStream_t stream) {
   static int granted[kMaxDevices];
   const topk_block_scores_args& a = p.a;
-  const size_t smem = 3 * ((a.dk + 63) / 64) * static_cast<size_t>(kChunk) + 1024;
+  const size_t smem = 2 * ((a.dk + 63) / 64) * static_cast<size_t>(kChunk) + 1024;
   const int rc = allow_smem(many_kernel<kGroup, kBf16>, 3 * (kManyDk / 64) * static_cast<size_t>(kChunk) + 1024, device, granted);
   if (rc != TOPK_OK) return rc;
   const int64_t columns = a.rows.max_blocks < a.max_columns ? a.rows.max_blocks : a.max_columns;
