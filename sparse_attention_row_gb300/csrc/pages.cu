@@ -594,32 +594,34 @@ struct CopyParams {
   Cache cache[kCaches];
 };
 
-// One piece of each of kAtOnce places of a page; T has the piece's size.
-template <typename T>
-__device__ __forceinline__ void copy_chunk(const Cache& c, int64_t source, int64_t target, uint32_t x0) {
-  const char* from = c.base + source * c.block_stride;
-  char* to = c.base + target * c.block_stride;
+// One piece of each of kAtOnce places of a page, on which both pages agree; T has the piece's size. Places of pages that are one run
+// are told apart from the others once, not piece by piece.
+template <typename T, bool kOneRun>
+__device__ __forceinline__ void copy_pieces(const Cache& c, const char* from, char* to, uint32_t x0) {
+  const auto place = [&](uint32_t x) -> int64_t {
+    if (kOneRun) return static_cast<int64_t>(x) * sizeof(T);
+    const uint32_t run = x / c.run_pieces, n0 = run / c.n1;
+    return n0 * c.stride0 + (run - n0 * c.n1) * c.stride1 + static_cast<int64_t>(x - run * c.run_pieces) * sizeof(T);
+  };
   T v[kAtOnce];
-  int64_t at[kAtOnce];
-#pragma unroll
-  for (int i = 0; i < kAtOnce; ++i) {
-    const uint32_t x = x0 + i * kCopyThreads;
-    if (x >= c.pieces) continue;
-    if (c.run_pieces == c.pieces) {
-      at[i] = static_cast<int64_t>(x) * sizeof(T);
-    } else {
-      const uint32_t run = x / c.run_pieces, n0 = run / c.n1;
-      at[i] = n0 * c.stride0 + (run - n0 * c.n1) * c.stride1 + static_cast<int64_t>(x - run * c.run_pieces) * sizeof(T);
-    }
-    v[i] = *reinterpret_cast<const T*>(from + at[i]);
-  }
 #pragma unroll
   for (int i = 0; i < kAtOnce; ++i)
-    if (x0 + i * kCopyThreads < c.pieces) *reinterpret_cast<T*>(to + at[i]) = v[i];
+    if (x0 + i * kCopyThreads < c.pieces) v[i] = *reinterpret_cast<const T*>(from + place(x0 + i * kCopyThreads));
+#pragma unroll
+  for (int i = 0; i < kAtOnce; ++i)
+    if (x0 + i * kCopyThreads < c.pieces) *reinterpret_cast<T*>(to + place(x0 + i * kCopyThreads)) = v[i];
+}
+
+template <typename T>
+__device__ __forceinline__ void copy_chunk(const Cache& c, const char* from, char* to, uint32_t x0) {
+  if (c.run_pieces == c.pieces)
+    copy_pieces<T, true>(c, from, to, x0);
+  else
+    copy_pieces<T, false>(c, from, to, x0);
 }
 
 template <int kCaches>
-__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyParams<kCaches> p) {
+__global__ void __launch_bounds__(kCopyThreads, 4) copy_kernel(const __grid_constant__ CopyParams<kCaches> p) {
   dependent_wait();
   dependent_launch();
   uint32_t flags = 0;
@@ -637,12 +639,14 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
       continue;
     }
     const uint32_t x0 = (chunk - c.first) * (kCopyThreads * kAtOnce) + threadIdx.x;
+    const char* from = c.base + source * c.block_stride;
+    char* to = c.base + target * c.block_stride;
     switch (c.shift) {
-      case 4: copy_chunk<uint4>(c, source, target, x0); break;
-      case 3: copy_chunk<uint2>(c, source, target, x0); break;
-      case 2: copy_chunk<uint32_t>(c, source, target, x0); break;
-      case 1: copy_chunk<uint16_t>(c, source, target, x0); break;
-      default: copy_chunk<uint8_t>(c, source, target, x0);
+      case 4: copy_chunk<uint4>(c, from, to, x0); break;
+      case 3: copy_chunk<uint2>(c, from, to, x0); break;
+      case 2: copy_chunk<uint32_t>(c, from, to, x0); break;
+      case 1: copy_chunk<uint16_t>(c, from, to, x0); break;
+      default: copy_chunk<uint8_t>(c, from, to, x0);
     }
   }
   if (flags && threadIdx.x == 0) atomicOr(p.status, flags);
