@@ -84,7 +84,7 @@ struct Walk {
   __device__ void size() { count = static_cast<int>(min(static_cast<int64_t>(tiles - at), left)); }
 };
 
-__device__ __forceinline__ int run_tiles(const Params& p, int64_t g) { return (p.f.runs[g].length + kTile - 1) / kTile; }
+__device__ __forceinline__ int run_tiles(const Params& p, int64_t g) { return static_cast<int>((p.f.runs[g].length + (kTile - 1u)) / kTile); }
 
 __device__ __forceinline__ void next_segment(const Params& p, Walk& w) {
   w.left -= w.count;
