@@ -162,11 +162,18 @@ __device__ __forceinline__ uint32_t cluster_ctas() {
   return n;
 }
 
-// All threads of the cluster meet; what they wrote before is seen behind it.
-__device__ __forceinline__ void cluster_sync() {
+// All threads of the cluster meet; what they wrote before is seen behind it. In one step, or in two with other work between them.
+__device__ __forceinline__ void cluster_arrive() {
   __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  cluster_arrive();
+  cluster_wait();
 }
 
 __device__ __forceinline__ int32_t read_peer(const int32_t* mine, uint32_t rank) {
@@ -380,16 +387,42 @@ __device__ __forceinline__ bool is_named(int32_t m) { return (m & kNamed) != 0; 
 __device__ __forceinline__ bool is_free_after(int32_t m) { return m == kFree || m < 0; }
 __device__ __forceinline__ int32_t ones(const bool (&hit)[4]) { return hit[0] + hit[1] + hit[2] + hit[3]; }
 
+// The counts of all CTAs of the cluster, summed up: first[r] of those before CTA r, first[ctas] of all. Every thread calls it, after
+// the cluster has met.
+__device__ __forceinline__ void gather_counts(const int32_t* mine, int32_t (&first)[kCluster + 1]) {
+  const int tid = threadIdx.x;
+  if (tid < 32) {
+    const int32_t x = tid < static_cast<int>(cluster_ctas()) ? read_peer(mine, tid) : 0;
+    int32_t sum = x;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int32_t y = __shfl_up_sync(~0u, sum, d);
+      if (tid >= d) sum += y;
+    }
+    if (tid <= kCluster) first[tid] = sum - x;
+  }
+  __syncthreads();
+}
+
+// The CTA that has the i-th of what is counted.
+__device__ __forceinline__ int holder(const int32_t (&first)[kCluster + 1], int64_t i) {
+  int r = 0;
+#pragma unroll
+  for (int step = kCluster / 2; step > 0; step >>= 1)
+    if (first[r + step] <= i) r += step;
+  return r;
+}
+
 __global__ void __launch_bounds__(kPageThreads, 1) compact_kernel(const __grid_constant__ CompactParams p) {
   __shared__ int2 warp_sum[kPageWarps];
-  __shared__ int32_t mine[3];
+  __shared__ int32_t mine[3], free_first[kCluster + 1], named_first[kCluster + 1], left_first[kCluster + 1];
   const topk_page_compact_args& a = p.a;
   const topk_page_pool& t = a.pool;
   const int tid = threadIdx.x;
   const int64_t rank = cluster_rank(), all_threads = cluster_ctas() * kPageThreads, me = rank * kPageThreads + tid;
   const int64_t padded = (t.num_blocks + 3) / 4 * 4;  // marks are read four at a time; those past the last page are kNothing
   int32_t* mark = static_cast<int32_t*>(a.scratch);
-  int32_t *low = mark + padded, *high = low + t.num_blocks;
+  int32_t *low = mark + padded, *high = low + t.num_blocks;  // each CTA's free and named pages, from its first page's place on
   uint32_t flags = 0;
   dependent_wait();
   dependent_launch();
@@ -402,58 +435,56 @@ __global__ void __launch_bounds__(kPageThreads, 1) compact_kernel(const __grid_c
   for (int64_t e = me; e < entries; e += all_threads) {
     const uint32_t r = static_cast<uint32_t>(e) / columns, c = static_cast<uint32_t>(e) - r * columns;
     const int32_t page = t.block_table[r * t.table_stride + c];
-    if (page >= 0 && page < t.num_blocks) mark[page] = kNamed;
+    if (page >= 0 && page < t.num_blocks) atomicOr(mark + page, static_cast<int32_t>(kNamed));
     if (page >= t.num_blocks) flags |= TOPK_DEV_BAD_BLOCK;
   }
-  cluster_sync();
 #pragma unroll 4
   for (int64_t f = taken + me; f < t.num_free; f += all_threads) {
     const int32_t page = t.free_blocks[f];
-    if (page < 0 || page >= t.num_blocks || atomicOr(mark + page, static_cast<int32_t>(kFree)) != kNothing) flags |= TOPK_DEV_BAD_BLOCK;
+    if (page < 0 || page >= t.num_blocks || (atomicOr(mark + page, static_cast<int32_t>(kFree)) & kFree)) flags |= TOPK_DEV_BAD_BLOCK;
   }
   cluster_sync();
   // this CTA's pages
   const int64_t per = (padded / 4 + cluster_ctas() - 1) / cluster_ctas() * 4, b0 = min(per * rank, padded), b1 = min(b0 + per, padded);
   const auto marks = [&](int64_t x) { return x + tid * 4 < b1 ? look4(mark + x + tid * 4) : make_int4(kNothing, kNothing, kNothing, kNothing); };
-  int32_t free_count = 0, named_count = 0;
+  int64_t free_here = b0, named_here = b0;
   for (int64_t x = b0; x < b1; x += kPages) {
     const int4 m = marks(x);
-    bool hit[4];
-    count4(m, is_free_now, hit);
-    free_count += ones(hit);
-    count4(m, is_named, hit);
-    named_count += ones(hit);
-  }
-  const Counts sums = count_before(free_count, named_count, warp_sum);
-  if (tid == 0) {
-    mine[0] = sums.all_a;
-    mine[1] = sums.all_b;
-  }
-  cluster_sync();
-  int64_t free_before, free_all, named_before, named_all;
-  sum_of_cluster(&mine[0], &free_before, &free_all);
-  sum_of_cluster(&mine[1], &named_before, &named_all);
-  for (int64_t x = b0; x < b1; x += kPages) {
-    const int4 m = marks(x);
+    if (m.x == kBoth || m.y == kBoth || m.z == kBoth || m.w == kBoth) flags |= TOPK_DEV_BAD_BLOCK;
     bool is_free[4], named[4];
     count4(m, is_free_now, is_free);
     count4(m, is_named, named);
     const Counts here = count_before(ones(is_free), ones(named), warp_sum);
-    int64_t at = free_before + here.a, from_top = named_all - 1 - (named_before + here.b);
+    int64_t at_free = free_here + here.a, at_named = named_here + here.b;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int32_t b = static_cast<int32_t>(x + tid * 4 + k);
-      if (is_free[k]) low[at++] = b;
-      if (named[k]) high[from_top--] = b;
+      if (is_free[k]) low[at_free++] = b;
+      if (named[k]) high[at_named++] = b;
     }
-    free_before += here.all_a;
-    named_before += here.all_b;
+    free_here += here.all_a;
+    named_here += here.all_b;
+  }
+  if (tid == 0) {
+    mine[0] = static_cast<int32_t>(free_here - b0);
+    mine[1] = static_cast<int32_t>(named_here - b0);
   }
   cluster_sync();
-  const int64_t pairs = min(free_all, named_all);
+  gather_counts(&mine[0], free_first);
+  gather_counts(&mine[1], named_first);
+  const int64_t free_all = free_first[kCluster], named_all = named_first[kCluster], pairs = min(free_all, named_all);
+  // the i-th free page from below, and the i-th named one from above
+  const auto free_at = [&](int64_t i) {
+    const int r = holder(free_first, i);
+    return look(low + min(per * r, padded) + (i - free_first[r]));
+  };
+  const auto named_at = [&](int64_t i) {
+    const int r = holder(named_first, named_all - 1 - i);
+    return look(high + min(per * r, padded) + (named_all - 1 - i - named_first[r]));
+  };
 #pragma unroll 2
   for (int64_t i = me; i < a.max_copies; i += all_threads) {
-    const int32_t from = i < pairs ? look(high + i) : -1, to = i < pairs ? look(low + i) : -1;
+    const int32_t from = i < pairs ? named_at(i) : -1, to = i < pairs ? free_at(i) : -1;
     const bool moves = to < from;
     const int32_t source = moves ? from : -1, target = moves ? to : -1;
     a.source[i] = source;
@@ -467,16 +498,7 @@ __global__ void __launch_bounds__(kPageThreads, 1) compact_kernel(const __grid_c
     }
   }
   cluster_sync();
-#pragma unroll 4
-  for (int64_t e = me; e < entries; e += all_threads) {
-    const uint32_t r = static_cast<uint32_t>(e) / columns, c = static_cast<uint32_t>(e) - r * columns;
-    int32_t page = t.block_table[r * t.table_stride + c];
-    if (page >= 0 && page < t.num_blocks) {
-      const int32_t m = look(mark + page);
-      if (m < 0) page = ~m;
-    }
-    a.block_table_out[r * a.table_out_stride + c] = page;
-  }
+  // the free pages that each CTA has now, while the table is rewritten
   int32_t count = 0;
   for (int64_t x = b0; x < b1; x += kPages) {
     const int4 m = marks(x);
@@ -494,10 +516,21 @@ __global__ void __launch_bounds__(kPageThreads, 1) compact_kernel(const __grid_c
   }
   const Counts left = count_before(count, 0, warp_sum);
   if (tid == 0) mine[2] = left.all_a;
-  cluster_sync();
-  int64_t before, all;
-  sum_of_cluster(&mine[2], &before, &all);
-  const int64_t taken_out = t.num_free - all;  // the list holds every free page once, so there are no more than it has places
+  cluster_arrive();
+#pragma unroll 4
+  for (int64_t e = me; e < entries; e += all_threads) {
+    const uint32_t r = static_cast<uint32_t>(e) / columns, c = static_cast<uint32_t>(e) - r * columns;
+    int32_t page = t.block_table[r * t.table_stride + c];
+    if (page >= 0 && page < t.num_blocks) {
+      const int32_t m = look(mark + page);
+      if (m < 0) page = ~m;
+    }
+    a.block_table_out[r * a.table_out_stride + c] = page;
+  }
+  cluster_wait();
+  gather_counts(&mine[2], left_first);
+  const int64_t taken_out = t.num_free - left_first[kCluster];  // the list holds every free page once, so there are no more than it has places
+  int64_t before = left_first[rank];
   for (int64_t x = b0; x < b1; x += kPages) {
     const int4 m = marks(x);
     bool hit[4];
@@ -512,7 +545,7 @@ __global__ void __launch_bounds__(kPageThreads, 1) compact_kernel(const __grid_c
   if (a.free_blocks_out != t.free_blocks)
     for (int64_t f = me; f < taken_out; f += all_threads) a.free_blocks_out[f] = t.free_blocks[f];
   if (flags) atomicOr(p.status, flags);
-  cluster_sync();  // no CTA leaves before its sums are read
+  cluster_sync();  // no CTA leaves before its sums are read, and `taken` has been read by all
   if (me == 0) *a.taken_out = static_cast<int32_t>(taken_out);
 }
 

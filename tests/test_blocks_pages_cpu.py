@@ -257,7 +257,7 @@ def test_kernels_use_the_wrappers(name):
 def test_the_clusters_barrier_brings_the_warp_together_first():
     text = source.source("pages.cu")
     bodies = [b for b in source.functions(text).values() if source.ALIGNED.search(b)]
-    assert len(bodies) == 1 and bodies[0].strip().startswith("__syncwarp();") and len(source.ALIGNED.findall(text)) == 2
+    assert len(bodies) == 2 and all(b.strip().startswith("__syncwarp();") for b in bodies) and len(source.ALIGNED.findall(text)) == 2
 
 
 @pytest.mark.parametrize("name", NEW + ["pages.cu"])
