@@ -66,9 +66,10 @@ typedef enum {
  * so this launch wrote rows of -1 instead of merging through them. Every such
  * launch does the same until topk_workspace_init clears the workspace. */
 #define TOPK_DEV_WORKSPACE_DIRTY 0x8u
-/* The paged calls (topk_kv_map, topk_index_logits, topk_paged_attention). */
-#define TOPK_DEV_BLOCKS_EXHAUSTED 0x10u /* topk_kv_map: free_blocks ran out; the tokens concerned got slot -1 */
-#define TOPK_DEV_TABLE_FULL 0x20u       /* topk_kv_map: a request outgrew its row of the table; slot -1 */
+/* The paged calls (topk_kv_map and those after it). */
+#define TOPK_DEV_BLOCKS_EXHAUSTED 0x10u /* topk_kv_map: free_blocks ran out; the tokens concerned got slot -1. topk_page_fork: the child
+                                         * got no page; topk_page_free: more pages came back than the list has room for */
+#define TOPK_DEV_TABLE_FULL 0x20u       /* topk_kv_map: a request outgrew its row of the table; slot -1. topk_block_means: likewise */
 #define TOPK_DEV_TOKENS_DROPPED 0x40u   /* topk_kv_map: more new tokens than max_tokens; the rest got no block and are not listed */
 #define TOPK_DEV_BAD_BLOCK 0x80u        /* a valid token's block, or a row's request, lies outside the cache or the table;
                                          * topk_kv_map: a new token's page is a negative one, as after a step without
@@ -650,7 +651,8 @@ int topk_page_free(const topk_page_free_args* args, void* stream);
  * Compacts the pool: pages that the table names move to lower numbers. The highest of them takes the place of the lowest free
  * page, the second highest that of the second lowest, and so on, while that lowers a number and `max_copies` moves
  * are not yet made. Lists the moves, whose contents topk_page_copy then brings over; writes the table and the shares
- * with the pages' new numbers, and the free pages in rising order to free_blocks[taken ..). Pages that
+ * with the pages' new numbers, and the free pages in rising order to free_blocks[taken ..). Every holder of a page that
+ * may move has to be a row of this table: other tables (prefixes', for one) are not renamed. Pages that
  * neither the table nor the list names stay where they are. A free page that the table names as well is taken off
  * the list, one that is listed twice, or is none of the pool, likewise (TOPK_DEV_BAD_BLOCK; taken rises). Outputs may be the inputs themselves;
  * entries free_blocks_out[0 .. taken_out) are copied from free_blocks.

@@ -14,7 +14,9 @@
 //   copy     every cache's pages in pieces of 16 KB over all CTAs, 16 bytes a thread and four loads at a time: bound by HBM.
 //
 // Free and compact are one cluster of 16 CTAs, whose barrier in hardware takes the place of further launches. They are bound by
-// latency up to some 100 000 entries of the table (a step is 1 to 2 us) and by 16 SMs' loads and atomics above.
+// latency (a step is 1 to 2 us) up to some 10 000 entries of the table and by 16 SMs' loads and atomics above: freeing 256 requests
+// of about 64 pages, most of them shared, takes 15 us (22 with 8 CTAs); compacting 18 K pages with 16 K entries 15 us (17), 1.1 M pages with
+// 1 M entries 169 us. The copy of 1024 pages of 32 KB takes 8 us.
 #include "paged.cuh"
 
 namespace ltk {
@@ -588,8 +590,8 @@ int cluster_size(void (*kernel)(Args), int* known) {
 }
 
 template <typename Args>
-int launch_cluster(void (*kernel)(Args), const Args& args, bool large, int* known, cudaStream_t stream) {
-  const int ctas = large ? cluster_size(kernel, known) : 8;
+int launch_cluster(void (*kernel)(Args), const Args& args, int* known, cudaStream_t stream) {
+  const int ctas = cluster_size(kernel, known);
   if (ctas == 0) return TOPK_ERR_CUDA;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = cluster_config(kernel, ctas, attr);
@@ -752,7 +754,7 @@ extern "C" int topk_page_free(const topk_page_free_args* args, void* stream) {
   p.a = a;
   p.status = static_cast<uint32_t*>(a.pool.workspace);
   static int known[kMaxDevices];
-  return launch_cluster(free_kernel, static_cast<const FreeParams&>(p), true, known, static_cast<cudaStream_t>(stream));
+  return launch_cluster(free_kernel, static_cast<const FreeParams&>(p), known, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int topk_page_compact(const topk_page_compact_args* args, void* stream) {
@@ -774,9 +776,7 @@ extern "C" int topk_page_compact(const topk_page_compact_args* args, void* strea
   p.a = a;
   p.status = static_cast<uint32_t*>(t.workspace);
   static int known[kMaxDevices];
-  // (18 K pages, 16 K entries: 21 us with 8 CTAs, 23 with 16, whose barriers take longer)
-  const bool large = t.num_blocks + t.num_requests * t.max_blocks > (1 << 18);
-  return launch_cluster(compact_kernel, static_cast<const CompactParams&>(p), large, known, static_cast<cudaStream_t>(stream));
+  return launch_cluster(compact_kernel, static_cast<const CompactParams&>(p), known, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int topk_page_copy(const topk_page_copy_args* args, void* stream) {

@@ -412,7 +412,8 @@ class PagedDecoder:
     def compact_pages(self, block_table, shares, free_blocks, taken, max_copies: int, table_out=None, shares_out=None, free_out=None,
                       taken_out=None, out: PageCopies | None = None, stream=None) -> PageCopies:
         """Moves the highest pages that the table names to the lowest free numbers, ``max_copies`` of them at most, and sorts the free
-        ones. In place, or into the tensors that are given. Returns the moves; ``copy_pages`` brings the contents over."""
+        ones. In place, or into the tensors that are given; tables made from this one (prefixes') are not renamed. Returns the moves;
+        ``copy_pages`` brings the contents over."""
         pool = self._pool(block_table, shares, free_blocks, taken)
         requests, columns, blocks, free = pool[1], pool[3], pool[5], pool[7]
         table, stride = pool[0], pool[2]
