@@ -119,7 +119,10 @@ inline int check_attention(const topk_attention_args& a) {
 }
 
 // Columns (rows and heads) of a unit at most, where rows share a prefix: kWideCols in wide_prefix.cu, which takes keys and values
-// of up to 128 dims that are not one, kSharedCols in the kernel of all forms.
+// of up to 128 dims that are not one, kSharedCols in the kernel of all forms. Past kSharedCols that one reads a prefix more than once,
+// and the wide one is the faster: 32 heads over 8, a prefix of 16 K tokens, in us wide against narrow: 72 columns 43, 50; 256 58, 78;
+// 512 85, 112; of 64 dims 96 columns 41, 51. Few units bring them closer: 16 heads over 2, 32 K tokens: 80 columns 41, 42; 256 47, 47;
+// 512 52, 63; over one 256 47, 42.
 constexpr int kSharedCols = 64, kWideCols = 256;
 
 int attend_wide(const topk_attention_args& a, const FormArgs& f, void* scratch, void* stream);

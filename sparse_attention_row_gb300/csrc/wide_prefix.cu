@@ -61,6 +61,7 @@ struct Params {
   float2* stat;    // [slices][2][kCols]: maximum (in powers of two) and sum
   float* tail;     // [slices][2][kCols]: the logarithm of the sum behind the prefix
   Join* join;      // [slices]
+  int32_t join_lanes;  // of the join's CTAs, which take the slices in turn
 };
 
 struct Smem {
@@ -533,29 +534,32 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   if (warp == kMmaWarp) tmem_free(tmem, 512);
 }
 
-// Joins the parts of the units that fell into several slices: 32 columns of a unit a CTA, lanes along the columns, four values a
-// thread at a time.
+// Joins the parts of the units that fell into several slices: 32 columns of a unit and some of its values a CTA, lanes along the
+// columns, four values a thread at a time. Where units are few and have many parts, kSplit CTAs share the values of 32 columns, and the
+// warps that are then left the parts; and a few CTAs look for the units among all slices. (The call of 32 rows, 16 heads over 2 and a prefix
+// of 32 K tokens, two units in 76 parts each: 47 us, 56 joined the other way. Of 64 rows, 32 heads over 8, 16 K tokens, eight units in 19
+// parts: 64 us, 58 the other way.)
 constexpr int kJoinCols = 32, kJoinWarps = 8, kMaxParts = 160;
 static_assert(kMaxParts <= kJoinWarps * 32);
 
-template <bool kBf16>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ Params p) {
+template <int kSplit, bool kBf16>
+__device__ __forceinline__ void join_unit(const Params& p, const Join& jn, int col0, int part0) {
+  constexpr int kQuads = kMaxDim / 4 / kSplit;                                // of four values, of this CTA
+  constexpr int kAcross = kQuads < kJoinWarps ? kQuads : kJoinWarps;          // warps along them
+  constexpr int kTeams = kJoinWarps / kAcross, kEach = kQuads / kAcross;      // teams that take the parts in turn; quads of a warp
   __shared__ int32_t place[kMaxParts];  // of each part
   __shared__ int32_t warp_parts[kJoinWarps];
   __shared__ float weight[kMaxParts][kJoinCols];
-  __shared__ float4 sums[kJoinCols][kMaxDim / 4 + 1];
+  __shared__ float4 sums[kJoinCols][kQuads + 1];
   __shared__ float of_tail[kJoinCols];
   __shared__ float2 stats[kJoinWarps][kJoinCols];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int col0 = blockIdx.x % (kCols / kJoinCols) * kJoinCols, at_join = blockIdx.x / (kCols / kJoinCols);
-  dependent_wait();
-  dependent_launch();
-  const Join jn = p.join[at_join];
-  if (jn.last < 0) return;
+  const int quads = p.v_cols / 4, quad0 = part0 * kQuads;
   const SharedRun run = p.f.runs[jn.rowgroup];
   const int cols = run.rows * p.group, spanned = jn.last - jn.first + 1;
-  if (col0 >= cols) return;
+  if (col0 >= cols || quad0 >= quads) return;
   int parts = 0;  // in order, without the slices that have no tiles
+  __syncthreads();  // the last unit's places and sums have been read
   {
     const int s = jn.first + tid;
     const bool is = tid < spanned && slice_begin(jn.tiles, p.slices, s) != slice_begin(jn.tiles, p.slices, s + 1);
@@ -605,32 +609,32 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     for (int i = warp; i < parts; i += kJoinWarps) weight[i][lane] = factor == 0.f ? 0.f : exp2f(weight[i][lane] - base) * factor;
     if (warp == 0) {
       of_tail[lane] = both.tail;
-      if (col < cols) {
+      if (part0 == 0 && col < cols) {
         const int j = col / p.group;
         p.a.lse[(run.row0 + j) * p.a.heads + jn.kv_head * p.group + col - j * p.group] = both.lse;
       }
     }
   }
   __syncthreads();
-  const int quads = p.v_cols / 4;
+  const int across = warp % kAcross, team = warp / kAcross;
   {
-    constexpr int kAtOnce = 4, kQuads = kMaxDim / 4 / kJoinWarps;
-    float4 x[kQuads];
+    constexpr int kAtOnce = kEach > 1 ? 4 : 8;
+    float4 x[kEach];
 #pragma unroll
-    for (int k = 0; k < kQuads; ++k) x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < parts; i0 += kAtOnce) {
-      float4 y[kAtOnce][kQuads];
+    for (int k = 0; k < kEach; ++k) x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = team; i0 < parts; i0 += kAtOnce * kTeams) {
+      float4 y[kAtOnce][kEach];
 #pragma unroll
       for (int a = 0; a < kAtOnce; ++a)
 #pragma unroll
-        for (int k = 0; k < kQuads; ++k)
-          y[a][k] = load_now(p.part + (static_cast<int64_t>(place[min(i0 + a, parts - 1)]) * quads + min(warp + k * kJoinWarps, quads - 1)) * kCols + col0 + lane);
+        for (int k = 0; k < kEach; ++k)
+          y[a][k] = load_now(p.part + (static_cast<int64_t>(place[min(i0 + a * kTeams, parts - 1)]) * quads + min(quad0 + across + k * kAcross, quads - 1)) * kCols + col0 + lane);
 #pragma unroll
       for (int a = 0; a < kAtOnce; ++a) {
-        const float w = i0 + a < parts ? weight[i0 + a][lane] : 0.f;
+        const float w = i0 + a * kTeams < parts ? weight[i0 + a * kTeams][lane] : 0.f;
         if (w == 0.f) continue;  // nothing seen, whatever stands there
 #pragma unroll
-        for (int k = 0; k < kQuads; ++k) {
+        for (int k = 0; k < kEach; ++k) {
           x[k].x += w * y[a][k].x;
           x[k].y += w * y[a][k].y;
           x[k].z += w * y[a][k].z;
@@ -638,24 +642,44 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
         }
       }
     }
+    for (int turn = 0; turn < kTeams; ++turn) {  // in the teams' order: the same sums every time
+      if (turn > 0) __syncthreads();
+      if (team != turn) continue;
 #pragma unroll
-    for (int k = 0; k < kQuads; ++k)
-      if (warp + k * kJoinWarps < quads) sums[lane][warp + k * kJoinWarps] = x[k];
+      for (int k = 0; k < kEach; ++k) {
+        float4* to = &sums[lane][across + k * kAcross];
+        const float4 y = turn == 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : *to;
+        *to = make_float4(x[k].x + y.x, x[k].y + y.y, x[k].z + y.z, x[k].w + y.w);
+      }
+    }
   }
   __syncthreads();
   // along the values: four a thread
-  for (int e = tid; e < kJoinCols * quads; e += kJoinWarps * 32) {
-    const int n = e / quads, d = e - n * quads, col = col0 + n, j = col / p.group;
+  for (int e = tid; e < kJoinCols * kQuads; e += kJoinWarps * 32) {
+    const int n = e / kQuads, d = quad0 + e % kQuads, col = col0 + n, j = col / p.group;
     if (col >= cols || d * 4 >= p.a.dv) continue;
     uint2* at = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.a.out) + (run.row0 + j) * p.a.out_row_stride +
                                          static_cast<int64_t>(jn.kv_head * p.group + col - j * p.group) * p.a.out_head_stride + d * 4);
     const uint2 old = *at;
     const float2 f = unpack2<kBf16>(old.x), g = unpack2<kBf16>(old.y);
-    const float4 x = sums[n][d];
+    const float4 x = sums[n][e % kQuads];
     const float w = of_tail[n];
     *at = make_uint2(pack2<kBf16>(x.x + w * f.x, x.y + w * f.y), pack2<kBf16>(x.z + w * g.x, x.w + w * g.y));
   }
 }
+
+template <int kSplit, bool kBf16>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ Params p) {
+  const int at = blockIdx.x / kSplit, col0 = at % (kCols / kJoinCols) * kJoinCols;
+  dependent_wait();
+  dependent_launch();
+  for (int s = at / (kCols / kJoinCols); s < p.slices; s += p.join_lanes) {
+    const Join jn = p.join[s];
+    if (jn.last >= 0) join_unit<kSplit, kBf16>(p, jn, col0, blockIdx.x % kSplit);
+  }
+}
+
+constexpr int kManySplit = 16, kFewSplit = 1, kFewUnitLanes = 16, kFewUnitParts = 24;
 
 constexpr size_t kSmem = 6 * kPiece + sizeof(Smem) + 1024;
 static_assert(kSmem <= 232448, "keys, values and queries of 256 columns");
@@ -669,7 +693,9 @@ int run_wide(const Params& p, int device, cudaStream_t stream) {
   if (rc != TOPK_OK) return rc;
   rc = launch(prefix_kernel<kBf16>, p, p.slices, kThreads, kSmem, stream);
   if (rc != TOPK_OK) return rc;
-  return launch(join_kernel<kBf16>, p, static_cast<int64_t>(p.slices) * (kCols / kJoinCols), kJoinWarps * 32, 0, stream);
+  const int64_t ctas = static_cast<int64_t>(p.join_lanes) * (kCols / kJoinCols);
+  if (p.join_lanes < p.slices) return launch(join_kernel<kManySplit, kBf16>, p, ctas * kManySplit, kJoinWarps * 32, 0, stream);
+  return launch(join_kernel<kFewSplit, kBf16>, p, ctas * kFewSplit, kJoinWarps * 32, 0, stream);
 }
 
 }  // namespace
@@ -693,6 +719,10 @@ int attend_wide(const topk_attention_args& a, const FormArgs& f, void* scratch, 
   const int64_t most = a.rows.num_rows * a.kv_heads * ((f.prefixes.most + kTile - 1) / kTile);
   int64_t slices = props.num_sms < kMaxParts ? props.num_sms : kMaxParts;
   p.slices = static_cast<int32_t>(slices < most ? slices : most);
+  // units if all rows share one prefix: where they have many parts each, more CTAs join each of them
+  const int pack = rows_of_run(a);
+  const int64_t units = (a.rows.num_rows + pack - 1) / pack * a.kv_heads;
+  p.join_lanes = p.slices >= kFewUnitParts * units && p.slices > kFewUnitLanes ? kFewUnitLanes : p.slices;
   char* w = static_cast<char*>(scratch);
   const size_t parts = parts_of(props.num_sms) * kCols;
   p.part = reinterpret_cast<float4*>(w);
