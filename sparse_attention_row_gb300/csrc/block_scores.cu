@@ -10,7 +10,7 @@
 //
 // Scores. All rows' blocks are dealt to the CTAs in equal shares, in order, after every CTA has summed them up.
 //
-//   few rows (up to four of a request): the sum over a group's heads comes first, in shared memory; a warp has 32 blocks of one
+//   few rows (one of a request, or up to four of large groups): the sum over a group's heads comes first, in shared memory; a warp has 32 blocks of one
 //   head, and eight lanes read a mean, 128 bytes at a time, and multiply it with the rows' queries. Bound by the means' way from
 //   HBM: 64 rows of 64 heads over 32 K to 131 K tokens in blocks of 64 take 33 us, 5.2 TB/s. (A thread to each mean reads the same
 //   bytes, but 16 of every line at a time: 50 us.)
@@ -481,7 +481,7 @@ int launch_few(ScoreParams& p, int sms, cudaStream_t stream) {
 // -- many rows
 
 constexpr int kManyThreads = 128;
-constexpr int kManyDk = 256;
+constexpr int kManyDk = 256, kManyGroup = 32;
 constexpr int kTile = 128;           // blocks, and columns (row, head) at most
 constexpr int kChunk = kTile * 128;  // bytes of 64 dims
 
@@ -592,7 +592,7 @@ __global__ void __launch_bounds__(kManyThreads) many_kernel(const __grid_constan
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               sum += v[i];
-              const bool ends = kGroup > 0 ? (kGroup <= 32 ? i % (kGroup <= 32 ? kGroup : 1) == kGroup - 1 : false) : ++held == group;
+              const bool ends = kGroup > 0 ? i % (kGroup > 0 ? kGroup : 1) == kGroup - 1 : ++held == group;
               if (ends) {
                 if (r < rows) {
                   const int n = seen[r];
@@ -640,14 +640,15 @@ int launch_many(ScoreParams& p, int device, const topk_device_props& props, cuda
 }
 
 template <bool kBf16>
-int run_scores(ScoreParams& p, int device, const topk_device_props& props, cudaStream_t stream) {
-  if (p.tile_rows > kFewRows) {
+int run_scores(ScoreParams& p, bool many, int device, const topk_device_props& props, cudaStream_t stream) {
+  if (many) {
     switch (p.group) {
       case 1: return launch_many<1, kBf16>(p, device, props, stream);
       case 2: return launch_many<2, kBf16>(p, device, props, stream);
       case 4: return launch_many<4, kBf16>(p, device, props, stream);
       case 8: return launch_many<8, kBf16>(p, device, props, stream);
       case 16: return launch_many<16, kBf16>(p, device, props, stream);
+      case 32: return launch_many<32, kBf16>(p, device, props, stream);
       default: return launch_many<0, kBf16>(p, device, props, stream);
     }
   }
@@ -728,11 +729,16 @@ extern "C" int topk_block_scores(const topk_block_scores_args* args, void* strea
   p.group = a.heads / a.kv_heads;
   const int64_t rows = a.rows.num_rows;
   // Rows that read the same means share them: the rows of a request; where each row brings its request, as many
-  // neighbours as a request has rows on average. More than kFewRows of them go to the tensor cores, as many as fill 128 columns.
+  // neighbours as a request has rows on average. Two and more of them go to the tensor cores, as many as fill 128 columns, unless a
+  // group is so large that a row's heads take most of those. (64 requests of 64 K tokens, 64 heads over 8: a row each 29 us this
+  // way, 28.5 by fused multiply-adds; two 31, 33; four 33, 42. 16 requests, a row each: 10.5, 8.5. 128 heads over one, two rows each: 27, 18.) A
+  // group that is no power of two has no kernel of its own there, and goes from four rows on (groups of 3, two rows: 43, 33; of 24,
+  // three: 18, 13; of 7, four: 44, 51).
   int64_t share = a.rows.next_n;
   if (a.rows.row_request != nullptr) share = a.rows.num_requests > 0 ? (rows + a.rows.num_requests - 1) / a.rows.num_requests : 1;
-  const int fill = kTile / p.group;
-  const int most = a.dk <= kManyDk && fill > kFewRows && share > kFewRows ? fill : kFewRows;
+  const int least = (p.group & (p.group - 1)) == 0 ? 2 : 4;
+  const bool many = a.dk <= kManyDk && p.group <= kManyGroup && share >= least;
+  const int most = many ? kTile / p.group : kFewRows;
   p.tile_rows = static_cast<int32_t>(share < most ? share : most);
   if (a.rows.row_request == nullptr) {
     p.request_tiles = (a.rows.next_n + p.tile_rows - 1) / p.tile_rows;
@@ -741,5 +747,5 @@ extern "C" int topk_block_scores(const topk_block_scores_args* args, void* strea
     p.tiles = (rows + p.tile_rows - 1) / p.tile_rows;
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return a.dtype == TOPK_DTYPE_BF16 ? run_scores<true>(p, device, props, s) : run_scores<false>(p, device, props, s);
+  return a.dtype == TOPK_DTYPE_BF16 ? run_scores<true>(p, many, device, props, s) : run_scores<false>(p, many, device, props, s);
 }
