@@ -18,7 +18,9 @@
 //   many rows: tensor cores, which take the heads one by one, since a sum of them would not fit the input type: S [128 blocks x 128
 //   columns] = means . Q^T, a thread a block, which sums a row's heads up as it reads them from tensor memory. Bound by the chain of
 //   a tile's copy, product and sums, which the CTAs on an SM overlap (three with one place for the means and 128 dims: 1024 rows
-//   of one request, 32 heads over 4, 32 K tokens take 18 us, 4096 rows 49; two with two places 21 and 56; fused multiply-adds 41).
+//   of one request, 32 heads over 4, 32 K tokens take 15.5 us, 4096 rows 42; fused multiply-adds 34 and 120; two CTAs with two places
+//   were 15% slower than three). At the start all CTAs' queries and means come at once: 36 bytes a cycle and SM. The sums are trees over 64 columns at a
+//   time, with the rows' tests behind them (32 and one after the other, a branch for each row: 18 and 49 us).
 #include "attention_parts.cuh"
 #include "paged.cuh"
 #include "token_copies.cuh"
@@ -215,12 +217,14 @@ __device__ __forceinline__ int seen_blocks(const ScoreParams& p, int tokens) {
   return tokens == 0 ? 0 : static_cast<int>(min(static_cast<int64_t>(block_column(p.R, tokens - 1)) + 1, p.a.max_columns));
 }
 
+__device__ __forceinline__ int steps_of(int blocks, int size) { return static_cast<int>((blocks + (size - 1u)) / size); }  // without a sum past 2^31
+
 // The rows [row0, end) of a tile, and within them runs of rows of the same request: those from row0 on.
 struct TileRows {
   int64_t row0, end;
   __device__ __forceinline__ TileRows(const ScoreParams& p, int64_t tile) {
     if (p.request_tiles > 0) {
-      const int64_t request = p.request_tiles == 1 ? tile : tile / p.request_tiles;
+      const int64_t request = p.request_tiles == 1 ? tile : static_cast<uint32_t>(tile) / static_cast<uint32_t>(p.request_tiles);  // there are no more tiles than rows
       row0 = request * p.R.next_n + (tile - request * p.request_tiles) * p.tile_rows;
       end = min(row0 + p.tile_rows, (request + 1) * p.R.next_n);
     } else {
@@ -235,7 +239,7 @@ struct TileRows {
     if (p.request_tiles > 0) {  // all rows of the tile; loads that do not wait for one another
       const int n = static_cast<int>(end - row0);
       int32_t longest = 0;
-#pragma unroll 8
+#pragma unroll 16
       for (int i = 0; i < n; ++i) longest = max(longest, p.R.lengths[row0 + i]);
       *most = seen_blocks(p, seen_tokens(p.R, longest, *request));
       return n;
@@ -254,7 +258,7 @@ struct TileRows {
     int most;
     while (t.row0 < t.end) {
       t.row0 += t.run(p, &request, &most);
-      sum += (most + size - 1) / size;
+      sum += steps_of(most, size);
     }
     return sum;
   }
@@ -291,7 +295,7 @@ __device__ __forceinline__ Share find_share(const ScoreParams& p, int slice, int
   int64_t at = pre - mine;
   if (begin >= at && begin < pre) {
     for (int64_t t = t0; t < t1; ++t) {
-      const int64_t n = TileRows(p, t).steps(p, size) * times;
+      const int64_t n = t + 1 < t1 ? TileRows(p, t).steps(p, size) * times : pre - at;  // of the last one what is left
       if (begin < at + n) {
         share = Share{t, begin - at, slice_begin(total, p.slices, slice + 1) - begin};
         break;
@@ -353,7 +357,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const __grid_consta
       int64_t request;
       int most;
       const int64_t row0 = t.row0;
-      const int rows = t.run(p, &request, &most), groups = (most + kTurnBlocks - 1) / kTurnBlocks;
+      const int rows = t.run(p, &request, &most), groups = steps_of(most, kTurnBlocks);
       t.row0 += rows;
       if (skip >= groups) {
         skip -= groups;
@@ -487,13 +491,13 @@ constexpr int kChunk = kTile * 128;  // bytes of 64 dims
 
 // kGroup: heads of a group, 0: any number.
 template <int kGroup, bool kBf16>
-__global__ void __launch_bounds__(kManyThreads) many_kernel(const __grid_constant__ ScoreParams p) {
+__global__ void __launch_bounds__(kManyThreads, 3) many_kernel(const __grid_constant__ ScoreParams p) {
   using namespace umma;
   extern __shared__ __align__(1024) uint8_t raw[];
   const topk_block_scores_args& a = p.a;
   const int chunks = (a.dk + 63) / 64, pieces = (chunks + 1) / 2;
   const uint32_t q_at = (smem_addr(raw) + 1023) & ~1023u, means_at = q_at + chunks * kChunk;
-  __shared__ int32_t seen[kTile];
+  __shared__ __align__(16) int32_t seen[kTile];  // blocks of each row, 0 behind the last one
   __shared__ uint64_t done;
   __shared__ uint32_t tmem_at, gave_up;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = kGroup > 0 ? kGroup : p.group;
@@ -522,13 +526,13 @@ __global__ void __launch_bounds__(kManyThreads) many_kernel(const __grid_constan
       int64_t request;
       int most;
       const int64_t row0 = t.row0;
-      const int rows = t.run(p, &request, &most), steps = (most + kTile - 1) / kTile;
+      const int rows = t.run(p, &request, &most), steps = steps_of(most, kTile);
       t.row0 += rows;
       if (skip >= static_cast<int64_t>(steps) * a.kv_heads) {
         skip -= static_cast<int64_t>(steps) * a.kv_heads;
         continue;
       }
-      if (tid < rows) seen[tid] = seen_blocks(p, seen_tokens(p.R, p.R.lengths[row0 + tid], request));
+      seen[tid] = tid < rows ? seen_blocks(p, seen_tokens(p.R, p.R.lengths[row0 + tid], request)) : 0;
       const int cols = rows * group;
       const uint32_t inst = instruction(kFormat, (cols + 15) / 16 * 16, false);
       const int32_t* table = p.R.block_table + request * p.R.table_stride;
@@ -583,25 +587,46 @@ __global__ void __launch_bounds__(kManyThreads) many_kernel(const __grid_constan
           const int j = step * kTile + tid;
           float* to = a.scores + row0 * a.score_row_stride + head * a.score_head_stride + j;
           const uint32_t from = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-          int r = 0, held = 0;
-          float sum = 0.f;
+          if constexpr (kGroup > 0) {
+            constexpr int kSpan = kGroup >= 8 ? 64 : kGroup > 1 ? 32 : 16, kRows = kSpan / kGroup;  // columns at a time
+            const float always = in ? INFINITY : -INFINITY;  // what the score is where it is not the sum
+            const bool fixed = !in || j < a.sink_blocks;
 #pragma unroll 1
-          for (int c = 0; c < cols; c += 32) {
-            float v[32];
-            tmem_load(from + c, v);
+            for (int c = 0; c < cols; c += kSpan) {
+              float v[kSpan];
+              if constexpr (kSpan == 64)
+                tmem_load64(from + c, v);
+              else
+                tmem_load(from + c, v);
+              const int32_t* n = seen + c / kGroup;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              sum += v[i];
-              const bool ends = kGroup > 0 ? i % (kGroup > 0 ? kGroup : 1) == kGroup - 1 : ++held == group;
-              if (ends) {
-                if (r < rows) {
-                  const int n = seen[r];
-                  if (j < n) *to = final_score(p, sum, in, j, n);
+              for (int r = 0; r < kRows; ++r) {
+                float* x = v + r * kGroup;
+#pragma unroll
+                for (int w = kGroup / 2; w > 0; w >>= 1)
+#pragma unroll
+                  for (int i = 0; i < w; ++i) x[i] += x[i + w];
+                if (j < n[r]) to[r * a.score_row_stride] = fixed || j >= n[r] - a.recent_blocks ? always : x[0];
+              }
+              to += kRows * a.score_row_stride;
+            }
+          } else {
+            int r = 0, held = 0;
+            float sum = 0.f;
+#pragma unroll 1
+            for (int c = 0; c < cols; c += 32) {
+              float v[32];
+              tmem_load(from + c, v);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                sum += v[i];
+                if (++held == group) {
+                  if (r < rows && j < seen[r]) *to = final_score(p, sum, in, j, seen[r]);
+                  to += a.score_row_stride;
+                  ++r;
+                  held = 0;
+                  sum = 0.f;
                 }
-                to += a.score_row_stride;
-                ++r;
-                held = 0;
-                sum = 0.f;
               }
             }
           }
@@ -731,7 +756,7 @@ extern "C" int topk_block_scores(const topk_block_scores_args* args, void* strea
   // Rows that read the same means share them: the rows of a request; where each row brings its request, as many
   // neighbours as a request has rows on average. Two and more of them go to the tensor cores, as many as fill 128 columns, unless a
   // group is so large that a row's heads take most of those. (64 requests of 64 K tokens, 64 heads over 8: a row each 29 us this
-  // way, 28.5 by fused multiply-adds; two 31, 33; four 33, 42. 16 requests, a row each: 10.5, 8.5. 128 heads over one, two rows each: 27, 18.) A
+  // way, 28 by fused multiply-adds; two 30, 32.5; four 32, 42. 16 requests, a row each: 10.5, 8.5. 128 heads over one, two rows each: 27, 18.) A
   // group that is no power of two has no kernel of its own there, and goes from four rows on (groups of 3, two rows: 43, 33; of 24,
   // three: 18, 13; of 7, four: 44, 51).
   int64_t share = a.rows.next_n;
