@@ -208,6 +208,19 @@ def test_scores_of_many_rows_of_a_request(dec, heads, kv, dk, dtype):
     assert dec.status() == sar.TOPK_DEV_BAD_BLOCK
 
 
+@pytest.mark.parametrize("next_n", [2, 3, 4, 6])
+@pytest.mark.parametrize("heads, kv", [(32, 1), (64, 2), (33, 1), (66, 2), (6, 2), (28, 4), (4, 2), (2, 2)])
+def test_scores_of_a_few_rows_of_a_request(dec, next_n, heads, kv):
+    # about the smallest tiles that the tensor cores take, of groups with and without a kernel of their own, and too large ones
+    lengths = [max(0, b + j) for b in (4100, 0, 1, 900) for j in range(next_n)]
+    lengths[0] = 17
+    requests = [r // next_n for r in range(len(lengths))]
+    case = scores_case(14, lengths, requests, heads, kv, 128, torch.float16, 8)
+    check_scores(dec, case, lengths, requests, 8, sinks=1, recent=2, next_n=next_n)
+    check_scores(dec, case, lengths, requests, 8, sinks=1, row_request=True)
+    ok(dec)
+
+
 def test_scores_that_are_no_numbers_stay_in_their_blocks(dec):
     for rows in (1, 9):
         means = torch.zeros(300, 1, 64).half()

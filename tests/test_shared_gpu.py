@@ -320,6 +320,17 @@ def test_many_columns_of_several_prefixes(dec, each):
     check(dec, case, prefixes, prefix_of, lengths, requests, 64, 16)
 
 
+@pytest.mark.parametrize("heads, kv, dk, dv", [(16, 1, 128, 128), (24, 2, 72, 40)])
+def test_many_columns_of_more_prefixes_than_rows_make_units(dec, heads, kv, dk, dv):
+    # a prefix for every one or two rows: units in a few parts each, where one prefix for all would be a unit or two in many
+    prefixes = [2500 - 190 * i for i in range(13)]
+    prefix_of = [i // 2 for i in range(22)] + [11, 12, 12, 12]
+    lengths = [prefixes[p] + 7 * i for i, p in enumerate(prefix_of)]
+    requests = list(range(len(lengths)))
+    case = make(24, prefixes, prefix_of, lengths, requests, heads, kv, dk, dv, False, torch.bfloat16, 16)
+    check(dec, case, prefixes, prefix_of, lengths, requests, dv, 16)
+
+
 def test_many_columns_with_scores_that_grow(dec):
     # scores that rise along the prefix, so that maxima move often, for some of the columns
     n = 40
