@@ -19,7 +19,7 @@ namespace ltk {
 namespace paged {
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kMostThreads = 1024;
 
 struct PlanParams {
   Rows R;
@@ -31,11 +31,11 @@ struct PlanParams {
   int32_t* run_count;
 };
 
-// One CTA: rows 1024 at a time, with the start of the run that the last segment ended in.
-__global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
-  __shared__ int64_t key[kThreads + 2];  // prefix and tokens of each row of the segment, and of its neighbours
-  __shared__ int32_t warp_start[kThreads / 32], warp_ends[kThreads / 32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// One CTA: up to 1024 rows at a time, a thread each, with the start of the run that the last segment ended in.
+__global__ void __launch_bounds__(kMostThreads) plan_kernel(const PlanParams p) {
+  __shared__ int64_t key[kMostThreads + 2];  // prefix and tokens of each row of the segment, and of its neighbours
+  __shared__ int32_t warp_start[kMostThreads / 32], warp_ends[kMostThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads / 32;
   dependent_wait();
   dependent_launch();
   const auto key_of = [&](int64_t row) -> int64_t {
@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
   uint32_t bits = 0;
   int64_t start = 0;  // of the run so far
   int32_t count = 0;  // runs listed
-  for (int64_t row0 = 0; row0 < p.R.num_rows; row0 += kThreads) {
+  for (int64_t row0 = 0; row0 < p.R.num_rows; row0 += threads) {
     const int64_t row = row0 + tid;
     const bool real = row < p.R.num_rows;
     const int64_t mine = key_of(row);
@@ -56,9 +56,9 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
       const int64_t k = key_of(row0 - 1);
       if (lane == 0) key[0] = k;
     }
-    if (warp == kThreads / 32 - 1) {
-      const int64_t k = key_of(row0 + kThreads);
-      if (lane == 0) key[kThreads + 1] = k;
+    if (warp == warps - 1) {
+      const int64_t k = key_of(row0 + threads);
+      if (lane == 0) key[threads + 1] = k;
     }
     if (real) {
       const int64_t request = row_request(p.R, row);
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
     if (lane == 0) warp_ends[warp] = __popc(who);
     __syncthreads();
     int32_t place = count + __popc(who & ((1u << lane) - 1)), total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
+    for (int w = 0; w < warps; ++w) {
       if (w < warp) place += warp_ends[w];
       total += warp_ends[w];
     }
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
     }
     count += total;
     int32_t last = -1;
-    for (int w = 0; w < kThreads / 32; ++w) last = max(last, warp_start[w]);
+    for (int w = 0; w < warps; ++w) last = max(last, warp_start[w]);
     if (last >= 0) start = row0 + last;
     __syncthreads();  // the next segment writes the sums again
   }
@@ -182,7 +182,8 @@ extern "C" int topk_shared_attention(const topk_shared_attention_args* args, voi
   p.skip = reinterpret_cast<int32_t*>(scratch + at.skip);
   p.runs = reinterpret_cast<SharedRun*>(scratch + at.runs);
   p.run_count = reinterpret_cast<int32_t*>(scratch);
-  rc = launch(plan_kernel, p, 1, kThreads, 0, static_cast<cudaStream_t>(stream));
+  const int threads = a.rows.num_rows < kMostThreads ? static_cast<int>((a.rows.num_rows + 31) / 32 * 32) : kMostThreads;
+  rc = launch(plan_kernel, p, 1, threads, 0, static_cast<cudaStream_t>(stream));
   if (rc != TOPK_OK) return rc;
 
   f.skip = p.skip;

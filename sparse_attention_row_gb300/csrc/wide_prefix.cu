@@ -535,10 +535,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
 }
 
 // Joins the parts of the units that fell into several slices: 32 columns of a unit and some of its values a CTA, lanes along the
-// columns, four values a thread at a time. Where units are few and have many parts, kSplit CTAs share the values of 32 columns, and the
-// warps that are then left the parts; and a few CTAs look for the units among all slices. (The call of 32 rows, 16 heads over 2 and a prefix
-// of 32 K tokens, two units in 76 parts each: 47 us, 56 joined the other way. Of 64 rows, 32 heads over 8, 16 K tokens, eight units in 19
-// parts: 64 us, 58 the other way.)
+// columns, four values a thread at a time. kSplit CTAs share the values of 32 columns, and the warps that are then left the parts. Where units
+// are few and have many parts, that is eight, and 16 CTAs look for the units among all slices; else two, and each slice has its own. (32 rows, 16
+// heads over 2, a prefix of 32 K tokens, two units in 76 parts: 47 us, the other way 51, with a CTA to 32 columns 58; 32 rows, 32 heads over 8, 16 K,
+// eight units in 19 parts: 45, 46, 48; 256 rows, 32 K, 32 units: 184, 172, 173.)
 constexpr int kJoinCols = 32, kJoinWarps = 8, kMaxParts = 160;
 static_assert(kMaxParts <= kJoinWarps * 32);
 
@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
   }
 }
 
-constexpr int kManySplit = 16, kFewSplit = 1, kFewUnitLanes = 16, kFewUnitParts = 24;
+constexpr int kManySplit = 8, kFewSplit = 2, kFewUnitLanes = 16, kFewUnitParts = 16;
 
 constexpr size_t kSmem = 6 * kPiece + sizeof(Smem) + 1024;
 static_assert(kSmem <= 232448, "keys, values and queries of 256 columns");
