@@ -110,12 +110,17 @@ __global__ void __launch_bounds__(kMostThreads) plan_kernel(const PlanParams p) 
   if (bits) atomicOr(p.R.status, bits);
 }
 
-// Bytes that all rows together read up to which each reads the prefix for itself, out of L2. (32 heads over 8: 134 MB 25 to 28 us,
-// shared 31 to 36; 537 MB 62 to 77 us, shared 36 to 56. 16 latent heads: 151 MB 29 to 35 us, shared 55 to 61; 604 MB 74 to 77 us,
-// shared 69 to 73. 128 latent heads fill the columns by themselves: 604 MB 194 us, shared 221.)
+// Bytes that all rows together read up to which each reads the prefix for itself, out of L2. (In us alone against shared. 32 heads over
+// 8: 134 MB 25 to 28 against 31 to 34, 268 MB 38 to 44 against 34 to 44, 537 MB 62 to 77 against 36 to 52. 16 heads over 2, wide units: 134 MB
+// 26 against 33, 268 MB 38 against 35 to 40; units of up to 64 columns, of which there are two, 268 MB 38 against 45. 16 latent heads: 151 MB 29 to
+// 35 against 55 to 61; 302 MB 46 to 50 against 61 to 69; 604 MB 74 to 77 against 70 to 81. 128 latent heads fill the columns by themselves: 604 MB
+// 194 against 221.)
 double read_alone(const topk_attention_args& a) {
   if (takes_wide(a)) return 256e6;
-  return a.heads / a.kv_heads >= kSharedCols ? DBL_MAX : 512e6;
+  if (a.heads / a.kv_heads >= kSharedCols) return DBL_MAX;
+  const int pack = rows_of_run(a);
+  const int64_t units = (a.rows.num_rows + pack - 1) / pack * a.kv_heads;
+  return a.v != nullptr && units >= 8 ? 256e6 : 512e6;
 }
 
 size_t round_up(size_t n) { return (n + 255) / 256 * 256; }
