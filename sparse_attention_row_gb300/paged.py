@@ -9,7 +9,7 @@ arguments are packed in one go: a call with its outputs given is enqueued in 7 t
 """
 from __future__ import annotations
 
-import ctypes
+import array
 import struct
 from typing import NamedTuple
 
@@ -52,8 +52,8 @@ class PageCaches:
     """Caches whose pages are copied together, read once: made by ``PagedDecoder.page_caches``."""
 
     def __init__(self, tensors, packed: bytes):
-        self.tensors, self.packed, self.address = tensors, ctypes.create_string_buffer(packed, max(len(packed), 1)), 0
-        self.address = ctypes.addressof(self.packed)
+        self.tensors, self.packed = tensors, array.array("B", packed)
+        self.address = self.packed.buffer_info()[0]
 
 
 class PagedDecoder:
@@ -132,6 +132,15 @@ class PagedDecoder:
             self._bad(what, t, f"a {dtype} tensor of {rows} contiguous rows")
         return t.data_ptr(), strides[0], shape[1]
 
+    def _table(self, what: str, t):
+        """int32 [rows, columns], rows contiguous: (address, rows, row stride, columns)."""
+        strides, shape = t.stride(), t.shape
+        if len(strides) != 2 or t.dtype is not self._i32 or t.get_device() != self.device or (strides[1] != 1 and shape[1] != 1):
+            self._bad(what, t, "an int32 tensor of contiguous rows")
+        rows, columns = shape
+        stride = strides[0]
+        return t.data_ptr(), rows, stride if rows > 1 or stride >= columns else columns, columns
+
     def _vectors(self, what: str, t, dtype, dims: int):
         """`dims` dimensions, the last one contiguous: (address, strides)."""
         strides = t.stride()
@@ -146,7 +155,8 @@ class PagedDecoder:
             p, (s0, s1, _) = self._vectors(what, t, dtype, 3)
             return p, s0, s1, 0, (shape[0], shape[1], 1), shape[2]
         p, (s0, s1, s2, _) = self._vectors(what, t, dtype, 4)
-        return p, s0, s1, s2, shape[:3], shape[3]
+        blocks, block_size, heads, dim = shape
+        return p, s0, s1, s2, (blocks, block_size, heads), dim
 
     def _empty(self, shape, dtype, stream):
         if stream is None:
@@ -203,11 +213,9 @@ class PagedDecoder:
             self._bad("lengths", lengths, f"a contiguous int32 tensor with 1 or 2 dimensions and {rows} entries")
         if next_n is None:
             next_n = lengths.shape[1] if dims == 2 else 1
-        requests = len(block_table)
-        table, stride, columns = self._matrix("block_table", block_table, self._i32, requests)
+        table, requests, stride, columns = self._table("block_table", block_table)
         return (rows, next_n, block_size, requests, num_blocks, lengths.data_ptr(),
-                0 if row_request is None else self._ints("row_request", row_request, rows), table,
-                stride if requests > 1 or stride >= columns else columns, columns)
+                0 if row_request is None else self._ints("row_request", row_request, rows), table, stride, columns)
 
     def index_logits(self, q, weights, keys, block_table, lengths, key_scales=None, next_n: int | None = None,
                      row_request=None, max_len: int | None = None, out=None, stream=None):
@@ -302,7 +310,7 @@ class PagedDecoder:
     def block_means(self, k_cache, block_table, context_lens, new_lens, means, stream=None):
         """Brings ``means`` ([blocks, kv_heads, dk], of k_cache's type, in place) up to date after a step in which the requests
         got ``new_lens`` tokens behind ``context_lens`` (int32 [requests]): the mean key of every page that holds one of them."""
-        dtype, n = k_cache.dtype, len(block_table)
+        dtype = k_cache.dtype
         kind = self._dtypes.get(dtype)
         if kind is None:
             raise ValueError(f"k_cache has an unsupported type {dtype}")
@@ -310,10 +318,10 @@ class PagedDecoder:
         mp, (m0, m1, _) = self._vectors("means", means, dtype, 3)
         if means.shape != (blocks, kv_heads, dk):
             self._bad("means", means, f"a {(blocks, kv_heads, dk)} tensor")
-        table, stride, columns = self._matrix("block_table", block_table, self._i32, n)
+        table, n, stride, columns = self._table("block_table", block_table)
         self._call(self._block_means, _MEANS.pack(
-            self._ints("context_lens", context_lens, n), self._ints("new_lens", new_lens, n), n, block_size, kind, table,
-            stride if n > 1 or stride >= columns else columns, columns, blocks, kv_heads, dk, kp, k0, k1, k2, mp, m0, m1, self._workspace_ptr), stream)
+            self._ints("context_lens", context_lens, n), self._ints("new_lens", new_lens, n), n, block_size, kind, table, stride, columns, blocks, kv_heads, dk,
+            kp, k0, k1, k2, mp, m0, m1, self._workspace_ptr), stream)
         return means
 
     def block_scores(self, q, means, block_table, lengths, block_size: int, sink_blocks: int = 0, recent_blocks: int = 0,
@@ -333,28 +341,36 @@ class PagedDecoder:
             raise ValueError("q and means must have the same last dimension")
         rows_args = self._rows(rows, lengths, block_table, blocks, block_size, next_n, row_request)
         if out is None:
-            out = self._empty((rows, kv_heads, block_table.shape[1]), self._f32, stream)
-        op, (o0, o1, _) = self._vectors("out", out, self._f32, 3)
-        if out.shape[:2] != (rows, kv_heads):
-            self._bad("out", out, f"a {(rows, kv_heads)} x columns tensor")
+            width = rows_args[-1]
+            out = self._empty((rows, kv_heads, width), self._f32, stream)
+            op, o0, o1 = out.data_ptr(), kv_heads * width, width
+        else:
+            op, (o0, o1, _) = self._vectors("out", out, self._f32, 3)
+            out_rows, out_heads, width = out.shape
+            if out_rows != rows or out_heads != kv_heads:
+                self._bad("out", out, f"a {(rows, kv_heads)} x columns tensor")
         if lens is None:
             lens = self._empty((rows, kv_heads), self._i32, stream)
-        lp, _, lens_heads = self._matrix("lens", lens, self._i32, rows)
-        if lens_heads != kv_heads or not lens.is_contiguous():
-            self._bad("lens", lens, f"a contiguous {(rows, kv_heads)} tensor")
+            lp = lens.data_ptr()
+        else:
+            lp, _, lens_heads = self._matrix("lens", lens, self._i32, rows)
+            if lens_heads != kv_heads or not lens.is_contiguous():
+                self._bad("lens", lens, f"a contiguous {(rows, kv_heads)} tensor")
         self._call(self._block_scores, _SCORES.pack(
-            *rows_args, kind, heads, kv_heads, dk, sink_blocks, recent_blocks, qp, q0, q1, mp, m0, m1, op, o0, o1, out.shape[2], lp, self._workspace_ptr), stream)
+            *rows_args, kind, heads, kv_heads, dk, sink_blocks, recent_blocks, qp, q0, q1, mp, m0, m1, op, o0, o1, width, lp, self._workspace_ptr), stream)
         return out, lens
 
     def block_attention(self, q, k_cache, block_table, lengths, blocks, v_cache=None, v_dim: int | None = None, scale: float | None = None,
                         next_n: int | None = None, row_request=None, out=None, lse=None, return_lse: bool = False, stream=None):
         """``attention`` over the tokens of chosen blocks: ``blocks`` int32 [rows, kv_heads, n], a list for each key-value head, or
         [rows, n], one for all heads of a row; columns of the row's request in the table, -1 where there is none."""
-        rows, kv_heads = q.shape[0], k_cache.shape[2] if k_cache.dim() == 4 else 1
-        bp, strides = self._vectors("blocks", blocks, self._i32, blocks.dim() if blocks.dim() in (2, 3) else 3)
-        if blocks.shape[0] != rows or (len(strides) == 3 and blocks.shape[1] != kv_heads):
+        shape = blocks.shape
+        by_head = len(shape) != 2
+        bp, strides = self._vectors("blocks", blocks, self._i32, 3 if by_head else 2)
+        rows, kv_heads = q.shape[0], k_cache.shape[2] if by_head and k_cache.dim() == 4 else 1
+        if shape[0] != rows or (by_head and shape[1] != kv_heads):
             self._bad("blocks", blocks, f"a {(rows, kv_heads)} x n or {rows} x n tensor")
-        more = bp, strides[0], strides[1] if len(strides) == 3 else 0, blocks.shape[-1]
+        more = bp, strides[0], strides[1] if by_head else 0, shape[-1]
         both = self._attend(self._block_attention, _BLOCKS, more, q, k_cache, block_table, lengths, v_cache, v_dim, None, scale, next_n, row_request, out, lse, return_lse, stream)
         return both if return_lse else both[0]
 
@@ -367,29 +383,29 @@ class PagedDecoder:
         ``prefix_lens[prefix_of[b]]`` tokens of the pages in ``prefix_table[prefix_of[b]]`` (int32 [requests], negative: nothing shared;
         [prefixes]; [prefixes, columns]). Their whole pages are read once for all neighbouring rows that begin with them. Lengths count the
         prefix, and the rows of ``block_table`` have its pages' columns."""
-        prefixes = len(prefix_table)
-        table, stride, columns = self._matrix("prefix_table", prefix_table, self._i32, prefixes)
+        table, prefixes, stride, columns = self._table("prefix_table", prefix_table)
         rows = q.shape[0]
         need = self._scratch.get(rows)
         if need is None:
             need = self._scratch[rows] = _sar.topk_shared_attention_scratch_size(self.device, rows)
         scratch = self._empty(need, self._u8, stream)
-        more = (self._ints("prefix_of", prefix_of, len(block_table)), prefixes, self._ints("prefix_lens", prefix_lens, prefixes), table,
-                stride if prefixes > 1 or stride >= columns else columns, columns, scratch.data_ptr(), need)
+        more = (self._ints("prefix_of", prefix_of, block_table.shape[0]), prefixes, self._ints("prefix_lens", prefix_lens, prefixes), table, stride, columns,
+                scratch.data_ptr(), need)
         both = self._attend(self._shared_attention, _SHARED, more, q, k_cache, block_table, lengths, v_cache, v_dim, None, scale, next_n, row_request, out, lse, True, stream)
         return both if return_lse else both[0]
 
     # ---- the pages ----
 
     def _pool(self, block_table, shares, free_blocks, taken):
-        requests, blocks, free = len(block_table), shares.numel(), free_blocks.numel()
-        table, stride, columns = self._matrix("block_table", block_table, self._i32, requests)
-        return (table, requests, stride if requests > 1 or stride >= columns else columns, columns, self._ints("shares", shares, blocks), blocks,
-                self._ints("free_blocks", free_blocks, free), free, self._ints("taken", taken, 1), self._workspace_ptr)
+        blocks, free = shares.numel(), free_blocks.numel()
+        table, requests, stride, columns = self._table("block_table", block_table)
+        return (table, requests, stride, columns, self._ints("shares", shares, blocks), blocks, self._ints("free_blocks", free_blocks, free), free,
+                self._ints("taken", taken, 1), self._workspace_ptr)
 
     def _copies(self, out, n: int, stream):
         if out is None:
-            out = PageCopies(self._empty(n, self._i32, stream), self._empty(n, self._i32, stream))
+            source, target = self._empty(n, self._i32, stream), self._empty(n, self._i32, stream)
+            return PageCopies(source, target), source.data_ptr(), target.data_ptr()
         return out, self._ints("out.source", out.source, n), self._ints("out.target", out.target, n)
 
     def fork_pages(self, parents, children, kept_lens, block_table, shares, free_blocks, taken, block_size: int,
@@ -418,10 +434,9 @@ class PagedDecoder:
         requests, columns, blocks, free = pool[1], pool[3], pool[5], pool[7]
         table, stride = pool[0], pool[2]
         if table_out is not None:
-            table, stride, wide = self._matrix("table_out", table_out, self._i32, requests)
-            if wide != columns:
+            table, tall, stride, wide = self._table("table_out", table_out)
+            if tall != requests or wide != columns:
                 self._bad("table_out", table_out, f"a {(requests, columns)} tensor")
-            stride = stride if requests > 1 or stride >= columns else columns
         out, source, target = self._copies(out, max_copies, stream)
         need = 12 * blocks + 16
         scratch = self._empty(need, self._u8, stream)
@@ -443,10 +458,11 @@ class PagedDecoder:
         shape = t.shape
         if not shape or t.get_device() != self.device:
             self._bad("a cache", t, "a [blocks, ...] tensor")
-        if t.is_contiguous() and shape[0] > 0:
-            run = t.numel() // shape[0] * t.element_size()
-            if run > 0:
-                return _CACHE.pack(t.data_ptr(), shape[0], run, 0, 0, 1, 1, run)
+        if t.is_contiguous():
+            blocks, all_bytes = shape[0], t.nbytes
+            if all_bytes > 0:
+                run = all_bytes // blocks
+                return _CACHE.pack(t.data_ptr(), blocks, run, 0, 0, 1, 1, run)
         if 0 in shape[1:]:
             self._bad("a cache", t, "a tensor whose pages hold something")
         size, strides = t.element_size(), t.stride()
