@@ -84,16 +84,24 @@ constexpr int places = kLatent ? 1 : 2;
 template <bool kLatent>
 constexpr int most_query_places = !kLatent && (kForm == Form::kTail || kForm == Form::kBlocks) ? 2 : 1;
 // CTAs that an SM can hold: two, where lists of blocks make many short units of few columns, whose tokens come from L2. (1024
-// rows of one request, 32 heads over 4, 16 blocks of 64 tokens each: 219 us, with one CTA 250. A warp that looks tokens up for the
+// rows of one request, 32 heads over 4, 16 blocks of 64 tokens each: 207 us, with one CTA 250. A warp that looks tokens up for the
 // copies, or four more that copy the values, brought less, 235.)
 template <int N, bool kLatent>
 constexpr int ctas_per_sm = !kLatent && N == 16 && kForm == Form::kBlocks ? 2 : 1;
+// Probabilities of a tile: a token's columns in a row of 128 bytes, or, where two CTAs have to find room, of 32 (16 columns): the ring
+// has a third slot then, for the keys that come while values are waited for. (The same call with 128 bytes and two slots: 219 us.)
+template <int N, bool kLatent>
+constexpr int p_row = ctas_per_sm<N, kLatent> == 2 ? 32 : 128;
 constexpr int kSoftmaxWarps = 8, kCopyWarps = 4;
 constexpr int kCopyThreads = kCopyWarps * 32;
 constexpr int kScoreWarp = kSoftmaxWarps + kCopyWarps, kValueWarp = kScoreWarp + 1;
 constexpr int kThreads = (kValueWarp + 1) * 32;
-constexpr int kTokenSlots = 8;  // more than the tiles that the copies can be ahead of the softmax: ring slots + 1
+// Places for a tile's positions: as many as the tiles that the copies can be ahead of the softmax, and one. The copies of a tile begin when
+// the values of the one before have found a slot of the ring: with two pieces a tile and six slots, four tiles back.
+template <int N, bool kLatent>
+constexpr int token_slots = ctas_per_sm<N, kLatent> == 2 ? 4 : 8;
 constexpr int kMaxSlots = 6;
+static_assert(kMaxSlots / 2 + 1 <= 4, "positions of the tiles that six slots hold, and one");
 constexpr int kMaxBlockCols = 64;
 constexpr int kTeam = 128, kJoinDims = 32;  // threads of a team
 constexpr int kMaxTeams = 4;                // which take the parts in turn
@@ -132,7 +140,7 @@ struct Params {
   FormArgs f;
 };
 
-template <int N>
+template <int N, int kTokenSlots = 8>
 struct Smem {  // behind the tiles
   static constexpr int kHalf = N / 2;
   int32_t token[kTokenSlots][128];  // position of each token of a tile, INT_MAX where nothing is to be seen
@@ -332,8 +340,8 @@ static __device__ __noinline__ void add_no_numbers(Values v, uint32_t o, uint32_
 }
 
 // The softmax warps call it for a tile of such tokens, which has been scored and not yet been multiplied with its values.
-template <int N, bool kBf16, bool kLatent>
-static __device__ __noinline__ void protect(const Params& p, Smem<N>& sm, uint32_t ring, uint32_t tile, uint32_t segment, bool first, uint32_t tmem) {
+template <int N, bool kBf16, bool kLatent, int kTokenSlots>
+static __device__ __noinline__ void protect(const Params& p, Smem<N, kTokenSlots>& sm, uint32_t ring, uint32_t tile, uint32_t segment, bool first, uint32_t tmem) {
   const int half = threadIdx.x >> 7, token = threadIdx.x & 127, split = sm.split[segment & 1][half];
   const int32_t* position = sm.token[tile % kTokenSlots];
   const Guard guard{&sm.gave_up, p.R.status};
@@ -367,13 +375,14 @@ static __device__ __noinline__ void protect(const Params& p, Smem<N>& sm, uint32
 
 template <int N, bool kBf16, bool kLatent>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm<N, kLatent>) attention_kernel(const __grid_constant__ Params p) {
-  constexpr int kPlaces = places<kLatent>;
+  constexpr int kPlaces = places<kLatent>, kTokenSlots = token_slots<N, kLatent>, kPRow = p_row<N, kLatent>, kPlace = kTile * kPRow;
   extern __shared__ __align__(1024) uint8_t raw[];
   const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
   const int query_places = most_query_places<kLatent> == 2 ? p.query_places : 1;
   const uint32_t q_at = base, ring = q_at + query_places * p.q_bytes, rest = ring + p.slots * kPiece;
   const uint32_t p_at = rest + (p.rest && !p.rest_is_p ? kChunk : 0);
-  Smem<N>& sm = *reinterpret_cast<Smem<N>*>(raw + (p_at + kPlaces * kChunk - smem_addr(raw)));
+  using Shared = Smem<N, kTokenSlots>;
+  Shared& sm = *reinterpret_cast<Shared*>(raw + (p_at + kPlaces * kPlace - smem_addr(raw)));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int block = blockIdx.x % p.blocks, slice = blockIdx.x / p.blocks;
   const Guard guard{&sm.gave_up, p.R.status};
@@ -670,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<N, kLatent>) attention_k
         fence_after();
         if (!kLatent) at.step(p.slots, k_ring);
         const bool add = t > 0 || *const_cast<volatile uint32_t*>(&sm.kept) == tile + 1;
-        const uint32_t p_tile = operand(p_at + (kPlaces == 2 ? b * kChunk : 0), 1024);
+        const uint32_t p_tile = operand(p_at + (kPlaces == 2 ? b * kPlace : 0), 1024);
 #pragma unroll 1
         for (int u = 0; u < p.v_pieces; ++u) {
           if (!kLatent) {
@@ -678,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<N, kLatent>) attention_k
             values.step(kMaxSlots);
             fence_async();
           }
-          mma16_tokens(tmem + u * N, operand(ring + at.slot * kPiece, kChunk), p_tile, kInst, add);
+          mma16_tokens<kPRow>(tmem + u * N, operand(ring + at.slot * kPiece, kChunk), p_tile, kInst, add);
           commit(empty + at.slot * 8);
           at.step(p.slots);
         }
@@ -824,11 +833,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<N, kLatent>) attention_k
         }
         // the product that read this place of P is done
         if (tile >= kPlaces) mbar_wait(smem_addr(&sm.o_done[(tile - kPlaces) & 1]), ((tile - kPlaces) >> 1) & 1, guard);
-        const uint32_t row = p_at + (kPlaces == 2 ? (tile & 1) * kChunk : 0) + token * 128;
+        const uint32_t row = p_at + (kPlaces == 2 ? (tile & 1) * kPlace : 0) + token * kPRow;
         {
 #pragma unroll
           for (int i = 0; i < H; i += 8) {
-            const uint32_t at = row + ((((half * H + i) >> 3) ^ (token & 7)) << 4);
+            const uint32_t at = row + ((((half * H + i) >> 3) ^ (kPRow == 32 ? token >> 2 & 1 : token & 7)) << 4);
             asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(pack2<kBf16>(s[i], s[i + 1])),
                          "r"(pack2<kBf16>(s[i + 2], s[i + 3])), "r"(pack2<kBf16>(s[i + 4], s[i + 5])),
                          "r"(pack2<kBf16>(s[i + 6], s[i + 7]))
@@ -1077,15 +1086,15 @@ static_assert(sizeof(Smem<64>) + 1024 + 9 * 64 * 128 + 4 * kPiece + kChunk <= 23
 
 template <int N, bool kBf16, bool kLatent>
 int run(Params& p, int device, int smem_limit, bool joins, cudaStream_t stream) {
-  const int extra = static_cast<int>(sizeof(Smem<N>)) + 1024;
+  const int extra = static_cast<int>(sizeof(Smem<N, token_slots<N, kLatent>>)) + 1024;
   p.q_bytes = p.k_chunks * N * 128;
   p.rest_is_p = 0;
-  constexpr int kPBytes = places<kLatent> * kChunk;
+  constexpr int kPBytes = places<kLatent> * kTile * p_row<N, kLatent>;
   const int most_smem = smem_limit;
-  // two CTAs on an SM, of which each keeps 1 KB for itself, if both have room for a tile
+  // two CTAs on an SM, which keeps 1 KB of its shared memory for each (and one CTA's largest share is all but that), if both have room for a tile
   if (p.ctas == 2) {
-    if (smem_limit / 2 - 1024 - extra - static_cast<int>(p.q_bytes) - kPBytes >= (p.k_pieces + p.v_pieces) * kPiece)
-      smem_limit = smem_limit / 2 - 1024;
+    const int half = (smem_limit + 1024) / 2 - 1024;
+    if (half - extra - static_cast<int>(p.q_bytes) - kPBytes >= (p.k_pieces + p.v_pieces) * kPiece) smem_limit = half;
   }
   int room = smem_limit - extra - static_cast<int>(p.q_bytes) - kPBytes;  // for the ring and, where it is not P, the rest
   if (p.rest) {
@@ -1094,7 +1103,7 @@ int run(Params& p, int device, int smem_limit, bool joins, cudaStream_t stream) 
     if (!p.rest_is_p) room -= kChunk;
   }
   // a second place for the queries, if four pieces or more remain, and a tile's values among them
-  p.query_places = most_query_places<kLatent> == 2 && (room - static_cast<int>(p.q_bytes)) / kPiece >= (p.ctas == 2 ? 2 : 4) ? 2 : 1;
+  p.query_places = most_query_places<kLatent> == 2 && (room - static_cast<int>(p.q_bytes)) / kPiece >= (p.ctas == 2 ? 3 : 4) ? 2 : 1;
   if (p.query_places == 2) room -= static_cast<int>(p.q_bytes);
   p.slots = room / kPiece < kMaxSlots ? room / kPiece : kMaxSlots;
   const int k_ring = p.k_pieces - p.rest;

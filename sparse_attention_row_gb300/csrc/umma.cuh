@@ -291,29 +291,34 @@ __device__ __forceinline__ void mma16_pair(uint32_t d, uint32_t a, uint32_t a_ne
       : "memory");
 }
 
-// MN-major operands, 128 rows: eight steps of 16 rows.
+// MN-major operands, 128 rows: eight steps of 16 rows. B's rows are 128 bytes, or 32 in 32-byte swizzle (16-byte pieces
+// exchanged where the row's number has bit 2 set), groups of eight rows 256 bytes apart.
+template <int kRowB = 128>
 __device__ __forceinline__ void mma16_tokens(uint32_t d, uint32_t a, uint32_t b, uint32_t inst, bool add) {
+  static_assert(kRowB == 128 || kRowB == 32);
+  constexpr uint32_t kHighB = kRowB == 128 ? kOperandHigh : (256u >> 4) | (1u << 14) | (6u << 29);
   d = uniform(d), a = uniform(a), b = uniform(b);
   asm volatile(
       "{\n .reg .pred p, q, t;\n .reg .b32 x, y;\n .reg .b64 a, b;\n"
       " setp.ne.u32 p, %5, 0;\n setp.eq.u32 t, 0, 0;\n elect.sync _|q, 0xffffffff;\n"
-      " add.u32 x, %1, 0; add.u32 y, %2, 0; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " add.u32 x, %1, 0; add.u32 y, %2, %6; mov.b64 a, {x, %3}; mov.b64 b, {y, %14};\n"
       " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n"
-      " add.u32 x, %1, 128; add.u32 y, %2, 128; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " add.u32 x, %1, 128; add.u32 y, %2, %7; mov.b64 a, {x, %3}; mov.b64 b, {y, %14};\n"
       " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
-      " add.u32 x, %1, 256; add.u32 y, %2, 256; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " add.u32 x, %1, 256; add.u32 y, %2, %8; mov.b64 a, {x, %3}; mov.b64 b, {y, %14};\n"
       " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
-      " add.u32 x, %1, 384; add.u32 y, %2, 384; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " add.u32 x, %1, 384; add.u32 y, %2, %9; mov.b64 a, {x, %3}; mov.b64 b, {y, %14};\n"
       " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
-      " add.u32 x, %1, 512; add.u32 y, %2, 512; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " add.u32 x, %1, 512; add.u32 y, %2, %10; mov.b64 a, {x, %3}; mov.b64 b, {y, %14};\n"
       " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
-      " add.u32 x, %1, 640; add.u32 y, %2, 640; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " add.u32 x, %1, 640; add.u32 y, %2, %11; mov.b64 a, {x, %3}; mov.b64 b, {y, %14};\n"
       " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
-      " add.u32 x, %1, 768; add.u32 y, %2, 768; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " add.u32 x, %1, 768; add.u32 y, %2, %12; mov.b64 a, {x, %3}; mov.b64 b, {y, %14};\n"
       " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
-      " add.u32 x, %1, 896; add.u32 y, %2, 896; mov.b64 a, {x, %3}; mov.b64 b, {y, %3};\n"
+      " add.u32 x, %1, 896; add.u32 y, %2, %13; mov.b64 a, {x, %3}; mov.b64 b, {y, %14};\n"
       " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
-      "}" ::"r"(d), "r"(a), "r"(b), "r"(kOperandHigh), "r"(inst), "r"(static_cast<uint32_t>(add))
+      "}" ::"r"(d), "r"(a), "r"(b), "r"(kOperandHigh), "r"(inst), "r"(static_cast<uint32_t>(add)), "n"(0), "n"(kRowB), "n"(2 * kRowB),
+      "n"(3 * kRowB), "n"(4 * kRowB), "n"(5 * kRowB), "n"(6 * kRowB), "n"(7 * kRowB), "r"(kHighB)
       : "memory");
 }
 
