@@ -1171,8 +1171,9 @@ int attend(const topk_attention_args& a, const FormArgs& f, void* stream) {
   const int64_t units = kForm == Form::kShared ? (a.rows.num_rows + p.pack - 1) / p.pack * a.kv_heads : p.row_groups * a.kv_heads;
   const int64_t longest = kForm == Form::kShared ? f.prefixes.most : p.R.max_len;
   const int64_t most = (kForm == Form::kShared ? a.rows.num_rows * a.kv_heads : units) * (lists ? p.row_tiles : (longest + kTile - 1) / kTile);
-  // two CTAs on an SM where a tile is two pieces and each has some units (64 rows of 64 heads over 8, 32 blocks: 94 us with one, 96 with two)
-  p.ctas = kForm == Form::kBlocks && !p.latent && p.block_cols <= 16 && p.k_pieces + p.v_pieces == 2 && units >= 8ll * sms ? 2 : 1;
+  // Two CTAs on an SM where a tile is two pieces and there are more units than SMs. (In us with one and two. 64 rows of 64 heads over 8, 32 blocks of
+  // 64 tokens each, from HBM: 92, 93; from L2 89, 59. 64 rows of 32 heads over 4, 16 blocks: 32, 25 and 30, 18. 8 rows of 64 heads over 8, 64 units: 15.5, 17.5.)
+  p.ctas = kForm == Form::kBlocks && !p.latent && p.block_cols <= 16 && p.k_pieces + p.v_pieces == 2 && units > sms ? 2 : 1;
   int64_t slices = sms * p.ctas / p.blocks < 1 ? 1 : sms * p.ctas / p.blocks;
   if (slices > most) slices = most;
   if (slices > kMaxParts) slices = kMaxParts;
