@@ -83,11 +83,11 @@ constexpr int places = kLatent ? 1 : 2;
 // to 2048 tokens of 256 rows, 32 heads over 8, with their prefix of 32 K: 313 us, with one place 321.)
 template <bool kLatent>
 constexpr int most_query_places = !kLatent && (kForm == Form::kTail || kForm == Form::kBlocks) ? 2 : 1;
-// CTAs that an SM can hold: two, where lists of blocks make many short units of few columns, whose tokens come from L2. (1024
+// CTAs that an SM can hold: two, where lists of blocks, or what stands behind prefixes, make many short units of few columns. (1024
 // rows of one request, 32 heads over 4, 16 blocks of 64 tokens each: 207 us, with one CTA 250. A warp that looks tokens up for the
 // copies, or four more that copy the values, brought less, 235.)
 template <int N, bool kLatent>
-constexpr int ctas_per_sm = !kLatent && N == 16 && kForm == Form::kBlocks ? 2 : 1;
+constexpr int ctas_per_sm = !kLatent && N == 16 && (kForm == Form::kBlocks || kForm == Form::kTail) ? 2 : 1;
 // Probabilities of a tile: a token's columns in a row of 128 bytes, or, where two CTAs have to find room, of 32 (16 columns): the ring
 // has a third slot then, for the keys that come while values are waited for. (The same call with 128 bytes and two slots: 219 us.)
 template <int N, bool kLatent>
@@ -1172,8 +1172,9 @@ int attend(const topk_attention_args& a, const FormArgs& f, void* stream) {
   const int64_t longest = kForm == Form::kShared ? f.prefixes.most : p.R.max_len;
   const int64_t most = (kForm == Form::kShared ? a.rows.num_rows * a.kv_heads : units) * (lists ? p.row_tiles : (longest + kTile - 1) / kTile);
   // Two CTAs on an SM where a tile is two pieces and there are more units than SMs. (In us with one and two. 64 rows of 64 heads over 8, 32 blocks of
-  // 64 tokens each, from HBM: 92, 93; from L2 89, 59. 64 rows of 32 heads over 4, 16 blocks: 32, 25 and 30, 18. 8 rows of 64 heads over 8, 64 units: 15.5, 17.5.)
-  p.ctas = kForm == Form::kBlocks && !p.latent && p.block_cols <= 16 && p.k_pieces + p.v_pieces == 2 && units > sms ? 2 : 1;
+  // 64 tokens each, from HBM: 92, 93; from L2 89, 59. 64 rows of 32 heads over 4, 16 blocks: 32, 25 and 30, 18. 8 rows of 64 heads over 8, 64 units: 15.5, 17.5.
+  // Tails of 128 tokens, 64 rows of 32 heads over 8, with their prefix: 44, 41; of up to 2 K, 256 rows: 303, 304; 8 rows: 31.5, 32.5.)
+  p.ctas = (kForm == Form::kBlocks || kForm == Form::kTail) && !p.latent && p.block_cols <= 16 && p.k_pieces + p.v_pieces == 2 && units > sms ? 2 : 1;
   int64_t slices = sms * p.ctas / p.blocks < 1 ? 1 : sms * p.ctas / p.blocks;
   if (slices > most) slices = most;
   if (slices > kMaxParts) slices = kMaxParts;
