@@ -655,7 +655,7 @@ int launch_many(ScoreParams& p, int device, const topk_device_props& props, cuda
   static int granted[kMaxDevices];
   const topk_block_scores_args& a = p.a;
   const size_t smem = 2 * ((a.dk + 63) / 64) * static_cast<size_t>(kChunk) + 1024;
-  const int rc = allow_smem(many_kernel<kGroup, kBf16>, 3 * (kManyDk / 64) * static_cast<size_t>(kChunk) + 1024, device, granted);
+  const int rc = allow_smem(many_kernel<kGroup, kBf16>, 2 * (kManyDk / 64) * static_cast<size_t>(kChunk) + 1024, device, granted);
   if (rc != TOPK_OK) return rc;
   const int64_t columns = a.rows.max_blocks < a.max_columns ? a.rows.max_blocks : a.max_columns;
   const int64_t most = a.rows.num_rows * a.kv_heads * ((columns + kTile - 1) / kTile);
