@@ -332,7 +332,9 @@ __device__ __forceinline__ float final_score(const ScoreParams& p, float score, 
 constexpr int kFewThreads = 256;
 constexpr int kFewWarps = kFewThreads / 32;
 constexpr int kFewRows = 4;
-constexpr int kQueryBytes = 48 * 1024;  // queries of a tile's rows and some of its heads
+// Queries of a tile's rows and some of its heads. Of the 48 KB that a launch may have without asking for more, the kernel's own arrays and
+// what the system keeps of each CTA's take 1 KB (432 dims of seven heads and four rows, 48 384 bytes, are refused at the launch).
+constexpr int kQueryBytes = 46 * 1024;
 constexpr int kTurnBlocks = 32;
 
 template <int kRows, bool kBf16>

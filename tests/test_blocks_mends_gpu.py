@@ -1,0 +1,37 @@
+"""Blocks, shared prefixes and pages where they went wrong once."""
+import pytest
+import torch
+
+import sparse_attention_row_gb300 as sar
+from tests import test_blocks_gpu as blocks
+from tests.gpu_util import require_cuda
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dec():
+    require_cuda()
+    return sar.PagedDecoder(0)
+
+
+@pytest.fixture(autouse=True)
+def _clear(request):
+    yield
+    if "dec" in request.fixturenames:
+        request.getfixturevalue("dec").reset()
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("next_n", [3, 4, 5])
+@pytest.mark.parametrize("heads, kv, dk", [(8, 8, 376), (8, 8, 384), (14, 7, 432), (6, 6, 504), (12, 6, 512), (24, 12, 512), (9, 9, 400), (5, 5, 576)])
+def test_scores_of_few_rows_whose_queries_fill_a_ctas_shared_memory(dec, next_n, heads, kv, dk):
+    lengths = [max(0, b + j) for b in (70, 0, 300) for j in range(next_n)]
+    requests = [r // next_n for r in range(len(lengths))]
+    case = blocks.scores_case(20, lengths, requests, heads, kv, dk, torch.bfloat16, 4)
+    blocks.check_scores(dec, case, lengths, requests, 4, sinks=1, recent=1, next_n=next_n)
+    blocks.check_scores(dec, case, lengths, requests, 4, row_request=True)
+    assert dec.status() == 0
