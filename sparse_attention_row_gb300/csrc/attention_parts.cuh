@@ -28,6 +28,12 @@ __device__ __forceinline__ int slice_of(int64_t tiles, int slices, int64_t x) {
     return static_cast<int>((static_cast<uint32_t>(x + 1) * static_cast<uint32_t>(slices) - 1) / static_cast<uint32_t>(tiles));
   return static_cast<int>(((x + 1) * slices - 1) / tiles);
 }
+// The group of tile x where every group has `per` of them: lists of blocks may be so long that 32 bits do not hold `per`, and its lower
+// ones are zero.
+__host__ __device__ __forceinline__ int64_t group_of(int64_t x, int64_t per) {
+  if (x < per) return 0;
+  return x < kSmallTiles ? static_cast<uint32_t>(x) / static_cast<uint32_t>(per) : x / per;
+}
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;

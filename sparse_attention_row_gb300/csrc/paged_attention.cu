@@ -429,8 +429,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<N, kLatent>) attention_k
       } else {
         sm.run_begin = slice_begin(sm.tiles, p.slices, slice);
         sm.run_end = slice_begin(sm.tiles, p.slices, slice + 1);
-        const int64_t per = static_cast<int64_t>(p.row_tiles) * p.a.kv_heads;
-        sm.start_group = sm.run_begin < kSmallTiles ? static_cast<uint32_t>(sm.run_begin) / static_cast<uint32_t>(per) : sm.run_begin / per;
+        sm.start_group = group_of(sm.run_begin, static_cast<int64_t>(p.row_tiles) * p.a.kv_heads);
       }
       sm.start_at = sm.run_begin - sm.start_group * p.a.kv_heads * p.row_tiles;
     }
