@@ -616,8 +616,8 @@ typedef struct {
  * what a child holds first. Lists that name a child twice, or a child as parent, are not allowed (the
  * call stays within its memory; the result is unspecified).
  * A parent or child outside the table: nothing is done for the pair (TOPK_DEV_BAD_BLOCK). Where the
- * parent has no page, or one outside the pool, or where no free page is left, the child's entry is -1
- * (TOPK_DEV_BAD_BLOCK, TOPK_DEV_BLOCKS_EXHAUSTED). Lengths are clamped into the table's width.
+ * parent has no page, or one outside the pool, or where the free page is none of the pool (it is taken off the list all the same),
+ * or none is left, the child's entry is -1 (TOPK_DEV_BAD_BLOCK; TOPK_DEV_BLOCKS_EXHAUSTED for the last). Lengths are clamped into the table's width.
  */
 typedef struct {
   topk_page_pool pool;

@@ -100,8 +100,15 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const __grid_constan
       const int64_t n = taken + before + rank[k];
       int32_t target = -1;
       if (g.source >= 0) {
-        if (n >= 0 && n < t.num_free) target = t.free_blocks[n];
-        if (target < 0) flags |= TOPK_DEV_BLOCKS_EXHAUSTED;
+        if (n >= 0 && n < t.num_free) {
+          target = t.free_blocks[n];
+          if (target < 0 || target >= t.num_blocks) {  // no page of the pool
+            target = -1;
+            flags |= TOPK_DEV_BAD_BLOCK;
+          }
+        } else {
+          flags |= TOPK_DEV_BLOCKS_EXHAUSTED;
+        }
       }
       if (tid == 0) {
         a.source[base + k] = target < 0 ? -1 : g.source;

@@ -35,3 +35,13 @@ def test_scores_of_few_rows_whose_queries_fill_a_ctas_shared_memory(dec, next_n,
     blocks.check_scores(dec, case, lengths, requests, 4, sinks=1, recent=1, next_n=next_n)
     blocks.check_scores(dec, case, lengths, requests, 4, row_request=True)
     assert dec.status() == 0
+
+
+def test_fork_enters_no_free_page_that_is_none(dec):
+    # 12 and -4 are no pages of the pool; they are taken off the list all the same
+    table = ints([[4, 5], [-1, -1], [-1, -1], [-1, -1], [-1, -1]])
+    shares, free, taken = ints([0] * 12), ints([12, 3, -4]), ints([0])
+    copies = dec.fork_pages(ints([0, 0, 0, 0]), ints([1, 2, 3, 4]), ints([5, 6, 7, 4]), table, shares, free, taken, 4)
+    assert copies.source.tolist() == [-1, 5, -1, -1] and copies.target.tolist() == [-1, 3, -1, -1]
+    assert table.tolist() == [[4, 5], [4, -1], [4, 3], [4, -1], [4, -1]] and int(taken) == 3
+    assert shares.tolist() == [0] * 4 + [4] + [0] * 7 and dec.status() == sar.TOPK_DEV_BAD_BLOCK
