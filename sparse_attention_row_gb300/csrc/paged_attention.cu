@@ -946,7 +946,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<N, kLatent>) attention_k
     }
   }
   if (kForm != Form::kShared && blockIdx.x == 0) report_rows(p.R, tid, kThreads);
-  if (kForm == Form::kWhole && blockIdx.x == 0) {
+  if ((kForm == Form::kWhole || kForm == Form::kTail) && blockIdx.x == 0) {  // of every request, with rows or without
     for (int64_t r = tid; r < p.R.num_requests; r += kThreads)
       if (p.f.prefixes.of[r] >= p.f.prefixes.count) atomicOr(p.R.status, TOPK_DEV_BAD_BLOCK);
   }

@@ -6,7 +6,7 @@
 //   plan    which rows share what, from the rows' lengths and requests, on the device: a run is as many neighbouring rows
 //           with the same prefix as fill a unit's columns, and every row gets its length behind the prefix.
 //   tails   attention over what is behind the prefixes, each request by itself (kTail): bound by HBM. Its results stand in
-//           `out` and `lse`.
+//           `out` and `lse`. It reports requests whose prefix is none.
 //   prefix  attention over the prefixes, a run of rows at a time, which joins its results with those of the tails as it writes
 //           them: wide_prefix.cu, 256 columns a run, or kShared of the kernel of all forms, 64.
 // Small calls take none of them, but one launch in which every row finds the prefix's pages in their table (kWhole).
@@ -64,10 +64,7 @@ __global__ void __launch_bounds__(kMostThreads) plan_kernel(const PlanParams p) 
       const int64_t request = row_request(p.R, row);
       const int32_t n = p.R.lengths[row];
       if (request >= p.R.num_requests) bits |= TOPK_DEV_BAD_BLOCK;
-      if (request >= 0 && request < p.R.num_requests) {
-        if (n < 0 || n > p.R.max_len) bits |= TOPK_DEV_LENGTH_CLAMPED;
-        if (p.prefixes.of[request] >= p.prefixes.count) bits |= TOPK_DEV_BAD_BLOCK;
-      }
+      if (request >= 0 && request < p.R.num_requests && (n < 0 || n > p.R.max_len)) bits |= TOPK_DEV_LENGTH_CLAMPED;
       const int shared = mine < 0 ? 0 : static_cast<int32_t>(mine);
       p.tail_lengths[row] = seen_tokens(p.R, n, request) - shared;
       p.skip[row] = block_column(p.R, shared);

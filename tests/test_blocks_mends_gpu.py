@@ -4,6 +4,7 @@ import torch
 
 import sparse_attention_row_gb300 as sar
 from tests import test_blocks_gpu as blocks
+from tests import test_shared_gpu as shared
 from tests.gpu_util import require_cuda
 
 pytestmark = pytest.mark.gpu
@@ -45,3 +46,16 @@ def test_fork_enters_no_free_page_that_is_none(dec):
     assert copies.source.tolist() == [-1, 5, -1, -1] and copies.target.tolist() == [-1, 3, -1, -1]
     assert table.tolist() == [[4, 5], [4, -1], [4, 3], [4, -1], [4, -1]] and int(taken) == 3
     assert shares.tolist() == [0] * 4 + [4] + [0] * 7 and dec.status() == sar.TOPK_DEV_BAD_BLOCK
+
+
+def test_prefixes_that_are_none_are_reported_whichever_way_a_call_takes(dec):
+    # the third request names a prefix that there is none of, and has no rows
+    lengths, requests = [40, 50, 33], [0, 1, 3]
+    case = shared.make(30, [32], [0, 0, -1, 0], lengths, requests, 4, 1, 64, 64, False, torch.float16, 16)
+    shared.check(dec, case, [32], [0, 0, 1, 0], lengths, requests, 64, 16, allowed=sar.TOPK_DEV_BAD_BLOCK, row_request=ints(requests))
+    q, k, v, hidden, whole, prefix_table = case
+    for table in shared.tables(q, k, v, 64, prefix_table, 16):
+        for third, bits in ((1, sar.TOPK_DEV_BAD_BLOCK), (0, 0), (-2 ** 31, 0), (2 ** 31 - 1, sar.TOPK_DEV_BAD_BLOCK)):
+            dec.reset()
+            dec.shared_attention(q.cuda(), k.cuda(), hidden.cuda(), ints(lengths), ints([0, 0, third, 0]), ints([32]), table.cuda(), v_cache=v.cuda(), row_request=ints(requests))
+            assert dec.status() == bits
