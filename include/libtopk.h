@@ -564,7 +564,8 @@ int topk_block_attention(const topk_block_attention_args* args, void* stream);
  * pages in prefix_table's row prefix_of[b]. The whole pages among those are read once for all rows, next to
  * each other, that begin with them, and not through the requests' own rows of the table. Lengths
  * count all tokens, the prefix's among them. A request whose prefix_of is negative begins with nothing shared; so
- * does, whatever it names, one of which some row sees fewer tokens than those whole pages hold.
+ * does, whatever it names, one of whose next_n rows some row sees fewer tokens than those whole pages hold. With row_request,
+ * each row decides that for itself: a row that sees them all reads the prefix, another one of the same request its row of the table.
  * The results are those of topk_paged_attention where the requests' own rows of the table name the same pages,
  * but that the part behind the prefix is rounded to the type of `out` before both are joined.
  * `attention.lse` must be given: it holds the statistics of that part meanwhile.

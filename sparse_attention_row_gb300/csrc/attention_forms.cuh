@@ -44,8 +44,8 @@ __device__ __forceinline__ int prefix_tokens(const Prefixes& p, const Rows& R, i
   return block_column(R, static_cast<int>(n < p.most ? n : p.most)) * R.block_size;
 }
 
-// The same for a row: 0 also where one of its request's rows, which read what follows together, sees less. By a whole
-// warp, each lane with a row of its own (or past the last one): requests of many rows are looked through by all lanes.
+// The same for a row: 0 also where one of its request's rows, which read what follows together, sees less. Rows that bring
+// their requests read by themselves, and each decides for itself. By a whole warp, each lane with a row of its own (or past the last one): requests of many rows are looked through by all lanes.
 __device__ __forceinline__ int row_prefix_tokens(const Prefixes& p, const Rows& R, int64_t row, int32_t* prefix) {
   const bool real = row >= 0 && row < R.num_rows;
   const int64_t request = real ? row_request(R, row) : -1;

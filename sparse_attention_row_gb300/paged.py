@@ -382,7 +382,8 @@ class PagedDecoder:
         """``attention`` over everything cached, for requests of which some begin with the same pages: request b with the first
         ``prefix_lens[prefix_of[b]]`` tokens of the pages in ``prefix_table[prefix_of[b]]`` (int32 [requests], negative: nothing shared;
         [prefixes]; [prefixes, columns]). Their whole pages are read once for all neighbouring rows that begin with them. Lengths count the
-        prefix, and the rows of ``block_table`` have its pages' columns."""
+        prefix, and the rows of ``block_table`` have its pages' columns. A request of which one of its ``next_n`` rows sees less than those
+        pages hold reads its own row of the table; with ``row_request`` that goes for each such row by itself."""
         table, prefixes, stride, columns = self._table("prefix_table", prefix_table)
         rows = q.shape[0]
         need = self._scratch.get(rows)

@@ -59,3 +59,19 @@ def test_prefixes_that_are_none_are_reported_whichever_way_a_call_takes(dec):
             dec.reset()
             dec.shared_attention(q.cuda(), k.cuda(), hidden.cuda(), ints(lengths), ints([0, 0, third, 0]), ints([32]), table.cuda(), v_cache=v.cuda(), row_request=ints(requests))
             assert dec.status() == bits
+
+
+@pytest.mark.parametrize("by_row", [False, True])
+def test_who_reads_the_prefix_of_a_request_with_a_row_that_sees_less(dec, by_row):
+    # the request's own row of the table names other pages than its prefix, and its second row sees less than that holds
+    g = torch.Generator().manual_seed(31)
+    q, k, v = (torch.randn(s, generator=g).half() for s in ((2, 4, 64), (8, 16, 2, 64), (8, 16, 2, 64)))
+    own, prefix = torch.tensor([[1, 2, 3]], dtype=torch.int32), torch.tensor([[6, 5]], dtype=torch.int32)
+    lengths, mixed = [40, 20], torch.tensor([[6, 5, 3], [1, 2, 3]], dtype=torch.int32)
+    want = blocks.pu.attention64(q, k, v, 64, mixed if by_row else own.expand(2, -1), lengths, [0, 1], 16, 64 ** -0.5)
+    room = want[0], want[1], want[2] * 2.1, want[3] + 1e-5  # the part behind the prefix is rounded once more
+    for table in shared.tables(q, k, v, 64, prefix, 16):
+        out, lse = dec.shared_attention(q.cuda(), k.cuda(), own.cuda(), ints(lengths), ints([0]), ints([32]), table.cuda(), v_cache=v.cuda(), return_lse=True,
+                                        **(dict(row_request=ints([0, 0])) if by_row else dict(next_n=2)))
+        blocks.pu.check_attention(out, lse, room, torch.float16)
+    assert dec.status() == 0
