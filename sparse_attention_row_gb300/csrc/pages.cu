@@ -247,6 +247,12 @@ __device__ __forceinline__ void sum_of_cluster(const int32_t* mine, int64_t* bef
 
 constexpr int64_t kMostFreed = 1 << 20;  // requests of a call
 constexpr int kOnceWords = kMostFreed / 8 / 32 + 2;
+// Requests that were listed before: up to kCompared of them are compared one with another. More are compared within pieces of a CTA's
+// share only, and for those before a piece there is a bit for each row of the table, kRowBits rows at a time: the steps then grow with the
+// number of requests and not with its square, unless the table's rows are so many more that they make the passes dear. (A call's us, all compared
+// and with bits: 1 K requests 23, 21; 4 K 50, 25; 16 K 470, 66; 262 K 119 000, 660.)
+constexpr int kCompared = 1024;
+constexpr int kRowBits = 24 * 1024 * 8;
 constexpr int kEach = 8;                       // places of a thread at a time, side by side
 constexpr int kRound = kEach * kPageThreads;  // places of a CTA
 
@@ -259,6 +265,7 @@ __global__ void __launch_bounds__(kPageThreads, 1) free_kernel(const __grid_cons
   __shared__ int2 warp_sum[kPageWarps];
   __shared__ int32_t mine;
   __shared__ uint32_t again[kOnceWords];  // bits of the requests of this CTA that were listed before
+  __shared__ uint32_t listed[kRowBits / 32];  // bits of rows that were
   const topk_page_free_args& a = p.a;
   const topk_page_pool& t = a.pool;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -270,12 +277,35 @@ __global__ void __launch_bounds__(kPageThreads, 1) free_kernel(const __grid_cons
   dependent_launch();
   const int64_t taken = min(max(static_cast<int64_t>(*t.taken), int64_t{0}), t.num_free);
   __syncthreads();
+  const bool many = a.num_freed > kCompared && a.num_freed > 16 * ((t.num_requests + kRowBits - 1) / kRowBits);
   for (int64_t i = i0 + warp; i < i1; i += kPageWarps) {
     const int32_t request = a.requests[i];
     bool found = false;
 #pragma unroll 8
-    for (int64_t j = lane; j < i; j += 32) found |= a.requests[j] == request;
+    for (int64_t j = (many ? i - (i - i0) % kPageThreads : 0) + lane; j < i; j += 32) found |= a.requests[j] == request;
     if (__any_sync(~0u, found) && lane == 0) atomicOr(&again[(i - i0) >> 5], 1u << ((i - i0) & 31));
+  }
+  for (int64_t row0 = 0; many && row0 < t.num_requests; row0 += kRowBits) {
+    for (int i = tid; i < kRowBits / 32; i += kPageThreads) listed[i] = 0;
+    const auto place = [&](int64_t i) {  // of a request's row in the bits, negative where it has none
+      const int64_t row = a.requests[i] - row0;
+      return row >= 0 && row < kRowBits ? static_cast<int>(row) : -1;
+    };
+    __syncthreads();
+#pragma unroll 8
+    for (int64_t i = tid; i < i0; i += kPageThreads) {
+      const int at = place(i);
+      if (at >= 0) atomicOr(&listed[at >> 5], 1u << (at & 31));
+    }
+    __syncthreads();
+    for (int64_t piece = i0; piece < i1; piece += kPageThreads) {
+      const int64_t i = piece + tid;
+      const int at = i < i1 ? place(i) : -1;
+      if (at >= 0 && (listed[at >> 5] >> (at & 31) & 1)) atomicOr(&again[(i - i0) >> 5], 1u << ((i - i0) & 31));
+      __syncthreads();
+      if (at >= 0) atomicOr(&listed[at >> 5], 1u << (at & 31));
+      __syncthreads();
+    }
   }
   __syncthreads();
   const int64_t places = (i1 - i0) * t.max_blocks;

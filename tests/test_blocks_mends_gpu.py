@@ -1,9 +1,12 @@
 """Blocks, shared prefixes and pages where they went wrong once."""
+import random
+
 import pytest
 import torch
 
 import sparse_attention_row_gb300 as sar
 from tests import test_blocks_gpu as blocks
+from tests import test_pages_gpu as pages
 from tests import test_shared_gpu as shared
 from tests.gpu_util import require_cuda
 
@@ -75,3 +78,44 @@ def test_who_reads_the_prefix_of_a_request_with_a_row_that_sees_less(dec, by_row
                                         **(dict(row_request=ints([0, 0])) if by_row else dict(next_n=2)))
         blocks.pu.check_attention(out, lse, room, torch.float16)
     assert dec.status() == 0
+
+
+@pytest.mark.parametrize("rows, listed", [(3000, 1024), (3000, 1025), (900, 5000), (30000, 40000), (500000, 60000), (500000, 45), (250000, 16 * 1024 + 1)])
+def test_requests_that_are_listed_twice_among_many(dec, rows, listed):
+    # anywhere in the list, some next to each other, some that are none; pages that several rows hold
+    rng = random.Random(listed)
+    pool = pages.Pool(rows, 1, rows, 4, rng)
+    owners = rows - rows // 3
+    pool.table, pool.taken = [[p] for p in pool.free[:owners]], owners
+    for r in range(owners, rows):
+        pool.table.append(list(rng.choice(pool.table[:200])))
+        pool.shares[pool.table[r][0]] += 1
+    gone = rng.choices(range(rows), k=listed - 4)
+    for at in (0, 7, len(gone) // 2, len(gone)):
+        gone.insert(at, gone[max(at - 1, 0)])
+    state = pool.device()
+    bad = list(gone)
+    bad[3:3] = [-1, rows, -2 ** 31, 2 ** 31 - 1, rows, -1]
+    dec.free_pages(ints(bad), *state)
+    pool.release(gone)
+    pool.same(state)
+    assert dec.status() == sar.TOPK_DEV_BAD_BLOCK
+
+
+def test_time_to_free_grows_with_the_number_of_requests(dec):
+    # a quarter of the most that a call takes: compared one with another they would take some hundred milliseconds
+    n = 1 << 18
+    rows = torch.randperm(n, device="cuda", dtype=torch.int32)
+    held = rows.tolist()  # the table is these numbers' memory
+    table, shares, free, taken = rows[:, None], torch.zeros_like(rows), torch.zeros_like(rows), ints([n])
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    listed = torch.randint(0, n, (n,), device="cuda", dtype=torch.int32)
+    torch.cuda.synchronize()
+    start.record()
+    dec.free_pages(listed, table, shares, free, taken)
+    end.record()
+    end.synchronize()
+    assert start.elapsed_time(end) < 20
+    first = list(dict.fromkeys(listed.tolist()))
+    assert int(taken) == n - len(first) and free[n - len(first):].tolist() == [held[r] for r in first]
+    assert not shares.any() and int((table < 0).sum()) == len(first) and dec.status() == 0
