@@ -522,6 +522,9 @@ int topk_block_means(const topk_block_means_args* args, void* stream);
  * recent_blocks blocks score +inf, so that they are selected first. Entries from n_r on are not
  * written. Sums and products are in fp32. A block whose page lies outside the cache scores -inf
  * (TOPK_DEV_BAD_BLOCK), and its mean is not read.
+ * A mean is that of all tokens that the page holds. A row in the middle of a piece, of a prompt or of drafted tokens, ends within its last
+ * block, whose score then depends on tokens behind the row, and with it which blocks are selected. With recent_blocks >= 1
+ * that block scores +inf whatever its mean: causal attention wants that. (topk_block_attention masks those tokens in any case.)
  * heads 1..1024, dk 8..576 in multiples of 8; types f16 and bf16; q and means are read in pieces of 16 bytes.
  */
 typedef struct {

@@ -329,7 +329,9 @@ class PagedDecoder:
         """Scores of every block (page) that a row sees, for each key-value head: the sum of the head's queries
         (q [rows, heads, dk]) times the page's mean key (``means`` [blocks, kv_heads, dk]); +inf for the first ``sink_blocks`` and the
         last ``recent_blocks``. Returns (fp32 [rows, kv_heads, columns], int32 [rows, kv_heads]: the blocks that each sees), which
-        is what the selection takes: ``selector(scores.flatten(0, 1), lens.flatten(), n)``. Scores past them are left as they are."""
+        is what the selection takes: ``selector(scores.flatten(0, 1), lens.flatten(), n)``. Scores past them are left as they are.
+        A row that is not its request's last one (of a prompt's piece, of drafted tokens) wants ``recent_blocks`` of 1 or more: its last block's
+        mean holds tokens behind the row, and with 0 they take part in which blocks are selected."""
         rows, heads, dk = q.shape
         dtype = q.dtype
         kind = self._dtypes.get(dtype)

@@ -119,3 +119,23 @@ def test_time_to_free_grows_with_the_number_of_requests(dec):
     first = list(dict.fromkeys(listed.tolist()))
     assert int(taken) == n - len(first) and free[n - len(first):].tolist() == [held[r] for r in first]
     assert not shares.any() and int((table < 0).sum()) == len(first) and dec.status() == 0
+
+
+@pytest.mark.parametrize("rows", [1, 3, 40])
+def test_recent_blocks_keep_what_follows_a_row_out_of_its_scores(dec, rows):
+    # a piece's rows, whose requests' last pages hold one to some tokens more than they see
+    block, lengths = 8, [31 + r for r in range(rows)]
+    q, more = torch.randn(rows, 4, 64).half(), lengths[-1] + 5
+    k = torch.randn(16, block, 2, 64).half().cuda()
+    table = torch.randperm(16)[None].int().cuda()
+    scores = []
+    for follows in (0.0, 100.0):  # the tokens behind each row, of its own last block
+        for r in range(rows):
+            cache = k.clone()
+            t = torch.arange(lengths[r], more)
+            cache[table[0, t // block].long(), t % block] = follows
+            means = dec.block_means(cache, table, ints([0]), ints([more]), torch.zeros(16, 2, 64).half().cuda())
+            out = torch.zeros(rows, 2, 16, device="cuda")
+            dec.block_scores(q.cuda(), means, table, ints(lengths), block, recent_blocks=1, next_n=rows, out=out)
+            scores.append(out[r])
+    assert torch.equal(torch.stack(scores[:rows]), torch.stack(scores[rows:])) and dec.status() == 0
