@@ -75,9 +75,10 @@ class Pool:
         self.decoder.copy_pages(self.caches, moves)
 
 
-def dense(pool: Pool, q, prefix_of, prefix_lens, prefix_rows):
-    """Attention over everything, prompts read once."""
-    return pool.decoder.shared_attention(q, pool.k, pool.table, pool.context, prefix_of, prefix_lens, pool.table[prefix_rows].contiguous(), v_cache=pool.v)
+def dense(pool: Pool, q, prefix_of, prefix_lens, prefix_rows, longest: int):
+    """Attention over everything, prompts read once. The prompts' table is as wide as the longest of them: the call goes by that."""
+    prefixes = pool.table[prefix_rows, :max(longest // pool.block, 1)]
+    return pool.decoder.shared_attention(q, pool.k, pool.table, pool.context, prefix_of, prefix_lens, prefixes, v_cache=pool.v)
 
 
 def sparse(pool: Pool, q, topk: int):
@@ -122,7 +123,7 @@ def run(prompts: int = 2, samples: int = 4, tokens: int = 300, steps: int = 3, b
             pool.compact(1000)
         pool.grow([0] * prompts + [1 + (r + step) % 2 for r in range(requests - prompts)])
         q = pool.draw(requests, heads, dim)
-        worst = max(worst, check(pool, q, dense(pool, q, prefix_of, prefix_lens, prefix_rows)))
+        worst = max(worst, check(pool, q, dense(pool, q, prefix_of, prefix_lens, prefix_rows, max(lengths))))
         out, chosen = sparse(pool, q, topk)
         worst = max(worst, check(pool, q, out, chosen))
     pool.drop(list(range(requests)))

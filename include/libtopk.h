@@ -572,6 +572,10 @@ int topk_block_attention(const topk_block_attention_args* args, void* stream);
  * The results are those of topk_paged_attention where the requests' own rows of the table name the same pages,
  * but that the part behind the prefix is rounded to the type of `out` before both are joined.
  * `attention.lse` must be given: it holds the statistics of that part meanwhile.
+ * The lengths are on the device, so the way through the call goes by prefix_blocks, the most that a prefix may have: a table no
+ * wider than the longest prefix at hand is the faster where prefixes are short. (8 rows of 32 heads over 8 with a prefix of
+ * 2 K tokens: 21 us, and 31 with a table eight times as wide.) The rules count rows as if all had one prefix; results differ by the way
+ * only in rounding.
  */
 typedef struct {
   topk_attention_args attention;

@@ -122,7 +122,8 @@ inline int check_attention(const topk_attention_args& a) {
 // of up to 128 dims that are not one, kSharedCols in the kernel of all forms. Past kSharedCols that one reads a prefix more than once,
 // and the wide one is the faster: 32 heads over 8, a prefix of 16 K tokens, in us wide against narrow: 72 columns 43, 50; 256 58, 78;
 // 512 85, 112; of 64 dims 96 columns 41, 51. Few units bring them closer: 16 heads over 2, 32 K tokens: 80 columns 41, 42; 256 47, 47;
-// 512 52, 63; over one 256 47, 42.
+// 512 52, 63; over one 256 47, 42. All of one prefix: of several, runs have fewer columns than rows times heads say, and the wide kernel's
+// units are then in part empty (32 rows of 32 heads over 8, 16 K tokens: one prefix 47, eight of 4 rows each 138).
 constexpr int kSharedCols = 64, kWideCols = 256;
 
 int attend_wide(const topk_attention_args& a, const FormArgs& f, void* scratch, void* stream);

@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kMostThreads) plan_kernel(const PlanParams p) 
 // 8: 134 MB 25 to 28 against 31 to 34, 268 MB 38 to 44 against 34 to 44, 537 MB 62 to 77 against 36 to 52. 16 heads over 2, wide units: 134 MB
 // 26 against 33, 268 MB 38 against 35 to 40; units of up to 64 columns, of which there are two, 268 MB 38 against 45. 16 latent heads: 151 MB 29 to
 // 35 against 55 to 61; 302 MB 46 to 50 against 61 to 69; 604 MB 74 to 77 against 70 to 81. 128 latent heads fill the columns by themselves: 604 MB
-// 194 against 221.)
+// 194 against 221. All of one prefix for all rows, and with a table as wide as the prefix: a wider one is taken for a longer prefix.)
 double read_alone(const topk_attention_args& a) {
   if (takes_wide(a)) return 256e6;
   if (a.heads / a.kv_heads >= kSharedCols) return DBL_MAX;

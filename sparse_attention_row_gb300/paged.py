@@ -385,7 +385,8 @@ class PagedDecoder:
         ``prefix_lens[prefix_of[b]]`` tokens of the pages in ``prefix_table[prefix_of[b]]`` (int32 [requests], negative: nothing shared;
         [prefixes]; [prefixes, columns]). Their whole pages are read once for all neighbouring rows that begin with them. Lengths count the
         prefix, and the rows of ``block_table`` have its pages' columns. A request of which one of its ``next_n`` rows sees less than those
-        pages hold reads its own row of the table; with ``row_request`` that goes for each such row by itself."""
+        pages hold reads its own row of the table; with ``row_request`` that goes for each such row by itself. How the call is done depends on
+        ``prefix_table``'s width: give it the columns that the longest prefix needs, not more, where prefixes are short."""
         table, prefixes, stride, columns = self._table("prefix_table", prefix_table)
         rows = q.shape[0]
         need = self._scratch.get(rows)
