@@ -697,7 +697,7 @@ typedef struct {
 /*
  * Copies page source[i] to page target[i] in every one of the caches (layers' keys, values, scales, means), for i < num_copies.
  * Pairs with a negative page are skipped; so are pairs with a page outside a cache, in that cache (TOPK_DEV_BAD_BLOCK). A page may be
- * the source of several pairs; no target is listed twice, or as a source. Pieces are as wide as addresses,
+ * the source of several pairs; no target is listed twice, or as a source, and no two pages of a cache overlap. Pieces are as wide as addresses,
  * strides and run_bytes of a cache allow, 16 bytes at most.
  */
 typedef struct {

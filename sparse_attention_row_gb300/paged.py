@@ -479,12 +479,12 @@ class PagedDecoder:
                 loops[-1][1] *= n
             else:
                 loops.append([stride, n])
-        ends = run
-        for stride, n in loops:
+        ends = 1  # of the dimensions so far, the pages' among them
+        for stride, n in sorted((stride, n) for stride, n in zip(strides, shape) if n > 1):
             if stride < ends:
                 self._bad("a cache", t, "a tensor whose elements do not overlap")
-            ends = stride * (n - 1) + ends
-        if len(loops) > 2 or (shape[0] > 1 and strides[0] == 0):
+            ends += stride * (n - 1)
+        if len(loops) > 2:
             self._bad("a cache", t, "a tensor whose pages are at most two loops over runs of memory")
         (s0, n0), (s1, n1) = (loops[::-1] + [[0, 1], [0, 1]])[:2]
         return _CACHE.pack(t.data_ptr(), shape[0], strides[0] * size, s0 * size, s1 * size, n0, n1, run * size)
