@@ -51,8 +51,8 @@ class PageCopies(NamedTuple):
 class PageCaches:
     """Caches whose pages are copied together, read once: made by ``PagedDecoder.page_caches``."""
 
-    def __init__(self, tensors, packed: bytes):
-        self.tensors, self.packed = tensors, array.array("B", packed)
+    def __init__(self, tensors, packed: bytes, device: int):
+        self.tensors, self.packed, self.device = tensors, array.array("B", packed), device
         self.address = self.packed.buffer_info()[0]
 
 
@@ -456,7 +456,7 @@ class PagedDecoder:
         caches = list(caches)
         if len(caches) > _sar.TOPK_MAX_PAGE_CACHES:
             raise ValueError(f"at most {_sar.TOPK_MAX_PAGE_CACHES} caches at a time")
-        return PageCaches(caches, b"".join([self._page_cache(t) for t in caches]))
+        return PageCaches(caches, b"".join([self._page_cache(t) for t in caches]), self.device)
 
     def _page_cache(self, t) -> bytes:
         shape = t.shape
@@ -494,6 +494,8 @@ class PagedDecoder:
         scales, means; or what ``page_caches`` made of them); pairs with a -1 are skipped. No target may be listed twice, or as a source."""
         if not isinstance(caches, PageCaches):
             caches = self.page_caches(caches)
+        elif caches.device != self.device:
+            raise ValueError(f"caches on device {caches.device} for a decoder on {self._dev}")
         n = copies.source.numel()
         self._call(self._copy, _COPY.pack(self._ints("source", copies.source, n), self._ints("target", copies.target, n), n, caches.address,
                                           len(caches.tensors), self._workspace_ptr), stream)

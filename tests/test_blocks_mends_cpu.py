@@ -26,3 +26,11 @@ def test_caches_whose_pages_lie_among_one_another_are_not(dec, make):
     t = make()
     c = sar.TopkPageCache.from_buffer_copy(dec._page_cache(t))
     assert (c.num_blocks, c.block_stride) == (t.shape[0], t.stride(0) * 4)
+
+
+def test_caches_of_another_device_are_refused(dec):
+    kept = dec.page_caches([torch.zeros(4, 8)])
+    other = object.__new__(sar.PagedDecoder)
+    other.device, other._dev = 1, torch.device("cuda", 1)
+    with pytest.raises(ValueError, match="device -1"):
+        other.copy_pages(kept, sar.PageCopies(torch.zeros(1).int(), torch.zeros(1).int()))
