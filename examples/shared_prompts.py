@@ -38,7 +38,7 @@ class Pool:
         self.context = ints(requests)
         self.decoder, self.selector = sar.PagedDecoder(torch.cuda.current_device()), sar.Selector(torch.cuda.current_device())
         self.caches = self.decoder.page_caches([self.k, self.v, self.means])
-        self.told = [torch.zeros(2, 0, kv_heads, dim, device="cuda") for _ in range(requests)]  # for the checks alone
+        self.told = [torch.zeros(2, 0, kv_heads, dim) for _ in range(requests)]  # on the host, for the checks alone
 
     def draw(self, *shape):
         return torch.randn(shape, generator=self.g, device="cuda", dtype=torch.bfloat16)
@@ -52,7 +52,7 @@ class Pool:
             cache.view(-1, self.kv_heads, self.dim)[m.slots] = x
         self.decoder.block_means(self.k, self.table, self.context, lens, self.means)
         self.context += lens
-        for r, piece in enumerate(fresh.float().split(new, 1)):
+        for r, piece in enumerate(fresh.float().cpu().split(new, 1)):
             self.told[r] = torch.cat([self.told[r], piece], 1)
 
     def drop(self, requests):
@@ -89,18 +89,19 @@ def sparse(pool: Pool, q, topk: int):
 
 
 def check(pool: Pool, q, out, chosen=None) -> float:
-    """The largest distance of `out` from attention in 64 bits."""
+    """The largest distance of `out` from attention in 64 bits, on the host."""
     worst, group = 0.0, q.shape[1] // pool.kv_heads
+    q, out, chosen = q.cpu().double(), out.cpu().double(), None if chosen is None else chosen.cpu()
     for r, (k, v) in enumerate(pool.told):
         for h in range(pool.kv_heads):
-            t = torch.arange(len(k), device="cuda")
+            t = torch.arange(len(k))
             if chosen is not None:
                 t = t[(t[:, None] // pool.block == chosen[r, h]).any(1)]
             if len(t) == 0:
                 continue
-            s = q[r, h * group:(h + 1) * group].double() @ k[t, h].double().T * pool.dim ** -0.5
+            s = q[r, h * group:(h + 1) * group] @ k[t, h].double().T * pool.dim ** -0.5
             want = torch.softmax(s, -1) @ v[t, h].double()
-            worst = max(worst, float((out[r, h * group:(h + 1) * group].double() - want).abs().max()))
+            worst = max(worst, float((out[r, h * group:(h + 1) * group] - want).abs().max()))
     return worst
 
 
